@@ -19,7 +19,7 @@ FLAGS = [
     "-fconstexpr-steps=100000000",
     "-Wall", "-Wno-unused-command-line-argument",
 ]
-SOURCES = ["dq_kernels.hip", "dq_api.cpp"]
+SOURCES = ["dq_kernels.hip", "dq_api.cpp", "dq_train.hip", "dq_train_api.cpp"]
 
 
 def build(verbose=False):

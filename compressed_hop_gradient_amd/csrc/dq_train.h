@@ -1,0 +1,59 @@
+// dq_train.h -- declarations shared by the training-step entry points
+// (dq_train_api.cpp) and their kernels (dq_train.hip).  Not part of the public ABI.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace dq {
+
+constexpr int kRouteMaxExperts = 1024;
+constexpr int kRouteMaxTopK = 16;
+
+struct DropoutArgs {
+    const void *x, *residual;
+    void *y;
+    int64_t rows, cols;
+    int64_t xs, rs, ys;                 // row strides, elements
+    uint32_t threshold;                 // T: dropped iff dither < T
+    float scale;                        // fl(65536 / (65536 - T)); 0 for T = 65536
+    uint32_t key0, key1, round, worker, site;
+    const uint32_t *d_round;
+};
+
+struct RouteArgs {
+    const void *logits;
+    int64_t tokens, stride;
+    int32_t E, k;
+    const uint8_t *mask;
+    int32_t renorm;
+    int32_t *ids;
+    float *gates;
+    // per-block partial statistics: float psum[nblk][E], then uint32 count[nblk][E],
+    // then uint32 routed[nblk]
+    float *psum;
+    uint32_t *count, *routed;
+    int32_t nblk;
+};
+
+struct RouteBackwardArgs {
+    const void *logits;
+    int64_t tokens, stride, dstride;
+    int32_t E, k;
+    const uint8_t *mask;
+    int32_t renorm;
+    const int32_t *ids;
+    const float *dgates, *coef, *dloss;
+    void *dlogits;
+};
+
+hipError_t launch_dropout(const DropoutArgs &a, int f32, hipStream_t s);
+// blocks of the router's forward kernel for this many tokens (its partials' rows)
+int route_blocks(int64_t tokens, int E);
+hipError_t launch_route(const RouteArgs &a, int f32, hipStream_t s);
+hipError_t launch_route_fold(const RouteArgs &a, double *stats, int accumulate, hipStream_t s);
+hipError_t launch_balance(const double *stats, int E, int k, float *loss, float *coef, int64_t *counts,
+                          hipStream_t s);
+hipError_t launch_route_backward(const RouteBackwardArgs &a, int f32, hipStream_t s);
+
+}  // namespace dq

@@ -1,0 +1,166 @@
+// dq_train_api.cpp -- the training-step entry points of include/dq.h: argument
+// checks and launches.  Stateless; all device work is enqueued on the caller's
+// stream and nothing synchronises.
+#include "dq.h"
+
+#include <cmath>
+
+#include "dq_train.h"
+
+using namespace dq;
+
+namespace {
+
+constexpr size_t kAlign = 256;
+
+size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
+
+bool is_kind(int32_t kind) { return kind == DQ_BF16 || kind == DQ_F32; }
+uintptr_t elem_bytes(int32_t kind) { return kind == DQ_F32 ? 4 : 2; }
+bool aligned(const void *p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+dq_status hip_status(hipError_t e) { return e == hipSuccess ? DQ_OK : DQ_EHIP; }
+
+// Whether an output (rows x cols, row stride os) meets an operand (row stride
+// is) other than element on element.  Row windows of equal stride may
+// interleave (two halves of one wide tensor).
+bool clash(const void *out, int64_t os, const void *in, int64_t is, int64_t rows, int64_t cols, int64_t es) {
+    if (!in || rows == 0 || cols == 0) return false;
+    if (rows == 1) os = is = cols;
+    if (out == in && os == is) return false;
+    const __int128 o = (__int128) reinterpret_cast<uintptr_t>(out), i = (__int128) reinterpret_cast<uintptr_t>(in);
+    const __int128 olen = ((__int128)(rows - 1) * os + cols) * es, ilen = ((__int128)(rows - 1) * is + cols) * es;
+    if (o + olen <= i || i + ilen <= o) return false;
+    if (os == is && (o - i) % es == 0) {
+        const int64_t at = (int64_t)((((o - i) / es) % os + os) % os);
+        if (at >= cols && at <= os - cols) return false;
+    }
+    return true;
+}
+
+bool bad_router(int32_t kind, int64_t tokens, int32_t E, int64_t stride, int32_t k) {
+    return !is_kind(kind) || tokens < 0 || tokens > ((int64_t)1 << 40) || E < 1 || E > kRouteMaxExperts || k < 1 ||
+           k > E || k > kRouteMaxTopK || stride < 0 || stride > ((int64_t)1 << 40);
+}
+
+}  // namespace
+
+extern "C" {
+
+dq_status dq_dropout(const void *x, const void *residual, void *y, int32_t kind, int64_t rows, int64_t cols,
+                     int64_t xs, int64_t rs, int64_t ys, double p, uint64_t seed, uint32_t round,
+                     const uint32_t *d_round, int32_t worker, uint32_t site, void *stream) {
+    constexpr int64_t kMost = (int64_t)1 << 51;
+    if (!is_kind(kind) || rows < 0 || cols < 0 || !(p >= 0.0 && p <= 1.0)) return DQ_EINVAL;
+    if (cols > 0 && rows >= kMost / cols + 1) return DQ_EINVAL;
+    if (rows * cols >= kMost || worker < 0 || worker > 65535 || site >= 0x80000000u) return DQ_EINVAL;
+    if (xs < 0 || rs < 0 || xs >= kMost || rs >= kMost || ys >= kMost) return DQ_EINVAL;
+    if (rows > 1 && ys < cols) return DQ_EINVAL;
+    if (rows == 0 || cols == 0) return DQ_OK;
+    if (!x || !y) return DQ_ENULL;
+    const uintptr_t es = elem_bytes(kind);
+    if (!aligned(x, es) || !aligned(residual, es) || !aligned(y, es) || !aligned(d_round, 4)) return DQ_EINVAL;
+    if (clash(y, ys, x, xs, rows, cols, (int64_t)es) || clash(y, ys, residual, rs, rows, cols, (int64_t)es))
+        return DQ_EINVAL;
+    DropoutArgs a{};
+    a.x = x;
+    a.residual = residual;
+    a.y = y;
+    // contiguous operands are one row, whatever their shape
+    if (rows == 1 || (xs == cols && ys == cols && (!residual || rs == cols))) {
+        cols *= rows;
+        rows = 1;
+        xs = rs = ys = cols;
+    }
+    a.rows = rows;
+    a.cols = cols;
+    a.xs = xs;
+    a.rs = rs;
+    a.ys = ys;
+    a.threshold = (uint32_t)std::floor(65536.0 * p + 0.5);
+    a.scale = a.threshold == 65536 ? 0.0f : (float)(65536.0 / (65536 - (int)a.threshold));
+    a.key0 = (uint32_t)seed;
+    a.key1 = (uint32_t)(seed >> 32);
+    a.round = round;
+    a.d_round = d_round;
+    a.worker = (uint32_t)worker;
+    a.site = site;
+    return hip_status(launch_dropout(a, kind == DQ_F32, static_cast<hipStream_t>(stream)));
+}
+
+size_t dq_route_workspace_bytes(int64_t tokens, int32_t E) {
+    if (tokens < 0 || tokens > ((int64_t)1 << 40) || E < 1 || E > kRouteMaxExperts) return 0;
+    const size_t n = (size_t)route_blocks(tokens, E);
+    return 2 * align_up(4 * n * (size_t)E) + align_up(4 * n);
+}
+
+dq_status dq_route(const void *logits, int32_t kind, int64_t tokens, int32_t E, int64_t stride, const uint8_t *mask,
+                   int32_t k, int32_t flags, int32_t *ids, float *gates, double *stats, void *ws, size_t ws_bytes,
+                   void *stream) {
+    if (bad_router(kind, tokens, E, stride, k) || (flags & ~(DQ_ROUTE_RENORM | DQ_ROUTE_ACCUMULATE)))
+        return DQ_EINVAL;
+    if (!stats || (tokens > 0 && (!logits || !ids || !gates))) return DQ_ENULL;
+    if (!aligned(logits, elem_bytes(kind)) || !aligned(ids, 4) || !aligned(gates, 4) || !aligned(stats, 8))
+        return DQ_EINVAL;
+    if (!ws || !aligned(ws, kAlign) || ws_bytes < dq_route_workspace_bytes(tokens, E)) return DQ_EWORKSPACE;
+    RouteArgs a{};
+    a.logits = logits;
+    a.tokens = tokens;
+    a.stride = stride;
+    a.E = E;
+    a.k = k;
+    a.mask = mask;
+    a.renorm = (flags & DQ_ROUTE_RENORM) != 0;
+    a.ids = ids;
+    a.gates = gates;
+    a.nblk = tokens == 0 ? 0 : route_blocks(tokens, E);
+    const size_t part = align_up(4 * (size_t)a.nblk * (size_t)E);
+    a.psum = static_cast<float *>(ws);
+    a.count = reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(ws) + part);
+    a.routed = reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(ws) + 2 * part);
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    if (tokens > 0) {
+        const hipError_t e = launch_route(a, kind == DQ_F32, s);
+        if (e != hipSuccess) return hip_status(e);
+    }
+    return hip_status(launch_route_fold(a, stats, (flags & DQ_ROUTE_ACCUMULATE) != 0, s));
+}
+
+dq_status dq_balance(const double *stats, int32_t E, int32_t k, float *loss, float *coef, int64_t *counts,
+                     void *stream) {
+    if (E < 1 || E > kRouteMaxExperts || k < 1 || k > E || k > kRouteMaxTopK) return DQ_EINVAL;
+    if (!stats) return DQ_ENULL;
+    if (!aligned(stats, 8) || !aligned(loss, 4) || !aligned(coef, 4) || !aligned(counts, 8)) return DQ_EINVAL;
+    return hip_status(launch_balance(stats, E, k, loss, coef, counts, static_cast<hipStream_t>(stream)));
+}
+
+dq_status dq_route_backward(const void *logits, int32_t kind, int64_t tokens, int32_t E, int64_t stride,
+                            const uint8_t *mask, int32_t k, int32_t flags, const int32_t *ids, const float *dgates,
+                            const float *coef, const float *dloss, void *dlogits, int64_t dstride, void *stream) {
+    if (bad_router(kind, tokens, E, stride, k) || (flags & ~DQ_ROUTE_RENORM)) return DQ_EINVAL;
+    if (dstride > ((int64_t)1 << 40) || (tokens > 1 && dstride < E)) return DQ_EINVAL;
+    if (tokens == 0) return DQ_OK;
+    if (!logits || !ids || !dlogits) return DQ_ENULL;
+    const uintptr_t es = elem_bytes(kind);
+    if (!aligned(logits, es) || !aligned(dlogits, es) || !aligned(ids, 4) || !aligned(dgates, 4) ||
+        !aligned(coef, 4) || !aligned(dloss, 4))
+        return DQ_EINVAL;
+    if (clash(dlogits, dstride, logits, stride, tokens, E, (int64_t)es)) return DQ_EINVAL;
+    RouteBackwardArgs a{};
+    a.logits = logits;
+    a.tokens = tokens;
+    a.stride = stride;
+    a.dstride = dstride;
+    a.E = E;
+    a.k = k;
+    a.mask = mask;
+    a.renorm = (flags & DQ_ROUTE_RENORM) != 0;
+    a.ids = ids;
+    a.dgates = dgates;
+    a.coef = coef;
+    a.dloss = dloss;
+    a.dlogits = dlogits;
+    return hip_status(launch_route_backward(a, kind == DQ_F32, static_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"

@@ -6,6 +6,7 @@ Argument marshalling only: every stage runs in the HIP kernels of
 import of this module's functions raises; there is no CPU fallback.
 """
 import ctypes as C
+import functools
 import os
 
 import torch
@@ -25,6 +26,7 @@ OPT_MAX_WIDTH = 8
 ALLOC_THRESHOLD, ALLOC_MEAN_CORRECTED, ALLOC_UNIFORM = 0, 1, 2
 MX_FP8_E4M3, MX_FP6_E3M2, MX_FP6_E2M3, MX_FP4_E2M1 = 0, 1, 2, 3
 OPT_EPS = 0   # dq_option_f64
+ROUTE_RENORM, ROUTE_ACCUMULATE = 1, 2   # dq_route_flags
 KERNEL_KINDS = ("stats", "allocate", "reorder", "compress", "hop_grad", "hop_packed",
                 "finalize", "mxfp8", "hop_final")
 
@@ -92,6 +94,16 @@ _SIGS = {
     "dq_check_round_half_up": (C.c_int, [C.c_uint32, C.c_uint32, C.c_void_p, C.c_void_p]),
     "dq_probe_stream": (C.c_int, [C.c_void_p, C.c_size_t, C.c_void_p, C.c_size_t, C.c_int32,
                                   C.c_void_p]),
+    "dq_dropout": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_int32, C.c_int64, C.c_int64, C.c_int64,
+                             C.c_int64, C.c_int64, C.c_double, C.c_uint64, C.c_uint32, C.c_void_p,
+                             C.c_int32, C.c_uint32, C.c_void_p]),
+    "dq_route_workspace_bytes": (C.c_size_t, [C.c_int64, C.c_int32]),
+    "dq_route": (C.c_int, [C.c_void_p, C.c_int32, C.c_int64, C.c_int32, C.c_int64, C.c_void_p, C.c_int32,
+                           C.c_int32, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p]),
+    "dq_balance": (C.c_int, [C.c_void_p, C.c_int32, C.c_int32, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p]),
+    "dq_route_backward": (C.c_int, [C.c_void_p, C.c_int32, C.c_int64, C.c_int32, C.c_int64, C.c_void_p, C.c_int32,
+                                    C.c_int32, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p,
+                                    C.c_int64, C.c_void_p]),
     "dq_get_info": (C.c_int, [C.c_void_p, C.POINTER(dq_info), C.c_void_p]),
     "dq_timing_read": (C.c_int, [C.c_void_p, C.POINTER(dq_timing)]),
     "dq_status_string": (C.c_char_p, [C.c_int32]),
@@ -194,6 +206,214 @@ def probe_stream(src, dst, reads_per_write, stream=None):
     _check(lib().dq_probe_stream(_ptr(src), src.numel() * src.element_size(), _ptr(dst),
                                  dst.numel() * dst.element_size(), int(reads_per_write),
                                  _stream(stream)), "dq_probe_stream")
+
+
+# ---- training step (every call takes stream=, as under torch.cuda.stream) --------
+
+def _rows(t, what):
+    """(rows, cols, row stride) of a tensor as a matrix of its last dimension:
+    one row when contiguous; any views whose rows lie at one stride."""
+    if t.is_contiguous():
+        return 1, t.numel(), t.numel()
+    if t.dim() == 0 or t.stride(-1) != 1 and t.size(-1) != 1:
+        raise ValueError(f"{what}: the last dimension must be contiguous")
+    rows, stride = 1, None
+    for size, step in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if size == 1:
+            continue
+        if stride is None:
+            stride = step
+        elif step != rows * stride:
+            raise ValueError(f"{what}: shape {tuple(t.shape)} with strides {t.stride()} has no common row stride")
+        rows *= size
+    return rows, t.size(-1), t.size(-1) if stride is None else stride
+
+
+def _gpu(t, what):
+    """A float tensor the kernels read: bf16 or fp32, on a GPU."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{what}: expected a torch.Tensor, got {type(t).__name__}")
+    if t.dtype != torch.bfloat16 and t.dtype != torch.float32:
+        raise TypeError(f"{what}: dtype {t.dtype} (bf16 or fp32 only)")
+    if t.device.type != "cuda":
+        raise ValueError(f"{what}: tensor on {t.device}, the kernels run on a GPU")
+    return t
+
+
+def _call(dev, name, *args):
+    """Call a stateless entry point on ``dev``'s current stream."""
+    fn = getattr(lib(), name)
+    if dev.index == torch.cuda.current_device():
+        _check(fn(*args, _stream(None)), name)
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, _stream(None)), name)
+
+
+def _on_stream(fn):
+    """``stream=s`` means: as under ``torch.cuda.stream(s)``, so that results and
+    scratch are allocated for the stream that uses them."""
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return fn(*args, **kw)
+        with torch.cuda.stream(stream):
+            return fn(*args, **kw)
+    return call
+
+
+def _opt(t):
+    return None if t is None else t.data_ptr()
+
+
+@_on_stream
+def dropout(x, p, residual=None, seed=1, rnd=0, worker=0, site=0, out=None):
+    """``residual + dropout(x)``, or ``dropout(x)`` (``dq_dropout``).
+
+    The mask is a function of (seed, rnd, worker, site, element) and is never
+    stored.  ``x``, ``residual`` and ``out`` are bf16 or fp32, of one dtype and
+    shape, contiguous or with rows at one stride; ``out`` may be ``x`` or
+    ``residual``.  ``rnd`` is the step: an int, or a one-element int32 GPU tensor that
+    the kernel reads (for captured graphs: a replay takes the tensor's new value)."""
+    dev = _gpu(x, "x").device
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    views = [_rows(x, "x"), None, _rows(out, "out")]
+    for t, what in ((residual, "residual"), (out, "out")):
+        if t is not None and (t.shape != x.shape or t.dtype != x.dtype or t.device != dev):
+            raise ValueError(f"{what}: {tuple(t.shape)} {t.dtype} on {t.device}, "
+                             f"x is {tuple(x.shape)} {x.dtype} on {dev}")
+    if residual is not None:
+        views[1] = _rows(residual, "residual")
+    cols = x.size(-1) if x.dim() else 1
+    if all(v is None or v[0] == 1 for v in views):
+        rows, cols = 1, x.numel()
+        xs = rs = ys = cols
+    else:
+        rows = x.numel() // cols if cols else 0
+        xs, rs, ys = (v[2] if v is not None and v[0] != 1 else cols for v in views)
+    d_round = None
+    if isinstance(rnd, torch.Tensor):
+        d_round = _tensor(rnd, "rnd", dev, numel=1, dtype=torch.int32).data_ptr()
+        rnd = 0
+    # beyond these, marshalling would wrap them into other numbers
+    if not (0 <= rnd < 1 << 32 and 0 <= worker < 1 << 16 and 0 <= site < 1 << 31 and 0 <= seed < 1 << 64):
+        raise ValueError(f"seed {seed}, rnd {rnd}, worker {worker}, site {site}: expected 64, 32, 16 and 31 bits")
+    _call(dev, "dq_dropout", x.data_ptr(), _opt(residual), out.data_ptr(),
+          F32 if x.dtype == torch.float32 else BF16, rows, cols, xs, rs, ys, p,
+          seed, rnd, d_round, worker, site)
+    return out
+
+
+def dropout_backward(dout, p, seed=1, rnd=0, worker=0, site=0, out=None, stream=None):
+    """Gradient of :func:`dropout` by ``x``, from the same numbers as the
+    forward call (the gradient by ``residual`` is ``dout`` itself)."""
+    return dropout(dout, p, None, seed, rnd, worker, site, out, stream=stream)
+
+
+def _logits(t, what="logits"):
+    _gpu(t, what)
+    if t.dim() != 2 or t.size(1) > 1 and t.stride(1) != 1 and t.numel():
+        raise ValueError(f"{what}: {tuple(t.shape)} with strides {t.stride()}, expected [tokens, experts] "
+                         "with contiguous rows")
+    return t
+
+
+def _token_mask(mask, tokens, dev):
+    if mask is None:
+        return None
+    _tensor(mask, "mask", dev, numel=tokens)
+    if mask.dtype != torch.bool and mask.dtype != torch.uint8:
+        raise TypeError(f"mask: dtype {mask.dtype}, expected bool or uint8")
+    return mask.data_ptr()
+
+
+def _result(t, shape, what, dtype, dev):
+    """A buffer of the caller's for a result, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    if isinstance(t, torch.Tensor) and t.shape != shape:
+        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    return _tensor(t, what, dev, dtype=dtype)
+
+
+@_on_stream
+def route(logits, top_k, renorm=True, mask=None, stats=None, accumulate=None, ids=None, gates=None):
+    """Expert choice of every token (``dq_route``): returns (ids, gates, stats).
+
+    ``logits`` is [tokens, experts], bf16 or fp32, rows at any stride; ``mask``
+    (bool or uint8, [tokens]) is false for tokens left out.  ``ids`` is int32 and
+    ``gates`` fp32, both [tokens, top_k], best choice first; -1 and 0 where a
+    token has fewer open experts (logits above -inf).  ``stats``, fp64
+    [2 experts + 1], holds choices and summed probabilities per expert and the
+    routed tokens: passed in, the call adds to it (workers in rank order), unless
+    ``accumulate`` is false.  Several processes sum their ``stats``."""
+    tokens, experts = _logits(logits).shape
+    dev = logits.device
+    if accumulate is None:
+        accumulate = stats is not None
+    elif accumulate and stats is None:
+        raise ValueError("accumulate needs stats")
+    shape = (tokens, top_k)
+    ids = _result(ids, shape, "ids", torch.int32, dev)
+    gates = _result(gates, shape, "gates", torch.float32, dev)
+    stats = _result(stats, (2 * experts + 1,), "stats", torch.float64, dev)
+    nbytes = lib().dq_route_workspace_bytes(tokens, experts)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    _call(dev, "dq_route", logits.data_ptr(), _kind(logits), tokens, experts, logits.stride(0),
+          _token_mask(mask, tokens, dev), top_k,
+          (ROUTE_RENORM if renorm else 0) | (ROUTE_ACCUMULATE if accumulate else 0),
+          ids.data_ptr(), gates.data_ptr(), stats.data_ptr(), ws.data_ptr(), nbytes)
+    return ids, gates, stats
+
+
+@_on_stream
+def balance(stats, top_k):
+    """Balance loss of the tokens in ``stats`` (``dq_balance``): returns
+    (loss [1] fp32, coef [experts] fp32, counts [experts] int64).  ``coef`` is
+    the loss's derivative by any token's probabilities, which
+    :func:`route_backward` takes."""
+    if not isinstance(stats, torch.Tensor) or stats.dim() != 1 or stats.numel() < 3 or stats.numel() % 2 == 0:
+        raise ValueError("stats: expected the [2 experts + 1] tensor of route()")
+    dev = stats.device
+    if dev.type != "cuda":
+        raise ValueError(f"stats: tensor on {dev}, the kernels run on a GPU")
+    _tensor(stats, "stats", dev, dtype=torch.float64)
+    experts = stats.numel() // 2
+    loss = torch.empty(1, dtype=torch.float32, device=dev)
+    coef = torch.empty(experts, dtype=torch.float32, device=dev)
+    counts = torch.empty(experts, dtype=torch.int64, device=dev)
+    _call(dev, "dq_balance", stats.data_ptr(), experts, top_k, loss.data_ptr(), coef.data_ptr(),
+          counts.data_ptr())
+    return loss, coef, counts
+
+
+@_on_stream
+def route_backward(logits, ids, dgates=None, coef=None, dloss=None, renorm=True, mask=None, out=None):
+    """Gradient by the logits (``dq_route_backward``) from the gates' gradient
+    ``dgates`` and the balance loss's, ``dloss`` (one fp32 element; None: 1) times
+    ``coef`` of :func:`balance`; either part may be None.  ``ids``, ``renorm`` and ``mask``
+    as in the forward call; ``out`` may be ``logits``."""
+    tokens, experts = _logits(logits).shape
+    dev = logits.device
+    if not isinstance(ids, torch.Tensor) or ids.dim() != 2 or ids.size(0) != tokens:
+        raise ValueError(f"ids: expected [{tokens}, top_k] of route()")
+    _tensor(ids, "ids", dev, dtype=torch.int32)
+    if dgates is not None:
+        _result(dgates, ids.shape, "dgates", torch.float32, dev)
+    if coef is not None:
+        _tensor(coef, "coef", dev, numel=experts, dtype=torch.float32)
+    if dloss is not None:
+        _tensor(dloss, "dloss", dev, numel=1, dtype=torch.float32)
+    if out is None:
+        out = torch.empty((tokens, experts), dtype=logits.dtype, device=dev)
+    elif _logits(out, "out").shape != logits.shape or out.dtype != logits.dtype or out.device != dev:
+        raise ValueError(f"out: {tuple(out.shape)} {out.dtype} on {out.device}, "
+                         f"logits are {tuple(logits.shape)} {logits.dtype} on {dev}")
+    _call(dev, "dq_route_backward", logits.data_ptr(), _kind(logits), tokens, experts, logits.stride(0),
+          _token_mask(mask, tokens, dev), ids.size(1), ROUTE_RENORM if renorm else 0, ids.data_ptr(), _opt(dgates),
+          _opt(coef), _opt(dloss), out.data_ptr(), out.stride(0))
+    return out
 
 
 class Plan:

@@ -391,6 +391,89 @@ size_t dq_mx_arena_bytes(const dq_plan *plan);
 dq_status dq_mx_allreduce(dq_plan *plan, int32_t format, const void *const *h_grads, int32_t kind,
                           void *d_arena, size_t arena_bytes, float *d_out, void *stream);
 
+/* ---- training step ----------------------------------------------------------
+ *
+ * What a data-parallel training step draws or sums per worker, next to the
+ * gradient round: dropout masks (one stream of random numbers per seed, round
+ * and worker, as the dithers of the codec) and the balance statistics of an
+ * expert router (folded over the workers, as dq_stats).  Stateless: no plan,
+ * every buffer is the caller's.  Errors of all of them: DQ_ENULL, DQ_EINVAL
+ * (sizes, strides, kind, alignment of a pointer to its element type, an output
+ * that overlaps another operand), DQ_EHIP; DQ_EWORKSPACE where one is taken. */
+
+/* y = residual + dropout(x), or dropout(x) with d_residual = NULL.  The mask is
+ * a function of (seed, round, worker, site, element) and is never stored:
+ * dropout's gradient by x is the same call on dy with the same numbers and no
+ * residual (the gradient by the residual is dy).
+ *
+ * Tensors are rows x cols of `kind` (DQ_BF16 or DQ_F32), row r of operand v at
+ * element r * v_stride; element i = r * cols + c is counted in the logical
+ * tensor, so strides do not change the mask.  d_y may be d_x or d_residual
+ * (with the same stride) and may not overlap them otherwise.
+ *
+ * With T = floor(65536 p + 1/2), p in [0, 1], element i is kept iff its 16-bit
+ * dither is >= T and multiplied by fl32(65536 / (65536 - T)): the inverse of
+ * the probability with which it is kept, so its mean is x for every p.  A
+ * dropped element counts as 0, NaN and infinity too; T = 65536 drops
+ * everything.  The sum with the residual is fp32, rounded once to `kind`.
+ *
+ * Dither of element i: Philox4x32-10, key = (seed lo32, seed hi32), counter =
+ * (lo32(i >> 3), (i >> 35) | worker << 16, round + *d_round, 2^31 | site),
+ * word (i & 7) >> 1, low half for even i.  The top bit of the last word keeps
+ * it apart from every dither of the codec.  worker in 0..65535, site (the call
+ * within the model) below 2^31, rows * cols below 2^51.  d_round (may be NULL: 0)
+ * is read by the kernel, so a captured graph takes a new round per replay. */
+dq_status dq_dropout(const void *d_x, const void *d_residual, void *d_y, int32_t kind, int64_t rows,
+                     int64_t cols, int64_t x_stride, int64_t residual_stride, int64_t y_stride, double p,
+                     uint64_t seed, uint32_t round, const uint32_t *d_round, int32_t worker, uint32_t site,
+                     void *stream);
+
+/* Expert router.  For every token, p = softmax of its n_experts logits (kind
+ * DQ_BF16 or DQ_F32, row t at element t * stride, stride >= 0), the top_k
+ * largest logits are chosen in falling order -- equal ones (-0 and +0 too) by
+ * the lowest index, NaN before +inf, -inf never -- and their probabilities are
+ * the gates, with DQ_ROUTE_RENORM divided by their sum.  Outputs, per token:
+ * d_ids[top_k] (-1 where fewer than top_k experts are open) and
+ * d_gates[top_k] (0 there).  d_mask (may be NULL): one byte per token, 0 for
+ * a token left out; such a token, and one with every logit -inf, gets ids -1
+ * and gates 0 and counts nowhere, whatever its logits hold.  A token with a NaN
+ * or +inf has NaN gates (and makes the balance loss NaN).
+ *
+ * d_stats (double[2 * n_experts + 1]: choices per expert, sum of p per expert,
+ * routed tokens) is set, or with DQ_ROUTE_ACCUMULATE added to: the statistic
+ * of several workers is their calls in rank order on one stream, and of several
+ * processes the sum of their d_stats.  Fixed summation order: the same calls give
+ * the same bits.
+ * n_experts in 1..1024, top_k in 1..min(n_experts, 16), tokens in 0..2^40. */
+typedef enum dq_route_flags { DQ_ROUTE_RENORM = 1, DQ_ROUTE_ACCUMULATE = 2 } dq_route_flags;
+size_t dq_route_workspace_bytes(int64_t tokens, int32_t n_experts);   /* 0 on bad arguments */
+dq_status dq_route(const void *d_logits, int32_t kind, int64_t tokens, int32_t n_experts, int64_t stride,
+                   const uint8_t *d_mask, int32_t top_k, int32_t flags, int32_t *d_ids, float *d_gates,
+                   double *d_stats, void *d_workspace, size_t workspace_bytes, void *stream);
+
+/* Balance loss of the tokens in d_stats (dq_route): with c the choices, S the
+ * summed probabilities and N the routed tokens,
+ *   loss = n_experts / (top_k N^2) * sum_e c_e S_e     (1 when balanced),
+ * d_coef[e] = n_experts c_e / (top_k N^2), the derivative of the loss by any
+ * token's p_e (choices have none), and d_counts[e] = c_e.  All 0 when N = 0.
+ * Any of the three outputs may be NULL. */
+dq_status dq_balance(const double *d_stats, int32_t n_experts, int32_t top_k, float *d_loss, float *d_coef,
+                     int64_t *d_counts, void *stream);
+
+/* Gradient by the logits, from the gates' (d_dgates[tokens][top_k], may be
+ * NULL) and the balance loss's (d_coef of dq_balance, may be NULL; times
+ * *d_dloss, NULL: 1).  d_ids, d_mask and DQ_ROUTE_RENORM as in the forward call.
+ * With a_e = dloss coef_e and g the gates:
+ *   RENORM:  dl_j = p_j (a_j - sum p a) + [j chosen] g_j (dg_j - sum g dg)
+ *   without: dl_j = p_j (a_j - sum p a - sum g dg) + [j chosen] g_j dg_j
+ * A token that was left out gets zeros.  d_dlogits has the logits' kind, row t
+ * at element t * dstride (dstride >= n_experts), and may be d_logits (same
+ * stride).  Entries of d_ids outside 0..n_experts-1 count as -1. */
+dq_status dq_route_backward(const void *d_logits, int32_t kind, int64_t tokens, int32_t n_experts,
+                            int64_t stride, const uint8_t *d_mask, int32_t top_k, int32_t flags,
+                            const int32_t *d_ids, const float *d_dgates, const float *d_coef,
+                            const float *d_dloss, void *d_dlogits, int64_t dstride, void *stream);
+
 /* ---- inspection ----------------------------------------------------------- */
 
 /* Copy the allocation result to the host.  SYNCHRONISES `stream`.

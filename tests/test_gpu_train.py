@@ -1,0 +1,680 @@
+"""Training-step operators on the GPU against their plain fp64 forms
+(train_ref.py): dropout bit for bit, the router's choices and counts exactly,
+its gates, loss and gradients within the roundings that an fp32 evaluation
+makes."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import train_ref as ref
+from compressed_hop_gradient_amd import dq, train
+
+pytestmark = pytest.mark.gpu
+
+DTYPES = [torch.bfloat16, torch.float32]
+U = ref.U
+
+
+@pytest.fixture(autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+def half_step(dtype):
+    """Relative error of one rounding to ``dtype`` (0 for fp32, whose rounding
+    the magnitudes count)."""
+    return torch.finfo(dtype).eps / 2 if dtype != torch.float32 else 0.0
+
+
+def bits(t):
+    return t.contiguous().view(torch.int32 if t.dtype == torch.float32 else torch.int16)
+
+
+def same(a, b):
+    return torch.equal(bits(a.cpu()), bits(b.cpu()))
+
+
+# ---- dropout ------------------------------------------------------------------
+
+KEY = dict(seed=0x123456789ABCDEF1, rnd=77, worker=5, site=3)
+
+
+def expected_dropout(x, p, residual=None, seed=1, rnd=0, worker=0, site=0):
+    """On the CPU, from fp32 operations in the documented order (each correctly
+    rounded, so the bits are determined)."""
+    x = x.cpu().float()
+    t = ref.threshold(p)
+    d = torch.from_numpy(ref.dithers(x.numel(), seed, rnd, worker, site)).reshape(x.shape)
+    scale = torch.tensor(0.0 if t == 65536 else 65536.0 / (65536 - t), dtype=torch.float32)
+    y = torch.where(d >= t, x * scale, torch.zeros(()))
+    return y if residual is None else residual.cpu().float() + y
+
+
+def randn(shape, dtype, seed=0):
+    g = torch.Generator().manual_seed(seed)
+    return torch.randn(shape, generator=g).to(dtype).cuda()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("with_residual", [False, True])
+@pytest.mark.parametrize("shape", [(1,), (7,), (8,), (9,), (3, 5), (64, 8), (255,), (33, 72), (17, 1337), (2, 3, 4100),
+                                   (), (0,), (4, 0)])
+def test_dropout_bits(shape, with_residual, dtype):
+    x = randn(shape, dtype)
+    r = randn(shape, dtype, 1) if with_residual else None
+    y = dq.dropout(x, 0.3, residual=r, **KEY)
+    assert y.shape == x.shape and y.dtype == dtype
+    assert same(y, expected_dropout(x, 0.3, r, **KEY).to(dtype))
+
+
+@pytest.mark.parametrize("p", [0.0, 1e-9, 1 / 65536, 0.1, 0.5, 0.9, 65535 / 65536, 1.0])
+@pytest.mark.parametrize("with_residual", [False, True])
+def test_dropout_rates(p, with_residual):
+    x, r = randn((5000,), torch.float32), randn((5000,), torch.float32, 1) if with_residual else None
+    y = dq.dropout(x, p, residual=r, **KEY)
+    assert same(y, expected_dropout(x, p, r, **KEY))
+    if p == 1.0 and r is not None:
+        assert torch.equal(y, r)
+    if p < 1e-8 and r is None:
+        assert torch.equal(y, x)
+
+
+def test_dropout_keeps_the_mean_and_the_rate():
+    n, p = 1 << 22, 0.1
+    y = dq.dropout(torch.ones(n, device="cuda"), p, **KEY)
+    t = ref.threshold(p)
+    q = 1 - t / 65536
+    kept = (y != 0).double().mean().item()
+    assert abs(kept - q) < 6 * math.sqrt(q * (1 - q) / n)            # 6 standard deviations
+    assert abs(y.double().mean().item() - 1) < 6 * math.sqrt((1 - q) / q / n)
+
+
+@pytest.mark.parametrize("changed", [dict(seed=2), dict(rnd=78), dict(worker=6), dict(site=4)])
+def test_dropout_key_parts_change_the_mask(changed):
+    x = torch.ones(4096, device="cuda")
+    key = {**KEY, **changed}
+    y = dq.dropout(x, 0.5, **key)
+    assert same(y, expected_dropout(x, 0.5, **key))
+    assert not torch.equal(y, dq.dropout(x, 0.5, **KEY))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows,cols,wide,at", [(37, 64, 128, 0), (37, 64, 128, 64), (37, 61, 128, 0), (37, 64, 67, 1),
+                                               (37, 8, 24, 8), (5, 1, 9, 2), (1024, 24, 1000, 16), (3, 2048, 4096, 0)])
+def test_dropout_views_have_the_mask_of_their_copy(rows, cols, wide, at, dtype):
+    """Row strides and alignments, of each operand on its own and of all."""
+    big, other = randn((rows, wide), dtype), randn((rows, wide), dtype, 1)
+    x, r = big[:, at:at + cols], other[:, at:at + cols]
+    want = expected_dropout(x, 0.4, r, **KEY).to(dtype)
+    for xv, rv in ((x, r), (x.contiguous(), r), (x, r.contiguous()), (x.contiguous(), r.contiguous())):
+        assert same(dq.dropout(xv, 0.4, residual=rv, **KEY), want)
+        out = torch.full((rows, wide), 7.0, dtype=dtype, device="cuda")
+        dq.dropout(xv, 0.4, residual=rv, out=out[:, at:at + cols], **KEY)
+        assert same(out[:, at:at + cols], want)
+        out[:, at:at + cols] = 7.0
+        assert bool((out == 7.0).all())                               # nothing beside the view
+    assert same(dq.dropout(x, 0.4, **KEY), expected_dropout(x, 0.4, **KEY).to(dtype))
+
+
+@pytest.mark.parametrize("off", [1, 2, 3, 5, 7])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_dropout_unaligned_pieces(off, dtype):
+    base = randn((4000,), dtype)
+    x = base[off:off + 2777]
+    out = torch.empty(4000, dtype=dtype, device="cuda")
+    assert same(dq.dropout(x, 0.4, **KEY), expected_dropout(x, 0.4, **KEY).to(dtype))
+    assert same(dq.dropout(x, 0.4, out=out[3:3 + 2777], **KEY), expected_dropout(x, 0.4, **KEY).to(dtype))
+
+
+def test_dropout_three_dimensional_and_broadcast_views():
+    x = randn((6, 4, 32), torch.bfloat16)
+    v = x[:, :, 8:24]
+    assert same(dq.dropout(v, 0.4, **KEY), expected_dropout(v, 0.4, **KEY).bfloat16())
+    b = randn((32,), torch.bfloat16).expand(6, 32)                   # row stride 0
+    assert same(dq.dropout(b, 0.4, **KEY), expected_dropout(b, 0.4, **KEY).bfloat16())
+    with pytest.raises(ValueError):
+        dq.dropout(x.transpose(1, 2), 0.4)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_dropout_in_place_and_halves_of_one_tensor(dtype):
+    x, r = randn((19, 72), dtype), randn((19, 72), dtype, 1)
+    want = expected_dropout(x, 0.4, r, **KEY).to(dtype)
+    a = x.clone()
+    assert same(dq.dropout(a, 0.4, residual=r, out=a, **KEY), want)
+    a = r.clone()
+    assert same(dq.dropout(x, 0.4, residual=a, out=a, **KEY), want)
+    wide = torch.cat((x, r), 1)
+    dq.dropout(wide[:, :72], 0.4, residual=r, out=wide[:, 72:], **KEY)
+    assert same(wide[:, 72:], want) and same(wide[:, :72], x)
+    with pytest.raises(dq.DQError):
+        dq.dropout(wide[:, :72], 0.4, out=wide[:, 1:73])
+
+
+@pytest.mark.parametrize("with_residual", [False, True])
+def test_dropped_values_do_not_leak(with_residual):
+    """Infinity and NaN at dropped places count as 0; at kept ones they pass."""
+    n = 4096
+    d = ref.dithers(n, **KEY)
+    t = ref.threshold(0.5)
+    drop = torch.from_numpy(d < t)
+    for v in (math.nan, math.inf, -math.inf):
+        x = torch.full((n,), v, device="cuda")
+        r = torch.ones(n, device="cuda") if with_residual else None
+        y = dq.dropout(x, 0.5, residual=r, **KEY).cpu()
+        assert bool((y[drop] == (1.0 if with_residual else 0.0)).all())
+        assert not bool(torch.isfinite(y[~drop]).any())
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_dropout_gradient(dtype):
+    """The gradient is the mask times the scale: the formula's, the operator's
+    own differences (exact: it is linear, and powers of two pass it), and equal
+    for a residual that is broadcast."""
+    x = randn((33, 40), dtype).requires_grad_()
+    r = randn((33, 40), dtype, 1).requires_grad_()
+    dy = randn((33, 40), dtype, 2)
+    y = train.dropout(x, 0.3, residual=r, **KEY)
+    gx, gr = torch.autograd.grad(y, (x, r), dy)
+    assert same(gx, expected_dropout(dy, 0.3, **KEY).to(dtype)) and same(gr, dy)
+    zero = torch.zeros_like(x)
+    step = dq.dropout(zero + 1, 0.3, **KEY)                            # f(0 + 1) - f(0)
+    assert same(torch.autograd.grad(train.dropout(x, 0.3, **KEY).sum(), x)[0], step)
+    row = randn((40,), dtype, 3).requires_grad_()
+    y = train.dropout(x, 0.3, residual=row.expand(33, 40), **KEY)
+    g, = torch.autograd.grad(y, row, torch.ones_like(dy))
+    assert torch.equal(g.float(), torch.full((40,), 33.0, device="cuda"))
+    y = train.dropout(row.expand(33, 40), 0.3, **KEY)                  # rows at stride 0
+    g, = torch.autograd.grad(y.float().sum(), row)
+    want = expected_dropout(torch.ones(33, 40), 0.3, **KEY).to(dtype).double().sum(0)
+    assert torch.allclose(g.double().cpu(), want, rtol=2 * torch.finfo(dtype).eps, atol=0)
+
+
+def test_dropout_needs_grad_only_where_asked():
+    x, r = randn((64,), torch.float32), randn((64,), torch.float32, 1).requires_grad_()
+    train.dropout(x, 0.5, residual=r).sum().backward()
+    assert torch.equal(r.grad, torch.ones_like(r))
+    x.requires_grad_()
+    assert torch.equal(train.dropout(x, 0.5, residual=r.detach(), training=False), r.detach() + x)
+    y = train.dropout(x, 0.5)
+    g, = torch.autograd.grad(y.sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError):
+        torch.autograd.grad(g.sum(), x)
+
+
+def test_round_on_the_device_and_its_change_is_noticed():
+    x = torch.ones(2048, device="cuda").requires_grad_()
+    rnd = torch.tensor([78], dtype=torch.int32, device="cuda")
+    key = dict(seed=1, worker=2, site=9)
+    assert same(dq.dropout(x.detach(), 0.5, rnd=rnd, **key), expected_dropout(x.detach(), 0.5, rnd=78, **key))
+    rnd.fill_(-1)                                                     # 2^32 - 1
+    assert same(dq.dropout(x.detach(), 0.5, rnd=rnd, **key),
+                expected_dropout(x.detach(), 0.5, rnd=2 ** 32 - 1, **key))
+    y = train.dropout(x, 0.5, rnd=rnd, **key)
+    rnd.add_(1)
+    with pytest.raises(RuntimeError):
+        y.sum().backward()
+
+
+@pytest.mark.parametrize("bad", [dict(worker=65536), dict(worker=-1), dict(site=1 << 31), dict(rnd=1 << 32),
+                                 dict(seed=-1), dict(seed=1 << 64)])
+def test_dropout_key_is_checked(bad):
+    with pytest.raises(ValueError):
+        dq.dropout(torch.ones(8, device="cuda"), 0.5, **bad)
+
+
+def test_dropout_refuses_mixed_operands():
+    x = torch.ones(8, 8, device="cuda")
+    for bad in (x[:4], x.bfloat16(), x.cpu()):
+        with pytest.raises(ValueError):
+            dq.dropout(x, 0.5, residual=bad)
+        with pytest.raises(ValueError):
+            dq.dropout(x, 0.5, out=bad)
+    with pytest.raises(TypeError):
+        dq.dropout(x, 0.5, rnd=torch.zeros(1, device="cuda"))
+    with pytest.raises(dq.DQError):
+        dq.dropout(x, 1.5)
+
+
+@pytest.mark.slow
+def test_dropout_beyond_32_bits():
+    """2^35 + 44 bf16 elements, in place: element offsets pass 2^32, and the last
+    blocks' index, its own second counter word (64 GiB of memory)."""
+    n = (1 << 35) + 44
+    x = torch.ones(n, dtype=torch.bfloat16, device="cuda")
+    print("[dropout] 2^35 elements", flush=True)
+    dq.dropout(x, 0.5, out=x, **KEY)
+    for first, count in ((0, 4096), ((1 << 31) - 64, 4096), ((1 << 32) - 64, 4096), ((1 << 35) - 64, 108)):
+        d = ref.dithers(count, first=first, **KEY)
+        want = torch.from_numpy(np.where(d >= 32768, 2.0, 0.0)).bfloat16()
+        assert same(x[first:first + count], want), first
+
+
+def test_dropout_on_another_stream():
+    x = randn((1 << 20,), torch.bfloat16)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    y = dq.dropout(x, 0.3, stream=s, **KEY)
+    with torch.cuda.stream(s):
+        z = dq.dropout(y, 0.0)
+    torch.cuda.current_stream().wait_stream(s)
+    want = expected_dropout(x, 0.3, **KEY).bfloat16()
+    assert same(y, want) and same(z, want)
+
+
+# ---- router ---------------------------------------------------------------------
+
+def logits_of(T, E, dtype, seed=0, closed=0.0, coarse=False):
+    g = np.random.default_rng(seed * 1000 + E)
+    l = g.normal(size=(T, E)) * 2 + g.normal(size=E)
+    if coarse:
+        l = np.round(l)                                               # many ties, -0 and +0 among them
+    if closed:
+        l[g.random((T, E)) < closed] = -np.inf
+        l[::5] = -np.inf
+    return torch.from_numpy(l).to(dtype).cuda()
+
+
+def check_forward(logits, k, renorm, mask, ids, gates):
+    r = ref.Routed(logits.double().cpu().numpy(), k, renorm, None if mask is None else mask.cpu().numpy())
+    assert np.array_equal(ids.cpu().numpy(), r.ids)
+    got = gates.double().cpu().numpy()
+    assert np.array_equal(np.isnan(got), np.isnan(r.gates))
+    fine = ~np.isnan(got)
+    assert np.all(np.abs(got - r.gates)[fine] <= r.roundings * U * r.gates[fine] + 1e-37)
+    return r
+
+
+def check_stats(stats, rs):
+    """Counts and tokens exactly; sums of p within the roundings of a p and of
+    the fp32 part of its sum (at most one addition per token)."""
+    E = rs[0].l.shape[1]
+    s = stats.cpu().numpy()
+    assert np.array_equal(s[:E], sum(r.counts for r in rs))
+    assert s[2 * E] == sum(r.tokens for r in rs)
+    want = sum(r.psum for r in rs)
+    most = max(r.roundings + len(r.l) for r in rs)
+    assert np.all(np.abs(s[E:2 * E] - want) <= most * U * want + 1e-37)
+    return most
+
+
+WIDTHS = [(1, 1), (2, 2), (3, 1), (7, 7), (8, 2), (9, 4), (16, 16), (31, 5), (32, 8), (60, 4), (64, 8), (65, 6),
+          (96, 3), (128, 1), (160, 6), (192, 16), (250, 8), (256, 8), (257, 2), (384, 9), (512, 8), (513, 4),
+          (1000, 16), (1024, 10)]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("E,k", WIDTHS)
+@pytest.mark.parametrize("coarse", [False, True])
+def test_route_widths(E, k, coarse, dtype):
+    for T, renorm in ((1, True), (67, False), (131, True)):
+        l = logits_of(T, E, dtype, T, coarse=coarse)
+        ids, gates, stats = dq.route(l, k, renorm)
+        r = check_forward(l, k, renorm, None, ids, gates)
+        check_stats(stats, [r])
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("E,k", [(8, 2), (60, 4), (64, 8), (256, 8), (1024, 16), (7, 7)])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_route_masks_and_closed_experts(E, k, renorm, dtype):
+    """Tokens left out (their logits NaN), experts closed to some tokens, tokens
+    with every expert closed, fewer open experts than choices."""
+    T = 203
+    l = logits_of(T, E, dtype, closed=0.5)
+    l[7] = -math.inf
+    l[7, E - 1] = 0.5                                                  # one open expert, the last
+    mask = torch.arange(T, device="cuda") % 3 != 1
+    l[1] = math.nan
+    l[4] = math.inf
+    for m in (mask, mask.to(torch.uint8) * 9):
+        ids, gates, stats = dq.route(l, k, renorm, m)
+        clean = l.clone()
+        clean[1] = clean[4] = 0
+        r = check_forward(clean, k, renorm, mask, ids, gates)
+        check_stats(stats, [r])
+        assert ids[1].eq(-1).all() and gates[4].eq(0).all() and ids[5].eq(-1).all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_route_everything_left_out(dtype):
+    l = torch.full((9, 12), -math.inf, dtype=dtype, device="cuda")
+    for kw in (dict(), dict(mask=torch.zeros(9, dtype=torch.bool, device="cuda"))):
+        x = l if not kw else torch.full_like(l, math.nan)
+        ids, gates, stats = dq.route(x, 3, **kw)
+        assert ids.eq(-1).all() and gates.eq(0).all() and stats.eq(0).all()
+        loss, coef, counts = dq.balance(stats, 3)
+        assert loss.eq(0).all() and coef.eq(0).all() and counts.eq(0).all()
+        d = dq.route_backward(x, ids, torch.full((9, 3), math.nan, device="cuda"), coef, **kw)
+        assert d.eq(0).all()
+    empty = torch.empty(0, 12, dtype=dtype, device="cuda")
+    ids, gates, stats = dq.route(empty, 3)
+    assert ids.shape == (0, 3) and stats.eq(0).all()
+    assert dq.route_backward(empty, ids).shape == (0, 12)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("E", [5, 64, 300])
+def test_route_nan_and_infinity(E, dtype):
+    """NaN first (either sign), then +inf; the row's gates and its gradient are
+    NaN, other rows are untouched, and the loss is NaN."""
+    l = logits_of(6, E, dtype)
+    l[1, 3] = math.nan
+    l[2, E - 1] = -math.nan
+    l[3, 2] = math.inf
+    l[4, 4] = math.nan
+    l[4, 1] = math.inf
+    l[4, 0] = -math.inf
+    ids, gates, stats = dq.route(l, 3)
+    r = check_forward(l, 3, True, None, ids, gates)
+    assert ids[4, 0] == 4 and ids[4, 1] == 1
+    assert np.array_equal(stats.cpu().numpy()[:E], r.counts) and stats[2 * E] == 6
+    loss, coef, _ = dq.balance(stats, 3)
+    assert loss.isnan().all()
+    d = dq.route_backward(l, ids, torch.ones(6, 3, device="cuda"), torch.ones(E, device="cuda"))
+    assert d[1:5].isnan().all() and not d[0].isnan().any() and not d[5].isnan().any()
+    nan = torch.full((2, E), math.nan, dtype=dtype, device="cuda")
+    ids, gates, _ = dq.route(nan, 2)
+    assert ids.tolist() == [[0, 1], [0, 1]] and gates.isnan().all()
+
+
+def test_route_extreme_logits():
+    """Values near the ends of fp32, and rows that are all equal."""
+    big = torch.finfo(torch.float32).max
+    l = torch.tensor([[big, -big, 0.0, big], [-big, -big, -big, -big], [88.0, -88.0, 87.5, 0.0],
+                      [-0.0, 0.0, -0.0, 0.0], [1e-40, -1e-40, 0.0, 1e-39]], device="cuda")
+    ids, gates, stats = dq.route(l, 2)
+    assert ids.tolist() == [[0, 3], [0, 1], [0, 2], [0, 1], [3, 0]]
+    assert torch.equal(gates[0], torch.tensor([0.5, 0.5], device="cuda"))
+    assert torch.equal(gates[1], torch.tensor([0.5, 0.5], device="cuda"))
+    assert stats[8] == 5 and bool(torch.isfinite(stats).all())
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("E,wide,at", [(64, 64, 0), (64, 128, 64), (64, 67, 1), (60, 64, 0), (256, 264, 8), (9, 10, 1)])
+def test_route_strided_rows(E, wide, at, dtype):
+    big = logits_of(150, wide, dtype)
+    l = big[:, at:at + E]
+    k = 4
+    ids, gates, stats = dq.route(l, k)
+    r = check_forward(l, k, True, None, ids, gates)
+    i2, g2, s2 = dq.route(l.contiguous(), k)
+    assert torch.equal(ids, i2)
+    dg = randn((150, k), torch.float32)
+    coef = dq.balance(stats, k)[1]
+    d = dq.route_backward(l, ids, dg, coef)
+    check_gradient(d, r, dg, coef, 1.0, dtype)
+    out = torch.full((150, wide), 7.0, dtype=dtype, device="cuda")
+    dq.route_backward(l, ids, dg, coef, out=out[:, at:at + E])
+    assert same(out[:, at:at + E], d)
+    out[:, at:at + E] = 7.0
+    assert bool((out == 7.0).all())
+    again = l.clone()
+    assert same(dq.route_backward(again, ids, dg, coef, out=again), d)
+    row = l[:1].expand(70, E)                                          # all tokens alike
+    i3 = dq.route(row, k)[0]
+    assert torch.equal(i3, ids[:1].expand(70, k))
+
+
+def check_gradient(d, r, dgates, coef, dloss, dtype):
+    want, mag = ref.backward(r, None if dgates is None else dgates.double().cpu().numpy(),
+                             None if coef is None else coef.double().cpu().numpy(), dloss)
+    got = d.double().cpu().numpy()
+    # beside the roundings of p and the gates: the sums of products (at most 40
+    # deep) and four operations; bf16's own smallest step at 0
+    tol = 2 * (r.roundings + 44) * U * mag + half_step(dtype) * np.abs(want) + 1e-37
+    assert np.all(np.abs(got - want) <= tol * (1 + half_step(dtype)))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("E,k", WIDTHS)
+def test_route_backward_widths(E, k, dtype):
+    for T, renorm in ((1, False), (67, True), (131, False)):
+        l = logits_of(T, E, dtype, T, closed=0.2 if T > 1 else 0.0)
+        mask = torch.arange(T, device="cuda") % 4 != 3
+        ids, gates, stats = dq.route(l, k, renorm, mask)
+        r = check_forward(l, k, renorm, mask, ids, gates)
+        coef = dq.balance(stats, k)[1]
+        dg = randn((T, k), torch.float32, E)
+        dloss = torch.tensor([0.37], device="cuda")
+        for kw in (dict(dgates=dg), dict(coef=coef), dict(dgates=dg, coef=coef, dloss=dloss), dict()):
+            d = dq.route_backward(l, ids, renorm=renorm, mask=mask, **kw)
+            check_gradient(d, r, kw.get("dgates"), kw.get("coef"), 0.37 if "dloss" in kw else 1.0, dtype)
+
+
+def test_gradient_against_differences():
+    """Directional derivatives of the GPU's own forward pass.  Central
+    differences with h = 2^-7 are off by h^2/6 times the third derivative (at most
+    a few times the scale of the direction, |v| <= 1: below 4e-4 of it) and by the
+    outputs' roundings over 2 h (2^-24 x 64 x 400 gates / 2^-6: 2e-3 at most; they average)."""
+    T, E, k = 40, 24, 3
+    l = logits_of(T, E, torch.float32)
+    w = randn((T, k), torch.float32, 5)
+    x = l.clone().requires_grad_()
+    r = train.route(x, k, renorm=True)
+    g, = torch.autograd.grad((r.gates * w).sum() + 3 * r.loss, x)
+    for seed in range(4):
+        v = torch.rand(T, E, generator=torch.Generator().manual_seed(seed)).cuda() * 2 - 1
+        h = 2.0 ** -7
+
+        def value(sign):
+            ids, gates, stats = dq.route(l + sign * h * v, k)
+            # the same choices: the gates in the first call's order (ids may swap)
+            full = torch.zeros(T, E, dtype=torch.float64)
+            full.scatter_(1, ids.long().cpu(), gates.double().cpu())
+            stay = torch.equal(ids.sort(1).values, r.ids.sort(1).values)
+            s = stats.double()
+            s[:E] = r.counts.double()                                # counts have no derivative
+            loss = (s[:E] * s[E:2 * E]).sum().item() * E / (k * s[2 * E].item() ** 2)
+            return (full.gather(1, r.ids.long().cpu()) * w.double().cpu()).sum().item() + 3 * loss, stay
+
+        (up, a), (down, b) = value(1), value(-1)
+        if not (a and b):
+            continue                                                 # a choice changed: no derivative there
+        assert abs((up - down) / (2 * h) - (g * v).double().sum().item()) < 5e-3
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_route_folds_workers_in_order(dtype):
+    E, k = 48, 4
+    ls = [logits_of(T, E, dtype, T) for T in (300, 1, 77, 0, 512)]
+    stats, rs = None, []
+    for l in ls:
+        ids, gates, stats = dq.route(l, k, stats=stats)
+        rs.append(check_forward(l, k, True, None, ids, gates) if len(l) else None)
+    rs = [r for r in rs if r is not None]
+    most = check_stats(stats, rs)
+    loss, coef, counts = dq.balance(stats, k)
+    wl, wc, wn, _ = ref.balance(rs)
+    assert np.array_equal(counts.cpu().numpy(), wn)
+    assert np.all(np.abs(coef.double().cpu().numpy() - wc) <= 2 * U * wc)
+    assert abs(loss.item() - wl) <= (most + 4) * U * wl
+    # processes: the sum of their statistics
+    parts = [dq.route(l, k)[2] for l in ls]
+    total = sum(parts[1:], parts[0].clone())
+    assert torch.equal(dq.balance(total, k)[2], counts)
+    assert abs(dq.balance(total, k)[0].item() - wl) <= (most + 4) * U * wl
+    # a buffer that is set anew
+    stats.fill_(math.nan)
+    s = dq.route(ls[0], k, stats=stats, accumulate=False)[2]
+    assert s is stats and torch.equal(s, parts[0])
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("T,E,k", [(4099, 60, 4), (20000, 8, 2), (33000, 64, 8), (9000, 256, 8)])
+def test_route_many_tokens_and_the_same_bits_again(T, E, k, dtype):
+    """Beyond one pass of the grid, against torch in fp64 on the CPU."""
+    l = logits_of(T, E, dtype)
+    ids, gates, stats = dq.route(l, k, False)
+    x = l.double().cpu()
+    order = torch.sort(x, dim=1, descending=True, stable=True)[1][:, :k]
+    p = torch.softmax(x, 1)
+    assert torch.equal(ids.long().cpu(), order)
+    span = (x.max() - x.min()).item()
+    c = 2 * (3 * span + 48)
+    want = p.gather(1, order)
+    assert bool(((gates.double().cpu() - want).abs() <= c * U * want).all())
+    s = stats.cpu()
+    assert torch.equal(s[:E], torch.bincount(order.reshape(-1), minlength=E).double()) and s[2 * E] == T
+    assert bool(((s[E:2 * E] - p.sum(0)).abs() <= (c + T) * U * p.sum(0)).all())
+    again = dq.route(l, k, False)
+    assert torch.equal(ids, again[0]) and torch.equal(gates, again[1]) and torch.equal(stats, again[2])
+    coef = dq.balance(stats, k)[1]
+    dg = randn((T, k), torch.float32)
+    d = dq.route_backward(l, ids, dg, coef, renorm=False)
+    assert same(d, dq.route_backward(l, ids, dg, coef, renorm=False))
+    up = coef.double().cpu().expand(T, E).clone().scatter_add_(1, order, dg.double().cpu())
+    want = p * (up - (p * up).sum(1, keepdim=True))
+    mag = p * (up.abs() + (p * up.abs()).sum(1, keepdim=True))
+    err = (d.double().cpu() - want).abs()
+    assert bool((err <= 2 * (c + 44) * U * mag + half_step(dtype) * want.abs() * 1.01 + 1e-37).all())
+
+
+def test_route_loss_of_many_tokens():
+    """fp32 sums stay short: 2^20 tokens, loss against fp64."""
+    T, E, k = 1 << 20, 16, 2
+    g = torch.Generator(device="cuda").manual_seed(3)
+    l = torch.randn(T, E, generator=g, device="cuda")
+    _, _, stats = dq.route(l, k)
+    p = torch.softmax(l.double(), 1).sum(0)
+    assert bool(((stats[E:2 * E] - p).abs() <= 1e-6 * p).all())
+
+
+def test_route_refuses():
+    l = torch.zeros(8, 16, device="cuda")
+    ids, gates, stats = dq.route(l, 2)
+    for call in (lambda: dq.route(l[0], 2), lambda: dq.route(l.t(), 2), lambda: dq.route(l, 2, mask=stats.bool()[:7]),
+                 lambda: dq.route(l, 2, mask=torch.zeros(8, dtype=torch.bool)),
+                 lambda: dq.route(l, 2, stats=stats[:-2]), lambda: dq.route(l, 2, accumulate=True),
+                 lambda: dq.route(l, 2, ids=ids[:, :1]), lambda: dq.route(l, 2, gates=gates.t()),
+                 lambda: dq.route_backward(l, ids[:4]), lambda: dq.route_backward(l, ids, gates[:4]),
+                 lambda: dq.route_backward(l, ids, coef=stats[:15].float()),
+                 lambda: dq.route_backward(l, ids, out=l.bfloat16()),
+                 lambda: dq.route_backward(l, ids, out=l[:4])):
+        with pytest.raises(ValueError):
+            call()
+    for call in (lambda: dq.route(l, 2, mask=torch.zeros(8, device="cuda")), lambda: dq.route(l, 2, ids=ids.long()),
+                 lambda: dq.route(l, 2, stats=stats.float()), lambda: dq.route_backward(l, ids.long()),
+                 lambda: dq.route_backward(l, ids, coef=torch.zeros(16, dtype=torch.float64, device="cuda"))):
+        with pytest.raises(TypeError):
+            call()
+    for call in (lambda: dq.route(l, 17), lambda: dq.route(l, 0), lambda: dq.balance(stats, 17),
+                 lambda: dq.route(torch.zeros(2, 1025, device="cuda"), 2),
+                 lambda: dq.route(torch.zeros(2, 64, device="cuda"), 17),
+                 lambda: dq.route_backward(l[1:], ids[1:], out=l[:-1])):
+        with pytest.raises(dq.DQError):
+            call()
+
+
+def test_ids_out_of_range_are_no_choice():
+    """The gradient does not index beyond the experts whatever ids hold."""
+    E = 20
+    l = logits_of(3, E, torch.float32)
+    ids = torch.tensor([[1, E], [-7, 2 ** 31 - 1], [-2 ** 31, 4]], dtype=torch.int32, device="cuda")
+    dg = torch.ones(3, 2, device="cuda")
+    a = dq.route_backward(l, ids, dg, renorm=False)
+    b = dq.route_backward(l, torch.where((ids >= 0) & (ids < E), ids, -1), dg, renorm=False)
+    assert torch.equal(a, b)
+
+
+# ---- autograd, streams, graphs -----------------------------------------------------
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_route_autograd(dtype):
+    E, k = 40, 4
+    ls = [logits_of(T, E, dtype, T).requires_grad_() for T in (50, 33)]
+    masks = [None, torch.arange(33, device="cuda") % 5 != 0]
+    dgs = [randn((50, k), torch.float32), randn((33, k), torch.float32, 1)]
+    dloss = torch.tensor([0.21], device="cuda")
+    r = train.route(ls, k, masks=masks)
+    rs = [check_forward(l.detach(), k, True, m, i, g.detach()) for l, m, i, g in zip(ls, masks, r.ids, r.gates)]
+    grads = torch.autograd.grad([*r.gates, r.loss], ls, [*dgs, dloss], retain_graph=True)
+    for g, rr, dg in zip(grads, rs, dgs):
+        check_gradient(g, rr, dg, r.coef, 0.21, dtype)
+    # the loss alone, one worker's gates alone
+    for g, rr in zip(torch.autograd.grad(r.loss, ls, retain_graph=True), rs):
+        check_gradient(g, rr, None, r.coef, 1.0, dtype)
+    g = torch.autograd.grad(r.gates[1].sum(), ls, retain_graph=True, allow_unused=True)
+    assert g[0] is None
+    check_gradient(g[1], rs[1], torch.ones(33, k), None, 1.0, dtype)
+    assert not r.ids[0].requires_grad and not r.counts.requires_grad and not r.coef.requires_grad
+    # one tensor, no list; a transposed one is copied
+    one = train.route(ls[0].detach().t().contiguous().t().requires_grad_(), k)
+    assert torch.equal(one.ids, r.ids[0])
+    one.loss.backward()
+
+
+def test_two_forwards_before_their_backwards():
+    """Nothing is shared between calls: gradients do not depend on what ran in
+    between."""
+    a, b = (logits_of(T, 24, torch.float32, T).requires_grad_() for T in (64, 96))
+    want = [torch.autograd.grad(train.route(x, 2).loss, x)[0] for x in (a, b)]
+    ra, rb = train.route(a, 2), train.route(b, 2)
+    ga, gb = torch.autograd.grad(ra.loss, a)[0], torch.autograd.grad(rb.loss, b)[0]
+    assert torch.equal(ga, want[0]) and torch.equal(gb, want[1])
+
+
+def test_reduce_sees_the_statistics():
+    l = logits_of(30, 12, torch.float32).requires_grad_()
+    doubled = train.route(l, 2, reduce=lambda s: s.mul_(2))              # as if a second rank had the same
+    alone = train.route(l, 2)
+    assert torch.equal(doubled.counts, 2 * alone.counts)
+    assert abs(doubled.loss.item() - alone.loss.item()) <= 4 * U * alone.loss.item()
+
+
+def test_route_on_another_stream():
+    l = logits_of(5000, 64, torch.bfloat16)
+    want = dq.route(l, 8)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = dq.route(l, 8, stream=s)
+    loss = dq.balance(got[2], 8, stream=s)
+    d = dq.route_backward(l, got[0], coef=loss[1], stream=s)
+    torch.cuda.current_stream().wait_stream(s)
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    assert same(d, dq.route_backward(l, want[0], coef=dq.balance(want[2], 8)[1]))
+
+
+def test_step_in_graph_replays():
+    """Forward and backward of the router and of dropout with the round on the
+    device, captured while an eager graph of the same leaf lives, replayed with
+    new inputs and rounds between eager work."""
+    T, E, k, H = 700, 64, 4, 96
+    l, x = logits_of(T, E, torch.bfloat16), randn((T, H), torch.bfloat16)
+    res, dg = randn((T, H), torch.bfloat16, 1), randn((T, k), torch.float32, 2)
+    rnd = torch.zeros(1, dtype=torch.int32, device="cuda")
+    dloss = torch.full((1,), 0.01, device="cuda")
+    leaf = l.requires_grad_()
+    alive = train.route(leaf, k)                                       # an eager graph of the leaf
+
+    def step(out=None):
+        ids, gates, stats = dq.route(l.detach(), k)
+        loss, coef, counts = dq.balance(stats, k)
+        y = dq.dropout(x, 0.1, residual=res, rnd=rnd, worker=1)
+        d = dq.route_backward(l.detach(), ids, dg, coef, dloss)
+        dx = dq.dropout_backward(y, 0.1, rnd=rnd, worker=1)
+        return ids, gates, stats, loss, coef, counts, y, d, dx
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = step()
+    torch.cuda.synchronize()
+    for rep in range(4):
+        with torch.no_grad():
+            l.copy_(logits_of(T, E, torch.bfloat16, 10 + rep))
+        rnd.fill_(rep)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(held, step()):
+            assert torch.equal(a, b), rep
+    assert alive.loss.item() > 0

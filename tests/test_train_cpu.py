@@ -1,0 +1,216 @@
+"""Training-step operators without a GPU: the plain forms that the GPU tests
+compare with (dithers against the oracle's Philox, gradients against
+differences), and the argument checks of the C ABI and the binding."""
+import ctypes as C
+
+import numpy as np
+import pytest
+import torch
+
+import train_ref as ref
+from compressed_hop_gradient_amd import dq, train
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return dq.lib()
+
+
+# ---- the plain forms -----------------------------------------------------------
+
+@pytest.mark.parametrize("block,seed,rnd,worker,site", [
+    (0, 1, 0, 0, 0), (5, 0x123456789ABCDEF0, 7, 3, 2), ((1 << 32) + 9, 2 ** 64 - 1, 2 ** 32 - 1, 65535, 2 ** 31 - 1)])
+def test_dithers_are_the_oracles_philox(block, seed, rnd, worker, site):
+    got = ref.dithers(24, seed, rnd, worker, site, first=8 * block)
+    for i in range(3):
+        assert list(got[8 * i:8 * i + 8]) == ref.dithers_by_oracle(block + i, seed, rnd, worker, site)
+
+
+def test_dithers_are_uniform_and_differ_by_worker_round_and_site():
+    n = 1 << 16
+    base = ref.dithers(n, 1, 0, 0, 0)
+    # each of 16 ranges holds n / 16 of them, within 6 standard deviations
+    h = np.bincount(base >> 12, minlength=16)
+    assert np.all(np.abs(h - n / 16) < 6 * np.sqrt(n / 16))
+    for other in (ref.dithers(n, 2, 0, 0, 0), ref.dithers(n, 1, 1, 0, 0), ref.dithers(n, 1, 0, 1, 0),
+                  ref.dithers(n, 1, 0, 0, 1)):
+        assert (other == base).mean() < 0.001
+        assert abs(np.corrcoef(other, base)[0, 1]) < 6 / np.sqrt(n)
+
+
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("E,k", [(5, 1), (9, 3), (16, 16)])
+def test_reference_gradient_against_differences(E, k, renorm):
+    """d/dl of sum_w (gates . dg) + dloss * loss, the choices held fixed (they
+    change only where logits tie)."""
+    rng = np.random.default_rng(E)
+    ls = [rng.normal(size=(7, E)), rng.normal(size=(4, E))]
+    if E > k + 1:
+        ls[0][2, 1] = -np.inf
+    ls[0][3] = -np.inf
+    masks = [np.array([1, 1, 1, 1, 1, 0, 1]), None]
+    dgs = [rng.normal(size=(len(l), k)) for l in ls]
+    dloss = 0.7
+
+    def value(x):
+        rs = [ref.Routed(l, k, renorm, m) for l, m in zip(x, masks)]
+        return sum((r.gates * np.where(r.ids >= 0, d, 0)).sum() for r, d in zip(rs, dgs)) + dloss * ref.balance(rs)[0]
+
+    rs = [ref.Routed(l, k, renorm, m) for l, m in zip(ls, masks)]
+    coef = ref.balance(rs)[1]
+    h = 1e-5
+    for w in range(2):
+        g, _ = ref.backward(rs[w], dgs[w], coef, dloss)
+        for t in range(len(ls[w])):
+            for j in range(E):
+                if not np.isfinite(ls[w][t, j]):
+                    assert g[t, j] == 0
+                    continue
+                up, down = [l.copy() for l in ls], [l.copy() for l in ls]
+                up[w][t, j] += h
+                down[w][t, j] -= h
+                # central differences: h^2 f''' / 6 and 2^-53 / h, both below 1e-9 here
+                assert abs((value(up) - value(down)) / (2 * h) - g[t, j]) < 1e-8
+
+
+def test_balance_is_one_when_balanced():
+    l = np.full((8, 4), -20.0)
+    l[np.arange(8), np.arange(8) % 4] = 20.0
+    assert abs(ref.balance([ref.Routed(l, 1)])[0] - 1.0) < 1e-12
+    l[:] = -20.0
+    l[:, 0] = 20.0
+    assert abs(ref.balance([ref.Routed(l, 1)])[0] - 4.0) < 1e-12      # all on one of four
+
+
+# ---- refusals of the C ABI -------------------------------------------------------
+
+FAKE = 1 << 20      # never read: every call below fails its checks, or has nothing to do
+
+
+def _dropout(lib, x=FAKE, res=None, y=4 * FAKE, kind=dq.BF16, rows=4, cols=64, xs=64, rs=64, ys=64, p=0.1, seed=1,
+             rnd=0, d_round=None, worker=0, site=0):
+    return lib.dq_dropout(x, res, y, kind, rows, cols, xs, rs, ys, p, seed, rnd, d_round, worker, site, None)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(kind=dq.PACKED), dict(kind=-1), dict(rows=-1), dict(cols=-1), dict(p=-0.1), dict(p=1.1),
+    dict(p=float("nan")), dict(worker=-1), dict(worker=65536), dict(site=1 << 31), dict(rows=1 << 40, cols=1 << 40),
+    dict(rows=1 << 26, cols=1 << 25), dict(xs=-1), dict(rs=-1), dict(ys=63), dict(ys=0), dict(xs=1 << 51),
+    dict(x=FAKE + 1), dict(y=4 * FAKE + 1), dict(res=FAKE + 1), dict(d_round=FAKE + 2),
+    dict(kind=dq.F32, x=FAKE + 2),
+    # outputs that meet an operand other than element on element
+    dict(y=FAKE + 2), dict(y=FAKE + 128), dict(y=FAKE, xs=128), dict(y=FAKE + 2, rows=1), dict(res=4 * FAKE + 16),
+    dict(y=FAKE + 126, xs=127, ys=127), dict(xs=0, x=4 * FAKE + 64)])
+def test_dropout_refuses(lib, bad):
+    assert _dropout(lib, **bad) == dq.DQ_EINVAL
+
+
+def test_dropout_null_and_empty(lib):
+    assert _dropout(lib, x=None) == dq.DQ_ENULL
+    assert _dropout(lib, y=None) == dq.DQ_ENULL
+    assert _dropout(lib, rows=0) == dq.DQ_OK
+    assert _dropout(lib, cols=0, x=None, y=None, ys=0) == dq.DQ_OK
+
+
+def _route(lib, l=FAKE, kind=dq.BF16, T=8, E=16, stride=16, mask=None, k=2, flags=1, ids=4 * FAKE, gates=5 * FAKE,
+           stats=6 * FAKE, ws=7 * FAKE, nbytes=1 << 20):
+    return lib.dq_route(l, kind, T, E, stride, mask, k, flags, ids, gates, stats, ws, nbytes, None)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(kind=dq.PACKED), dict(T=-1), dict(T=(1 << 40) + 1), dict(E=0), dict(E=1025), dict(stride=-1), dict(k=0),
+    dict(k=17, E=32), dict(k=3, E=2), dict(flags=4), dict(l=FAKE + 1), dict(kind=dq.F32, l=FAKE + 2),
+    dict(ids=4 * FAKE + 2), dict(gates=5 * FAKE + 2), dict(stats=6 * FAKE + 4)])
+def test_route_refuses(lib, bad):
+    assert _route(lib, **bad) == dq.DQ_EINVAL
+
+
+def test_route_null_and_workspace(lib):
+    for name in ("l", "ids", "gates", "stats"):
+        assert _route(lib, **{name: None}) == dq.DQ_ENULL
+    need = lib.dq_route_workspace_bytes(8, 16)
+    assert need > 0
+    assert _route(lib, nbytes=need - 1) == dq.DQ_EWORKSPACE
+    assert _route(lib, ws=None) == dq.DQ_EWORKSPACE
+    assert _route(lib, ws=7 * FAKE + 128) == dq.DQ_EWORKSPACE
+    for args in ((-1, 16), (8, 0), (8, 1025), ((1 << 40) + 1, 16)):
+        assert lib.dq_route_workspace_bytes(*args) == 0
+    # bounded however many tokens there are
+    assert lib.dq_route_workspace_bytes(1 << 40, 1024) < 64 << 20
+
+
+def test_balance_refuses(lib):
+    ok = (FAKE, 16, 2, 2 * FAKE, 3 * FAKE, 4 * FAKE, None)
+    for i, v, rc in ((0, None, dq.DQ_ENULL), (0, FAKE + 4, dq.DQ_EINVAL), (1, 0, dq.DQ_EINVAL),
+                     (1, 1025, dq.DQ_EINVAL), (2, 0, dq.DQ_EINVAL), (2, 17, dq.DQ_EINVAL),
+                     (3, FAKE + 2, dq.DQ_EINVAL), (4, FAKE + 2, dq.DQ_EINVAL), (5, FAKE + 4, dq.DQ_EINVAL)):
+        args = list(ok)
+        args[i] = v
+        assert lib.dq_balance(*args) == rc, (i, v)
+
+
+def _backward(lib, l=FAKE, kind=dq.BF16, T=8, E=16, stride=16, mask=None, k=2, flags=1, ids=4 * FAKE, dg=5 * FAKE,
+              coef=6 * FAKE, dloss=7 * FAKE, out=8 * FAKE, dstride=16):
+    return lib.dq_route_backward(l, kind, T, E, stride, mask, k, flags, ids, dg, coef, dloss, out, dstride, None)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(kind=7), dict(T=-1), dict(E=0), dict(E=1025), dict(k=0), dict(k=17, E=32), dict(flags=2), dict(dstride=15),
+    dict(l=FAKE + 1), dict(out=8 * FAKE + 1), dict(ids=4 * FAKE + 1), dict(dg=5 * FAKE + 2), dict(coef=6 * FAKE + 2),
+    dict(dloss=7 * FAKE + 2), dict(out=FAKE + 2), dict(out=FAKE, stride=32), dict(dstride=1 << 41)])
+def test_route_backward_refuses(lib, bad):
+    assert _backward(lib, **bad) == dq.DQ_EINVAL
+
+
+def test_route_backward_null_and_empty(lib):
+    for name in ("l", "ids", "out"):
+        assert _backward(lib, **{name: None}) == dq.DQ_ENULL
+    assert _backward(lib, T=0, l=None, ids=None, out=None) == dq.DQ_OK
+
+
+# ---- refusals of the binding -----------------------------------------------------
+
+def test_binding_refuses_host_tensors_and_types():
+    x = torch.zeros(4, 8)
+    for call in (lambda: dq.dropout(x, 0.1), lambda: dq.dropout_backward(x, 0.1), lambda: dq.route(x, 2),
+                 lambda: dq.balance(torch.zeros(17, dtype=torch.float64), 2),
+                 lambda: dq.route_backward(x, torch.zeros(4, 2, dtype=torch.int32)),
+                 lambda: train.dropout(x, 0.1), lambda: train.route(x, 2), lambda: train.route([x, x], 2)):
+        with pytest.raises(ValueError):
+            call()
+    for bad in (x.half(), x.double(), x.int(), None, 3.0):
+        with pytest.raises(TypeError):
+            dq.dropout(bad, 0.1)
+        with pytest.raises(TypeError):
+            dq.route(bad, 2)
+    for bad in (torch.zeros(4, dtype=torch.float64), torch.zeros(1, dtype=torch.float64), torch.zeros(3, 3), None):
+        with pytest.raises(ValueError):
+            dq.balance(bad, 2)
+
+
+def test_rows_of_views():
+    x = torch.zeros(6, 4, 32)
+    assert dq._rows(x, "x") == (1, 768, 768)
+    assert dq._rows(x[:, :, 3:9], "x") == (24, 6, 32)
+    assert dq._rows(x[:, 1:2, 3:9], "x") == (6, 6, 128)
+    assert dq._rows(x[2, :, :5], "x") == (4, 5, 32)
+    assert dq._rows(x[:, :, :1], "x") == (24, 1, 32)
+    assert dq._rows(torch.zeros(32).expand(6, 32), "x") == (6, 32, 0)
+    assert dq._rows(x[:0, :, :5], "x")[1] == 0
+    for bad in (x.transpose(1, 2), x[:, :2, :5], x[:, :, ::2], x[:, :3], torch.zeros(1).expand(5)):
+        with pytest.raises(ValueError):
+            dq._rows(bad, "x")
+
+
+def test_route_wrapper_checks_the_list():
+    with pytest.raises(ValueError):
+        train.route([], 2)
+    with pytest.raises(ValueError):
+        train.route([torch.zeros(4, 8)], 2, masks=[None, None])
+    with pytest.raises(ValueError):
+        train.route([torch.zeros(4, 8), torch.zeros(4, 9)], 2)
+
+
+def test_eval_dropout_is_the_input():
+    x = torch.zeros(4, 8)
+    assert train.dropout(x, 0.5, training=False) is x
