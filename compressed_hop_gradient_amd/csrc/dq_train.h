@@ -21,6 +21,20 @@ struct DropoutArgs {
     const uint32_t *d_round;
 };
 
+// Statistics of one router call: a row per block of its kernel.
+struct RoutePart {
+    float *psum;            // [nblk][E] summed probabilities
+    uint32_t *count;        // [nblk][E] choices
+    uint32_t *routed;       // [nblk] routed tokens
+    int32_t nblk;
+    // scratch of a balance call that folds this part first: blocks that are done
+    // (0 between calls), and their shares of the loss
+    uint32_t *done;
+    double *share;
+};
+constexpr int kRouteMaxParts = 16;
+constexpr int kBalanceColumns = 16;     // experts of a balance block
+
 struct RouteArgs {
     const void *logits;
     int64_t tokens, stride;
@@ -29,11 +43,18 @@ struct RouteArgs {
     int32_t renorm;
     int32_t *ids;
     float *gates;
-    // per-block partial statistics: float psum[nblk][E], then uint32 count[nblk][E],
-    // then uint32 routed[nblk]
-    float *psum;
-    uint32_t *count, *routed;
-    int32_t nblk;
+    RoutePart part;              // out: nblk rows of partial statistics
+};
+
+struct BalanceArgs {
+    RoutePart part[kRouteMaxParts];
+    int32_t parts;
+    const double *sums;
+    int32_t E, k;
+    double *stats;
+    float *loss, *coef;
+    int64_t *counts;
+    int32_t columns;        // experts of a block: kBalanceColumns, or all
 };
 
 struct RouteBackwardArgs {
@@ -51,9 +72,7 @@ hipError_t launch_dropout(const DropoutArgs &a, int f32, hipStream_t s);
 // blocks of the router's forward kernel for this many tokens (its partials' rows)
 int route_blocks(int64_t tokens, int E);
 hipError_t launch_route(const RouteArgs &a, int f32, hipStream_t s);
-hipError_t launch_route_fold(const RouteArgs &a, double *stats, int accumulate, hipStream_t s);
-hipError_t launch_balance(const double *stats, int E, int k, float *loss, float *coef, int64_t *counts,
-                          hipStream_t s);
+hipError_t launch_balance(const BalanceArgs &a, hipStream_t s);
 hipError_t launch_route_backward(const RouteBackwardArgs &a, int f32, hipStream_t s);
 
 }  // namespace dq

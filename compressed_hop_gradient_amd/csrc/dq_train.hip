@@ -3,6 +3,8 @@
 // statistics and gradients.  fp32 arithmetic, no contraction.
 #include "dq_train.h"
 
+#include <type_traits>
+
 namespace dq {
 
 namespace {
@@ -167,15 +169,425 @@ hipError_t dropout_access(const DropoutArgs &a, hipStream_t s) {
 // router
 // ---------------------------------------------------------------------------
 
-// Order key of a logit: the unsigned order of keys is the order of the values,
-// -0 = +0, NaN above +inf.  The key of -inf, 0x007FFFFF, is the smallest.
-__device__ __forceinline__ uint32_t order_key(float x) {
-    x += 0.0f;
-    if (x != x) return 0xFFFFFFFFu;
-    const uint32_t u = __float_as_uint(x);
-    return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+// A token's logits lie in G lanes (a power of two), 8 CH of them in each: chunk
+// i of lane g holds experts 8 (i G + g) .. + 7.  A wave takes 64 / G tokens.
+
+constexpr float kLog2e = 1.44269504088896340736f;
+
+// Logits of one chunk as loaded: -inf where there is no such expert, and for
+// a token that is left out.
+template <bool F32>
+struct Chunk;
+template <>
+struct Chunk<false> {
+    u32x4 w;
+    __device__ __forceinline__ void clear() { w = u32x4{0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u}; }
+    __device__ __forceinline__ void load(const uint16_t *p) { w = *reinterpret_cast<const u32x4 *>(p); }
+    __device__ __forceinline__ void load(const uint16_t *p, int n) {
+        for (int j = 0; j < 4; j++) {
+            if (2 * j < n) w[j] = (w[j] & 0xFFFF0000u) | p[2 * j];
+            if (2 * j + 1 < n) w[j] = (w[j] & 0xFFFFu) | (uint32_t)p[2 * j + 1] << 16;
+        }
+    }
+    __device__ __forceinline__ float at(int j) const {
+        return __uint_as_float(j & 1 ? w[j >> 1] & 0xFFFF0000u : w[j >> 1] << 16);
+    }
+};
+template <>
+struct Chunk<true> {
+    float v[8];
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int j = 0; j < 8; j++) v[j] = -INFINITY;
+    }
+    __device__ __forceinline__ void load(const float *p) {
+        const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    }
+    __device__ __forceinline__ void load(const float *p, int n) {
+#pragma unroll
+        for (int j = 0; j < 8; j++)
+            if (j < n) v[j] = p[j];
+    }
+    __device__ __forceinline__ float at(int j) const { return v[j]; }
+};
+
+// VEC: every row 16-byte aligned, E a multiple of 8
+template <bool F32, int G, int CH, bool VEC>
+__device__ __forceinline__ void load_row(Chunk<F32> c[CH], const typename Elem<F32>::type *row, int g, int E,
+                                         bool there) {
+#pragma unroll
+    for (int i = 0; i < CH; i++) {
+        const int at = 8 * (i * G + g);
+        if (VEC) {
+            if (there && at < E) c[i].load(row + at);
+            else c[i].clear();
+        } else {
+            c[i].clear();
+            if (there) c[i].load(row + at, E - at);
+        }
+    }
 }
-constexpr uint32_t kKeyMinusInf = 0x007FFFFFu;
+
+// Order key of a logit and its expert: keys are distinct, a larger logit has
+// the larger key (-0 = +0, NaN above +inf) and of equal ones the lower index.
+// bf16: the 16 ordered bits, then 16 bits of ~index.  fp32: 32 ordered bits
+// and 20 bits of ~index as the mantissa of a double in [1, 2), which has a
+// one-instruction maximum.
+template <bool F32>
+struct Key;
+template <>
+struct Key<false> {
+    typedef uint32_t type;
+    static __device__ __forceinline__ uint32_t none() { return 0; }
+    // j < 8 is flipped in the low bits of inv
+    static __device__ __forceinline__ uint32_t make(float x, uint32_t inv, int j) {
+        const uint32_t u = __float_as_uint(x);
+        const uint32_t flip = __builtin_amdgcn_bitop3_b32((int32_t)u >> 31, 0x7FFF0000u, j, 0x6A);   // (a & b) ^ c
+        return xor3(u, flip, inv ^ 0x80000000u);
+    }
+    static __device__ __forceinline__ uint32_t nan(uint32_t inv) { return 0xFFFF0000u | inv; }
+    static __device__ __forceinline__ uint32_t hi(uint32_t a, uint32_t b) { return max(a, b); }
+    static __device__ __forceinline__ uint32_t lo(uint32_t a, uint32_t b) { return min(a, b); }
+    static __device__ __forceinline__ bool open(uint32_t k) { return k >= 0x00800000u; }   // above -inf
+    static __device__ __forceinline__ int index(uint32_t k) { return (int)(~k & 0xFFFFu); }
+    static __device__ __forceinline__ float value(uint32_t k) {
+        return __uint_as_float((k & 0x80000000u ? k ^ 0x80000000u : ~k) & 0xFFFF0000u);
+    }
+    template <class F>
+    static __device__ __forceinline__ uint32_t moved(uint32_t k, F f) { return f(k); }
+};
+template <>
+struct Key<true> {
+    typedef double type;
+    static __device__ __forceinline__ double pack(uint32_t o, uint32_t inv) {
+        return __builtin_bit_cast(double, (uint64_t)(0x3FF00000u | o >> 12) << 32 | (o << 20 | inv));
+    }
+    static __device__ __forceinline__ double none() { return 1.0; }
+    static __device__ __forceinline__ double make(float x, uint32_t inv, int j) {
+        const uint32_t u = __float_as_uint(x);
+        return pack(u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u), inv ^ j);
+    }
+    static __device__ __forceinline__ double nan(uint32_t inv) { return pack(0xFFFFFFFFu, inv); }
+    static __device__ __forceinline__ double hi(double a, double b) { return __builtin_fmax(a, b); }
+    static __device__ __forceinline__ double lo(double a, double b) { return __builtin_fmin(a, b); }
+    static __device__ __forceinline__ uint32_t order(double k) {
+        return (uint32_t)(__builtin_bit_cast(uint64_t, k) >> 20);
+    }
+    static __device__ __forceinline__ bool open(double k) { return order(k) > 0x007FFFFFu; }
+    static __device__ __forceinline__ int index(double k) {
+        return (int)(~(uint32_t)__builtin_bit_cast(uint64_t, k) & 0xFFFFu);
+    }
+    static __device__ __forceinline__ float value(double k) {
+        const uint32_t o = order(k);
+        return __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o);
+    }
+    template <class F>
+    static __device__ __forceinline__ double moved(double k, F f) {
+        const uint64_t b = __builtin_bit_cast(uint64_t, k);
+        return __builtin_bit_cast(double, (uint64_t)f((uint32_t)(b >> 32)) << 32 | f((uint32_t)b));
+    }
+};
+
+// The value of the lane that holds the other half of a group of 2 D lanes:
+// lane ^ D for D = 1, 2 and beyond 8, the mirrored lane of the half row and row
+// for 4 and 8 (the same half; values are equal within a half here).
+template <int D>
+__device__ __forceinline__ uint32_t other_half(uint32_t x) {
+    if (D == 1) return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0xB1, 0xF, 0xF, false);
+    if (D == 2) return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x4E, 0xF, 0xF, false);
+    if (D == 4) return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x141, 0xF, 0xF, false);
+    if (D == 8) return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x140, 0xF, 0xF, false);
+    return (uint32_t)__shfl_xor((int)x, D, 64);
+}
+template <int D>
+__device__ __forceinline__ float other_half(float x) {
+    return __uint_as_float(other_half<D>(__float_as_uint(x)));
+}
+
+template <int G, int D = 1>
+__device__ __forceinline__ float group_max(float x) {
+    if constexpr (D < G) return group_max<G, 2 * D>(fmaxf(x, other_half<D>(x)));
+    return x;
+}
+template <int G, int D = 1>
+__device__ __forceinline__ float group_sum(float x) {
+    if constexpr (D < G) return group_sum<G, 2 * D>(x + other_half<D>(x));
+    return x;
+}
+
+// Falling lists of the KP largest keys.  Sorting: Batcher's odd-even merge
+// network; two lists: the larger of a_i and b_(KP-1-i) are the KP largest, a
+// bitonic sequence that log2 KP stages sort.
+template <bool F32, int KP>
+struct Best {
+    typedef Key<F32> K;
+    typedef typename K::type T;
+    static __device__ __forceinline__ void order(T &a, T &b) {
+        const T h = K::hi(a, b);
+        b = K::lo(a, b);
+        a = h;
+    }
+    static __device__ __forceinline__ void sort(T *v) {
+#pragma unroll
+        for (int p = 1; p < KP; p *= 2)
+#pragma unroll
+            for (int q = p; q >= 1; q /= 2)
+#pragma unroll
+                for (int j = q % p; j + q < KP; j += 2 * q)
+#pragma unroll
+                    for (int i = 0; i < q; i++)
+                        if (i + j + q < KP && (i + j) / (2 * p) == (i + j + q) / (2 * p)) order(v[i + j], v[i + j + q]);
+    }
+    static __device__ __forceinline__ void settle(T *v) {
+#pragma unroll
+        for (int d = KP / 2; d >= 1; d /= 2)
+#pragma unroll
+            for (int i = 0; i < KP; i++)
+                if (!(i & d)) order(v[i], v[i | d]);
+    }
+    template <int G, int D = 1>
+    static __device__ __forceinline__ void across(T *v) {
+        if constexpr (D < G) {
+            T o[KP];
+#pragma unroll
+            for (int i = 0; i < KP; i++)
+                o[i] = K::hi(v[i], K::moved(v[KP - 1 - i], [](uint32_t x) { return other_half<D>(x); }));
+#pragma unroll
+            for (int i = 0; i < KP; i++) v[i] = o[i];
+            settle(v);
+            across<G, 2 * D>(v);
+        }
+    }
+};
+
+// Logits of a row, their largest and e = exp(l - m), and Z = sum e.  Z = 0 only
+// where every logit is -inf; NaN or +inf makes Z NaN, and with it all that is
+// divided by it.
+template <bool F32, int G, int CH>
+__device__ __forceinline__ void softmax_row(const Chunk<F32> c[CH], float l[8 * CH], float e[8 * CH], float &m,
+                                            float &Z) {
+    m = -INFINITY;
+#pragma unroll
+    for (int v = 0; v < 8 * CH; v++) {
+        l[v] = c[v / 8].at(v % 8) + 0.0f;      // -0 becomes +0
+        m = fmaxf(m, l[v]);
+    }
+    m = group_max<G>(m);
+    if (m == -INFINITY) m = 0.0f;
+    float z[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int v = 0; v < 8 * CH; v++) {
+        e[v] = __builtin_amdgcn_exp2f((l[v] - m) * kLog2e);
+        z[v % 4] += e[v];
+    }
+    Z = group_sum<G>((z[0] + z[1]) + (z[2] + z[3]));
+}
+
+template <bool F32, int G, int CH, int KP, bool VEC>
+__global__ __launch_bounds__(256, (CH == 4 ? (F32 ? 2 : 3) : 4)) void k_route(RouteArgs a) {
+    typedef typename Elem<F32>::type T;
+    typedef Key<F32> K;
+    typedef typename K::type KT;
+    constexpr int V = 8 * CH, C = V * G, R = 256 / G;     // per lane; columns; tokens of a block's pass
+    __shared__ uint32_t hist[C];
+    __shared__ float sums[R * C];
+    __shared__ uint32_t routed_of[4];
+    const int g = threadIdx.x % G, r = threadIdx.x / G;
+    for (int j = threadIdx.x; j < C; j += 256) hist[j] = 0;
+    __syncthreads();
+    float acc[V];
+#pragma unroll
+    for (int v = 0; v < V; v++) acc[v] = 0.0f;
+    uint32_t routed = 0;
+    const int64_t step = (int64_t)gridDim.x * R;
+    int64_t t = (int64_t)blockIdx.x * R + r;
+    const auto load = [&](Chunk<F32> *c, int64_t at) {
+        const bool there = at < a.tokens && (!a.mask || a.mask[at]);
+        load_row<F32, G, CH, VEC>(c, static_cast<const T *>(a.logits) + at * a.stride, g, a.E, there);
+    };
+    Chunk<F32> next[CH];
+    load(next, t);
+    for (int64_t base = (int64_t)blockIdx.x * R; base < a.tokens; base += step, t += step) {
+        Chunk<F32> c[CH];
+#pragma unroll
+        for (int i = 0; i < CH; i++) c[i] = next[i];
+        load(next, t + step);
+        float l[V], e[V], m, Z;
+        softmax_row<F32, G, CH>(c, l, e, m, Z);
+        const float inv = Z == 0.0f ? 0.0f : 1.0f / Z;
+        if (g == 0) routed += Z != 0.0f;
+#pragma unroll
+        for (int v = 0; v < V; v++) acc[v] = __builtin_fmaf(e[v], inv, acc[v]);
+
+        // ~index of the lane's first expert; opaque, or its variants of all
+        // elements are kept in registers across the loop, which spills
+        uint32_t inv0 = 0xFFFFu ^ (8u * (uint32_t)g);
+        asm volatile("" : "+v"(inv0));
+        KT key[V < KP ? KP : V];
+#pragma unroll
+        for (int v = 0; v < V; v++) key[v] = K::make(l[v], inv0 ^ (8u * G * (v / 8)), v % 8);
+#pragma unroll
+        for (int v = V; v < KP; v++) key[v] = K::none();
+        if (__any(Z != Z)) {
+            asm volatile("; a row with NaN or +inf" : "+v"(inv0));     // a branch, not selects
+#pragma unroll
+            for (int v = 0; v < V; v++)
+                if (l[v] != l[v]) key[v] = K::nan(inv0 ^ (8u * G * (v / 8) + v % 8));
+        }
+        typedef Best<F32, KP> B;
+        B::sort(key);
+#pragma unroll
+        for (int v = KP; v < V; v += KP) {
+            B::sort(key + v);
+#pragma unroll
+            for (int i = 0; i < KP; i++) key[i] = K::hi(key[i], key[v + KP - 1 - i]);
+            B::settle(key);
+        }
+        B::template across<G>(key);
+
+        // lane g writes choices g, g + G, ..
+        constexpr int S = (KP + G - 1) / G;
+        float ge[S], top = 0.0f;
+        int id[S];
+#pragma unroll
+        for (int s = 0; s < S; s++) {
+            KT mine = key[s * G];
+#pragma unroll
+            for (int i = 1; i < G; i++)
+                if (s * G + i < KP && g == i) mine = key[s * G + i < KP ? s * G + i : 0];
+            const bool open = s * G + g < a.k && K::open(mine);
+            id[s] = open ? K::index(mine) : -1;
+            ge[s] = open ? __builtin_amdgcn_exp2f((K::value(mine) - m) * kLog2e) : 0.0f;
+            top += ge[s];
+        }
+        top = a.renorm ? group_sum<G>(top) : Z;
+        const float by = Z == 0.0f ? 0.0f : 1.0f / (Z != Z ? Z : top);
+#pragma unroll
+        for (int s = 0; s < S; s++) {
+            if (s * G + g < a.k && t < a.tokens) {
+                a.ids[t * a.k + s * G + g] = id[s];
+                a.gates[t * a.k + s * G + g] = id[s] < 0 ? 0.0f : ge[s] * by;
+                if (id[s] >= 0) atomicAdd(&hist[id[s]], 1u);
+            }
+        }
+    }
+    // the block's sums: token rows side by side in LDS, then over the rows
+#pragma unroll
+    for (int v = 0; v < V; v++) sums[r * C + 8 * ((v / 8) * G + g) + v % 8] = acc[v];
+    for (int d = 32; d; d >>= 1) routed += __shfl_xor((int)routed, d, 64);
+    if ((threadIdx.x & 63) == 0) routed_of[threadIdx.x >> 6] = routed;
+    __syncthreads();
+    constexpr int P = C < 256 ? 256 / C : 1;            // threads per column
+    for (int j = threadIdx.x; j < C * P; j += 256) {
+        const int col = j % C, part = j / C;
+        float sum = 0.0f;
+        for (int i = part; i < R; i += P) sum += sums[i * C + col];
+        if (P > 1) {
+            __syncthreads();
+            sums[part * C + col] = sum;
+            __syncthreads();
+            if (part != 0) break;
+            for (int i = 1; i < P; i++) sum += sums[i * C + col];
+        }
+        if (col < a.E) {
+            a.part.psum[(int)blockIdx.x * a.E + col] = sum;
+            a.part.count[(int)blockIdx.x * a.E + col] = hist[col];
+        }
+    }
+    if (threadIdx.x == 0) {
+        a.part.routed[blockIdx.x] = routed_of[0] + routed_of[1] + routed_of[2] + routed_of[3];
+        if (blockIdx.x == 0) *a.part.done = 0;
+    }
+}
+
+// Folds the parts in a fixed order and computes the loss.  A block takes
+// a.columns experts, 1024 / a.columns threads each over the rows, then a tree;
+// where there are several blocks, the last one to finish adds up their shares of
+// the loss, in block order.
+__global__ __launch_bounds__(1024) void k_balance(BalanceArgs a) {
+    __shared__ double ps[1024], cs[1024], ts[1024];
+    const int i = threadIdx.x, columns = a.columns;
+    const int c = i & (columns - 1), j = (int)blockIdx.x * columns + c;
+    double p = 0.0, n = 0.0, t = 0.0;
+    for (int q = 0; q < a.parts; q++) {
+        const RoutePart &part = a.part[q];
+        for (int b = i; b < part.nblk; b += 1024) t += part.routed[b];
+        if (j < a.E) {
+#pragma unroll 8
+            for (int b = i / columns; b < part.nblk; b += 1024 / columns) {
+                p += part.psum[b * a.E + j];
+                n += part.count[b * a.E + j];
+            }
+        }
+    }
+    ps[i] = p;
+    cs[i] = n;
+    ts[i] = t;
+    __syncthreads();
+    for (int d = 512; d; d >>= 1) {
+        if (i < d) {
+            if (d >= columns) {
+                ps[i] += ps[i + d];
+                cs[i] += cs[i + d];
+            }
+            ts[i] += ts[i + d];
+        }
+        __syncthreads();
+    }
+    const double N = ts[0] + (a.sums ? a.sums[2 * a.E] : 0.0);
+    const double f = N > 0.0 ? (double)a.E / ((double)a.k * N * N) : 0.0;
+    double share = 0.0;
+    if (i < columns && j < a.E) {
+        p = ps[i] + (a.sums ? a.sums[a.E + j] : 0.0);
+        n = cs[i] + (a.sums ? a.sums[j] : 0.0);
+        if (a.stats) {
+            a.stats[j] = n;
+            a.stats[a.E + j] = p;
+        }
+        const double w = f * n;
+        if (a.coef) a.coef[j] = (float)w;
+        if (a.counts) a.counts[j] = (int64_t)n;
+        share = w * p;
+    }
+    __syncthreads();
+    ps[i] = share;
+    __syncthreads();
+    for (int d = columns / 2; d; d >>= 1) {
+        if (i < d) ps[i] += ps[i + d];
+        __syncthreads();
+    }
+    // a.stats may be a.sums: its last element, which every block reads, is
+    // written by the last one
+    if (gridDim.x == 1) {
+        if (i == 0) {
+            if (a.loss) *a.loss = (float)ps[0];
+            if (a.stats) a.stats[2 * a.E] = N;
+        }
+        return;
+    }
+    const RoutePart &first = a.part[0];
+    if (i == 0) {
+        __hip_atomic_store(first.share + blockIdx.x, ps[0], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        const uint32_t before =
+            __hip_atomic_fetch_add(first.done, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+        if (before == gridDim.x - 1) {
+            double sum = 0.0;
+            for (unsigned b = 0; b < gridDim.x; b++)
+                sum += __hip_atomic_load(first.share + b, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            if (a.loss) *a.loss = (float)sum;
+            if (a.stats) a.stats[2 * a.E] = N;
+            *first.done = 0;
+        }
+    }
+}
+
+// LDS traffic between the lanes of one wave: orders it for the compiler too
+__device__ __forceinline__ void wave_lds_sync() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
 
 __device__ __forceinline__ float wave_sum(float v) {
 #pragma unroll
@@ -187,20 +599,11 @@ __device__ __forceinline__ float wave_max(float v) {
     for (int d = 32; d; d >>= 1) v = fmaxf(v, __shfl_xor(v, d, 64));
     return v;
 }
-__device__ __forceinline__ uint64_t wave_max(uint64_t v) {
-#pragma unroll
-    for (int d = 32; d; d >>= 1) {
-        const uint64_t o = __shfl_xor((unsigned long long)v, d, 64);
-        v = o > v ? o : v;
-    }
-    return v;
-}
-
 // One wave per token, V experts per lane (lane, lane + 64, ..).  With m the
 // largest logit, e = exp(l - m) and Z = sum e; Z = 0 only where every logit is
 // -inf, and NaN or +inf makes Z NaN and with it the row's gates and sums.
 template <bool F32, int V>
-__device__ __forceinline__ void softmax_row(const typename Elem<F32>::type *row, int E, int lane, float l[V],
+__device__ __forceinline__ void wave_softmax(const typename Elem<F32>::type *row, int E, int lane, float l[V],
                                             float e[V], float &m, float &Z) {
     m = -INFINITY;
 #pragma unroll
@@ -218,140 +621,6 @@ __device__ __forceinline__ void softmax_row(const typename Elem<F32>::type *row,
         Z += e[v];
     }
     Z = wave_sum(Z);
-}
-
-template <bool F32, int V>
-__global__ __launch_bounds__(256) void k_route(RouteArgs a) {
-    typedef typename Elem<F32>::type T;
-    __shared__ uint32_t hist[64 * V];
-    __shared__ float sums[4][64 * V];
-    __shared__ uint32_t routed_of[4];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    for (int j = threadIdx.x; j < a.E; j += 256) hist[j] = 0;
-    __syncthreads();
-    float acc[V];
-#pragma unroll
-    for (int v = 0; v < V; v++) acc[v] = 0.0f;
-    uint32_t routed = 0;
-    for (int64_t t = (int64_t)blockIdx.x * 4 + wave; t < a.tokens; t += 4 * (int64_t)gridDim.x) {
-        float l[V], e[V], m = 0.0f, Z = 0.0f;
-        if (!a.mask || a.mask[t])
-            softmax_row<F32, V>(static_cast<const T *>(a.logits) + t * a.stride, a.E, lane, l, e, m, Z);
-        if (Z == 0.0f) {   // left out, or no expert open
-            if (lane < a.k) {
-                a.ids[t * a.k + lane] = -1;
-                a.gates[t * a.k + lane] = 0.0f;
-            }
-            continue;
-        }
-        routed++;
-        const float inv = 1.0f / Z;
-        uint64_t key[V];
-#pragma unroll
-        for (int v = 0; v < V; v++) {
-            acc[v] += e[v] * inv;
-            key[v] = (uint64_t)order_key(l[v]) << 32 | (uint32_t)~(lane + 64 * v);
-        }
-        // k times the largest key (value, then lowest index); lane s keeps choice s
-        int id = -1;
-        float g = 0.0f, top = 0.0f;
-        for (int s = 0; s < a.k; s++) {
-            uint64_t best = 0;
-#pragma unroll
-            for (int v = 0; v < V; v++) best = key[v] > best ? key[v] : best;
-            best = wave_max(best);
-            if ((uint32_t)(best >> 32) <= kKeyMinusInf) break;
-            const int j = (int)~(uint32_t)best;
-            float es = 0.0f;
-#pragma unroll
-            for (int v = 0; v < V; v++) {
-                if (key[v] == best) {
-                    key[v] = 0;
-                    es = e[v];
-                }
-            }
-            es = __shfl(es, j & 63, 64);
-            top += es;
-            if (lane == s) {
-                id = j;
-                g = es;
-            }
-        }
-        if (lane < a.k) {
-            a.ids[t * a.k + lane] = id;
-            a.gates[t * a.k + lane] = id < 0 ? 0.0f : g / (a.renorm ? top : Z);
-            if (id >= 0) atomicAdd(&hist[id], 1u);
-        }
-    }
-#pragma unroll
-    for (int v = 0; v < V; v++) sums[wave][lane + 64 * v] = acc[v];
-    if (lane == 0) routed_of[wave] = routed;
-    __syncthreads();
-    for (int j = threadIdx.x; j < a.E; j += 256) {
-        a.psum[(int64_t)blockIdx.x * a.E + j] = ((sums[0][j] + sums[1][j]) + sums[2][j]) + sums[3][j];
-        a.count[(int64_t)blockIdx.x * a.E + j] = hist[j];
-    }
-    if (threadIdx.x == 0)
-        a.routed[blockIdx.x] = routed_of[0] + routed_of[1] + routed_of[2] + routed_of[3];
-}
-
-// Folds the blocks' partial statistics in a fixed order: a block per 64
-// experts, 16 threads per expert over the rows, then a tree; the extra block
-// sums the routed tokens.
-__global__ __launch_bounds__(1024) void k_route_fold(RouteArgs a, double *stats, int accumulate) {
-    __shared__ double ps[16][64];
-    __shared__ double cs[16][64];
-    const int c = threadIdx.x & 63, r = threadIdx.x >> 6;
-    const bool tokens = blockIdx.x == gridDim.x - 1;
-    const int j = tokens ? 0 : (int)blockIdx.x * 64 + c;
-    double p = 0.0, n = 0.0;
-    if (tokens) {
-        for (int b = threadIdx.x; b < a.nblk; b += 1024) n += a.routed[b];
-    } else if (j < a.E) {
-        for (int b = r; b < a.nblk; b += 16) {
-            p += a.psum[(int64_t)b * a.E + j];
-            n += a.count[(int64_t)b * a.E + j];
-        }
-    }
-    ps[r][c] = p;
-    cs[r][c] = n;
-    __syncthreads();
-    if (r != 0) return;
-    for (int i = 1; i < 16; i++) {
-        p += ps[i][c];
-        n += cs[i][c];
-    }
-    if (tokens) {
-        for (int d = 32; d; d >>= 1) n += __shfl_xor(n, d, 64);
-        if (c == 0) stats[2 * a.E] = accumulate ? stats[2 * a.E] + n : n;
-    } else if (j < a.E) {
-        stats[j] = accumulate ? stats[j] + n : n;
-        stats[a.E + j] = accumulate ? stats[a.E + j] + p : p;
-    }
-}
-
-__global__ __launch_bounds__(256) void k_balance(const double *stats, int E, int k, float *loss, float *coef,
-                                                 int64_t *counts) {
-    __shared__ double part[4];
-    const double N = stats[2 * E];
-    const double f = N > 0.0 ? (double)E / ((double)k * N * N) : 0.0;
-    double sum = 0.0;
-    for (int j = threadIdx.x; j < E; j += 256) {
-        const double c = stats[j], w = f * c;
-        if (coef) coef[j] = (float)w;
-        if (counts) counts[j] = (int64_t)c;
-        sum += w * stats[E + j];
-    }
-    for (int d = 32; d; d >>= 1) sum += __shfl_xor(sum, d, 64);
-    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = sum;
-    __syncthreads();
-    if (loss && threadIdx.x == 0) *loss = (float)(((part[0] + part[1]) + part[2]) + part[3]);
-}
-
-// LDS traffic between the lanes of one wave: orders it for the compiler too
-__device__ __forceinline__ void wave_lds_sync() {
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
 }
 
 // One wave per token.  The chosen experts' own term goes through a row of LDS,
@@ -373,7 +642,7 @@ __global__ __launch_bounds__(256) void k_route_backward(RouteBackwardArgs a) {
     for (int64_t t = (int64_t)blockIdx.x * 4 + wave; t < a.tokens; t += 4 * (int64_t)gridDim.x) {
         float l[V], e[V], m = 0.0f, Z = 0.0f;
         if (!a.mask || a.mask[t])
-            softmax_row<F32, V>(static_cast<const T *>(a.logits) + t * a.stride, a.E, lane, l, e, m, Z);
+            wave_softmax<F32, V>(static_cast<const T *>(a.logits) + t * a.stride, a.E, lane, l, e, m, Z);
         T *out = static_cast<T *>(a.dlogits) + t * a.dstride;
         if (Z == 0.0f) {
 #pragma unroll
@@ -436,13 +705,38 @@ hipError_t by_width(int E, int f32, Args... args) {
     return Launch<false, 16>::go(args...);
 }
 
-template <bool F32, int V>
-struct Forward {
-    static hipError_t go(const RouteArgs *a, hipStream_t s) {
-        hipLaunchKernelGGL((k_route<F32, V>), dim3((unsigned)a->nblk), dim3(256), 0, s, *a);
-        return hipGetLastError();
-    }
-};
+
+template <bool F32, int G, int CH, bool VEC>
+hipError_t route_choices(const RouteArgs &a, hipStream_t s) {
+    const dim3 grid((unsigned)a.part.nblk), block(256);
+    if (a.k <= 2) hipLaunchKernelGGL((k_route<F32, G, CH, 2, VEC>), grid, block, 0, s, a);
+    else if (a.k <= 4) hipLaunchKernelGGL((k_route<F32, G, CH, 4, VEC>), grid, block, 0, s, a);
+    else if (a.k <= 8) hipLaunchKernelGGL((k_route<F32, G, CH, 8, VEC>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((k_route<F32, G, CH, 16, VEC>), grid, block, 0, s, a);
+    return hipGetLastError();
+}
+
+// lanes and chunks of a token of E experts
+template <class F>
+auto by_experts(int E, F f) {
+    if (E <= 8) return f(std::integral_constant<int, 1>(), std::integral_constant<int, 1>());
+    if (E <= 16) return f(std::integral_constant<int, 2>(), std::integral_constant<int, 1>());
+    if (E <= 32) return f(std::integral_constant<int, 4>(), std::integral_constant<int, 1>());
+    if (E <= 64) return f(std::integral_constant<int, 8>(), std::integral_constant<int, 1>());
+    if (E <= 128) return f(std::integral_constant<int, 8>(), std::integral_constant<int, 2>());
+    if (E <= 256) return f(std::integral_constant<int, 8>(), std::integral_constant<int, 4>());
+    if (E <= 512) return f(std::integral_constant<int, 16>(), std::integral_constant<int, 4>());
+    return f(std::integral_constant<int, 32>(), std::integral_constant<int, 4>());
+}
+
+template <bool F32>
+hipError_t route_experts(const RouteArgs &a, hipStream_t s) {
+    const bool vec = a.E % 8 == 0 && reinterpret_cast<uintptr_t>(a.logits) % 16 == 0 &&
+                     a.stride * (F32 ? 4 : 2) % 16 == 0;
+    return by_experts(a.E, [&](auto G, auto CH) {
+        return vec ? route_choices<F32, G.value, CH.value, true>(a, s) : route_choices<F32, G.value, CH.value, false>(a, s);
+    });
+}
 template <bool F32, int V>
 struct Backward {
     static hipError_t go(const RouteBackwardArgs *a, hipStream_t s) {
@@ -460,21 +754,25 @@ hipError_t launch_dropout(const DropoutArgs &a, int f32, hipStream_t s) {
     return a.residual ? dropout_access<false, true>(a, s) : dropout_access<false, false>(a, s);
 }
 
-int route_blocks(int64_t tokens, int) {
-    const int64_t want = (tokens + 3) / 4;
-    return (int)(want < 1 ? 1 : want < 2048 ? want : 2048);
+int route_blocks(int64_t tokens, int E) {
+    // what the chip holds at once: 8, 4 or 3 blocks per CU by the lanes' registers
+    const int64_t rows = by_experts(E, [](auto G, auto) { return 256 / G.value; });
+    const int64_t most = by_experts(E, [](auto, auto CH) { return 256 * (CH.value == 1 ? 6 : CH.value == 2 ? 4 : 3); });
+    const int64_t want = (tokens + rows - 1) / rows;
+    return (int)(want < 1 ? 1 : want < most ? want : most);
 }
 
-hipError_t launch_route(const RouteArgs &a, int f32, hipStream_t s) { return by_width<Forward>(a.E, f32, &a, s); }
-
-hipError_t launch_route_fold(const RouteArgs &a, double *stats, int accumulate, hipStream_t s) {
-    hipLaunchKernelGGL(k_route_fold, dim3((unsigned)(a.E + 63) / 64 + 1), dim3(1024), 0, s, a, stats, accumulate);
-    return hipGetLastError();
+hipError_t launch_route(const RouteArgs &a, int f32, hipStream_t s) {
+    return f32 ? route_experts<true>(a, s) : route_experts<false>(a, s);
 }
 
-hipError_t launch_balance(const double *stats, int E, int k, float *loss, float *coef, int64_t *counts,
-                          hipStream_t s) {
-    hipLaunchKernelGGL(k_balance, dim3(1), dim3(256), 0, s, stats, E, k, loss, coef, counts);
+hipError_t launch_balance(const BalanceArgs &args, hipStream_t s) {
+    BalanceArgs a = args;
+    int64_t rows = 0;
+    for (int q = 0; q < a.parts; q++) rows += a.part[q].nblk;
+    // few rows: one block, a thread per expert
+    a.columns = rows <= 8 ? kRouteMaxExperts : kBalanceColumns;
+    hipLaunchKernelGGL(k_balance, dim3((unsigned)((a.E + a.columns - 1) / a.columns)), dim3(1024), 0, s, a);
     return hipGetLastError();
 }
 

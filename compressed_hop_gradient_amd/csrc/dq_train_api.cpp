@@ -38,8 +38,30 @@ bool clash(const void *out, int64_t os, const void *in, int64_t is, int64_t rows
     return true;
 }
 
+constexpr int64_t kMostTokens = (int64_t)1 << 40;
+
+// A part's buffer: its rows, then the scratch of a balance call
+struct PartAt {
+    RoutePart part;
+    size_t bytes;
+};
+PartAt part_at(void *d_part, int64_t tokens, int32_t E) {
+    uint8_t *base = static_cast<uint8_t *>(d_part);
+    PartAt p{};
+    p.part.nblk = route_blocks(tokens, E);
+    const size_t n = (size_t)p.part.nblk, row = align_up(4 * n * (size_t)E);
+    size_t at = 0;
+    p.part.psum = reinterpret_cast<float *>(base);
+    p.part.count = reinterpret_cast<uint32_t *>(base + (at += row));
+    p.part.routed = reinterpret_cast<uint32_t *>(base + (at += row));
+    p.part.share = reinterpret_cast<double *>(base + (at += align_up(4 * n)));
+    p.part.done = reinterpret_cast<uint32_t *>(base + (at += 8 * (kRouteMaxExperts / kBalanceColumns)));
+    p.bytes = at + kAlign;
+    return p;
+}
+
 bool bad_router(int32_t kind, int64_t tokens, int32_t E, int64_t stride, int32_t k) {
-    return !is_kind(kind) || tokens < 0 || tokens > ((int64_t)1 << 40) || E < 1 || E > kRouteMaxExperts || k < 1 ||
+    return !is_kind(kind) || tokens < 0 || tokens > kMostTokens || E < 1 || E > kRouteMaxExperts || k < 1 ||
            k > E || k > kRouteMaxTopK || stride < 0 || stride > ((int64_t)1 << 40);
 }
 
@@ -88,21 +110,17 @@ dq_status dq_dropout(const void *x, const void *residual, void *y, int32_t kind,
     return hip_status(launch_dropout(a, kind == DQ_F32, static_cast<hipStream_t>(stream)));
 }
 
-size_t dq_route_workspace_bytes(int64_t tokens, int32_t E) {
-    if (tokens < 0 || tokens > ((int64_t)1 << 40) || E < 1 || E > kRouteMaxExperts) return 0;
-    const size_t n = (size_t)route_blocks(tokens, E);
-    return 2 * align_up(4 * n * (size_t)E) + align_up(4 * n);
+size_t dq_route_part_bytes(int64_t tokens, int32_t E) {
+    if (tokens < 0 || tokens > kMostTokens || E < 1 || E > kRouteMaxExperts) return 0;
+    return part_at(nullptr, tokens, E).bytes;
 }
 
 dq_status dq_route(const void *logits, int32_t kind, int64_t tokens, int32_t E, int64_t stride, const uint8_t *mask,
-                   int32_t k, int32_t flags, int32_t *ids, float *gates, double *stats, void *ws, size_t ws_bytes,
-                   void *stream) {
-    if (bad_router(kind, tokens, E, stride, k) || (flags & ~(DQ_ROUTE_RENORM | DQ_ROUTE_ACCUMULATE)))
-        return DQ_EINVAL;
-    if (!stats || (tokens > 0 && (!logits || !ids || !gates))) return DQ_ENULL;
-    if (!aligned(logits, elem_bytes(kind)) || !aligned(ids, 4) || !aligned(gates, 4) || !aligned(stats, 8))
-        return DQ_EINVAL;
-    if (!ws || !aligned(ws, kAlign) || ws_bytes < dq_route_workspace_bytes(tokens, E)) return DQ_EWORKSPACE;
+                   int32_t k, int32_t flags, int32_t *ids, float *gates, void *part, size_t part_bytes, void *stream) {
+    if (bad_router(kind, tokens, E, stride, k) || (flags & ~DQ_ROUTE_RENORM)) return DQ_EINVAL;
+    if (tokens > 0 && (!logits || !ids || !gates)) return DQ_ENULL;
+    if (!aligned(logits, elem_bytes(kind)) || !aligned(ids, 4) || !aligned(gates, 4)) return DQ_EINVAL;
+    if (!part || !aligned(part, kAlign) || part_bytes < dq_route_part_bytes(tokens, E)) return DQ_EWORKSPACE;
     RouteArgs a{};
     a.logits = logits;
     a.tokens = tokens;
@@ -113,25 +131,33 @@ dq_status dq_route(const void *logits, int32_t kind, int64_t tokens, int32_t E, 
     a.renorm = (flags & DQ_ROUTE_RENORM) != 0;
     a.ids = ids;
     a.gates = gates;
-    a.nblk = tokens == 0 ? 0 : route_blocks(tokens, E);
-    const size_t part = align_up(4 * (size_t)a.nblk * (size_t)E);
-    a.psum = static_cast<float *>(ws);
-    a.count = reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(ws) + part);
-    a.routed = reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(ws) + 2 * part);
-    const hipStream_t s = static_cast<hipStream_t>(stream);
-    if (tokens > 0) {
-        const hipError_t e = launch_route(a, kind == DQ_F32, s);
-        if (e != hipSuccess) return hip_status(e);
-    }
-    return hip_status(launch_route_fold(a, stats, (flags & DQ_ROUTE_ACCUMULATE) != 0, s));
+    a.part = part_at(part, tokens, E).part;
+    return hip_status(launch_route(a, kind == DQ_F32, static_cast<hipStream_t>(stream)));
 }
 
-dq_status dq_balance(const double *stats, int32_t E, int32_t k, float *loss, float *coef, int64_t *counts,
-                     void *stream) {
+dq_status dq_balance(const dq_route_part *parts, int32_t n_parts, const double *sums, int32_t E, int32_t k,
+                     double *stats, float *loss, float *coef, int64_t *counts, void *stream) {
     if (E < 1 || E > kRouteMaxExperts || k < 1 || k > E || k > kRouteMaxTopK) return DQ_EINVAL;
-    if (!stats) return DQ_ENULL;
-    if (!aligned(stats, 8) || !aligned(loss, 4) || !aligned(coef, 4) || !aligned(counts, 8)) return DQ_EINVAL;
-    return hip_status(launch_balance(stats, E, k, loss, coef, counts, static_cast<hipStream_t>(stream)));
+    if (n_parts < 0 || n_parts > kRouteMaxParts) return DQ_EINVAL;
+    if ((n_parts > 0 && !parts) || (n_parts == 0 && !sums)) return DQ_ENULL;
+    if (!aligned(sums, 8) || !aligned(stats, 8) || !aligned(loss, 4) || !aligned(coef, 4) || !aligned(counts, 8))
+        return DQ_EINVAL;
+    BalanceArgs a{};
+    a.parts = n_parts;
+    for (int32_t q = 0; q < n_parts; q++) {
+        if (parts[q].tokens < 0 || parts[q].tokens > kMostTokens) return DQ_EINVAL;
+        if (!parts[q].d_part) return DQ_ENULL;
+        if (!aligned(parts[q].d_part, kAlign)) return DQ_EINVAL;
+        a.part[q] = part_at(parts[q].d_part, parts[q].tokens, E).part;
+    }
+    a.sums = sums;
+    a.E = E;
+    a.k = k;
+    a.stats = stats;
+    a.loss = loss;
+    a.coef = coef;
+    a.counts = counts;
+    return hip_status(launch_balance(a, static_cast<hipStream_t>(stream)));
 }
 
 dq_status dq_route_backward(const void *logits, int32_t kind, int64_t tokens, int32_t E, int64_t stride,

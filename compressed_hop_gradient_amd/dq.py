@@ -26,7 +26,8 @@ OPT_MAX_WIDTH = 8
 ALLOC_THRESHOLD, ALLOC_MEAN_CORRECTED, ALLOC_UNIFORM = 0, 1, 2
 MX_FP8_E4M3, MX_FP6_E3M2, MX_FP6_E2M3, MX_FP4_E2M1 = 0, 1, 2, 3
 OPT_EPS = 0   # dq_option_f64
-ROUTE_RENORM, ROUTE_ACCUMULATE = 1, 2   # dq_route_flags
+ROUTE_RENORM = 1   # dq_route_flags
+ROUTE_MAX_PARTS = 16
 KERNEL_KINDS = ("stats", "allocate", "reorder", "compress", "hop_grad", "hop_packed",
                 "finalize", "mxfp8", "hop_final")
 
@@ -47,6 +48,10 @@ class dq_layout(C.Structure):
 class dq_timing(C.Structure):
     _fields_ = [("ms", C.c_double * len(KERNEL_KINDS)), ("launches", C.c_int64 * len(KERNEL_KINDS)),
                 ("coords", C.c_int64 * len(KERNEL_KINDS))]
+
+
+class dq_route_part(C.Structure):
+    _fields_ = [("d_part", C.c_void_p), ("tokens", C.c_int64)]
 
 
 class DQError(RuntimeError):
@@ -97,10 +102,11 @@ _SIGS = {
     "dq_dropout": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_int32, C.c_int64, C.c_int64, C.c_int64,
                              C.c_int64, C.c_int64, C.c_double, C.c_uint64, C.c_uint32, C.c_void_p,
                              C.c_int32, C.c_uint32, C.c_void_p]),
-    "dq_route_workspace_bytes": (C.c_size_t, [C.c_int64, C.c_int32]),
+    "dq_route_part_bytes": (C.c_size_t, [C.c_int64, C.c_int32]),
     "dq_route": (C.c_int, [C.c_void_p, C.c_int32, C.c_int64, C.c_int32, C.c_int64, C.c_void_p, C.c_int32,
-                           C.c_int32, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p]),
-    "dq_balance": (C.c_int, [C.c_void_p, C.c_int32, C.c_int32, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p]),
+                           C.c_int32, C.c_void_p, C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p]),
+    "dq_balance": (C.c_int, [C.c_void_p, C.c_int32, C.c_void_p, C.c_int32, C.c_int32, C.c_void_p, C.c_void_p,
+                             C.c_void_p, C.c_void_p, C.c_void_p]),
     "dq_route_backward": (C.c_int, [C.c_void_p, C.c_int32, C.c_int64, C.c_int32, C.c_int64, C.c_void_p, C.c_int32,
                                     C.c_int32, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p,
                                     C.c_int64, C.c_void_p]),
@@ -337,54 +343,92 @@ def _result(t, shape, what, dtype, dev):
     return _tensor(t, what, dev, dtype=dtype)
 
 
+class RouteStats:
+    """Balance statistics of the workers routed so far: the parts that
+    :func:`route` wrote, folded on demand."""
+
+    def __init__(self, experts, device):
+        self.experts, self.device = experts, device
+        self.parts = []        # (buffer of dq_route, its tokens)
+        self.sums = None       # what was folded before them, fp64 [2 experts + 1]
+
+    def _add(self, part, tokens):
+        if len(self.parts) == ROUTE_MAX_PARTS:
+            self.fold()
+        self.parts.append((part, tokens))
+
+    def _balance(self, top_k, stats, loss, coef, counts):
+        n = len(self.parts)
+        array = (dq_route_part * n)(*[(p.data_ptr(), t) for p, t in self.parts])
+        _call(self.device, "dq_balance", array, n, _opt(self.sums), self.experts, top_k, _opt(stats), _opt(loss),
+              _opt(coef), _opt(counts))
+
+    def fold(self):
+        """The statistics as one tensor: choices per expert, summed
+        probabilities per expert, routed tokens (fp64 [2 experts + 1]).  Those
+        of several processes add up; a change to the tensor is one to these
+        statistics."""
+        if self.parts:
+            stats = self.sums
+            if stats is None:
+                stats = torch.empty(2 * self.experts + 1, dtype=torch.float64, device=self.device)
+            self._balance(1, stats, None, None, None)
+            self.sums, self.parts = stats, []
+        return self.sums
+
+
 @_on_stream
-def route(logits, top_k, renorm=True, mask=None, stats=None, accumulate=None, ids=None, gates=None):
+def route(logits, top_k, renorm=True, mask=None, stats=None, ids=None, gates=None):
     """Expert choice of every token (``dq_route``): returns (ids, gates, stats).
 
     ``logits`` is [tokens, experts], bf16 or fp32, rows at any stride; ``mask``
     (bool or uint8, [tokens]) is false for tokens left out.  ``ids`` is int32 and
     ``gates`` fp32, both [tokens, top_k], best choice first; -1 and 0 where a
-    token has fewer open experts (logits above -inf).  ``stats``, fp64
-    [2 experts + 1], holds choices and summed probabilities per expert and the
-    routed tokens: passed in, the call adds to it (workers in rank order), unless
-    ``accumulate`` is false.  Several processes sum their ``stats``."""
+    token has fewer open experts (logits above -inf).  ``stats`` is a
+    :class:`RouteStats` for :func:`balance`: one that is passed in takes these tokens
+    in addition (the workers in rank order)."""
     tokens, experts = _logits(logits).shape
     dev = logits.device
-    if accumulate is None:
-        accumulate = stats is not None
-    elif accumulate and stats is None:
-        raise ValueError("accumulate needs stats")
+    if stats is None:
+        stats = RouteStats(experts, dev)
+    elif not isinstance(stats, RouteStats):
+        raise TypeError(f"stats: expected a RouteStats, got {type(stats).__name__}")
+    elif stats.experts != experts or stats.device != dev:
+        raise ValueError(f"stats of {stats.experts} experts on {stats.device}, "
+                         f"logits of {experts} on {dev}")
     shape = (tokens, top_k)
     ids = _result(ids, shape, "ids", torch.int32, dev)
     gates = _result(gates, shape, "gates", torch.float32, dev)
-    stats = _result(stats, (2 * experts + 1,), "stats", torch.float64, dev)
-    nbytes = lib().dq_route_workspace_bytes(tokens, experts)
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    nbytes = lib().dq_route_part_bytes(tokens, experts)
+    part = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     _call(dev, "dq_route", logits.data_ptr(), _kind(logits), tokens, experts, logits.stride(0),
-          _token_mask(mask, tokens, dev), top_k,
-          (ROUTE_RENORM if renorm else 0) | (ROUTE_ACCUMULATE if accumulate else 0),
-          ids.data_ptr(), gates.data_ptr(), stats.data_ptr(), ws.data_ptr(), nbytes)
+          _token_mask(mask, tokens, dev), top_k, ROUTE_RENORM if renorm else 0, ids.data_ptr(), gates.data_ptr(),
+          part.data_ptr(), nbytes)
+    stats._add(part, tokens)
     return ids, gates, stats
 
 
 @_on_stream
 def balance(stats, top_k):
-    """Balance loss of the tokens in ``stats`` (``dq_balance``): returns
-    (loss [1] fp32, coef [experts] fp32, counts [experts] int64).  ``coef`` is
-    the loss's derivative by any token's probabilities, which
-    :func:`route_backward` takes."""
-    if not isinstance(stats, torch.Tensor) or stats.dim() != 1 or stats.numel() < 3 or stats.numel() % 2 == 0:
-        raise ValueError("stats: expected the [2 experts + 1] tensor of route()")
+    """Balance loss of the tokens in ``stats`` (``dq_balance``), a
+    :class:`RouteStats` or the tensor that its ``fold`` gives: returns (loss [1] fp32,
+    coef [experts] fp32, counts [experts] int64).  ``coef`` is the loss's
+    derivative by any token's probabilities, which :func:`route_backward` takes."""
+    if isinstance(stats, torch.Tensor):
+        if stats.dim() != 1 or stats.numel() < 3 or stats.numel() % 2 == 0:
+            raise ValueError(f"stats: shape {tuple(stats.shape)}, expected [2 experts + 1]")
+        if stats.device.type != "cuda":
+            raise ValueError(f"stats: tensor on {stats.device}, the kernels run on a GPU")
+        sums = _tensor(stats, "stats", stats.device, dtype=torch.float64)
+        stats = RouteStats(sums.numel() // 2, sums.device)
+        stats.sums = sums
+    elif not isinstance(stats, RouteStats):
+        raise TypeError(f"stats: expected a RouteStats or its tensor, got {type(stats).__name__}")
     dev = stats.device
-    if dev.type != "cuda":
-        raise ValueError(f"stats: tensor on {dev}, the kernels run on a GPU")
-    _tensor(stats, "stats", dev, dtype=torch.float64)
-    experts = stats.numel() // 2
     loss = torch.empty(1, dtype=torch.float32, device=dev)
-    coef = torch.empty(experts, dtype=torch.float32, device=dev)
-    counts = torch.empty(experts, dtype=torch.int64, device=dev)
-    _call(dev, "dq_balance", stats.data_ptr(), experts, top_k, loss.data_ptr(), coef.data_ptr(),
-          counts.data_ptr())
+    coef = torch.empty(stats.experts, dtype=torch.float32, device=dev)
+    counts = torch.empty(stats.experts, dtype=torch.int64, device=dev)
+    stats._balance(top_k, None, loss, coef, counts)
     return loss, coef, counts
 
 

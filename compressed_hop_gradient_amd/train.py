@@ -69,6 +69,7 @@ class _Route(torch.autograd.Function):
             ids.append(i)
             gates.append(g)
         if reduce is not None:
+            stats = stats.fold()
             reduce(stats)
         loss, coef, counts = dq.balance(stats, top_k)
         ctx.renorm = renorm

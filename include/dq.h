@@ -439,26 +439,39 @@ dq_status dq_dropout(const void *d_x, const void *d_residual, void *d_y, int32_t
  * and gates 0 and counts nowhere, whatever its logits hold.  A token with a NaN
  * or +inf has NaN gates (and makes the balance loss NaN).
  *
- * d_stats (double[2 * n_experts + 1]: choices per expert, sum of p per expert,
- * routed tokens) is set, or with DQ_ROUTE_ACCUMULATE added to: the statistic
- * of several workers is their calls in rank order on one stream, and of several
- * processes the sum of their d_stats.  Fixed summation order: the same calls give
- * the same bits.
+ * d_part (256-byte aligned, dq_route_part_bytes) receives the statistics of
+ * these tokens in the form dq_balance takes: partial sums, in the caller's
+ * buffer until then.
  * n_experts in 1..1024, top_k in 1..min(n_experts, 16), tokens in 0..2^40. */
-typedef enum dq_route_flags { DQ_ROUTE_RENORM = 1, DQ_ROUTE_ACCUMULATE = 2 } dq_route_flags;
-size_t dq_route_workspace_bytes(int64_t tokens, int32_t n_experts);   /* 0 on bad arguments */
+typedef enum dq_route_flags { DQ_ROUTE_RENORM = 1 } dq_route_flags;
+size_t dq_route_part_bytes(int64_t tokens, int32_t n_experts);   /* 0 on bad arguments */
 dq_status dq_route(const void *d_logits, int32_t kind, int64_t tokens, int32_t n_experts, int64_t stride,
                    const uint8_t *d_mask, int32_t top_k, int32_t flags, int32_t *d_ids, float *d_gates,
-                   double *d_stats, void *d_workspace, size_t workspace_bytes, void *stream);
+                   void *d_part, size_t part_bytes, void *stream);
 
-/* Balance loss of the tokens in d_stats (dq_route): with c the choices, S the
- * summed probabilities and N the routed tokens,
- *   loss = n_experts / (top_k N^2) * sum_e c_e S_e     (1 when balanced),
- * d_coef[e] = n_experts c_e / (top_k N^2), the derivative of the loss by any
- * token's p_e (choices have none), and d_counts[e] = c_e.  All 0 when N = 0.
- * Any of the three outputs may be NULL. */
-dq_status dq_balance(const double *d_stats, int32_t n_experts, int32_t top_k, float *d_loss, float *d_coef,
-                     int64_t *d_counts, void *stream);
+/* Balance statistics and loss over all workers.  h_parts is a HOST array of
+ * n_parts (0..DQ_ROUTE_MAX_PARTS) parts that dq_route wrote, one per worker, with
+ * the token counts of those calls; they are folded in the array's order, after
+ * d_sums if it is given: statistics in the form of d_stats, of earlier workers or
+ * of other processes (those of several processes add up).
+ *   d_stats   double[2 * n_experts + 1]: choices per expert, sum of p per
+ *             expert, routed tokens; may be d_sums
+ *   d_loss    with c the choices, S the summed p and N the routed tokens,
+ *             n_experts / (top_k N^2) * sum_e c_e S_e     (1 when balanced)
+ *   d_coef    float[n_experts], n_experts c_e / (top_k N^2): the derivative of the
+ *             loss by any token's p_e (choices have none)
+ *   d_counts  c
+ * Any of them may be NULL; the last three are 0 when N = 0.  The same parts give
+ * the same bits.  Two calls with the same first part must not overlap in time
+ * (it holds their scratch). */
+#define DQ_ROUTE_MAX_PARTS 16
+typedef struct dq_route_part {
+    void *d_part;
+    int64_t tokens;
+} dq_route_part;
+dq_status dq_balance(const dq_route_part *h_parts, int32_t n_parts, const double *d_sums, int32_t n_experts,
+                     int32_t top_k, double *d_stats, float *d_loss, float *d_coef, int64_t *d_counts,
+                     void *stream);
 
 /* Gradient by the logits, from the gates' (d_dgates[tokens][top_k], may be
  * NULL) and the balance loss's (d_coef of dq_balance, may be NULL; times

@@ -292,7 +292,7 @@ def check_stats(stats, rs):
     """Counts and tokens exactly; sums of p within the roundings of a p and of
     the fp32 part of its sum (at most one addition per token)."""
     E = rs[0].l.shape[1]
-    s = stats.cpu().numpy()
+    s = stats.fold().cpu().numpy()
     assert np.array_equal(s[:E], sum(r.counts for r in rs))
     assert s[2 * E] == sum(r.tokens for r in rs)
     want = sum(r.psum for r in rs)
@@ -345,14 +345,14 @@ def test_route_everything_left_out(dtype):
     for kw in (dict(), dict(mask=torch.zeros(9, dtype=torch.bool, device="cuda"))):
         x = l if not kw else torch.full_like(l, math.nan)
         ids, gates, stats = dq.route(x, 3, **kw)
-        assert ids.eq(-1).all() and gates.eq(0).all() and stats.eq(0).all()
+        assert ids.eq(-1).all() and gates.eq(0).all()
         loss, coef, counts = dq.balance(stats, 3)
-        assert loss.eq(0).all() and coef.eq(0).all() and counts.eq(0).all()
+        assert loss.eq(0).all() and coef.eq(0).all() and counts.eq(0).all() and stats.fold().eq(0).all()
         d = dq.route_backward(x, ids, torch.full((9, 3), math.nan, device="cuda"), coef, **kw)
         assert d.eq(0).all()
     empty = torch.empty(0, 12, dtype=dtype, device="cuda")
     ids, gates, stats = dq.route(empty, 3)
-    assert ids.shape == (0, 3) and stats.eq(0).all()
+    assert ids.shape == (0, 3) and stats.fold().eq(0).all()
     assert dq.route_backward(empty, ids).shape == (0, 12)
 
 
@@ -371,8 +371,8 @@ def test_route_nan_and_infinity(E, dtype):
     ids, gates, stats = dq.route(l, 3)
     r = check_forward(l, 3, True, None, ids, gates)
     assert ids[4, 0] == 4 and ids[4, 1] == 1
-    assert np.array_equal(stats.cpu().numpy()[:E], r.counts) and stats[2 * E] == 6
-    loss, coef, _ = dq.balance(stats, 3)
+    loss, coef, counts = dq.balance(stats, 3)
+    assert np.array_equal(counts.cpu().numpy(), r.counts) and stats.fold()[2 * E] == 6
     assert loss.isnan().all()
     d = dq.route_backward(l, ids, torch.ones(6, 3, device="cuda"), torch.ones(E, device="cuda"))
     assert d[1:5].isnan().all() and not d[0].isnan().any() and not d[5].isnan().any()
@@ -390,7 +390,7 @@ def test_route_extreme_logits():
     assert ids.tolist() == [[0, 3], [0, 1], [0, 2], [0, 1], [3, 0]]
     assert torch.equal(gates[0], torch.tensor([0.5, 0.5], device="cuda"))
     assert torch.equal(gates[1], torch.tensor([0.5, 0.5], device="cuda"))
-    assert stats[8] == 5 and bool(torch.isfinite(stats).all())
+    assert stats.fold()[8] == 5 and bool(torch.isfinite(stats.fold()).all())
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
@@ -466,7 +466,7 @@ def test_gradient_against_differences():
             full = torch.zeros(T, E, dtype=torch.float64)
             full.scatter_(1, ids.long().cpu(), gates.double().cpu())
             stay = torch.equal(ids.sort(1).values, r.ids.sort(1).values)
-            s = stats.double()
+            s = stats.fold()
             s[:E] = r.counts.double()                                # counts have no derivative
             loss = (s[:E] * s[E:2 * E]).sum().item() * E / (k * s[2 * E].item() ** 2)
             return (full.gather(1, r.ids.long().cpu()) * w.double().cpu()).sum().item() + 3 * loss, stay
@@ -492,15 +492,35 @@ def test_route_folds_workers_in_order(dtype):
     assert np.array_equal(counts.cpu().numpy(), wn)
     assert np.all(np.abs(coef.double().cpu().numpy() - wc) <= 2 * U * wc)
     assert abs(loss.item() - wl) <= (most + 4) * U * wl
-    # processes: the sum of their statistics
-    parts = [dq.route(l, k)[2] for l in ls]
+    # the same in any grouping: folded in between, as a tensor, as the sum of
+    # the statistics of several processes
+    again = None
+    for n, l in enumerate(ls):
+        again = dq.route(l, k, stats=again)[2]
+        if n % 2:
+            again.fold()
+    parts = [dq.route(l, k)[2].fold() for l in ls]
     total = sum(parts[1:], parts[0].clone())
-    assert torch.equal(dq.balance(total, k)[2], counts)
-    assert abs(dq.balance(total, k)[0].item() - wl) <= (most + 4) * U * wl
-    # a buffer that is set anew
-    stats.fill_(math.nan)
-    s = dq.route(ls[0], k, stats=stats, accumulate=False)[2]
-    assert s is stats and torch.equal(s, parts[0])
+    for s in (again, again.fold(), total):
+        other = dq.balance(s, k)
+        assert torch.equal(other[2], counts) and torch.equal(other[1], coef)
+        assert abs(other[0].item() - wl) <= (most + 4) * U * wl
+    # twice the same bits
+    assert all(torch.equal(a, b) for a, b in zip(dq.balance(total, k), other))
+
+
+def test_more_workers_than_one_fold_takes():
+    E, k, n = 24, 2, 2 * dq.ROUTE_MAX_PARTS + 3
+    ls = [logits_of(5 + w, E, torch.float32, w) for w in range(n)]
+    stats = None
+    for l in ls:
+        stats = dq.route(l, k, stats=stats)[2]
+    loss, coef, counts = dq.balance(stats, k)
+    rs = [ref.Routed(l.double().cpu().numpy(), k) for l in ls]
+    wl, wc, wn, N = ref.balance(rs)
+    assert np.array_equal(counts.cpu().numpy(), wn)
+    assert abs(loss.item() - wl) <= (max(r.roundings + len(r.l) for r in rs) + 4) * U * wl
+    assert stats.fold()[2 * E] == N
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
@@ -517,11 +537,12 @@ def test_route_many_tokens_and_the_same_bits_again(T, E, k, dtype):
     c = 2 * (3 * span + 48)
     want = p.gather(1, order)
     assert bool(((gates.double().cpu() - want).abs() <= c * U * want).all())
-    s = stats.cpu()
+    s = stats.fold().cpu()
     assert torch.equal(s[:E], torch.bincount(order.reshape(-1), minlength=E).double()) and s[2 * E] == T
     assert bool(((s[E:2 * E] - p.sum(0)).abs() <= (c + T) * U * p.sum(0)).all())
     again = dq.route(l, k, False)
-    assert torch.equal(ids, again[0]) and torch.equal(gates, again[1]) and torch.equal(stats, again[2])
+    assert torch.equal(ids, again[0]) and torch.equal(gates, again[1])
+    assert torch.equal(stats.fold(), again[2].fold())
     coef = dq.balance(stats, k)[1]
     dg = randn((T, k), torch.float32)
     d = dq.route_backward(l, ids, dg, coef, renorm=False)
@@ -540,24 +561,24 @@ def test_route_loss_of_many_tokens():
     l = torch.randn(T, E, generator=g, device="cuda")
     _, _, stats = dq.route(l, k)
     p = torch.softmax(l.double(), 1).sum(0)
-    assert bool(((stats[E:2 * E] - p).abs() <= 1e-6 * p).all())
+    assert bool(((stats.fold()[E:2 * E] - p).abs() <= 1e-6 * p).all())
 
 
 def test_route_refuses():
     l = torch.zeros(8, 16, device="cuda")
     ids, gates, stats = dq.route(l, 2)
-    for call in (lambda: dq.route(l[0], 2), lambda: dq.route(l.t(), 2), lambda: dq.route(l, 2, mask=stats.bool()[:7]),
+    for call in (lambda: dq.route(l[0], 2), lambda: dq.route(l.t(), 2), lambda: dq.route(l, 2, mask=torch.zeros(7, dtype=torch.bool, device="cuda")),
                  lambda: dq.route(l, 2, mask=torch.zeros(8, dtype=torch.bool)),
-                 lambda: dq.route(l, 2, stats=stats[:-2]), lambda: dq.route(l, 2, accumulate=True),
+                 lambda: dq.route(l[:, :15], 2, stats=stats), lambda: dq.balance(stats.fold()[:-1], 2),
                  lambda: dq.route(l, 2, ids=ids[:, :1]), lambda: dq.route(l, 2, gates=gates.t()),
                  lambda: dq.route_backward(l, ids[:4]), lambda: dq.route_backward(l, ids, gates[:4]),
-                 lambda: dq.route_backward(l, ids, coef=stats[:15].float()),
+                 lambda: dq.route_backward(l, ids, coef=stats.fold()[:15].float()),
                  lambda: dq.route_backward(l, ids, out=l.bfloat16()),
                  lambda: dq.route_backward(l, ids, out=l[:4])):
         with pytest.raises(ValueError):
             call()
     for call in (lambda: dq.route(l, 2, mask=torch.zeros(8, device="cuda")), lambda: dq.route(l, 2, ids=ids.long()),
-                 lambda: dq.route(l, 2, stats=stats.float()), lambda: dq.route_backward(l, ids.long()),
+                 lambda: dq.route(l, 2, stats=stats.fold()), lambda: dq.balance(stats.fold().float(), 2), lambda: dq.route_backward(l, ids.long()),
                  lambda: dq.route_backward(l, ids, coef=torch.zeros(16, dtype=torch.float64, device="cuda"))):
         with pytest.raises(TypeError):
             call()
@@ -634,8 +655,10 @@ def test_route_on_another_stream():
     loss = dq.balance(got[2], 8, stream=s)
     d = dq.route_backward(l, got[0], coef=loss[1], stream=s)
     torch.cuda.current_stream().wait_stream(s)
-    assert all(torch.equal(a, b) for a, b in zip(want, got))
-    assert same(d, dq.route_backward(l, want[0], coef=dq.balance(want[2], 8)[1]))
+    assert all(torch.equal(a, b) for a, b in zip(want[:2], got[:2]))
+    want_loss = dq.balance(want[2], 8)
+    assert all(torch.equal(a, b) for a, b in zip(want_loss, loss))
+    assert same(d, dq.route_backward(l, want[0], coef=want_loss[1]))
 
 
 def test_step_in_graph_replays():
@@ -656,7 +679,7 @@ def test_step_in_graph_replays():
         y = dq.dropout(x, 0.1, residual=res, rnd=rnd, worker=1)
         d = dq.route_backward(l.detach(), ids, dg, coef, dloss)
         dx = dq.dropout_backward(y, 0.1, rnd=rnd, worker=1)
-        return ids, gates, stats, loss, coef, counts, y, d, dx
+        return ids, gates, stats.fold(), loss, coef, counts, y, d, dx
 
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())

@@ -113,40 +113,48 @@ def test_dropout_null_and_empty(lib):
 
 
 def _route(lib, l=FAKE, kind=dq.BF16, T=8, E=16, stride=16, mask=None, k=2, flags=1, ids=4 * FAKE, gates=5 * FAKE,
-           stats=6 * FAKE, ws=7 * FAKE, nbytes=1 << 20):
-    return lib.dq_route(l, kind, T, E, stride, mask, k, flags, ids, gates, stats, ws, nbytes, None)
+           part=7 * FAKE, nbytes=1 << 20):
+    return lib.dq_route(l, kind, T, E, stride, mask, k, flags, ids, gates, part, nbytes, None)
 
 
 @pytest.mark.parametrize("bad", [
     dict(kind=dq.PACKED), dict(T=-1), dict(T=(1 << 40) + 1), dict(E=0), dict(E=1025), dict(stride=-1), dict(k=0),
     dict(k=17, E=32), dict(k=3, E=2), dict(flags=4), dict(l=FAKE + 1), dict(kind=dq.F32, l=FAKE + 2),
-    dict(ids=4 * FAKE + 2), dict(gates=5 * FAKE + 2), dict(stats=6 * FAKE + 4)])
+    dict(ids=4 * FAKE + 2), dict(gates=5 * FAKE + 2)])
 def test_route_refuses(lib, bad):
     assert _route(lib, **bad) == dq.DQ_EINVAL
 
 
-def test_route_null_and_workspace(lib):
-    for name in ("l", "ids", "gates", "stats"):
+def test_route_null_and_part(lib):
+    for name in ("l", "ids", "gates"):
         assert _route(lib, **{name: None}) == dq.DQ_ENULL
-    need = lib.dq_route_workspace_bytes(8, 16)
+    need = lib.dq_route_part_bytes(8, 16)
     assert need > 0
     assert _route(lib, nbytes=need - 1) == dq.DQ_EWORKSPACE
-    assert _route(lib, ws=None) == dq.DQ_EWORKSPACE
-    assert _route(lib, ws=7 * FAKE + 128) == dq.DQ_EWORKSPACE
+    assert _route(lib, part=None) == dq.DQ_EWORKSPACE
+    assert _route(lib, part=7 * FAKE + 128) == dq.DQ_EWORKSPACE
     for args in ((-1, 16), (8, 0), (8, 1025), ((1 << 40) + 1, 16)):
-        assert lib.dq_route_workspace_bytes(*args) == 0
+        assert lib.dq_route_part_bytes(*args) == 0
     # bounded however many tokens there are
-    assert lib.dq_route_workspace_bytes(1 << 40, 1024) < 64 << 20
+    for E in (1, 8, 64, 256, 1024):
+        assert lib.dq_route_part_bytes(0, E) > 0
+        assert lib.dq_route_part_bytes(1 << 40, E) < 64 << 20
+
+
+def _balance(lib, parts=((7 * FAKE, 8),), n=None, sums=None, E=16, k=2, stats=FAKE, loss=2 * FAKE, coef=3 * FAKE,
+             counts=4 * FAKE):
+    array = None if parts is None else (dq.dq_route_part * max(1, len(parts)))(*parts)
+    return lib.dq_balance(array, len(parts or ()) if n is None else n, sums, E, k, stats, loss, coef, counts, None)
 
 
 def test_balance_refuses(lib):
-    ok = (FAKE, 16, 2, 2 * FAKE, 3 * FAKE, 4 * FAKE, None)
-    for i, v, rc in ((0, None, dq.DQ_ENULL), (0, FAKE + 4, dq.DQ_EINVAL), (1, 0, dq.DQ_EINVAL),
-                     (1, 1025, dq.DQ_EINVAL), (2, 0, dq.DQ_EINVAL), (2, 17, dq.DQ_EINVAL),
-                     (3, FAKE + 2, dq.DQ_EINVAL), (4, FAKE + 2, dq.DQ_EINVAL), (5, FAKE + 4, dq.DQ_EINVAL)):
-        args = list(ok)
-        args[i] = v
-        assert lib.dq_balance(*args) == rc, (i, v)
+    for bad in (dict(E=0), dict(E=1025), dict(k=0), dict(k=17, E=32), dict(k=17), dict(n=-1), dict(n=17),
+                dict(sums=FAKE + 4), dict(stats=FAKE + 4), dict(loss=FAKE + 2), dict(coef=FAKE + 2),
+                dict(counts=FAKE + 4), dict(parts=((7 * FAKE, -1),)), dict(parts=((7 * FAKE + 128, 8),)),
+                dict(parts=((7 * FAKE, (1 << 40) + 1),))):
+        assert _balance(lib, **bad) == dq.DQ_EINVAL, bad
+    for bad in (dict(parts=None, n=1), dict(parts=()), dict(parts=((None, 8),))):
+        assert _balance(lib, **bad) == dq.DQ_ENULL, bad
 
 
 def _backward(lib, l=FAKE, kind=dq.BF16, T=8, E=16, stride=16, mask=None, k=2, flags=1, ids=4 * FAKE, dg=5 * FAKE,
@@ -183,8 +191,11 @@ def test_binding_refuses_host_tensors_and_types():
             dq.dropout(bad, 0.1)
         with pytest.raises(TypeError):
             dq.route(bad, 2)
-    for bad in (torch.zeros(4, dtype=torch.float64), torch.zeros(1, dtype=torch.float64), torch.zeros(3, 3), None):
+    for bad in (torch.zeros(4, dtype=torch.float64), torch.zeros(1, dtype=torch.float64), torch.zeros(3, 3)):
         with pytest.raises(ValueError):
+            dq.balance(bad, 2)
+    for bad in (None, [1.0]):
+        with pytest.raises(TypeError):
             dq.balance(bad, 2)
 
 
