@@ -34,6 +34,7 @@ struct RoutePart {
 };
 constexpr int kRouteMaxParts = 16;
 constexpr int kBalanceColumns = 16;     // experts of a balance block
+constexpr int kBalanceFewRows = 16;     // up to so many rows one block takes all experts
 
 struct RouteArgs {
     const void *logits;
@@ -54,7 +55,6 @@ struct BalanceArgs {
     double *stats;
     float *loss, *coef;
     int64_t *counts;
-    int32_t columns;        // experts of a block: kBalanceColumns, or all
 };
 
 struct RouteBackwardArgs {

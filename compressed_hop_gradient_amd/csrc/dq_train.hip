@@ -502,46 +502,82 @@ __global__ __launch_bounds__(256, (CH == 4 ? (F32 ? 2 : 3) : 4)) void k_route(Ro
     }
 }
 
-// Folds the parts in a fixed order and computes the loss.  A block takes
-// a.columns experts, 1024 / a.columns threads each over the rows, then a tree;
-// where there are several blocks, the last one to finish adds up their shares of
-// the loss, in block order.
+__device__ __forceinline__ double wave_sum(double v, int from = 32) {
+    for (int d = from; d; d >>= 1) v += __shfl_xor(v, d, 64);
+    return v;
+}
+
+// Folds the parts and computes the loss, every sum in a fixed order.  A block
+// of 16 waves takes 16 experts, 64 threads for each over the rows; where there
+// are few rows one block takes all experts, a thread each.  The last of several
+// blocks to finish adds up their shares of the loss.
+template <bool ONE>
 __global__ __launch_bounds__(1024) void k_balance(BalanceArgs a) {
-    __shared__ double ps[1024], cs[1024], ts[1024];
-    const int i = threadIdx.x, columns = a.columns;
-    const int c = i & (columns - 1), j = (int)blockIdx.x * columns + c;
+    constexpr int COLUMNS = ONE ? kRouteMaxExperts : kBalanceColumns;
+    __shared__ double ps[16][16], cs[16][16], ts[16];
+    const int i = threadIdx.x, lane = i & 63, wave = i >> 6;
+    const int j = ONE ? i : (int)blockIdx.x * COLUMNS + i % COLUMNS;
+    const double sum_n = a.sums ? a.sums[2 * a.E] : 0.0;
     double p = 0.0, n = 0.0, t = 0.0;
+    // rows in groups of U whose loads are all in flight before the first is added
+    constexpr int STEP = ONE ? 1 : 1024 / COLUMNS, U = 12;
+    const int col = j < a.E ? j : 0;
     for (int q = 0; q < a.parts; q++) {
         const RoutePart &part = a.part[q];
-        for (int b = i; b < part.nblk; b += 1024) t += part.routed[b];
-        if (j < a.E) {
-#pragma unroll 8
-            for (int b = i / columns; b < part.nblk; b += 1024 / columns) {
-                p += part.psum[b * a.E + j];
-                n += part.count[b * a.E + j];
+        const int rows = part.nblk;
+        for (int b0 = ONE ? 0 : i / COLUMNS; b0 < rows; b0 += U * STEP) {
+            float x[U];
+            uint32_t m[U];
+#pragma unroll
+            for (int u = 0; u < U; u++) {
+                const int at = min(b0 + u * STEP, rows - 1) * a.E + col;
+                x[u] = part.psum[at];
+                m[u] = part.count[at];
+            }
+#pragma unroll
+            for (int u = 0; u < U; u++) {
+                const bool there = b0 + u * STEP < rows;
+                p += there ? x[u] : 0.0f;
+                n += there ? m[u] : 0u;
             }
         }
+        for (int b = i; b < rows; b += 1024) t += part.routed[b];
     }
-    ps[i] = p;
-    cs[i] = n;
-    ts[i] = t;
+    t = wave_sum(t);
+    if (!ONE) {
+        p += __shfl_xor(p, 32, 64);
+        p += __shfl_xor(p, 16, 64);
+        n += __shfl_xor(n, 32, 64);
+        n += __shfl_xor(n, 16, 64);
+        if (lane < 16) {
+            ps[wave][lane] = p;
+            cs[wave][lane] = n;
+        }
+    }
+    if (lane == 0) ts[wave] = t;
     __syncthreads();
-    for (int d = 512; d; d >>= 1) {
-        if (i < d) {
-            if (d >= columns) {
-                ps[i] += ps[i + d];
-                cs[i] += cs[i + d];
-            }
-            ts[i] += ts[i + d];
+    if (!ONE && wave != 0) return;
+    double N = sum_n;
+    for (int w = 0; w < 16; w++) N += ts[w];
+    if (!ONE) {
+        // lane c adds up the waves w, w + 4, .. with w = c / 16
+        p = n = 0.0;
+        for (int w = lane / 16; w < 16; w += 4) {
+            p += ps[w][lane % 16];
+            n += cs[w][lane % 16];
         }
-        __syncthreads();
+        p += __shfl_xor(p, 32, 64);
+        p += __shfl_xor(p, 16, 64);
+        n += __shfl_xor(n, 32, 64);
+        n += __shfl_xor(n, 16, 64);
     }
-    const double N = ts[0] + (a.sums ? a.sums[2 * a.E] : 0.0);
     const double f = N > 0.0 ? (double)a.E / ((double)a.k * N * N) : 0.0;
     double share = 0.0;
-    if (i < columns && j < a.E) {
-        p = ps[i] + (a.sums ? a.sums[a.E + j] : 0.0);
-        n = cs[i] + (a.sums ? a.sums[j] : 0.0);
+    if ((ONE || lane < 16) && j < a.E) {
+        if (a.sums) {
+            n += a.sums[j];
+            p += a.sums[a.E + j];
+        }
         if (a.stats) {
             a.stats[j] = n;
             a.stats[a.E + j] = p;
@@ -551,35 +587,30 @@ __global__ __launch_bounds__(1024) void k_balance(BalanceArgs a) {
         if (a.counts) a.counts[j] = (int64_t)n;
         share = w * p;
     }
-    __syncthreads();
-    ps[i] = share;
-    __syncthreads();
-    for (int d = columns / 2; d; d >>= 1) {
-        if (i < d) ps[i] += ps[i + d];
+    share = wave_sum(share, ONE ? 32 : 8);
+    if (ONE) {
+        if (lane == 0) ps[0][wave] = share;
         __syncthreads();
-    }
-    // a.stats may be a.sums: its last element, which every block reads, is
-    // written by the last one
-    if (gridDim.x == 1) {
-        if (i == 0) {
-            if (a.loss) *a.loss = (float)ps[0];
-            if (a.stats) a.stats[2 * a.E] = N;
+        share = 0.0;
+        for (int w = 0; w < 16; w++) share += ps[0][w];
+    } else if (gridDim.x > 1) {
+        const RoutePart &first = a.part[0];
+        uint32_t before = 0;
+        if (lane == 0) {
+            __hip_atomic_store(first.share + blockIdx.x, share, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            before = __hip_atomic_fetch_add(first.done, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
         }
-        return;
+        if (__builtin_amdgcn_readfirstlane(before) != gridDim.x - 1) return;
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+        share = lane < (int)gridDim.x ? __hip_atomic_load(first.share + lane, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)
+                                      : 0.0;
+        share = wave_sum(share);
+        if (lane == 0) *first.done = 0;
     }
-    const RoutePart &first = a.part[0];
+    // a.stats may be a.sums, whose last element every block reads
     if (i == 0) {
-        __hip_atomic_store(first.share + blockIdx.x, ps[0], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        const uint32_t before =
-            __hip_atomic_fetch_add(first.done, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
-        if (before == gridDim.x - 1) {
-            double sum = 0.0;
-            for (unsigned b = 0; b < gridDim.x; b++)
-                sum += __hip_atomic_load(first.share + b, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            if (a.loss) *a.loss = (float)sum;
-            if (a.stats) a.stats[2 * a.E] = N;
-            *first.done = 0;
-        }
+        if (a.loss) *a.loss = (float)share;
+        if (a.stats) a.stats[2 * a.E] = N;
     }
 }
 
@@ -766,13 +797,15 @@ hipError_t launch_route(const RouteArgs &a, int f32, hipStream_t s) {
     return f32 ? route_experts<true>(a, s) : route_experts<false>(a, s);
 }
 
-hipError_t launch_balance(const BalanceArgs &args, hipStream_t s) {
-    BalanceArgs a = args;
+hipError_t launch_balance(const BalanceArgs &a, hipStream_t s) {
+    static_assert(kRouteMaxExperts / kBalanceColumns <= 64, "a wave adds up the blocks' shares");
     int64_t rows = 0;
     for (int q = 0; q < a.parts; q++) rows += a.part[q].nblk;
-    // few rows: one block, a thread per expert
-    a.columns = rows <= 8 ? kRouteMaxExperts : kBalanceColumns;
-    hipLaunchKernelGGL(k_balance, dim3((unsigned)((a.E + a.columns - 1) / a.columns)), dim3(1024), 0, s, a);
+    if (rows <= kBalanceFewRows)
+        hipLaunchKernelGGL(k_balance<true>, dim3(1), dim3(1024), 0, s, a);
+    else
+        hipLaunchKernelGGL(k_balance<false>, dim3((unsigned)((a.E + kBalanceColumns - 1) / kBalanceColumns)), dim3(1024),
+                           0, s, a);
     return hipGetLastError();
 }
 
