@@ -371,7 +371,7 @@ __device__ __forceinline__ void softmax_row(const Chunk<F32> c[CH], float l[8 * 
     m = -INFINITY;
 #pragma unroll
     for (int v = 0; v < 8 * CH; v++) {
-        l[v] = c[v / 8].at(v % 8) + 0.0f;      // -0 becomes +0
+        l[v] = c[v / 8].at(v % 8);
         m = fmaxf(m, l[v]);
     }
     m = group_max<G>(m);
@@ -427,7 +427,7 @@ __global__ __launch_bounds__(256, (CH == 4 ? (F32 ? 2 : 3) : 4)) void k_route(Ro
         asm volatile("" : "+v"(inv0));
         KT key[V < KP ? KP : V];
 #pragma unroll
-        for (int v = 0; v < V; v++) key[v] = K::make(l[v], inv0 ^ (8u * G * (v / 8)), v % 8);
+        for (int v = 0; v < V; v++) key[v] = K::make(l[v] + 0.0f, inv0 ^ (8u * G * (v / 8)), v % 8);   // -0 is +0
 #pragma unroll
         for (int v = V; v < KP; v++) key[v] = K::none();
         if (__any(Z != Z)) {
@@ -620,130 +620,122 @@ __device__ __forceinline__ void wave_lds_sync() {
     __builtin_amdgcn_wave_barrier();
 }
 
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-    for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d, 64);
-    return v;
-}
-__device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-    for (int d = 32; d; d >>= 1) v = fmaxf(v, __shfl_xor(v, d, 64));
-    return v;
-}
-// One wave per token, V experts per lane (lane, lane + 64, ..).  With m the
-// largest logit, e = exp(l - m) and Z = sum e; Z = 0 only where every logit is
-// -inf, and NaN or +inf makes Z NaN and with it the row's gates and sums.
-template <bool F32, int V>
-__device__ __forceinline__ void wave_softmax(const typename Elem<F32>::type *row, int E, int lane, float l[V],
-                                            float e[V], float &m, float &Z) {
-    m = -INFINITY;
-#pragma unroll
-    for (int v = 0; v < V; v++) {
-        const int j = lane + 64 * v;
-        l[v] = j < E ? Elem<F32>::up(row[j]) : -INFINITY;
-        m = fmaxf(m, l[v]);
-    }
-    m = wave_max(m);
-    if (m == -INFINITY) m = 0.0f;
-    Z = 0.0f;
-#pragma unroll
-    for (int v = 0; v < V; v++) {
-        e[v] = expf(l[v] - m);
-        Z += e[v];
-    }
-    Z = wave_sum(Z);
-}
-
-// One wave per token.  The chosen experts' own term goes through a row of LDS,
-// scattered by the lanes that hold the choices.
-template <bool F32, int V>
+// The gradient of a row is p_j (a_j - D) + h_j, where h is 0 but for the chosen
+// experts: the lanes that hold the choices scatter it into a row of LDS, which is 0
+// between rows.  A row is read and written once; its choices are read a row
+// ahead, so that their logits are on the way while the softmax is computed.
+template <bool F32, int G, int CH, int S, bool VEC>
 __global__ __launch_bounds__(256) void k_route_backward(RouteBackwardArgs a) {
-    typedef typename Elem<F32>::type T;
-    __shared__ float chosen[4][64 * V];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    float *own = chosen[wave];
-    float up[V];
+    typedef Elem<F32> El;
+    typedef typename El::type T;
+    constexpr int V = 8 * CH, C = V * G, R = 256 / G;
+    __shared__ alignas(16) float rows[R * C];
+    const int g = threadIdx.x % G, r = threadIdx.x / G;
+    float *h = rows + r * C;
+    const T *logits = static_cast<const T *>(a.logits);
     const float w = a.dloss ? *a.dloss : 1.0f;
+    float up[V];
 #pragma unroll
     for (int v = 0; v < V; v++) {
-        const int j = lane + 64 * v;
+        const int j = 8 * ((v / 8) * G + g) + v % 8;
         up[v] = a.coef && j < a.E ? w * a.coef[j] : 0.0f;
-        own[j] = 0.0f;
+        h[j] = 0.0f;
     }
-    for (int64_t t = (int64_t)blockIdx.x * 4 + wave; t < a.tokens; t += 4 * (int64_t)gridDim.x) {
-        float l[V], e[V], m = 0.0f, Z = 0.0f;
-        if (!a.mask || a.mask[t])
-            wave_softmax<F32, V>(static_cast<const T *>(a.logits) + t * a.stride, a.E, lane, l, e, m, Z);
-        T *out = static_cast<T *>(a.dlogits) + t * a.dstride;
-        if (Z == 0.0f) {
+    struct Row {
+        Chunk<F32> c[CH];
+        int id[S];
+        float dg[S];
+    };
+    // lane g holds choices g, g + G, ..
+    const auto load = [&](Row &row, int64_t t) {
+        const bool there = t < a.tokens && (!a.mask || a.mask[t]);
+        load_row<F32, G, CH, VEC>(row.c, logits + t * a.stride, g, a.E, there);
 #pragma unroll
-            for (int v = 0; v < V; v++)
-                if (lane + 64 * v < a.E) out[lane + 64 * v] = Elem<F32>::down(0.0f);
-            continue;
+        for (int s = 0; s < S; s++) {
+            row.id[s] = -1;
+            row.dg[s] = 0.0f;
+            if (there && a.dgates && s * G + g < a.k) {
+                row.id[s] = a.ids[t * a.k + s * G + g];
+                row.dg[s] = a.dgates[t * a.k + s * G + g];
+            }
         }
-        const float inv = 1.0f / Z;
+    };
+    const int64_t step = (int64_t)gridDim.x * R;
+    int64_t t = (int64_t)blockIdx.x * R + r;
+    Row next;
+    load(next, t);
+    for (int64_t base = (int64_t)blockIdx.x * R; base < a.tokens; base += step, t += step) {
+        Row row = next;
+        float gs[S];
+#pragma unroll
+        for (int s = 0; s < S; s++) {
+            if ((uint32_t)row.id[s] >= (uint32_t)a.E) row.id[s] = -1;
+            gs[s] = row.id[s] >= 0 ? El::up(logits[t * a.stride + row.id[s]]) : -INFINITY;
+        }
+        load(next, t + step);
+        float l[V], e[V], m, Z;
+        softmax_row<F32, G, CH>(row.c, l, e, m, Z);
+        const float inv = Z == 0.0f ? 0.0f : 1.0f / Z;
         float dot = 0.0f;
 #pragma unroll
         for (int v = 0; v < V; v++) {
             e[v] *= inv;
-            dot += e[v] * up[v];
+            dot = __builtin_fmaf(e[v], up[v], dot);
         }
-        int id = -1;
-        float dg = 0.0f, g = 0.0f;
-        if (a.dgates && lane < a.k) {
-            id = a.ids[t * a.k + lane];
-            if ((uint32_t)id >= (uint32_t)a.E) id = -1;
-            if (id >= 0) {
-                dg = a.dgates[t * a.k + lane];
-                g = expf(Elem<F32>::up(static_cast<const T *>(a.logits)[t * a.stride + id]) - m);
+        float top = 0.0f, gd = 0.0f;
+#pragma unroll
+        for (int s = 0; s < S; s++) {
+            gs[s] = row.id[s] >= 0 ? __builtin_amdgcn_exp2f((gs[s] - m) * kLog2e) : 0.0f;
+            top += gs[s];
+        }
+        float by = inv;
+        if (a.renorm) {
+            top = group_sum<G>(top);
+            by = top == 0.0f ? 0.0f : 1.0f / top;      // no choice
+        }
+#pragma unroll
+        for (int s = 0; s < S; s++) {
+            gs[s] *= by;
+            if (row.id[s] >= 0) gd = __builtin_fmaf(gs[s], row.dg[s], gd);
+        }
+        gd = group_sum<G>(gd);
+        dot = group_sum<G>(dot) + (a.renorm ? 0.0f : gd);
+#pragma unroll
+        for (int s = 0; s < S; s++)
+            if (row.id[s] >= 0) h[row.id[s]] = gs[s] * (a.renorm ? row.dg[s] - gd : row.dg[s]);
+        wave_lds_sync();
+        if (t < a.tokens) {
+            T *out = static_cast<T *>(a.dlogits) + t * a.dstride;
+#pragma unroll
+            for (int i = 0; i < CH; i++) {
+                const int at = 8 * (i * G + g);
+                float d[8];
+                __builtin_memcpy(d, __builtin_assume_aligned(h + at, 16), sizeof d);
+#pragma unroll
+                for (int j = 0; j < 8; j++) d[j] = __builtin_fmaf(e[8 * i + j], up[8 * i + j] - dot, d[j]);
+                if (VEC) {
+                    if (at < a.E) store8<F32>(out, at, d);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; j++)
+                        if (at + j < a.E) out[at + j] = El::down(d[j]);
+                }
             }
         }
-        float top = 0.0f;
-        if (a.renorm) {
-            top = wave_sum(g);
-            g = top != 0.0f ? g / top : 0.0f;   // top = 0 without a choice
-        } else {
-            g *= inv;
-        }
-        const float gd = wave_sum(g * dg);
-        if (id >= 0) own[id] = g * (a.renorm ? dg - gd : dg);
-        dot = wave_sum(dot) + (a.renorm ? 0.0f : gd);
         wave_lds_sync();
 #pragma unroll
-        for (int v = 0; v < V; v++) {
-            const int j = lane + 64 * v;
-            if (j < a.E) out[j] = Elem<F32>::down(e[v] * (up[v] - dot) + own[j]);
-        }
-        wave_lds_sync();
-        if (id >= 0) own[id] = 0.0f;
+        for (int s = 0; s < S; s++)
+            if (row.id[s] >= 0) h[row.id[s]] = 0.0f;
     }
 }
-
-template <template <bool, int> class Launch, class... Args>
-hipError_t by_width(int E, int f32, Args... args) {
-    const int v = (E + 63) / 64;
-    if (f32) {
-        if (v <= 1) return Launch<true, 1>::go(args...);
-        if (v <= 2) return Launch<true, 2>::go(args...);
-        if (v <= 4) return Launch<true, 4>::go(args...);
-        if (v <= 8) return Launch<true, 8>::go(args...);
-        return Launch<true, 16>::go(args...);
-    }
-    if (v <= 1) return Launch<false, 1>::go(args...);
-    if (v <= 2) return Launch<false, 2>::go(args...);
-    if (v <= 4) return Launch<false, 4>::go(args...);
-    if (v <= 8) return Launch<false, 8>::go(args...);
-    return Launch<false, 16>::go(args...);
-}
-
 
 template <bool F32, int G, int CH, bool VEC>
 hipError_t route_choices(const RouteArgs &a, hipStream_t s) {
     const dim3 grid((unsigned)a.part.nblk), block(256);
     if (a.k <= 2) hipLaunchKernelGGL((k_route<F32, G, CH, 2, VEC>), grid, block, 0, s, a);
     else if (a.k <= 4) hipLaunchKernelGGL((k_route<F32, G, CH, 4, VEC>), grid, block, 0, s, a);
-    else if (a.k <= 8) hipLaunchKernelGGL((k_route<F32, G, CH, 8, VEC>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((k_route<F32, G, CH, 16, VEC>), grid, block, 0, s, a);
+    else if (a.k <= 8 || G * CH == 1) hipLaunchKernelGGL((k_route<F32, G, CH, 8, VEC>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((k_route<F32, G, CH, G * CH == 1 ? 8 : 16, VEC>), grid, block, 0, s, a);
     return hipGetLastError();
 }
 
@@ -760,23 +752,44 @@ auto by_experts(int E, F f) {
     return f(std::integral_constant<int, 32>(), std::integral_constant<int, 4>());
 }
 
+bool rows_on_16(const void *p, int64_t stride, int E, bool f32) {
+    return E % 8 == 0 && reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride * (f32 ? 4 : 2) % 16 == 0;
+}
+
 template <bool F32>
 hipError_t route_experts(const RouteArgs &a, hipStream_t s) {
-    const bool vec = a.E % 8 == 0 && reinterpret_cast<uintptr_t>(a.logits) % 16 == 0 &&
-                     a.stride * (F32 ? 4 : 2) % 16 == 0;
+    const bool vec = rows_on_16(a.logits, a.stride, a.E, F32);
     return by_experts(a.E, [&](auto G, auto CH) {
-        return vec ? route_choices<F32, G.value, CH.value, true>(a, s) : route_choices<F32, G.value, CH.value, false>(a, s);
+        return vec ? route_choices<F32, G.value, CH.value, true>(a, s)
+                   : route_choices<F32, G.value, CH.value, false>(a, s);
     });
 }
-template <bool F32, int V>
-struct Backward {
-    static hipError_t go(const RouteBackwardArgs *a, hipStream_t s) {
-        const int64_t want = (a->tokens + 3) / 4;
-        hipLaunchKernelGGL((k_route_backward<F32, V>), dim3((unsigned)(want < 8192 ? want : 8192)), dim3(256), 0, s,
-                           *a);
-        return hipGetLastError();
-    }
-};
+
+template <bool F32, int G, int CH, bool VEC>
+hipError_t backward_choices(const RouteBackwardArgs &a, hipStream_t s) {
+    // choices of a lane: at most all of 8 experts in one lane
+    constexpr int R = 256 / G, most = G == 1 ? 8 : G < kRouteMaxTopK ? kRouteMaxTopK / G : 1;
+    static_assert(G > 1 || CH == 1, "");
+    const int64_t want = (a.tokens + R - 1) / R;
+    const dim3 grid((unsigned)(want < 1024 ? want : 1024)), block(256);
+    const int each = (a.k + G - 1) / G;
+    if (each <= 1 || most == 1) hipLaunchKernelGGL((k_route_backward<F32, G, CH, 1, VEC>), grid, block, 0, s, a);
+    else if (each <= 2 || most == 2)
+        hipLaunchKernelGGL((k_route_backward<F32, G, CH, most < 2 ? most : 2, VEC>), grid, block, 0, s, a);
+    else if (each <= 4 || most == 4)
+        hipLaunchKernelGGL((k_route_backward<F32, G, CH, most < 4 ? most : 4, VEC>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((k_route_backward<F32, G, CH, most, VEC>), grid, block, 0, s, a);
+    return hipGetLastError();
+}
+
+template <bool F32>
+hipError_t backward_experts(const RouteBackwardArgs &a, hipStream_t s) {
+    const bool vec = rows_on_16(a.logits, a.stride, a.E, F32) && rows_on_16(a.dlogits, a.dstride, a.E, F32);
+    return by_experts(a.E, [&](auto G, auto CH) {
+        return vec ? backward_choices<F32, G.value, CH.value, true>(a, s)
+                   : backward_choices<F32, G.value, CH.value, false>(a, s);
+    });
+}
 
 }  // namespace
 
@@ -810,7 +823,7 @@ hipError_t launch_balance(const BalanceArgs &a, hipStream_t s) {
 }
 
 hipError_t launch_route_backward(const RouteBackwardArgs &a, int f32, hipStream_t s) {
-    return by_width<Backward>(a.E, f32, &a, s);
+    return f32 ? backward_experts<true>(a, s) : backward_experts<false>(a, s);
 }
 
 }  // namespace dq
