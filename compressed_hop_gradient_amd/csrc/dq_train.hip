@@ -231,51 +231,88 @@ __device__ __forceinline__ void load_row(Chunk<F32> c[CH], const typename Elem<F
 }
 
 // Order key of a logit and its expert: keys are distinct, a larger logit has
-// the larger key (-0 = +0, NaN above +inf) and of equal ones the lower index.
-// bf16: the 16 ordered bits, then 16 bits of ~index.  fp32: 32 ordered bits
-// and 20 bits of ~index as the mantissa of a double in [1, 2), which has a
-// one-instruction maximum.
+// the larger key and of equal ones the lower index.  bf16: the bits in signed
+// order, then 16 bits of ~index.  fp32: the bits in unsigned order and 20 bits of
+// ~index as the mantissa of a double in [1, 2), which has a one-instruction
+// maximum.  make8 is for rows without NaN and ranks -0 below +0; make takes
+// anything (-0 = +0, NaN above +inf).  inv: ~index of the first of 8 experts.
 template <bool F32>
 struct Key;
 template <>
 struct Key<false> {
-    typedef uint32_t type;
-    static __device__ __forceinline__ uint32_t none() { return 0; }
-    // j < 8 is flipped in the low bits of inv
-    static __device__ __forceinline__ uint32_t make(float x, uint32_t inv, int j) {
-        const uint32_t u = __float_as_uint(x);
-        const uint32_t flip = __builtin_amdgcn_bitop3_b32((int32_t)u >> 31, 0x7FFF0000u, j, 0x6A);   // (a & b) ^ c
-        return xor3(u, flip, inv ^ 0x80000000u);
+    typedef int32_t type;
+    static constexpr int32_t kNone = INT32_MIN;
+    static __device__ __forceinline__ uint32_t ordered(uint32_t w) {     // both halves; its own inverse
+        typedef short s16x2 __attribute__((ext_vector_type(2)));
+        const s16x2 sign = __builtin_bit_cast(s16x2, w) >> 15;
+        return __builtin_amdgcn_bitop3_b32(__builtin_bit_cast(uint32_t, sign), 0x7FFF7FFFu, w, 0x6A);   // (a & b) ^ c
     }
-    static __device__ __forceinline__ uint32_t nan(uint32_t inv) { return 0xFFFF0000u | inv; }
-    static __device__ __forceinline__ uint32_t hi(uint32_t a, uint32_t b) { return max(a, b); }
-    static __device__ __forceinline__ uint32_t lo(uint32_t a, uint32_t b) { return min(a, b); }
-    static __device__ __forceinline__ bool open(uint32_t k) { return k >= 0x00800000u; }   // above -inf
-    static __device__ __forceinline__ int index(uint32_t k) { return (int)(~k & 0xFFFFu); }
-    static __device__ __forceinline__ float value(uint32_t k) {
-        return __uint_as_float((k & 0x80000000u ? k ^ 0x80000000u : ~k) & 0xFFFF0000u);
+    static __device__ __forceinline__ void make8(const Chunk<false> &c, uint32_t inv, int32_t key[8]) {
+#pragma unroll
+        for (int q = 0; q < 4; q++) {
+            const uint32_t o = ordered(c.w[q]);
+            key[2 * q] = (int32_t)(o << 16 | (inv ^ (2 * q)));
+            key[2 * q + 1] = (int32_t)((o & 0xFFFF0000u) | (inv ^ (2 * q + 1)));
+        }
+    }
+    static __device__ __forceinline__ int32_t make(float x, uint32_t inv) {
+        x += 0.0f;
+        const uint32_t o = x != x ? 0x7FFF0000u : ordered(__float_as_uint(x)) & 0xFFFF0000u;
+        return (int32_t)(o | inv);
+    }
+    static __device__ __forceinline__ int32_t hi(int32_t a, int32_t b) { return max(a, b); }
+    static __device__ __forceinline__ int32_t lo(int32_t a, int32_t b) { return min(a, b); }
+    static __device__ __forceinline__ int32_t flip(int32_t k, uint32_t x) { return (int32_t)((uint32_t)k ^ x); }
+    static __device__ __forceinline__ bool open(int32_t k) { return k >= (int32_t)0x80800000u; }   // above -inf
+    static __device__ __forceinline__ bool positive(int32_t k) { return k >= 0x00010000; }
+    static __device__ __forceinline__ bool zero(int32_t k) { return (uint32_t)(k + 0x10000) < 0x20000u; }
+    static __device__ __forceinline__ int index(int32_t k) { return (int)(~(uint32_t)k & 0xFFFFu); }
+    static __device__ __forceinline__ float value(int32_t k) {
+        return __uint_as_float(ordered((uint32_t)k) & 0xFFFF0000u);
     }
     template <class F>
-    static __device__ __forceinline__ uint32_t moved(uint32_t k, F f) { return f(k); }
+    static __device__ __forceinline__ int32_t moved(int32_t k, F f) { return (int32_t)f((uint32_t)k); }
 };
 template <>
 struct Key<true> {
     typedef double type;
+    static constexpr double kNone = 1.0;
     static __device__ __forceinline__ double pack(uint32_t o, uint32_t inv) {
-        return __builtin_bit_cast(double, (uint64_t)(0x3FF00000u | o >> 12) << 32 | (o << 20 | inv));
+        const uint32_t h = __builtin_amdgcn_alignbit(0x3FFu, o, 12), l = o << 20 | inv;
+        return __builtin_bit_cast(double, (uint64_t)h << 32 | l);
     }
-    static __device__ __forceinline__ double none() { return 1.0; }
-    static __device__ __forceinline__ double make(float x, uint32_t inv, int j) {
-        const uint32_t u = __float_as_uint(x);
-        return pack(u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u), inv ^ j);
+    static __device__ __forceinline__ uint32_t ordered(uint32_t u) {
+        return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
     }
-    static __device__ __forceinline__ double nan(uint32_t inv) { return pack(0xFFFFFFFFu, inv); }
-    static __device__ __forceinline__ double hi(double a, double b) { return __builtin_fmax(a, b); }
-    static __device__ __forceinline__ double lo(double a, double b) { return __builtin_fmin(a, b); }
+    static __device__ __forceinline__ void make8(const Chunk<true> &c, uint32_t inv, double key[8]) {
+#pragma unroll
+        for (int j = 0; j < 8; j++) key[j] = pack(ordered(__float_as_uint(c.v[j])), inv ^ j);
+    }
+    static __device__ __forceinline__ double make(float x, uint32_t inv) {
+        x += 0.0f;
+        return pack(x != x ? 0xFFFFFFFFu : ordered(__float_as_uint(x)), inv);
+    }
+    // (fmax and fmin would first quiet every operand that they cannot prove to
+    // be no signalling NaN)
+    static __device__ __forceinline__ double hi(double a, double b) {
+        double r;
+        asm("v_max_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+        return r;
+    }
+    static __device__ __forceinline__ double lo(double a, double b) {
+        double r;
+        asm("v_min_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+        return r;
+    }
+    static __device__ __forceinline__ double flip(double k, uint32_t x) {
+        return __builtin_bit_cast(double, __builtin_bit_cast(uint64_t, k) ^ x);
+    }
     static __device__ __forceinline__ uint32_t order(double k) {
         return (uint32_t)(__builtin_bit_cast(uint64_t, k) >> 20);
     }
-    static __device__ __forceinline__ bool open(double k) { return order(k) > 0x007FFFFFu; }
+    static __device__ __forceinline__ bool open(double k) { return order(k) > 0x007FFFFFu; }       // above -inf
+    static __device__ __forceinline__ bool positive(double k) { return order(k) > 0x80000000u; }
+    static __device__ __forceinline__ bool zero(double k) { return order(k) - 0x7FFFFFFFu < 2u; }
     static __device__ __forceinline__ int index(double k) {
         return (int)(~(uint32_t)__builtin_bit_cast(uint64_t, k) & 0xFFFFu);
     }
@@ -317,6 +354,15 @@ __device__ __forceinline__ float group_sum(float x) {
     return x;
 }
 
+template <bool F32, int G, int D = 1>
+__device__ __forceinline__ typename Key<F32>::type group_most(typename Key<F32>::type k) {
+    if constexpr (D < G) {
+        const auto other = Key<F32>::moved(k, [](uint32_t x) { return other_half<D>(x); });
+        return group_most<F32, G, 2 * D>(Key<F32>::hi(k, other));
+    }
+    return k;
+}
+
 // Falling lists of the KP largest keys.  Sorting: Batcher's odd-even merge
 // network; two lists: the larger of a_i and b_(KP-1-i) are the KP largest, a
 // bitonic sequence that log2 KP stages sort.
@@ -347,6 +393,12 @@ struct Best {
             for (int i = 0; i < KP; i++)
                 if (!(i & d)) order(v[i], v[i | d]);
     }
+    // v takes the KP largest of v and w
+    static __device__ __forceinline__ void merge(T *v, const T *w) {
+#pragma unroll
+        for (int i = 0; i < KP; i++) v[i] = K::hi(v[i], w[KP - 1 - i]);
+        settle(v);
+    }
     template <int G, int D = 1>
     static __device__ __forceinline__ void across(T *v) {
         if constexpr (D < G) {
@@ -362,27 +414,97 @@ struct Best {
     }
 };
 
-// Logits of a row, their largest and e = exp(l - m), and Z = sum e.  Z = 0 only
-// where every logit is -inf; NaN or +inf makes Z NaN, and with it all that is
-// divided by it.
+// 1 / x to an ulp for 1 <= x < 2^126; NaN stays NaN
+__device__ __forceinline__ float reciprocal(float x) {
+    const float r = __builtin_amdgcn_rcpf(x);
+    return __builtin_fmaf(__builtin_fmaf(-x, r, 1.0f), r, r);
+}
+
+// e = exp(l - m) of a row whose largest logit is m, and Z = sum e.  Z = 0 only
+// where every logit is -inf (m is 0 there); NaN or +inf makes Z NaN, and with
+// it all that is divided by it.  The exponent (l - m) log2 e takes one fma, whose
+// rounding of m log2 e is the same factor in every e and cancels in e / Z;
+// near the ends of the range m log2 e overflows and the difference comes first.
 template <bool F32, int G, int CH>
-__device__ __forceinline__ void softmax_row(const Chunk<F32> c[CH], float l[8 * CH], float e[8 * CH], float &m,
-                                            float &Z) {
-    m = -INFINITY;
-#pragma unroll
-    for (int v = 0; v < 8 * CH; v++) {
-        l[v] = c[v / 8].at(v % 8);
-        m = fmaxf(m, l[v]);
-    }
-    m = group_max<G>(m);
-    if (m == -INFINITY) m = 0.0f;
+__device__ __forceinline__ void exponentials(const Chunk<F32> c[CH], float m, float e[8 * CH], float &Z) {
     float z[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (__any(!(fabsf(m) < 1e37f))) {
+        asm volatile("; extreme logits");        // a branch, not selects
 #pragma unroll
-    for (int v = 0; v < 8 * CH; v++) {
-        e[v] = __builtin_amdgcn_exp2f((l[v] - m) * kLog2e);
-        z[v % 4] += e[v];
+        for (int v = 0; v < 8 * CH; v++) e[v] = __builtin_amdgcn_exp2f((c[v / 8].at(v % 8) - m) * kLog2e);
+    } else {
+        const float by = -m * kLog2e;
+#pragma unroll
+        for (int v = 0; v < 8 * CH; v++)
+            e[v] = __builtin_amdgcn_exp2f(__builtin_fmaf(c[v / 8].at(v % 8), kLog2e, by));
     }
+#pragma unroll
+    for (int v = 0; v < 8 * CH; v++) z[v % 4] += e[v];
     Z = group_sum<G>((z[0] + z[1]) + (z[2] + z[3]));
+}
+
+// The falling list of a row's KP largest keys, in all of its lanes
+template <bool F32, int G, int CH, int KP>
+__device__ __forceinline__ void pick(const Chunk<F32> c[CH], uint32_t inv, typename Key<F32>::type best[KP]) {
+    typedef Key<F32> K;
+    typedef Best<F32, KP> B;
+    constexpr int U = KP < 8 ? 8 : KP, N = U / 8;     // elements and chunks that are sorted together
+#pragma unroll
+    for (int i = 0; i < CH; i += N) {
+        typename K::type key[U];
+#pragma unroll
+        for (int n = 0; n < N; n++) {
+            if (i + n < CH) {
+                K::make8(c[i + n], inv, key + 8 * n);
+                if (n > 0)
+#pragma unroll
+                    for (int j = 0; j < 8; j++) key[8 * n + j] = K::flip(key[8 * n + j], 8u * G * n);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; j++) key[8 * n + j] = K::kNone;
+            }
+        }
+        B::sort(key);
+#pragma unroll
+        for (int v = KP; v < U; v += KP) {
+            B::sort(key + v);
+            B::merge(key, key + v);
+        }
+        if (i == 0) {
+#pragma unroll
+            for (int j = 0; j < KP; j++) best[j] = key[j];
+        } else {
+            // chunk i's indices
+#pragma unroll
+            for (int j = 0; j < KP; j++) key[j] = K::flip(key[j], 8u * G * i);
+            B::merge(best, key);
+        }
+    }
+    B::template across<G>(best);
+}
+
+// The same list one key at a time, for rows with NaN or with zeros of both
+// signs among the choices
+template <bool F32, int G, int CH, int KP>
+__device__ __forceinline__ void pick_any(const Chunk<F32> c[CH], uint32_t inv, int k,
+                                         typename Key<F32>::type best[KP]) {
+    typedef Key<F32> K;
+    typename K::type last = K::kNone;
+#pragma unroll
+    for (int i = 0; i < KP; i++) best[i] = K::kNone;
+#pragma nounroll
+    for (int s = 0; s < k; s++) {
+        typename K::type most = K::kNone;
+#pragma unroll
+        for (int v = 0; v < 8 * CH; v++) {
+            const typename K::type key = K::make(c[v / 8].at(v % 8), inv ^ (8u * G * (v / 8) + v % 8));
+            if (s == 0 || key < last) most = K::hi(most, key);
+        }
+        last = group_most<F32, G>(most);
+#pragma unroll
+        for (int i = 0; i < KP; i++)
+            if (s == i) best[i] = last;
+    }
 }
 
 template <bool F32, int G, int CH, int KP, bool VEC>
@@ -401,6 +523,7 @@ __global__ __launch_bounds__(256, (CH == 4 ? (F32 ? 2 : 3) : 4)) void k_route(Ro
 #pragma unroll
     for (int v = 0; v < V; v++) acc[v] = 0.0f;
     uint32_t routed = 0;
+    const uint32_t inv = 0xFFFFu ^ (8u * (uint32_t)g);
     const int64_t step = (int64_t)gridDim.x * R;
     int64_t t = (int64_t)blockIdx.x * R + r;
     const auto load = [&](Chunk<F32> *c, int64_t at) {
@@ -414,38 +537,25 @@ __global__ __launch_bounds__(256, (CH == 4 ? (F32 ? 2 : 3) : 4)) void k_route(Ro
 #pragma unroll
         for (int i = 0; i < CH; i++) c[i] = next[i];
         load(next, t + step);
-        float l[V], e[V], m, Z;
-        softmax_row<F32, G, CH>(c, l, e, m, Z);
-        const float inv = Z == 0.0f ? 0.0f : 1.0f / Z;
+        KT best[KP];
+        pick<F32, G, CH, KP>(c, inv, best);
+        float m = K::open(best[0]) ? K::value(best[0]) : 0.0f, e[V], Z;
+        exponentials<F32, G, CH>(c, m, e, Z);
+        bool odd = Z != Z;
+        if (__any(!K::positive(best[KP - 1]))) {
+            asm volatile("; choices down to zero");
+#pragma unroll
+            for (int i = 0; i < KP; i++) odd = odd || K::zero(best[i]);
+        }
+        if (__any(odd)) {
+            uint32_t start = inv;
+            asm volatile("; NaN, or zeros that may tie" : "+v"(start));   // (opaque: no constants of it are kept)
+            pick_any<F32, G, CH, KP>(c, start, a.k, best);
+        }
+        const float by_z = Z == 0.0f ? 0.0f : reciprocal(Z);
         if (g == 0) routed += Z != 0.0f;
 #pragma unroll
-        for (int v = 0; v < V; v++) acc[v] = __builtin_fmaf(e[v], inv, acc[v]);
-
-        // ~index of the lane's first expert; opaque, or its variants of all
-        // elements are kept in registers across the loop, which spills
-        uint32_t inv0 = 0xFFFFu ^ (8u * (uint32_t)g);
-        asm volatile("" : "+v"(inv0));
-        KT key[V < KP ? KP : V];
-#pragma unroll
-        for (int v = 0; v < V; v++) key[v] = K::make(l[v] + 0.0f, inv0 ^ (8u * G * (v / 8)), v % 8);   // -0 is +0
-#pragma unroll
-        for (int v = V; v < KP; v++) key[v] = K::none();
-        if (__any(Z != Z)) {
-            asm volatile("; a row with NaN or +inf" : "+v"(inv0));     // a branch, not selects
-#pragma unroll
-            for (int v = 0; v < V; v++)
-                if (l[v] != l[v]) key[v] = K::nan(inv0 ^ (8u * G * (v / 8) + v % 8));
-        }
-        typedef Best<F32, KP> B;
-        B::sort(key);
-#pragma unroll
-        for (int v = KP; v < V; v += KP) {
-            B::sort(key + v);
-#pragma unroll
-            for (int i = 0; i < KP; i++) key[i] = K::hi(key[i], key[v + KP - 1 - i]);
-            B::settle(key);
-        }
-        B::template across<G>(key);
+        for (int v = 0; v < V; v++) acc[v] = __builtin_fmaf(e[v], by_z, acc[v]);
 
         // lane g writes choices g, g + G, ..
         constexpr int S = (KP + G - 1) / G;
@@ -453,17 +563,17 @@ __global__ __launch_bounds__(256, (CH == 4 ? (F32 ? 2 : 3) : 4)) void k_route(Ro
         int id[S];
 #pragma unroll
         for (int s = 0; s < S; s++) {
-            KT mine = key[s * G];
+            KT mine = best[s * G];
 #pragma unroll
             for (int i = 1; i < G; i++)
-                if (s * G + i < KP && g == i) mine = key[s * G + i < KP ? s * G + i : 0];
+                if (s * G + i < KP && g == i) mine = best[s * G + i < KP ? s * G + i : 0];
             const bool open = s * G + g < a.k && K::open(mine);
             id[s] = open ? K::index(mine) : -1;
             ge[s] = open ? __builtin_amdgcn_exp2f((K::value(mine) - m) * kLog2e) : 0.0f;
             top += ge[s];
         }
-        top = a.renorm ? group_sum<G>(top) : Z;
-        const float by = Z == 0.0f ? 0.0f : 1.0f / (Z != Z ? Z : top);
+        // a choice is the row's largest logit, so that the sum is 1 or more
+        const float by = Z != Z ? Z : Z == 0.0f ? 0.0f : a.renorm ? reciprocal(group_sum<G>(top)) : by_z;
 #pragma unroll
         for (int s = 0; s < S; s++) {
             if (s * G + g < a.k && t < a.tokens) {
@@ -673,9 +783,13 @@ __global__ __launch_bounds__(256) void k_route_backward(RouteBackwardArgs a) {
             gs[s] = row.id[s] >= 0 ? El::up(logits[t * a.stride + row.id[s]]) : -INFINITY;
         }
         load(next, t + step);
-        float l[V], e[V], m, Z;
-        softmax_row<F32, G, CH>(row.c, l, e, m, Z);
-        const float inv = Z == 0.0f ? 0.0f : 1.0f / Z;
+        float m = -INFINITY, e[V], Z;
+#pragma unroll
+        for (int v = 0; v < V; v++) m = fmaxf(m, row.c[v / 8].at(v % 8));
+        m = group_max<G>(m);
+        if (m == -INFINITY) m = 0.0f;
+        exponentials<F32, G, CH>(row.c, m, e, Z);
+        const float inv = Z == 0.0f ? 0.0f : reciprocal(Z);
         float dot = 0.0f;
 #pragma unroll
         for (int v = 0; v < V; v++) {
