@@ -169,8 +169,9 @@ hipError_t dropout_access(const DropoutArgs &a, hipStream_t s) {
 // router
 // ---------------------------------------------------------------------------
 
-// A token's logits lie in G lanes (a power of two), 8 CH of them in each: chunk
-// i of lane g holds experts 8 (i G + g) .. + 7.  A wave takes 64 / G tokens.
+// A token's logits lie in G lanes (a power of two), 8 CH of them in each, in
+// chunks of W that are 16 bytes: chunk i of lane g holds experts W (i G + g) ..
+// + W - 1.  A wave takes 64 / G tokens.
 
 constexpr float kLog2e = 1.44269504088896340736f;
 
@@ -180,10 +181,12 @@ template <bool F32>
 struct Chunk;
 template <>
 struct Chunk<false> {
+    static constexpr int W = 8;
     u32x4 w;
     __device__ __forceinline__ void clear() { w = u32x4{0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u}; }
     __device__ __forceinline__ void load(const uint16_t *p) { w = *reinterpret_cast<const u32x4 *>(p); }
     __device__ __forceinline__ void load(const uint16_t *p, int n) {
+#pragma unroll
         for (int j = 0; j < 4; j++) {
             if (2 * j < n) w[j] = (w[j] & 0xFFFF0000u) | p[2 * j];
             if (2 * j + 1 < n) w[j] = (w[j] & 0xFFFFu) | (uint32_t)p[2 * j + 1] << 16;
@@ -192,50 +195,59 @@ struct Chunk<false> {
     __device__ __forceinline__ float at(int j) const {
         return __uint_as_float(j & 1 ? w[j >> 1] & 0xFFFF0000u : w[j >> 1] << 16);
     }
+    static __device__ __forceinline__ void store(uint16_t *p, const float d[8]) { store8<false>(p, 0, d); }
 };
 template <>
 struct Chunk<true> {
-    float v[8];
-    __device__ __forceinline__ void clear() {
-#pragma unroll
-        for (int j = 0; j < 8; j++) v[j] = -INFINITY;
-    }
+    static constexpr int W = 4;
+    float v[4];
+    __device__ __forceinline__ void clear() { v[0] = v[1] = v[2] = v[3] = -INFINITY; }
     __device__ __forceinline__ void load(const float *p) {
-        const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
+        const float4 a = *reinterpret_cast<const float4 *>(p);
         v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
     }
     __device__ __forceinline__ void load(const float *p, int n) {
 #pragma unroll
-        for (int j = 0; j < 8; j++)
+        for (int j = 0; j < 4; j++)
             if (j < n) v[j] = p[j];
     }
     __device__ __forceinline__ float at(int j) const { return v[j]; }
+    static __device__ __forceinline__ void store(float *p, const float d[4]) {
+        *reinterpret_cast<float4 *>(p) = make_float4(d[0], d[1], d[2], d[3]);
+    }
 };
 
-// VEC: every row 16-byte aligned, E a multiple of 8
-template <bool F32, int G, int CH, bool VEC>
-__device__ __forceinline__ void load_row(Chunk<F32> c[CH], const typename Elem<F32>::type *row, int g, int E,
-                                         bool there) {
+// The logits of a row that one lane holds.  VEC: every row 16-byte aligned, E
+// a multiple of W.
+template <bool F32, int G, int CH>
+struct Slice {
+    static constexpr int W = Chunk<F32>::W, V = 8 * CH, N = V / W;
+    Chunk<F32> c[N];
+    // expert of element v in lane g
+    static __device__ __forceinline__ int expert(int v, int g) { return W * ((v / W) * G + g) + v % W; }
+    __device__ __forceinline__ float at(int v) const { return c[v / W].at(v % W); }
+    template <bool VEC>
+    __device__ __forceinline__ void load(const typename Elem<F32>::type *row, int g, int E, bool there) {
 #pragma unroll
-    for (int i = 0; i < CH; i++) {
-        const int at = 8 * (i * G + g);
-        if (VEC) {
-            if (there && at < E) c[i].load(row + at);
-            else c[i].clear();
-        } else {
-            c[i].clear();
-            if (there) c[i].load(row + at, E - at);
+        for (int i = 0; i < N; i++) {
+            const int at = W * (i * G + g);
+            if (VEC) {
+                if (there && at < E) c[i].load(row + at);
+                else c[i].clear();
+            } else {
+                c[i].clear();
+                if (there) c[i].load(row + at, E - at);
+            }
         }
     }
-}
+};
 
 // Order key of a logit and its expert: keys are distinct, a larger logit has
 // the larger key and of equal ones the lower index.  bf16: the bits in signed
 // order, then 16 bits of ~index.  fp32: the bits in unsigned order and 20 bits of
 // ~index as the mantissa of a double in [1, 2), which has a one-instruction
-// maximum.  make8 is for rows without NaN and ranks -0 below +0; make takes
-// anything (-0 = +0, NaN above +inf).  inv: ~index of the first of 8 experts.
+// maximum.  chunk is for rows without NaN and ranks -0 below +0; make takes
+// anything (-0 = +0, NaN above +inf).  inv: ~index, of a chunk's first expert.
 template <bool F32>
 struct Key;
 template <>
@@ -247,7 +259,7 @@ struct Key<false> {
         const s16x2 sign = __builtin_bit_cast(s16x2, w) >> 15;
         return __builtin_amdgcn_bitop3_b32(__builtin_bit_cast(uint32_t, sign), 0x7FFF7FFFu, w, 0x6A);   // (a & b) ^ c
     }
-    static __device__ __forceinline__ void make8(const Chunk<false> &c, uint32_t inv, int32_t key[8]) {
+    static __device__ __forceinline__ void chunk(const Chunk<false> &c, uint32_t inv, int32_t key[8]) {
 #pragma unroll
         for (int q = 0; q < 4; q++) {
             const uint32_t o = ordered(c.w[q]);
@@ -284,9 +296,9 @@ struct Key<true> {
     static __device__ __forceinline__ uint32_t ordered(uint32_t u) {
         return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
     }
-    static __device__ __forceinline__ void make8(const Chunk<true> &c, uint32_t inv, double key[8]) {
+    static __device__ __forceinline__ void chunk(const Chunk<true> &c, uint32_t inv, double key[4]) {
 #pragma unroll
-        for (int j = 0; j < 8; j++) key[j] = pack(ordered(__float_as_uint(c.v[j])), inv ^ j);
+        for (int j = 0; j < 4; j++) key[j] = pack(ordered(__float_as_uint(c.v[j])), inv ^ j);
     }
     static __device__ __forceinline__ double make(float x, uint32_t inv) {
         x += 0.0f;
@@ -426,42 +438,43 @@ __device__ __forceinline__ float reciprocal(float x) {
 // rounding of m log2 e is the same factor in every e and cancels in e / Z;
 // near the ends of the range m log2 e overflows and the difference comes first.
 template <bool F32, int G, int CH>
-__device__ __forceinline__ void exponentials(const Chunk<F32> c[CH], float m, float e[8 * CH], float &Z) {
+__device__ __forceinline__ void exponentials(const Slice<F32, G, CH> &l, float m, float e[8 * CH], float &Z) {
     float z[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     if (__any(!(fabsf(m) < 1e37f))) {
         asm volatile("; extreme logits");        // a branch, not selects
 #pragma unroll
-        for (int v = 0; v < 8 * CH; v++) e[v] = __builtin_amdgcn_exp2f((c[v / 8].at(v % 8) - m) * kLog2e);
+        for (int v = 0; v < 8 * CH; v++) e[v] = __builtin_amdgcn_exp2f((l.at(v) - m) * kLog2e);
     } else {
         const float by = -m * kLog2e;
 #pragma unroll
         for (int v = 0; v < 8 * CH; v++)
-            e[v] = __builtin_amdgcn_exp2f(__builtin_fmaf(c[v / 8].at(v % 8), kLog2e, by));
+            e[v] = __builtin_amdgcn_exp2f(__builtin_fmaf(l.at(v), kLog2e, by));
     }
 #pragma unroll
     for (int v = 0; v < 8 * CH; v++) z[v % 4] += e[v];
     Z = group_sum<G>((z[0] + z[1]) + (z[2] + z[3]));
 }
 
-// The falling list of a row's KP largest keys, in all of its lanes
+// The falling list of a row's KP largest keys, in all of its lanes.  inv: ~index
+// of the lane's first expert
 template <bool F32, int G, int CH, int KP>
-__device__ __forceinline__ void pick(const Chunk<F32> c[CH], uint32_t inv, typename Key<F32>::type best[KP]) {
+__device__ __forceinline__ void pick(const Slice<F32, G, CH> &l, uint32_t inv, typename Key<F32>::type best[KP]) {
     typedef Key<F32> K;
     typedef Best<F32, KP> B;
-    constexpr int U = KP < 8 ? 8 : KP, N = U / 8;     // elements and chunks that are sorted together
+    constexpr int W = Slice<F32, G, CH>::W, U = KP < 8 ? 8 : KP, N = U / W;   // elements and chunks sorted together
 #pragma unroll
-    for (int i = 0; i < CH; i += N) {
+    for (int i = 0; i < Slice<F32, G, CH>::N; i += N) {
         typename K::type key[U];
 #pragma unroll
         for (int n = 0; n < N; n++) {
-            if (i + n < CH) {
-                K::make8(c[i + n], inv, key + 8 * n);
+            if (i + n < Slice<F32, G, CH>::N) {
+                K::chunk(l.c[i + n], inv, key + W * n);
                 if (n > 0)
 #pragma unroll
-                    for (int j = 0; j < 8; j++) key[8 * n + j] = K::flip(key[8 * n + j], 8u * G * n);
+                    for (int j = 0; j < W; j++) key[W * n + j] = K::flip(key[W * n + j], W * G * n);
             } else {
 #pragma unroll
-                for (int j = 0; j < 8; j++) key[8 * n + j] = K::kNone;
+                for (int j = 0; j < W; j++) key[W * n + j] = K::kNone;
             }
         }
         B::sort(key);
@@ -476,7 +489,7 @@ __device__ __forceinline__ void pick(const Chunk<F32> c[CH], uint32_t inv, typen
         } else {
             // chunk i's indices
 #pragma unroll
-            for (int j = 0; j < KP; j++) key[j] = K::flip(key[j], 8u * G * i);
+            for (int j = 0; j < KP; j++) key[j] = K::flip(key[j], W * G * i);
             B::merge(best, key);
         }
     }
@@ -486,7 +499,7 @@ __device__ __forceinline__ void pick(const Chunk<F32> c[CH], uint32_t inv, typen
 // The same list one key at a time, for rows with NaN or with zeros of both
 // signs among the choices
 template <bool F32, int G, int CH, int KP>
-__device__ __forceinline__ void pick_any(const Chunk<F32> c[CH], uint32_t inv, int k,
+__device__ __forceinline__ void pick_any(const Slice<F32, G, CH> &l, uint32_t inv, int k,
                                          typename Key<F32>::type best[KP]) {
     typedef Key<F32> K;
     typename K::type last = K::kNone;
@@ -497,7 +510,7 @@ __device__ __forceinline__ void pick_any(const Chunk<F32> c[CH], uint32_t inv, i
         typename K::type most = K::kNone;
 #pragma unroll
         for (int v = 0; v < 8 * CH; v++) {
-            const typename K::type key = K::make(c[v / 8].at(v % 8), inv ^ (8u * G * (v / 8) + v % 8));
+            const typename K::type key = K::make(l.at(v), inv ^ Slice<F32, G, CH>::expert(v, 0));
             if (s == 0 || key < last) most = K::hi(most, key);
         }
         last = group_most<F32, G>(most);
@@ -508,11 +521,12 @@ __device__ __forceinline__ void pick_any(const Chunk<F32> c[CH], uint32_t inv, i
 }
 
 template <bool F32, int G, int CH, int KP, bool VEC>
-__global__ __launch_bounds__(256, (CH == 4 ? (F32 ? 2 : 3) : 4)) void k_route(RouteArgs a) {
+__global__ __launch_bounds__(256, KP == 16 ? 3 : 4) void k_route(RouteArgs a) {
     typedef typename Elem<F32>::type T;
     typedef Key<F32> K;
     typedef typename K::type KT;
-    constexpr int V = 8 * CH, C = V * G, R = 256 / G;     // per lane; columns; tokens of a block's pass
+    typedef Slice<F32, G, CH> L;
+    constexpr int V = L::V, C = V * G, R = 256 / G;       // per lane; columns; tokens of a block's pass
     __shared__ uint32_t hist[C];
     __shared__ float sums[R * C];
     __shared__ uint32_t routed_of[4];
@@ -523,24 +537,17 @@ __global__ __launch_bounds__(256, (CH == 4 ? (F32 ? 2 : 3) : 4)) void k_route(Ro
 #pragma unroll
     for (int v = 0; v < V; v++) acc[v] = 0.0f;
     uint32_t routed = 0;
-    const uint32_t inv = 0xFFFFu ^ (8u * (uint32_t)g);
+    const uint32_t inv = 0xFFFFu ^ (uint32_t)L::expert(0, g);
     const int64_t step = (int64_t)gridDim.x * R;
     int64_t t = (int64_t)blockIdx.x * R + r;
-    const auto load = [&](Chunk<F32> *c, int64_t at) {
-        const bool there = at < a.tokens && (!a.mask || a.mask[at]);
-        load_row<F32, G, CH, VEC>(c, static_cast<const T *>(a.logits) + at * a.stride, g, a.E, there);
-    };
-    Chunk<F32> next[CH];
-    load(next, t);
     for (int64_t base = (int64_t)blockIdx.x * R; base < a.tokens; base += step, t += step) {
-        Chunk<F32> c[CH];
-#pragma unroll
-        for (int i = 0; i < CH; i++) c[i] = next[i];
-        load(next, t + step);
+        L l;
+        const bool there = t < a.tokens && (!a.mask || a.mask[t]);
+        l.template load<VEC>(static_cast<const T *>(a.logits) + t * a.stride, g, a.E, there);
         KT best[KP];
-        pick<F32, G, CH, KP>(c, inv, best);
+        pick<F32, G, CH, KP>(l, inv, best);
         float m = K::open(best[0]) ? K::value(best[0]) : 0.0f, e[V], Z;
-        exponentials<F32, G, CH>(c, m, e, Z);
+        exponentials<F32, G, CH>(l, m, e, Z);
         bool odd = Z != Z;
         if (__any(!K::positive(best[KP - 1]))) {
             asm volatile("; choices down to zero");
@@ -550,7 +557,7 @@ __global__ __launch_bounds__(256, (CH == 4 ? (F32 ? 2 : 3) : 4)) void k_route(Ro
         if (__any(odd)) {
             uint32_t start = inv;
             asm volatile("; NaN, or zeros that may tie" : "+v"(start));   // (opaque: no constants of it are kept)
-            pick_any<F32, G, CH, KP>(c, start, a.k, best);
+            pick_any<F32, G, CH, KP>(l, start, a.k, best);
         }
         const float by_z = Z == 0.0f ? 0.0f : reciprocal(Z);
         if (g == 0) routed += Z != 0.0f;
@@ -585,7 +592,7 @@ __global__ __launch_bounds__(256, (CH == 4 ? (F32 ? 2 : 3) : 4)) void k_route(Ro
     }
     // the block's sums: token rows side by side in LDS, then over the rows
 #pragma unroll
-    for (int v = 0; v < V; v++) sums[r * C + 8 * ((v / 8) * G + g) + v % 8] = acc[v];
+    for (int v = 0; v < V; v++) sums[r * C + L::expert(v, g)] = acc[v];
     for (int d = 32; d; d >>= 1) routed += __shfl_xor((int)routed, d, 64);
     if ((threadIdx.x & 63) == 0) routed_of[threadIdx.x >> 6] = routed;
     __syncthreads();
@@ -738,28 +745,21 @@ template <bool F32, int G, int CH, int S, bool VEC>
 __global__ __launch_bounds__(256) void k_route_backward(RouteBackwardArgs a) {
     typedef Elem<F32> El;
     typedef typename El::type T;
-    constexpr int V = 8 * CH, C = V * G, R = 256 / G;
+    typedef Slice<F32, G, CH> L;
+    constexpr int V = L::V, W = L::W, C = V * G, R = 256 / G;
     __shared__ alignas(16) float rows[R * C];
     const int g = threadIdx.x % G, r = threadIdx.x / G;
     float *h = rows + r * C;
     const T *logits = static_cast<const T *>(a.logits);
-    const float w = a.dloss ? *a.dloss : 1.0f;
-    float up[V];
-#pragma unroll
-    for (int v = 0; v < V; v++) {
-        const int j = 8 * ((v / 8) * G + g) + v % 8;
-        up[v] = a.coef && j < a.E ? w * a.coef[j] : 0.0f;
-        h[j] = 0.0f;
-    }
     struct Row {
-        Chunk<F32> c[CH];
+        L l;
         int id[S];
         float dg[S];
     };
     // lane g holds choices g, g + G, ..
     const auto load = [&](Row &row, int64_t t) {
         const bool there = t < a.tokens && (!a.mask || a.mask[t]);
-        load_row<F32, G, CH, VEC>(row.c, logits + t * a.stride, g, a.E, there);
+        row.l.template load<VEC>(logits + t * a.stride, g, a.E, there);
 #pragma unroll
         for (int s = 0; s < S; s++) {
             row.id[s] = -1;
@@ -774,6 +774,21 @@ __global__ __launch_bounds__(256) void k_route_backward(RouteBackwardArgs a) {
     int64_t t = (int64_t)blockIdx.x * R + r;
     Row next;
     load(next, t);
+    // dloss coef of the lane's experts; loads of all of them in flight at once
+    float up[V];
+    if (a.coef) {
+        const float w = a.dloss ? *a.dloss : 1.0f;
+#pragma unroll
+        for (int v = 0; v < V; v++) up[v] = a.coef[min(L::expert(v, g), a.E - 1)];
+#pragma unroll
+        for (int v = 0; v < V; v++) up[v] *= w;
+    } else {
+#pragma unroll
+        for (int v = 0; v < V; v++) up[v] = 0.0f;
+    }
+    for (int j = 4 * g; j < C; j += 4 * G)
+        *reinterpret_cast<float4 *>(__builtin_assume_aligned(h + j, 16)) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    wave_lds_sync();
     for (int64_t base = (int64_t)blockIdx.x * R; base < a.tokens; base += step, t += step) {
         Row row = next;
         float gs[S];
@@ -785,10 +800,10 @@ __global__ __launch_bounds__(256) void k_route_backward(RouteBackwardArgs a) {
         load(next, t + step);
         float m = -INFINITY, e[V], Z;
 #pragma unroll
-        for (int v = 0; v < V; v++) m = fmaxf(m, row.c[v / 8].at(v % 8));
+        for (int v = 0; v < V; v++) m = fmaxf(m, row.l.at(v));
         m = group_max<G>(m);
         if (m == -INFINITY) m = 0.0f;
-        exponentials<F32, G, CH>(row.c, m, e, Z);
+        exponentials<F32, G, CH>(row.l, m, e, Z);
         const float inv = Z == 0.0f ? 0.0f : reciprocal(Z);
         float dot = 0.0f;
 #pragma unroll
@@ -821,17 +836,17 @@ __global__ __launch_bounds__(256) void k_route_backward(RouteBackwardArgs a) {
         if (t < a.tokens) {
             T *out = static_cast<T *>(a.dlogits) + t * a.dstride;
 #pragma unroll
-            for (int i = 0; i < CH; i++) {
-                const int at = 8 * (i * G + g);
-                float d[8];
+            for (int i = 0; i < L::N; i++) {
+                const int at = L::expert(W * i, g);
+                float d[W];
                 __builtin_memcpy(d, __builtin_assume_aligned(h + at, 16), sizeof d);
 #pragma unroll
-                for (int j = 0; j < 8; j++) d[j] = __builtin_fmaf(e[8 * i + j], up[8 * i + j] - dot, d[j]);
+                for (int j = 0; j < W; j++) d[j] = __builtin_fmaf(e[W * i + j], up[W * i + j] - dot, d[j]);
                 if (VEC) {
-                    if (at < a.E) store8<F32>(out, at, d);
+                    if (at < a.E) Chunk<F32>::store(out + at, d);
                 } else {
 #pragma unroll
-                    for (int j = 0; j < 8; j++)
+                    for (int j = 0; j < W; j++)
                         if (at + j < a.E) out[at + j] = El::down(d[j]);
                 }
             }
@@ -853,26 +868,42 @@ hipError_t route_choices(const RouteArgs &a, hipStream_t s) {
     return hipGetLastError();
 }
 
-// lanes and chunks of a token of E experts
+// Lanes and chunks of a token of E experts: f(G, CH)
+template <int G, int CH, class F>
+auto shape(F f) {
+    return f(std::integral_constant<int, G>(), std::integral_constant<int, CH>());
+}
 template <class F>
 auto by_experts(int E, F f) {
-    if (E <= 8) return f(std::integral_constant<int, 1>(), std::integral_constant<int, 1>());
-    if (E <= 16) return f(std::integral_constant<int, 2>(), std::integral_constant<int, 1>());
-    if (E <= 32) return f(std::integral_constant<int, 4>(), std::integral_constant<int, 1>());
-    if (E <= 64) return f(std::integral_constant<int, 8>(), std::integral_constant<int, 1>());
-    if (E <= 128) return f(std::integral_constant<int, 8>(), std::integral_constant<int, 2>());
-    if (E <= 256) return f(std::integral_constant<int, 8>(), std::integral_constant<int, 4>());
-    if (E <= 512) return f(std::integral_constant<int, 16>(), std::integral_constant<int, 4>());
-    return f(std::integral_constant<int, 32>(), std::integral_constant<int, 4>());
+    if (E <= 8) return shape<1, 1>(f);
+    if (E <= 16) return shape<2, 1>(f);
+    if (E <= 32) return shape<4, 1>(f);
+    if (E <= 64) return shape<8, 1>(f);
+    if (E <= 128) return shape<8, 2>(f);
+    if (E <= 256) return shape<16, 2>(f);
+    if (E <= 512) return shape<32, 2>(f);
+    return shape<64, 2>(f);
+}
+constexpr int64_t kManyTokens = 32768;
+// The same with longer lists in fewer lanes, for E > 128: fewer steps across
+// lanes per token, but half as many waves
+template <class F>
+auto by_experts_long(int E, F f) {
+    if (E <= 256) return shape<8, 4>(f);
+    if (E <= 512) return shape<16, 4>(f);
+    return shape<32, 4>(f);
 }
 
 bool rows_on_16(const void *p, int64_t stride, int E, bool f32) {
-    return E % 8 == 0 && reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride * (f32 ? 4 : 2) % 16 == 0;
+    return E % (f32 ? 4 : 8) == 0 && reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride * (f32 ? 4 : 2) % 16 == 0;
 }
 
 template <bool F32>
 hipError_t route_experts(const RouteArgs &a, hipStream_t s) {
     const bool vec = rows_on_16(a.logits, a.stride, a.E, F32);
+    if constexpr (!F32)
+        if (vec && a.E > 128 && a.tokens >= kManyTokens)
+            return by_experts_long(a.E, [&](auto G, auto CH) { return route_choices<F32, G.value, CH.value, true>(a, s); });
     return by_experts(a.E, [&](auto G, auto CH) {
         return vec ? route_choices<F32, G.value, CH.value, true>(a, s)
                    : route_choices<F32, G.value, CH.value, false>(a, s);
@@ -913,9 +944,9 @@ hipError_t launch_dropout(const DropoutArgs &a, int f32, hipStream_t s) {
 }
 
 int route_blocks(int64_t tokens, int E) {
-    // what the chip holds at once: 8, 4 or 3 blocks per CU by the lanes' registers
+    // at most what the chip holds at once
     const int64_t rows = by_experts(E, [](auto G, auto) { return 256 / G.value; });
-    const int64_t most = by_experts(E, [](auto, auto CH) { return 256 * (CH.value == 1 ? 6 : CH.value == 2 ? 4 : 3); });
+    const int64_t most = by_experts(E, [](auto, auto CH) { return 256 * (CH.value == 1 ? 6 : 4); });
     const int64_t want = (tokens + rows - 1) / rows;
     return (int)(want < 1 ? 1 : want < most ? want : most);
 }
