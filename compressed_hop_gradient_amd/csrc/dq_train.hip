@@ -185,16 +185,17 @@ struct Chunk<false> {
     u32x4 w;
     __device__ __forceinline__ void clear() { w = u32x4{0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u}; }
     __device__ __forceinline__ void load(const uint16_t *p) { w = *reinterpret_cast<const u32x4 *>(p); }
-    __device__ __forceinline__ void load(const uint16_t *p, int n) {
+    __device__ __forceinline__ void load(const uint16_t *row, int at, int E) {
 #pragma unroll
         for (int j = 0; j < 4; j++) {
-            if (2 * j < n) w[j] = (w[j] & 0xFFFF0000u) | p[2 * j];
-            if (2 * j + 1 < n) w[j] = (w[j] & 0xFFFFu) | (uint32_t)p[2 * j + 1] << 16;
+            const uint32_t a = row[min(at + 2 * j, E - 1)], b = row[min(at + 2 * j + 1, E - 1)];
+            w[j] = (at + 2 * j < E ? a : 0xFF80u) | (at + 2 * j + 1 < E ? b : 0xFF80u) << 16;
         }
     }
     __device__ __forceinline__ float at(int j) const {
         return __uint_as_float(j & 1 ? w[j >> 1] & 0xFFFF0000u : w[j >> 1] << 16);
     }
+    __device__ __forceinline__ void arrived() { asm volatile("" : "+v"(w)); }
     static __device__ __forceinline__ void store(uint16_t *p, const float d[8]) { store8<false>(p, 0, d); }
 };
 template <>
@@ -206,12 +207,15 @@ struct Chunk<true> {
         const float4 a = *reinterpret_cast<const float4 *>(p);
         v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
     }
-    __device__ __forceinline__ void load(const float *p, int n) {
+    __device__ __forceinline__ void load(const float *row, int at, int E) {
 #pragma unroll
-        for (int j = 0; j < 4; j++)
-            if (j < n) v[j] = p[j];
+        for (int j = 0; j < 4; j++) {
+            const float x = row[min(at + j, E - 1)];
+            v[j] = at + j < E ? x : -INFINITY;
+        }
     }
     __device__ __forceinline__ float at(int j) const { return v[j]; }
+    __device__ __forceinline__ void arrived() { asm volatile("" : "+v"(v[0]), "+v"(v[1]), "+v"(v[2]), "+v"(v[3])); }
     static __device__ __forceinline__ void store(float *p, const float d[4]) {
         *reinterpret_cast<float4 *>(p) = make_float4(d[0], d[1], d[2], d[3]);
     }
@@ -226,19 +230,25 @@ struct Slice {
     // expert of element v in lane g
     static __device__ __forceinline__ int expert(int v, int g) { return W * ((v / W) * G + g) + v % W; }
     __device__ __forceinline__ float at(int v) const { return c[v / W].at(v % W); }
+    // Loads that nothing waits for: no branch, every address inside the row;
+    // keep() then leaves -inf where no logit belongs.
     template <bool VEC>
-    __device__ __forceinline__ void load(const typename Elem<F32>::type *row, int g, int E, bool there) {
+    __device__ __forceinline__ void load(const typename Elem<F32>::type *row, int g, int E) {
 #pragma unroll
         for (int i = 0; i < N; i++) {
             const int at = W * (i * G + g);
-            if (VEC) {
-                if (there && at < E) c[i].load(row + at);
-                else c[i].clear();
-            } else {
-                c[i].clear();
-                if (there) c[i].load(row + at, E - at);
-            }
+            if (VEC) c[i].load(row + (at < E ? at : 0));
+            else c[i].load(row, at, E);
         }
+    }
+    __device__ __forceinline__ void arrived() {
+#pragma unroll
+        for (int i = 0; i < N; i++) c[i].arrived();
+    }
+    __device__ __forceinline__ void keep(bool there, int g, int E) {
+#pragma unroll
+        for (int i = 0; i < N; i++)
+            if (!there || W * (i * G + g) >= E) c[i].clear();
     }
 };
 
@@ -521,7 +531,7 @@ __device__ __forceinline__ void pick_any(const Slice<F32, G, CH> &l, uint32_t in
 }
 
 template <bool F32, int G, int CH, int KP, bool VEC>
-__global__ __launch_bounds__(256, KP == 16 ? 3 : 4) void k_route(RouteArgs a) {
+__global__ __launch_bounds__(256, KP == 16 || CH == 4 || !VEC ? 3 : 4) void k_route(RouteArgs a) {
     typedef typename Elem<F32>::type T;
     typedef Key<F32> K;
     typedef typename K::type KT;
@@ -542,8 +552,9 @@ __global__ __launch_bounds__(256, KP == 16 ? 3 : 4) void k_route(RouteArgs a) {
     int64_t t = (int64_t)blockIdx.x * R + r;
     for (int64_t base = (int64_t)blockIdx.x * R; base < a.tokens; base += step, t += step) {
         L l;
-        const bool there = t < a.tokens && (!a.mask || a.mask[t]);
-        l.template load<VEC>(static_cast<const T *>(a.logits) + t * a.stride, g, a.E, there);
+        const int64_t at = t < a.tokens ? t : 0;
+        l.template load<VEC>(static_cast<const T *>(a.logits) + at * a.stride, g, a.E);
+        l.keep(t < a.tokens && (!a.mask || a.mask[at]), g, a.E);
         KT best[KP];
         pick<F32, G, CH, KP>(l, inv, best);
         float m = K::open(best[0]) ? K::value(best[0]) : 0.0f, e[V], Z;
@@ -755,18 +766,22 @@ __global__ __launch_bounds__(256) void k_route_backward(RouteBackwardArgs a) {
         L l;
         int id[S];
         float dg[S];
+        uint8_t mask;
     };
-    // lane g holds choices g, g + G, ..
+    // lane g holds choices g, g + G, ..; nothing waits for these loads
     const auto load = [&](Row &row, int64_t t) {
-        const bool there = t < a.tokens && (!a.mask || a.mask[t]);
-        row.l.template load<VEC>(logits + t * a.stride, g, a.E, there);
+        if (t >= a.tokens) t = 0;
+        row.l.template load<VEC>(logits + t * a.stride, g, a.E);
+        row.mask = 1;
+        if (a.mask) row.mask = a.mask[t];
 #pragma unroll
         for (int s = 0; s < S; s++) {
+            const int64_t at = t * a.k + (s * G + g < a.k ? s * G + g : 0);
             row.id[s] = -1;
             row.dg[s] = 0.0f;
-            if (there && a.dgates && s * G + g < a.k) {
-                row.id[s] = a.ids[t * a.k + s * G + g];
-                row.dg[s] = a.dgates[t * a.k + s * G + g];
+            if (a.dgates) {
+                row.id[s] = a.ids[at];
+                row.dg[s] = a.dgates[at];
             }
         }
     };
@@ -776,28 +791,41 @@ __global__ __launch_bounds__(256) void k_route_backward(RouteBackwardArgs a) {
     load(next, t);
     // dloss coef of the lane's experts; loads of all of them in flight at once
     float up[V];
-    if (a.coef) {
-        const float w = a.dloss ? *a.dloss : 1.0f;
+    const float w = a.coef ? (a.dloss ? *a.dloss : 1.0f) : 0.0f;
+    if (VEC && a.coef && reinterpret_cast<uintptr_t>(a.coef) % 16 == 0) {
+#pragma unroll
+        for (int v = 0; v < V; v += 4) {
+            const int at = L::expert(v, g);
+            const float4 x = *reinterpret_cast<const float4 *>(a.coef + (at < a.E ? at : 0));
+            up[v] = x.x;
+            up[v + 1] = x.y;
+            up[v + 2] = x.z;
+            up[v + 3] = x.w;
+        }
+    } else if (a.coef) {
 #pragma unroll
         for (int v = 0; v < V; v++) up[v] = a.coef[min(L::expert(v, g), a.E - 1)];
-#pragma unroll
-        for (int v = 0; v < V; v++) up[v] *= w;
     } else {
 #pragma unroll
         for (int v = 0; v < V; v++) up[v] = 0.0f;
     }
-    for (int j = 4 * g; j < C; j += 4 * G)
-        *reinterpret_cast<float4 *>(__builtin_assume_aligned(h + j, 16)) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+    for (int v = 0; v < V; v++) up[v] *= w;
+#pragma unroll
+    for (int v = 0; v < V; v += 4)
+        *reinterpret_cast<float4 *>(__builtin_assume_aligned(h + 4 * g + v * G, 16)) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     wave_lds_sync();
     for (int64_t base = (int64_t)blockIdx.x * R; base < a.tokens; base += step, t += step) {
         Row row = next;
-        float gs[S];
+        const bool there = t < a.tokens && row.mask;
+        typename El::type ls[S];
 #pragma unroll
         for (int s = 0; s < S; s++) {
-            if ((uint32_t)row.id[s] >= (uint32_t)a.E) row.id[s] = -1;
-            gs[s] = row.id[s] >= 0 ? El::up(logits[t * a.stride + row.id[s]]) : -INFINITY;
+            if (!there || s * G + g >= a.k || (uint32_t)row.id[s] >= (uint32_t)a.E) row.id[s] = -1;
+            ls[s] = logits[(there ? t : 0) * a.stride + (row.id[s] < 0 ? 0 : row.id[s])];
         }
         load(next, t + step);
+        row.l.keep(there, g, a.E);
         float m = -INFINITY, e[V], Z;
 #pragma unroll
         for (int v = 0; v < V; v++) m = fmaxf(m, row.l.at(v));
@@ -805,16 +833,13 @@ __global__ __launch_bounds__(256) void k_route_backward(RouteBackwardArgs a) {
         if (m == -INFINITY) m = 0.0f;
         exponentials<F32, G, CH>(row.l, m, e, Z);
         const float inv = Z == 0.0f ? 0.0f : reciprocal(Z);
-        float dot = 0.0f;
+        float dots[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int v = 0; v < V; v++) {
-            e[v] *= inv;
-            dot = __builtin_fmaf(e[v], up[v], dot);
-        }
-        float top = 0.0f, gd = 0.0f;
+        for (int v = 0; v < V; v++) dots[v % 4] = __builtin_fmaf(e[v], up[v], dots[v % 4]);
+        float gs[S], top = 0.0f, gd = 0.0f;
 #pragma unroll
         for (int s = 0; s < S; s++) {
-            gs[s] = row.id[s] >= 0 ? __builtin_amdgcn_exp2f((gs[s] - m) * kLog2e) : 0.0f;
+            gs[s] = row.id[s] >= 0 ? __builtin_amdgcn_exp2f((El::up(ls[s]) - m) * kLog2e) : 0.0f;
             top += gs[s];
         }
         float by = inv;
@@ -828,11 +853,18 @@ __global__ __launch_bounds__(256) void k_route_backward(RouteBackwardArgs a) {
             if (row.id[s] >= 0) gd = __builtin_fmaf(gs[s], row.dg[s], gd);
         }
         gd = group_sum<G>(gd);
-        dot = group_sum<G>(dot) + (a.renorm ? 0.0f : gd);
+        // p (a - D) = e (a / Z - D / Z)
+        float dot = inv * group_sum<G>((dots[0] + dots[1]) + (dots[2] + dots[3]));
+        dot = -inv * (dot + (a.renorm ? 0.0f : gd));
 #pragma unroll
         for (int s = 0; s < S; s++)
             if (row.id[s] >= 0) h[row.id[s]] = gs[s] * (a.renorm ? row.dg[s] - gd : row.dg[s]);
         wave_lds_sync();
+        // the next row is waited for here: after the stores below it would be
+        // waited for together with them
+        next.l.arrived();
+#pragma unroll
+        for (int s = 0; s < S; s++) asm volatile("" : "+v"(next.id[s]), "+v"(next.dg[s]));
         if (t < a.tokens) {
             T *out = static_cast<T *>(a.dlogits) + t * a.dstride;
 #pragma unroll
@@ -841,7 +873,8 @@ __global__ __launch_bounds__(256) void k_route_backward(RouteBackwardArgs a) {
                 float d[W];
                 __builtin_memcpy(d, __builtin_assume_aligned(h + at, 16), sizeof d);
 #pragma unroll
-                for (int j = 0; j < W; j++) d[j] = __builtin_fmaf(e[W * i + j], up[W * i + j] - dot, d[j]);
+                for (int j = 0; j < W; j++)
+                    d[j] = __builtin_fmaf(e[W * i + j], __builtin_fmaf(up[W * i + j], inv, dot), d[j]);
                 if (VEC) {
                     if (at < a.E) Chunk<F32>::store(out + at, d);
                 } else {
