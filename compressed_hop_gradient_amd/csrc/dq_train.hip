@@ -286,14 +286,11 @@ struct Key<false> {
     static __device__ __forceinline__ int32_t lo(int32_t a, int32_t b) { return min(a, b); }
     static __device__ __forceinline__ int32_t flip(int32_t k, uint32_t x) { return (int32_t)((uint32_t)k ^ x); }
     static __device__ __forceinline__ bool open(int32_t k) { return k >= (int32_t)0x80800000u; }   // above -inf
-    static __device__ __forceinline__ bool positive(int32_t k) { return k >= 0x00010000; }
     static __device__ __forceinline__ bool zero(int32_t k) { return (uint32_t)(k + 0x10000) < 0x20000u; }
     static __device__ __forceinline__ int index(int32_t k) { return (int)(~(uint32_t)k & 0xFFFFu); }
     static __device__ __forceinline__ float value(int32_t k) {
         return __uint_as_float(ordered((uint32_t)k) & 0xFFFF0000u);
     }
-    template <class F>
-    static __device__ __forceinline__ int32_t moved(int32_t k, F f) { return (int32_t)f((uint32_t)k); }
 };
 template <>
 struct Key<true> {
@@ -333,7 +330,6 @@ struct Key<true> {
         return (uint32_t)(__builtin_bit_cast(uint64_t, k) >> 20);
     }
     static __device__ __forceinline__ bool open(double k) { return order(k) > 0x007FFFFFu; }       // above -inf
-    static __device__ __forceinline__ bool positive(double k) { return order(k) > 0x80000000u; }
     static __device__ __forceinline__ bool zero(double k) { return order(k) - 0x7FFFFFFFu < 2u; }
     static __device__ __forceinline__ int index(double k) {
         return (int)(~(uint32_t)__builtin_bit_cast(uint64_t, k) & 0xFFFFu);
@@ -342,47 +338,63 @@ struct Key<true> {
         const uint32_t o = order(k);
         return __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o);
     }
-    template <class F>
-    static __device__ __forceinline__ double moved(double k, F f) {
-        const uint64_t b = __builtin_bit_cast(uint64_t, k);
-        return __builtin_bit_cast(double, (uint64_t)f((uint32_t)(b >> 32)) << 32 | f((uint32_t)b));
-    }
 };
 
-// The value of the lane that holds the other half of a group of 2 D lanes:
-// lane ^ D for D = 1, 2 and beyond 8, the mirrored lane of the half row and row
-// for 4 and 8 (the same half; values are equal within a half here).
-template <int D>
-__device__ __forceinline__ uint32_t other_half(uint32_t x) {
-    if (D == 1) return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0xB1, 0xF, 0xF, false);
-    if (D == 2) return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x4E, 0xF, 0xF, false);
-    if (D == 4) return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x141, 0xF, 0xF, false);
-    if (D == 8) return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x140, 0xF, 0xF, false);
-    return (uint32_t)__shfl_xor((int)x, D, 64);
+// op(x, the value of the other half of a group of 2 D lanes), the same in both
+// halves: lane ^ 1 and ^ 2, the mirrored lane of the half row and of the row (where
+// a half's lanes hold one value), then rows and halves of the wave swapped.
+template <int D, class Op>
+__device__ __forceinline__ uint32_t with_other_half(uint32_t x, Op op) {
+    if constexpr (D <= 8) {
+        constexpr int kControl = D == 1 ? 0xB1 : D == 2 ? 0x4E : D == 4 ? 0x141 : 0x140;
+        return op(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, kControl, 0xF, 0xF, false));
+    } else {
+        const auto both = D == 16 ? __builtin_amdgcn_permlane16_swap(x, x, false, false)
+                                  : __builtin_amdgcn_permlane32_swap(x, x, false, false);
+        return op(both[0], both[1]);
+    }
 }
-template <int D>
-__device__ __forceinline__ float other_half(float x) {
-    return __uint_as_float(other_half<D>(__float_as_uint(x)));
-}
-
 template <int G, int D = 1>
 __device__ __forceinline__ float group_max(float x) {
-    if constexpr (D < G) return group_max<G, 2 * D>(fmaxf(x, other_half<D>(x)));
+    if constexpr (D < G)
+        return group_max<G, 2 * D>(__uint_as_float(with_other_half<D>(__float_as_uint(x), [](uint32_t a, uint32_t b) {
+            return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+        })));
     return x;
 }
 template <int G, int D = 1>
 __device__ __forceinline__ float group_sum(float x) {
-    if constexpr (D < G) return group_sum<G, 2 * D>(x + other_half<D>(x));
+    if constexpr (D < G)
+        return group_sum<G, 2 * D>(__uint_as_float(with_other_half<D>(__float_as_uint(x), [](uint32_t a, uint32_t b) {
+            return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+        })));
     return x;
 }
-
-template <bool F32, int G, int D = 1>
-__device__ __forceinline__ typename Key<F32>::type group_most(typename Key<F32>::type k) {
+template <int G, int D = 1>
+__device__ __forceinline__ int32_t group_most(int32_t x) {
+    if constexpr (D < G)
+        return group_most<G, 2 * D>((int32_t)with_other_half<D>(
+            (uint32_t)x, [](uint32_t a, uint32_t b) { return (uint32_t)max((int32_t)a, (int32_t)b); }));
+    return x;
+}
+// of both words of a double, then the larger
+template <int G, int D = 1>
+__device__ __forceinline__ double group_most(double x) {
     if constexpr (D < G) {
-        const auto other = Key<F32>::moved(k, [](uint32_t x) { return other_half<D>(x); });
-        return group_most<F32, G, 2 * D>(Key<F32>::hi(k, other));
+        const uint64_t b = __builtin_bit_cast(uint64_t, x);
+        uint32_t own[2] = {(uint32_t)b, (uint32_t)(b >> 32)}, other[2];
+#pragma unroll
+        for (int i = 0; i < 2; i++)
+            with_other_half<D>(own[i], [&](uint32_t p, uint32_t q) {
+                own[i] = p;
+                other[i] = q;
+                return p;
+            });
+        return group_most<G, 2 * D>(
+            Key<true>::hi(__builtin_bit_cast(double, (uint64_t)own[1] << 32 | own[0]),
+                          __builtin_bit_cast(double, (uint64_t)other[1] << 32 | other[0])));
     }
-    return k;
+    return x;
 }
 
 // Falling lists of the KP largest keys.  Sorting: Batcher's odd-even merge
@@ -421,19 +433,6 @@ struct Best {
         for (int i = 0; i < KP; i++) v[i] = K::hi(v[i], w[KP - 1 - i]);
         settle(v);
     }
-    template <int G, int D = 1>
-    static __device__ __forceinline__ void across(T *v) {
-        if constexpr (D < G) {
-            T o[KP];
-#pragma unroll
-            for (int i = 0; i < KP; i++)
-                o[i] = K::hi(v[i], K::moved(v[KP - 1 - i], [](uint32_t x) { return other_half<D>(x); }));
-#pragma unroll
-            for (int i = 0; i < KP; i++) v[i] = o[i];
-            settle(v);
-            across<G, 2 * D>(v);
-        }
-    }
 };
 
 // 1 / x to an ulp for 1 <= x < 2^126; NaN stays NaN
@@ -442,34 +441,44 @@ __device__ __forceinline__ float reciprocal(float x) {
     return __builtin_fmaf(__builtin_fmaf(-x, r, 1.0f), r, r);
 }
 
-// e = exp(l - m) of a row whose largest logit is m, and Z = sum e.  Z = 0 only
-// where every logit is -inf (m is 0 there); NaN or +inf makes Z NaN, and with
-// it all that is divided by it.  The exponent (l - m) log2 e takes one fma, whose
-// rounding of m log2 e is the same factor in every e and cancels in e / Z;
-// near the ends of the range m log2 e overflows and the difference comes first.
+// exp(l - m) where m is the row's largest logit, or 0.  The exponent takes one
+// fma, whose rounding of m log2 e is the same factor for all of the row and
+// cancels in quotients; near the ends of the range m log2 e overflows, and the
+// difference comes first.
+constexpr float kNearTheEnds = 1e37f;
+__device__ __forceinline__ float exponential(float l, float m) {
+    const float x = __builtin_fmaf(l, kLog2e, -m * kLog2e), y = (l - m) * kLog2e;
+    return __builtin_amdgcn_exp2f(fabsf(m) < kNearTheEnds ? x : y);
+}
+
+// e = exp(l - m) of a row and Z = sum e.  Z = 0 only where every logit is -inf;
+// NaN or +inf makes Z NaN, and with it all that is divided by it.
 template <bool F32, int G, int CH>
 __device__ __forceinline__ void exponentials(const Slice<F32, G, CH> &l, float m, float e[8 * CH], float &Z) {
     float z[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (__any(!(fabsf(m) < 1e37f))) {
+    if (__any(!(fabsf(m) < kNearTheEnds))) {
         asm volatile("; extreme logits");        // a branch, not selects
 #pragma unroll
-        for (int v = 0; v < 8 * CH; v++) e[v] = __builtin_amdgcn_exp2f((l.at(v) - m) * kLog2e);
+        for (int v = 0; v < 8 * CH; v++) e[v] = exponential(l.at(v), m);
     } else {
         const float by = -m * kLog2e;
 #pragma unroll
-        for (int v = 0; v < 8 * CH; v++)
-            e[v] = __builtin_amdgcn_exp2f(__builtin_fmaf(l.at(v), kLog2e, by));
+        for (int v = 0; v < 8 * CH; v++) e[v] = __builtin_amdgcn_exp2f(__builtin_fmaf(l.at(v), kLog2e, by));
     }
 #pragma unroll
     for (int v = 0; v < 8 * CH; v++) z[v % 4] += e[v];
     Z = group_sum<G>((z[0] + z[1]) + (z[2] + z[3]));
 }
 
-// The falling list of a row's KP largest keys, in all of its lanes.  inv: ~index
-// of the lane's first expert
+// The KP largest keys of a row in falling order: lane g has the ones at g, g + G,
+// .. in mine, all lanes the first in most.  Each lane sorts its own KP largest; then
+// KP times the largest head of the G lists is taken off its list.  inv: ~index of
+// the lane's first expert
 template <bool F32, int G, int CH, int KP>
-__device__ __forceinline__ void pick(const Slice<F32, G, CH> &l, uint32_t inv, typename Key<F32>::type best[KP]) {
+__device__ __forceinline__ void pick(const Slice<F32, G, CH> &l, uint32_t inv, int g,
+                                     typename Key<F32>::type mine[(KP + G - 1) / G], typename Key<F32>::type &most) {
     typedef Key<F32> K;
+    typename K::type best[KP];
     typedef Best<F32, KP> B;
     constexpr int W = Slice<F32, G, CH>::W, U = KP < 8 ? 8 : KP, N = U / W;   // elements and chunks sorted together
 #pragma unroll
@@ -503,18 +512,36 @@ __device__ __forceinline__ void pick(const Slice<F32, G, CH> &l, uint32_t inv, t
             B::merge(best, key);
         }
     }
-    B::template across<G>(best);
+    if constexpr (G == 1) {
+#pragma unroll
+        for (int i = 0; i < KP; i++) mine[i] = best[i];
+        most = best[0];
+    } else {
+#pragma unroll
+        for (int s = 0; s < KP; s++) {
+            const typename K::type head = group_most<G>(best[0]);
+            if (s == 0) most = head;
+            if (g == s % G) mine[s / G] = head;
+            const bool taken = best[0] == head;
+            typename K::type own = best[0];
+#pragma unroll
+            for (int i = 0; i + 1 < KP - s; i++) {
+                typename K::type next = best[i + 1];
+                asm("" : "+v"(next));         // a select of values, not of their places in the list
+                best[i] = taken ? next : own;
+                own = next;
+            }
+        }
+    }
 }
 
-// The same list one key at a time, for rows with NaN or with zeros of both
-// signs among the choices
+// The same one key at a time, for rows with NaN or with zeros of both signs
+// among the choices; the largest key is not needed again
 template <bool F32, int G, int CH, int KP>
-__device__ __forceinline__ void pick_any(const Slice<F32, G, CH> &l, uint32_t inv, int k,
-                                         typename Key<F32>::type best[KP]) {
+__device__ __forceinline__ void pick_any(const Slice<F32, G, CH> &l, uint32_t inv, int g, int k,
+                                         typename Key<F32>::type mine[(KP + G - 1) / G]) {
     typedef Key<F32> K;
     typename K::type last = K::kNone;
-#pragma unroll
-    for (int i = 0; i < KP; i++) best[i] = K::kNone;
 #pragma nounroll
     for (int s = 0; s < k; s++) {
         typename K::type most = K::kNone;
@@ -523,10 +550,10 @@ __device__ __forceinline__ void pick_any(const Slice<F32, G, CH> &l, uint32_t in
             const typename K::type key = K::make(l.at(v), inv ^ Slice<F32, G, CH>::expert(v, 0));
             if (s == 0 || key < last) most = K::hi(most, key);
         }
-        last = group_most<F32, G>(most);
+        last = group_most<G>(most);
 #pragma unroll
-        for (int i = 0; i < KP; i++)
-            if (s == i) best[i] = last;
+        for (int i = 0; i < (KP + G - 1) / G; i++)
+            if (s == i * G + g) mine[i] = last;
     }
 }
 
@@ -537,6 +564,7 @@ __global__ __launch_bounds__(256, KP == 16 || CH == 4 || !VEC ? 3 : 4) void k_ro
     typedef typename K::type KT;
     typedef Slice<F32, G, CH> L;
     constexpr int V = L::V, C = V * G, R = 256 / G;       // per lane; columns; tokens of a block's pass
+    constexpr int S = (KP + G - 1) / G;                   // choices of a lane: g, g + G, ..
     __shared__ uint32_t hist[C];
     __shared__ float sums[R * C];
     __shared__ uint32_t routed_of[4];
@@ -554,40 +582,36 @@ __global__ __launch_bounds__(256, KP == 16 || CH == 4 || !VEC ? 3 : 4) void k_ro
         L l;
         const int64_t at = t < a.tokens ? t : 0;
         l.template load<VEC>(static_cast<const T *>(a.logits) + at * a.stride, g, a.E);
-        l.keep(t < a.tokens && (!a.mask || a.mask[at]), g, a.E);
-        KT best[KP];
-        pick<F32, G, CH, KP>(l, inv, best);
-        float m = K::open(best[0]) ? K::value(best[0]) : 0.0f, e[V], Z;
+        const bool there = t < a.tokens && (!a.mask || a.mask[at]);
+        if (!__all(there) || a.E < C) {
+            asm volatile("; logits that do not exist");
+            l.keep(there, g, a.E);
+        }
+        KT mine[S], most;
+        pick<F32, G, CH, KP>(l, inv, g, mine, most);
+        const float m = K::open(most) ? K::value(most) : 0.0f;
+        float e[V], Z;
         exponentials<F32, G, CH>(l, m, e, Z);
         bool odd = Z != Z;
-        if (__any(!K::positive(best[KP - 1]))) {
-            asm volatile("; choices down to zero");
 #pragma unroll
-            for (int i = 0; i < KP; i++) odd = odd || K::zero(best[i]);
-        }
+        for (int s = 0; s < S; s++) odd = odd || (s * G + g < KP && K::zero(mine[s]));
         if (__any(odd)) {
             uint32_t start = inv;
             asm volatile("; NaN, or zeros that may tie" : "+v"(start));   // (opaque: no constants of it are kept)
-            pick_any<F32, G, CH, KP>(l, start, a.k, best);
+            pick_any<F32, G, CH, KP>(l, start, g, a.k, mine);
         }
         const float by_z = Z == 0.0f ? 0.0f : reciprocal(Z);
         if (g == 0) routed += Z != 0.0f;
 #pragma unroll
         for (int v = 0; v < V; v++) acc[v] = __builtin_fmaf(e[v], by_z, acc[v]);
 
-        // lane g writes choices g, g + G, ..
-        constexpr int S = (KP + G - 1) / G;
         float ge[S], top = 0.0f;
         int id[S];
 #pragma unroll
         for (int s = 0; s < S; s++) {
-            KT mine = best[s * G];
-#pragma unroll
-            for (int i = 1; i < G; i++)
-                if (s * G + i < KP && g == i) mine = best[s * G + i < KP ? s * G + i : 0];
-            const bool open = s * G + g < a.k && K::open(mine);
-            id[s] = open ? K::index(mine) : -1;
-            ge[s] = open ? __builtin_amdgcn_exp2f((K::value(mine) - m) * kLog2e) : 0.0f;
+            const bool open = s * G + g < a.k && K::open(mine[s]);
+            id[s] = open ? K::index(mine[s]) : -1;
+            ge[s] = open ? exponential(K::value(mine[s]), m) : 0.0f;
             top += ge[s];
         }
         // a choice is the row's largest logit, so that the sum is 1 or more
@@ -839,7 +863,7 @@ __global__ __launch_bounds__(256) void k_route_backward(RouteBackwardArgs a) {
         float gs[S], top = 0.0f, gd = 0.0f;
 #pragma unroll
         for (int s = 0; s < S; s++) {
-            gs[s] = row.id[s] >= 0 ? __builtin_amdgcn_exp2f((El::up(ls[s]) - m) * kLog2e) : 0.0f;
+            gs[s] = row.id[s] >= 0 ? exponential(El::up(ls[s]), m) : 0.0f;
             top += gs[s];
         }
         float by = inv;
