@@ -99,12 +99,15 @@ __device__ __forceinline__ void store8(void *p, int64_t at, const float v[8]) {
     }
 }
 
-// kFlat: one row, 16-byte aligned; kRows: rows of a multiple of 8 elements,
-// every row 16-byte aligned; kAny: element by element, any alignment
-enum Access { kFlat, kRows, kAny };
+template <bool F32, bool RES>
+__device__ __forceinline__ float dropout_one(float x, float r, bool keep, float scale) {
+    const float y = keep ? x * scale : 0.0f;
+    return RES ? r + y : y;
+}
 
-// A thread takes the eight elements of one Philox block.
-template <bool F32, bool RES, int ACCESS>
+// Rows of a multiple of 8 elements, all 16-byte aligned, or one row of any
+// length (ROWS false): a thread takes the eight elements of one Philox block.
+template <bool F32, bool RES, bool ROWS>
 __global__ __launch_bounds__(256) void k_dropout(DropoutArgs a, int64_t blocks) {
     typedef Elem<F32> El;
     typedef typename El::type T;
@@ -114,34 +117,80 @@ __global__ __launch_bounds__(256) void k_dropout(DropoutArgs a, int64_t blocks) 
         uint32_t w[4] = {0, 0, 0, 0};
         if (a.threshold) dropout_words((uint64_t)b, a, round, w);   // T = 0 keeps everything
         int64_t row = 0, col = 8 * b;
-        if (ACCESS != kFlat) {
+        if (ROWS) {
             row = col / a.cols;
             col -= row * a.cols;
         }
-        if (ACCESS != kAny && 8 * b + 8 <= n) {
+        if (ROWS || 8 * b + 8 <= n) {
             float x[8], r[8];
             load8<F32>(a.x, row * a.xs + col, x);
             if (RES) load8<F32>(a.residual, row * a.rs + col, r);
 #pragma unroll
-            for (int j = 0; j < 8; j++) {
-                x[j] = dither(w, j) >= a.threshold ? x[j] * a.scale : 0.0f;
-                if (RES) x[j] = r[j] + x[j];
-            }
+            for (int j = 0; j < 8; j++)
+                x[j] = dropout_one<F32, RES>(x[j], r[j], dither(w, j) >= a.threshold, a.scale);
             store8<F32>(a.y, row * a.ys + col, x);
         } else {
-            const int m = (int)(n - 8 * b < 8 ? n - 8 * b : 8);
 #pragma unroll
             for (int j = 0; j < 8; j++) {
-                if (j >= m) break;
-                float v = El::up(static_cast<const T *>(a.x)[row * a.xs + col]);
-                v = dither(w, j) >= a.threshold ? v * a.scale : 0.0f;
-                if (RES) v = El::up(static_cast<const T *>(a.residual)[row * a.rs + col]) + v;
-                static_cast<T *>(a.y)[row * a.ys + col] = El::down(v);
-                if (++col == a.cols) {
-                    col = 0;
+                if (col + j >= n) break;
+                const float r = RES ? El::up(static_cast<const T *>(a.residual)[col + j]) : 0.0f;
+                static_cast<T *>(a.y)[col + j] = El::down(dropout_one<F32, RES>(
+                    El::up(static_cast<const T *>(a.x)[col + j]), r, dither(w, j) >= a.threshold, a.scale));
+            }
+        }
+    }
+}
+
+// Any alignment and row length: a wave draws 64 Philox blocks and then takes
+// their 512 elements 64 at a time, side by side in its lanes.
+template <bool F32, bool RES>
+__global__ __launch_bounds__(256) void k_dropout_any(DropoutArgs a, int64_t tiles) {
+    typedef Elem<F32> El;
+    typedef typename El::type T;
+    const uint32_t round = a.round + (a.d_round ? *a.d_round : 0);
+    const int64_t n = a.rows * a.cols;
+    const int lane = threadIdx.x & 63;
+    // cols < 64: the rows that 64 elements go down, and what is left of them
+    const int skip = a.cols < 64 ? 64 / (int)a.cols : 1;
+    const int64_t left = a.cols < 64 ? 64 % (int)a.cols : 64 - a.cols;
+    for (int64_t tile = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); tile < tiles; tile += (int64_t)gridDim.x * 4) {
+        uint32_t keep = 0xFF;
+        if (a.threshold) {
+            uint32_t w[4];
+            dropout_words((uint64_t)(64 * tile + lane), a, round, w);
+            keep = 0;
+#pragma unroll
+            for (int j = 0; j < 8; j++) keep |= (uint32_t)(dither(w, j) >= a.threshold) << j;
+        }
+        int64_t at = 512 * tile + lane, row = at / a.cols, col = at - row * a.cols;
+        T x[8], r[8];
+        int64_t y[8];
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            const bool there = at + 64 * i < n;
+            x[i] = static_cast<const T *>(a.x)[there ? row * a.xs + col : 0];
+            if (RES) r[i] = static_cast<const T *>(a.residual)[there ? row * a.rs + col : 0];
+            y[i] = there ? row * a.ys + col : -1;
+            // 64 elements on
+            if (a.cols < 64) {
+                row += skip;
+                col += left;
+                if (col >= a.cols) {
+                    col -= a.cols;
                     row++;
                 }
+            } else {
+                const bool next = col + 64 >= a.cols;
+                col += next ? left : 64;
+                row += next;
             }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            const bool kept = (uint32_t)__shfl((int)keep, 8 * i + lane / 8, 64) >> (lane & 7) & 1;
+            if (y[i] >= 0)
+                static_cast<T *>(a.y)[y[i]] =
+                    El::down(dropout_one<F32, RES>(El::up(x[i]), RES ? El::up(r[i]) : 0.0f, kept, a.scale));
         }
     }
 }
@@ -149,19 +198,19 @@ __global__ __launch_bounds__(256) void k_dropout(DropoutArgs a, int64_t blocks) 
 template <bool F32, bool RES>
 hipError_t dropout_access(const DropoutArgs &a, hipStream_t s) {
     const int64_t es = F32 ? 4 : 2;
-    const int64_t blocks = (a.rows * a.cols + 7) / 8;
-    const int64_t want = (blocks + 255) / 256;
-    const dim3 grid((unsigned)(want < (1 << 20) ? want : (1 << 20))), block(256);
+    const int64_t blocks = (a.rows * a.cols + 7) / 8, tiles = (blocks + 63) / 64;
+    const auto grid = [](int64_t want) { return dim3((unsigned)(want < (1 << 20) ? want : (1 << 20))); };
+    const dim3 block(256);
     const auto on16 = [&](const void *p, int64_t stride) {
         return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (a.rows == 1 || stride * es % 16 == 0);
     };
     const bool vec = on16(a.x, a.xs) && on16(a.y, a.ys) && (!RES || on16(a.residual, a.rs));
     if (vec && a.rows == 1)
-        hipLaunchKernelGGL((k_dropout<F32, RES, kFlat>), grid, block, 0, s, a, blocks);
+        hipLaunchKernelGGL((k_dropout<F32, RES, false>), grid((blocks + 255) / 256), block, 0, s, a, blocks);
     else if (vec && a.cols % 8 == 0)
-        hipLaunchKernelGGL((k_dropout<F32, RES, kRows>), grid, block, 0, s, a, blocks);
+        hipLaunchKernelGGL((k_dropout<F32, RES, true>), grid((blocks + 255) / 256), block, 0, s, a, blocks);
     else
-        hipLaunchKernelGGL((k_dropout<F32, RES, kAny>), grid, block, 0, s, a, blocks);
+        hipLaunchKernelGGL((k_dropout_any<F32, RES>), grid((tiles + 3) / 4), block, 0, s, a, tiles);
     return hipGetLastError();
 }
 
@@ -170,28 +219,22 @@ hipError_t dropout_access(const DropoutArgs &a, hipStream_t s) {
 // ---------------------------------------------------------------------------
 
 // A token's logits lie in G lanes (a power of two), 8 CH of them in each, in
-// chunks of W that are 16 bytes: chunk i of lane g holds experts W (i G + g) ..
-// + W - 1.  A wave takes 64 / G tokens.
+// chunks of W: chunk i of lane g holds experts W (i G + g) .. + W - 1.  A wave
+// takes 64 / G tokens.  Chunks are 16 bytes where every row is 16-byte aligned and
+// E a multiple of W, else single logits, so that lanes side by side read and
+// write logits side by side.
 
 constexpr float kLog2e = 1.44269504088896340736f;
 
-// Logits of one chunk as loaded: -inf where there is no such expert, and for
-// a token that is left out.
-template <bool F32>
+// One chunk as loaded; what does not exist is set to -inf by clear().
+template <bool F32, bool VEC>
 struct Chunk;
 template <>
-struct Chunk<false> {
+struct Chunk<false, true> {
     static constexpr int W = 8;
     u32x4 w;
     __device__ __forceinline__ void clear() { w = u32x4{0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u}; }
     __device__ __forceinline__ void load(const uint16_t *p) { w = *reinterpret_cast<const u32x4 *>(p); }
-    __device__ __forceinline__ void load(const uint16_t *row, int at, int E) {
-#pragma unroll
-        for (int j = 0; j < 4; j++) {
-            const uint32_t a = row[min(at + 2 * j, E - 1)], b = row[min(at + 2 * j + 1, E - 1)];
-            w[j] = (at + 2 * j < E ? a : 0xFF80u) | (at + 2 * j + 1 < E ? b : 0xFF80u) << 16;
-        }
-    }
     __device__ __forceinline__ float at(int j) const {
         return __uint_as_float(j & 1 ? w[j >> 1] & 0xFFFF0000u : w[j >> 1] << 16);
     }
@@ -199,7 +242,7 @@ struct Chunk<false> {
     static __device__ __forceinline__ void store(uint16_t *p, const float d[8]) { store8<false>(p, 0, d); }
 };
 template <>
-struct Chunk<true> {
+struct Chunk<true, true> {
     static constexpr int W = 4;
     float v[4];
     __device__ __forceinline__ void clear() { v[0] = v[1] = v[2] = v[3] = -INFINITY; }
@@ -207,38 +250,40 @@ struct Chunk<true> {
         const float4 a = *reinterpret_cast<const float4 *>(p);
         v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
     }
-    __device__ __forceinline__ void load(const float *row, int at, int E) {
-#pragma unroll
-        for (int j = 0; j < 4; j++) {
-            const float x = row[min(at + j, E - 1)];
-            v[j] = at + j < E ? x : -INFINITY;
-        }
-    }
     __device__ __forceinline__ float at(int j) const { return v[j]; }
     __device__ __forceinline__ void arrived() { asm volatile("" : "+v"(v[0]), "+v"(v[1]), "+v"(v[2]), "+v"(v[3])); }
     static __device__ __forceinline__ void store(float *p, const float d[4]) {
         *reinterpret_cast<float4 *>(p) = make_float4(d[0], d[1], d[2], d[3]);
     }
 };
+template <bool F32>
+struct Chunk<F32, false> {
+    typedef typename Elem<F32>::type T;
+    static constexpr int W = 1;
+    T v;
+    __device__ __forceinline__ void clear() { v = Elem<F32>::down(-INFINITY); }
+    __device__ __forceinline__ void load(const T *p) { v = *p; }
+    __device__ __forceinline__ float at(int) const { return Elem<F32>::up(v); }
+    __device__ __forceinline__ void arrived() { asm volatile("" : "+v"(v)); }
+    static __device__ __forceinline__ void store(T *p, const float d[1]) { *p = Elem<F32>::down(d[0]); }
+};
 
-// The logits of a row that one lane holds.  VEC: every row 16-byte aligned, E
-// a multiple of W.
-template <bool F32, int G, int CH>
+// The logits of a row that one lane holds
+template <bool F32, int G, int CH, bool VEC>
 struct Slice {
-    static constexpr int W = Chunk<F32>::W, V = 8 * CH, N = V / W;
-    Chunk<F32> c[N];
+    typedef Chunk<F32, VEC> C;
+    static constexpr int W = C::W, V = 8 * CH, N = V / W;
+    C c[N];
     // expert of element v in lane g
-    static __device__ __forceinline__ int expert(int v, int g) { return W * ((v / W) * G + g) + v % W; }
+    static __device__ __forceinline__ constexpr int expert(int v, int g) { return W * ((v / W) * G + g) + v % W; }
     __device__ __forceinline__ float at(int v) const { return c[v / W].at(v % W); }
     // Loads that nothing waits for: no branch, every address inside the row;
     // keep() then leaves -inf where no logit belongs.
-    template <bool VEC>
     __device__ __forceinline__ void load(const typename Elem<F32>::type *row, int g, int E) {
 #pragma unroll
         for (int i = 0; i < N; i++) {
             const int at = W * (i * G + g);
-            if (VEC) c[i].load(row + (at < E ? at : 0));
-            else c[i].load(row, at, E);
+            c[i].load(row + (at < E ? at : 0));
         }
     }
     __device__ __forceinline__ void arrived() {
@@ -269,7 +314,10 @@ struct Key<false> {
         const s16x2 sign = __builtin_bit_cast(s16x2, w) >> 15;
         return __builtin_amdgcn_bitop3_b32(__builtin_bit_cast(uint32_t, sign), 0x7FFF7FFFu, w, 0x6A);   // (a & b) ^ c
     }
-    static __device__ __forceinline__ void chunk(const Chunk<false> &c, uint32_t inv, int32_t key[8]) {
+    static __device__ __forceinline__ void chunk(const Chunk<false, false> &c, uint32_t inv, int32_t key[1]) {
+        key[0] = (int32_t)(ordered(c.v) << 16 | inv);
+    }
+    static __device__ __forceinline__ void chunk(const Chunk<false, true> &c, uint32_t inv, int32_t key[8]) {
 #pragma unroll
         for (int q = 0; q < 4; q++) {
             const uint32_t o = ordered(c.w[q]);
@@ -303,7 +351,10 @@ struct Key<true> {
     static __device__ __forceinline__ uint32_t ordered(uint32_t u) {
         return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
     }
-    static __device__ __forceinline__ void chunk(const Chunk<true> &c, uint32_t inv, double key[4]) {
+    static __device__ __forceinline__ void chunk(const Chunk<true, false> &c, uint32_t inv, double key[1]) {
+        key[0] = pack(ordered(__float_as_uint(c.v)), inv);
+    }
+    static __device__ __forceinline__ void chunk(const Chunk<true, true> &c, uint32_t inv, double key[4]) {
 #pragma unroll
         for (int j = 0; j < 4; j++) key[j] = pack(ordered(__float_as_uint(c.v[j])), inv ^ j);
     }
@@ -453,8 +504,8 @@ __device__ __forceinline__ float exponential(float l, float m) {
 
 // e = exp(l - m) of a row and Z = sum e.  Z = 0 only where every logit is -inf;
 // NaN or +inf makes Z NaN, and with it all that is divided by it.
-template <bool F32, int G, int CH>
-__device__ __forceinline__ void exponentials(const Slice<F32, G, CH> &l, float m, float e[8 * CH], float &Z) {
+template <bool F32, int G, int CH, bool VEC>
+__device__ __forceinline__ void exponentials(const Slice<F32, G, CH, VEC> &l, float m, float e[8 * CH], float &Z) {
     float z[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     if (__any(!(fabsf(m) < kNearTheEnds))) {
         asm volatile("; extreme logits");        // a branch, not selects
@@ -474,19 +525,19 @@ __device__ __forceinline__ void exponentials(const Slice<F32, G, CH> &l, float m
 // .. in mine, all lanes the first in most.  Each lane sorts its own KP largest; then
 // KP times the largest head of the G lists is taken off its list.  inv: ~index of
 // the lane's first expert
-template <bool F32, int G, int CH, int KP>
-__device__ __forceinline__ void pick(const Slice<F32, G, CH> &l, uint32_t inv, int g,
+template <int KP, bool F32, int G, int CH, bool VEC>
+__device__ __forceinline__ void pick(const Slice<F32, G, CH, VEC> &l, uint32_t inv, int g,
                                      typename Key<F32>::type mine[(KP + G - 1) / G], typename Key<F32>::type &most) {
     typedef Key<F32> K;
     typename K::type best[KP];
     typedef Best<F32, KP> B;
-    constexpr int W = Slice<F32, G, CH>::W, U = KP < 8 ? 8 : KP, N = U / W;   // elements and chunks sorted together
+    constexpr int W = Slice<F32, G, CH, VEC>::W, U = KP < 8 ? 8 : KP, N = U / W;   // elements and chunks sorted together
 #pragma unroll
-    for (int i = 0; i < Slice<F32, G, CH>::N; i += N) {
+    for (int i = 0; i < Slice<F32, G, CH, VEC>::N; i += N) {
         typename K::type key[U];
 #pragma unroll
         for (int n = 0; n < N; n++) {
-            if (i + n < Slice<F32, G, CH>::N) {
+            if (i + n < Slice<F32, G, CH, VEC>::N) {
                 K::chunk(l.c[i + n], inv, key + W * n);
                 if (n > 0)
 #pragma unroll
@@ -537,8 +588,8 @@ __device__ __forceinline__ void pick(const Slice<F32, G, CH> &l, uint32_t inv, i
 
 // The same one key at a time, for rows with NaN or with zeros of both signs
 // among the choices; the largest key is not needed again
-template <bool F32, int G, int CH, int KP>
-__device__ __forceinline__ void pick_any(const Slice<F32, G, CH> &l, uint32_t inv, int g, int k,
+template <int KP, bool F32, int G, int CH, bool VEC>
+__device__ __forceinline__ void pick_any(const Slice<F32, G, CH, VEC> &l, uint32_t inv, int g, int k,
                                          typename Key<F32>::type mine[(KP + G - 1) / G]) {
     typedef Key<F32> K;
     typename K::type last = K::kNone;
@@ -547,7 +598,7 @@ __device__ __forceinline__ void pick_any(const Slice<F32, G, CH> &l, uint32_t in
         typename K::type most = K::kNone;
 #pragma unroll
         for (int v = 0; v < 8 * CH; v++) {
-            const typename K::type key = K::make(l.at(v), inv ^ Slice<F32, G, CH>::expert(v, 0));
+            const typename K::type key = K::make(l.at(v), inv ^ Slice<F32, G, CH, VEC>::expert(v, 0));
             if (s == 0 || key < last) most = K::hi(most, key);
         }
         last = group_most<G>(most);
@@ -562,7 +613,7 @@ __global__ __launch_bounds__(256, KP == 16 || CH == 4 || !VEC ? 3 : 4) void k_ro
     typedef typename Elem<F32>::type T;
     typedef Key<F32> K;
     typedef typename K::type KT;
-    typedef Slice<F32, G, CH> L;
+    typedef Slice<F32, G, CH, VEC> L;
     constexpr int V = L::V, C = V * G, R = 256 / G;       // per lane; columns; tokens of a block's pass
     constexpr int S = (KP + G - 1) / G;                   // choices of a lane: g, g + G, ..
     __shared__ uint32_t hist[C];
@@ -581,24 +632,24 @@ __global__ __launch_bounds__(256, KP == 16 || CH == 4 || !VEC ? 3 : 4) void k_ro
     for (int64_t base = (int64_t)blockIdx.x * R; base < a.tokens; base += step, t += step) {
         L l;
         const int64_t at = t < a.tokens ? t : 0;
-        l.template load<VEC>(static_cast<const T *>(a.logits) + at * a.stride, g, a.E);
+        l.load(static_cast<const T *>(a.logits) + at * a.stride, g, a.E);
         const bool there = t < a.tokens && (!a.mask || a.mask[at]);
         if (!__all(there) || a.E < C) {
             asm volatile("; logits that do not exist");
             l.keep(there, g, a.E);
         }
         KT mine[S], most;
-        pick<F32, G, CH, KP>(l, inv, g, mine, most);
+        pick<KP>(l, inv, g, mine, most);
         const float m = K::open(most) ? K::value(most) : 0.0f;
         float e[V], Z;
-        exponentials<F32, G, CH>(l, m, e, Z);
+        exponentials(l, m, e, Z);
         bool odd = Z != Z;
 #pragma unroll
         for (int s = 0; s < S; s++) odd = odd || (s * G + g < KP && K::zero(mine[s]));
         if (__any(odd)) {
             uint32_t start = inv;
             asm volatile("; NaN, or zeros that may tie" : "+v"(start));   // (opaque: no constants of it are kept)
-            pick_any<F32, G, CH, KP>(l, start, g, a.k, mine);
+            pick_any<KP>(l, start, g, a.k, mine);
         }
         const float by_z = Z == 0.0f ? 0.0f : reciprocal(Z);
         if (g == 0) routed += Z != 0.0f;
@@ -780,7 +831,7 @@ template <bool F32, int G, int CH, int S, bool VEC>
 __global__ __launch_bounds__(256) void k_route_backward(RouteBackwardArgs a) {
     typedef Elem<F32> El;
     typedef typename El::type T;
-    typedef Slice<F32, G, CH> L;
+    typedef Slice<F32, G, CH, VEC> L;
     constexpr int V = L::V, W = L::W, C = V * G, R = 256 / G;
     __shared__ alignas(16) float rows[R * C];
     const int g = threadIdx.x % G, r = threadIdx.x / G;
@@ -795,7 +846,7 @@ __global__ __launch_bounds__(256) void k_route_backward(RouteBackwardArgs a) {
     // lane g holds choices g, g + G, ..; nothing waits for these loads
     const auto load = [&](Row &row, int64_t t) {
         if (t >= a.tokens) t = 0;
-        row.l.template load<VEC>(logits + t * a.stride, g, a.E);
+        row.l.load(logits + t * a.stride, g, a.E);
         row.mask = 1;
         if (a.mask) row.mask = a.mask[t];
 #pragma unroll
@@ -855,7 +906,7 @@ __global__ __launch_bounds__(256) void k_route_backward(RouteBackwardArgs a) {
         for (int v = 0; v < V; v++) m = fmaxf(m, row.l.at(v));
         m = group_max<G>(m);
         if (m == -INFINITY) m = 0.0f;
-        exponentials<F32, G, CH>(row.l, m, e, Z);
+        exponentials(row.l, m, e, Z);
         const float inv = Z == 0.0f ? 0.0f : reciprocal(Z);
         float dots[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -895,17 +946,11 @@ __global__ __launch_bounds__(256) void k_route_backward(RouteBackwardArgs a) {
             for (int i = 0; i < L::N; i++) {
                 const int at = L::expert(W * i, g);
                 float d[W];
-                __builtin_memcpy(d, __builtin_assume_aligned(h + at, 16), sizeof d);
+                __builtin_memcpy(d, __builtin_assume_aligned(h + at, W < 4 ? 4 : 16), sizeof d);
 #pragma unroll
                 for (int j = 0; j < W; j++)
                     d[j] = __builtin_fmaf(e[W * i + j], __builtin_fmaf(up[W * i + j], inv, dot), d[j]);
-                if (VEC) {
-                    if (at < a.E) Chunk<F32>::store(out + at, d);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < W; j++)
-                        if (at + j < a.E) out[at + j] = El::down(d[j]);
-                }
+                if (at < a.E) L::C::store(out + at, d);
             }
         }
         wave_lds_sync();

@@ -412,8 +412,11 @@ def test_route_strided_rows(E, wide, at, dtype):
     assert same(out[:, at:at + E], d)
     out[:, at:at + E] = 7.0
     assert bool((out == 7.0).all())
-    again = l.clone()
+    # in place, at this layout bit for bit; at another one sums run in another order
+    again = big.clone()[:, at:at + E]
     assert same(dq.route_backward(again, ids, dg, coef, out=again), d)
+    again = l.clone()
+    check_gradient(dq.route_backward(again, ids, dg, coef, out=again), r, dg, coef, 1.0, dtype)
     row = l[:1].expand(70, E)                                          # all tokens alike
     i3 = dq.route(row, k)[0]
     assert torch.equal(i3, ids[:1].expand(70, k))
