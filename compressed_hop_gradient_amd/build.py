@@ -2,6 +2,7 @@
 without a GPU)."""
 import os
 import subprocess
+import tempfile
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -10,7 +11,7 @@ LIB = os.path.join(PKG, "libdq.so")
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [
-    "-O3", "--offload-arch=gfx950", "-std=c++17", "-fPIC", "-shared",
+    "-O3", "--offload-arch=gfx950", "-std=c++17", "-fPIC",
     # numerics shared with the CPU oracle: no contraction, IEEE division, no fast-math
     "-ffp-contract=off", "-fhip-fp32-correctly-rounded-divide-sqrt", "-fno-fast-math",
     # packed FP32 instructions are kept out of every kernel
@@ -19,23 +20,42 @@ FLAGS = [
     "-fconstexpr-steps=100000000",
     "-Wall", "-Wno-unused-command-line-argument",
 ]
-SOURCES = ["dq_kernels.hip", "dq_api.cpp", "dq_train.hip", "dq_train_api.cpp"]
+SOURCES = ["dq_kernels.hip", "dq_api.cpp", "dq_dropout.hip", "dq_route.hip", "dq_route_backward.hip",
+           "dq_train_api.cpp"]
 
 
 def build(verbose=False):
-    """Compile every HIP source of the package into ``libdq.so`` (always rebuilds)."""
-    tmp = LIB + ".tmp"
-    cmd = [HIPCC] + FLAGS + ["-I", os.path.join(ROOT, "include"), "-I", CSRC] + \
-          [os.path.join(CSRC, s) for s in SOURCES] + ["-o", tmp]
-    if verbose:
-        print(" ".join(cmd))
-    res = subprocess.run(cmd, capture_output=True, text=True)
+    """Compile every HIP source of the package into ``libdq.so`` (always rebuilds);
+    the sources compile side by side."""
     noise = "is not a recognized feature for this target"
-    err = "\n".join(l for l in (res.stderr or "").splitlines() if noise not in l)
-    if res.returncode != 0:
-        raise RuntimeError("hipcc failed:\n" + err)
-    if verbose and err.strip():
-        print(err)
+
+    def finish(proc):
+        _, err = proc.communicate()
+        err = "\n".join(l for l in (err or "").splitlines() if noise not in l)
+        if proc.returncode != 0:
+            raise RuntimeError("hipcc failed:\n" + err)
+        if verbose and err.strip():
+            print(err)
+
+    def start(args):
+        if verbose:
+            print(" ".join(args))
+        return subprocess.Popen(args, stdout=subprocess.DEVNULL, stderr=subprocess.PIPE, text=True)
+
+    tmp = LIB + ".tmp"
+    with tempfile.TemporaryDirectory(prefix="dq_build_") as objs:
+        out = [os.path.join(objs, os.path.splitext(s)[0] + ".o") for s in SOURCES]
+        procs = [start([HIPCC] + FLAGS + ["-I", os.path.join(ROOT, "include"), "-I", CSRC, "-c",
+                                          os.path.join(CSRC, s), "-o", o]) for s, o in zip(SOURCES, out)]
+        failed = None
+        for p in procs:
+            try:
+                finish(p)
+            except RuntimeError as e:
+                failed = failed or e
+        if failed:
+            raise failed
+        finish(start([HIPCC, "--offload-arch=gfx950", "-fPIC", "-shared"] + out + ["-o", tmp]))
     os.replace(tmp, LIB)
     return LIB
 
