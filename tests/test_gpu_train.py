@@ -704,3 +704,42 @@ def test_step_in_graph_replays():
         for a, b in zip(held, step()):
             assert torch.equal(a, b), rep
     assert alive.loss.item() > 0
+
+
+# ---- together ------------------------------------------------------------------------
+
+def _example():
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "moe_step.py")
+    spec = importlib.util.spec_from_file_location("moe_step", path)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    return m
+
+
+def test_moe_example_learns_with_compressed_gradients():
+    """Router, dropout and gradient round in one data-parallel step: the loss
+    falls well below chance (ln 16 = 2.77) and tokens stay spread."""
+    moe = _example()
+    t = moe.Trainer(workers=4, tokens=256)
+    first = t.step(0)
+    for step in range(1, 60):
+        last = t.step(step)
+    assert first[0] > 2.0 and last[0] < 0.5 * first[0]
+    assert all(c.sum().item() == 4 * 256 * moe.TOP_K for c in last[2])
+    assert last[1] < 2.0
+
+
+def test_moe_example_step_against_fp32_gradients():
+    """The same step with its gradients summed in fp32: the forward pass is the
+    same (up to the order of library sums), the compressed update differs by
+    the round's quantisation only."""
+    moe = _example()
+    a, b = moe.Trainer(workers=2, tokens=64), moe.Trainer(workers=2, tokens=64, exact=True)
+    ra, rb = a.step(0), b.step(0)
+    assert abs(ra[0] - rb[0]) < 1e-5 and abs(ra[1] - rb[1]) < 1e-5
+    start = moe.init()
+    da = torch.cat([(w - start[k]).reshape(-1) for k, w in a.weights.items()]).double()
+    db = torch.cat([(w - start[k]).reshape(-1) for k, w in b.weights.items()]).double()
+    assert ((da - db).norm() / db.norm()).item() < 0.2
