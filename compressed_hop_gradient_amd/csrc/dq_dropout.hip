@@ -35,7 +35,7 @@ __device__ __forceinline__ uint32_t dither(const uint32_t w[4], int j) {
     return j & 1 ? w[j >> 1] >> 16 : w[j >> 1] & 0xFFFFu;
 }
 
-template <bool F32, bool RES>
+template <bool RES>
 __device__ __forceinline__ float dropout_one(float x, float r, bool keep, float scale) {
     const float y = keep ? x * scale : 0.0f;
     return RES ? r + y : y;
@@ -63,14 +63,14 @@ __global__ __launch_bounds__(256) void k_dropout(DropoutArgs a, int64_t blocks) 
             if (RES) load8<F32>(a.residual, row * a.rs + col, r);
 #pragma unroll
             for (int j = 0; j < 8; j++)
-                x[j] = dropout_one<F32, RES>(x[j], r[j], dither(w, j) >= a.threshold, a.scale);
+                x[j] = dropout_one<RES>(x[j], RES ? r[j] : 0.0f, dither(w, j) >= a.threshold, a.scale);
             store8<F32>(a.y, row * a.ys + col, x);
         } else {
 #pragma unroll
             for (int j = 0; j < 8; j++) {
                 if (col + j >= n) break;
                 const float r = RES ? El::up(static_cast<const T *>(a.residual)[col + j]) : 0.0f;
-                static_cast<T *>(a.y)[col + j] = El::down(dropout_one<F32, RES>(
+                static_cast<T *>(a.y)[col + j] = El::down(dropout_one<RES>(
                     El::up(static_cast<const T *>(a.x)[col + j]), r, dither(w, j) >= a.threshold, a.scale));
             }
         }
@@ -126,7 +126,7 @@ __global__ __launch_bounds__(256) void k_dropout_any(DropoutArgs a, int64_t tile
             const bool kept = (uint32_t)__shfl((int)keep, 8 * i + lane / 8, 64) >> (lane & 7) & 1;
             if (y[i] >= 0)
                 static_cast<T *>(a.y)[y[i]] =
-                    El::down(dropout_one<F32, RES>(El::up(x[i]), RES ? El::up(r[i]) : 0.0f, kept, a.scale));
+                    El::down(dropout_one<RES>(El::up(x[i]), RES ? El::up(r[i]) : 0.0f, kept, a.scale));
         }
     }
 }

@@ -276,7 +276,7 @@ __global__ __launch_bounds__(256, KP == 16 || CH == 4 || !VEC ? 3 : 4) void k_ro
     int64_t t = (int64_t)blockIdx.x * R + r;
     for (int64_t base = (int64_t)blockIdx.x * R; base < a.tokens; base += step, t += step) {
         L l;
-        const int64_t at = t < a.tokens ? t : 0;
+        const int64_t at = t < a.tokens ? t : a.tokens - 1;
         l.load(static_cast<const T *>(a.logits) + at * a.stride, g, a.E);
         const bool there = t < a.tokens && (!a.mask || a.mask[at]);
         if (!__all(there) || a.E < C) {

@@ -35,7 +35,7 @@ __global__ __launch_bounds__(256) void k_route_backward(RouteBackwardArgs a) {
     };
     // lane g holds choices g, g + G, ..; nothing waits for these loads
     const auto load = [&](Row &row, int64_t t) {
-        if (t >= a.tokens) t = 0;
+        if (t >= a.tokens) t = a.tokens - 1;
         row.l.load(logits + t * a.stride, g, a.E);
         row.mask = 1;
         if (a.mask) row.mask = a.mask[t];
@@ -87,9 +87,9 @@ __global__ __launch_bounds__(256) void k_route_backward(RouteBackwardArgs a) {
 #pragma unroll
         for (int s = 0; s < S; s++) {
             if (!there || s * G + g >= a.k || (uint32_t)row.id[s] >= (uint32_t)a.E) row.id[s] = -1;
-            ls[s] = logits[(there ? t : 0) * a.stride + (row.id[s] < 0 ? 0 : row.id[s])];
+            ls[s] = logits[(t < a.tokens ? t : a.tokens - 1) * a.stride + (row.id[s] < 0 ? 0 : row.id[s])];
         }
-        load(next, t + step);
+        if (base + step < a.tokens) load(next, t + step);
         row.l.keep(there, g, a.E);
         float m = -INFINITY, e[V], Z;
 #pragma unroll
