@@ -60,8 +60,11 @@ def dropout(x, p, residual=None, training=True, seed=1, rnd=0, worker=0, site=0)
 
 
 class _Route(torch.autograd.Function):
+    """loss, *gates; ids, counts and coef, which have no gradient, go into
+    ``found``."""
+
     @staticmethod
-    def forward(ctx, top_k, renorm, masks, reduce, *logits):
+    def forward(ctx, top_k, renorm, masks, reduce, found, *logits):
         ids, gates, stats = [], [], None
         logits = [_by_rows(l) for l in logits]
         for l, m in zip(logits, masks):
@@ -72,25 +75,26 @@ class _Route(torch.autograd.Function):
             stats = stats.fold()
             reduce(stats)
         loss, coef, counts = dq.balance(stats, top_k)
+        found += (ids, counts, coef)
         ctx.renorm = renorm
         ctx.save_for_backward(coef, *logits, *ids, *masks)
-        ctx.mark_non_differentiable(coef, counts, *ids)
         ctx.set_materialize_grads(False)
-        return (loss, coef, counts, *ids, *gates)
+        return (loss, *gates)
 
     @staticmethod
     @once_differentiable
-    def backward(ctx, dloss, dcoef, dcounts, *rest):
+    def backward(ctx, dloss, *dgates):
         coef, *saved = ctx.saved_tensors
-        n = len(saved) // 3
-        dgates = rest[n:]
+        n = len(dgates)
+        if dloss is None:
+            coef = None
         grads = [None] * n
-        for w in range(n):
-            if ctx.needs_input_grad[4 + w] and (dloss is not None or dgates[w] is not None):
-                dg = None if dgates[w] is None else dgates[w].contiguous()
-                grads[w] = dq.route_backward(saved[w], saved[n + w], dg, None if dloss is None else coef, dloss,
-                                             ctx.renorm, saved[2 * n + w])
-        return (None, None, None, None, *grads)
+        for w, dg in enumerate(dgates):
+            if ctx.needs_input_grad[5 + w] and (dloss is not None or dg is not None):
+                if dg is not None and not dg.is_contiguous():
+                    dg = dg.contiguous()
+                grads[w] = dq.route_backward(saved[w], saved[n + w], dg, coef, dloss, ctx.renorm, saved[2 * n + w])
+        return (None, None, None, None, None, *grads)
 
 
 def route(logits, top_k, renorm=True, masks=None, reduce=None):
@@ -107,12 +111,14 @@ def route(logits, top_k, renorm=True, masks=None, reduce=None):
     are to be summed, not averaged)."""
     one = isinstance(logits, torch.Tensor)
     ls = [logits] if one else list(logits)
-    ms = [masks] * len(ls) if masks is None else [masks] if one else list(masks)
+    ms = [masks] * len(ls) if masks is None or one else list(masks)
     if not ls or len(ms) != len(ls):
         raise ValueError(f"{len(ls)} logits with {len(ms)} masks")
-    shapes = {(l.size(-1), l.device) for l in ls}
-    if len(shapes) != 1:
-        raise ValueError(f"the workers' logits differ in experts or device: {sorted(map(str, shapes))}")
-    loss, coef, counts, *rest = _Route.apply(top_k, renorm, ms, reduce, *ls)
-    ids, gates = rest[:len(ls)], rest[len(ls):]
+    for l in ls[1:]:
+        if l.size(-1) != ls[0].size(-1) or l.device != ls[0].device:
+            raise ValueError(f"the workers' logits differ in experts or device: {tuple(l.shape)} on {l.device}, "
+                             f"{tuple(ls[0].shape)} on {ls[0].device}")
+    found = []
+    loss, *gates = _Route.apply(top_k, renorm, ms, reduce, found, *ls)
+    ids, counts, coef = found
     return Routing(ids[0] if one else ids, gates[0] if one else gates, loss, counts, coef)
