@@ -355,73 +355,16 @@ __device__ __forceinline__ double wave_sum(double v, int from = 32) {
     return v;
 }
 
-// Folds the parts and computes the loss, every sum in a fixed order.  A block
-// of 16 waves takes 16 experts, 64 threads for each over the rows; where there
-// are few rows one block takes all experts, a thread each.  The last of several
-// blocks to finish adds up their shares of the loss.
-template <bool ONE>
-__global__ __launch_bounds__(1024) void k_balance(BalanceArgs a) {
-    constexpr int COLUMNS = ONE ? kRouteMaxExperts : kBalanceColumns;
-    __shared__ double ps[16][16], cs[16][16], ts[16];
-    const int i = threadIdx.x, lane = i & 63, wave = i >> 6;
-    const int j = ONE ? i : (int)blockIdx.x * COLUMNS + i % COLUMNS;
-    const double sum_n = a.sums ? a.sums[2 * a.E] : 0.0;
-    double p = 0.0, n = 0.0, t = 0.0;
-    // rows in groups of U whose loads are all in flight before the first is added
-    constexpr int STEP = ONE ? 1 : 1024 / COLUMNS, U = 12;
-    const int col = j < a.E ? j : 0;
-    for (int q = 0; q < a.parts; q++) {
-        const RoutePart &part = a.part[q];
-        const int rows = part.nblk;
-        for (int b0 = ONE ? 0 : i / COLUMNS; b0 < rows; b0 += U * STEP) {
-            float x[U];
-            uint32_t m[U];
-#pragma unroll
-            for (int u = 0; u < U; u++) {
-                const int at = min(b0 + u * STEP, rows - 1) * a.E + col;
-                x[u] = part.psum[at];
-                m[u] = part.count[at];
-            }
-#pragma unroll
-            for (int u = 0; u < U; u++) {
-                const bool there = b0 + u * STEP < rows;
-                p += there ? x[u] : 0.0f;
-                n += there ? m[u] : 0u;
-            }
-        }
-        for (int b = i; b < rows; b += 1024) t += part.routed[b];
-    }
-    t = wave_sum(t);
-    if (!ONE) {
-        p += __shfl_xor(p, 32, 64);
-        p += __shfl_xor(p, 16, 64);
-        n += __shfl_xor(n, 32, 64);
-        n += __shfl_xor(n, 16, 64);
-        if (lane < 16) {
-            ps[wave][lane] = p;
-            cs[wave][lane] = n;
-        }
-    }
-    if (lane == 0) ts[wave] = t;
-    __syncthreads();
-    if (!ONE && wave != 0) return;
-    double N = sum_n;
-    for (int w = 0; w < 16; w++) N += ts[w];
-    if (!ONE) {
-        // lane c adds up the waves w, w + 4, .. with w = c / 16
-        p = n = 0.0;
-        for (int w = lane / 16; w < 16; w += 4) {
-            p += ps[w][lane % 16];
-            n += cs[w][lane % 16];
-        }
-        p += __shfl_xor(p, 32, 64);
-        p += __shfl_xor(p, 16, 64);
-        n += __shfl_xor(n, 32, 64);
-        n += __shfl_xor(n, 16, 64);
-    }
+// The outputs from the folded parts: thread j has expert j's choices n and summed
+// probabilities p of all parts, and all threads the routed tokens N.
+__device__ __forceinline__ void balance_outputs(const BalanceArgs &a, double p, double n, double N) {
+    __shared__ double shares[16];
+    const int j = threadIdx.x;
+    if (a.sums) N += a.sums[2 * a.E];
+    __syncthreads();                  // a.stats may be a.sums, whose last element all threads read
     const double f = N > 0.0 ? (double)a.E / ((double)a.k * N * N) : 0.0;
     double share = 0.0;
-    if ((ONE || lane < 16) && j < a.E) {
+    if (j < a.E) {
         if (a.sums) {
             n += a.sums[j];
             p += a.sums[a.E + j];
@@ -429,37 +372,138 @@ __global__ __launch_bounds__(1024) void k_balance(BalanceArgs a) {
         if (a.stats) {
             a.stats[j] = n;
             a.stats[a.E + j] = p;
+            if (j == 0) a.stats[2 * a.E] = N;
         }
         const double w = f * n;
         if (a.coef) a.coef[j] = (float)w;
         if (a.counts) a.counts[j] = (int64_t)n;
         share = w * p;
     }
-    share = wave_sum(share, ONE ? 32 : 8);
-    if (ONE) {
-        if (lane == 0) ps[0][wave] = share;
-        __syncthreads();
-        share = 0.0;
-        for (int w = 0; w < 16; w++) share += ps[0][w];
-    } else if (gridDim.x > 1) {
-        const RoutePart &first = a.part[0];
-        uint32_t before = 0;
-        if (lane == 0) {
-            __hip_atomic_store(first.share + blockIdx.x, share, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            before = __hip_atomic_fetch_add(first.done, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+    share = wave_sum(share);
+    if ((j & 63) == 0) shares[j >> 6] = share;
+    __syncthreads();
+    if (j == 0 && a.loss) {
+        for (int w = 1; w < 16; w++) share += shares[w];
+        *a.loss = (float)share;
+    }
+}
+
+// Sums column `col` of a part's rows first, first + step, ..: in groups of U rows
+// whose loads are all in flight before the first is added.
+template <int U>
+__device__ __forceinline__ void fold_rows(const RoutePart &part, int E, int col, int first, int step, double &p,
+                                          double &n) {
+    const int rows = part.nblk;
+    for (int b0 = first; b0 < rows; b0 += U * step) {
+        float x[U];
+        uint32_t m[U];
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            const int at = min(b0 + u * step, rows - 1) * E + col;
+            x[u] = part.psum[at];
+            m[u] = part.count[at];
         }
-        if (__builtin_amdgcn_readfirstlane(before) != gridDim.x - 1) return;
-        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
-        share = lane < (int)gridDim.x ? __hip_atomic_load(first.share + lane, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)
-                                      : 0.0;
-        share = wave_sum(share);
-        if (lane == 0) *first.done = 0;
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            const bool there = b0 + u * step < rows;
+            p += there ? x[u] : 0.0f;
+            n += there ? m[u] : 0u;
+        }
     }
-    // a.stats may be a.sums, whose last element every block reads
-    if (i == 0) {
-        if (a.loss) *a.loss = (float)share;
-        if (a.stats) a.stats[2 * a.E] = N;
+}
+
+// Few rows: one block for all parts, C >= E columns (a power of two) of 1024 / C
+// threads.
+__global__ __launch_bounds__(1024) void k_balance_few(BalanceArgs a, int C) {
+    __shared__ double ps[1024], cs[1024], ts[16];
+    const int i = threadIdx.x, j = i & (C - 1), col = j < a.E ? j : 0;
+    double p = 0.0, n = 0.0, t = 0.0;
+    for (int q = 0; q < a.parts; q++) {
+        for (int b = i; b < a.part[q].nblk; b += 1024) t += a.part[q].routed[b];
+        if (a.part[q].nblk <= 1024 / C) fold_rows<1>(a.part[q], a.E, col, i / C, 1024 / C, p, n);
+        else fold_rows<16>(a.part[q], a.E, col, i / C, 1024 / C, p, n);
     }
+    t = wave_sum(t);
+    ps[i] = p;
+    cs[i] = n;
+    if ((i & 63) == 0) ts[i >> 6] = t;
+    __syncthreads();
+    double N = 0.0;
+    for (int w = 0; w < 16; w++) N += ts[w];
+    if (i < C) {
+#pragma unroll 4
+        for (int r = C; r < 1024; r += C) {
+            p += ps[r + j];
+            n += cs[r + j];
+        }
+    }
+    balance_outputs(a, p, n, N);
+}
+
+// A block of 16 waves folds 16 experts of one part, 64 threads for each over the
+// rows; the last block to finish adds the parts up.  Every sum runs in a fixed
+// order.
+__global__ __launch_bounds__(1024) void k_balance(BalanceArgs a) {
+    constexpr int COLUMNS = kBalanceColumns, STEP = 1024 / COLUMNS;
+    __shared__ double ps[16][COLUMNS], cs[16][COLUMNS], ts[16];
+    __shared__ bool last;
+    const RoutePart &part = a.part[blockIdx.y];
+    const int i = threadIdx.x, lane = i & 63, wave = i >> 6, rows = part.nblk;
+    const int j = (int)blockIdx.x * COLUMNS + i % COLUMNS, col = j < a.E ? j : 0;
+    double p = 0.0, n = 0.0, t = 0.0;
+    fold_rows<16>(part, a.E, col, i / COLUMNS, STEP, p, n);
+    if (blockIdx.x == 0)
+        for (int b = i; b < rows; b += 1024) t += part.routed[b];
+    static_assert(COLUMNS == 16, "lanes 16 apart hold one expert");
+    p += __shfl_xor(p, 32, 64);
+    p += __shfl_xor(p, 16, 64);
+    n += __shfl_xor(n, 32, 64);
+    n += __shfl_xor(n, 16, 64);
+    t = wave_sum(t);
+    if (lane < COLUMNS) {
+        ps[wave][lane] = p;
+        cs[wave][lane] = n;
+    }
+    if (lane == 0) ts[wave] = t;
+    __syncthreads();
+    const auto put = [&](int at, double v) {
+        __hip_atomic_store(part.fold + at, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    };
+    if (i < COLUMNS) {
+        p = n = t = 0.0;
+        for (int w = 0; w < 16; w++) {
+            p += ps[w][i];
+            n += cs[w][i];
+            t += ts[w];
+        }
+        if (j < a.E) {
+            put(j, n);
+            put(a.E + j, p);
+        }
+        if (j == 0) put(2 * a.E, t);
+        // All that passes between blocks goes through agent-scope atomics, which
+        // no cache holds back; they have only to be finished before the count.
+        // (A release fence would also write back the whole L2: 4 us here.)
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        if (i == 0)
+            last = __hip_atomic_fetch_add(a.part[0].done, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+                   gridDim.x * gridDim.y - 1;
+    }
+    __syncthreads();
+    if (!last) return;
+    if (i == 0) __hip_atomic_store(a.part[0].done, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    double N = 0.0;
+    p = n = 0.0;
+    const int e = i < a.E ? i : 0;
+    for (int q = 0; q < a.parts; q++) {
+        const auto get = [&](int at) {
+            return __hip_atomic_load(a.part[q].fold + at, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        };
+        n += get(e);
+        p += get(a.E + e);
+        N += get(2 * a.E);
+    }
+    balance_outputs(a, p, n, N);
 }
 
 template <bool F32, int G, int CH, bool VEC>
@@ -509,14 +553,19 @@ hipError_t launch_route(const RouteArgs &a, int f32, hipStream_t s) {
 }
 
 hipError_t launch_balance(const BalanceArgs &a, hipStream_t s) {
-    static_assert(kRouteMaxExperts / kBalanceColumns <= 64, "a wave adds up the blocks' shares");
+    static_assert(kRouteMaxExperts == 1024, "a block has a thread for each expert");
     int64_t rows = 0;
     for (int q = 0; q < a.parts; q++) rows += a.part[q].nblk;
-    if (rows <= kBalanceFewRows)
-        hipLaunchKernelGGL(k_balance<true>, dim3(1), dim3(1024), 0, s, a);
+    int C = 16;
+    while (C < a.E) C *= 2;
+    // what one block reads in one go (16 rows a thread) needs no second step
+    // between blocks: 256 rows of 64 experts take 6.1 us against 7.1
+    if (rows * C <= 16 * 1024)
+        hipLaunchKernelGGL(k_balance_few, dim3(1), dim3(1024), 0, s, a, C);
     else
-        hipLaunchKernelGGL(k_balance<false>, dim3((unsigned)((a.E + kBalanceColumns - 1) / kBalanceColumns)), dim3(1024),
-                           0, s, a);
+        hipLaunchKernelGGL(k_balance,
+                           dim3((unsigned)((a.E + kBalanceColumns - 1) / kBalanceColumns), (unsigned)a.parts),
+                           dim3(1024), 0, s, a);
     return hipGetLastError();
 }
 

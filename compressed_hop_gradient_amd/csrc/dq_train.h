@@ -27,14 +27,13 @@ struct RoutePart {
     uint32_t *count;        // [nblk][E] choices
     uint32_t *routed;       // [nblk] routed tokens
     int32_t nblk;
-    // scratch of a balance call that folds this part first: blocks that are done
-    // (0 between calls), and their shares of the loss
+    // scratch of a balance call: blocks that are done (of the first part's call; 0
+    // between calls), and this part's folded statistics, double[2 E + 1]
     uint32_t *done;
-    double *share;
+    double *fold;
 };
 constexpr int kRouteMaxParts = 16;
 constexpr int kBalanceColumns = 16;     // experts of a balance block
-constexpr int kBalanceFewRows = 16;     // up to so many rows one block takes all experts
 
 struct RouteArgs {
     const void *logits;

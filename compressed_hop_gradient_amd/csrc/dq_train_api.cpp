@@ -54,8 +54,8 @@ PartAt part_at(void *d_part, int64_t tokens, int32_t E) {
     p.part.psum = reinterpret_cast<float *>(base);
     p.part.count = reinterpret_cast<uint32_t *>(base + (at += row));
     p.part.routed = reinterpret_cast<uint32_t *>(base + (at += row));
-    p.part.share = reinterpret_cast<double *>(base + (at += align_up(4 * n)));
-    p.part.done = reinterpret_cast<uint32_t *>(base + (at += 8 * (kRouteMaxExperts / kBalanceColumns)));
+    p.part.fold = reinterpret_cast<double *>(base + (at += align_up(4 * n)));
+    p.part.done = reinterpret_cast<uint32_t *>(base + (at += align_up(8 * (2 * (size_t)E + 1))));
     p.bytes = at + kAlign;
     return p;
 }
