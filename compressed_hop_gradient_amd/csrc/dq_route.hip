@@ -253,6 +253,20 @@ __device__ __forceinline__ void pick_any(const Slice<F32, G, CH, VEC> &l, uint32
     }
 }
 
+// p = softmax(l), the k largest l, their p (divided by their sum with renorm), and
+// per block the sums over its tokens that the balance loss needs: one pass, a
+// row is read once.  All of it is per lane but four reductions over G lanes.  The
+// probabilities are summed in the lanes' registers over all rows of a block and
+// meet in LDS at its end; choices are counted in LDS.
+//
+// Bound: vector instructions.  131072 x 256 bf16, k = 8, takes 26 us where the
+// 67 MB alone take 13; 671 instructions per 8 tokens, 0.4 of them in sorting and
+// merging, and the VALUs are busy 80% of the time (fp32, 65536 x 256: 21 us, 90%).
+// k = 2 takes 18 us.  Measured and not kept, on the same rows: rows loaded one pass
+// ahead (no faster; the registers cost a wave per SIMD), 4 waves per SIMD where
+// registers then spill (31 us), merging whole lists across lanes instead of
+// taking heads off them (27.4 us), the blocks' sums added by 64-bit atomics
+// (+4 to +10 us).
 template <bool F32, int G, int CH, int KP, bool VEC>
 __global__ __launch_bounds__(256, KP == 16 || CH == 4 || !VEC ? 3 : 4) void k_route(RouteArgs a) {
     typedef typename Elem<F32>::type T;
@@ -442,7 +456,9 @@ __global__ __launch_bounds__(1024) void k_balance_few(BalanceArgs a, int C) {
 
 // A block of 16 waves folds 16 experts of one part, 64 threads for each over the
 // rows; the last block to finish adds the parts up.  Every sum runs in a fixed
-// order.
+// order.  Bound by latency: the rows' loads, the count, the last block's loads.
+// Four parts of 1024 rows by 256 experts (8 MB): 11 us, 23 with a loop over the
+// parts in every block.
 __global__ __launch_bounds__(1024) void k_balance(BalanceArgs a) {
     constexpr int COLUMNS = kBalanceColumns, STEP = 1024 / COLUMNS;
     __shared__ double ps[16][COLUMNS], cs[16][COLUMNS], ts[16];
@@ -516,9 +532,11 @@ hipError_t route_choices(const RouteArgs &a, hipStream_t s) {
     return hipGetLastError();
 }
 
-constexpr int64_t kManyTokens = 32768;
 // The same with longer lists in fewer lanes, for E > 128: fewer steps across
-// lanes per token, but half as many waves
+// lanes per token, but half as many waves.  256 bf16 experts, k = 8: 131072 tokens
+// 29.2 us against 32.7, 8192 tokens 5.0 against 4.5 (fp32 keys take twice the
+// registers: 23.5 against 21.9 us for 65536 tokens).
+constexpr int64_t kManyTokens = 32768;
 template <class F>
 auto by_experts_long(int E, F f) {
     if (E <= 256) return shape<8, 4>(f);

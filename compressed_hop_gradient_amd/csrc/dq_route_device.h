@@ -153,7 +153,10 @@ __device__ __forceinline__ void exponentials(const Slice<F32, G, CH, VEC> &l, fl
     Z = group_sum<G>((z[0] + z[1]) + (z[2] + z[3]));
 }
 
-// Lanes and chunks of a token of E experts: f(G, CH)
+// Lanes and chunks of a token of E experts: f(G, CH).  Measured at E = 256 with
+// 131072 bf16 and 65536 fp32 tokens, k = 8: forward (32, 1) 46.0 and 31.2 us, (16, 2)
+// 32.7 and 21.9, (8, 4) 29.2 and 23.5, (4, 8) 28.5 and 23.8; gradient 40.9 and 30.6,
+// 35.6 and 33.9, 41.7 and 38.9, 44.3 and 55.4.  At E = 64 (8, 1) and (4, 2) are alike.
 template <int G, int CH, class F>
 auto shape(F f) {
     return f(std::integral_constant<int, G>(), std::integral_constant<int, CH>());
