@@ -534,9 +534,9 @@ hipError_t route_choices(const RouteArgs &a, hipStream_t s) {
 
 // The same with longer lists in fewer lanes, for E > 128: fewer steps across
 // lanes per token, but half as many waves.  256 bf16 experts, k = 8: 131072 tokens
-// 29.2 us against 32.7, 8192 tokens 5.0 against 4.5 (fp32 keys take twice the
-// registers: 23.5 against 21.9 us for 65536 tokens).
-constexpr int64_t kManyTokens = 32768;
+// 25.8 us against 30.2, 8192 tokens 4.23 against 4.26, 1024 tokens 3.97 against 3.56
+// (fp32 keys take twice the registers: 24.5 against 21.1 us for 65536 tokens).
+constexpr int64_t kManyTokens = 16384;
 template <class F>
 auto by_experts_long(int E, F f) {
     if (E <= 256) return shape<8, 4>(f);

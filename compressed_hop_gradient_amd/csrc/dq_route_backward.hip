@@ -20,7 +20,7 @@ __device__ __forceinline__ void wave_lds_sync() {
 // their logits are on the way while the softmax is computed.
 //
 // Bound: memory, with the VALUs busy 86% of the time.  131072 x 256 bf16, k = 8
-// (142 MB with the choices): 27 us, 5.2 TB/s; 65536 x 256 fp32: 25 us, 5.7 TB/s; 8192
+// (142 MB with the choices): 27 to 28.5 us, 5.1 TB/s; 65536 x 256 fp32: 25.5 us, 5.5 TB/s; 8192
 // tokens 3.7 and 5.2 us.  All blocks read the same few lines of coef first, which
 // serialises them: with 16 single loads a lane instead of 4 wide ones the same
 // take 33.8, 28.8, 6.9 and 6.7 us.  At most 1024 blocks (4 per CU): each pays for

@@ -154,9 +154,10 @@ __device__ __forceinline__ void exponentials(const Slice<F32, G, CH, VEC> &l, fl
 }
 
 // Lanes and chunks of a token of E experts: f(G, CH).  Measured at E = 256 with
-// 131072 bf16 and 65536 fp32 tokens, k = 8: forward (32, 1) 46.0 and 31.2 us, (16, 2)
-// 32.7 and 21.9, (8, 4) 29.2 and 23.5, (4, 8) 28.5 and 23.8; gradient 40.9 and 30.6,
-// 35.6 and 33.9, 41.7 and 38.9, 44.3 and 55.4.  At E = 64 (8, 1) and (4, 2) are alike.
+// 131072 bf16 and 65536 fp32 tokens, k = 8: forward (32, 1) 39.1 and 28.6 us, (16, 2)
+// 30.2 and 21.1, (8, 4) 25.8 and 24.5; gradient 36.9 and 25.9, 28.5 and 25.7, 29.3 and
+// 27.8.  At E = 64 and 8192 tokens (8, 1) 3.3 and 3.7, (4, 2) 3.9 and 4.5; at 131072
+// bf16 11.4 and 11.0.
 template <int G, int CH, class F>
 auto shape(F f) {
     return f(std::integral_constant<int, G>(), std::integral_constant<int, CH>());
