@@ -268,7 +268,9 @@ __device__ __forceinline__ void pick_any(const Slice<F32, G, CH, VEC> &l, uint32
 // taking heads off them (27.4 us), the blocks' sums added by 64-bit atomics
 // (+4 to +10 us).
 template <bool F32, int G, int CH, int KP, bool VEC>
-__global__ __launch_bounds__(256, KP == 16 || CH == 4 || !VEC ? 3 : 4) void k_route(RouteArgs a) {
+__global__ __launch_bounds__(256, KP == 16 || CH == 4 || !VEC ? 3 : 4) void k_route(RouteArgs args) {
+    const RouteWorker &a = args.worker[blockIdx.y];
+    if ((int)blockIdx.x >= a.part.nblk) return;
     typedef typename Elem<F32>::type T;
     typedef Key<F32> K;
     typedef typename K::type KT;
@@ -286,16 +288,16 @@ __global__ __launch_bounds__(256, KP == 16 || CH == 4 || !VEC ? 3 : 4) void k_ro
     for (int v = 0; v < V; v++) acc[v] = 0.0f;
     uint32_t routed = 0;
     const uint32_t inv = 0xFFFFu ^ (uint32_t)L::expert(0, g);
-    const int64_t step = (int64_t)gridDim.x * R;
+    const int64_t step = (int64_t)a.part.nblk * R;
     int64_t t = (int64_t)blockIdx.x * R + r;
     for (int64_t base = (int64_t)blockIdx.x * R; base < a.tokens; base += step, t += step) {
         L l;
         const int64_t at = t < a.tokens ? t : a.tokens - 1;
-        l.load(static_cast<const T *>(a.logits) + at * a.stride, g, a.E);
+        l.load(static_cast<const T *>(a.logits) + at * a.stride, g, args.E);
         const bool there = t < a.tokens && (!a.mask || a.mask[at]);
-        if (!__all(there) || a.E < C) {
+        if (!__all(there) || args.E < C) {
             asm volatile("; logits that do not exist");
-            l.keep(there, g, a.E);
+            l.keep(there, g, args.E);
         }
         KT mine[S], most;
         pick<KP>(l, inv, g, mine, most);
@@ -308,7 +310,7 @@ __global__ __launch_bounds__(256, KP == 16 || CH == 4 || !VEC ? 3 : 4) void k_ro
         if (__any(odd)) {
             uint32_t start = inv;
             asm volatile("; NaN, or zeros that may tie" : "+v"(start));   // (opaque: no constants of it are kept)
-            pick_any<KP>(l, start, g, a.k, mine);
+            pick_any<KP>(l, start, g, args.k, mine);
         }
         const float by_z = Z == 0.0f ? 0.0f : reciprocal(Z);
         if (g == 0) routed += Z != 0.0f;
@@ -319,18 +321,18 @@ __global__ __launch_bounds__(256, KP == 16 || CH == 4 || !VEC ? 3 : 4) void k_ro
         int id[S];
 #pragma unroll
         for (int s = 0; s < S; s++) {
-            const bool open = s * G + g < a.k && K::open(mine[s]);
+            const bool open = s * G + g < args.k && K::open(mine[s]);
             id[s] = open ? K::index(mine[s]) : -1;
             ge[s] = open ? exponential(K::value(mine[s]), m) : 0.0f;
             top += ge[s];
         }
         // a choice is the row's largest logit, so that the sum is 1 or more
-        const float by = Z != Z ? Z : Z == 0.0f ? 0.0f : a.renorm ? reciprocal(group_sum<G>(top)) : by_z;
+        const float by = Z != Z ? Z : Z == 0.0f ? 0.0f : args.renorm ? reciprocal(group_sum<G>(top)) : by_z;
 #pragma unroll
         for (int s = 0; s < S; s++) {
-            if (s * G + g < a.k && t < a.tokens) {
-                a.ids[t * a.k + s * G + g] = id[s];
-                a.gates[t * a.k + s * G + g] = id[s] < 0 ? 0.0f : ge[s] * by;
+            if (s * G + g < args.k && t < a.tokens) {
+                a.ids[t * args.k + s * G + g] = id[s];
+                a.gates[t * args.k + s * G + g] = id[s] < 0 ? 0.0f : ge[s] * by;
                 if (id[s] >= 0) atomicAdd(&hist[id[s]], 1u);
             }
         }
@@ -353,14 +355,14 @@ __global__ __launch_bounds__(256, KP == 16 || CH == 4 || !VEC ? 3 : 4) void k_ro
             if (part != 0) break;
             for (int i = 1; i < P; i++) sum += sums[i * C + col];
         }
-        if (col < a.E) {
-            a.part.psum[(int)blockIdx.x * a.E + col] = sum;
-            a.part.count[(int)blockIdx.x * a.E + col] = hist[col];
+        if (col < args.E) {
+            a.part.psum()[(int)blockIdx.x * args.E + col] = sum;
+            a.part.count(args.E)[(int)blockIdx.x * args.E + col] = hist[col];
         }
     }
     if (threadIdx.x == 0) {
-        a.part.routed[blockIdx.x] = routed_of[0] + routed_of[1] + routed_of[2] + routed_of[3];
-        if (blockIdx.x == 0) *a.part.done = 0;
+        a.part.routed(args.E)[blockIdx.x] = routed_of[0] + routed_of[1] + routed_of[2] + routed_of[3];
+        if (blockIdx.x == 0) *a.part.done(args.E) = 0;
     }
 }
 
@@ -408,14 +410,16 @@ template <int U>
 __device__ __forceinline__ void fold_rows(const RoutePart &part, int E, int col, int first, int step, double &p,
                                           double &n) {
     const int rows = part.nblk;
+    const float *psum = part.psum();
+    const uint32_t *count = part.count(E);
     for (int b0 = first; b0 < rows; b0 += U * step) {
         float x[U];
         uint32_t m[U];
 #pragma unroll
         for (int u = 0; u < U; u++) {
             const int at = min(b0 + u * step, rows - 1) * E + col;
-            x[u] = part.psum[at];
-            m[u] = part.count[at];
+            x[u] = psum[at];
+            m[u] = count[at];
         }
 #pragma unroll
         for (int u = 0; u < U; u++) {
@@ -433,7 +437,7 @@ __global__ __launch_bounds__(1024) void k_balance_few(BalanceArgs a, int C) {
     const int i = threadIdx.x, j = i & (C - 1), col = j < a.E ? j : 0;
     double p = 0.0, n = 0.0, t = 0.0;
     for (int q = 0; q < a.parts; q++) {
-        for (int b = i; b < a.part[q].nblk; b += 1024) t += a.part[q].routed[b];
+        for (int b = i; b < a.part[q].nblk; b += 1024) t += a.part[q].routed(a.E)[b];
         if (a.part[q].nblk <= 1024 / C) fold_rows<1>(a.part[q], a.E, col, i / C, 1024 / C, p, n);
         else fold_rows<16>(a.part[q], a.E, col, i / C, 1024 / C, p, n);
     }
@@ -469,7 +473,7 @@ __global__ __launch_bounds__(1024) void k_balance(BalanceArgs a) {
     double p = 0.0, n = 0.0, t = 0.0;
     fold_rows<16>(part, a.E, col, i / COLUMNS, STEP, p, n);
     if (blockIdx.x == 0)
-        for (int b = i; b < rows; b += 1024) t += part.routed[b];
+        for (int b = i; b < rows; b += 1024) t += part.routed(a.E)[b];
     static_assert(COLUMNS == 16, "lanes 16 apart hold one expert");
     p += __shfl_xor(p, 32, 64);
     p += __shfl_xor(p, 16, 64);
@@ -483,7 +487,7 @@ __global__ __launch_bounds__(1024) void k_balance(BalanceArgs a) {
     if (lane == 0) ts[wave] = t;
     __syncthreads();
     const auto put = [&](int at, double v) {
-        __hip_atomic_store(part.fold + at, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        __hip_atomic_store(part.fold(a.E) + at, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     };
     if (i < COLUMNS) {
         p = n = t = 0.0;
@@ -502,18 +506,18 @@ __global__ __launch_bounds__(1024) void k_balance(BalanceArgs a) {
         // (A release fence would also write back the whole L2: 4 us here.)
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         if (i == 0)
-            last = __hip_atomic_fetch_add(a.part[0].done, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+            last = __hip_atomic_fetch_add(a.part[0].done(a.E), 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
                    gridDim.x * gridDim.y - 1;
     }
     __syncthreads();
     if (!last) return;
-    if (i == 0) __hip_atomic_store(a.part[0].done, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (i == 0) __hip_atomic_store(a.part[0].done(a.E), 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     double N = 0.0;
     p = n = 0.0;
     const int e = i < a.E ? i : 0;
     for (int q = 0; q < a.parts; q++) {
         const auto get = [&](int at) {
-            return __hip_atomic_load(a.part[q].fold + at, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            return __hip_atomic_load(a.part[q].fold(a.E) + at, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         };
         n += get(e);
         p += get(a.E + e);
@@ -524,7 +528,9 @@ __global__ __launch_bounds__(1024) void k_balance(BalanceArgs a) {
 
 template <bool F32, int G, int CH, bool VEC>
 hipError_t route_choices(const RouteArgs &a, hipStream_t s) {
-    const dim3 grid((unsigned)a.part.nblk), block(256);
+    int most = 1;
+    for (int w = 0; w < a.workers; w++) most = a.worker[w].part.nblk > most ? a.worker[w].part.nblk : most;
+    const dim3 grid((unsigned)most, (unsigned)a.workers), block(256);
     if (a.k <= 2) hipLaunchKernelGGL((k_route<F32, G, CH, 2, VEC>), grid, block, 0, s, a);
     else if (a.k <= 4) hipLaunchKernelGGL((k_route<F32, G, CH, 4, VEC>), grid, block, 0, s, a);
     else if (a.k <= 8 || G * CH == 1) hipLaunchKernelGGL((k_route<F32, G, CH, 8, VEC>), grid, block, 0, s, a);
@@ -546,9 +552,14 @@ auto by_experts_long(int E, F f) {
 
 template <bool F32>
 hipError_t route_experts(const RouteArgs &a, hipStream_t s) {
-    const bool vec = rows_on_16(a.logits, a.stride, a.E, F32);
+    bool vec = true;
+    int64_t tokens = 0;
+    for (int w = 0; w < a.workers; w++) {
+        vec = vec && rows_on_16(a.worker[w].logits, a.worker[w].stride, a.E, F32);
+        tokens += a.worker[w].tokens;
+    }
     if constexpr (!F32)
-        if (vec && a.E > 128 && a.tokens >= kManyTokens)
+        if (vec && a.E > 128 && tokens >= kManyTokens)
             return by_experts_long(a.E, [&](auto G, auto CH) { return route_choices<F32, G.value, CH.value, true>(a, s); });
     return by_experts(a.E, [&](auto G, auto CH) {
         return vec ? route_choices<F32, G.value, CH.value, true>(a, s)

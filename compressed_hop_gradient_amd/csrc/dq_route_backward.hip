@@ -26,11 +26,13 @@ __device__ __forceinline__ void wave_lds_sync() {
 // take 33.8, 28.8, 6.9 and 6.7 us.  At most 1024 blocks (4 per CU): each pays for
 // its start (2048: 28.1 and 25.5 us).
 template <bool F32, int G, int CH, int S, bool VEC>
-__global__ __launch_bounds__(256) void k_route_backward(RouteBackwardArgs a) {
+__global__ __launch_bounds__(256) void k_route_backward(RouteBackwardArgs args) {
+    const RouteBackwardWorker &a = args.worker[blockIdx.y];
     typedef Elem<F32> El;
     typedef typename El::type T;
     typedef Slice<F32, G, CH, VEC> L;
     constexpr int V = L::V, W = L::W, C = V * G, R = 256 / G;
+    if ((int64_t)blockIdx.x * R >= a.tokens) return;
     __shared__ alignas(16) float rows[R * C];
     const int g = threadIdx.x % G, r = threadIdx.x / G;
     float *h = rows + r * C;
@@ -44,12 +46,12 @@ __global__ __launch_bounds__(256) void k_route_backward(RouteBackwardArgs a) {
     // lane g holds choices g, g + G, ..; nothing waits for these loads
     const auto load = [&](Row &row, int64_t t) {
         if (t >= a.tokens) t = a.tokens - 1;
-        row.l.load(logits + t * a.stride, g, a.E);
+        row.l.load(logits + t * a.stride, g, args.E);
         row.mask = 1;
         if (a.mask) row.mask = a.mask[t];
 #pragma unroll
         for (int s = 0; s < S; s++) {
-            const int64_t at = t * a.k + (s * G + g < a.k ? s * G + g : 0);
+            const int64_t at = t * args.k + (s * G + g < args.k ? s * G + g : 0);
             row.id[s] = -1;
             row.dg[s] = 0.0f;
             if (a.dgates) {
@@ -64,20 +66,20 @@ __global__ __launch_bounds__(256) void k_route_backward(RouteBackwardArgs a) {
     load(next, t);
     // dloss coef of the lane's experts; loads of all of them in flight at once
     float up[V];
-    const float w = a.coef ? (a.dloss ? *a.dloss : 1.0f) : 0.0f;
-    if (VEC && a.coef && reinterpret_cast<uintptr_t>(a.coef) % 16 == 0) {
+    const float w = args.coef ? (args.dloss ? *args.dloss : 1.0f) : 0.0f;
+    if (VEC && args.coef && reinterpret_cast<uintptr_t>(args.coef) % 16 == 0) {
 #pragma unroll
         for (int v = 0; v < V; v += 4) {
             const int at = L::expert(v, g);
-            const float4 x = *reinterpret_cast<const float4 *>(a.coef + (at < a.E ? at : 0));
+            const float4 x = *reinterpret_cast<const float4 *>(args.coef + (at < args.E ? at : 0));
             up[v] = x.x;
             up[v + 1] = x.y;
             up[v + 2] = x.z;
             up[v + 3] = x.w;
         }
-    } else if (a.coef) {
+    } else if (args.coef) {
 #pragma unroll
-        for (int v = 0; v < V; v++) up[v] = a.coef[min(L::expert(v, g), a.E - 1)];
+        for (int v = 0; v < V; v++) up[v] = args.coef[min(L::expert(v, g), args.E - 1)];
     } else {
 #pragma unroll
         for (int v = 0; v < V; v++) up[v] = 0.0f;
@@ -94,11 +96,11 @@ __global__ __launch_bounds__(256) void k_route_backward(RouteBackwardArgs a) {
         typename El::type ls[S];
 #pragma unroll
         for (int s = 0; s < S; s++) {
-            if (!there || s * G + g >= a.k || (uint32_t)row.id[s] >= (uint32_t)a.E) row.id[s] = -1;
+            if (!there || s * G + g >= args.k || (uint32_t)row.id[s] >= (uint32_t)args.E) row.id[s] = -1;
             ls[s] = logits[(t < a.tokens ? t : a.tokens - 1) * a.stride + (row.id[s] < 0 ? 0 : row.id[s])];
         }
         if (base + step < a.tokens) load(next, t + step);
-        row.l.keep(there, g, a.E);
+        row.l.keep(there, g, args.E);
         float m = -INFINITY, e[V], Z;
 #pragma unroll
         for (int v = 0; v < V; v++) m = fmaxf(m, row.l.at(v));
@@ -116,7 +118,7 @@ __global__ __launch_bounds__(256) void k_route_backward(RouteBackwardArgs a) {
             top += gs[s];
         }
         float by = inv;
-        if (a.renorm) {
+        if (args.renorm) {
             top = group_sum<G>(top);
             by = top == 0.0f ? 0.0f : 1.0f / top;      // no choice
         }
@@ -128,10 +130,10 @@ __global__ __launch_bounds__(256) void k_route_backward(RouteBackwardArgs a) {
         gd = group_sum<G>(gd);
         // p (a - D) = e (a / Z - D / Z)
         float dot = inv * group_sum<G>((dots[0] + dots[1]) + (dots[2] + dots[3]));
-        dot = -inv * (dot + (a.renorm ? 0.0f : gd));
+        dot = -inv * (dot + (args.renorm ? 0.0f : gd));
 #pragma unroll
         for (int s = 0; s < S; s++)
-            if (row.id[s] >= 0) h[row.id[s]] = gs[s] * (a.renorm ? row.dg[s] - gd : row.dg[s]);
+            if (row.id[s] >= 0) h[row.id[s]] = gs[s] * (args.renorm ? row.dg[s] - gd : row.dg[s]);
         wave_lds_sync();
         // the next row is waited for here: after the stores below it would be
         // waited for together with them
@@ -148,7 +150,7 @@ __global__ __launch_bounds__(256) void k_route_backward(RouteBackwardArgs a) {
 #pragma unroll
                 for (int j = 0; j < W; j++)
                     d[j] = __builtin_fmaf(e[W * i + j], __builtin_fmaf(up[W * i + j], inv, dot), d[j]);
-                if (at < a.E) L::C::store(out + at, d);
+                if (at < args.E) L::C::store(out + at, d);
             }
         }
         wave_lds_sync();
@@ -163,8 +165,11 @@ hipError_t backward_choices(const RouteBackwardArgs &a, hipStream_t s) {
     // choices of a lane: at most all of 8 experts in one lane
     constexpr int R = 256 / G, most = G == 1 ? 8 : G < kRouteMaxTopK ? kRouteMaxTopK / G : 1;
     static_assert(G > 1 || CH == 1, "");
-    const int64_t want = (a.tokens + R - 1) / R;
-    const dim3 grid((unsigned)(want < 1024 ? want : 1024)), block(256);
+    int64_t want = 0;
+    for (int w = 0; w < a.workers; w++) want = a.worker[w].tokens > want ? a.worker[w].tokens : want;
+    want = (want + R - 1) / R;
+    const int64_t blocks = 1024 / a.workers;
+    const dim3 grid((unsigned)(want < blocks ? want : blocks), (unsigned)a.workers), block(256);
     const int each = (a.k + G - 1) / G;
     if (each <= 1 || most == 1) hipLaunchKernelGGL((k_route_backward<F32, G, CH, 1, VEC>), grid, block, 0, s, a);
     else if (each <= 2 || most == 2)
@@ -177,7 +182,10 @@ hipError_t backward_choices(const RouteBackwardArgs &a, hipStream_t s) {
 
 template <bool F32>
 hipError_t backward_experts(const RouteBackwardArgs &a, hipStream_t s) {
-    const bool vec = rows_on_16(a.logits, a.stride, a.E, F32) && rows_on_16(a.dlogits, a.dstride, a.E, F32);
+    bool vec = true;
+    for (int w = 0; w < a.workers; w++)
+        vec = vec && rows_on_16(a.worker[w].logits, a.worker[w].stride, a.E, F32) &&
+              rows_on_16(a.worker[w].dlogits, a.worker[w].dstride, a.E, F32);
     return by_experts(a.E, [&](auto G, auto CH) {
         return vec ? backward_choices<F32, G.value, CH.value, true>(a, s)
                    : backward_choices<F32, G.value, CH.value, false>(a, s);

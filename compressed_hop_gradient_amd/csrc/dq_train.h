@@ -21,29 +21,44 @@ struct DropoutArgs {
     const uint32_t *d_round;
 };
 
-// Statistics of one router call: a row per block of its kernel.
+// Statistics of one worker's tokens, in the caller's buffer: a row per block of
+// the router's kernel, then the scratch of a balance call.
 struct RoutePart {
-    float *psum;            // [nblk][E] summed probabilities
-    uint32_t *count;        // [nblk][E] choices
-    uint32_t *routed;       // [nblk] routed tokens
+    uint8_t *base;
     int32_t nblk;
-    // scratch of a balance call: blocks that are done (of the first part's call; 0
-    // between calls), and this part's folded statistics, double[2 E + 1]
-    uint32_t *done;
-    double *fold;
+    static __host__ __device__ size_t up(size_t x) { return (x + 255) / 256 * 256; }
+    __host__ __device__ size_t table(int E) const { return up(4 * (size_t)nblk * (size_t)E); }
+    // [nblk][E] summed probabilities, [nblk][E] choices, [nblk] routed tokens
+    __host__ __device__ float *psum() const { return reinterpret_cast<float *>(base); }
+    __host__ __device__ uint32_t *count(int E) const { return reinterpret_cast<uint32_t *>(base + table(E)); }
+    __host__ __device__ uint32_t *routed(int E) const { return reinterpret_cast<uint32_t *>(base + 2 * table(E)); }
+    // the part folded, double[2 E + 1], and blocks that are done (of the call
+    // whose first part this is; 0 between calls)
+    __host__ __device__ size_t fold_at(int E) const { return 2 * table(E) + up(4 * (size_t)nblk); }
+    __host__ __device__ size_t done_at(int E) const { return fold_at(E) + up(8 * (2 * (size_t)E + 1)); }
+    __host__ __device__ double *fold(int E) const { return reinterpret_cast<double *>(base + fold_at(E)); }
+    __host__ __device__ uint32_t *done(int E) const { return reinterpret_cast<uint32_t *>(base + done_at(E)); }
+    size_t bytes(int E) const { return done_at(E) + 256; }
 };
 constexpr int kRouteMaxParts = 16;
 constexpr int kBalanceColumns = 16;     // experts of a balance block
 
-struct RouteArgs {
+// One worker's tokens in a router launch; the launch's workers are the second
+// dimension of the grid.  Four of them: arguments of 2 KB for sixteen would make
+// every launch, of one worker too, 1.2 us longer on the host.
+constexpr int kRouteGroup = 4;
+struct RouteWorker {
     const void *logits;
     int64_t tokens, stride;
-    int32_t E, k;
     const uint8_t *mask;
-    int32_t renorm;
     int32_t *ids;
     float *gates;
     RoutePart part;              // out: nblk rows of partial statistics
+};
+struct RouteArgs {
+    RouteWorker worker[kRouteGroup];
+    int32_t workers;
+    int32_t E, k, renorm;
 };
 
 struct BalanceArgs {
@@ -56,15 +71,19 @@ struct BalanceArgs {
     int64_t *counts;
 };
 
-struct RouteBackwardArgs {
+struct RouteBackwardWorker {
     const void *logits;
     int64_t tokens, stride, dstride;
-    int32_t E, k;
     const uint8_t *mask;
-    int32_t renorm;
     const int32_t *ids;
-    const float *dgates, *coef, *dloss;
+    const float *dgates;
     void *dlogits;
+};
+struct RouteBackwardArgs {
+    RouteBackwardWorker worker[kRouteGroup];
+    int32_t workers;
+    int32_t E, k, renorm;
+    const float *coef, *dloss;
 };
 
 hipError_t launch_dropout(const DropoutArgs &a, int f32, hipStream_t s);

@@ -13,8 +13,6 @@ namespace {
 
 constexpr size_t kAlign = 256;
 
-size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
-
 bool is_kind(int32_t kind) { return kind == DQ_BF16 || kind == DQ_F32; }
 uintptr_t elem_bytes(int32_t kind) { return kind == DQ_F32 ? 4 : 2; }
 bool aligned(const void *p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
@@ -40,24 +38,8 @@ bool clash(const void *out, int64_t os, const void *in, int64_t is, int64_t rows
 
 constexpr int64_t kMostTokens = (int64_t)1 << 40;
 
-// A part's buffer: its rows, then the scratch of a balance call
-struct PartAt {
-    RoutePart part;
-    size_t bytes;
-};
-PartAt part_at(void *d_part, int64_t tokens, int32_t E) {
-    uint8_t *base = static_cast<uint8_t *>(d_part);
-    PartAt p{};
-    p.part.nblk = route_blocks(tokens, E);
-    const size_t n = (size_t)p.part.nblk, row = align_up(4 * n * (size_t)E);
-    size_t at = 0;
-    p.part.psum = reinterpret_cast<float *>(base);
-    p.part.count = reinterpret_cast<uint32_t *>(base + (at += row));
-    p.part.routed = reinterpret_cast<uint32_t *>(base + (at += row));
-    p.part.fold = reinterpret_cast<double *>(base + (at += align_up(4 * n)));
-    p.part.done = reinterpret_cast<uint32_t *>(base + (at += align_up(8 * (2 * (size_t)E + 1))));
-    p.bytes = at + kAlign;
-    return p;
+RoutePart part_at(void *d_part, int64_t tokens, int32_t E) {
+    return RoutePart{static_cast<uint8_t *>(d_part), route_blocks(tokens, E)};
 }
 
 bool bad_router(int32_t kind, int64_t tokens, int32_t E, int64_t stride, int32_t k) {
@@ -112,27 +94,37 @@ dq_status dq_dropout(const void *x, const void *residual, void *y, int32_t kind,
 
 size_t dq_route_part_bytes(int64_t tokens, int32_t E) {
     if (tokens < 0 || tokens > kMostTokens || E < 1 || E > kRouteMaxExperts) return 0;
-    return part_at(nullptr, tokens, E).bytes;
+    return part_at(nullptr, tokens, E).bytes(E);
 }
 
-dq_status dq_route(const void *logits, int32_t kind, int64_t tokens, int32_t E, int64_t stride, const uint8_t *mask,
-                   int32_t k, int32_t flags, int32_t *ids, float *gates, void *part, size_t part_bytes, void *stream) {
-    if (bad_router(kind, tokens, E, stride, k) || (flags & ~DQ_ROUTE_RENORM)) return DQ_EINVAL;
-    if (tokens > 0 && (!logits || !ids || !gates)) return DQ_ENULL;
-    if (!aligned(logits, elem_bytes(kind)) || !aligned(ids, 4) || !aligned(gates, 4)) return DQ_EINVAL;
-    if (!part || !aligned(part, kAlign) || part_bytes < dq_route_part_bytes(tokens, E)) return DQ_EWORKSPACE;
+dq_status dq_route(const dq_route_worker *workers, int32_t n, int32_t kind, int32_t E, int32_t k, int32_t flags,
+                   void *stream) {
+    if (n < 0 || (flags & ~DQ_ROUTE_RENORM) || bad_router(kind, 0, E, 0, k)) return DQ_EINVAL;
+    if (n > 0 && !workers) return DQ_ENULL;
+    for (int32_t w = 0; w < n; w++) {
+        const dq_route_worker &in = workers[w];
+        if (bad_router(kind, in.tokens, E, in.stride, k)) return DQ_EINVAL;
+        if (in.tokens > 0 && (!in.d_logits || !in.d_ids || !in.d_gates)) return DQ_ENULL;
+        if (!aligned(in.d_logits, elem_bytes(kind)) || !aligned(in.d_ids, 4) || !aligned(in.d_gates, 4))
+            return DQ_EINVAL;
+        if (!in.d_part || !aligned(in.d_part, kAlign) || in.part_bytes < dq_route_part_bytes(in.tokens, E))
+            return DQ_EWORKSPACE;
+    }
     RouteArgs a{};
-    a.logits = logits;
-    a.tokens = tokens;
-    a.stride = stride;
     a.E = E;
     a.k = k;
-    a.mask = mask;
     a.renorm = (flags & DQ_ROUTE_RENORM) != 0;
-    a.ids = ids;
-    a.gates = gates;
-    a.part = part_at(part, tokens, E).part;
-    return hip_status(launch_route(a, kind == DQ_F32, static_cast<hipStream_t>(stream)));
+    for (int32_t w = 0; w < n; w++) {
+        const dq_route_worker &in = workers[w];
+        a.worker[a.workers++] = RouteWorker{in.d_logits, in.tokens, in.stride, in.d_mask, in.d_ids, in.d_gates,
+                                            part_at(in.d_part, in.tokens, E)};
+        if (a.workers == kRouteGroup || w == n - 1) {
+            const hipError_t e = launch_route(a, kind == DQ_F32, static_cast<hipStream_t>(stream));
+            if (e != hipSuccess) return hip_status(e);
+            a.workers = 0;
+        }
+    }
+    return DQ_OK;
 }
 
 dq_status dq_balance(const dq_route_part *parts, int32_t n_parts, const double *sums, int32_t E, int32_t k,
@@ -148,7 +140,7 @@ dq_status dq_balance(const dq_route_part *parts, int32_t n_parts, const double *
         if (parts[q].tokens < 0 || parts[q].tokens > kMostTokens) return DQ_EINVAL;
         if (!parts[q].d_part) return DQ_ENULL;
         if (!aligned(parts[q].d_part, kAlign)) return DQ_EINVAL;
-        a.part[q] = part_at(parts[q].d_part, parts[q].tokens, E).part;
+        a.part[q] = part_at(parts[q].d_part, parts[q].tokens, E);
     }
     a.sums = sums;
     a.E = E;
@@ -160,33 +152,41 @@ dq_status dq_balance(const dq_route_part *parts, int32_t n_parts, const double *
     return hip_status(launch_balance(a, static_cast<hipStream_t>(stream)));
 }
 
-dq_status dq_route_backward(const void *logits, int32_t kind, int64_t tokens, int32_t E, int64_t stride,
-                            const uint8_t *mask, int32_t k, int32_t flags, const int32_t *ids, const float *dgates,
-                            const float *coef, const float *dloss, void *dlogits, int64_t dstride, void *stream) {
-    if (bad_router(kind, tokens, E, stride, k) || (flags & ~DQ_ROUTE_RENORM)) return DQ_EINVAL;
-    if (dstride > ((int64_t)1 << 40) || (tokens > 1 && dstride < E)) return DQ_EINVAL;
-    if (tokens == 0) return DQ_OK;
-    if (!logits || !ids || !dlogits) return DQ_ENULL;
+dq_status dq_route_backward(const dq_route_grad *workers, int32_t n, int32_t kind, int32_t E, int32_t k,
+                            int32_t flags, const float *coef, const float *dloss, void *stream) {
+    if (n < 0 || (flags & ~DQ_ROUTE_RENORM) || bad_router(kind, 0, E, 0, k)) return DQ_EINVAL;
+    if (!aligned(coef, 4) || !aligned(dloss, 4)) return DQ_EINVAL;
+    if (n > 0 && !workers) return DQ_ENULL;
     const uintptr_t es = elem_bytes(kind);
-    if (!aligned(logits, es) || !aligned(dlogits, es) || !aligned(ids, 4) || !aligned(dgates, 4) ||
-        !aligned(coef, 4) || !aligned(dloss, 4))
-        return DQ_EINVAL;
-    if (clash(dlogits, dstride, logits, stride, tokens, E, (int64_t)es)) return DQ_EINVAL;
+    for (int32_t w = 0; w < n; w++) {
+        const dq_route_grad &in = workers[w];
+        if (bad_router(kind, in.tokens, E, in.stride, k)) return DQ_EINVAL;
+        if (in.dstride > kMostTokens || (in.tokens > 1 && in.dstride < E)) return DQ_EINVAL;
+        if (in.tokens == 0) continue;
+        if (!in.d_logits || !in.d_ids || !in.d_dlogits) return DQ_ENULL;
+        if (!aligned(in.d_logits, es) || !aligned(in.d_dlogits, es) || !aligned(in.d_ids, 4) ||
+            !aligned(in.d_dgates, 4))
+            return DQ_EINVAL;
+        if (clash(in.d_dlogits, in.dstride, in.d_logits, in.stride, in.tokens, E, (int64_t)es)) return DQ_EINVAL;
+    }
     RouteBackwardArgs a{};
-    a.logits = logits;
-    a.tokens = tokens;
-    a.stride = stride;
-    a.dstride = dstride;
     a.E = E;
     a.k = k;
-    a.mask = mask;
     a.renorm = (flags & DQ_ROUTE_RENORM) != 0;
-    a.ids = ids;
-    a.dgates = dgates;
     a.coef = coef;
     a.dloss = dloss;
-    a.dlogits = dlogits;
-    return hip_status(launch_route_backward(a, kind == DQ_F32, static_cast<hipStream_t>(stream)));
+    for (int32_t w = 0; w < n; w++) {
+        const dq_route_grad &in = workers[w];
+        if (in.tokens > 0)
+            a.worker[a.workers++] = RouteBackwardWorker{in.d_logits, in.tokens, in.stride, in.dstride,
+                                                        in.d_mask, in.d_ids, in.d_dgates, in.d_dlogits};
+        if (a.workers == kRouteGroup || (w == n - 1 && a.workers > 0)) {
+            const hipError_t e = launch_route_backward(a, kind == DQ_F32, static_cast<hipStream_t>(stream));
+            if (e != hipSuccess) return hip_status(e);
+            a.workers = 0;
+        }
+    }
+    return DQ_OK;
 }
 
 }  // extern "C"

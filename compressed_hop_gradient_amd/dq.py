@@ -50,6 +50,16 @@ class dq_timing(C.Structure):
                 ("coords", C.c_int64 * len(KERNEL_KINDS))]
 
 
+class dq_route_worker(C.Structure):
+    _fields_ = [("d_logits", C.c_void_p), ("tokens", C.c_int64), ("stride", C.c_int64), ("d_mask", C.c_void_p),
+                ("d_ids", C.c_void_p), ("d_gates", C.c_void_p), ("d_part", C.c_void_p), ("part_bytes", C.c_size_t)]
+
+
+class dq_route_grad(C.Structure):
+    _fields_ = [("d_logits", C.c_void_p), ("tokens", C.c_int64), ("stride", C.c_int64), ("d_mask", C.c_void_p),
+                ("d_ids", C.c_void_p), ("d_dgates", C.c_void_p), ("d_dlogits", C.c_void_p), ("dstride", C.c_int64)]
+
+
 class dq_route_part(C.Structure):
     _fields_ = [("d_part", C.c_void_p), ("tokens", C.c_int64)]
 
@@ -103,13 +113,11 @@ _SIGS = {
                              C.c_int64, C.c_int64, C.c_double, C.c_uint64, C.c_uint32, C.c_void_p,
                              C.c_int32, C.c_uint32, C.c_void_p]),
     "dq_route_part_bytes": (C.c_size_t, [C.c_int64, C.c_int32]),
-    "dq_route": (C.c_int, [C.c_void_p, C.c_int32, C.c_int64, C.c_int32, C.c_int64, C.c_void_p, C.c_int32,
-                           C.c_int32, C.c_void_p, C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p]),
+    "dq_route": (C.c_int, [C.c_void_p, C.c_int32, C.c_int32, C.c_int32, C.c_int32, C.c_int32, C.c_void_p]),
     "dq_balance": (C.c_int, [C.c_void_p, C.c_int32, C.c_void_p, C.c_int32, C.c_int32, C.c_void_p, C.c_void_p,
                              C.c_void_p, C.c_void_p, C.c_void_p]),
-    "dq_route_backward": (C.c_int, [C.c_void_p, C.c_int32, C.c_int64, C.c_int32, C.c_int64, C.c_void_p, C.c_int32,
-                                    C.c_int32, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p,
-                                    C.c_int64, C.c_void_p]),
+    "dq_route_backward": (C.c_int, [C.c_void_p, C.c_int32, C.c_int32, C.c_int32, C.c_int32, C.c_int32, C.c_void_p,
+                                    C.c_void_p, C.c_void_p]),
     "dq_get_info": (C.c_int, [C.c_void_p, C.POINTER(dq_info), C.c_void_p]),
     "dq_timing_read": (C.c_int, [C.c_void_p, C.POINTER(dq_timing)]),
     "dq_status_string": (C.c_char_p, [C.c_int32]),
@@ -361,17 +369,17 @@ class RouteStats:
 
     def __init__(self, experts, device):
         self.experts, self.device = experts, device
-        self.parts = []        # (buffer of dq_route, its tokens)
+        self.parts = []        # (buffer of dq_route, its address, its tokens)
         self.sums = None       # what was folded before them, fp64 [2 experts + 1]
 
-    def _add(self, part, tokens):
+    def _add(self, part, at, tokens):
         if len(self.parts) == ROUTE_MAX_PARTS:
             self.fold()
-        self.parts.append((part, tokens))
+        self.parts.append((part, at, tokens))
 
     def _balance(self, top_k, stats, loss, coef, counts):
         n = len(self.parts)
-        array = (dq_route_part * n)(*[(p.data_ptr(), t) for p, t in self.parts])
+        array = (dq_route_part * n)(*[p[1:] for p in self.parts])
         _call(self.device, "dq_balance", array, n, _opt(self.sums), self.experts, top_k, _opt(stats), _opt(loss),
               _opt(coef), _opt(counts))
 
@@ -394,6 +402,53 @@ def _part_bytes(tokens, experts):
     return lib().dq_route_part_bytes(tokens, experts)
 
 
+def _workers(logits, masks):
+    """The workers' logits and masks as lists, of one dtype, width and device."""
+    masks = [None] * len(logits) if masks is None else masks
+    if not logits or len(masks) != len(logits):
+        raise ValueError(f"{len(logits)} logits with {len(masks)} masks")
+    first = _logits(logits[0])
+    for l in logits[1:]:
+        if _logits(l).size(1) != first.size(1) or l.dtype != first.dtype or l.device != first.device:
+            raise ValueError(f"the workers' logits differ: {tuple(l.shape)} {l.dtype} on {l.device}, "
+                             f"{tuple(first.shape)} {first.dtype} on {first.device}")
+    return masks
+
+
+def _side_by_side(tokens, width, dtype, dev):
+    """A [tokens, width] tensor per worker, in one buffer."""
+    if len(tokens) == 1:
+        return [torch.empty((tokens[0], width), dtype=dtype, device=dev)]
+    return list(torch.empty((sum(tokens), width), dtype=dtype, device=dev).split(tokens))
+
+
+def _results(given, tokens, width, what, dtype, dev):
+    """The caller's buffers for a [tokens, width] result of each worker, or new
+    ones."""
+    if given is None:
+        return _side_by_side(tokens, width, dtype, dev)
+    if len(given) != len(tokens):
+        raise ValueError(f"{len(given)} {what} for {len(tokens)} workers")
+    return [_result(t, (n, width), what, dtype, dev) for t, n in zip(given, tokens)]
+
+
+def _route_stats(stats, logits, top_k):
+    if top_k < 1:
+        raise ValueError(f"top_k {top_k}")
+    if stats is None:
+        return RouteStats(logits.size(1), logits.device)
+    if not isinstance(stats, RouteStats):
+        raise TypeError(f"stats: expected a RouteStats, got {type(stats).__name__}")
+    if stats.experts != logits.size(1) or stats.device != logits.device:
+        raise ValueError(f"stats of {stats.experts} experts on {stats.device}, "
+                         f"logits of {logits.size(1)} on {logits.device}")
+    return stats
+
+
+def _route(io, n, logits, top_k, renorm, stats):
+    _call(stats.device, "dq_route", io, n, _kind(logits), stats.experts, top_k, ROUTE_RENORM if renorm else 0)
+
+
 @_on_stream
 def route(logits, top_k, renorm=True, mask=None, stats=None, ids=None, gates=None):
     """Expert choice of every token (``dq_route``): returns (ids, gates, stats).
@@ -403,25 +458,38 @@ def route(logits, top_k, renorm=True, mask=None, stats=None, ids=None, gates=Non
     ``gates`` fp32, both [tokens, top_k], best choice first; -1 and 0 where a
     token has fewer open experts (logits above -inf).  ``stats`` is a
     :class:`RouteStats` for :func:`balance`: one that is passed in takes these tokens
-    in addition (the workers in rank order)."""
+    in addition (the workers in rank order).
+
+    With lists of the workers' ``logits`` (and ``mask``) one call takes them all, and
+    ``ids`` and ``gates`` are lists."""
+    if isinstance(logits, (list, tuple)):
+        masks = _workers(logits, mask)
+        stats = _route_stats(stats, logits[0], top_k)
+        tokens = [l.size(0) for l in logits]
+        ids = _results(ids, tokens, top_k, "ids", torch.int32, stats.device)
+        gates = _results(gates, tokens, top_k, "gates", torch.float32, stats.device)
+        nbytes = [_part_bytes(t, stats.experts) for t in tokens]
+        part = torch.empty(sum(nbytes), dtype=torch.uint8, device=stats.device)
+        at, io = part.data_ptr(), []
+        for l, t, m, i, g, n in zip(logits, tokens, masks, ids, gates, nbytes):
+            io.append((l.data_ptr(), t, l.stride(0), _token_mask(m, t, stats.device), i.data_ptr(), g.data_ptr(), at, n))
+            at += n
+        _route((dq_route_worker * len(io))(*io), len(io), logits[0], top_k, renorm, stats)
+        for w in io:
+            stats._add(part, w[6], w[1])
+        return ids, gates, stats
     tokens, experts = _logits(logits).shape
     dev = logits.device
-    if stats is None:
-        stats = RouteStats(experts, dev)
-    elif not isinstance(stats, RouteStats):
-        raise TypeError(f"stats: expected a RouteStats, got {type(stats).__name__}")
-    elif stats.experts != experts or stats.device != dev:
-        raise ValueError(f"stats of {stats.experts} experts on {stats.device}, "
-                         f"logits of {experts} on {dev}")
-    shape = (tokens, top_k)
-    ids = _result(ids, shape, "ids", torch.int32, dev)
-    gates = _result(gates, shape, "gates", torch.float32, dev)
+    stats = _route_stats(stats, logits, top_k)
+    ids = _result(ids, (tokens, top_k), "ids", torch.int32, dev)
+    gates = _result(gates, (tokens, top_k), "gates", torch.float32, dev)
     nbytes = _part_bytes(tokens, experts)
     part = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    _call(dev, "dq_route", logits.data_ptr(), _kind(logits), tokens, experts, logits.stride(0),
-          _token_mask(mask, tokens, dev), top_k, ROUTE_RENORM if renorm else 0, ids.data_ptr(), gates.data_ptr(),
-          part.data_ptr(), nbytes)
-    stats._add(part, tokens)
+    at = part.data_ptr()
+    io = dq_route_worker(logits.data_ptr(), tokens, logits.stride(0), _token_mask(mask, tokens, dev), ids.data_ptr(),
+                         gates.data_ptr(), at, nbytes)
+    _route(C.byref(io), 1, logits, top_k, renorm, stats)
+    stats._add(part, at, tokens)
     return ids, gates, stats
 
 
@@ -449,31 +517,58 @@ def balance(stats, top_k):
     return loss, coef, counts
 
 
-@_on_stream
-def route_backward(logits, ids, dgates=None, coef=None, dloss=None, renorm=True, mask=None, out=None):
-    """Gradient by the logits (``dq_route_backward``) from the gates' gradient
-    ``dgates`` and the balance loss's, ``dloss`` (one fp32 element; None: 1) times
-    ``coef`` of :func:`balance`; either part may be None.  ``ids``, ``renorm`` and ``mask``
-    as in the forward call; ``out`` may be ``logits``."""
-    tokens, experts = _logits(logits).shape
-    dev = logits.device
+def _grad_fields(logits, ids, dgates, mask, out):
+    tokens, dev = logits.size(0), logits.device
     if not isinstance(ids, torch.Tensor) or ids.dim() != 2 or ids.size(0) != tokens:
         raise ValueError(f"ids: expected [{tokens}, top_k] of route()")
     _tensor(ids, "ids", dev, dtype=torch.int32)
     if dgates is not None:
         _result(dgates, ids.shape, "dgates", torch.float32, dev)
+    if _logits(out, "out").shape != logits.shape or out.dtype != logits.dtype or out.device != dev:
+        raise ValueError(f"out: {tuple(out.shape)} {out.dtype} on {out.device}, "
+                         f"logits are {tuple(logits.shape)} {logits.dtype} on {dev}")
+    return (logits.data_ptr(), tokens, logits.stride(0), _token_mask(mask, tokens, dev), ids.data_ptr(), _opt(dgates),
+            out.data_ptr(), out.stride(0))
+
+
+def _route_grad(io, n, logits, ids, coef, dloss, renorm):
+    dev, experts = logits.device, logits.size(1)
     if coef is not None:
         _tensor(coef, "coef", dev, numel=experts, dtype=torch.float32)
     if dloss is not None:
         _tensor(dloss, "dloss", dev, numel=1, dtype=torch.float32)
+    _call(dev, "dq_route_backward", io, n, _kind(logits), experts, ids.size(1), ROUTE_RENORM if renorm else 0,
+          _opt(coef), _opt(dloss))
+
+
+@_on_stream
+def route_backward(logits, ids, dgates=None, coef=None, dloss=None, renorm=True, mask=None, out=None):
+    """Gradient by the logits (``dq_route_backward``) from the gates' gradient
+    ``dgates`` and the balance loss's, ``dloss`` (one fp32 element; None: 1) times
+    ``coef`` of :func:`balance`; either part may be None.  ``ids``, ``renorm`` and ``mask``
+    as in the forward call; ``out`` may be ``logits``.  Lists as in :func:`route`, with
+    None in ``dgates`` for a worker without."""
+    if isinstance(logits, (list, tuple)):
+        masks = _workers(logits, mask)
+        n = len(logits)
+        dgates = [None] * n if dgates is None else dgates
+        if len(ids) != n or len(dgates) != n or out is not None and len(out) != n:
+            raise ValueError(f"{len(ids)} ids, {len(dgates)} dgates and {0 if out is None else len(out)} out "
+                             f"for {n} workers")
+        tops = {i.size(-1) for i in ids if isinstance(i, torch.Tensor) and i.dim() == 2}
+        if len(tops) != 1:
+            raise ValueError(f"ids: expected [tokens, top_k] of route() for every worker, got top_k of {sorted(tops)}")
+        outs = out
+        if out is None:
+            outs = _side_by_side([l.size(0) for l in logits], logits[0].size(1), logits[0].dtype, logits[0].device)
+        io = [_grad_fields(*w) for w in zip(logits, ids, dgates, masks, outs)]
+        _route_grad((dq_route_grad * n)(*io), n, logits[0], ids[0], coef, dloss, renorm)
+        return outs
+    _logits(logits)
     if out is None:
-        out = torch.empty((tokens, experts), dtype=logits.dtype, device=dev)
-    elif _logits(out, "out").shape != logits.shape or out.dtype != logits.dtype or out.device != dev:
-        raise ValueError(f"out: {tuple(out.shape)} {out.dtype} on {out.device}, "
-                         f"logits are {tuple(logits.shape)} {logits.dtype} on {dev}")
-    _call(dev, "dq_route_backward", logits.data_ptr(), _kind(logits), tokens, experts, logits.stride(0),
-          _token_mask(mask, tokens, dev), ids.size(1), ROUTE_RENORM if renorm else 0, ids.data_ptr(), _opt(dgates),
-          _opt(coef), _opt(dloss), out.data_ptr(), out.stride(0))
+        out = torch.empty_like(logits, memory_format=torch.contiguous_format)
+    io = dq_route_grad(*_grad_fields(logits, ids, dgates, mask, out))
+    _route_grad(C.byref(io), 1, logits, ids, coef, dloss, renorm)
     return out
 
 

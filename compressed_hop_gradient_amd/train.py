@@ -65,12 +65,8 @@ class _Route(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, top_k, renorm, masks, reduce, found, *logits):
-        ids, gates, stats = [], [], None
         logits = [_by_rows(l) for l in logits]
-        for l, m in zip(logits, masks):
-            i, g, stats = dq.route(l, top_k, renorm, m, stats)
-            ids.append(i)
-            gates.append(g)
+        ids, gates, stats = dq.route(logits, top_k, renorm, masks)
         if reduce is not None:
             stats = stats.fold()
             reduce(stats)
@@ -86,14 +82,15 @@ class _Route(torch.autograd.Function):
     def backward(ctx, dloss, *dgates):
         coef, *saved = ctx.saved_tensors
         n = len(dgates)
-        if dloss is None:
-            coef = None
         grads = [None] * n
-        for w, dg in enumerate(dgates):
-            if ctx.needs_input_grad[5 + w] and (dloss is not None or dg is not None):
-                if dg is not None and not dg.is_contiguous():
-                    dg = dg.contiguous()
-                grads[w] = dq.route_backward(saved[w], saved[n + w], dg, coef, dloss, ctx.renorm, saved[2 * n + w])
+        # without the loss, only the workers whose gates were used
+        at = [w for w, dg in enumerate(dgates) if ctx.needs_input_grad[5 + w] and (dloss is not None or dg is not None)]
+        if at:
+            dgs = [dgates[w] if dgates[w] is None else dgates[w].contiguous() for w in at]
+            for w, d in zip(at, dq.route_backward([saved[w] for w in at], [saved[n + w] for w in at], dgs,
+                                                  None if dloss is None else coef, dloss, ctx.renorm,
+                                                  [saved[2 * n + w] for w in at])):
+                grads[w] = d
         return (None, None, None, None, None, *grads)
 
 
@@ -112,12 +109,6 @@ def route(logits, top_k, renorm=True, masks=None, reduce=None):
     one = isinstance(logits, torch.Tensor)
     ls = [logits] if one else list(logits)
     ms = [masks] * len(ls) if masks is None or one else list(masks)
-    if not ls or len(ms) != len(ls):
-        raise ValueError(f"{len(ls)} logits with {len(ms)} masks")
-    for l in ls[1:]:
-        if l.size(-1) != ls[0].size(-1) or l.device != ls[0].device:
-            raise ValueError(f"the workers' logits differ in experts or device: {tuple(l.shape)} on {l.device}, "
-                             f"{tuple(ls[0].shape)} on {ls[0].device}")
     found = []
     loss, *gates = _Route.apply(top_k, renorm, ms, reduce, found, *ls)
     ids, counts, coef = found

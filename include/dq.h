@@ -428,26 +428,35 @@ dq_status dq_dropout(const void *d_x, const void *d_residual, void *d_y, int32_t
                      uint64_t seed, uint32_t round, const uint32_t *d_round, int32_t worker, uint32_t site,
                      void *stream);
 
-/* Expert router.  For every token, p = softmax of its n_experts logits (kind
- * DQ_BF16 or DQ_F32, row t at element t * stride, stride >= 0), the top_k
- * largest logits are chosen in falling order -- equal ones (-0 and +0 too) by
- * the lowest index, NaN before +inf, -inf never -- and their probabilities are
- * the gates, with DQ_ROUTE_RENORM divided by their sum.  Outputs, per token:
- * d_ids[top_k] (-1 where fewer than top_k experts are open) and
- * d_gates[top_k] (0 there).  d_mask (may be NULL): one byte per token, 0 for
- * a token left out; such a token, and one with every logit -inf, gets ids -1
- * and gates 0 and counts nowhere, whatever its logits hold.  A token with a NaN
- * or +inf has NaN gates (and makes the balance loss NaN).
- *
- * d_part (256-byte aligned, dq_route_part_bytes) receives the statistics of
- * these tokens in the form dq_balance takes: partial sums, in the caller's
+/* Expert router of n_workers workers' tokens, four workers to a launch.  For
+ * every token, p = softmax of its n_experts logits (kind DQ_BF16 or
+ * DQ_F32, row t at element t * stride, stride >= 0), the top_k largest logits are
+ * chosen in falling order -- equal ones (-0 and +0 too) by the lowest index, NaN
+ * before +inf, -inf never -- and their probabilities are the gates, with
+ * DQ_ROUTE_RENORM divided by their sum.  Outputs, per token: d_ids[top_k] (-1
+ * where fewer than top_k experts are open) and d_gates[top_k] (0 there).
+ * d_mask (may be NULL): one byte per token, 0 for a token left out; such a token,
+ * and one with every logit -inf, gets ids -1 and gates 0 and counts nowhere,
+ * whatever its logits hold.  A token with a NaN or +inf has NaN gates (and makes
+ * the balance loss NaN).
+ * d_part (256-byte aligned, dq_route_part_bytes) receives the statistics of a
+ * worker's tokens in the form dq_balance takes: partial sums, in the caller's
  * buffer until then.
- * n_experts in 1..1024, top_k in 1..min(n_experts, 16), tokens in 0..2^40. */
+ * n_experts in 1..1024, top_k in 1..min(n_experts, 16), tokens in 0..2^40 (with
+ * 0, only d_part is used).  h_workers is a HOST array. */
 typedef enum dq_route_flags { DQ_ROUTE_RENORM = 1 } dq_route_flags;
+typedef struct dq_route_worker {
+    const void *d_logits;
+    int64_t tokens, stride;
+    const uint8_t *d_mask;
+    int32_t *d_ids;
+    float *d_gates;
+    void *d_part;
+    size_t part_bytes;
+} dq_route_worker;
 size_t dq_route_part_bytes(int64_t tokens, int32_t n_experts);   /* 0 on bad arguments */
-dq_status dq_route(const void *d_logits, int32_t kind, int64_t tokens, int32_t n_experts, int64_t stride,
-                   const uint8_t *d_mask, int32_t top_k, int32_t flags, int32_t *d_ids, float *d_gates,
-                   void *d_part, size_t part_bytes, void *stream);
+dq_status dq_route(const dq_route_worker *h_workers, int32_t n_workers, int32_t kind, int32_t n_experts,
+                   int32_t top_k, int32_t flags, void *stream);
 
 /* Balance statistics and loss over all workers.  h_parts is a HOST array of
  * n_parts (0..DQ_ROUTE_MAX_PARTS) parts that dq_route wrote, one per worker, with
@@ -473,19 +482,29 @@ dq_status dq_balance(const dq_route_part *h_parts, int32_t n_parts, const double
                      int32_t top_k, double *d_stats, float *d_loss, float *d_coef, int64_t *d_counts,
                      void *stream);
 
-/* Gradient by the logits, from the gates' (d_dgates[tokens][top_k], may be
- * NULL) and the balance loss's (d_coef of dq_balance, may be NULL; times
- * *d_dloss, NULL: 1).  d_ids, d_mask and DQ_ROUTE_RENORM as in the forward call.
- * With a_e = dloss coef_e and g the gates:
+/* Gradient by the logits of n_workers' tokens, four workers to a launch, from
+ * the gates' (d_dgates[tokens][top_k], may be NULL) and the balance loss's (d_coef of
+ * dq_balance, may be NULL; times *d_dloss, NULL: 1).  d_ids, d_mask and
+ * DQ_ROUTE_RENORM as in the forward call.  With a_e = dloss coef_e and g the
+ * gates:
  *   RENORM:  dl_j = p_j (a_j - sum p a) + [j chosen] g_j (dg_j - sum g dg)
  *   without: dl_j = p_j (a_j - sum p a - sum g dg) + [j chosen] g_j dg_j
  * A token that was left out gets zeros.  d_dlogits has the logits' kind, row t
  * at element t * dstride (dstride >= n_experts), and may be d_logits (same
- * stride).  Entries of d_ids outside 0..n_experts-1 count as -1. */
-dq_status dq_route_backward(const void *d_logits, int32_t kind, int64_t tokens, int32_t n_experts,
-                            int64_t stride, const uint8_t *d_mask, int32_t top_k, int32_t flags,
-                            const int32_t *d_ids, const float *d_dgates, const float *d_coef,
-                            const float *d_dloss, void *d_dlogits, int64_t dstride, void *stream);
+ * stride).  Entries of d_ids outside 0..n_experts-1 count as -1.  h_workers is a
+ * HOST array. */
+typedef struct dq_route_grad {
+    const void *d_logits;
+    int64_t tokens, stride;
+    const uint8_t *d_mask;
+    const int32_t *d_ids;
+    const float *d_dgates;
+    void *d_dlogits;
+    int64_t dstride;
+} dq_route_grad;
+dq_status dq_route_backward(const dq_route_grad *h_workers, int32_t n_workers, int32_t kind, int32_t n_experts,
+                            int32_t top_k, int32_t flags, const float *d_coef, const float *d_dloss,
+                            void *stream);
 
 /* ---- inspection ----------------------------------------------------------- */
 

@@ -512,6 +512,50 @@ def test_route_folds_workers_in_order(dtype):
     assert all(torch.equal(a, b) for a, b in zip(dq.balance(total, k), other))
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("E,k", [(8, 2), (60, 4), (64, 8), (256, 8)])
+def test_workers_in_one_launch_are_the_workers_one_by_one(E, k, dtype):
+    """Bit for bit, with workers of different sizes, without tokens, with and
+    without masks, and more of them than one launch takes."""
+    sizes = [300, 0, 1, 77] + [40] * 15
+    ls = [logits_of(T, E, dtype, T, closed=0.2 if T == 77 else 0.0) for T in sizes]
+    masks = [torch.arange(T, device="cuda") % 4 != 1 if T == 300 else None for T in sizes]
+    ids, gates, stats = dq.route(ls, k, mask=masks)
+    one = None
+    for l, m, i, g in zip(ls, masks, ids, gates):
+        i1, g1, one = dq.route(l, k, mask=m, stats=one)
+        assert torch.equal(i, i1) and torch.equal(g, g1)
+    (loss, coef, counts), want = dq.balance(stats, k), dq.balance(one, k)
+    assert torch.equal(counts, want[2]) and torch.equal(coef, want[1])
+    assert abs(loss.item() - want[0].item()) <= 4 * U * want[0].item()     # (folded in other groups)
+    dgs = [randn((T, k), torch.float32, T) if T != 77 else None for T in sizes]
+    dloss = torch.tensor([0.4], device="cuda")
+    ds = dq.route_backward(ls, ids, dgs, coef, dloss, mask=masks)
+    for l, m, i, dg, d in zip(ls, masks, ids, dgs, ds):
+        assert same(d, dq.route_backward(l, i, dg, coef, dloss, mask=m))
+    outs = [torch.empty_like(l) for l in ls]
+    again = dq.route_backward(ls, ids, dgs, coef, dloss, mask=masks, out=outs)
+    assert all(a is o and same(a, d) for a, o, d in zip(again, outs, ds))
+    held = [torch.empty_like(i) for i in ids], [torch.empty_like(g) for g in gates]
+    got = dq.route(ls, k, mask=masks, ids=held[0], gates=held[1])
+    assert all(a is b and torch.equal(a, c) for a, b, c in zip(got[0], held[0], ids))
+
+
+def test_workers_of_different_alignment_in_one_launch():
+    """One unaligned worker sends all of them element by element: choices stay,
+    gates and gradients within the roundings."""
+    E, k = 64, 8
+    big = logits_of(90, E + 3, torch.bfloat16)
+    ls = [logits_of(50, E, torch.bfloat16), big[:, 1:E + 1]]
+    ids, gates, stats = dq.route(ls, k)
+    rs = [check_forward(l, k, True, None, i, g) for l, i, g in zip(ls, ids, gates)]
+    check_stats(stats, rs)
+    coef = dq.balance(stats, k)[1]
+    dgs = [randn(i.shape, torch.float32) for i in ids]
+    for d, r, dg in zip(dq.route_backward(ls, ids, dgs, coef), rs, dgs):
+        check_gradient(d, r, dg, coef, 1.0, torch.bfloat16)
+
+
 def test_more_workers_than_one_fold_takes():
     E, k, n = 24, 2, 2 * dq.ROUTE_MAX_PARTS + 3
     ls = [logits_of(5 + w, E, torch.float32, w) for w in range(n)]
@@ -585,7 +629,13 @@ def test_route_refuses():
                  lambda: dq.route_backward(l, ids, coef=torch.zeros(16, dtype=torch.float64, device="cuda"))):
         with pytest.raises(TypeError):
             call()
-    for call in (lambda: dq.route(l, 17), lambda: dq.route(l, 0), lambda: dq.balance(stats, 17),
+    for call in (lambda: dq.route(l, 0), lambda: dq.route([l, l[:, :8]], 2), lambda: dq.route([l, l.bfloat16()], 2),
+                 lambda: dq.route([l, l], 2, mask=[None]), lambda: dq.route([l, l], 2, ids=[ids]),
+                 lambda: dq.route_backward([l, l], [ids]), lambda: dq.route_backward([l, l], [ids, ids], [gates]),
+                 lambda: dq.route_backward([l, l], [ids, ids], out=[l])):
+        with pytest.raises(ValueError):
+            call()
+    for call in (lambda: dq.route(l, 17), lambda: dq.balance(stats, 17),
                  lambda: dq.route(torch.zeros(2, 1025, device="cuda"), 2),
                  lambda: dq.route(torch.zeros(2, 64, device="cuda"), 17),
                  lambda: dq.route_backward(l[1:], ids[1:], out=l[:-1])):

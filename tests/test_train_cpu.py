@@ -113,8 +113,13 @@ def test_dropout_null_and_empty(lib):
 
 
 def _route(lib, l=FAKE, kind=dq.BF16, T=8, E=16, stride=16, mask=None, k=2, flags=1, ids=4 * FAKE, gates=5 * FAKE,
-           part=7 * FAKE, nbytes=1 << 20):
-    return lib.dq_route(l, kind, T, E, stride, mask, k, flags, ids, gates, part, nbytes, None)
+           part=7 * FAKE, nbytes=1 << 20, n=1):
+    """One call; with n = 2 a worker of no tokens and nothing wrong comes first
+    (the bad one must be found before anything is launched)."""
+    io = (dq.dq_route_worker * 2)((None, 0, 0, None, None, None, 9 * FAKE, 1 << 20),
+                                  (l, T, stride, mask, ids, gates, part, nbytes))
+    at = C.byref(io, C.sizeof(dq.dq_route_worker)) if n == 1 else io
+    return lib.dq_route(at, n, kind, E, k, flags, None)
 
 
 @pytest.mark.parametrize("bad", [
@@ -123,6 +128,20 @@ def _route(lib, l=FAKE, kind=dq.BF16, T=8, E=16, stride=16, mask=None, k=2, flag
     dict(ids=4 * FAKE + 2), dict(gates=5 * FAKE + 2)])
 def test_route_refuses(lib, bad):
     assert _route(lib, **bad) == dq.DQ_EINVAL
+    assert _route(lib, n=2, **bad) == dq.DQ_EINVAL
+
+
+def test_route_worker_counts(lib):
+    io = (dq.dq_route_worker * 17)()
+    assert lib.dq_route(io, 17, dq.BF16, 16, 2, 1, None) == dq.DQ_EWORKSPACE                       # no part
+    assert lib.dq_route(io, -1, dq.BF16, 16, 2, 1, None) == dq.DQ_EINVAL
+    assert lib.dq_route(None, 1, dq.BF16, 16, 2, 1, None) == dq.DQ_ENULL
+    assert lib.dq_route(None, 0, dq.BF16, 16, 2, 1, None) == dq.DQ_OK
+    io = (dq.dq_route_grad * 17)()
+    assert lib.dq_route_backward(io, 17, dq.BF16, 16, 2, 1, None, None, None) == dq.DQ_OK          # no tokens
+    assert lib.dq_route_backward(io, -1, dq.BF16, 16, 2, 1, None, None, None) == dq.DQ_EINVAL
+    assert lib.dq_route_backward(None, 1, dq.BF16, 16, 2, 1, None, None, None) == dq.DQ_ENULL
+    assert lib.dq_route_backward(None, 0, dq.BF16, 16, 2, 1, None, None, None) == dq.DQ_OK
 
 
 def test_route_null_and_part(lib):
@@ -159,7 +178,9 @@ def test_balance_refuses(lib):
 
 def _backward(lib, l=FAKE, kind=dq.BF16, T=8, E=16, stride=16, mask=None, k=2, flags=1, ids=4 * FAKE, dg=5 * FAKE,
               coef=6 * FAKE, dloss=7 * FAKE, out=8 * FAKE, dstride=16):
-    return lib.dq_route_backward(l, kind, T, E, stride, mask, k, flags, ids, dg, coef, dloss, out, dstride, None)
+    io = (dq.dq_route_grad * 2)((None, 0, 0, None, None, None, None, 0),
+                                (l, T, stride, mask, ids, dg, out, dstride))
+    return lib.dq_route_backward(io, 2, kind, E, k, flags, coef, dloss, None)
 
 
 @pytest.mark.parametrize("bad", [
@@ -220,6 +241,10 @@ def test_route_wrapper_checks_the_list():
         train.route([torch.zeros(4, 8)], 2, masks=[None, None])
     with pytest.raises(ValueError):
         train.route([torch.zeros(4, 8), torch.zeros(4, 9)], 2)
+    for call in (lambda: dq.route([], 2), lambda: dq.route_backward([], []),
+                 lambda: dq.route([torch.zeros(4, 8)], 2, mask=[None, None])):
+        with pytest.raises(ValueError):
+            call()
 
 
 def test_eval_dropout_is_the_input():
