@@ -254,11 +254,15 @@ def _gpu(t, what):
     return t
 
 
+def _raw_stream(dev):
+    """The current stream's handle (torch.cuda.current_stream builds an object:
+    2.9 us where a whole call takes about 10, against 0.1)."""
+    return torch._C._cuda_getCurrentRawStream(dev.index)
+
+
 def _call(dev, name, *args):
     """Call a stateless entry point on ``dev``'s current stream."""
-    # torch.cuda.current_stream builds an object: 2.9 us where a whole call
-    # takes about 10, against 0.1 us
-    stream = torch._C._cuda_getCurrentRawStream(dev.index)
+    stream = _raw_stream(dev)
     if dev.index == torch.cuda.current_device():
         rc = getattr(lib(), name)(*args, stream)
     else:
@@ -369,17 +373,21 @@ class RouteStats:
 
     def __init__(self, experts, device):
         self.experts, self.device = experts, device
-        self.parts = []        # (buffer of dq_route, its address, its tokens)
+        self.parts = []        # (buffer of dq_route, the part in it, its tokens, the stream it was made on)
         self.sums = None       # what was folded before them, fp64 [2 experts + 1]
 
     def _add(self, part, at, tokens):
         if len(self.parts) == ROUTE_MAX_PARTS:
             self.fold()
-        self.parts.append((part, at, tokens))
+        self.parts.append((part, at, tokens, _raw_stream(self.device)))
 
     def _balance(self, top_k, stats, loss, coef, counts):
         n = len(self.parts)
-        array = (dq_route_part * n)(*[p[1:] for p in self.parts])
+        array = (dq_route_part * n)(*[p[1:3] for p in self.parts])
+        now = _raw_stream(self.device)
+        for part, _, _, made in self.parts:
+            if made != now:       # its memory is not to be reused there before this call has read it
+                part.record_stream(torch.cuda.current_stream(self.device))
         _call(self.device, "dq_balance", array, n, _opt(self.sums), self.experts, top_k, _opt(stats), _opt(loss),
               _opt(coef), _opt(counts))
 
@@ -415,18 +423,10 @@ def _workers(logits, masks):
     return masks
 
 
-def _side_by_side(tokens, width, dtype, dev):
-    """A [tokens, width] tensor per worker, in one buffer."""
-    if len(tokens) == 1:
-        return [torch.empty((tokens[0], width), dtype=dtype, device=dev)]
-    return list(torch.empty((sum(tokens), width), dtype=dtype, device=dev).split(tokens))
-
-
 def _results(given, tokens, width, what, dtype, dev):
     """The caller's buffers for a [tokens, width] result of each worker, or new
     ones."""
-    if given is None:
-        return _side_by_side(tokens, width, dtype, dev)
+    given = [None] * len(tokens) if given is None else given
     if len(given) != len(tokens):
         raise ValueError(f"{len(given)} {what} for {len(tokens)} workers")
     return [_result(t, (n, width), what, dtype, dev) for t, n in zip(given, tokens)]
@@ -560,7 +560,7 @@ def route_backward(logits, ids, dgates=None, coef=None, dloss=None, renorm=True,
             raise ValueError(f"ids: expected [tokens, top_k] of route() for every worker, got top_k of {sorted(tops)}")
         outs = out
         if out is None:
-            outs = _side_by_side([l.size(0) for l in logits], logits[0].size(1), logits[0].dtype, logits[0].device)
+            outs = [torch.empty_like(l, memory_format=torch.contiguous_format) for l in logits]
         io = [_grad_fields(*w) for w in zip(logits, ids, dgates, masks, outs)]
         _route_grad((dq_route_grad * n)(*io), n, logits[0], ids[0], coef, dloss, renorm)
         return outs

@@ -681,6 +681,34 @@ def test_route_autograd(dtype):
     one.loss.backward()
 
 
+def test_results_of_a_list_are_tensors_of_their_own():
+    """Changing one worker's gates or gradient in place touches no other's."""
+    ls = [logits_of(T, 24, torch.float32, T).requires_grad_() for T in (20, 30)]
+    r = train.route(ls, 2)
+    kept = r.gates[1].detach().clone()
+    r.gates[0].mul_(2)
+    assert torch.equal(r.gates[1], kept)
+    (r.gates[0].sum() + r.gates[1].square().sum() + r.loss).backward()
+    other = ls[1].grad.clone()
+    ls[0].grad.zero_()
+    assert torch.equal(ls[1].grad, other)
+
+
+def test_balance_on_another_stream_than_the_parts():
+    l = logits_of(3000, 64, torch.bfloat16)
+    want = dq.balance(dq.route(l, 8)[2], 8)
+    s = torch.cuda.Stream()
+    for _ in range(20):
+        stats = dq.route(l, 8)[2]
+        s.wait_stream(torch.cuda.current_stream())
+        got = dq.balance(stats, 8, stream=s)
+        del stats                                  # its parts may be taken by what comes next here
+        torch.full((1 << 20,), 7, dtype=torch.uint8, device="cuda")
+        dq.route(l * 0, 8)
+        torch.cuda.current_stream().wait_stream(s)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_two_forwards_before_their_backwards():
     """Nothing is shared between calls: gradients do not depend on what ran in
     between."""
