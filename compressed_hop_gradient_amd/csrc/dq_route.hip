@@ -326,13 +326,14 @@ __global__ __launch_bounds__(256, KP == 16 || CH == 4 || !VEC ? 3 : 4) void k_ro
             ge[s] = open ? exponential(K::value(mine[s]), m) : 0.0f;
             top += ge[s];
         }
-        // a choice is the row's largest logit, so that the sum is 1 or more
-        const float by = Z != Z ? Z : Z == 0.0f ? 0.0f : args.renorm ? reciprocal(group_sum<G>(top)) : by_z;
+        // with renorm a quotient, so that a choice alone has the gate 1
+        if (args.renorm) top = group_sum<G>(top);
 #pragma unroll
         for (int s = 0; s < S; s++) {
             if (s * G + g < args.k && t < a.tokens) {
                 a.ids[t * args.k + s * G + g] = id[s];
-                a.gates[t * args.k + s * G + g] = id[s] < 0 ? 0.0f : ge[s] * by;
+                const float gate = args.renorm ? ge[s] / top : ge[s] * by_z;
+                a.gates[t * args.k + s * G + g] = id[s] < 0 ? 0.0f : Z != Z ? Z : gate;
                 if (id[s] >= 0) atomicAdd(&hist[id[s]], 1u);
             }
         }

@@ -117,14 +117,12 @@ __global__ __launch_bounds__(256) void k_route_backward(RouteBackwardArgs args) 
             gs[s] = row.id[s] >= 0 ? exponential(El::up(ls[s]), m) : 0.0f;
             top += gs[s];
         }
-        float by = inv;
-        if (args.renorm) {
-            top = group_sum<G>(top);
-            by = top == 0.0f ? 0.0f : 1.0f / top;      // no choice
-        }
+        if (args.renorm) top = group_sum<G>(top);
 #pragma unroll
         for (int s = 0; s < S; s++) {
-            gs[s] *= by;
+            // with renorm a quotient, so that a choice alone has the gate 1; 0 where
+            // a choice that is not the forward pass's has no weight
+            gs[s] = !args.renorm ? gs[s] * inv : top == 0.0f ? 0.0f : gs[s] / top;
             if (row.id[s] >= 0) gd = __builtin_fmaf(gs[s], row.dg[s], gd);
         }
         gd = group_sum<G>(gd);

@@ -118,7 +118,7 @@ __device__ __forceinline__ float group_sum(float x) {
         })));
     return x;
 }
-// 1 / x to an ulp for 1 <= x < 2^126; NaN stays NaN
+// 1 / x to an ulp for 2^-1 <= x < 2^126; NaN stays NaN
 __device__ __forceinline__ float reciprocal(float x) {
     const float r = __builtin_amdgcn_rcpf(x);
     return __builtin_fmaf(__builtin_fmaf(-x, r, 1.0f), r, r);
@@ -126,12 +126,12 @@ __device__ __forceinline__ float reciprocal(float x) {
 
 // exp(l - m) where m is the row's largest logit, or 0.  The exponent takes one
 // fma, whose rounding of m log2 e is the same factor for all of the row and
-// cancels in quotients; near the ends of the range m log2 e overflows, and the
-// difference comes first.
-constexpr float kNearTheEnds = 1e37f;
+// cancels in quotients.  Up to |m| = 2^20 that factor is within 2^(1/22) of 1;
+// far from zero it would pass every bound, and the difference comes first.
+constexpr float kFar = 1048576.0f;
 __device__ __forceinline__ float exponential(float l, float m) {
     const float x = __builtin_fmaf(l, kLog2e, -m * kLog2e), y = (l - m) * kLog2e;
-    return __builtin_amdgcn_exp2f(fabsf(m) < kNearTheEnds ? x : y);
+    return __builtin_amdgcn_exp2f(fabsf(m) < kFar ? x : y);
 }
 
 // e = exp(l - m) of a row and Z = sum e.  Z = 0 only where every logit is -inf;
@@ -139,8 +139,8 @@ __device__ __forceinline__ float exponential(float l, float m) {
 template <bool F32, int G, int CH, bool VEC>
 __device__ __forceinline__ void exponentials(const Slice<F32, G, CH, VEC> &l, float m, float e[8 * CH], float &Z) {
     float z[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (__any(!(fabsf(m) < kNearTheEnds))) {
-        asm volatile("; extreme logits");        // a branch, not selects
+    if (__any(!(fabsf(m) < kFar))) {
+        asm volatile("; logits far from zero");        // a branch, not selects
 #pragma unroll
         for (int v = 0; v < 8 * CH; v++) e[v] = exponential(l.at(v), m);
     } else {

@@ -394,6 +394,61 @@ def test_route_extreme_logits():
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("E", [7, 64, 256])
+def test_route_far_from_zero(E, dtype):
+    """Rows of any size: the softmax depends on differences alone, which are
+    exact for these logits (a few steps of the type around +-2^n).  Where the
+    steps are large the probabilities are 0 and 1, ties share."""
+    rng = np.random.default_rng(E)
+    rows = []
+    for n in (3, 10, 19, 20, 21, 24, 31, 33, 40, 60, 100, 120, 126):
+        for sign in (1.0, -1.0):
+            step = 2.0 ** n * torch.finfo(dtype).eps
+            rows.append(sign * 2.0 ** n + step * rng.integers(0, 6, E))
+    l = torch.from_numpy(np.array(rows)).to(dtype).cuda()
+    assert bool((l.double().cpu() == torch.from_numpy(np.array(rows))).all())
+    for renorm in (True, False):
+        ids, gates, stats = dq.route(l, 3, renorm)
+        x = l.double().cpu()
+        assert torch.equal(ids.long().cpu(), torch.sort(x, dim=1, descending=True, stable=True)[1][:, :3])
+        p = torch.softmax(x, 1)
+        g = p.gather(1, ids.long().cpu())
+        if renorm:
+            g = g / g.sum(1, keepdim=True)
+        # exponents: three roundings of differences that matter only below 104 (e^-104 is 0 in fp32)
+        c = 2 * (3 * 104 + 48)
+        assert bool(((gates.double().cpu() - g).abs() <= c * U * g + 1e-37).all())
+        assert bool(((stats.fold()[E:2 * E].cpu() - p.sum(0)).abs() <= c * U * p.sum(0) + 1e-37).all())
+        dg = randn((len(l), 3), torch.float32)
+        d = dq.route_backward(l, ids, dg, renorm=renorm)
+        assert bool(torch.isfinite(d).all())
+        up = torch.zeros_like(x).scatter_(1, ids.long().cpu(), dg.double().cpu())
+        if renorm:
+            want = torch.zeros_like(x).scatter_(1, ids.long().cpu(), g * (dg.double().cpu() - (g * dg.double().cpu()).sum(1, keepdim=True)))
+            mag = torch.zeros_like(x).scatter_(1, ids.long().cpu(), g * (dg.double().cpu().abs() + (g * dg.double().cpu().abs()).sum(1, keepdim=True)))
+        else:
+            want = p * (up - (p * up).sum(1, keepdim=True))
+            mag = p * (up.abs() + (p * up.abs()).sum(1, keepdim=True))
+        assert bool(((d.double().cpu() - want).abs() <= 2 * (c + 44) * U * mag + 1.01 * half_step(dtype) * want.abs() + 1e-37).all())
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("E", [1, 5, 64, 256])
+def test_one_choice_has_gate_one_and_no_gradient(E, dtype):
+    """A choice divided by itself is 1, and 1 has no gradient: exactly."""
+    l = logits_of(300, E, dtype) * 7
+    ids, gates, _ = dq.route(l, 1)
+    assert bool((gates == 1).all())
+    assert bool((dq.route_backward(l, ids, randn((300, 1), torch.float32)) == 0).all())
+    if E > 1:
+        l[:] = -math.inf
+        l[:, E - 2] = 3.3
+        ids, gates, _ = dq.route(l, 2 if E < 64 else 8)
+        assert bool((gates[:, 0] == 1).all()) and bool((gates[:, 1:] == 0).all()) and bool((ids[:, 0] == E - 2).all())
+        assert bool((dq.route_backward(l, ids, randn(gates.shape, torch.float32)) == 0).all())
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("E,wide,at", [(64, 64, 0), (64, 128, 64), (64, 67, 1), (60, 64, 0), (256, 264, 8), (9, 10, 1)])
 def test_route_strided_rows(E, wide, at, dtype):
     big = logits_of(150, wide, dtype)
