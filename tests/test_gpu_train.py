@@ -253,6 +253,26 @@ def test_dropout_beyond_32_bits():
         assert same(x[first:first + count], want), first
 
 
+def test_row_offsets_beyond_32_bits():
+    """Rows 2^31 elements apart (13 GB a tensor, of which only the rows are
+    touched): dropout at any alignment, the router and its gradient."""
+    stride, E, k = (1 << 31) + 8, 64, 4
+    x = torch.empty(3 * stride, dtype=torch.bfloat16, device="cuda").view(3, stride)
+    y = torch.empty(3 * stride, dtype=torch.bfloat16, device="cuda").view(3, stride)
+    for cols in (64, 61):
+        rows, out = x[:, 3:3 + cols] if cols == 61 else x[:, :cols], y[:, :cols]
+        rows.copy_(randn((3, cols), torch.bfloat16, cols))
+        print(f"[offsets] {cols} columns", flush=True)
+        dq.dropout(rows, 0.4, out=out, **KEY)
+        assert same(out, expected_dropout(rows, 0.4, **KEY).bfloat16())
+    l = x[:, :E]
+    l.copy_(logits_of(3, E, torch.bfloat16))
+    ids, gates, stats = dq.route(l, k)
+    r = check_forward(l, k, True, None, ids, gates)
+    dg, coef = randn((3, k), torch.float32), dq.balance(stats, k)[1]
+    check_gradient(dq.route_backward(l, ids, dg, coef, out=y[:, :E]), r, dg, coef, 1.0, torch.bfloat16)
+
+
 def test_dropout_on_another_stream():
     x = randn((1 << 20,), torch.bfloat16)
     s = torch.cuda.Stream()
