@@ -11,7 +11,7 @@ namespace {
 // keeps an element; the gradient by x is the same m s on dy.  Every operand is
 // touched once, and what is left to do is the mask: one generator call for 8
 // elements (16 random bits each), so that its 20 64-bit products are shared and
-// memory stays the bound, with the VALUs busy 61% of the time (bf16, no residual).
+// memory stays the bound, with the VALUs busy 59% of the time (bf16, no residual).
 //
 // 16384 x 8192 bf16 with a residual (805 MB): 136 us, 5.9 TB/s; 8192 x 8192 bf16
 // without one (268 MB): 46 us, 5.8 TB/s; 8192 x 2048 fp32 (134 MB): 25 us, 5.3 TB/s.
@@ -19,7 +19,8 @@ namespace {
 
 // The eight 16-bit dithers of elements 8b .. 8b + 7 as four words, low half
 // first: Philox4x32-10 (Salmon et al., SC'11) on (b, worker, round, site).  A
-// product is one 64-bit multiply, a three-way xor one instruction.
+// product is one 64-bit multiply, a three-way xor one instruction.  The compiler may
+// hold all round keys (the codec's kernels may not): 57 to 106 SGPRs, none spilled.
 __device__ __forceinline__ void dropout_words(uint64_t b, const DropoutArgs &a, uint32_t round, uint32_t w[4]) {
     uint32_t x0 = (uint32_t)b, x1 = (uint32_t)(b >> 32) | a.worker << 16, x2 = round, x3 = 0x80000000u | a.site;
     uint32_t k0 = a.key0, k1 = a.key1;

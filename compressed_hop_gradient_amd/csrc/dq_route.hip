@@ -259,12 +259,13 @@ __device__ __forceinline__ void pick_any(const Slice<F32, G, CH, VEC> &l, uint32
 // probabilities are summed in the lanes' registers over all rows of a block and
 // meet in LDS at its end; choices are counted in LDS.
 //
-// Bound: vector instructions.  131072 x 256 bf16, k = 8, takes 26 us where the
-// 67 MB alone take 13; 671 instructions per 8 tokens, 0.4 of them in sorting and
-// merging, and the VALUs are busy 80% of the time (fp32, 65536 x 256: 21 us, 90%).
-// k = 2 takes 18 us.  Measured and not kept, on the same rows: rows loaded one pass
-// ahead (no faster; the registers cost a wave per SIMD), 4 waves per SIMD where
-// registers then spill (31 us), merging whole lists across lanes instead of
+// Bound: vector instructions.  131072 x 256 bf16, k = 8, takes 26.8 us (in a
+// replayed graph of such calls) where the 67 MB alone take 13; 689 instructions per
+// 8 tokens, 0.4 of them in sorting and merging, and the VALUs are busy 77% of the
+// time (fp32, 65536 x 256: 20.9 us, 88%).  k = 2 takes 19.1 us.  Measured and not
+// kept, on the same rows, when they took 26 (gates were products then): rows loaded
+// one pass ahead (no faster; the registers cost a wave per SIMD), 4 waves per SIMD
+// where registers then spill (31 us), merging whole lists across lanes instead of
 // taking heads off them (27.4 us), the blocks' sums added by 64-bit atomics
 // (+4 to +10 us).
 template <bool F32, int G, int CH, int KP, bool VEC>
@@ -541,8 +542,8 @@ hipError_t route_choices(const RouteArgs &a, hipStream_t s) {
 
 // The same with longer lists in fewer lanes, for E > 128: fewer steps across
 // lanes per token, but half as many waves.  256 bf16 experts, k = 8: 131072 tokens
-// 25.8 us against 30.2, 8192 tokens 4.23 against 4.26, 1024 tokens 3.97 against 3.56
-// (fp32 keys take twice the registers: 24.5 against 21.1 us for 65536 tokens).
+// 26.8 us against 30.5, 8192 tokens 4.57 against 4.45, 1024 tokens 4.36 against 3.70
+// (fp32 keys take twice the registers: 24.7 against 20.9 us for 65536 tokens).
 constexpr int64_t kManyTokens = 16384;
 template <class F>
 auto by_experts_long(int E, F f) {

@@ -19,11 +19,11 @@ __device__ __forceinline__ void wave_lds_sync() {
 // (which costs less than reading p); its choices are read a row ahead, so that
 // their logits are on the way while the softmax is computed.
 //
-// Bound: memory, with the VALUs busy 86% of the time.  131072 x 256 bf16, k = 8
-// (142 MB with the choices): 27 to 28.5 us, 5.1 TB/s; 65536 x 256 fp32: 25.5 us, 5.5 TB/s; 8192
-// tokens 3.7 and 5.2 us.  All blocks read the same few lines of coef first, which
+// Bound: memory, with the VALUs busy 81% of the time.  131072 x 256 bf16, k = 8
+// (142 MB with the choices): 27 to 29.5 us, 4.8 to 5.3 TB/s; 65536 x 256 fp32: 25 to
+// 26 us, 5.3 to 5.5 TB/s; 8192 tokens 3.8 and 5.6 us.  All blocks read the same few lines of coef first, which
 // serialises them: with 16 single loads a lane instead of 4 wide ones the same
-// take 33.8, 28.8, 6.9 and 6.7 us.  At most 1024 blocks (4 per CU): each pays for
+// took 33.8, 28.8, 6.9 and 6.7 us (against 27, 25.5, 3.7 and 5.2 in that run).  At most 1024 blocks (4 per CU): each pays for
 // its start (2048: 28.1 and 25.5 us).
 template <bool F32, int G, int CH, int S, bool VEC>
 __global__ __launch_bounds__(256) void k_route_backward(RouteBackwardArgs args) {

@@ -154,10 +154,10 @@ __device__ __forceinline__ void exponentials(const Slice<F32, G, CH, VEC> &l, fl
 }
 
 // Lanes and chunks of a token of E experts: f(G, CH).  Measured at E = 256 with
-// 131072 bf16 and 65536 fp32 tokens, k = 8: forward (32, 1) 39.1 and 28.6 us, (16, 2)
-// 30.2 and 21.1, (8, 4) 25.8 and 24.5; gradient 36.9 and 25.9, 28.5 and 25.7, 29.3 and
-// 27.8.  At E = 64 and 8192 tokens (8, 1) 3.3 and 3.7, (4, 2) 3.9 and 4.5; at 131072
-// bf16 11.4 and 11.0.
+// 131072 bf16 and 65536 fp32 tokens, k = 8: forward (32, 1) 40.2 and 29.7 us, (16, 2)
+// 30.5 and 21.2, (8, 4) 26.8 and 24.7; gradient 37.4 and 26.1, 29.4 and 26.0, 29.5 and
+// 27.6.  Forward at E = 64 and 8192 tokens (8, 1) 3.5 and 3.8, (4, 2) 4.3 and 4.9; at
+// 131072 bf16 12.1 and 11.8.
 template <int G, int CH, class F>
 auto shape(F f) {
     return f(std::integral_constant<int, G>(), std::integral_constant<int, CH>());
