@@ -140,15 +140,25 @@ __global__ __launch_bounds__(256) void k_route_backward(RouteBackwardArgs args) 
         for (int s = 0; s < S; s++) asm volatile("" : "+v"(next.id[s]), "+v"(next.dg[s]));
         if (t < a.tokens) {
             T *out = static_cast<T *>(a.dlogits) + t * a.dstride;
+            if (Z == 0.0f) {
+                asm volatile("; a token left out: 0, whatever the loss's gradient is");   // a branch, not selects
+                const float d[W] = {};
 #pragma unroll
-            for (int i = 0; i < L::N; i++) {
-                const int at = L::expert(W * i, g);
-                float d[W];
-                __builtin_memcpy(d, __builtin_assume_aligned(h + at, W < 4 ? 4 : 16), sizeof d);
+                for (int i = 0; i < L::N; i++) {
+                    const int at = L::expert(W * i, g);
+                    if (at < args.E) L::C::store(out + at, d);
+                }
+            } else {
 #pragma unroll
-                for (int j = 0; j < W; j++)
-                    d[j] = __builtin_fmaf(e[W * i + j], __builtin_fmaf(up[W * i + j], inv, dot), d[j]);
-                if (at < args.E) L::C::store(out + at, d);
+                for (int i = 0; i < L::N; i++) {
+                    const int at = L::expert(W * i, g);
+                    float d[W];
+                    __builtin_memcpy(d, __builtin_assume_aligned(h + at, W < 4 ? 4 : 16), sizeof d);
+#pragma unroll
+                    for (int j = 0; j < W; j++)
+                        d[j] = __builtin_fmaf(e[W * i + j], __builtin_fmaf(up[W * i + j], inv, dot), d[j]);
+                    if (at < args.E) L::C::store(out + at, d);
+                }
             }
         }
         wave_lds_sync();

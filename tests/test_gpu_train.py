@@ -729,6 +729,28 @@ def test_ids_out_of_range_are_no_choice():
     assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("E,wide,k", [(12, 13, 3), (64, 64, 8), (256, 256, 8), (1000, 1000, 16)])
+def test_left_out_tokens_get_zeros_whatever_the_loss_is(E, wide, k, dtype):
+    """A loss scale that overflowed, or a bad coefficient, reaches routed tokens
+    only."""
+    T = 45
+    l = logits_of(T, wide, dtype)[:, :E]
+    l[::7] = -math.inf
+    mask = torch.arange(T, device="cuda") % 3 != 1
+    left = ~mask | (torch.arange(T, device="cuda") % 7 == 0)
+    l[1] = math.nan
+    for renorm in (True, False):
+        ids, gates, stats = dq.route(l, k, renorm, mask)
+        coef = dq.balance(stats, k)[1]
+        dg = randn((T, k), torch.float32)
+        for bad in (math.inf, -math.inf, math.nan):
+            broken = coef.clone()
+            broken[E // 2] = bad
+            for kw in (dict(coef=coef, dloss=torch.full((1,), bad, device="cuda")), dict(coef=broken)):
+                d = dq.route_backward(l, ids, dg, renorm=renorm, mask=mask, **kw)
+                assert bool((d[left] == 0).all()) and bool(d[~left].isnan().any(1).all())
+
 # ---- autograd, streams, graphs -----------------------------------------------------
 
 @pytest.mark.parametrize("dtype", DTYPES)
