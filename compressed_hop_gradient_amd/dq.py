@@ -394,12 +394,11 @@ class RouteStats:
     def fold(self):
         """The statistics as one tensor: choices per expert, summed
         probabilities per expert, routed tokens (fp64 [2 experts + 1]).  Those
-        of several processes add up; a change to the tensor is one to these
-        statistics."""
+        of several processes add up; a change to the latest such tensor is one to
+        these statistics.  A fold that has new parts makes a new one and leaves
+        earlier ones as they are."""
         if self.parts:
-            stats = self.sums
-            if stats is None:
-                stats = torch.empty(2 * self.experts + 1, dtype=torch.float64, device=self.device)
+            stats = torch.empty(2 * self.experts + 1, dtype=torch.float64, device=self.device)
             self._balance(1, stats, None, None, None)
             self.sums, self.parts = stats, []
         return self.sums

@@ -806,6 +806,22 @@ def test_balance_on_another_stream_than_the_parts():
         assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
+def test_statistics_that_were_handed_out_keep_their_values():
+    """A fold gives a tensor of its own: later tokens, the fold that a 17th part
+    makes, and later folds leave it alone."""
+    l = logits_of(500, 40, torch.float32)
+    stats = dq.route(l, 4)[2]
+    first = stats.fold()
+    kept = first.clone()
+    for _ in range(dq.ROUTE_MAX_PARTS + 1):
+        dq.route(l, 4, stats=stats)
+    second = stats.fold()
+    assert torch.equal(first, kept) and second[80] == (dq.ROUTE_MAX_PARTS + 2) * 500
+    assert stats.fold() is second                  # nothing new
+    second.mul_(2)                                 # the latest one is the statistics
+    assert torch.equal(dq.balance(stats, 4)[2], second[:40].long())
+
+
 def test_two_forwards_before_their_backwards():
     """Nothing is shared between calls: gradients do not depend on what ran in
     between."""
