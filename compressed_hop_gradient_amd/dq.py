@@ -369,12 +369,15 @@ def _result(t, shape, what, dtype, dev):
 
 class RouteStats:
     """Balance statistics of the workers routed so far: the parts that
-    :func:`route` wrote, folded on demand."""
+    :func:`route` wrote, folded on demand.  The first part holds the scratch of a
+    fold, so calls on one object must not run side by side on several streams (let
+    the later stream wait for the earlier, as for any tensor)."""
 
     def __init__(self, experts, device):
         self.experts, self.device = experts, device
         self.parts = []        # (buffer of dq_route, the part in it, its tokens, the stream it was made on)
         self.sums = None       # what was folded before them, fp64 [2 experts + 1]
+        self._sums_on = None   # the stream that was made on, if it was made here
 
     def _add(self, part, at, tokens):
         if len(self.parts) == ROUTE_MAX_PARTS:
@@ -388,6 +391,8 @@ class RouteStats:
         for part, _, _, made in self.parts:
             if made != now:       # its memory is not to be reused there before this call has read it
                 part.record_stream(torch.cuda.current_stream(self.device))
+        if self.sums is not None and self._sums_on != now:
+            self.sums.record_stream(torch.cuda.current_stream(self.device))
         _call(self.device, "dq_balance", array, n, _opt(self.sums), self.experts, top_k, _opt(stats), _opt(loss),
               _opt(coef), _opt(counts))
 
@@ -400,7 +405,7 @@ class RouteStats:
         if self.parts:
             stats = torch.empty(2 * self.experts + 1, dtype=torch.float64, device=self.device)
             self._balance(1, stats, None, None, None)
-            self.sums, self.parts = stats, []
+            self.sums, self._sums_on, self.parts = stats, _raw_stream(self.device), []
         return self.sums
 
 

@@ -822,6 +822,29 @@ def test_statistics_that_were_handed_out_keep_their_values():
     assert torch.equal(dq.balance(stats, 4)[2], second[:40].long())
 
 
+@pytest.mark.parametrize("form", ["stats", "tensor"])
+@pytest.mark.parametrize("workers", [1, dq.ROUTE_MAX_PARTS + 2])
+def test_balance_on_another_stream_than_the_fold(workers, form):
+    """Folded statistics (the tensor, too) may be dropped right after another
+    stream was given them."""
+    E = 1000
+    ls = [logits_of(300, E, torch.bfloat16, w) for w in range(workers)]
+    want = dq.balance(dq.route(ls, 8)[2].fold(), 8)
+    s = torch.cuda.Stream()
+    for rep in range(20):
+        stats = dq.route(ls, 8)[2]
+        if rep % 2 or form == "tensor" or workers == 1:
+            stats.fold()
+        s.wait_stream(torch.cuda.current_stream())
+        got = dq.balance(stats if form == "stats" else stats.fold(), 8, stream=s)
+        del stats
+        for _ in range(8):                             # the sums' memory, if it is free here
+            torch.full((2 * E + 1,), 7.0, dtype=torch.float64, device="cuda")
+        torch.cuda.current_stream().wait_stream(s)
+        assert torch.equal(got[2], want[2]) and torch.equal(got[1], want[1])
+        assert abs(got[0].item() - want[0].item()) <= 4 * U * want[0].item()
+
+
 def test_two_forwards_before_their_backwards():
     """Nothing is shared between calls: gradients do not depend on what ran in
     between."""

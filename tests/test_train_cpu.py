@@ -234,6 +234,32 @@ def test_rows_of_views():
             dq._rows(bad, "x")
 
 
+def test_folded_statistics_stay_until_other_streams_have_read_them(monkeypatch):
+    """Sums that a fold made on one stream are recorded on the stream of a later
+    balance or fold; a part and its sums on their own stream are not."""
+    now, recorded = [1], []
+    monkeypatch.setattr(dq, "_raw_stream", lambda dev: now[0])
+    monkeypatch.setattr(dq, "_call", lambda *a: None)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda dev=None: now[0])
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: recorded.append((t.data_ptr(), s)))
+    stats = dq.RouteStats(8, torch.device("cpu"))
+    part = torch.empty(64, dtype=torch.uint8)
+    stats._add(part, part.data_ptr(), 4)
+    first = stats.fold()
+    dq.balance(stats, 2)
+    assert recorded == []
+    now[0] = 2
+    dq.balance(stats, 2)
+    assert recorded == [(first.data_ptr(), 2)]
+    stats._add(part, part.data_ptr(), 4)
+    second = stats.fold()                      # reads the first on stream 2, makes another there
+    dq.balance(stats, 2)
+    assert recorded == 2 * [(first.data_ptr(), 2)]
+    now[0] = 1
+    dq.balance(stats, 2)
+    assert recorded[2:] == [(second.data_ptr(), 1)]
+
+
 def test_route_wrapper_checks_the_list():
     with pytest.raises(ValueError):
         train.route([], 2)
