@@ -399,8 +399,10 @@ dq_status dq_mx_allreduce(dq_plan *plan, int32_t format, const void *const *h_gr
  * expert router (folded over the workers, as dq_stats).  Stateless: no plan,
  * every buffer is the caller's.  Errors of all of them: DQ_ENULL, DQ_EINVAL
  * (sizes, strides, kind, alignment of a pointer to its element type, an output
- * that overlaps its operand), DQ_EHIP, and DQ_EWORKSPACE for a part buffer that
- * is missing, too small or misaligned.  Nothing is launched where a check fails. */
+ * that overlaps an operand or another output of the call, of any worker, where
+ * the call does not allow it; row windows of one stride may interleave), DQ_EHIP,
+ * and DQ_EWORKSPACE for a part buffer that is missing, too small or misaligned.
+ * Nothing is launched where a check fails. */
 
 /* y = residual + dropout(x), or dropout(x) with d_residual = NULL.  The mask is
  * a function of (seed, round, worker, site, element) and is never stored:

@@ -631,6 +631,33 @@ def test_workers_of_different_alignment_in_one_launch():
         check_gradient(d, r, dg, coef, 1.0, torch.bfloat16)
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_workers_in_columns_of_one_tensor(dtype):
+    """Logits and gradients of the workers as interleaving windows, gradients in
+    place and beside the logits: as from tensors of their own."""
+    T, E, k = 75, 24, 3
+    wide = logits_of(T, 4 * E, dtype)
+    ls = [wide[:, :E], wide[:, E:2 * E]]
+    ids, gates, stats = dq.route(ls, k)
+    coef = dq.balance(stats, k)[1]
+    dgs = [randn((T, k), torch.float32, w) for w in range(2)]
+    want = dq.route_backward([l.clone() for l in ls], ids, dgs, coef)
+    kept = wide.clone()
+    outs = [wide[:, 3 * E:], wide[:, 2 * E:3 * E]]
+    dq.route_backward(ls, ids, dgs, coef, out=outs)
+    assert all(same(o, d) for o, d in zip(outs, want)) and same(wide[:, :2 * E], kept[:, :2 * E])
+    dq.route_backward(ls, ids, dgs, coef, out=ls)
+    assert all(same(o, d) for o, d in zip(ls, want)) and all(same(o, d) for o, d in zip(outs, want))
+    x = kept[:, :E]
+    y = dq.dropout(x, 0.4, residual=x, out=wide[:, E:2 * E], **KEY)
+    assert same(y, expected_dropout(x, 0.4, x, **KEY).to(dtype)) and same(wide[:, :E], want[0])
+    for bad in ([ls[1], outs[0]], [outs[0], outs[0]], [outs[0], wide[:, 2 * E + 1:3 * E + 1]]):
+        with pytest.raises(dq.DQError):
+            dq.route_backward(ls, ids, dgs, coef, out=bad)
+    with pytest.raises(dq.DQError):
+        dq.route(ls, k, ids=[ids[0], ids[0]])
+
+
 def test_more_workers_than_one_fold_takes():
     E, k, n = 24, 2, 2 * dq.ROUTE_MAX_PARTS + 3
     ls = [logits_of(5 + w, E, torch.float32, w) for w in range(n)]

@@ -197,6 +197,67 @@ def test_route_backward_null_and_empty(lib):
     assert _backward(lib, T=0, l=None, ids=None, out=None) == dq.DQ_OK
 
 
+# Outputs that meet an operand or each other.  T = 8, E = 16, k = 2 bf16: 256 bytes
+# of logits, 64 of ids and of gates, 8 of the mask.
+
+def _route_two(lib, **changed):
+    """Two workers, 1 MB of addresses for every buffer; a change is to the second's
+    or, with an _ in front, to the first's."""
+    first = dict(l=1, mask=2, ids=3, gates=4, part=5)
+    second = dict(l=6, mask=7, ids=8, gates=9, part=10)
+    at = [{n: m * FAKE for n, m in w.items()} for w in (first, second)]
+    for name, v in changed.items():
+        at[0 if name[0] == "_" else 1][name.lstrip("_")] = v
+    io = (dq.dq_route_worker * 2)(*[(w["l"], 8, 16, w["mask"], w["ids"], w["gates"], w["part"], FAKE) for w in at])
+    return lib.dq_route(io, 2, dq.BF16, 16, 2, 1, None)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(ids=6 * FAKE), dict(gates=6 * FAKE + 252), dict(part=6 * FAKE), dict(ids=7 * FAKE + 4), dict(gates=8 * FAKE),
+    dict(gates=8 * FAKE + 60), dict(ids=10 * FAKE + 64), dict(part=9 * FAKE),
+    # with the other worker's
+    dict(ids=1 * FAKE + 128), dict(_ids=6 * FAKE), dict(gates=2 * FAKE), dict(ids=3 * FAKE), dict(ids=4 * FAKE + 32),
+    dict(gates=4 * FAKE), dict(part=5 * FAKE), dict(part=5 * FAKE + 256), dict(_part=1 * FAKE), dict(_gates=10 * FAKE)])
+def test_route_refuses_outputs_that_overlap(lib, bad):
+    assert _route_two(lib, **bad) == dq.DQ_EINVAL
+
+
+def _backward_two(lib, coef=11 * FAKE, dloss=12 * FAKE, stride=16, _stride=16, dstride=16, _dstride=16, **changed):
+    first = dict(l=1, mask=2, ids=3, dg=4, out=5)
+    second = dict(l=6, mask=7, ids=8, dg=9, out=10)
+    at = [{n: m * FAKE for n, m in w.items()} for w in (first, second)]
+    for name, v in changed.items():
+        at[0 if name[0] == "_" else 1][name.lstrip("_")] = v
+    io = (dq.dq_route_grad * 2)(*[(w["l"], 8, s, w["mask"], w["ids"], w["dg"], w["out"], d)
+                                  for w, s, d in zip(at, (_stride, stride), (_dstride, dstride))])
+    return lib.dq_route_backward(io, 2, dq.BF16, 16, 2, 1, coef, dloss, None)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(out=6 * FAKE + 32), dict(out=7 * FAKE), dict(out=8 * FAKE), dict(out=9 * FAKE + 62), dict(out=11 * FAKE + 60),
+    dict(out=12 * FAKE), dict(dloss=10 * FAKE + 252), dict(coef=5 * FAKE),
+    # with the other worker's; in place where that is another worker's logits too
+    dict(out=1 * FAKE), dict(_out=6 * FAKE), dict(out=2 * FAKE), dict(out=3 * FAKE), dict(out=4 * FAKE),
+    dict(out=5 * FAKE), dict(out=5 * FAKE + 224), dict(l=1 * FAKE, out=1 * FAKE), dict(_out=FAKE, l=FAKE + 32),
+    # windows of one tensor that interleave and meet: 3 elements, 1 element, at another stride
+    dict(out=5 * FAKE + 26, dstride=64, _dstride=64), dict(out=5 * FAKE + 98, dstride=64, _dstride=64),
+    dict(out=5 * FAKE + 32, dstride=64, _dstride=48)])
+def test_route_backward_refuses_outputs_that_overlap(lib, bad):
+    assert _backward_two(lib, **bad) == dq.DQ_EINVAL
+
+
+@pytest.mark.parametrize("bad", [
+    dict(sums=FAKE + 8), dict(sums=FAKE - 256), dict(loss=FAKE + 256), dict(coef=FAKE + 64), dict(counts=FAKE),
+    dict(coef=4 * FAKE), dict(loss=3 * FAKE + 60), dict(sums=2 * FAKE), dict(stats=7 * FAKE + 512), dict(loss=7 * FAKE),
+    dict(sums=7 * FAKE + 256), dict(parts=((7 * FAKE, 8), (7 * FAKE + 256, 8))), dict(parts=((7 * FAKE, 8), (7 * FAKE, 9)))])
+def test_balance_refuses_outputs_that_overlap(lib, bad):
+    assert _balance(lib, **bad) == dq.DQ_EINVAL
+
+
+def test_dropout_refuses_an_output_over_its_round_index(lib):
+    for at in (0, 4, 508):
+        assert _dropout(lib, d_round=4 * FAKE + at) == dq.DQ_EINVAL
+
 # ---- refusals of the binding -----------------------------------------------------
 
 def test_binding_refuses_host_tensors_and_types():
