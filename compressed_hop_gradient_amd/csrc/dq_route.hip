@@ -281,7 +281,7 @@ __global__ __launch_bounds__(256, KP == 16 || CH == 4 || !VEC ? 3 : 4) void k_ro
     __shared__ uint32_t hist[C];
     __shared__ float sums[R * C];
     __shared__ uint32_t routed_of[4];
-    const int g = threadIdx.x % G, r = threadIdx.x / G;
+    const int g = threadIdx.x % G, r = threadIdx.x / G, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     for (int j = threadIdx.x; j < C; j += 256) hist[j] = 0;
     __syncthreads();
     float acc[V];
@@ -339,14 +339,17 @@ __global__ __launch_bounds__(256, KP == 16 || CH == 4 || !VEC ? 3 : 4) void k_ro
             }
         }
     }
-    // the block's sums: token rows side by side in LDS, then over the rows
+    // the block's sums: token rows side by side in LDS, then over the rows.  The
+    // thread's number is made again: held over the loop for this, it was spilled
+    // (& 255 tells the compiler its range).
+    const int own = (64 * wave + (int)__builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0))) & 255;
 #pragma unroll
-    for (int v = 0; v < V; v++) sums[r * C + L::expert(v, g)] = acc[v];
+    for (int v = 0; v < V; v++) sums[own / G * C + L::expert(v, own % G)] = acc[v];
     for (int d = 32; d; d >>= 1) routed += __shfl_xor((int)routed, d, 64);
-    if ((threadIdx.x & 63) == 0) routed_of[threadIdx.x >> 6] = routed;
+    if ((own & 63) == 0) routed_of[wave] = routed;
     __syncthreads();
     constexpr int P = C < 256 ? 256 / C : 1;            // threads per column
-    for (int j = threadIdx.x; j < C * P; j += 256) {
+    for (int j = own; j < C * P; j += 256) {
         const int col = j % C, part = j / C;
         float sum = 0.0f;
         for (int i = part; i < R; i += P) sum += sums[i * C + col];
@@ -362,7 +365,7 @@ __global__ __launch_bounds__(256, KP == 16 || CH == 4 || !VEC ? 3 : 4) void k_ro
             a.part.count(args.E)[(int)blockIdx.x * args.E + col] = hist[col];
         }
     }
-    if (threadIdx.x == 0) {
+    if (own == 0) {
         a.part.routed(args.E)[blockIdx.x] = routed_of[0] + routed_of[1] + routed_of[2] + routed_of[3];
         if (blockIdx.x == 0) *a.part.done(args.E) = 0;
     }
@@ -530,21 +533,31 @@ __global__ __launch_bounds__(1024) void k_balance(BalanceArgs a) {
 
 template <bool F32, int G, int CH, bool VEC>
 hipError_t route_choices(const RouteArgs &a, hipStream_t s) {
+    // 8 experts, or long lists of up to 512 experts, are never asked for more than 8
+    constexpr int most_choices = G * CH == 1 || (CH == 4 && G < 32) ? 8 : kRouteMaxTopK;
     int most = 1;
     for (int w = 0; w < a.workers; w++) most = a.worker[w].part.nblk > most ? a.worker[w].part.nblk : most;
     const dim3 grid((unsigned)most, (unsigned)a.workers), block(256);
     if (a.k <= 2) hipLaunchKernelGGL((k_route<F32, G, CH, 2, VEC>), grid, block, 0, s, a);
     else if (a.k <= 4) hipLaunchKernelGGL((k_route<F32, G, CH, 4, VEC>), grid, block, 0, s, a);
-    else if (a.k <= 8 || G * CH == 1) hipLaunchKernelGGL((k_route<F32, G, CH, 8, VEC>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((k_route<F32, G, CH, G * CH == 1 ? 8 : 16, VEC>), grid, block, 0, s, a);
+    else if (a.k <= 8 || most_choices == 8) hipLaunchKernelGGL((k_route<F32, G, CH, 8, VEC>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((k_route<F32, G, CH, most_choices, VEC>), grid, block, 0, s, a);
     return hipGetLastError();
 }
 
-// The same with longer lists in fewer lanes, for E > 128: fewer steps across
-// lanes per token, but half as many waves.  256 bf16 experts, k = 8: 131072 tokens
-// 26.8 us against 30.5, 8192 tokens 4.57 against 4.45, 1024 tokens 4.36 against 3.70
-// (fp32 keys take twice the registers: 24.7 against 20.9 us for 65536 tokens).
+// The same with longer lists in fewer lanes, for bf16 and E > 128: fewer steps
+// across lanes per token, but half as many waves (and fp32 keys take twice the
+// registers: 24.7 against 20.9 us for 65536 x 256).  bf16, us, long lists against short:
+//              131072 x 256   65536 x 512   32768 x 1024   16384 x 256, 512, 1024
+//   k = 2      19.6  21.9     20.1  23.1    20.9  24.0
+//   k = 8      25.3  28.4     26.1  31.1    27.8  33.7     6.8  7.0  10.5  11.1  16.9  19.1
+//   k = 16     42.2  39.5     42.2  42.5    35.9  46.4    10.1  9.0  15.2  14.6  20.3  25.3
+// (k = 16 up to 512 experts: 16 keys beside the lists do not fit the registers), and
+// with k = 8 of 256, 8192 tokens 4.57 against 4.45, 1024 tokens 4.36 against 3.70.
 constexpr int64_t kManyTokens = 16384;
+inline bool long_lists(int64_t tokens, int E, int k) {
+    return tokens >= kManyTokens && E > 128 && (k <= 8 || E > 512);
+}
 template <class F>
 auto by_experts_long(int E, F f) {
     if (E <= 256) return shape<8, 4>(f);
@@ -561,7 +574,7 @@ hipError_t route_experts(const RouteArgs &a, hipStream_t s) {
         tokens += a.worker[w].tokens;
     }
     if constexpr (!F32)
-        if (vec && a.E > 128 && tokens >= kManyTokens)
+        if (vec && long_lists(tokens, a.E, a.k))
             return by_experts_long(a.E, [&](auto G, auto CH) { return route_choices<F32, G.value, CH.value, true>(a, s); });
     return by_experts(a.E, [&](auto G, auto CH) {
         return vec ? route_choices<F32, G.value, CH.value, true>(a, s)

@@ -2,6 +2,7 @@
 compare with (dithers against the oracle's Philox, gradients against
 differences), and the argument checks of the C ABI and the binding."""
 import ctypes as C
+import re
 
 import numpy as np
 import pytest
@@ -80,6 +81,17 @@ def test_balance_is_one_when_balanced():
     l[:] = -20.0
     l[:, 0] = 20.0
     assert abs(ref.balance([ref.Routed(l, 1)])[0] - 4.0) < 1e-12      # all on one of four
+
+
+# ---- the built kernels -----------------------------------------------------------
+
+def test_no_kernel_uses_scratch_memory(lib):
+    """By the kernels' metadata in the library (its values below 128 are one byte)."""
+    with open(dq.LIB_PATH, "rb") as f:
+        image = f.read()
+    for key in (rb"private_segment_fixed_size", rb"vgpr_spill_count"):
+        found = re.findall(rb"\." + key + rb"(.)", image, re.S)
+        assert len(found) > 200 and set(found) == {b"\0"}
 
 
 # ---- refusals of the C ABI -------------------------------------------------------
