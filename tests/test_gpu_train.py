@@ -703,6 +703,100 @@ def test_route_many_tokens_and_the_same_bits_again(T, E, k, dtype):
     assert bool((err <= 2 * (c + 44) * U * mag + half_step(dtype) * want.abs() * 1.01 + 1e-37).all())
 
 
+def routed_in_fp64(l, k, renorm, mask):
+    """(ids, gates, p) by torch in fp64: stable sorting keeps equal logits (-0 = +0)
+    by index and has NaN first."""
+    x = l.double()
+    ok = ~(x == -math.inf).all(1)
+    ok = ok if mask is None else ok & mask
+    v, order = torch.sort(x, dim=1, descending=True, stable=True)
+    ids = torch.where(ok[:, None] & (v[:, :k] != -math.inf), order[:, :k], -1)
+    p = torch.where(ok[:, None], torch.softmax(x, 1), 0.0)
+    g = torch.where(ids >= 0, p.gather(1, ids.clamp(min=0)), 0.0)
+    return ids, torch.where(ids >= 0, g / g.sum(1, keepdim=True), 0.0) if renorm else g, p
+
+
+@pytest.mark.parametrize("odd", [False, True])
+@pytest.mark.parametrize("E,sizes", [(136, [12000, 4500, 33]), (256, [40001]), (256, [12000, 0, 4500, 33]),
+                                     (384, [16500]), (512, [12000, 4500, 33]), (513, [16400]), (1000, [16400]),
+                                     (1024, [12000, 4500, 33])])
+def test_route_many_tokens_of_many_experts(E, sizes, odd):
+    """bf16 beyond 16384 tokens a call and 128 experts, where lists grow longer: every
+    number of choices, masks, closed experts, ties, zeros of both signs; with odd,
+    rows of NaN and +inf too (their probabilities, NaN, go into no sum here)."""
+    ls, masks = [], []
+    for n, T in enumerate(sizes):
+        l = logits_of(T, E, torch.float32, n + 1)
+        l[::3] = l[::3].round()                                       # ties, zeros of both signs among them
+        l[1::7] = torch.where(l[1::7] > 0.5, -0.0, 0.0)               # only zeros
+        l[2::5] = torch.where(torch.randn(l[2::5].shape, generator=torch.Generator("cuda").manual_seed(n), device="cuda")
+                              < 0.3, -math.inf, l[2::5])
+        l[4::11] = -math.inf
+        if T > 20:
+            l[15, E // 2 + 1:] = -math.inf
+            l[15, :E // 2] = -math.inf                                # one open expert
+        if odd:
+            l[3::13, E // 3] = math.nan
+            l[5::17, E - 1] = math.inf
+        ls.append(l.bfloat16())
+        masks.append(None if n == 1 else torch.arange(T, device="cuda") % 9 != 4)
+    finite = [l[l.isfinite()].double() for l in ls if len(l)]
+    c = 2 * (3 * max((f.max() - f.min()).item() for f in finite) + 48)
+    for k in (1, 2, 3, 4, 8, 9, 16):
+        renorm = k % 2 == 0
+        ids, gates, stats = dq.route(ls, k, renorm, masks)
+        count, psum, tokens = torch.zeros(E, device="cuda"), torch.zeros(E, dtype=torch.float64, device="cuda"), 0
+        for l, m, i, g in zip(ls, masks, ids, gates):
+            wi, wg, p = routed_in_fp64(l, k, renorm, m)
+            assert torch.equal(i.long(), wi)
+            assert torch.equal(g.isnan(), wg.isnan())
+            assert bool(((g.double() - wg).abs() <= c * U * wg + 1e-37)[~wg.isnan()].all())
+            count += torch.bincount(wi.reshape(-1) + 1, minlength=E + 1)[1:]
+            psum += p.sum(0)
+            tokens += int((wi[:, 0] >= 0).sum())
+        s = stats.fold()
+        assert torch.equal(s[:E], count.double()) and s[2 * E] == tokens
+        if not odd:
+            assert bool(((s[E:2 * E] - psum).abs() <= (c + max(sizes)) * U * psum + 1e-37).all())
+
+
+@pytest.mark.parametrize("E", [250, 1000])
+@pytest.mark.parametrize("sizes", [[9000, 3001], [9000, 3001, 0, 1], [2000, 1] * 8])
+def test_balance_of_many_rows_of_several_parts(sizes, E):
+    """Parts of unequal size, more rows than one block folds; alone, after earlier
+    sums, and with the sums overwritten by the result (the C call allows it)."""
+    k = 4
+    ls = [logits_of(T, E, torch.bfloat16, n + 1) for n, T in enumerate(sizes)]
+    outs = [dq.route(l, k)[2] for l in ls]
+    parts = (dq.dq_route_part * len(ls))(*[(o.parts[0][1], T) for o, T in zip(outs, sizes)])
+    want = torch.zeros(2 * E + 1, dtype=torch.float64, device="cuda")
+    span = 0.0
+    for l in ls:
+        ids, _, p = routed_in_fp64(l, k, True, None)
+        want[:E] += torch.bincount(ids.reshape(-1), minlength=E)
+        want[E:2 * E] += p.sum(0)
+        want[2 * E] += len(l)
+        span = max(span, (l.double().max() - l.double().min()).item() if len(l) else 0.0)
+    most = 2 * (3 * span + 48) + max(sizes)
+    before = dq.route(logits_of(70, E, torch.bfloat16, 99), k)[2].fold()
+    for sums in (None, before, before.clone()):
+        stats = sums if sums is not None and sums is not before else torch.empty_like(want)
+        total = want if sums is None else want + before
+        n = total[2 * E].item()
+        loss, coef = torch.empty(1, device="cuda"), torch.empty(E, device="cuda")
+        counts = torch.empty(E, dtype=torch.int64, device="cuda")
+        rc = dq.lib().dq_balance(parts, len(ls), None if sums is None else sums.data_ptr(), E, k, stats.data_ptr(),
+                                 loss.data_ptr(), coef.data_ptr(), counts.data_ptr(),
+                                 torch.cuda.current_stream().cuda_stream)
+        assert rc == dq.DQ_OK
+        assert torch.equal(stats[:E], total[:E]) and stats[2 * E] == n and torch.equal(counts, total[:E].long())
+        assert bool(((stats[E:2 * E] - total[E:2 * E]).abs() <= most * U * total[E:2 * E]).all())
+        wc = E * total[:E] / (k * n * n)
+        assert bool(((coef.double() - wc).abs() <= 2 * U * wc).all())
+        wl = (wc * total[E:2 * E]).sum().item()
+        assert abs(loss.item() - wl) <= (most + 4) * U * wl
+
+
 def test_route_loss_of_many_tokens():
     """fp32 sums stay short: 2^20 tokens, loss against fp64."""
     T, E, k = 1 << 20, 16, 2
