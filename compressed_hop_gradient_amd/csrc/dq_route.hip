@@ -1,6 +1,8 @@
 // dq_route.hip -- expert router for gfx950: softmax, choice of the top_k experts,
 // gates and balance statistics of every token in one pass over the logits, and
 // the balance loss.  fp32 arithmetic, no contraction.
+#include <algorithm>
+
 #include "dq_route_device.h"
 
 namespace dq {
@@ -585,10 +587,14 @@ hipError_t route_experts(const RouteArgs &a, hipStream_t s) {
 }  // namespace
 
 int route_blocks(int64_t tokens, int E) {
-    // at most what the chip holds at once
+    // 4 or 6 blocks of 256 threads per CU, about what the chip holds at once (3 of the
+    // kernels compiled for 3 waves per SIMD), and more of them where a lane would add
+    // more than 64 tokens' probabilities in fp32: one sum of 5461 equal terms was off
+    // by 5e-5.  (Up to 2^22 sums, 50 MB a part: 2^24 tokens of 256 experts.)
     const int64_t rows = by_experts(E, [](auto G, auto) { return 256 / G.value; });
-    const int64_t most = by_experts(E, [](auto, auto CH) { return 256 * (CH.value == 1 ? 6 : 4); });
-    const int64_t want = (tokens + rows - 1) / rows;
+    const int64_t chip = by_experts(E, [](auto, auto CH) { return 256 * (CH.value == 1 ? 6 : 4); });
+    const int64_t few_terms = std::min((tokens + 64 * rows - 1) / (64 * rows), (int64_t)(1 << 22) / E);
+    const int64_t want = (tokens + rows - 1) / rows, most = std::max(chip, few_terms);
     return (int)(want < 1 ? 1 : want < most ? want : most);
 }
 

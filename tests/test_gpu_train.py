@@ -703,6 +703,20 @@ def test_route_many_tokens_and_the_same_bits_again(T, E, k, dtype):
     assert bool((err <= 2 * (c + 44) * U * mag + half_step(dtype) * want.abs() * 1.01 + 1e-37).all())
 
 
+def test_route_sums_of_very_many_tokens():
+    """2^31 tokens that are all alike (one row, stride 0): every addition to an fp32
+    sum rounds the same way, so only few may go into one."""
+    T, E = 1 << 31, 7
+    row = torch.zeros(1, E, dtype=torch.bfloat16, device="cuda")
+    print("[route] 2^31 tokens", flush=True)
+    ids, gates, stats = dq.route(row.expand(T, E), 1)
+    assert bool((ids == 0).all()) and bool((gates == 1).all())
+    s = stats.fold().cpu()
+    assert s[0] == T and s[2 * E] == T and s[1:E].eq(0).all()
+    # roundings of p as everywhere (no span), 64 additions in a lane, 40 between lanes
+    assert bool(((s[E:2 * E] - T / E).abs() <= (2 * 48 + 64 + 40) * U * T / E).all())
+
+
 def routed_in_fp64(l, k, renorm, mask):
     """(ids, gates, p) by torch in fp64: stable sorting keeps equal logits (-0 = +0)
     by index and has NaN first."""
