@@ -998,6 +998,43 @@ def test_reduce_sees_the_statistics():
     assert abs(doubled.loss.item() - alone.loss.item()) <= 4 * U * alone.loss.item()
 
 
+def _routing_of_rank(rank, port, path):
+    """One of two processes, each with its own worker's tokens."""
+    import torch.distributed as dist
+    dist.init_process_group("gloo", init_method=f"tcp://127.0.0.1:{port}", rank=rank, world_size=2)
+
+    def reduce(stats):
+        host = stats.cpu()                           # gloo works on host tensors
+        dist.all_reduce(host)
+        stats.copy_(host)
+
+    l = logits_of((300, 77)[rank], 64, torch.bfloat16, rank).requires_grad_()
+    r = train.route(l, 4, reduce=reduce)
+    dl, = torch.autograd.grad(r.loss, l)
+    torch.save([t.detach().cpu() for t in (r.ids, r.gates, r.loss, r.coef, r.counts, dl)], f"{path}{rank}")
+    dist.destroy_process_group()
+
+
+def test_reduce_over_two_processes(tmp_path):
+    """The balance loss of two processes' workers is the one that a process with both
+    computes, and so is each one's part of the gradient."""
+    import socket
+    import torch.multiprocessing as mp
+    ls = [logits_of(T, 64, torch.bfloat16, n).requires_grad_() for n, T in enumerate((300, 77))]
+    r = train.route(ls, 4)
+    dls = torch.autograd.grad(r.loss, ls)
+    with socket.socket() as s:
+        s.bind(("127.0.0.1", 0))
+        port = s.getsockname()[1]
+    mp.spawn(_routing_of_rank, args=(port, str(tmp_path / "r")), nprocs=2, join=True)
+    for rank in range(2):
+        ids, gates, loss, coef, counts, dl = torch.load(tmp_path / f"r{rank}", weights_only=True)
+        assert torch.equal(ids, r.ids[rank].cpu()) and torch.equal(gates, r.gates[rank].detach().cpu())
+        assert torch.equal(counts, r.counts.cpu()) and torch.equal(coef, r.coef.cpu())
+        assert abs(loss.item() - r.loss.item()) <= 4 * U * r.loss.item()
+        assert same(dl, dls[rank])
+
+
 def test_route_on_another_stream():
     l = logits_of(5000, 64, torch.bfloat16)
     want = dq.route(l, 8)
