@@ -11,10 +11,10 @@ namespace {
 // keeps an element; the gradient by x is the same m s on dy.  Every operand is
 // touched once, and what is left to do is the mask: one generator call for 8
 // elements (16 random bits each), so that its 20 64-bit products are shared and
-// memory stays the bound, with the VALUs busy 59% of the time (bf16, no residual).
+// memory stays the bound, with the VALUs busy 62% of the time (bf16, no residual).
 //
 // 16384 x 8192 bf16 with a residual (805 MB): 136 us, 5.9 TB/s; 8192 x 8192 bf16
-// without one (268 MB): 46 us, 5.8 TB/s; 8192 x 2048 fp32 (134 MB): 25 us, 5.3 TB/s.
+// without one (268 MB): 45 us, 6.0 TB/s; 8192 x 2048 fp32 (134 MB): 25 us, 5.3 TB/s.
 // A copy of 256 MB reaches 5.5 TB/s on the same card.
 
 // The eight 16-bit dithers of elements 8b .. 8b + 7 as four words, low half

@@ -257,19 +257,23 @@ __device__ __forceinline__ void pick_any(const Slice<F32, G, CH, VEC> &l, uint32
 
 // p = softmax(l), the k largest l, their p (divided by their sum with renorm), and
 // per block the sums over its tokens that the balance loss needs: one pass, a
-// row is read once.  All of it is per lane but four reductions over G lanes.  The
+// row is read once.  All of it is per lane but KP + 1 reductions over G lanes (the
+// heads of the lists, the softmax's denominator) and with renorm one more.  The
 // probabilities are summed in the lanes' registers over all rows of a block and
 // meet in LDS at its end; choices are counted in LDS.
 //
-// Bound: vector instructions.  131072 x 256 bf16, k = 8, takes 26.8 us (in a
+// Bound: vector instructions.  131072 x 256 bf16, k = 8, takes 25.1 to 26.4 us (in a
 // replayed graph of such calls) where the 67 MB alone take 13; 689 instructions per
-// 8 tokens, 0.4 of them in sorting and merging, and the VALUs are busy 77% of the
-// time (fp32, 65536 x 256: 20.9 us, 88%).  k = 2 takes 19.1 us.  Measured and not
-// kept, on the same rows, when they took 26 (gates were products then): rows loaded
-// one pass ahead (no faster; the registers cost a wave per SIMD), 4 waves per SIMD
-// where registers then spill (31 us), merging whole lists across lanes instead of
-// taking heads off them (27.4 us), the blocks' sums added by 64-bit atomics
-// (+4 to +10 us).
+// 8 tokens, 0.4 of them in sorting and merging, and the VALUs are busy 76% of the
+// time (fp32, 65536 x 256: 21.1 to 22.3 us, 88%; 131072 x 64 bf16: 12.0 us where 17 MB
+// and the 8 MB of results take 5, 82%).  k = 2 takes 19.6 us.  Rows with zeros among
+// the choices go through pick_any: where all logits are 0, as before the first step of
+// a router that starts so, the same rows take 59 us (k = 2 31, 64 experts 19).
+// Measured and not kept, on the same rows, when they took 26 (gates were products
+// then): rows loaded one pass ahead (no faster; the registers cost a wave per SIMD),
+// 4 waves per SIMD where registers then spill (31 us), merging whole lists across
+// lanes instead of taking heads off them (27.4 us), the blocks' sums added by 64-bit
+// atomics (+4 to +10 us); long sums cut by a second sum in LDS (+0.3 to +2.5 us).
 template <bool F32, int G, int CH, int KP, bool VEC>
 __global__ __launch_bounds__(256, KP == 16 || CH == 4 || !VEC ? 3 : 4) void k_route(RouteArgs args) {
     const RouteWorker &a = args.worker[blockIdx.y];
@@ -549,13 +553,13 @@ hipError_t route_choices(const RouteArgs &a, hipStream_t s) {
 
 // The same with longer lists in fewer lanes, for bf16 and E > 128: fewer steps
 // across lanes per token, but half as many waves (and fp32 keys take twice the
-// registers: 24.7 against 20.9 us for 65536 x 256).  bf16, us, long lists against short:
-//              131072 x 256   65536 x 512   32768 x 1024   16384 x 256, 512, 1024
-//   k = 2      19.6  21.9     20.1  23.1    20.9  24.0
-//   k = 8      25.3  28.4     26.1  31.1    27.8  33.7     6.8  7.0  10.5  11.1  16.9  19.1
-//   k = 16     42.2  39.5     42.2  42.5    35.9  46.4    10.1  9.0  15.2  14.6  20.3  25.3
+// registers: 23.6 against 22.0 us for 65536 x 256).  bf16, us, long lists and short:
+//            131072 x 256  65536 x 512  32768 x 1024  16384 x 256   512         1024
+//   k = 2    19.6  21.8    19.7  22.4   21.2  24.4
+//   k = 8    25.7  29.3    26.0  31.0   27.7  33.5     6.7  6.7   10.6  11.1  17.3  19.6
+//   k = 16   42.8  39.4    43.1  42.4   34.7  45.9     9.8  8.6   15.6  14.8  20.5  25.5
 // (k = 16 up to 512 experts: 16 keys beside the lists do not fit the registers), and
-// with k = 8 of 256, 8192 tokens 4.57 against 4.45, 1024 tokens 4.36 against 3.70.
+// with k = 8 of 256, 8192 tokens 4.9 against 4.8, 1024 tokens 4.6 against 4.0.
 constexpr int64_t kManyTokens = 16384;
 inline bool long_lists(int64_t tokens, int E, int k) {
     return tokens >= kManyTokens && E > 128 && (k <= 8 || E > 512);

@@ -20,8 +20,8 @@ __device__ __forceinline__ void wave_lds_sync() {
 // their logits are on the way while the softmax is computed.
 //
 // Bound: memory, with the VALUs busy 81% of the time.  131072 x 256 bf16, k = 8
-// (142 MB with the choices): 27 to 29.5 us, 4.8 to 5.3 TB/s; 65536 x 256 fp32: 25 to
-// 26 us, 5.3 to 5.5 TB/s; 8192 tokens 3.8 and 5.6 us.  All blocks read the same few lines of coef first, which
+// (142 MB with the choices): 27 to 30 us, 4.7 to 5.3 TB/s; 65536 x 256 fp32: 25 to
+// 26.5 us, 5.3 to 5.5 TB/s; 8192 tokens 4.1 and 5.9 us.  All blocks read the same few lines of coef first, which
 // serialises them: with 16 single loads a lane instead of 4 wide ones the same
 // took 33.8, 28.8, 6.9 and 6.7 us (against 27, 25.5, 3.7 and 5.2 in that run).  At most 1024 blocks (4 per CU): each pays for
 // its start (2048: 28.1 and 25.5 us).

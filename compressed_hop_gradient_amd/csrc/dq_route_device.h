@@ -126,8 +126,12 @@ __device__ __forceinline__ float reciprocal(float x) {
 
 // exp(l - m) where m is the row's largest logit, or 0.  The exponent takes one
 // fma, whose rounding of m log2 e is the same factor for all of the row and
-// cancels in quotients.  Up to |m| = 2^20 that factor is within 2^(1/22) of 1;
-// far from zero it would pass every bound, and the difference comes first.
+// cancels in quotients.  Up to |m| = 2^20 that factor is within 2^(1/16) of 1;
+// far from zero it would pass every bound, and the difference comes first.  Beside
+// that factor a value is off by at most (1.25 |l - m| + 2) 2^-24 of itself: half a step
+// of the exponent, log2 e's own rounding and the instruction's last place.
+// (One token of 64 experts is off by 8e-8 in its outputs, where a library's exp
+// leaves 2e-8.)  A longer exponent would cost instructions, which are the bound.
 constexpr float kFar = 1048576.0f;
 __device__ __forceinline__ float exponential(float l, float m) {
     const float x = __builtin_fmaf(l, kLog2e, -m * kLog2e), y = (l - m) * kLog2e;
@@ -154,10 +158,10 @@ __device__ __forceinline__ void exponentials(const Slice<F32, G, CH, VEC> &l, fl
 }
 
 // Lanes and chunks of a token of E experts: f(G, CH).  Measured at E = 256 with
-// 131072 bf16 and 65536 fp32 tokens, k = 8: forward (32, 1) 40.2 and 29.7 us, (16, 2)
-// 30.5 and 21.2, (8, 4) 26.8 and 24.7; gradient 37.4 and 26.1, 29.4 and 26.0, 29.5 and
-// 27.6.  Forward at E = 64 and 8192 tokens (8, 1) 3.5 and 3.8, (4, 2) 4.3 and 4.9; at
-// 131072 bf16 12.1 and 11.8.
+// 131072 bf16 and 65536 fp32 tokens, k = 8: forward (32, 1) 39.0 and 30.9 us, (16, 2)
+// 30.0 and 22.1, (8, 4) 26.2 and 23.6; gradient 37.4 and 26.4, 28.8 and 26.0, 29.2 and
+// 28.0.  Forward at E = 64 and 8192 tokens (8, 1) 3.7 and 3.9, (4, 2) 4.5 and 5.1; at
+// 131072 bf16 12.0 and 11.8.
 template <int G, int CH, class F>
 auto shape(F f) {
     return f(std::integral_constant<int, G>(), std::integral_constant<int, CH>());

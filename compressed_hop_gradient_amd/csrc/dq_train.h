@@ -1,5 +1,6 @@
 // dq_train.h -- declarations shared by the training-step entry points
-// (dq_train_api.cpp) and their kernels (dq_train.hip).  Not part of the public ABI.
+// (dq_train_api.cpp) and their kernels (dq_dropout.hip, dq_route.hip,
+// dq_route_backward.hip).  Not part of the public ABI.
 #pragma once
 
 #include <hip/hip_runtime.h>

@@ -501,8 +501,9 @@ def route(logits, top_k, renorm=True, mask=None, stats=None, ids=None, gates=Non
 def balance(stats, top_k):
     """Balance loss of the tokens in ``stats`` (``dq_balance``), a
     :class:`RouteStats` or the tensor that its ``fold`` gives: returns (loss [1] fp32,
-    coef [experts] fp32, counts [experts] int64).  ``coef`` is the loss's
-    derivative by any token's probabilities, which :func:`route_backward` takes."""
+    coef [experts] fp32, counts [experts] int64).  ``top_k`` is that of the route
+    calls.  ``coef`` is the loss's derivative by any token's probabilities, which
+    :func:`route_backward` takes."""
     if isinstance(stats, torch.Tensor):
         if stats.dim() != 1 or stats.numel() < 3 or stats.numel() % 2 == 0:
             raise ValueError(f"stats: shape {tuple(stats.shape)}, expected [2 experts + 1]")
