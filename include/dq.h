@@ -494,8 +494,8 @@ dq_status dq_balance(const dq_route_part *h_parts, int32_t n_parts, const double
  *   without: dl_j = p_j (a_j - sum p a - sum g dg) + [j chosen] g_j dg_j
  * A token that was left out or has every logit -inf gets zeros, whatever d_coef,
  * d_dloss and d_dgates hold.  d_dlogits has the logits' kind, row t at element
- * t * dstride (dstride >= n_experts), and may be d_logits (same stride).  Entries of d_ids outside 0..n_experts-1 count as -1.  h_workers is a
- * HOST array. */
+ * t * dstride (dstride >= n_experts), and may be d_logits (same stride).  Entries
+ * of d_ids outside 0..n_experts-1 count as -1.  h_workers is a HOST array. */
 typedef struct dq_route_grad {
     const void *d_logits;
     int64_t tokens, stride;
