@@ -18,29 +18,10 @@ namespace {
 // A copy of 256 MB reaches 5.5 TB/s on the same card.
 
 // The eight 16-bit dithers of elements 8b .. 8b + 7 as four words, low half
-// first: Philox4x32-10 (Salmon et al., SC'11) on (b, worker, round, site).  A
-// product is one 64-bit multiply, a three-way xor one instruction.  The compiler may
-// hold all round keys (the codec's kernels may not): 57 to 106 SGPRs, none spilled.
+// first: Philox on (b, worker, round, site).  The compiler may hold all round keys
+// (the codec's kernels may not): 57 to 106 SGPRs, none spilled.
 __device__ __forceinline__ void dropout_words(uint64_t b, const DropoutArgs &a, uint32_t round, uint32_t w[4]) {
-    uint32_t x0 = (uint32_t)b, x1 = (uint32_t)(b >> 32) | a.worker << 16, x2 = round, x3 = 0x80000000u | a.site;
-    uint32_t k0 = a.key0, k1 = a.key1;
-#pragma unroll
-    for (int r = 0; r < 10; r++) {
-        if (r > 0) {
-            k0 += 0x9E3779B9u;
-            k1 += 0xBB67AE85u;
-        }
-        const uint64_t pa = (uint64_t)0xD2511F53u * x0;
-        const uint64_t pb = (uint64_t)0xCD9E8D57u * x2;
-        x0 = xor3((uint32_t)(pb >> 32), x1, k0);
-        x1 = (uint32_t)pb;
-        x2 = xor3((uint32_t)(pa >> 32), x3, k1);
-        x3 = (uint32_t)pa;
-    }
-    w[0] = x0;
-    w[1] = x1;
-    w[2] = x2;
-    w[3] = x3;
+    philox_words((uint32_t)b, (uint32_t)(b >> 32) | a.worker << 16, round, 0x80000000u | a.site, a.key0, a.key1, w);
 }
 
 __device__ __forceinline__ uint32_t dither(const uint32_t w[4], int j) {

@@ -9,8 +9,33 @@ namespace {
 
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 
+__device__ __forceinline__ int clampi(int x, int lo, int hi) { return x < lo ? lo : x > hi ? hi : x; }
+
 __device__ __forceinline__ uint32_t xor3(uint32_t a, uint32_t b, uint32_t c) {
     return __builtin_amdgcn_bitop3_b32(a, b, c, 0x96);
+}
+
+// Philox4x32-10 (Salmon et al., SC'11) of counter (x0, x1, x2, x3).  A product is one
+// 64-bit multiply, a three-way xor one instruction.
+__device__ __forceinline__ void philox_words(uint32_t x0, uint32_t x1, uint32_t x2, uint32_t x3, uint32_t k0,
+                                             uint32_t k1, uint32_t w[4]) {
+#pragma unroll
+    for (int r = 0; r < 10; r++) {
+        if (r > 0) {
+            k0 += 0x9E3779B9u;
+            k1 += 0xBB67AE85u;
+        }
+        const uint64_t pa = (uint64_t)0xD2511F53u * x0;
+        const uint64_t pb = (uint64_t)0xCD9E8D57u * x2;
+        x0 = xor3((uint32_t)(pb >> 32), x1, k0);
+        x1 = (uint32_t)pb;
+        x2 = xor3((uint32_t)(pa >> 32), x3, k1);
+        x3 = (uint32_t)pa;
+    }
+    w[0] = x0;
+    w[1] = x1;
+    w[2] = x2;
+    w[3] = x3;
 }
 
 // fp32 -> bf16 bits, round to nearest even (NaN stays NaN)

@@ -28,6 +28,10 @@ MX_FP8_E4M3, MX_FP6_E3M2, MX_FP6_E2M3, MX_FP4_E2M1 = 0, 1, 2, 3
 OPT_EPS = 0   # dq_option_f64
 ROUTE_RENORM = 1   # dq_route_flags
 ROUTE_MAX_PARTS = 16
+EXPERT_GATHER, EXPERT_TURNED = 1, 2   # dq_expert_flags
+GATHER_NONE, GATHER_X, GATHER_DOUT = 0, 1, 2
+KEEP_DITHER = 1
+ACT_SWIGLU, ACT_RELU = 0, 1
 KERNEL_KINDS = ("stats", "allocate", "reorder", "compress", "hop_grad", "hop_packed",
                 "finalize", "mxfp8", "hop_final")
 
@@ -62,6 +66,16 @@ class dq_route_grad(C.Structure):
 
 class dq_route_part(C.Structure):
     _fields_ = [("d_part", C.c_void_p), ("tokens", C.c_int64)]
+
+
+class dq_expert_lists(C.Structure):
+    _fields_ = [("d_offsets", C.c_void_p), ("d_source", C.c_void_p), ("d_row", C.c_void_p), ("tokens", C.c_int64),
+                ("top_k", C.c_int32), ("n_experts", C.c_int32)]
+
+
+class dq_keep_key(C.Structure):
+    _fields_ = [("seed", C.c_uint64), ("d_round", C.c_void_p), ("round", C.c_uint32), ("worker", C.c_int32),
+                ("site", C.c_uint32), ("flags", C.c_int32)]
 
 
 class DQError(RuntimeError):
@@ -118,6 +132,26 @@ _SIGS = {
                              C.c_void_p, C.c_void_p, C.c_void_p]),
     "dq_route_backward": (C.c_int, [C.c_void_p, C.c_int32, C.c_int32, C.c_int32, C.c_int32, C.c_int32, C.c_void_p,
                                     C.c_void_p, C.c_void_p]),
+    "dq_expert_rows_bytes": (C.c_size_t, [C.c_int64, C.c_int32, C.c_int32]),
+    "dq_expert_rows": (C.c_int, [C.c_void_p, C.c_int64, C.c_int32, C.c_int32, C.c_void_p, C.c_void_p, C.c_void_p,
+                                 C.c_void_p, C.c_size_t, C.c_void_p]),
+    "dq_expert_matmul": (C.c_int, [C.c_void_p, C.c_void_p, C.c_int64, C.c_int32, C.c_void_p, C.c_int64, C.c_int64,
+                                   C.c_void_p, C.c_int64, C.c_int32, C.c_int64, C.c_int64, C.c_void_p]),
+    "dq_expert_matmul_grad_bytes": (C.c_size_t, [C.c_int64, C.c_int32, C.c_int32, C.c_int32, C.c_int64, C.c_int64]),
+    "dq_expert_matmul_grad": (C.c_int, [C.c_void_p, C.c_void_p, C.c_int64, C.c_void_p, C.c_void_p, C.c_void_p,
+                                        C.c_int64, C.c_int32, C.c_void_p, C.c_int32, C.c_int32, C.c_int64,
+                                        C.c_int64, C.c_void_p, C.c_size_t, C.c_void_p]),
+    "dq_expert_sum": (C.c_int, [C.c_void_p, C.c_void_p, C.c_int64, C.c_void_p, C.c_int64, C.c_void_p, C.c_int64,
+                                C.c_int32, C.c_int64, C.c_void_p]),
+    "dq_keep8": (C.c_int, [C.c_void_p, C.c_int32, C.c_int64, C.c_int64, C.c_int64, C.c_void_p, C.c_void_p, C.c_void_p,
+                           C.c_void_p]),
+    "dq_restore8": (C.c_int, [C.c_void_p, C.c_void_p, C.c_int32, C.c_int64, C.c_int64, C.c_void_p, C.c_int64,
+                              C.c_void_p]),
+    "dq_expert_act": (C.c_int, [C.c_void_p, C.c_int32, C.c_void_p, C.c_int64, C.c_void_p, C.c_void_p, C.c_int64,
+                                C.c_int32, C.c_int64, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p]),
+    "dq_expert_act_backward": (C.c_int, [C.c_void_p, C.c_int32, C.c_void_p, C.c_int64, C.c_void_p, C.c_void_p,
+                                         C.c_void_p, C.c_int64, C.c_void_p, C.c_void_p, C.c_int64, C.c_void_p,
+                                         C.c_int64, C.c_void_p, C.c_int32, C.c_int64, C.c_void_p]),
     "dq_get_info": (C.c_int, [C.c_void_p, C.POINTER(dq_info), C.c_void_p]),
     "dq_timing_read": (C.c_int, [C.c_void_p, C.POINTER(dq_timing)]),
     "dq_status_string": (C.c_char_p, [C.c_int32]),
@@ -575,6 +609,334 @@ def route_backward(logits, ids, dgates=None, coef=None, dloss=None, renorm=True,
     io = dq_route_grad(*_grad_fields(logits, ids, dgates, mask, out))
     _route_grad(C.byref(io), 1, logits, ids, coef, dloss, renorm)
     return out
+
+
+# ---- experts (every call takes stream=, as above) ---------------------------------
+
+_ACTS = {"swiglu": ACT_SWIGLU, "relu": ACT_RELU}
+
+
+def _round_of(rnd, dev):
+    """(number, device pointer) of a round index: an int, or one int32 element
+    that the kernel reads."""
+    if isinstance(rnd, torch.Tensor):
+        return 0, _tensor(rnd, "rnd", dev, numel=1, dtype=torch.int32).data_ptr()
+    return rnd, None
+
+
+def _keep_key(dither, seed, rnd, worker, site, dev):
+    rnd, d_round = _round_of(rnd, dev)
+    # beyond these, marshalling would wrap them into other numbers
+    if not (0 <= rnd < 1 << 32 and 0 <= worker < 1 << 16 and 0 <= site < 1 << 31 and 0 <= seed < 1 << 64):
+        raise ValueError(f"seed {seed}, rnd {rnd}, worker {worker}, site {site}: expected 64, 32, 16 and 31 bits")
+    return C.byref(dq_keep_key(seed, d_round, rnd, worker, site, KEEP_DITHER if dither else 0))
+
+
+class Kept8:
+    """A tensor kept in 8 bits by :func:`keep8`: int8 ``codes`` of its shape, uint8
+    ``exponents`` (one for every 32 elements of its last dimension, which it
+    replaces), and the ``dtype`` it had."""
+
+    def __init__(self, codes, exponents, dtype):
+        if not isinstance(codes, torch.Tensor) or codes.dim() == 0 or codes.device.type != "cuda":
+            raise ValueError("codes: expected a tensor of at least one dimension on a GPU")
+        _tensor(codes, "codes", codes.device, dtype=torch.int8)
+        _tensor(exponents, "exponents", codes.device, dtype=torch.uint8)
+        if exponents.shape != codes.shape[:-1] + ((codes.size(-1) + 31) // 32,):
+            raise ValueError(f"exponents: shape {tuple(exponents.shape)} for codes of {tuple(codes.shape)}")
+        if dtype != torch.bfloat16 and dtype != torch.float32:
+            raise TypeError(f"dtype {dtype} (bf16 or fp32 only)")
+        self.codes, self.exponents, self.dtype = codes, exponents, dtype
+
+    @property
+    def shape(self):
+        return self.codes.shape
+
+    @property
+    def device(self):
+        return self.codes.device
+
+
+def _matrix_rows(t, what):
+    """(rows, cols, row stride) of a tensor as a matrix of its last dimension, the
+    row kept whole."""
+    if t.dim() == 0:
+        raise ValueError(f"{what}: expected at least one dimension")
+    cols = t.size(-1)
+    if t.is_contiguous():
+        return (t.numel() // cols if cols else 0), cols, cols
+    _, _, stride = _rows(t, what)
+    return t.numel() // cols, cols, stride
+
+
+@_on_stream
+def keep8(x, dither=True, seed=1, rnd=0, worker=0, site=0):
+    """``x`` in 8 bits, for the backward pass (``dq_keep8``): a :class:`Kept8` of 33
+    bytes for 32 elements of the last dimension, which share a power of two.
+
+    With ``dither`` the rounding is random, by numbers of (seed, rnd, worker, site,
+    element), and the kept value's mean is ``x``; without, it is the nearest.  ``x`` is
+    bf16 or fp32, contiguous or with rows at one stride; ``rnd`` as in
+    :func:`dropout`."""
+    dev = _gpu(x, "x").device
+    rows, cols, stride = _matrix_rows(x, "x")
+    codes = torch.empty(x.shape, dtype=torch.int8, device=dev)
+    exponents = torch.empty(x.shape[:-1] + ((cols + 31) // 32,), dtype=torch.uint8, device=dev)
+    _call(dev, "dq_keep8", x.data_ptr(), _kind(x), rows, cols, stride, codes.data_ptr(), exponents.data_ptr(),
+          _keep_key(dither, seed, rnd, worker, site, dev))
+    return Kept8(codes, exponents, x.dtype)
+
+
+@_on_stream
+def restore8(kept, out=None):
+    """The values that ``kept`` stands for (``dq_restore8``), exactly, in the dtype of
+    what was kept; NaN for a block that was not finite (or beyond 127 2^121)."""
+    if not isinstance(kept, Kept8):
+        raise TypeError(f"kept: expected a Kept8, got {type(kept).__name__}")
+    if out is None:
+        out = torch.empty(kept.shape, dtype=kept.dtype, device=kept.device)
+    elif _gpu(out, "out").shape != kept.shape or out.dtype != kept.dtype or out.device != kept.device:
+        raise ValueError(f"out: {tuple(out.shape)} {out.dtype} on {out.device}, "
+                         f"kept is {tuple(kept.shape)} {kept.dtype} on {kept.device}")
+    rows, cols, stride = _matrix_rows(out, "out")
+    _call(kept.device, "dq_restore8", kept.codes.data_ptr(), kept.exponents.data_ptr(), _kind(out), rows, cols,
+          out.data_ptr(), stride)
+    return out
+
+
+class ExpertRows:
+    """Rows of every expert, as :func:`expert_rows` lists them: ``offsets`` int32
+    [experts + 1], the experts' first rows; ``source`` int32 [tokens * top_k], the slot
+    (token * top_k + choice) of every row, those without an expert last; ``row`` int32
+    [tokens, top_k], the row of every slot, -1 without an expert."""
+
+    def __init__(self, offsets, source, row):
+        if not isinstance(row, torch.Tensor) or row.dim() != 2 or row.device.type != "cuda":
+            raise ValueError("row: expected a tensor [tokens, top_k] on a GPU")
+        dev = row.device
+        _tensor(row, "row", dev, dtype=torch.int32)
+        _tensor(source, "source", dev, numel=row.numel(), dtype=torch.int32)
+        _tensor(offsets, "offsets", dev, dtype=torch.int32)
+        if offsets.dim() != 1 or offsets.numel() < 2:
+            raise ValueError(f"offsets: shape {tuple(offsets.shape)}, expected [experts + 1]")
+        self.offsets, self.source, self.row, self.device = offsets, source, row, dev
+        self.tokens, self.top_k = row.shape
+        self.slots, self.experts = row.numel(), offsets.numel() - 1
+        self._io = C.byref(dq_expert_lists(offsets.data_ptr(), source.data_ptr(), row.data_ptr(), self.tokens,
+                                           self.top_k, self.experts))
+
+
+@functools.lru_cache(maxsize=256)
+def _rows_bytes(tokens, top_k, experts):
+    return lib().dq_expert_rows_bytes(tokens, top_k, experts)
+
+
+@_on_stream
+def expert_rows(ids, experts):
+    """:class:`ExpertRows` of the choices ``ids`` [tokens, top_k] int32 of
+    :func:`route` (``dq_expert_rows``): every expert's slots in the order of the tokens.
+    Ids outside 0 .. experts - 1 are no choice.  Nothing waits for the GPU: how many
+    rows an expert has stays on the device."""
+    if not isinstance(ids, torch.Tensor) or ids.dim() != 2 or ids.device.type != "cuda":
+        raise ValueError("ids: expected [tokens, top_k] of route() on a GPU")
+    dev = ids.device
+    _tensor(ids, "ids", dev, dtype=torch.int32)
+    tokens, top_k = ids.shape
+    need = _rows_bytes(tokens, top_k, experts)
+    if not need:
+        raise ValueError(f"{tokens} tokens of {top_k} choices among {experts} experts")
+    offsets = torch.empty(experts + 1, dtype=torch.int32, device=dev)
+    source = torch.empty(tokens * top_k, dtype=torch.int32, device=dev)
+    row = torch.empty((tokens, top_k), dtype=torch.int32, device=dev)
+    work = torch.empty(need, dtype=torch.uint8, device=dev)
+    _call(dev, "dq_expert_rows", ids.data_ptr(), tokens, top_k, experts, offsets.data_ptr(), source.data_ptr(),
+          row.data_ptr(), work.data_ptr(), need)
+    return ExpertRows(offsets, source, row)
+
+
+def _expert_rows(rows):
+    if not isinstance(rows, ExpertRows):
+        raise TypeError(f"rows: expected an ExpertRows, got {type(rows).__name__}")
+    return rows
+
+
+def _row_matrix(t, what, n, dev, cols=None, dtype=None):
+    """An operand [n, cols] whose rows are contiguous; its row stride."""
+    _gpu(t, what)
+    if t.dim() != 2 or t.size(0) != n or cols is not None and t.size(1) != cols or t.device != dev or \
+            dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{what}: {tuple(t.shape)} {t.dtype} on {t.device}, expected [{n}, "
+                         f"{'width' if cols is None else cols}] {dtype or 'bf16 or fp32'} on {dev}")
+    if t.size(1) > 1 and t.stride(1) != 1 and t.numel():
+        raise ValueError(f"{what}: strides {t.stride()}, the last dimension must be contiguous")
+    return t.stride(0)
+
+
+def _row_result(t, what, n, cols, x):
+    """A caller's buffer [n, cols] for a result like ``x``, or a new one."""
+    if t is None:
+        return torch.empty((n, cols), dtype=x.dtype, device=x.device), cols
+    return t, _row_matrix(t, what, n, x.device, cols, x.dtype)
+
+
+@_on_stream
+def expert_matmul(x, w, rows, gather=False, out=None):
+    """``x[r] @ w[e(r)]`` for every expert's rows (``dq_expert_matmul``): [tokens *
+    top_k, outer] of the dtype of ``x``.
+
+    ``x`` is [tokens * top_k, inner] in the order of ``rows``, or with ``gather`` the tokens
+    themselves, [tokens, inner], read where they lie.  ``w`` is [experts, inner, outer],
+    contiguous along one of the last two: the gradient by ``x`` is
+    ``expert_matmul(dout, w.transpose(1, 2), rows)``.  Rows of ``x`` and ``out`` may lie at any
+    stride.  Rows without an expert are left as they were (uninitialised in a new
+    ``out``)."""
+    dev = _expert_rows(rows).device
+    xs = _row_matrix(x, "x", rows.tokens if gather else rows.slots, dev)
+    if not isinstance(w, torch.Tensor) or w.dim() != 3 or w.size(0) != rows.experts or w.size(1) != x.size(1) or \
+            w.dtype != x.dtype or w.device != dev:
+        raise ValueError(f"w: {tuple(w.shape)} {w.dtype} on {w.device}, expected [{rows.experts}, {x.size(1)}, outer] "
+                         f"{x.dtype} on {dev}" if isinstance(w, torch.Tensor) else "w: expected a torch.Tensor")
+    _, inner, outer = w.shape
+    we, w1, w2 = w.stride()
+    flags = EXPERT_GATHER if gather else 0
+    if w2 == 1 or outer == 1:
+        ws = w1
+    elif w1 == 1 or inner == 1:
+        ws, flags = w2, flags | EXPERT_TURNED
+    else:
+        raise ValueError(f"w: strides {w.stride()}, one of the last two dimensions must be contiguous")
+    out, ys = _row_result(out, "out", rows.slots, outer, x)
+    _call(dev, "dq_expert_matmul", rows._io, x.data_ptr(), xs, flags, w.data_ptr(), we, ws, out.data_ptr(), ys,
+          _kind(x), inner, outer)
+    return out
+
+
+@functools.lru_cache(maxsize=256)
+def _grad_bytes(tokens, top_k, experts, kind, inner, outer):
+    return lib().dq_expert_matmul_grad_bytes(tokens, top_k, experts, kind, inner, outer)
+
+
+@_on_stream
+def expert_matmul_grad(x, dout, rows, gather=None, dtype=None, out=None):
+    """The gradient of :func:`expert_matmul` by ``w``: the sum of ``x[r]^T dout[r]`` over
+    every expert's rows (``dq_expert_matmul_grad``), [experts, inner, outer] of ``dtype``
+    (that of ``dout``, or fp32); zeros for an expert without rows.
+
+    ``gather`` names which of ``"x"`` and ``"dout"`` holds tokens instead of rows, if one
+    does.  ``x`` may be a :class:`Kept8`, which is decoded as it is read."""
+    dev = _expert_rows(rows).device
+    if gather not in (None, "x", "dout"):
+        raise ValueError(f"gather {gather!r}: expected None, 'x' or 'dout'")
+    n = rows.tokens if gather == "x" else rows.slots
+    ds = _row_matrix(dout, "dout", rows.tokens if gather == "dout" else rows.slots, dev)
+    if isinstance(x, Kept8):
+        if x.codes.dim() != 2 or x.shape[0] != n or x.dtype != dout.dtype or x.device != dev:
+            raise ValueError(f"x: kept {tuple(x.shape)} {x.dtype} on {x.device}, expected [{n}, inner] {dout.dtype} "
+                             f"on {dev}")
+        at, xs, codes, exponents, inner = None, 0, x.codes.data_ptr(), x.exponents.data_ptr(), x.shape[1]
+    else:
+        xs = _row_matrix(x, "x", n, dev, dtype=dout.dtype)
+        at, codes, exponents, inner = x.data_ptr(), None, None, x.size(1)
+    outer = dout.size(1)
+    dtype = dout.dtype if dtype is None else dtype
+    if dtype != dout.dtype and dtype != torch.float32:
+        raise TypeError(f"dtype {dtype}: expected {dout.dtype} or fp32")
+    out = _result(out, (rows.experts, inner, outer), "out", dtype, dev)
+    kind = _kind(dout)
+    need = _grad_bytes(rows.tokens, rows.top_k, rows.experts, kind, inner, outer)
+    work = torch.empty(need, dtype=torch.uint8, device=dev)
+    _call(dev, "dq_expert_matmul_grad", rows._io, at, xs, codes, exponents, dout.data_ptr(), ds,
+          GATHER_X if gather == "x" else GATHER_DOUT if gather else GATHER_NONE, out.data_ptr(), kind, _kind(out),
+          inner, outer, work.data_ptr(), need)
+    return out
+
+
+@_on_stream
+def expert_sum(y, rows, residual=None, out=None):
+    """Every token's rows added up, and its ``residual``: ``residual[t] + sum_j y[row[t,
+    j]]`` (``dq_expert_sum``), [tokens, width].  Choices without an expert add nothing.
+    It is the way back of the experts' outputs and the gradient of gathering.
+    ``out`` may be ``residual``."""
+    dev = _expert_rows(rows).device
+    ys = _row_matrix(y, "y", rows.slots, dev)
+    width, rs = y.size(1), 0
+    if residual is not None:
+        rs = _row_matrix(residual, "residual", rows.tokens, dev, width, y.dtype)
+    out, os_ = _row_result(out, "out", rows.tokens, width, y)
+    _call(dev, "dq_expert_sum", rows._io, y.data_ptr(), ys, _opt(residual), rs, out.data_ptr(), os_, _kind(y), width)
+    return out
+
+
+def _act(act, columns):
+    """(number, width) of an activation over so many columns of u."""
+    if act not in _ACTS:
+        raise ValueError(f"act {act!r}: expected one of {sorted(_ACTS)}")
+    if act == "swiglu" and columns % 2:
+        raise ValueError(f"u: {columns} columns, expected gate and value halves")
+    return _ACTS[act], columns // 2 if act == "swiglu" else columns
+
+
+def _gates(gates, rows):
+    if not isinstance(gates, torch.Tensor) or gates.shape != rows.row.shape:
+        raise ValueError(f"gates: expected [{rows.tokens}, {rows.top_k}] of route()")
+    return _tensor(gates, "gates", rows.device, dtype=torch.float32).data_ptr()
+
+
+@_on_stream
+def expert_act(u, gates, rows, act="swiglu", keep=False, dither=True, seed=1, rnd=0, worker=0, site=0, out=None):
+    """The activation between the experts' products, weighted by the router's
+    ``gates`` (``dq_expert_act``): with ``act="swiglu"``, ``u`` = (g, v) in two halves and
+    ``gate * silu(g) * v``; with ``"relu"``, ``gate * max(u, 0)``.
+
+    ``u`` is [tokens * top_k, columns].  With ``keep`` returns (a, kept): the rows of
+    ``u`` are also kept in 8 bits, as :func:`keep8` would keep them with the same
+    numbers, in one pass."""
+    dev = _expert_rows(rows).device
+    us = _row_matrix(u, "u", rows.slots, dev)
+    columns = u.size(1)
+    number, width = _act(act, columns)
+    at = _gates(gates, rows)
+    a, as_ = _row_result(out, "out", rows.slots, width, u)
+    kept = codes = exponents = key = None
+    if keep:
+        key = _keep_key(dither, seed, rnd, worker, site, dev)
+        kept = Kept8(torch.empty((rows.slots, columns), dtype=torch.int8, device=dev),
+                     torch.empty((rows.slots, (columns + 31) // 32), dtype=torch.uint8, device=dev), u.dtype)
+        codes, exponents = kept.codes.data_ptr(), kept.exponents.data_ptr()
+    _call(dev, "dq_expert_act", rows._io, number, u.data_ptr(), us, at, a.data_ptr(), as_, _kind(u), width, codes,
+          exponents, key)
+    return (a, kept) if keep else a
+
+
+@_on_stream
+def expert_act_backward(u, da, gates, rows, act="swiglu", du=None, dgates=None, a=None, again=True):
+    """Gradient of :func:`expert_act`, from ``u`` or the :class:`Kept8` of it: returns
+    (du, dgates, a).  ``a`` is the activation once more, from the same ``u``, for
+    :func:`expert_matmul_grad` of the next product (None without ``again``).  ``du``,
+    ``dgates`` and ``a`` may be given as buffers; the gates of slots without an expert
+    get 0."""
+    dev = _expert_rows(rows).device
+    das = _row_matrix(da, "da", rows.slots, dev)
+    if isinstance(u, Kept8):
+        if u.codes.dim() != 2 or u.shape[0] != rows.slots or u.dtype != da.dtype or u.device != dev:
+            raise ValueError(f"u: kept {tuple(u.shape)} {u.dtype} on {u.device}, expected [{rows.slots}, columns] "
+                             f"{da.dtype} on {dev}")
+        columns, at, us, codes, exponents = u.shape[1], None, 0, u.codes.data_ptr(), u.exponents.data_ptr()
+    else:
+        us = _row_matrix(u, "u", rows.slots, dev, dtype=da.dtype)
+        columns, at, codes, exponents = u.size(1), u.data_ptr(), None, None
+    number, width = _act(act, columns)
+    if da.size(1) != width:
+        raise ValueError(f"da: {da.size(1)} columns, expected {width}")
+    g = _gates(gates, rows)
+    du, dus = _row_result(du, "du", rows.slots, columns, da)
+    dgates = _result(dgates, gates.shape, "dgates", torch.float32, dev)
+    as_ = 0
+    if again or a is not None:
+        a, as_ = _row_result(a, "a", rows.slots, width, da)
+    _call(dev, "dq_expert_act_backward", rows._io, number, at, us, codes, exponents, da.data_ptr(), das, g,
+          du.data_ptr(), dus, _opt(a), as_, dgates.data_ptr(), _kind(da), width)
+    return du, dgates, a
 
 
 class Plan:

@@ -509,6 +509,121 @@ dq_status dq_route_backward(const dq_route_grad *h_workers, int32_t n_workers, i
                             int32_t top_k, int32_t flags, const float *d_coef, const float *d_dloss,
                             void *stream);
 
+/* ---- experts ------------------------------------------------------------------
+ *
+ * What follows the router in a mixture-of-experts step: the chosen experts' rows,
+ * products over them, the activation between two products, and activations kept
+ * in 8 bits for the backward pass.  Stateless, and with the errors and overlap
+ * rules of the training step above; nothing is launched where a check fails.
+ * Sizes: n_experts in 1..1024, top_k in 1..16, tokens * top_k below 2^31, widths
+ * in 1..2^24.
+ *
+ * Slot t * top_k + j is token t's choice j.  The slots sorted by their expert,
+ * stably, are the ROWS; those without one (an id outside 0..n_experts-1) come last
+ * and belong to no expert.  Expert e has rows d_offsets[e] .. d_offsets[e + 1] - 1;
+ * row r comes from slot d_source[r]; slot s went to row d_row[s], -1 without an
+ * expert.  Calls over the rows read how many there are from the lists on the
+ * device, leave rows without an expert as they were, and never address beyond
+ * tokens * top_k rows, whatever the lists hold. */
+typedef struct dq_expert_lists {
+    const int32_t *d_offsets;   /* [n_experts + 1] */
+    const int32_t *d_source;    /* [tokens * top_k] */
+    const int32_t *d_row;       /* [tokens * top_k] */
+    int64_t tokens;
+    int32_t top_k, n_experts;
+} dq_expert_lists;
+
+/* The lists of d_ids[tokens][top_k] (of dq_route, or any; a token may name an
+ * expert twice).  d_work: 256-byte aligned, dq_expert_rows_bytes (0 on bad
+ * arguments); two calls in flight need one each. */
+size_t dq_expert_rows_bytes(int64_t tokens, int32_t top_k, int32_t n_experts);
+dq_status dq_expert_rows(const int32_t *d_ids, int64_t tokens, int32_t top_k, int32_t n_experts,
+                         int32_t *d_offsets, int32_t *d_source, int32_t *d_row, void *d_work,
+                         size_t work_bytes, void *stream);
+
+/* y[r] = x[r] w[e(r)] for every expert's rows, rounded once from fp32 sums.
+ * x: row r at element r * x_stride, or with DQ_EXPERT_GATHER the row's token,
+ * t * x_stride (gathered as it is read; no copy is made).  w: element (i, j) of
+ * expert e at e * w_expert_stride + i * w_stride + j, or + j * w_stride + i with
+ * DQ_EXPERT_TURNED: the gradient by x is the same call on dy with the other flag.
+ * All of `kind`.  bf16 products are exact and summed in fp32; fp32 ones are fp32
+ * throughout. */
+typedef enum dq_expert_flags { DQ_EXPERT_GATHER = 1, DQ_EXPERT_TURNED = 2 } dq_expert_flags;
+dq_status dq_expert_matmul(const dq_expert_lists *lists, const void *d_x, int64_t x_stride, int32_t flags,
+                           const void *d_w, int64_t w_expert_stride, int64_t w_stride, void *d_y,
+                           int64_t y_stride, int32_t kind, int64_t inner, int64_t outer, void *stream);
+
+/* dw[e] = sum over e's rows of x[r]^T dy[r], [n_experts][inner][outer] of out_kind
+ * (DQ_F32 or `kind`), zeros for an expert without rows.  One of x and dy may hold
+ * tokens, gathered as above; x may be given as the codes of dq_keep8 (d_codes and
+ * d_exponents, rows without gaps; d_x NULL), which are decoded as they are read.
+ * Sums in fp32; the same call gives the same bits.  d_work: 256-byte aligned,
+ * dq_expert_matmul_grad_bytes (0 on bad arguments). */
+typedef enum dq_expert_gather { DQ_GATHER_NONE = 0, DQ_GATHER_X = 1, DQ_GATHER_DOUT = 2 } dq_expert_gather;
+size_t dq_expert_matmul_grad_bytes(int64_t tokens, int32_t top_k, int32_t n_experts, int32_t kind,
+                                   int64_t inner, int64_t outer);
+dq_status dq_expert_matmul_grad(const dq_expert_lists *lists, const void *d_x, int64_t x_stride,
+                                const int8_t *d_codes, const uint8_t *d_exponents, const void *d_dy,
+                                int64_t dy_stride, int32_t gather, void *d_dw, int32_t kind,
+                                int32_t out_kind, int64_t inner, int64_t outer, void *d_work,
+                                size_t work_bytes, void *stream);
+
+/* out[t] = residual[t] + sum_j y[d_row[t][j]] (d_residual NULL: without), in fp32 in
+ * the order of j, rounded once; choices without a row add nothing.  The way back of
+ * the rows, and the gradient of gathering them.  d_out may be d_residual (same
+ * stride). */
+dq_status dq_expert_sum(const dq_expert_lists *lists, const void *d_y, int64_t y_stride,
+                        const void *d_residual, int64_t residual_stride, void *d_out, int64_t out_stride,
+                        int32_t kind, int64_t width, void *stream);
+
+/* Activations in 8 bits.  Every 32 elements of a row (its last block may be
+ * short) share 2^s, s the smallest from -110 with max|x| <= 127 2^s:
+ *   |code| = floor((floor(|x| 2^(16 - s)) + d) / 2^16), with x's sign;
+ *   x is kept as code 2^s, which bf16 holds exactly.
+ * d is the element's 16-bit dither, so that the kept value's mean is x (to 2^-16 of
+ * 2^s), or 32768 without DQ_KEEP_DITHER: the nearest.  The exponent's byte is s + 127;
+ * 255 for a block with an infinity, NaN or |x| > 127 2^121 (the last hundredth of
+ * fp32's range), which is restored as NaN throughout.
+ * d_codes[rows][cols], d_exponents[rows][(cols + 31) / 32].  Dither of element i =
+ * r * cols + c: as dq_dropout's, with counter word 1 = (i >> 35) | 2^15 | worker << 16,
+ * which keeps it apart from a dropout under the same numbers.  rows * cols up to
+ * 2^50.  d_round as in dq_dropout. */
+typedef enum dq_keep_flags { DQ_KEEP_DITHER = 1 } dq_keep_flags;
+typedef struct dq_keep_key {
+    uint64_t seed;
+    const uint32_t *d_round;
+    uint32_t round;
+    int32_t worker;
+    uint32_t site;
+    int32_t flags;
+} dq_keep_key;
+dq_status dq_keep8(const void *d_x, int32_t kind, int64_t rows, int64_t cols, int64_t x_stride,
+                   int8_t *d_codes, uint8_t *d_exponents, const dq_keep_key *key, void *stream);
+dq_status dq_restore8(const int8_t *d_codes, const uint8_t *d_exponents, int32_t kind, int64_t rows,
+                      int64_t cols, void *d_y, int64_t y_stride, void *stream);
+
+/* The activation of every expert's rows, weighted by the row's gate
+ * d_gates[d_source[r]] (fp32, [tokens][top_k]):
+ *   DQ_ACT_SWIGLU  u = (g, v), 2 * width columns: a = gate g / (1 + exp(-g)) v
+ *   DQ_ACT_RELU    u of width columns:            a = gate max(u, 0)
+ * in fp32, rounded once.  With d_codes and d_exponents the rows of u are kept as
+ * dq_keep8 keeps a matrix of tokens * top_k rows (key: its numbers), in the same
+ * pass. */
+typedef enum dq_act { DQ_ACT_SWIGLU = 0, DQ_ACT_RELU = 1 } dq_act;
+dq_status dq_expert_act(const dq_expert_lists *lists, int32_t act, const void *d_u, int64_t u_stride,
+                        const float *d_gates, void *d_a, int64_t a_stride, int32_t kind, int64_t width,
+                        int8_t *d_codes, uint8_t *d_exponents, const dq_keep_key *key, void *stream);
+
+/* Its gradient, from u or from what was kept of it (d_u NULL): d_du of u's shape,
+ * d_dgates[tokens][top_k] (may be NULL; 0 for a slot without a row), and d_again (may
+ * be NULL), the activation once more, which the weights' gradient of the next
+ * product takes. */
+dq_status dq_expert_act_backward(const dq_expert_lists *lists, int32_t act, const void *d_u, int64_t u_stride,
+                                 const int8_t *d_codes, const uint8_t *d_exponents, const void *d_da,
+                                 int64_t da_stride, const float *d_gates, void *d_du, int64_t du_stride,
+                                 void *d_again, int64_t again_stride, float *d_dgates, int32_t kind,
+                                 int64_t width, void *stream);
+
 /* ---- inspection ----------------------------------------------------------- */
 
 /* Copy the allocation result to the host.  SYNCHRONISES `stream`.
