@@ -1,5 +1,8 @@
 // dq_expert_product.hip -- products grouped by expert for gfx950: rows by the
 // experts' weights, and the weights' gradient.
+#include <algorithm>
+
+#include "dq.h"
 #include "dq_expert_tile.h"
 
 namespace dq {
@@ -7,7 +10,29 @@ namespace dq {
 namespace {
 
 // y[r] = x[r] w[e(r)] over the experts' rows: A is x, contiguous along the inner
-// index; B is w, contiguous along the outer one, or along the inner one (TURNED).
+// index; B is w, contiguous along the outer one, or along the inner one (TURNED).  The
+// products of inner indexes from `from`, `inner` of them.
+template <class C, int LA, int LB, bool TURNED>
+__device__ __forceinline__ void product_tile(const ExpertProductArgs &a, const RowTile &t, int n0, int from, int inner,
+                                             char *lds, Acc<C> &acc) {
+    typedef typename C::T T;
+    Along<C, C::BM, LA> x;
+    x.start(static_cast<const T *>(a.x) + (a.gather ? 0 : t.first * a.xs) + from, inner, [&](int i) {
+        i = min(i, t.rows - 1);
+        return a.gather ? row_at(a.l, t.first + i, 1, a.xs) : i * a.xs;
+    });
+    const T *w = static_cast<const T *>(a.w) + t.e * a.we;
+    if constexpr (TURNED) {
+        Along<C, C::BN, LB> b;
+        b.start(w + n0 * a.ws + from, inner, [&](int i) { return min(i, a.N - 1 - n0) * a.ws; });
+        multiply<C>(lds, x, b, inner, acc);
+    } else {
+        Across<C, C::BN, LB, false> b(RowsDown<false>(a.ws, from));
+        b.start(w, n0, a.N, inner);
+        multiply<C>(lds, x, b, inner, acc);
+    }
+}
+
 template <class C, int LA, int LB, bool TURNED>
 __global__ __launch_bounds__(C::kThreads) void k_product(ExpertProductArgs a, int nt) {
     typedef typename C::T T;
@@ -16,29 +41,52 @@ __global__ __launch_bounds__(C::kThreads) void k_product(ExpertProductArgs a, in
     if (!find_tile<C::kThreads>(a.l, C::BM, nt, t, reinterpret_cast<int *>(lds))) return;
     const int n0 = t.n * C::BN;
     Acc<C> acc;
-    typename std::conditional<TURNED, Along<C, C::BN, LB>, Across<C, C::BN, LB>>::type b;
-    Along<C, C::BM, LA> x;
-    x.start(static_cast<const T *>(a.x), a.K, [&](int i) {
-        const int r = t.first + (i < t.rows ? i : t.rows - 1);
-        return row_at(a.l, r, a.gather, a.xs);
-    });
-    const T *w = static_cast<const T *>(a.w) + t.e * a.we;
-    if constexpr (TURNED)
-        b.start(w, a.K, [&](int i) { return (int64_t)min(n0 + i, a.N - 1) * a.ws; });
-    else
-        b.start(w, n0, a.N, a.K);
-    const auto row_b = [&](int k) { return (int64_t)k * a.ws; };
-    multiply<C>(lds, x, b, a.K, [](int) { return (int64_t)0; }, row_b, acc);
+    product_tile<C, LA, LB, TURNED>(a, t, n0, 0, a.K, lds, acc);
     acc.store([&](int m) { return m < t.rows ? static_cast<T *>(a.y) + (t.first + m) * a.ys : nullptr; }, n0, a.N,
               vec_out<T>(a.y, a.ys, a.N));
 }
 
+// The same for few rows, which the weights' bytes bound: a tile is one wave's, four of
+// them take a quarter of the inner index each, wait for their own loads alone, and add up.
+constexpr int kFewWaves = 4;
+template <class C, bool TURNED>
+__global__ __launch_bounds__(64 * kFewWaves) void k_product_few(ExpertProductArgs a, int nt) {
+    typedef typename C::T T;
+    extern __shared__ __align__(1024) char lds[];
+    RowTile t;
+    if (!find_tile<64 * kFewWaves>(a.l, C::BM, nt, t, reinterpret_cast<int *>(lds))) return;
+    const int n0 = t.n * C::BN, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int per = ((a.K + kFewWaves - 1) / kFewWaves + C::BK - 1) / C::BK * C::BK, from = min(wave * per, a.K);
+    char *own = lds + wave * C::kLds;
+    Acc<C> acc;
+    product_tile<C, kAsync, kAsync, TURNED>(a, t, n0, from, min(per, a.K - from), own, acc);
+    acc.put(reinterpret_cast<float *>(own));
+    __syncthreads();
+    static_assert(C::BM * C::BN == 4 * 64 * kFewWaves && C::kLds >= 4 * C::BM * C::BN, "four sums a thread");
+    const int m = threadIdx.x * 4 / C::BN, n = threadIdx.x * 4 % C::BN;
+    if (m >= t.rows) return;
+    f32x4 sum = {0, 0, 0, 0};
+#pragma unroll
+    for (int w = 0; w < kFewWaves; w++)
+        sum += *reinterpret_cast<const f32x4 *>(lds + w * C::kLds + 16 * threadIdx.x);
+    T *y = static_cast<T *>(a.y) + (t.first + m) * a.ys + n0 + n;
+    if (vec_out<T>(a.y, a.ys, a.N) && n0 + n < a.N) {
+        store_four(y, sum);
+    } else {
+#pragma unroll
+        for (int q = 0; q < 4; q++)
+            if (n0 + n + q < a.N) store_one(y + q, sum[q]);
+    }
+}
+
+constexpr int kWeightsRun = 8;
+
 // dw[e] = the sum of x[r]^T dy[r] over e's rows (or over a part of them, into fp32).
-template <class C, int LA, int LB, typename Out>
+template <class C, int LA, int LB, int GATHER, typename Out>
 __global__ __launch_bounds__(C::kThreads) void k_weights(ExpertWeightsArgs a, int mt, int nt, int64_t total) {
     typedef typename C::T T;
     extern __shared__ __align__(1024) char lds[];
-    int64_t id = own_tile(blockIdx.x, total);
+    int64_t id = own_tile_in_runs(blockIdx.x, kWeightsRun);
     if (id >= total) return;
     const int part = (int)(id % a.parts);
     id /= a.parts;
@@ -54,17 +102,16 @@ __global__ __launch_bounds__(C::kThreads) void k_weights(ExpertWeightsArgs a, in
         first += at;
     }
     Acc<C> acc;
-    Across<C, C::BM, LA> x;
-    Across<C, C::BN, LB> dy;
-    if constexpr (LA == kKept || LA == kKeptAny)
+    // of codes, the row's number
+    constexpr bool kGatherX = GATHER == DQ_GATHER_X, kGatherDy = GATHER == DQ_GATHER_DOUT;
+    Across<C, C::BM, LA, kGatherX> x(RowsDown<kGatherX>(a.l, first, LA == kKept ? 1 : a.xs));
+    Across<C, C::BN, LB, kGatherDy> dy(RowsDown<kGatherDy>(a.l, first, a.dys));
+    if constexpr (LA == kKept)
         x.start(a.codes, a.exponents, m0, a.K, rows);
     else
         x.start(static_cast<const T *>(a.x), m0, a.K, rows);
     dy.start(static_cast<const T *>(a.dy), n0, a.N, rows);
-    // of codes, the row's number
-    const int64_t xs = LA == kKept || LA == kKeptAny ? 1 : a.xs;
-    multiply<C>(lds, x, dy, rows, [&](int k) { return row_at(a.l, first + k, a.gather_x, xs); },
-                [&](int k) { return row_at(a.l, first + k, a.gather_dy, a.dys); }, acc);
+    multiply<C>(lds, x, dy, rows, acc);
     Out *dw = static_cast<Out *>(a.parts > 1 ? (void *)a.partial : a.dw) +
               ((int64_t)part * a.l.E + e) * a.K * a.N;
     acc.store([&](int m) { return m0 + m < a.K ? dw + (int64_t)(m0 + m) * a.N : nullptr; }, n0, a.N,
@@ -87,80 +134,148 @@ int64_t most_row_tiles(const ExpertLists &l) {
     return most < l.slots ? most : l.slots;
 }
 
-dim3 whole_rounds(int64_t tiles) { return dim3((unsigned)((tiles + 7) / 8 * 8)); }
+dim3 whole_rounds(int64_t tiles, int run = 1) {
+    return dim3((unsigned)((tiles + 8 * run - 1) / (8 * run) * (8 * run)));
+}
 
-template <class C, int LA, int LB, bool TURNED>
-hipError_t product_as(const ExpertProductArgs &a, hipStream_t s) {
+template <class C, class K>
+hipError_t product_launch(K kernel, int threads, int lds, const ExpertProductArgs &a, hipStream_t s) {
     const int nt = (a.N + C::BN - 1) / C::BN;
     const int64_t tiles = most_row_tiles<C>(a.l) * nt;
     if (tiles > (1 << 30)) return hipErrorInvalidValue;
-    const auto kernel = k_product<C, LA, LB, TURNED>;
-    const hipError_t e = room_for(kernel, C::kLds);
+    const hipError_t e = room_for(kernel, lds);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(kernel, whole_rounds(tiles), dim3(C::kThreads), C::kLds, s, a, nt);
+    hipLaunchKernelGGL(kernel, whole_rounds(tiles), dim3(threads), lds, s, a, nt);
     return hipGetLastError();
 }
-
+template <class C, int LA, int LB>
+hipError_t product_as(const ExpertProductArgs &a, hipStream_t s) {
+    if (a.turned) return product_launch<C>(k_product<C, LA, LB, true>, C::kThreads, C::kLds, a, s);
+    return product_launch<C>(k_product<C, LA, LB, false>, C::kThreads, C::kLds, a, s);
+}
 template <class C>
-hipError_t product_loads(const ExpertProductArgs &a, hipStream_t s) {
-    constexpr int64_t es = sizeof(typename C::T);
-    const bool va = on16(a.x, a.xs * es) && a.K % C::kChunk == 0;
-    const bool vb = on16(a.w, a.ws * es) && (a.l.E == 1 || a.we * es % 16 == 0) &&
-                    (a.turned ? a.K : a.N) % C::kChunk == 0;
-    if (a.turned) {
-        if (va && vb) return product_as<C, kAsync, kAsync, true>(a, s);
-        return product_as<C, kAny, kAny, true>(a, s);
-    }
-    if (va && vb) return product_as<C, kAsync, kAsync, false>(a, s);
-    return product_as<C, kAny, kAny, false>(a, s);
+hipError_t product_few(const ExpertProductArgs &a, hipStream_t s) {
+    if (a.turned) return product_launch<C>(k_product_few<C, true>, 64 * kFewWaves, kFewWaves * C::kLds, a, s);
+    return product_launch<C>(k_product_few<C, false>, 64 * kFewWaves, kFewWaves * C::kLds, a, s);
+}
+
+// Whether offsets into so many rows fit the 32 bits of the loads into LDS.
+bool near(int64_t rows, int64_t stride, int64_t cols, int64_t es) {
+    return ((rows - 1) * stride + cols) * es < (int64_t)kNowhere;
+}
+
+#ifndef FORCE
+#define FORCE -1
+#endif
+template <typename T>
+bool product_async(const ExpertProductArgs &a) {
+    constexpr int64_t es = sizeof(T), chunk = 16 / es;
+    return on16(a.x, a.xs * es) && a.K % chunk == 0 && on16(a.w, a.ws * es) && (a.l.E == 1 || a.we * es % 16 == 0) &&
+           (a.turned ? a.K : a.N) % chunk == 0 && near(a.gather ? a.l.tokens : 256, a.xs, a.K, es) &&
+           near(a.turned ? 256 : 64, a.ws, a.turned ? a.K : a.N, es);
+}
+
+template <class C, int LA, int LB, int GATHER, typename Out>
+hipError_t weights_gathered(const ExpertWeightsArgs &a, hipStream_t s) {
+    const int mt = (a.K + C::BM - 1) / C::BM, nt = (a.N + C::BN - 1) / C::BN;
+    const int64_t tiles = (int64_t)mt * nt * a.l.E * a.parts;
+    if (tiles > (1 << 30)) return hipErrorInvalidValue;
+    const auto kernel = k_weights<C, LA, LB, GATHER, Out>;
+    const hipError_t e = room_for(kernel, C::kLds);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(kernel, whole_rounds(tiles, kWeightsRun), dim3(C::kThreads), C::kLds, s, a, mt, nt, tiles);
+    return hipGetLastError();
 }
 
 template <class C, int LA, int LB, typename Out>
 hipError_t weights_as(const ExpertWeightsArgs &a, hipStream_t s) {
-    const int mt = (a.K + C::BM - 1) / C::BM, nt = (a.N + C::BN - 1) / C::BN;
-    const int64_t tiles = (int64_t)mt * nt * a.l.E * a.parts;
-    if (tiles > (1 << 30)) return hipErrorInvalidValue;
-    const auto kernel = k_weights<C, LA, LB, Out>;
-    const hipError_t e = room_for(kernel, C::kLds);
-    if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(kernel, whole_rounds(tiles), dim3(C::kThreads), C::kLds, s, a, mt, nt, tiles);
-    return hipGetLastError();
+    if (a.gather == DQ_GATHER_X) return weights_gathered<C, LA, LB, DQ_GATHER_X, Out>(a, s);
+    if (a.gather == DQ_GATHER_DOUT) return weights_gathered<C, LA, LB, DQ_GATHER_DOUT, Out>(a, s);
+    return weights_gathered<C, LA, LB, DQ_GATHER_NONE, Out>(a, s);
 }
 
-template <class C, typename Out>
+template <class C, class Any, typename Out>
 hipError_t weights_loads(const ExpertWeightsArgs &a, hipStream_t s) {
-    constexpr int64_t es = sizeof(typename C::T);
-    const bool vb = on16(a.dy, a.dys * es) && a.N % C::kChunk == 0;
-    if (a.codes) {
-        const bool va = on16(a.codes, 16) && a.K % 16 == 0;
-        if (va && vb) return weights_as<C, kKept, kAsync, Out>(a, s);
-        return weights_as<C, kKeptAny, kAny, Out>(a, s);
-    }
-    const bool va = on16(a.x, a.xs * es) && a.K % C::kChunk == 0;
-    if (va && vb) return weights_as<C, kAsync, kAsync, Out>(a, s);
-    return weights_as<C, kAny, kAny, Out>(a, s);
+    constexpr int64_t es = sizeof(typename C::T), chunk = 16 / es;
+    const bool dy_async =
+        on16(a.dy, a.dys * es) && a.N % chunk == 0 && near(a.gather == DQ_GATHER_DOUT ? a.l.tokens : 64, a.dys, a.N, es);
+    if (a.codes) return dy_async ? weights_as<Any, kKept, kAsync, Out>(a, s) : weights_as<Any, kKept, kAny, Out>(a, s);
+    if (dy_async && on16(a.x, a.xs * es) && a.K % chunk == 0 &&
+        near(a.gather == DQ_GATHER_X ? a.l.tokens : 64, a.xs, a.K, es))
+        return weights_as<C, kAsync, kAsync, Out>(a, s);
+    return weights_as<Any, kAny, kAny, Out>(a, s);
 }
 
-template <class C>
+template <class C, class Any>
 hipError_t weights_out(const ExpertWeightsArgs &a, hipStream_t s) {
-    if (a.out_f32 || a.parts > 1) return weights_loads<C, float>(a, s);
-    if constexpr (sizeof(typename C::T) == 2) return weights_loads<C, uint16_t>(a, s);
+    if (a.out_f32 || a.parts > 1) return weights_loads<C, Any, float>(a, s);
+    if constexpr (sizeof(typename C::T) == 2) return weights_loads<C, Any, uint16_t>(a, s);
     return hipErrorInvalidValue;
+}
+
+// Which tile: the one whose blocks are done first, by how many of them a CU gets.
+// Measured: a block's start and end take about 4 us, a step s1 where it has the CU to
+// itself and sN where the CU is full of them; a wave of the few-row form takes a quarter
+// of the steps.  bf16, 64 experts, 2048 x 2816, us of few / small / mid / big: 0.125 rows
+// an expert 20 / 24 / 29 / 52, 16: 163 / 142 / 146 / 191, 64: 328 / 185 / 190 / 200, 512:
+// 1909 / 673 / 559 / 457; 8 experts of 1024 x 1024 and 64 rows 14 / 15 / 18 / 29, 512 rows
+// 60 / 24 / 25 / 36.  fp32, 8 experts of 1024 x 1024, few / small / mid: 2 rows 13 / 29 /
+// 76, 64: 28 / 30 / 78, 1024: 238 / 170 / 209.
+struct TileCost {
+    int bm, bn, step, full;              // step: inner elements; full: blocks a CU holds
+    float s1, sn;                        // us
+};
+constexpr TileCost kCostBf16[] = {
+    {64, 128, 32, 3, 0.30f, 0.68f}, {128, 128, 32, 2, 0.39f, 0.70f}, {256, 256, 32, 1, 0.80f, 0.80f},
+    {16, 64, 32 * kFewWaves, 2, 0.40f, 0.67f}};
+constexpr TileCost kCostF32[] = {
+    {64, 64, 16, 5, 0.39f, 1.45f}, {128, 128, 16, 2, 1.12f, 2.10f}, {16, 64, 16 * kFewWaves, 2, 0.40f, 0.90f}};
+
+template <int N>
+int pick_tile(const TileCost (&costs)[N], const ExpertProductArgs &a, double es) {
+    const double slots = a.l.slots, E = a.l.E, met = slots < E ? slots : E;
+    const double memory = met * a.K * a.N * es / 5.5e6;
+    int best = 0;
+    double least = 0;
+    for (int i = 0; i < N; i++) {
+        const TileCost &c = costs[i];
+        const double mt = std::max(met, std::min(slots, slots / c.bm + E / 2));
+        const int64_t per_cu = ((int64_t)mt * ((a.N + c.bn - 1) / c.bn) + 255) / 256, rest = per_cu % c.full;
+        const double rounds = (double)(per_cu / c.full) * c.sn +
+                              (rest ? c.s1 + (c.sn - c.s1) * (rest - 1) / std::max(1, c.full - 1) : 0.0);
+        const double us = std::max(memory, 4 + rounds * ((a.K + c.step - 1) / c.step));
+        if (i == 0 || us < 0.97 * least) {
+            best = i;
+            least = us;
+        }
+    }
+    return best;
 }
 
 }  // namespace
 
 hipError_t launch_expert_product(const ExpertProductArgs &a, int f32, hipStream_t s) {
-    if (a.l.slots == 0 || a.N == 0) return hipSuccess;
-    if (f32) return product_loads<TileF32>(a, s);
-    return product_loads<TileMid>(a, s);
+    if (a.l.slots == 0) return hipSuccess;
+    if (f32) {
+        if (!product_async<float>(a)) return product_as<TileAnyF32, kAny, kAny>(a, s);
+        const int pick = FORCE >= 0 ? FORCE : pick_tile(kCostF32, a, 4);
+        if (pick == 0) return product_as<TileSmallF32, kAsync, kAsync>(a, s);
+        if (pick == 1) return product_as<TileMidF32, kAsync, kAsync>(a, s);
+        return product_few<TileFewF32>(a, s);
+    }
+    if (!product_async<uint16_t>(a)) return product_as<TileAny, kAny, kAny>(a, s);
+    const int pick = FORCE >= 0 ? FORCE : pick_tile(kCostBf16, a, 2);
+    if (pick == 0) return product_as<TileSmall, kAsync, kAsync>(a, s);
+    if (pick == 1) return product_as<TileMid, kAsync, kAsync>(a, s);
+    if (pick == 2) return product_as<TileBig, kAsync, kAsync>(a, s);
+    return product_few<TileFew>(a, s);
 }
 
 int expert_weights_parts(int64_t, int, int64_t, int64_t, int) { return 1; }
 
 hipError_t launch_expert_weights(const ExpertWeightsArgs &a, int f32, hipStream_t s) {
     if (a.K == 0 || a.N == 0) return hipSuccess;
-    hipError_t e = f32 ? weights_out<TileF32>(a, s) : weights_out<TileMid>(a, s);
+    hipError_t e = f32 ? weights_out<TileMidF32, TileAnyF32>(a, s) : weights_out<TileBig, TileAny>(a, s);
     if (e != hipSuccess || a.parts == 1) return e;
     const int64_t n = (int64_t)a.l.E * a.K * a.N, blocks = (n + 1023) / 1024;
     const dim3 grid((unsigned)(blocks < 65536 ? blocks : 65536));

@@ -17,27 +17,41 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 #define DQ_LDS(p) ((__attribute__((address_space(3))) void *)(p))
 #define DQ_GLOBAL(p) ((const __attribute__((address_space(1))) void *)(p))
 
-// What is read in the place of what is not there.
-__device__ const __align__(16) uint32_t kZeros[4] = {0, 0, 0, 0};
-
-// A block's tile is BM x BN, its inner step BK elements (128 bytes); its waves are
-// WM x WN, each with (BM / WM) x (BN / WN) in accumulators of 16 x 16.
-template <typename Element, int BM_, int BN_, int WM_, int WN_>
+// A block's tile is BM x BN, its inner step BK elements (64 bytes or 128 of a row);
+// its waves are WM x WN, each with (BM / WM) x (BN / WN) in accumulators of 16 x 16.
+// kStages steps lie in LDS.
+template <typename Element, int BM_, int BN_, int WM_, int WN_, int ROW_, int STAGES_>
 struct Tiling {
     typedef Element T;
     static constexpr bool kF32 = sizeof(T) == 4;
-    static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, BK = 128 / (int)sizeof(T);
+    static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, kRow = ROW_, BK = kRow / (int)sizeof(T);
     static constexpr int kThreads = 64 * WM * WN, kChunk = 16 / (int)sizeof(T);
     static constexpr int TM = BM / WM / 16, TN = BN / WN / 16;
-    static constexpr int kBytesA = BM * 128, kBytesB = BN * 128;
-    static constexpr int kStages = 2, kLds = kStages * (kBytesA + kBytesB);
+    static constexpr int kBytesA = BM * kRow, kBytesB = BN * kRow;
+    static constexpr int kStages = STAGES_, kLds = kStages * (kBytesA + kBytesB);
+    // the thread within the tile's threads: all of a block's, or one wave's
+    static __device__ __forceinline__ int tid() { return kThreads == 64 ? threadIdx.x & 63 : threadIdx.x; }
+    // the tile's wave, the same in all lanes
+    static __device__ __forceinline__ int wave() {
+        return kThreads == 64 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    }
 };
-typedef Tiling<uint16_t, 128, 128, 2, 2> TileMid;
-typedef Tiling<float, 128, 128, 2, 2> TileF32;
+#ifndef FEWS
+#define FEWS 4
+#endif
+typedef Tiling<uint16_t, 256, 256, 2, 4, 64, 4> TileBig;
+typedef Tiling<uint16_t, 128, 128, 2, 2, 64, 4> TileMid;
+typedef Tiling<uint16_t, 64, 128, 2, 2, 64, 4> TileSmall;
+typedef Tiling<uint16_t, 16, 64, 1, 1, 64, FEWS> TileFew;      // a wave's
+typedef Tiling<uint16_t, 128, 128, 2, 2, 128, 2> TileAny;
+typedef Tiling<float, 128, 128, 2, 2, 64, 4> TileMidF32;
+typedef Tiling<float, 64, 64, 2, 2, 64, 4> TileSmallF32;
+typedef Tiling<float, 16, 64, 1, 1, 64, FEWS> TileFewF32;
+typedef Tiling<float, 64, 64, 2, 1, 128, 2> TileAnyF32;
 
-// How an operand is loaded: 16 bytes at a time straight into LDS; element by
-// element through registers; from 8-bit codes, 16 at a time or one by one.
-constexpr int kAsync = 0, kAny = 1, kKept = 2, kKeptAny = 3;
+// How an operand is loaded: straight into LDS, where everything lies on 16 bytes; at any
+// alignment through registers; from 8-bit codes, decoded in registers.
+constexpr int kAsync = 0, kAny = 1, kKept = 2;
 
 // First row of expert e: the offsets, held to the rows there are and in order (an
 // offset below the one before it makes that expert empty).
@@ -56,11 +70,56 @@ __device__ __forceinline__ int64_t row_at(const ExpertLists &l, int row, int gat
     return t < 0 ? -1 : t * stride;
 }
 
+// The rows down which an operand's inner index runs: `first` + k, or GATHERed the token
+// of that row.  In two halves, so that a list's entry is in flight while a step is
+// computed: entry() is one load, always made (a load under a condition would be waited
+// for where the branches join, and with it every load into LDS before it).
+template <bool GATHER>
+struct RowsDown {
+    int64_t stride;
+    const int32_t *source;
+    uint32_t slots, k;
+    int first;
+    __device__ __forceinline__ explicit RowsDown(int64_t s, int f = 0)
+        : stride(s), source(nullptr), slots(0), k(1), first(f) {}
+    __device__ __forceinline__ RowsDown(const ExpertLists &l, int f, int64_t s)
+        : stride(s), source(l.source), slots((uint32_t)l.slots), k((uint32_t)l.k), first(f) {}
+    __device__ __forceinline__ uint32_t entry(int at) const {
+        if constexpr (GATHER) return (uint32_t)source[min((uint32_t)(first + at), slots - 1)];
+        return (uint32_t)(first + at);
+    }
+    // of an `at` that all lanes share
+    __device__ __forceinline__ uint32_t shared_entry(int at) const {
+        const uint32_t i = __builtin_amdgcn_readfirstlane(min((uint32_t)(first + at), slots - 1));
+        return (uint32_t)((const __attribute__((address_space(4))) int32_t *)(uintptr_t)source)[i];
+    }
+    // slot / k: (slot + 1/2) / k is 1/32 or more from any whole number, the product off
+    // by less than 2^-20
+    __device__ __forceinline__ uint32_t token(uint32_t slot) const {
+        return (uint32_t)__builtin_fma((double)slot, 1.0 / k, 0.5 / k);
+    }
+    // elements; below 0: nowhere
+    __device__ __forceinline__ int64_t offset(uint32_t entry) const {
+        if constexpr (!GATHER) return (int64_t)entry * stride;
+        return entry < slots ? (int64_t)token(entry) * stride : -1;
+    }
+    // bytes, of a tensor that has fewer than kNowhere
+    __device__ __forceinline__ uint32_t near_offset(uint32_t entry, uint32_t es) const {
+        const uint32_t at = token(entry) * ((uint32_t)stride * es);
+        return entry < slots ? at : 0xFFFFFFFFu;
+    }
+};
+
 // Blocks come to the eight XCDs in turn; each XCD gets a run of neighbouring tiles,
 // which share operands in its L2.
 __device__ __forceinline__ int64_t own_tile(int64_t block, int64_t total) {
     const int64_t run = (total + 7) / 8, at = block / 8;
     return at < run ? block % 8 * run + at : total;
+}
+// The same in runs of `run` tiles, for tiles of unequal work.
+__device__ __forceinline__ int64_t own_tile_in_runs(int64_t block, int run) {
+    const int64_t at = block / 8;
+    return at / run * (8 * run) + block % 8 * run + at % run;
 }
 
 struct RowTile {
@@ -124,74 +183,109 @@ __device__ __forceinline__ bool find_tile(const ExpertLists &l, int bm, int nt, 
     return true;
 }
 
-// kChunk elements from p, those below `have` (of which there may be none).
+// 16 bytes of elements from p (at any alignment: the hardware splits such loads), of
+// which `have` are there, perhaps none.
 template <typename T>
 __device__ __forceinline__ u32x4 load_some(const T *p, int have) {
+    constexpr int kMost = 16 / (int)sizeof(T), kWord = 4 / (int)sizeof(T);
     u32x4 v = {0, 0, 0, 0};
-    if constexpr (sizeof(T) == 2) {
+    if (have >= kMost) {
+        __builtin_memcpy(&v, p, 16);
+        return v;
+    }
 #pragma unroll
-        for (int j = 0; j < 8; j++)
-            if (j < have) v[j / 2] |= (uint32_t)p[j] << 16 * (j & 1);
-    } else {
-#pragma unroll
-        for (int j = 0; j < 4; j++)
-            if (j < have) v[j] = __float_as_uint(p[j]);
+    for (int j = 0; j < kMost; j++) {
+        if (j >= have) continue;
+        if constexpr (sizeof(T) == 4)
+            v[j] = __builtin_bit_cast(uint32_t, p[j]);
+        else
+            v[j / kWord] |= (uint32_t)(typename std::make_unsigned<T>::type)p[j] << 32 / kWord * (j % kWord);
     }
     return v;
 }
 
-__device__ __forceinline__ void to_lds(const void *from, char *wave_base) {
-    __builtin_amdgcn_global_load_lds(DQ_GLOBAL(from), DQ_LDS(wave_base), 16, 0, 0);
-}
+// Loads of 16 bytes a lane from a moving base (the same in all lanes) and 32-bit
+// offsets straight into LDS, 1 KB for a wave.  At kNowhere and beyond, the range
+// check of the buffer gives zeros.  The load is written out because the compiler, told
+// of it, holds every transposing LDS read back until all such loads have landed; it has
+// no result in registers, and all_waves() waits for it.  M0, where in LDS it goes, is
+// used by nothing else here, and needs a cycle to arrive.
+constexpr uint32_t kNowhere = 0xFFFFFFF0u;
+struct Stream {
+    uint32_t lo, hi;
+    __device__ __forceinline__ void at(const void *p) {
+        const uint64_t q = reinterpret_cast<uint64_t>(p);
+        lo = __builtin_amdgcn_readfirstlane((uint32_t)q);
+        hi = __builtin_amdgcn_readfirstlane((uint32_t)(q >> 32));
+    }
+    __device__ __forceinline__ void to_lds(int64_t ahead, uint32_t offset, const char *wave_base) const {
+        const uint64_t q = ((uint64_t)hi << 32 | lo) + (uint64_t)ahead;
+        const u32x4 buffer = {(uint32_t)q, (uint32_t)(q >> 32) & 0xFFFFu, kNowhere, 0x00020000u};
+        const uint32_t m0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)DQ_LDS(const_cast<char *>(wave_base)));
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(m0), "v"(offset),
+                     "s"(buffer)
+                     : "memory");
+    }
+};
 
 // An operand whose rows (the tile's M or N) are contiguous along the inner index.
-// In LDS a row is 128 bytes, its chunk c at place c ^ (row & 7), so that the
-// 16 rows of a matrix operand are read without bank conflicts.
+// In LDS a row's chunks of 16 bytes are exchanged, by c ^ (row & 7) in rows of 128
+// bytes, by c ^ (row / 2 & 3) in rows of 64, so that eight neighbouring rows of a matrix
+// operand meet all banks.
 template <class C, int ROWS, int L>
 struct Along {
     typedef typename C::T T;
-    static constexpr int kBytes = ROWS * 128, kPer = ROWS * 8 / C::kThreads;
-    static_assert(ROWS * 8 % C::kThreads == 0 && C::kThreads % 64 == 0, "whole chunks");
-    const T *p[kPer];
+    static constexpr int kRowChunks = C::kRow / 16, kPer = ROWS * kRowChunks / C::kThreads, BK = C::BK;
+    static constexpr bool kAsyncLoad = L == kAsync;
+    static_assert(ROWS * kRowChunks % C::kThreads == 0 && C::kThreads % (16 * kRowChunks) == 0, "whole chunks");
+    struct Entries {};
+    Stream from;                       // kAsync
+    uint32_t off[kAsyncLoad ? kPer : 1];
+    const T *p[kAsyncLoad ? 1 : kPer];  // else
+    u32x4 v[kAsyncLoad ? 1 : kPer];
     int K, kc;
-    u32x4 v[L == kAsync ? 1 : kPer];
 
+    static __device__ __forceinline__ int swap(int chunk, int row) {
+        return kRowChunks == 8 ? chunk ^ (row & 7) : chunk ^ (row >> 1 & 3);
+    }
+    // row(i): where the tile's row i starts, from base (below 0: nowhere)
     template <class Row>
     __device__ __forceinline__ void start(const T *base, int inner, Row row) {
         K = inner;
-        const int r0 = threadIdx.x >> 3;
-        kc = ((threadIdx.x & 7) ^ (r0 & 7)) * C::kChunk;
+        const int r0 = C::tid() / kRowChunks;
+        kc = swap(C::tid() % kRowChunks, r0) * C::kChunk;
+        if constexpr (kAsyncLoad) from.at(base);
 #pragma unroll
         for (int i = 0; i < kPer; i++) {
-            const int64_t at = row(r0 + i * (C::kThreads / 8));
-            p[i] = at < 0 ? nullptr : base + at + kc;
+            const int64_t at = row(r0 + i * (C::kThreads / kRowChunks));
+            if constexpr (kAsyncLoad)
+                off[i] = at < 0 ? kNowhere : (uint32_t)((at + kc) * sizeof(T));
+            else
+                p[i] = at < 0 ? nullptr : base + at + kc;
         }
     }
-    template <class Row>
-    __device__ __forceinline__ void ahead(int, Row) {}
-    __device__ __forceinline__ void issue(char *buf, int k0) {
+    __device__ __forceinline__ void ahead(int, Entries &) const {}
+    __device__ __forceinline__ void issue(char *buf, int k0, const Entries &) {
         const int have = K - k0 - kc;
 #pragma unroll
         for (int i = 0; i < kPer; i++) {
-            const bool there = p[i] != nullptr && have > 0;
-            if constexpr (L == kAsync) {
-                const void *from = there ? static_cast<const void *>(p[i] + k0) : kZeros;
-                to_lds(from, buf + ((threadIdx.x & ~63) + i * C::kThreads) * 16);
-            } else {
-                v[i] = load_some(p[i] + k0, there ? have : 0);
-            }
+            if constexpr (kAsyncLoad)
+                from.to_lds((int64_t)k0 * sizeof(T), have > 0 ? off[i] : kNowhere,
+                            buf + (64 * C::wave() + i * C::kThreads) * 16);
+            else
+                v[i] = load_some(p[i] + k0, p[i] ? have : 0);
         }
     }
     __device__ __forceinline__ void commit(char *buf) {
-        if constexpr (L != kAsync)
+        if constexpr (!kAsyncLoad)
 #pragma unroll
             for (int i = 0; i < kPer; i++)
-                *reinterpret_cast<u32x4 *>(buf + (threadIdx.x + i * C::kThreads) * 16) = v[i];
+                *reinterpret_cast<u32x4 *>(buf + (C::tid() + i * C::kThreads) * 16) = v[i];
     }
     // rows row0 .. row0 + 15, half h of the step: lane l has row l & 15, chunk (l >> 4) + 4 h
     static __device__ __forceinline__ u32x4 frag(const char *buf, int row0, int h) {
         const int lane = threadIdx.x & 63, row = row0 + (lane & 15);
-        return *reinterpret_cast<const u32x4 *>(buf + row * 128 + (((lane >> 4) + 4 * h) ^ (lane & 7)) * 16);
+        return *reinterpret_cast<const u32x4 *>(buf + row * C::kRow + swap((lane >> 4) + 4 * h, lane) * 16);
     }
 };
 
@@ -199,18 +293,26 @@ struct Along {
 // LDS as it lies in memory, BK rows of COLS elements, with units of 16 elements
 // exchanged within a row: bf16 is turned by the transposing LDS read, where 16 lanes
 // take 4 rows of 32 bytes, fp32 read by elements, where the wave takes 4 rows.
-template <class C, int COLS, int L>
+template <class C, int COLS, int L, bool GATHER>
 struct Across {
     typedef typename C::T T;
     static constexpr int kRow = COLS * (int)sizeof(T), kBytes = C::BK * kRow, kUnits = COLS / 16;
-    static constexpr bool kFromKept = L == kKept || L == kKeptAny;
+    static constexpr bool kFromKept = L == kKept;
     static constexpr int kPieces = kFromKept ? C::BK * kUnits : kBytes / 16;
-    static constexpr int kPer = kPieces / C::kThreads, kPerRow = kPieces / C::BK;
+    static constexpr int kPer = kPieces / C::kThreads, kPerRow = kPieces / C::BK, BK = C::BK;
+    static constexpr bool kAsyncLoad = L == kAsync;
     static_assert(kPieces % C::kThreads == 0 && kUnits % 4 == 0, "whole pieces");
-    const T *base;
-    const int8_t *codes;
+    Stream from;                       // kAsync
+    const T *base;                     // kAny
+    const int8_t *codes;               // kKept
     const uint8_t *exponents;
-    int64_t off[kPer];
+    RowsDown<GATHER> rows;
+    // through the scalar cache: a wave's load of 1 KB meets kShared rows
+    static constexpr bool kScalar = kAsyncLoad && GATHER && C::kRow == 64;
+    static constexpr int kShared = kScalar ? 64 / kPerRow : 1;
+    struct Entries {
+        uint32_t at[GATHER || !kAsyncLoad ? kPer : 1][kShared];
+    };
     int K, N, col0;
     u32x4 v[L == kAsync ? 1 : kPer];
     uint8_t ex[kFromKept ? kPer : 1];
@@ -220,8 +322,10 @@ struct Across {
         if constexpr (kUnits % 8 == 0) return (k & 3) | (k >> 1 & 4);
         return k & 3;
     }
+    __device__ __forceinline__ explicit Across(const RowsDown<GATHER> &r) : rows(r) {}
     __device__ __forceinline__ void start(const T *b, int c0, int cols, int inner) {
         base = b;
+        if constexpr (kAsyncLoad) from.at(b);
         col0 = c0;
         N = cols;
         K = inner;
@@ -233,45 +337,60 @@ struct Across {
         N = cols;
         K = inner;
     }
-    static __device__ __forceinline__ int piece_row(int i) { return (threadIdx.x + i * C::kThreads) / kPerRow; }
+    static __device__ __forceinline__ int piece_row(int i) { return (C::tid() + i * C::kThreads) / kPerRow; }
     __device__ __forceinline__ int piece_col(int i) const {
-        const int at = (threadIdx.x + i * C::kThreads) % kPerRow;
+        const int at = (C::tid() + i * C::kThreads) % kPerRow;
         if (kFromKept) return col0 + 16 * at;
         constexpr int kUnit = 16 / C::kChunk;
         return col0 + ((at / kUnit ^ swap(piece_row(i))) * kUnit + at % kUnit) * C::kChunk;
     }
-    // where the rows of the step at k0 lie (its lists are read a step ahead)
-    template <class Row>
-    __device__ __forceinline__ void ahead(int k0, Row row) {
+    // the lists' entries for the step at k0
+    __device__ __forceinline__ void ahead(int k0, Entries &e) const {
+        if constexpr (kScalar) {
+            const int row = C::wave() * kShared;
 #pragma unroll
-        for (int i = 0; i < kPer; i++) {
-            const int k = k0 + piece_row(i);
-            off[i] = k < K ? row(k) : -1;
+            for (int i = 0; i < kPer; i++)
+#pragma unroll
+                for (int j = 0; j < kShared; j++)
+                    e.at[i][j] = rows.shared_entry(k0 + row + j + i * (C::kThreads / kPerRow));
+        } else if constexpr (GATHER || !kAsyncLoad) {
+#pragma unroll
+            for (int i = 0; i < kPer; i++) e.at[i][0] = rows.entry(k0 + piece_row(i));
         }
     }
-    __device__ __forceinline__ void issue(char *buf, int) {
+    static __device__ __forceinline__ uint32_t entry_of(const Entries &e, int i) {
+        uint32_t v = e.at[i][0];
+#pragma unroll
+        for (int j = 1; j < kShared; j++)
+            // by a mask: a select would become an indexed read of the list, from scratch memory
+            v ^= (e.at[i][j - 1] ^ e.at[i][j]) & -(uint32_t)((threadIdx.x & 63) / kPerRow >= j);
+        return v;
+    }
+    __device__ __forceinline__ void issue(char *buf, int k0, const Entries &e) {
 #pragma unroll
         for (int i = 0; i < kPer; i++) {
             const int col = piece_col(i);
-            const bool there = off[i] >= 0 && col < N;
             if constexpr (L == kAsync) {
-                const void *from = there ? static_cast<const void *>(base + off[i] + col) : kZeros;
-                to_lds(from, buf + ((threadIdx.x & ~63) + i * C::kThreads) * 16);
-            } else if constexpr (L == kAny) {
-                v[i] = load_some(base + off[i] + col, there ? N - col : 0);
-            } else {
+                // rows that are not gathered: the base moves, the offsets stay
+                const int64_t moved = GATHER ? 0 : (int64_t)(rows.first + k0) * rows.stride * (int64_t)sizeof(T);
+                const uint32_t off = GATHER ? rows.near_offset(entry_of(e, GATHER ? i : 0), sizeof(T))
+                                            : (uint32_t)piece_row(i) * (uint32_t)(rows.stride * (int64_t)sizeof(T));
+                const bool there = off < kNowhere && col < N && k0 + piece_row(i) < K;
+                from.to_lds(moved, there ? off + (uint32_t)(col * sizeof(T)) : kNowhere,
+                            buf + (64 * C::wave() + i * C::kThreads) * 16);
+                continue;
+            }
+            const int64_t off = rows.offset(e.at[i][0]);
+            const bool there = off >= 0 && col < N && k0 + piece_row(i) < K;
+            if constexpr (L == kAny) {
+                v[i] = load_some(base + off + col, there ? N - col : 0);
+            } else if constexpr (kFromKept) {
                 v[i] = u32x4{0, 0, 0, 0};
                 ex[i] = 127;
                 if (there) {
-                    ex[i] = exponents[off[i] * ((N + 31) / 32) + col / 32];
-                    const int8_t *c = codes + off[i] * N + col;
-                    if constexpr (L == kKept) {
-                        v[i] = *reinterpret_cast<const u32x4 *>(c);
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 16; j++)
-                            if (col + j < N) v[i][j / 4] |= (uint32_t)(uint8_t)c[j] << 8 * (j & 3);
-                    }
+                    ex[i] = exponents[off * ((N + 31) / 32) + col / 32];
+                    const int8_t *c = codes + off * N + col;
+                    v[i] = load_some(c, N - col);
                 }
             }
         }
@@ -280,11 +399,11 @@ struct Across {
         if constexpr (L == kAny) {
 #pragma unroll
             for (int i = 0; i < kPer; i++)
-                *reinterpret_cast<u32x4 *>(buf + (threadIdx.x + i * C::kThreads) * 16) = v[i];
+                *reinterpret_cast<u32x4 *>(buf + (C::tid() + i * C::kThreads) * 16) = v[i];
         } else if constexpr (kFromKept) {
 #pragma unroll
             for (int i = 0; i < kPer; i++) {
-                const int k = piece_row(i), unit = (threadIdx.x + i * C::kThreads) % kPerRow;
+                const int k = piece_row(i), unit = (C::tid() + i * C::kThreads) % kPerRow;
                 u32x4 *to = reinterpret_cast<u32x4 *>(buf + k * kRow + (unit ^ swap(k)) * 16 * sizeof(T));
                 const float scale = __uint_as_float((uint32_t)ex[i] << 23);
                 float f[16];
@@ -361,35 +480,45 @@ struct Acc {
 #pragma unroll
             for (int j = 0; j < C::TN; j++) v[i][j] = f32x4{0, 0, 0, 0};
     }
-    static __device__ __forceinline__ int wave() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
-    static __device__ __forceinline__ int m0() { return wave() / C::WN * (C::BM / C::WM); }
-    static __device__ __forceinline__ int n0() { return wave() % C::WN * (C::BN / C::WN); }
+    static __device__ __forceinline__ int m0() { return C::wave() / C::WN * (C::BM / C::WM); }
+    static __device__ __forceinline__ int n0() { return C::wave() % C::WN * (C::BN / C::WN); }
 
-    template <class A, class B>
-    __device__ __forceinline__ void step(const char *a, const char *b) {
+    // half a step's matrix operands
+    struct Half {
+        u32x4 a[C::TM], b[C::TN];
+        template <class A, class B>
+        __device__ __forceinline__ void read(const char *lds, int h) {
 #pragma unroll
-        for (int h = 0; h < 2; h++) {
-            u32x4 fa[C::TM], fb[C::TN];
+            for (int j = 0; j < C::TN; j++) b[j] = B::frag(lds + C::kBytesA, n0() + 16 * j, h);
 #pragma unroll
-            for (int j = 0; j < C::TN; j++) fb[j] = B::frag(b, n0() + 16 * j, h);
-#pragma unroll
-            for (int i = 0; i < C::TM; i++) fa[i] = A::frag(a, m0() + 16 * i, h);
-#pragma unroll
-            for (int i = 0; i < C::TM; i++)
-#pragma unroll
-                for (int j = 0; j < C::TN; j++) {
-                    if constexpr (C::kF32) {
-#pragma unroll
-                        for (int q = 0; q < 4; q++)
-                            v[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(
-                                __uint_as_float(fb[j][q]), __uint_as_float(fa[i][q]), v[i][j], 0, 0, 0);
-                    } else {
-                        v[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, fb[j]),
-                                                                         __builtin_bit_cast(bf16x8, fa[i]), v[i][j],
-                                                                         0, 0, 0);
-                    }
-                }
+            for (int i = 0; i < C::TM; i++) a[i] = A::frag(lds, m0() + 16 * i, h);
         }
+    };
+    __device__ __forceinline__ void add(const Half &f) {
+#pragma unroll
+        for (int i = 0; i < C::TM; i++)
+#pragma unroll
+            for (int j = 0; j < C::TN; j++) {
+                if constexpr (C::kF32) {
+#pragma unroll
+                    for (int q = 0; q < 4; q++)
+                        v[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(f.b[j][q]),
+                                                                       __uint_as_float(f.a[i][q]), v[i][j], 0, 0, 0);
+                } else {
+                    v[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, f.b[j]),
+                                                                     __builtin_bit_cast(bf16x8, f.a[i]), v[i][j], 0, 0,
+                                                                     0);
+                }
+            }
+    }
+    // into LDS, [BM][BN] floats
+    __device__ __forceinline__ void put(float *to) const {
+        const int lane = threadIdx.x & 63;
+#pragma unroll
+        for (int i = 0; i < C::TM; i++)
+#pragma unroll
+            for (int j = 0; j < C::TN; j++)
+                store_four(to + (m0() + 16 * i + (lane & 15)) * C::BN + n0() + 16 * j + (lane >> 4) * 4, v[i][j]);
     }
     // row(m): where the tile's row m goes, NULL: nowhere
     template <class Row>
@@ -414,42 +543,147 @@ struct Acc {
     }
 };
 
-// LDS filled by every wave, its old contents read by every wave.
-__device__ __forceinline__ void step_done() {
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+// All but the last LEFT loads of this wave have landed, its LDS reads and writes are
+// done, and so for every wave of the tile.
+template <class C, int LEFT>
+__device__ __forceinline__ void all_waves() {
+    static_assert(LEFT < 64, "six bits");
+    // by the builtin, so that the compiler counts no LDS read as open behind it: beside a
+    // scalar load it could only wait for all of them
+    __builtin_amdgcn_s_waitcnt(0xC07F);                  // lgkmcnt(0)
+    if constexpr (C::kThreads == 64)
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LEFT) : "memory");
+    else
+        asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(LEFT) : "memory");
 }
 
-// acc += A B over `inner`, two steps in LDS: one is loaded while the other is used.
-template <class C, class A, class B, class RowA, class RowB>
-__device__ __forceinline__ void multiply(char *lds, A &a, B &b, int inner, RowA row_a, RowB row_b, Acc<C> &acc) {
+// Step k0 into LDS: by loads that land there, or from registers, whose next step is then
+// loaded.  Past the end zeros are stored.
+template <class Op>
+__device__ __forceinline__ void fill(Op &op, char *buf, int k0, typename Op::Entries &e) {
+    if constexpr (Op::kAsyncLoad) {
+        op.issue(buf, k0, e);
+        op.ahead(k0 + Op::BK, e);
+    } else {
+        op.commit(buf);
+        op.issue(nullptr, k0 + Op::BK, e);
+        op.ahead(k0 + 2 * Op::BK, e);
+    }
+}
+
+// acc += A B over `inner`.  Two steps in LDS; the barrier stands in the middle of a
+// step's products, when the step after it has landed and the second half's operands are
+// in registers: LDS reads run beside the other half's products, loads beside a
+// whole step's.
+template <class C, class A, class B>
+__device__ __forceinline__ void multiply_halves(char *lds, A &a, B &b, int inner, Acc<C> &acc) {
     constexpr int kStep = C::kBytesA + C::kBytesB;
+    constexpr bool kBothAsync = A::kAsyncLoad && B::kAsyncLoad;
     if (inner <= 0) return;
     const int steps = (inner + C::BK - 1) / C::BK;
-    a.ahead(0, row_a);
-    b.ahead(0, row_b);
-    a.issue(lds, 0);
-    b.issue(lds + C::kBytesA, 0);
-    a.ahead(C::BK, row_a);
-    b.ahead(C::BK, row_b);
-    a.commit(lds);
-    b.commit(lds + C::kBytesA);
-    step_done();
+    typename A::Entries ea[2];
+    typename B::Entries eb[2];
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+        a.ahead(i * C::BK, ea[i]);
+        b.ahead(i * C::BK, eb[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+        a.issue(lds + i * kStep, i * C::BK, ea[i]);
+        b.issue(lds + i * kStep + C::kBytesA, i * C::BK, eb[i]);
+        a.commit(lds + i * kStep);
+        b.commit(lds + i * kStep + C::kBytesA);
+    }
+    all_waves<C, kBothAsync ? A::kPer + B::kPer : 0>();
+    a.ahead(2 * C::BK, ea[0]);
+    b.ahead(2 * C::BK, eb[0]);
+    if (!A::kAsyncLoad) a.issue(nullptr, 2 * C::BK, ea[0]);
+    if (!B::kAsyncLoad) b.issue(nullptr, 2 * C::BK, eb[0]);
+    if (!A::kAsyncLoad) a.ahead(3 * C::BK, ea[0]);
+    if (!B::kAsyncLoad) b.ahead(3 * C::BK, eb[0]);
+    typename Acc<C>::Half first, second;
+    first.template read<A, B>(lds, 0);
     for (int t = 0; t < steps; t++) {
         char *now = lds + (t & 1) * kStep, *next = lds + (~t & 1) * kStep;
-        const bool more = t + 1 < steps;
-        if (more) {
-            a.issue(next, (t + 1) * C::BK);
-            b.issue(next + C::kBytesA, (t + 1) * C::BK);
-            a.ahead((t + 2) * C::BK, row_a);
-            b.ahead((t + 2) * C::BK, row_b);
+        second.template read<A, B>(now, 1);
+        acc.add(first);
+        __builtin_amdgcn_sched_barrier(0);
+        all_waves<C, 0>();
+        __builtin_amdgcn_sched_barrier(0);
+        if (t + 1 < steps) {
+            first.template read<A, B>(next, 0);
+            const int k = (t + 2) * C::BK;
+            fill(a, now, k, ea[0]);
+            fill(b, now + C::kBytesA, k, eb[0]);
         }
-        acc.template step<A, B>(now, now + C::kBytesA);
-        if (more) {
-            a.commit(next);
-            b.commit(next + C::kBytesA);
-        }
-        step_done();
+        acc.add(second);
+        __builtin_amdgcn_sched_barrier(0);
     }
+}
+
+// acc += A B over `inner`, all operands by loads into LDS: a step's products run beside
+// the LDS reads of the next and the loads of the kStages - 1 after it.  One barrier a step:
+// behind it the next step has landed, and the operands of this one are in registers, so
+// that its place in LDS is free.  Loads past the end are made, of zeros, to keep count.
+template <class C, class A, class B>
+__device__ __forceinline__ void multiply_stages(char *lds, A &a, B &b, int inner, Acc<C> &acc) {
+    constexpr int kStep = C::kBytesA + C::kBytesB, S = C::kStages;
+    static_assert(C::kRow == 64 && S >= 3, "a step is one matrix instruction deep");
+    if (inner <= 0) return;
+    const int steps = (inner + C::BK - 1) / C::BK;
+    {
+        typename A::Entries ea[S];
+        typename B::Entries eb[S];
+#pragma unroll
+        for (int i = 0; i < S; i++) {
+            a.ahead(i * C::BK, ea[i]);
+            b.ahead(i * C::BK, eb[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < S; i++) {
+            a.issue(lds + i * kStep, i * C::BK, ea[i]);
+            b.issue(lds + i * kStep + C::kBytesA, i * C::BK, eb[i]);
+        }
+    }
+    constexpr int kLoads = A::kPer + B::kPer;
+    all_waves<C, (S - 1) * kLoads>();
+    typename Acc<C>::Half half[2];
+    half[0].template read<A, B>(lds, 0);
+    all_waves<C, (S - 2) * kLoads>();
+    int at = 0;                                          // the stage of step t
+    typename A::Entries ea;
+    typename B::Entries eb;
+    a.ahead(S * C::BK, ea);
+    b.ahead(S * C::BK, eb);
+    const auto step = [&](int t, typename Acc<C>::Half &now, typename Acc<C>::Half &next) {
+        const int k = (t + S) * C::BK;
+        a.issue(lds + at, k, ea);
+        b.issue(lds + at + C::kBytesA, k, eb);
+        a.ahead(k + C::BK, ea);
+        b.ahead(k + C::BK, eb);
+        at = at + kStep == S * kStep ? 0 : at + kStep;
+        next.template read<A, B>(lds + at, 0);
+        acc.add(now);
+        __builtin_amdgcn_sched_barrier(0);
+        all_waves<C, (S - 2) * kLoads>();
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    int t = 0;
+    for (; t + 1 < steps; t += 2) {
+        step(t, half[0], half[1]);
+        step(t + 1, half[1], half[0]);
+    }
+    if (t < steps) acc.add(half[0]);
+    all_waves<C, 0>();                                      // nothing may land in LDS after the block
+}
+
+template <class C, class A, class B>
+__device__ __forceinline__ void multiply(char *lds, A &a, B &b, int inner, Acc<C> &acc) {
+    if constexpr (C::kRow == 64)
+        multiply_stages<C>(lds, a, b, inner, acc);
+    else
+        multiply_halves<C>(lds, a, b, inner, acc);
 }
 
 template <class K>

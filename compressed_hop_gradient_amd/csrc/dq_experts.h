@@ -104,7 +104,7 @@ struct ExpertWeightsArgs {
     const uint8_t *exponents;
     const void *dy;
     int64_t dys;
-    int32_t gather_x, gather_dy;
+    int32_t gather;                     // dq_expert_gather
     void *dw;                           // [E][K][N]
     int32_t out_f32;
     int32_t K, N;

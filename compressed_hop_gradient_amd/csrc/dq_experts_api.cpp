@@ -306,8 +306,7 @@ dq_status dq_expert_matmul_grad(const dq_expert_lists *l, const void *x, int64_t
     a.exponents = exponents;
     a.dy = dy;
     a.dys = dys;
-    a.gather_x = gather == DQ_GATHER_X;
-    a.gather_dy = gather == DQ_GATHER_DOUT;
+    a.gather = gather;
     a.dw = dw;
     a.out_f32 = out_kind == DQ_F32;
     a.K = (int32_t)inner;
