@@ -42,14 +42,13 @@ __global__ __launch_bounds__(C::kThreads) void k_product(ExpertProductArgs a, in
     const int n0 = t.n * C::BN;
     Acc<C> acc;
     product_tile<C, LA, LB, TURNED>(a, t, n0, 0, a.K, lds, acc);
-    acc.store([&](int m) { return m < t.rows ? static_cast<T *>(a.y) + (t.first + m) * a.ys : nullptr; }, n0, a.N,
-              vec_out<T>(a.y, a.ys, a.N));
+    acc.store([&](int m) { return m < t.rows ? static_cast<T *>(a.y) + (t.first + m) * a.ys : nullptr; }, n0, a.N);
 }
 
 // The same for few rows, which the weights' bytes bound: a tile is one wave's, four of
 // them take a quarter of the inner index each, wait for their own loads alone, and add up.
 constexpr int kFewWaves = 4;
-template <class C, bool TURNED>
+template <class C, int L, bool TURNED>
 __global__ __launch_bounds__(64 * kFewWaves) void k_product_few(ExpertProductArgs a, int nt) {
     typedef typename C::T T;
     extern __shared__ __align__(1024) char lds[];
@@ -59,7 +58,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_product_few(ExpertProductArg
     const int per = ((a.K + kFewWaves - 1) / kFewWaves + C::BK - 1) / C::BK * C::BK, from = min(wave * per, a.K);
     char *own = lds + wave * C::kLds;
     Acc<C> acc;
-    product_tile<C, kAsync, kAsync, TURNED>(a, t, n0, from, min(per, a.K - from), own, acc);
+    product_tile<C, L, L, TURNED>(a, t, n0, from, min(per, a.K - from), own, acc);
     acc.put(reinterpret_cast<float *>(own));
     __syncthreads();
     static_assert(C::BM * C::BN == 4 * 64 * kFewWaves && C::kLds >= 4 * C::BM * C::BN, "four sums a thread");
@@ -69,14 +68,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_product_few(ExpertProductArg
 #pragma unroll
     for (int w = 0; w < kFewWaves; w++)
         sum += *reinterpret_cast<const f32x4 *>(lds + w * C::kLds + 16 * threadIdx.x);
-    T *y = static_cast<T *>(a.y) + (t.first + m) * a.ys + n0 + n;
-    if (vec_out<T>(a.y, a.ys, a.N) && n0 + n < a.N) {
-        store_four(y, sum);
-    } else {
-#pragma unroll
-        for (int q = 0; q < 4; q++)
-            if (n0 + n + q < a.N) store_one(y + q, sum[q]);
-    }
+    store_columns(static_cast<T *>(a.y) + (t.first + m) * a.ys, n0 + n, a.N, sum);
 }
 
 constexpr int kWeightsRun = 8;
@@ -114,8 +106,7 @@ __global__ __launch_bounds__(C::kThreads) void k_weights(ExpertWeightsArgs a, in
     multiply<C>(lds, x, dy, rows, acc);
     Out *dw = static_cast<Out *>(a.parts > 1 ? (void *)a.partial : a.dw) +
               ((int64_t)part * a.l.E + e) * a.K * a.N;
-    acc.store([&](int m) { return m0 + m < a.K ? dw + (int64_t)(m0 + m) * a.N : nullptr; }, n0, a.N,
-              vec_out<Out>(dw, a.N, a.N));
+    acc.store([&](int m) { return m0 + m < a.K ? dw + (int64_t)(m0 + m) * a.N : nullptr; }, n0, a.N);
 }
 
 // The parts' sums, in their order.
@@ -153,10 +144,10 @@ hipError_t product_as(const ExpertProductArgs &a, hipStream_t s) {
     if (a.turned) return product_launch<C>(k_product<C, LA, LB, true>, C::kThreads, C::kLds, a, s);
     return product_launch<C>(k_product<C, LA, LB, false>, C::kThreads, C::kLds, a, s);
 }
-template <class C>
+template <class C, int L>
 hipError_t product_few(const ExpertProductArgs &a, hipStream_t s) {
-    if (a.turned) return product_launch<C>(k_product_few<C, true>, 64 * kFewWaves, kFewWaves * C::kLds, a, s);
-    return product_launch<C>(k_product_few<C, false>, 64 * kFewWaves, kFewWaves * C::kLds, a, s);
+    if (a.turned) return product_launch<C>(k_product_few<C, L, true>, 64 * kFewWaves, kFewWaves * C::kLds, a, s);
+    return product_launch<C>(k_product_few<C, L, false>, 64 * kFewWaves, kFewWaves * C::kLds, a, s);
 }
 
 // Whether offsets into so many rows fit the 32 bits of the loads into LDS.
@@ -194,24 +185,17 @@ hipError_t weights_as(const ExpertWeightsArgs &a, hipStream_t s) {
     return weights_gathered<C, LA, LB, DQ_GATHER_NONE, Out>(a, s);
 }
 
-template <class C, class Any, typename Out>
-hipError_t weights_loads(const ExpertWeightsArgs &a, hipStream_t s) {
-    constexpr int64_t es = sizeof(typename C::T), chunk = 16 / es;
-    const bool dy_async =
-        on16(a.dy, a.dys * es) && a.N % chunk == 0 && near(a.gather == DQ_GATHER_DOUT ? a.l.tokens : 64, a.dys, a.N, es);
-    if (a.codes) return dy_async ? weights_as<Any, kKept, kAsync, Out>(a, s) : weights_as<Any, kKept, kAny, Out>(a, s);
-    if (dy_async && on16(a.x, a.xs * es) && a.K % chunk == 0 &&
-        near(a.gather == DQ_GATHER_X ? a.l.tokens : 64, a.xs, a.K, es))
-        return weights_as<C, kAsync, kAsync, Out>(a, s);
-    return weights_as<Any, kAny, kAny, Out>(a, s);
-}
-
-template <class C, class Any>
-hipError_t weights_out(const ExpertWeightsArgs &a, hipStream_t s) {
-    if (a.out_f32 || a.parts > 1) return weights_loads<C, Any, float>(a, s);
-    if constexpr (sizeof(typename C::T) == 2) return weights_loads<C, Any, uint16_t>(a, s);
-    return hipErrorInvalidValue;
-}
+template <typename T>
+struct WeightsLoads {
+    static constexpr int64_t es = sizeof(T), chunk = 16 / es;
+    bool x, dy;
+    explicit WeightsLoads(const ExpertWeightsArgs &a) {
+        dy = on16(a.dy, a.dys * es) && a.N % chunk == 0 &&
+             near(a.gather == DQ_GATHER_DOUT ? a.l.tokens : 64, a.dys, a.N, es);
+        x = a.x && on16(a.x, a.xs * es) && a.K % chunk == 0 &&
+            near(a.gather == DQ_GATHER_X ? a.l.tokens : 64, a.xs, a.K, es);
+    }
+};
 
 // Which tile: the one whose blocks are done first, by how many of them a CU gets.
 // Measured: a block's start and end take about 4 us, a step s1 where it has the CU to
@@ -252,32 +236,83 @@ int pick_tile(const TileCost (&costs)[N], const ExpertProductArgs &a, double es)
     return best;
 }
 
+// As above, for tiles of dw whose inner index is an expert's rows.
+template <int N>
+int pick_weights_tile(const TileCost (&costs)[N], const ExpertWeightsArgs &a) {
+    int best = 0;
+    double least = 0;
+    for (int i = 0; i < N; i++) {
+        const TileCost &c = costs[i];
+        const int64_t blocks = (int64_t)((a.K + c.bm - 1) / c.bm) * ((a.N + c.bn - 1) / c.bn) * a.l.E * a.parts;
+        const int64_t per_cu = (blocks + 255) / 256, rest = per_cu % c.full;
+        const double steps = (double)a.l.slots / a.l.E / a.parts / c.step + 8;       // 8: a tile's start and end
+        const double us = steps * ((double)(per_cu / c.full) * c.sn +
+                                   (rest ? c.s1 + (c.sn - c.s1) * (rest - 1) / std::max(1, c.full - 1) : 0.0));
+        if (i == 0 || us < 0.97 * least) {
+            best = i;
+            least = us;
+        }
+    }
+    return best;
+}
+constexpr TileCost kWeightsBf16[] = {
+    {256, 256, 32, 1, 0.80f, 0.80f}, {128, 128, 32, 2, 0.39f, 0.70f}, {64, 64, 32, 4, 0.25f, 0.55f}};
+constexpr TileCost kWeightsF32[] = {{128, 128, 16, 2, 1.12f, 2.10f}, {64, 64, 16, 5, 0.39f, 1.45f}};
+
+template <typename Out>
+hipError_t weights_bf16(const ExpertWeightsArgs &a, hipStream_t s) {
+    const WeightsLoads<uint16_t> on(a);
+    if (a.codes) return on.dy ? weights_as<TileAny, kKept, kAsync, Out>(a, s) : weights_as<TileAny, kKept, kAny, Out>(a, s);
+    if (!on.x || !on.dy) return weights_as<TileAny, kAny, kAny, Out>(a, s);
+    const int pick = FORCE >= 0 ? FORCE : pick_weights_tile(kWeightsBf16, a);
+    if (pick == 0) return weights_as<TileBig, kAsync, kAsync, Out>(a, s);
+    if (pick == 1) return weights_as<TileMid, kAsync, kAsync, Out>(a, s);
+    return weights_as<TileNarrow, kAsync, kAsync, Out>(a, s);
+}
+hipError_t weights_f32(const ExpertWeightsArgs &a, hipStream_t s) {
+    const WeightsLoads<float> on(a);
+    if (a.codes)
+        return on.dy ? weights_as<TileAnyF32, kKept, kAsync, float>(a, s) : weights_as<TileAnyF32, kKept, kAny, float>(a, s);
+    if (!on.x || !on.dy) return weights_as<TileAnyF32, kAny, kAny, float>(a, s);
+    const int pick = FORCE >= 0 ? FORCE : pick_weights_tile(kWeightsF32, a);
+    if (pick == 0) return weights_as<TileMidF32, kAsync, kAsync, float>(a, s);
+    return weights_as<TileSmallF32, kAsync, kAsync, float>(a, s);
+}
+
 }  // namespace
 
 hipError_t launch_expert_product(const ExpertProductArgs &a, int f32, hipStream_t s) {
     if (a.l.slots == 0) return hipSuccess;
     if (f32) {
-        if (!product_async<float>(a)) return product_as<TileAnyF32, kAny, kAny>(a, s);
         const int pick = FORCE >= 0 ? FORCE : pick_tile(kCostF32, a, 4);
+        if (!product_async<float>(a))
+            return pick == 2 ? product_few<TileFewAnyF32, kAny>(a, s) : product_as<TileAnyF32, kAny, kAny>(a, s);
         if (pick == 0) return product_as<TileSmallF32, kAsync, kAsync>(a, s);
         if (pick == 1) return product_as<TileMidF32, kAsync, kAsync>(a, s);
-        return product_few<TileFewF32>(a, s);
+        return product_few<TileFewF32, kAsync>(a, s);
     }
-    if (!product_async<uint16_t>(a)) return product_as<TileAny, kAny, kAny>(a, s);
     const int pick = FORCE >= 0 ? FORCE : pick_tile(kCostBf16, a, 2);
+    if (!product_async<uint16_t>(a))
+        return pick == 3 ? product_few<TileFewAny, kAny>(a, s) : product_as<TileAny, kAny, kAny>(a, s);
     if (pick == 0) return product_as<TileSmall, kAsync, kAsync>(a, s);
     if (pick == 1) return product_as<TileMid, kAsync, kAsync>(a, s);
     if (pick == 2) return product_as<TileBig, kAsync, kAsync>(a, s);
-    return product_few<TileFew>(a, s);
+    return product_few<TileFew, kAsync>(a, s);
 }
 
-int expert_weights_parts(int64_t, int, int64_t, int64_t, int) { return 1; }
+// Enough parts that tiles of 128 x 128 give every CU a block, of 128 rows of an average
+// expert at least.
+int expert_weights_parts(int64_t slots, int E, int64_t K, int64_t N, int) {
+    const int64_t tiles = (K + 127) / 128 * ((N + 127) / 128) * E, most = slots / E / 128;
+    const int64_t parts = tiles >= 256 ? 1 : (255 + tiles) / tiles;
+    return (int)std::max((int64_t)1, std::min(parts, most));
+}
 
 hipError_t launch_expert_weights(const ExpertWeightsArgs &a, int f32, hipStream_t s) {
-    if (a.K == 0 || a.N == 0) return hipSuccess;
-    hipError_t e = f32 ? weights_out<TileMidF32, TileAnyF32>(a, s) : weights_out<TileBig, TileAny>(a, s);
+    const hipError_t e = f32 ? weights_f32(a, s)
+                             : a.out_f32 || a.parts > 1 ? weights_bf16<float>(a, s) : weights_bf16<uint16_t>(a, s);
     if (e != hipSuccess || a.parts == 1) return e;
-    const int64_t n = (int64_t)a.l.E * a.K * a.N, blocks = (n + 1023) / 1024;
+    const int64_t n = (int64_t)a.l.E * a.K * a.N, blocks = (n + 255) / 256;
     const dim3 grid((unsigned)(blocks < 65536 ? blocks : 65536));
     if (a.out_f32)
         hipLaunchKernelGGL((k_weights_join<float>), grid, dim3(256), 0, s, a.partial, a.parts, n, static_cast<float *>(a.dw));

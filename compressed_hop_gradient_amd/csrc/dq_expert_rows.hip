@@ -127,49 +127,39 @@ __global__ __launch_bounds__(kRowsThreads) void k_rows_place(ExpertRowsArgs a) {
 // ---- way back -----------------------------------------------------------------
 
 // out[t] = residual[t] + the token's rows in the order of its choices, fp32, rounded
-// once; a choice without a row adds nothing.  VEC: eight elements a thread.
-template <bool F32, bool RES, bool VEC>
+// once; a choice without a row adds nothing.  A thread takes eight elements, four of a
+// token's rows in flight.
+template <bool F32, bool RES, bool EVEN>
 __global__ __launch_bounds__(256) void k_expert_sum(ExpertSumArgs a, int lanes) {
-    typedef Elem<F32> El;
-    typedef typename El::type T;
-    constexpr int kEach = VEC ? 8 : 1;
     const int64_t token = (int64_t)blockIdx.x * (256 / lanes) + threadIdx.x / lanes;
     if (token >= a.l.tokens) return;
     const int32_t *rows = a.l.row + token * a.l.k;
-    const T *y = static_cast<const T *>(a.y);
-    for (int c = (threadIdx.x % lanes) * kEach; c < a.width; c += lanes * kEach) {
-        float s[kEach];
-        if constexpr (!RES) {
-#pragma unroll
-            for (int q = 0; q < kEach; q++) s[q] = 0.0f;
-        } else if constexpr (VEC) {
-            load8<F32>(a.residual, token * a.rs + c, s);
+    by_eights<EVEN>((threadIdx.x % lanes) * 8, lanes * 8, a.width, [&](auto full, int c) {
+        constexpr bool kFull = decltype(full)::value;
+        const int have = a.width - c;
+        float s[8];
+        if constexpr (RES) {
+            load_eight<F32, kFull>(a.residual, token * a.rs + c, have, s);
         } else {
-            s[0] = El::up(static_cast<const T *>(a.residual)[token * a.rs + c]);
+#pragma unroll
+            for (int q = 0; q < 8; q++) s[q] = 0.0f;
         }
         for (int j0 = 0; j0 < a.l.k; j0 += 4) {
-            float v[4][kEach];
+            float v[4][8];
             bool there[4];
 #pragma unroll
             for (int j = 0; j < 4; j++) {
                 const uint32_t r = j0 + j < a.l.k ? (uint32_t)rows[j0 + j] : 0xFFFFFFFFu;
                 there[j] = r < (uint32_t)a.l.slots;
-                const int64_t at = (there[j] ? (int64_t)r : 0) * a.ys + c;
-                if constexpr (VEC)
-                    load8<F32>(y, at, v[j]);
-                else
-                    v[j][0] = El::up(y[at]);
+                load_eight<F32, kFull>(a.y, (there[j] ? (int64_t)r : 0) * a.ys + c, have, v[j]);
             }
 #pragma unroll
             for (int j = 0; j < 4; j++)
 #pragma unroll
-                for (int q = 0; q < kEach; q++) s[q] += there[j] ? v[j][q] : 0.0f;
+                for (int q = 0; q < 8; q++) s[q] += there[j] ? v[j][q] : 0.0f;
         }
-        if constexpr (VEC)
-            store8<F32>(a.out, token * a.os + c, s);
-        else
-            static_cast<T *>(a.out)[token * a.os + c] = El::down(s[0]);
-    }
+        store_eight<F32, kFull>(a.out, token * a.os + c, have, s);
+    });
 }
 
 // ---- activation ---------------------------------------------------------------
@@ -189,59 +179,44 @@ __device__ __forceinline__ float sigmoid(float x) {
 __device__ __forceinline__ float relu(float x) { return x <= 0.0f ? 0.0f : x; }
 __device__ __forceinline__ float relu_back(float x, float d) { return x <= 0.0f ? 0.0f : x > 0.0f ? d : x; }
 
-template <bool F32, bool VEC>
-__device__ __forceinline__ void read(const void *p, int64_t at, float *v) {
-    if constexpr (VEC)
-        load8<F32>(p, at, v);
-    else
-        v[0] = Elem<F32>::up(static_cast<const typename Elem<F32>::type *>(p)[at]);
-}
-template <bool F32, bool VEC>
-__device__ __forceinline__ void write(void *p, int64_t at, const float *v) {
-    if constexpr (VEC)
-        store8<F32>(p, at, v);
-    else
-        static_cast<typename Elem<F32>::type *>(p)[at] = Elem<F32>::down(v[0]);
-}
-
-// `lanes` threads to a row (64 or a power of two below): no division, and the gate's
-// gradient, a sum over the row, stays in a wave.
-template <bool F32, bool GATED, bool VEC, bool KEEP>
+// `lanes` threads to a row (64 or a power of two below), eight columns each: no
+// division, and the gate's gradient, a sum over the row, stays in a wave.  EVEN: widths of
+// whole eights; KEEP: of whole blocks of 32, which four neighbouring threads hold.
+template <bool F32, bool GATED, bool EVEN, bool KEEP>
 __global__ __launch_bounds__(256) void k_act(ExpertActArgs a, int lanes) {
-    constexpr int kEach = VEC ? 8 : 1;
     const int rows = clampi(a.l.offsets[a.l.E], 0, a.l.slots), U = GATED ? 2 * a.width : a.width;
     const uint32_t round = KEEP ? a.key.round + (a.key.d_round ? *a.key.d_round : 0) : 0;
     const int64_t row = (int64_t)blockIdx.x * (256 / lanes) + threadIdx.x / lanes;
     if (row >= rows) return;
     const uint32_t slot = (uint32_t)a.l.source[row];
     const float gate = slot < (uint32_t)a.l.slots ? a.gates[slot] : 0.0f;
-    for (int c = (threadIdx.x % lanes) * kEach; c < a.width; c += lanes * kEach) {
-        float g[kEach], v[kEach], o[kEach];
-        read<F32, VEC>(a.u, row * a.us + c, g);
-        if (GATED) read<F32, VEC>(a.u, row * a.us + a.width + c, v);
+    by_eights<EVEN>((threadIdx.x % lanes) * 8, lanes * 8, a.width, [&](auto full, int c) {
+        constexpr bool kFull = decltype(full)::value;
+        const int have = a.width - c;
+        float g[8], v[8], o[8];
+        load_eight<F32, kFull>(a.u, row * a.us + c, have, g);
+        if (GATED) load_eight<F32, kFull>(a.u, row * a.us + a.width + c, have, v);
 #pragma unroll
-        for (int q = 0; q < kEach; q++)
-            o[q] = gate * (GATED ? g[q] * sigmoid(g[q]) * v[q] : relu(g[q]));
-        write<F32, VEC>(a.a, row * a.as + c, o);
-        if constexpr (KEEP) {
+        for (int q = 0; q < 8; q++) o[q] = gate * (GATED ? g[q] * sigmoid(g[q]) * v[q] : relu(g[q]));
+        store_eight<F32, kFull>(a.a, row * a.as + c, have, o);
+        if constexpr (KEEP && kFull) {
             const int64_t blocks = U / 32;
 #pragma unroll
             for (int half = 0; half < (GATED ? 2 : 1); half++) {
                 const int col = half * a.width + c;
                 uint32_t w[4], exponent;
                 keep_dithers<true>(row * U + col, a.key, round, w);
-                *reinterpret_cast<uint2 *>(a.codes + row * U + col) = keep_eight(half ? v : g, w, exponent);
+                store_codes<true>(a.codes + row * U + col, 8, keep_eight(half ? v : g, w, exponent));
                 if ((threadIdx.x & 3) == 0) a.exponents[row * blocks + col / 32] = (uint8_t)exponent;
             }
         }
-    }
+    });
 }
 
 // From the kept codes or from u itself: du, the activation again, and the gates'
 // gradient (0 for a slot without an expert).
-template <bool F32, bool GATED, bool VEC, bool KEPT>
+template <bool F32, bool GATED, bool EVEN, bool KEPT>
 __global__ __launch_bounds__(256) void k_act_backward(ExpertActArgs a, int lanes) {
-    constexpr int kEach = VEC ? 8 : 1;
     const int rows = clampi(a.l.offsets[a.l.E], 0, a.l.slots), U = GATED ? 2 * a.width : a.width;
     const int64_t row = (int64_t)blockIdx.x * (256 / lanes) + threadIdx.x / lanes;
     if (row >= a.l.slots) return;
@@ -254,28 +229,30 @@ __global__ __launch_bounds__(256) void k_act_backward(ExpertActArgs a, int lanes
     }
     const float gate = known ? a.gates[slot] : 0.0f;
     const int64_t blocks = (U + 31) / 32;
-    const auto half = [&](int col, float *v) {
-        if constexpr (!KEPT) {
-            read<F32, VEC>(a.u, row * a.us + col, v);
-        } else {
-            const float scale = kept_scale(a.exponents[row * blocks + col / 32]);
-            if constexpr (VEC) {
-                const uint2 c = *reinterpret_cast<const uint2 *>(a.codes + row * U + col);
-#pragma unroll
-                for (int q = 0; q < 8; q++) v[q] = kept_value(q < 4 ? c.x : c.y, q & 3, scale);
-            } else {
-                v[0] = (float)a.codes[row * U + col] * scale;
-            }
-        }
-    };
     float sum = 0.0f;
-    for (int c = lane * kEach; c < a.width; c += lanes * kEach) {
-        float g[kEach], v[kEach], d[kEach], dg[kEach], dv[kEach], o[kEach];
-        half(c, g);
-        if (GATED) half(a.width + c, v);
-        read<F32, VEC>(a.da, row * a.das + c, d);
+    by_eights<EVEN>(lane * 8, lanes * 8, a.width, [&](auto full, int c) {
+        constexpr bool kFull = decltype(full)::value;
+        const int have = a.width - c;
+        const auto columns = [&](int col, float *v) {
+            if constexpr (!KEPT) {
+                load_eight<F32, kFull>(a.u, row * a.us + col, have, v);
+            } else {
+                // of one block, or (the value half of an odd width) of two
+                const uint8_t *e = a.exponents + row * blocks;
+                const float s0 = kept_scale(e[col / 32]);
+                const float s1 = EVEN ? s0 : kept_scale(e[(col + (have < 8 ? have : 8) - 1) / 32]);
+                const uint2 w = load_codes<kFull>(a.codes + row * U + col, have);
 #pragma unroll
-        for (int q = 0; q < kEach; q++) {
+                for (int q = 0; q < 8; q++)
+                    v[q] = kept_value(q < 4 ? w.x : w.y, q & 3, EVEN || col % 32 + q < 32 ? s0 : s1);
+            }
+        };
+        float g[8], v[8], d[8], dg[8], dv[8], o[8];
+        columns(c, g);
+        if (GATED) columns(a.width + c, v);
+        load_eight<F32, kFull>(a.da, row * a.das + c, have, d);
+#pragma unroll
+        for (int q = 0; q < 8; q++) {
             float h;
             if (GATED) {
                 const float s = sigmoid(g[q]), silu = g[q] * s, t = gate * d[q];
@@ -287,83 +264,69 @@ __global__ __launch_bounds__(256) void k_act_backward(ExpertActArgs a, int lanes
                 dg[q] = relu_back(g[q], gate * d[q]);
             }
             o[q] = gate * h;
-            sum += d[q] * h;
+            sum += kFull || q < have ? d[q] * h : 0.0f;
         }
-        write<F32, VEC>(a.du, row * a.dus + c, dg);
-        if (GATED) write<F32, VEC>(a.du, row * a.dus + a.width + c, dv);
-        if (a.a) write<F32, VEC>(a.a, row * a.as + c, o);
-    }
+        store_eight<F32, kFull>(a.du, row * a.dus + c, have, dg);
+        if (GATED) store_eight<F32, kFull>(a.du, row * a.dus + a.width + c, have, dv);
+        if (a.a) store_eight<F32, kFull>(a.a, row * a.as + c, have, o);
+    });
     for (int d = lanes / 2; d > 0; d /= 2) sum += __shfl_xor(sum, d, 64);
     if (a.dgates && known && lane == 0) a.dgates[slot] = sum;
 }
 
-int lanes_for(int chunks, int least) {
+// Threads to a row of so many columns.
+int lanes_for(int width, int least) {
     int lanes = least;
-    while (lanes < chunks && lanes < 64) lanes *= 2;
+    while (8 * lanes < width && lanes < 64) lanes *= 2;
     return lanes;
-}
-
-bool vec8(const void *p, int64_t stride, int64_t es) {
-    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride * es % 16 == 0;
 }
 
 dim3 row_grid(int64_t rows, int lanes) { return dim3((unsigned)((rows + 256 / lanes - 1) / (256 / lanes))); }
 
 template <bool F32, bool GATED>
 hipError_t act_as(const ExpertActArgs &a, hipStream_t s) {
-    const int64_t es = F32 ? 4 : 2, U = GATED ? 2 * a.width : a.width;
-    const bool vec = a.width % 8 == 0 && vec8(a.u, a.us, es) && vec8(a.a, a.as, es);
-    const bool fused = a.codes && vec && a.width % 32 == 0 && reinterpret_cast<uintptr_t>(a.codes) % 8 == 0;
-    const int lanes = vec ? lanes_for(a.width / 8, 4) : lanes_for(a.width, 4);
+    const bool fused = a.codes && a.width % 32 == 0;
+    const int lanes = lanes_for(a.width, 4);
     const dim3 grid = row_grid(a.l.slots, lanes), block(256);
     if (fused)
         hipLaunchKernelGGL((k_act<F32, GATED, true, true>), grid, block, 0, s, a, lanes);
-    else if (vec)
+    else if (a.width % 8 == 0)
         hipLaunchKernelGGL((k_act<F32, GATED, true, false>), grid, block, 0, s, a, lanes);
     else
         hipLaunchKernelGGL((k_act<F32, GATED, false, false>), grid, block, 0, s, a, lanes);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || !a.codes || fused) return e;
-    // blocks of 32 that cross the halves, or rows off their alignment
+    // blocks of 32 that cross the halves, or are short
+    const int64_t U = GATED ? 2 * (int64_t)a.width : a.width;
     const KeepArgs k{a.u, a.l.slots, U, a.us, a.l.offsets + a.l.E, a.codes, a.exponents, a.key};
     return launch_keep8(k, F32, s);
 }
 
-template <bool F32, bool GATED>
+template <bool F32, bool GATED, bool EVEN>
 hipError_t act_backward_as(const ExpertActArgs &a, hipStream_t s) {
-    const int64_t es = F32 ? 4 : 2;
-    const bool vec = a.width % 8 == 0 && vec8(a.du, a.dus, es) && vec8(a.da, a.das, es) &&
-                     (!a.a || vec8(a.a, a.as, es)) &&
-                     (a.codes ? reinterpret_cast<uintptr_t>(a.codes) % 8 == 0 : vec8(a.u, a.us, es));
-    const int lanes = vec ? lanes_for(a.width / 8, 4) : lanes_for(a.width, 4);
+    const int lanes = lanes_for(a.width, 4);
     const dim3 grid = row_grid(a.l.slots, lanes), block(256);
-    if (a.codes && vec)
-        hipLaunchKernelGGL((k_act_backward<F32, GATED, true, true>), grid, block, 0, s, a, lanes);
-    else if (a.codes)
-        hipLaunchKernelGGL((k_act_backward<F32, GATED, false, true>), grid, block, 0, s, a, lanes);
-    else if (vec)
-        hipLaunchKernelGGL((k_act_backward<F32, GATED, true, false>), grid, block, 0, s, a, lanes);
+    if (a.codes)
+        hipLaunchKernelGGL((k_act_backward<F32, GATED, EVEN, true>), grid, block, 0, s, a, lanes);
     else
-        hipLaunchKernelGGL((k_act_backward<F32, GATED, false, false>), grid, block, 0, s, a, lanes);
+        hipLaunchKernelGGL((k_act_backward<F32, GATED, EVEN, false>), grid, block, 0, s, a, lanes);
     return hipGetLastError();
 }
-
 template <bool F32>
+hipError_t act_backward_of(const ExpertActArgs &a, hipStream_t s) {
+    const bool even = a.width % 8 == 0;
+    if (a.gated) return even ? act_backward_as<F32, true, true>(a, s) : act_backward_as<F32, true, false>(a, s);
+    return even ? act_backward_as<F32, false, true>(a, s) : act_backward_as<F32, false, false>(a, s);
+}
+
+template <bool F32, bool EVEN>
 hipError_t sum_as(const ExpertSumArgs &a, hipStream_t s) {
-    const int64_t es = F32 ? 4 : 2;
-    const bool vec = a.width % 8 == 0 && vec8(a.y, a.ys, es) && vec8(a.out, a.os, es) &&
-                     (!a.residual || vec8(a.residual, a.rs, es));
-    int lanes = vec ? lanes_for(a.width / 8, 1) : lanes_for(a.width, 1);
-    if (lanes == 64 && a.width > (vec ? 1024 : 128)) lanes = 256;
+    const int lanes = a.width > 1024 ? 256 : lanes_for(a.width, 1);
     const dim3 grid = row_grid(a.l.tokens, lanes), block(256);
-    if (a.residual && vec)
-        hipLaunchKernelGGL((k_expert_sum<F32, true, true>), grid, block, 0, s, a, lanes);
-    else if (a.residual)
-        hipLaunchKernelGGL((k_expert_sum<F32, true, false>), grid, block, 0, s, a, lanes);
-    else if (vec)
-        hipLaunchKernelGGL((k_expert_sum<F32, false, true>), grid, block, 0, s, a, lanes);
+    if (a.residual)
+        hipLaunchKernelGGL((k_expert_sum<F32, true, EVEN>), grid, block, 0, s, a, lanes);
     else
-        hipLaunchKernelGGL((k_expert_sum<F32, false, false>), grid, block, 0, s, a, lanes);
+        hipLaunchKernelGGL((k_expert_sum<F32, false, EVEN>), grid, block, 0, s, a, lanes);
     return hipGetLastError();
 }
 
@@ -388,7 +351,8 @@ hipError_t launch_expert_rows(const ExpertRowsArgs &a, hipStream_t s) {
 
 hipError_t launch_expert_sum(const ExpertSumArgs &a, int f32, hipStream_t s) {
     if (a.l.tokens == 0) return hipSuccess;
-    return f32 ? sum_as<true>(a, s) : sum_as<false>(a, s);
+    if (a.width % 8 == 0) return f32 ? sum_as<true, true>(a, s) : sum_as<false, true>(a, s);
+    return f32 ? sum_as<true, false>(a, s) : sum_as<false, false>(a, s);
 }
 
 hipError_t launch_expert_act(const ExpertActArgs &a, int f32, hipStream_t s) {
@@ -399,8 +363,7 @@ hipError_t launch_expert_act(const ExpertActArgs &a, int f32, hipStream_t s) {
 
 hipError_t launch_expert_act_backward(const ExpertActArgs &a, int f32, hipStream_t s) {
     if (a.l.slots == 0) return hipSuccess;
-    if (f32) return a.gated ? act_backward_as<true, true>(a, s) : act_backward_as<true, false>(a, s);
-    return a.gated ? act_backward_as<false, true>(a, s) : act_backward_as<false, false>(a, s);
+    return f32 ? act_backward_of<true>(a, s) : act_backward_of<false>(a, s);
 }
 
 }  // namespace dq

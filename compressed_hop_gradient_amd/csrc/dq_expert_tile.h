@@ -36,18 +36,18 @@ struct Tiling {
         return kThreads == 64 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     }
 };
-#ifndef FEWS
-#define FEWS 4
-#endif
 typedef Tiling<uint16_t, 256, 256, 2, 4, 64, 4> TileBig;
 typedef Tiling<uint16_t, 128, 128, 2, 2, 64, 4> TileMid;
 typedef Tiling<uint16_t, 64, 128, 2, 2, 64, 4> TileSmall;
-typedef Tiling<uint16_t, 16, 64, 1, 1, 64, FEWS> TileFew;      // a wave's
+typedef Tiling<uint16_t, 16, 64, 1, 1, 64, 4> TileFew;      // a wave's
 typedef Tiling<uint16_t, 128, 128, 2, 2, 128, 2> TileAny;
 typedef Tiling<float, 128, 128, 2, 2, 64, 4> TileMidF32;
 typedef Tiling<float, 64, 64, 2, 2, 64, 4> TileSmallF32;
-typedef Tiling<float, 16, 64, 1, 1, 64, FEWS> TileFewF32;
+typedef Tiling<float, 16, 64, 1, 1, 64, 4> TileFewF32;
 typedef Tiling<float, 64, 64, 2, 1, 128, 2> TileAnyF32;
+typedef Tiling<uint16_t, 16, 64, 1, 1, 128, 2> TileFewAny;
+typedef Tiling<float, 16, 64, 1, 1, 128, 2> TileFewAnyF32;
+typedef Tiling<uint16_t, 64, 64, 2, 2, 64, 4> TileNarrow;
 
 // How an operand is loaded: straight into LDS, where everything lies on 16 bytes; at any
 // alignment through registers; from 8-bit codes, decoded in registers.
@@ -237,12 +237,14 @@ struct Along {
     typedef typename C::T T;
     static constexpr int kRowChunks = C::kRow / 16, kPer = ROWS * kRowChunks / C::kThreads, BK = C::BK;
     static constexpr bool kAsyncLoad = L == kAsync;
-    static_assert(ROWS * kRowChunks % C::kThreads == 0 && C::kThreads % (16 * kRowChunks) == 0, "whole chunks");
+    static_assert(ROWS * kRowChunks % C::kThreads == 0 && C::kThreads % (8 * kRowChunks) == 0, "whole chunks");
     struct Entries {};
     Stream from;                       // kAsync
     uint32_t off[kAsyncLoad ? kPer : 1];
     const T *p[kAsyncLoad ? 1 : kPer];  // else
-    u32x4 v[kAsyncLoad ? 1 : kPer];
+    struct Regs {
+        u32x4 v[kAsyncLoad ? 1 : kPer];
+    };
     int K, kc;
 
     static __device__ __forceinline__ int swap(int chunk, int row) {
@@ -265,7 +267,7 @@ struct Along {
         }
     }
     __device__ __forceinline__ void ahead(int, Entries &) const {}
-    __device__ __forceinline__ void issue(char *buf, int k0, const Entries &) {
+    __device__ __forceinline__ void issue(char *buf, int k0, const Entries &, Regs &r) {
         const int have = K - k0 - kc;
 #pragma unroll
         for (int i = 0; i < kPer; i++) {
@@ -273,14 +275,14 @@ struct Along {
                 from.to_lds((int64_t)k0 * sizeof(T), have > 0 ? off[i] : kNowhere,
                             buf + (64 * C::wave() + i * C::kThreads) * 16);
             else
-                v[i] = load_some(p[i] + k0, p[i] ? have : 0);
+                r.v[i] = load_some(p[i] + k0, p[i] ? have : 0);
         }
     }
-    __device__ __forceinline__ void commit(char *buf) {
+    __device__ __forceinline__ void commit(char *buf, const Regs &r) {
         if constexpr (!kAsyncLoad)
 #pragma unroll
             for (int i = 0; i < kPer; i++)
-                *reinterpret_cast<u32x4 *>(buf + (C::tid() + i * C::kThreads) * 16) = v[i];
+                *reinterpret_cast<u32x4 *>(buf + (C::tid() + i * C::kThreads) * 16) = r.v[i];
     }
     // rows row0 .. row0 + 15, half h of the step: lane l has row l & 15, chunk (l >> 4) + 4 h
     static __device__ __forceinline__ u32x4 frag(const char *buf, int row0, int h) {
@@ -314,8 +316,10 @@ struct Across {
         uint32_t at[GATHER || !kAsyncLoad ? kPer : 1][kShared];
     };
     int K, N, col0;
-    u32x4 v[L == kAsync ? 1 : kPer];
-    uint8_t ex[kFromKept ? kPer : 1];
+    struct Regs {
+        u32x4 v[L == kAsync ? 1 : kPer];
+        uint8_t ex[kFromKept ? kPer : 1];
+    };
 
     static __device__ __forceinline__ int swap(int k) {
         if constexpr (C::kF32) return k >> 2 & 3;
@@ -366,7 +370,7 @@ struct Across {
             v ^= (e.at[i][j - 1] ^ e.at[i][j]) & -(uint32_t)((threadIdx.x & 63) / kPerRow >= j);
         return v;
     }
-    __device__ __forceinline__ void issue(char *buf, int k0, const Entries &e) {
+    __device__ __forceinline__ void issue(char *buf, int k0, const Entries &e, Regs &r) {
 #pragma unroll
         for (int i = 0; i < kPer; i++) {
             const int col = piece_col(i);
@@ -383,32 +387,32 @@ struct Across {
             const int64_t off = rows.offset(e.at[i][0]);
             const bool there = off >= 0 && col < N && k0 + piece_row(i) < K;
             if constexpr (L == kAny) {
-                v[i] = load_some(base + off + col, there ? N - col : 0);
+                r.v[i] = load_some(base + off + col, there ? N - col : 0);
             } else if constexpr (kFromKept) {
-                v[i] = u32x4{0, 0, 0, 0};
-                ex[i] = 127;
+                r.v[i] = u32x4{0, 0, 0, 0};
+                r.ex[i] = 127;
                 if (there) {
-                    ex[i] = exponents[off * ((N + 31) / 32) + col / 32];
+                    r.ex[i] = exponents[off * ((N + 31) / 32) + col / 32];
                     const int8_t *c = codes + off * N + col;
-                    v[i] = load_some(c, N - col);
+                    r.v[i] = load_some(c, N - col);
                 }
             }
         }
     }
-    __device__ __forceinline__ void commit(char *buf) {
+    __device__ __forceinline__ void commit(char *buf, const Regs &r) {
         if constexpr (L == kAny) {
 #pragma unroll
             for (int i = 0; i < kPer; i++)
-                *reinterpret_cast<u32x4 *>(buf + (C::tid() + i * C::kThreads) * 16) = v[i];
+                *reinterpret_cast<u32x4 *>(buf + (C::tid() + i * C::kThreads) * 16) = r.v[i];
         } else if constexpr (kFromKept) {
 #pragma unroll
             for (int i = 0; i < kPer; i++) {
                 const int k = piece_row(i), unit = (C::tid() + i * C::kThreads) % kPerRow;
                 u32x4 *to = reinterpret_cast<u32x4 *>(buf + k * kRow + (unit ^ swap(k)) * 16 * sizeof(T));
-                const float scale = __uint_as_float((uint32_t)ex[i] << 23);
+                const float scale = __uint_as_float((uint32_t)r.ex[i] << 23);
                 float f[16];
 #pragma unroll
-                for (int j = 0; j < 16; j++) f[j] = (float)(int8_t)(v[i][j / 4] >> 8 * (j & 3)) * scale;
+                for (int j = 0; j < 16; j++) f[j] = (float)(int8_t)(r.v[i][j / 4] >> 8 * (j & 3)) * scale;
                 if constexpr (C::kF32) {
 #pragma unroll
                     for (int j = 0; j < 4; j++)
@@ -457,16 +461,22 @@ struct Across {
 
 __device__ __forceinline__ void store_one(float *p, float v) { *p = v; }
 __device__ __forceinline__ void store_one(uint16_t *p, float v) { *p = (uint16_t)bf16_bits(v); }
-__device__ __forceinline__ void store_four(float *p, f32x4 v) { *reinterpret_cast<f32x4 *>(p) = v; }
+// at any alignment of the element
+__device__ __forceinline__ void store_four(float *p, f32x4 v) { __builtin_memcpy(p, &v, 16); }
 __device__ __forceinline__ void store_four(uint16_t *p, f32x4 v) {
-    *reinterpret_cast<uint2 *>(p) =
-        make_uint2(bf16_bits(v[0]) | bf16_bits(v[1]) << 16, bf16_bits(v[2]) | bf16_bits(v[3]) << 16);
+    const uint2 w = make_uint2(bf16_bits(v[0]) | bf16_bits(v[1]) << 16, bf16_bits(v[2]) | bf16_bits(v[3]) << 16);
+    __builtin_memcpy(p, &w, 8);
 }
-
-// Whether four neighbouring outputs can be stored together.
+// columns n .. n + 3 of a row of N
 template <typename Out>
-__device__ __forceinline__ bool vec_out(const void *p, int64_t stride, int n) {
-    return reinterpret_cast<uintptr_t>(p) % (4 * sizeof(Out)) == 0 && stride % 4 == 0 && n % 4 == 0;
+__device__ __forceinline__ void store_columns(Out *row, int n, int N, f32x4 v) {
+    if (n + 4 <= N) {
+        store_four(row + n, v);
+    } else {
+#pragma unroll
+        for (int q = 0; q < 3; q++)
+            if (n + q < N) store_one(row + n + q, v[q]);
+    }
 }
 
 // fp32 accumulators of a wave.  The products are taken turned (B first), so that a
@@ -518,27 +528,19 @@ struct Acc {
         for (int i = 0; i < C::TM; i++)
 #pragma unroll
             for (int j = 0; j < C::TN; j++)
-                store_four(to + (m0() + 16 * i + (lane & 15)) * C::BN + n0() + 16 * j + (lane >> 4) * 4, v[i][j]);
+                *reinterpret_cast<f32x4 *>(to + (m0() + 16 * i + (lane & 15)) * C::BN + n0() + 16 * j +
+                                           (lane >> 4) * 4) = v[i][j];
     }
     // row(m): where the tile's row m goes, NULL: nowhere
     template <class Row>
-    __device__ __forceinline__ void store(Row row, int col0, int N, bool four) const {
+    __device__ __forceinline__ void store(Row row, int col0, int N) const {
         const int lane = threadIdx.x & 63;
 #pragma unroll
         for (int i = 0; i < C::TM; i++) {
             auto *p = row(m0() + 16 * i + (lane & 15));
             if (!p) continue;
 #pragma unroll
-            for (int j = 0; j < C::TN; j++) {
-                const int n = col0 + n0() + 16 * j + (lane >> 4) * 4;
-                if (four && n < N) {
-                    store_four(p + n, v[i][j]);
-                } else {
-#pragma unroll
-                    for (int q = 0; q < 4; q++)
-                        if (n + q < N) store_one(p + n + q, v[i][j][q]);
-                }
-            }
+            for (int j = 0; j < C::TN; j++) store_columns(p, col0 + n0() + 16 * j + (lane >> 4) * 4, N, v[i][j]);
         }
     }
 };
@@ -560,48 +562,59 @@ __device__ __forceinline__ void all_waves() {
 // Step k0 into LDS: by loads that land there, or from registers, whose next step is then
 // loaded.  Past the end zeros are stored.
 template <class Op>
-__device__ __forceinline__ void fill(Op &op, char *buf, int k0, typename Op::Entries &e) {
+__device__ __forceinline__ void fill(Op &op, char *buf, int k0, typename Op::Entries &e, typename Op::Regs &r) {
     if constexpr (Op::kAsyncLoad) {
-        op.issue(buf, k0, e);
+        op.issue(buf, k0, e, r);
         op.ahead(k0 + Op::BK, e);
     } else {
-        op.commit(buf);
-        op.issue(nullptr, k0 + Op::BK, e);
+        op.commit(buf, r);
+        op.issue(nullptr, k0 + Op::BK, e, r);
         op.ahead(k0 + 2 * Op::BK, e);
     }
 }
 
-// acc += A B over `inner`.  Two steps in LDS; the barrier stands in the middle of a
-// step's products, when the step after it has landed and the second half's operands are
-// in registers: LDS reads run beside the other half's products, loads beside a
-// whole step's.
+// acc += A B over `inner`, an operand at least through registers.  Two steps in LDS; the
+// barrier stands in the middle of a step's products, when the step after it is in LDS and
+// the second half's operands are in registers: LDS reads run beside the other half's
+// products, loads beside a whole step's.
 template <class C, class A, class B>
 __device__ __forceinline__ void multiply_halves(char *lds, A &a, B &b, int inner, Acc<C> &acc) {
     constexpr int kStep = C::kBytesA + C::kBytesB;
-    constexpr bool kBothAsync = A::kAsyncLoad && B::kAsyncLoad;
     if (inner <= 0) return;
     const int steps = (inner + C::BK - 1) / C::BK;
-    typename A::Entries ea[2];
-    typename B::Entries eb[2];
-#pragma unroll
-    for (int i = 0; i < 2; i++) {
-        a.ahead(i * C::BK, ea[i]);
-        b.ahead(i * C::BK, eb[i]);
+    typename A::Entries ea;
+    typename B::Entries eb;
+    typename A::Regs ra;
+    typename B::Regs rb;
+    {
+        typename A::Entries ea1;
+        typename B::Entries eb1;
+        typename A::Regs ra1;
+        typename B::Regs rb1;
+        a.ahead(0, ea);
+        b.ahead(0, eb);
+        a.ahead(C::BK, ea1);
+        b.ahead(C::BK, eb1);
+        a.issue(lds, 0, ea, ra);
+        b.issue(lds + C::kBytesA, 0, eb, rb);
+        a.issue(lds + kStep, C::BK, ea1, ra1);
+        b.issue(lds + kStep + C::kBytesA, C::BK, eb1, rb1);
+        a.ahead(2 * C::BK, ea);
+        b.ahead(2 * C::BK, eb);
+        a.commit(lds, ra);
+        b.commit(lds + C::kBytesA, rb);
+        a.commit(lds + kStep, ra1);
+        b.commit(lds + kStep + C::kBytesA, rb1);
     }
-#pragma unroll
-    for (int i = 0; i < 2; i++) {
-        a.issue(lds + i * kStep, i * C::BK, ea[i]);
-        b.issue(lds + i * kStep + C::kBytesA, i * C::BK, eb[i]);
-        a.commit(lds + i * kStep);
-        b.commit(lds + i * kStep + C::kBytesA);
+    if constexpr (!A::kAsyncLoad) {
+        a.issue(nullptr, 2 * C::BK, ea, ra);
+        a.ahead(3 * C::BK, ea);
     }
-    all_waves<C, kBothAsync ? A::kPer + B::kPer : 0>();
-    a.ahead(2 * C::BK, ea[0]);
-    b.ahead(2 * C::BK, eb[0]);
-    if (!A::kAsyncLoad) a.issue(nullptr, 2 * C::BK, ea[0]);
-    if (!B::kAsyncLoad) b.issue(nullptr, 2 * C::BK, eb[0]);
-    if (!A::kAsyncLoad) a.ahead(3 * C::BK, ea[0]);
-    if (!B::kAsyncLoad) b.ahead(3 * C::BK, eb[0]);
+    if constexpr (!B::kAsyncLoad) {
+        b.issue(nullptr, 2 * C::BK, eb, rb);
+        b.ahead(3 * C::BK, eb);
+    }
+    all_waves<C, 0>();
     typename Acc<C>::Half first, second;
     first.template read<A, B>(lds, 0);
     for (int t = 0; t < steps; t++) {
@@ -614,8 +627,8 @@ __device__ __forceinline__ void multiply_halves(char *lds, A &a, B &b, int inner
         if (t + 1 < steps) {
             first.template read<A, B>(next, 0);
             const int k = (t + 2) * C::BK;
-            fill(a, now, k, ea[0]);
-            fill(b, now + C::kBytesA, k, eb[0]);
+            fill(a, now, k, ea, ra);
+            fill(b, now + C::kBytesA, k, eb, rb);
         }
         acc.add(second);
         __builtin_amdgcn_sched_barrier(0);
@@ -632,6 +645,8 @@ __device__ __forceinline__ void multiply_stages(char *lds, A &a, B &b, int inner
     static_assert(C::kRow == 64 && S >= 3, "a step is one matrix instruction deep");
     if (inner <= 0) return;
     const int steps = (inner + C::BK - 1) / C::BK;
+    typename A::Regs ra;                                 // unused
+    typename B::Regs rb;
     {
         typename A::Entries ea[S];
         typename B::Entries eb[S];
@@ -642,8 +657,8 @@ __device__ __forceinline__ void multiply_stages(char *lds, A &a, B &b, int inner
         }
 #pragma unroll
         for (int i = 0; i < S; i++) {
-            a.issue(lds + i * kStep, i * C::BK, ea[i]);
-            b.issue(lds + i * kStep + C::kBytesA, i * C::BK, eb[i]);
+            a.issue(lds + i * kStep, i * C::BK, ea[i], ra);
+            b.issue(lds + i * kStep + C::kBytesA, i * C::BK, eb[i], rb);
         }
     }
     constexpr int kLoads = A::kPer + B::kPer;
@@ -658,8 +673,8 @@ __device__ __forceinline__ void multiply_stages(char *lds, A &a, B &b, int inner
     b.ahead(S * C::BK, eb);
     const auto step = [&](int t, typename Acc<C>::Half &now, typename Acc<C>::Half &next) {
         const int k = (t + S) * C::BK;
-        a.issue(lds + at, k, ea);
-        b.issue(lds + at + C::kBytesA, k, eb);
+        a.issue(lds + at, k, ea, ra);
+        b.issue(lds + at + C::kBytesA, k, eb, rb);
         a.ahead(k + C::BK, ea);
         b.ahead(k + C::BK, eb);
         at = at + kStep == S * kStep ? 0 : at + kStep;

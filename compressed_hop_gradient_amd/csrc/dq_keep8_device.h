@@ -76,6 +76,30 @@ __device__ __forceinline__ uint32_t max_of_four(uint32_t m) {
 
 __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
 
+// `have` of eight codes, to or from any address.
+template <bool FULL>
+__device__ __forceinline__ void store_codes(int8_t *p, int have, uint2 c) {
+    if constexpr (FULL) {
+        __builtin_memcpy(p, &c, 8);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; j++)
+            if (j < have) p[j] = (int8_t)((j < 4 ? c.x : c.y) >> 8 * (j & 3));
+    }
+}
+template <bool FULL>
+__device__ __forceinline__ uint2 load_codes(const int8_t *p, int have) {
+    uint2 c = make_uint2(0, 0);
+    if constexpr (FULL) {
+        __builtin_memcpy(&c, p, 8);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; j++)
+            if (j < have) (j < 4 ? c.x : c.y) |= (uint32_t)(uint8_t)p[j] << 8 * (j & 3);
+    }
+    return c;
+}
+
 // Eight neighbouring elements of a block that four neighbouring lanes hold together:
 // their codes as two words, and the block's exponent.
 __device__ __forceinline__ uint2 keep_eight(const float x[8], const uint32_t w[4], uint32_t &exponent) {

@@ -2,6 +2,8 @@
 // training-step kernels (device code).
 #pragma once
 
+#include <type_traits>
+
 #include "dq_train.h"
 
 namespace dq {
@@ -73,6 +75,52 @@ __device__ __forceinline__ void load8(const void *p, int64_t at, float v[8]) {
             v[2 * j] = __uint_as_float(a[j] << 16);
             v[2 * j + 1] = __uint_as_float(a[j] & 0xFFFF0000u);
         }
+    }
+}
+
+// The same at any alignment of the elements (the hardware splits such accesses); FULL:
+// all eight are there, else `have` of them, the others read as 0 and are not written.  A
+// branch on it stands around all accesses of an eight, not at each: where branches join,
+// loads are waited for.
+template <bool F32, bool FULL>
+__device__ __forceinline__ void load_eight(const void *p, int64_t at, int have, float v[8]) {
+    typedef typename Elem<F32>::type T;
+    const T *q = static_cast<const T *>(p) + at;
+    if constexpr (FULL) {
+        T w[8];
+        __builtin_memcpy(w, q, sizeof(w));
+#pragma unroll
+        for (int j = 0; j < 8; j++) v[j] = Elem<F32>::up(w[j]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; j++) v[j] = j < have ? Elem<F32>::up(q[j]) : 0.0f;
+    }
+}
+template <bool F32, bool FULL>
+__device__ __forceinline__ void store_eight(void *p, int64_t at, int have, const float v[8]) {
+    typedef typename Elem<F32>::type T;
+    T *q = static_cast<T *>(p) + at;
+    if constexpr (FULL) {
+        T w[8];
+#pragma unroll
+        for (int j = 0; j < 8; j++) w[j] = Elem<F32>::down(v[j]);
+        __builtin_memcpy(q, w, sizeof(w));
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; j++)
+            if (j < have) q[j] = Elem<F32>::down(v[j]);
+    }
+}
+
+// body(full, c) for the eights from column `first`, `step` columns apart, of rows of
+// `width`; EVEN: of whole eights.
+template <bool EVEN, class Body>
+__device__ __forceinline__ void by_eights(int first, int step, int width, Body body) {
+    for (int c = first; c < width; c += step) {
+        if (EVEN || c + 8 <= width)
+            body(std::true_type(), c);
+        else
+            body(std::false_type(), c);
     }
 }
 
