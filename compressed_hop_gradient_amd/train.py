@@ -1,5 +1,6 @@
 """Autograd forms of the training-step operators: dropout from the
-counter-based generator, and the expert router with its balance loss.
+counter-based generator, the expert router with its balance loss, and the
+experts that it chooses.
 
 A data-parallel step computes these per worker before its gradients go through
 a round (``dq.Plan.allreduce``, or ``ddp_hook`` in DDP).  ``rnd`` is the round
@@ -113,3 +114,67 @@ def route(logits, top_k, renorm=True, masks=None, reduce=None):
     loss, *gates = _Route.apply(top_k, renorm, ms, reduce, found, *ls)
     ids, counts, coef = found
     return Routing(ids[0] if one else ids, gates[0] if one else gates, loss, counts, coef)
+
+
+class _Experts(torch.autograd.Function):
+    """The experts of one worker's tokens; see ``experts``."""
+
+    @staticmethod
+    def forward(ctx, x, gates, w_in, w_out, ids, act, keep, key):
+        rows = dq.expert_rows(ids, w_in.size(0))
+        x, gates = _by_rows(x), gates.contiguous()
+        u = dq.expert_matmul(x, w_in, rows, gather=True)
+        kept = [x, u]
+        if keep:
+            # two draws: the rows of u take the site after the tokens'
+            kept[0] = dq.keep8(x, **key)
+            a, kept[1] = dq.expert_act(u, gates, rows, act, keep=True, **{**key, "site": key["site"] + 1})
+        else:
+            a = dq.expert_act(u, gates, rows, act)
+        y = dq.expert_sum(dq.expert_matmul(a, w_out, rows), rows)
+        ctx.act, ctx.dtype = act, x.dtype
+        saved = [t for k in kept for t in ((k.codes, k.exponents) if keep else (k,))]
+        ctx.save_for_backward(gates, w_in, w_out, rows.offsets, rows.source, rows.row, *saved)
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        gates, w_in, w_out, offsets, source, row, *saved = ctx.saved_tensors
+        need_x, need_gates, need_in, need_out = ctx.needs_input_grad[:4]
+        rows = dq.ExpertRows(offsets, source, row)
+        x, u = saved if len(saved) == 2 else (dq.Kept8(*saved[:2], ctx.dtype), dq.Kept8(*saved[2:], ctx.dtype))
+        dy = _by_rows(dy)
+        dx = dw_in = dw_out = None
+        da = dq.expert_matmul(dy, w_out.transpose(1, 2), rows, gather=True)
+        du, dgates, a = dq.expert_act_backward(u, da, gates, rows, ctx.act, again=need_out)
+        if need_out:
+            dw_out = dq.expert_matmul_grad(a, dy, rows, gather="dout")
+        if need_in:
+            dw_in = dq.expert_matmul_grad(x, du, rows, gather="x")
+        if need_x:
+            dx = dq.expert_sum(dq.expert_matmul(du, w_in.transpose(1, 2), rows), rows)
+        return dx, dgates if need_gates else None, dw_in, dw_out, None, None, None, None
+
+
+def experts(x, ids, gates, w_in, w_out, act="swiglu", keep=False, dither=True, seed=1, rnd=0, worker=0, site=0):
+    """What the chosen experts make of one worker's tokens: ``sum_j gates[t, j]
+    act(x[t] @ w_in[e]) @ w_out[e]`` over the choices e = ``ids[t, j]``, [tokens, hidden];
+    zeros for a token without any.  Differentiable by ``x``, ``gates`` and both weights.
+
+    ``ids`` and ``gates`` are one worker's of :func:`route`; ``x`` is [tokens, hidden],
+    ``w_in`` [experts, hidden, columns] and ``w_out`` [experts, width, hidden], all bf16 or all
+    fp32; with ``act="swiglu"`` columns = 2 width (gate half first), with ``"relu"``
+    columns = width.  The tokens are gathered as they are read, products and sums
+    are fp32 inside, and what goes between the steps is rounded to the dtype.
+
+    With ``keep`` the backward pass works from ``x`` and ``x @ w_in`` in 8 bits (a half or
+    a quarter of the memory), kept as ``dq.keep8`` does with these numbers: ``x`` at
+    ``site``, the rows at ``site + 1`` (below 2^31), so the next call in a model takes ``site + 2``.
+    ``rnd`` is the round index of the step, an int.  Given the gradient by ``x @ w_in``, that by
+    ``w_in`` is then right in the mean; the activation's gradient and ``w_out``'s are taken
+    at the kept values, off by their rounding (a 64th to a 127th of a block's largest)."""
+    if keep and not 0 <= site < (1 << 31) - 1:
+        raise ValueError(f"site {site}: site and site + 1 must be below 2^31")
+    key = dict(dither=dither, seed=seed, rnd=rnd, worker=worker, site=site)
+    return _Experts.apply(x, gates, w_in, w_out, ids, act, keep, key)

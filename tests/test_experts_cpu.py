@@ -1,0 +1,317 @@
+"""The experts' operators without a GPU: the plain forms that the GPU tests
+compare with (gradients against differences, dithers against the kernels'
+documented counter), and the argument checks of the C ABI and the binding."""
+import ctypes as C
+
+import numpy as np
+import pytest
+import torch
+
+import experts_ref as ref
+import train_ref
+from compressed_hop_gradient_amd import dq, train
+
+FAKE = 1 << 20      # never dereferenced: every call below fails its checks first, or has nothing to do
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return dq.lib()
+
+
+# ---- the plain forms -------------------------------------------------------------
+
+def test_rows_are_a_stable_sort():
+    ids = np.array([[2, 0], [-1, 2], [1, 5], [0, 0]])
+    r = ref.Rows(ids, 3)
+    assert r.offsets.tolist() == [0, 3, 4, 6] and r.source.tolist() == [1, 6, 7, 4, 0, 3, 2, 5]
+    assert r.row.tolist() == [[4, 0], [-1, 5], [3, -1], [1, 2]]
+
+
+def test_dithers_are_apart_from_dropouts():
+    """The counter is dropout's with bit 15 of its second word: element i + 2^50 of
+    a dropout under the same numbers, which no memory holds."""
+    key = dict(seed=0x123456789ABCDEF0, rnd=7, worker=3, site=2)
+    assert ref.dithers(40, **key).tolist() == train_ref.dithers(40, first=1 << 50, **key).tolist()
+    assert ref.dithers(40, **key).tolist() != train_ref.dithers(40, **key).tolist()
+
+
+@pytest.mark.parametrize("dither", [False, True])
+def test_kept_values_are_near(dither):
+    rng = np.random.default_rng(0)
+    x = rng.normal(size=(5, 70)) * np.exp(3 * rng.normal(size=(5, 70)))
+    codes, exps, values = ref.keep(x, ref.dithers(350) if dither else 32768)
+    step = np.repeat(2.0 ** (exps - 127), 32, 1)[:, :70]
+    assert np.abs(codes).max() <= 127 and (np.abs(values - x) <= (1 if dither else 0.5) * step * (1 + 2 ** -15)).all()
+    # the smallest power of two that fits
+    for b in range(3):
+        m = np.abs(x[:, 32 * b:32 * b + 32]).max(1)
+        assert (m <= 127 * 2.0 ** (exps[:, b] - 127)).all() and (m > 127 * 2.0 ** (exps[:, b] - 128)).all()
+
+
+@pytest.mark.parametrize("kind", ["swiglu", "relu"])
+def test_reference_gradient_against_differences(kind):
+    """Every input of an experts' layer, by central differences: h^2 f''' / 6 and 2^-53 /
+    h, below 1e-8 here."""
+    rng = np.random.default_rng(1)
+    T, k, E, H, F = 5, 2, 3, 4, 3
+    ids = np.array([[0, 2], [1, -1], [-1, -1], [2, 2], [1, 0]])
+    rows = ref.Rows(ids, E)
+    x, gates, dy = rng.normal(size=(T, H)), rng.uniform(size=(T, k)), rng.normal(size=(T, H))
+    w_in, w_out = rng.normal(size=(E, H, F * (2 if kind == "swiglu" else 1))), rng.normal(size=(E, F, H))
+    gate_of = lambda g: g.reshape(-1)[rows.source[:rows.n]]
+
+    def value(x, gates, w_in, w_out):
+        u = ref.matmul(x, w_in, rows, gather=True)[0]
+        y = ref.matmul(ref.act(u, gate_of(gates), kind), w_out, rows)[0]
+        return (ref.back(y, rows)[0] * dy).sum()
+
+    args = [x, gates, w_in, w_out]
+    u = ref.matmul(x, w_in, rows, gather=True)[0]
+    da = ref.matmul(dy, w_out.transpose(0, 2, 1), rows, gather=True)[0]
+    (du, dgate, a), _ = ref.act_backward(u, da, gate_of(gates), kind)
+    dgates = np.zeros(T * k)
+    dgates[rows.source[:rows.n]] = dgate
+    grads = [ref.back(ref.matmul(du, w_in.transpose(0, 2, 1), rows)[0], rows)[0], dgates.reshape(T, k),
+             ref.matmul_grad(x, du, rows, "x")[0], ref.matmul_grad(a, dy, rows, "dout")[0]]
+    h = 1e-5
+    for n, (arg, grad) in enumerate(zip(args, grads)):
+        for i in np.ndindex(arg.shape):
+            up, down = [a.copy() for a in args], [a.copy() for a in args]
+            up[n][i] += h
+            down[n][i] -= h
+            assert abs((value(*up) - value(*down)) / (2 * h) - grad[i]) < 1e-7, (n, i)
+
+
+# ---- refusals of the C ABI ---------------------------------------------------------
+
+# Buffers of 1 MB of addresses each.  8 tokens, 2 choices, 4 experts: 16 slots.
+
+def _lists(offsets=1 * FAKE, source=2 * FAKE, row=3 * FAKE, tokens=8, k=2, E=4):
+    return C.byref(dq.dq_expert_lists(offsets, source, row, tokens, k, E))
+
+
+def _lists_of(args):
+    return _lists(**{n: args.pop(n) for n in ("offsets", "source", "row", "tokens", "k", "E") if n in args})
+
+
+def _rows(lib, ids=1 * FAKE, tokens=8, k=2, E=4, offsets=2 * FAKE, source=3 * FAKE, row=4 * FAKE, work=5 * FAKE,
+          size=FAKE):
+    return lib.dq_expert_rows(ids, tokens, k, E, offsets, source, row, work, size, None)
+
+
+def _matmul(lib, **a):
+    l = _lists_of(a)
+    d = dict(x=4 * FAKE, xs=32, flags=0, w=5 * FAKE, we=32 * 16, ws=16, y=6 * FAKE, ys=16, kind=dq.BF16, inner=32,
+             outer=16)
+    assert set(a) <= set(d), a
+    return lib.dq_expert_matmul(l, *{**d, **a}.values(), None)
+
+
+def _grad(lib, **a):
+    l = _lists_of(a)
+    d = dict(x=4 * FAKE, xs=32, codes=None, exponents=None, dy=5 * FAKE, dys=16, gather=0, dw=6 * FAKE, kind=dq.BF16,
+             out=dq.BF16, inner=32, outer=16, work=7 * FAKE, size=FAKE)
+    assert set(a) <= set(d), a
+    return lib.dq_expert_matmul_grad(l, *{**d, **a}.values(), None)
+
+
+def _sum(lib, **a):
+    l = _lists_of(a)
+    d = dict(y=4 * FAKE, ys=16, residual=5 * FAKE, rs=16, out=6 * FAKE, os=16, kind=dq.F32, width=16)
+    assert set(a) <= set(d), a
+    return lib.dq_expert_sum(l, *{**d, **a}.values(), None)
+
+
+def _key(**a):
+    d = dict(seed=1, d_round=None, round=0, worker=0, site=0, flags=1)
+    return C.byref(dq.dq_keep_key(*{**d, **a}.values()))
+
+
+KEYS = [dict(d_round=FAKE + 2), dict(worker=-1), dict(worker=65536), dict(site=1 << 31), dict(flags=2)]
+
+
+def _keep(lib, x=1 * FAKE, kind=dq.BF16, rows=4, cols=40, xs=40, codes=2 * FAKE, exponents=3 * FAKE, key=None):
+    return lib.dq_keep8(x, kind, rows, cols, xs, codes, exponents, key or _key(), None)
+
+
+def _restore(lib, codes=1 * FAKE, exponents=2 * FAKE, kind=dq.BF16, rows=4, cols=40, y=3 * FAKE, ys=40):
+    return lib.dq_restore8(codes, exponents, kind, rows, cols, y, ys, None)
+
+
+def _act(lib, **a):
+    l = _lists_of(a)
+    d = dict(act=0, u=4 * FAKE, us=32, gates=5 * FAKE, a=6 * FAKE, as_=16, kind=dq.BF16, width=16, codes=7 * FAKE,
+             exponents=8 * FAKE, key=_key())
+    assert set(a) <= set(d), a
+    return lib.dq_expert_act(l, *{**d, **a}.values(), None)
+
+
+def _back(lib, **a):
+    l = _lists_of(a)
+    d = dict(act=0, u=4 * FAKE, us=32, codes=None, exponents=None, da=5 * FAKE, das=16, gates=6 * FAKE, du=7 * FAKE,
+             dus=32, again=8 * FAKE, as_=16, dgates=9 * FAKE, kind=dq.BF16, width=16)
+    assert set(a) <= set(d), a
+    return lib.dq_expert_act_backward(l, *{**d, **a}.values(), None)
+
+
+LISTS = [dict(tokens=-1), dict(tokens=1 << 30), dict(k=0), dict(k=17), dict(E=0), dict(E=1025), dict(offsets=FAKE + 2),
+         dict(source=2 * FAKE + 1), dict(row=3 * FAKE + 2)]
+
+
+@pytest.mark.parametrize("call", [_matmul, _grad, _sum, _act, _back])
+def test_every_call_checks_its_lists(lib, call):
+    for bad in LISTS:
+        assert call(lib, **bad) == dq.DQ_EINVAL, bad
+    for name in ("offsets", "source", "row"):
+        assert call(lib, **{name: None}) == dq.DQ_ENULL, name
+
+
+def test_rows_refuses(lib):
+    for bad in (dict(tokens=-1), dict(tokens=1 << 30), dict(k=0), dict(k=17), dict(E=0), dict(E=1025), dict(ids=FAKE + 1),
+                dict(offsets=2 * FAKE + 2), dict(source=3 * FAKE + 2), dict(row=4 * FAKE + 1), dict(offsets=FAKE + 60),
+                dict(source=4 * FAKE), dict(row=2 * FAKE + 16), dict(row=5 * FAKE), dict(ids=3 * FAKE)):
+        assert _rows(lib, **bad) == dq.DQ_EINVAL, bad
+    for bad in (dict(ids=None), dict(offsets=None), dict(source=None), dict(row=None)):
+        assert _rows(lib, **bad) == dq.DQ_ENULL, bad
+    for bad in (dict(work=None), dict(work=5 * FAKE + 128), dict(size=255), dict(tokens=100000, size=1024)):
+        assert _rows(lib, **bad) == dq.DQ_EWORKSPACE, bad
+    assert lib.dq_expert_rows_bytes(8, 2, 4) == 256 and lib.dq_expert_rows_bytes(1 << 30, 2, 4) == 0
+    assert lib.dq_expert_rows_bytes(8, 0, 4) == 0 and lib.dq_expert_rows_bytes(8, 2, 1025) == 0
+
+
+@pytest.mark.parametrize("bad", [
+    dict(kind=2), dict(flags=4), dict(inner=0), dict(outer=0), dict(inner=(1 << 24) + 1), dict(xs=-1), dict(ws=-1),
+    dict(we=-1), dict(ys=15), dict(xs=1 << 41), dict(x=4 * FAKE + 1), dict(w=5 * FAKE + 1), dict(y=6 * FAKE + 1),
+    # y over x (whole, or the tokens alone), w, the lists
+    dict(y=4 * FAKE + 1022), dict(y=4 * FAKE + 510, flags=1), dict(y=5 * FAKE + 4 * 512 * 2 - 2),
+    dict(y=5 * FAKE + 4 * 512 * 2 - 2, flags=2, ws=32), dict(y=FAKE), dict(y=2 * FAKE + 62), dict(y=3 * FAKE)])
+def test_matmul_refuses(lib, bad):
+    assert _matmul(lib, **bad) == dq.DQ_EINVAL
+
+
+def test_matmul_null_and_empty(lib):
+    for name in ("x", "w", "y"):
+        assert _matmul(lib, **{name: None}) == dq.DQ_ENULL
+    assert _matmul(lib, tokens=0, source=None, row=None, x=None, y=None) == dq.DQ_OK
+
+
+@pytest.mark.parametrize("bad", [
+    dict(kind=2), dict(out=2), dict(kind=dq.F32, out=dq.BF16), dict(gather=-1), dict(gather=3), dict(inner=0), dict(outer=0),
+    dict(xs=-1), dict(dys=1 << 41), dict(x=4 * FAKE + 1), dict(dy=5 * FAKE + 1), dict(dw=6 * FAKE + 1),
+    dict(out=dq.F32, dw=6 * FAKE + 2), dict(codes=8 * FAKE, exponents=9 * FAKE),
+    dict(dw=4 * FAKE + 1022), dict(dw=5 * FAKE), dict(dw=5 * FAKE - 4094), dict(dw=FAKE), dict(dw=7 * FAKE),
+    dict(work=4 * FAKE), dict(x=None, codes=8 * FAKE, exponents=9 * FAKE, dw=8 * FAKE),
+    dict(x=None, codes=8 * FAKE, exponents=9 * FAKE, dw=9 * FAKE + 14)])
+def test_matmul_grad_refuses(lib, bad):
+    assert _grad(lib, **bad) == dq.DQ_EINVAL
+
+
+def test_matmul_grad_null_and_workspace(lib):
+    for bad in (dict(x=None), dict(dy=None), dict(dw=None), dict(codes=8 * FAKE), dict(x=None, exponents=8 * FAKE)):
+        assert _grad(lib, **bad) == dq.DQ_ENULL, bad
+    for bad in (dict(work=None), dict(work=7 * FAKE + 128), dict(size=255), dict(tokens=100000, size=4096)):
+        assert _grad(lib, **bad) == dq.DQ_EWORKSPACE, bad
+    size = lib.dq_expert_matmul_grad_bytes
+    assert size(8, 2, 4, dq.BF16, 32, 16) == 256 and size(100000, 2, 4, dq.BF16, 32, 16) > 256
+    for bad in ((-1, 2, 4, 0, 32, 16), (8, 17, 4, 0, 32, 16), (8, 2, 0, 0, 32, 16), (8, 2, 4, 2, 32, 16), (8, 2, 4, 0, 0, 16),
+                (8, 2, 4, 0, 32, 1 << 25)):
+        assert size(*bad) == 0
+
+
+@pytest.mark.parametrize("bad", [
+    dict(kind=2), dict(width=0), dict(width=(1 << 24) + 1), dict(ys=-1), dict(rs=-1), dict(os=15), dict(y=4 * FAKE + 2),
+    dict(residual=5 * FAKE + 2), dict(out=6 * FAKE + 2), dict(out=4 * FAKE + 1020), dict(out=5 * FAKE + 64),
+    dict(out=5 * FAKE, os=32), dict(out=FAKE), dict(out=3 * FAKE + 60)])
+def test_sum_refuses(lib, bad):
+    assert _sum(lib, **bad) == dq.DQ_EINVAL
+
+
+def test_sum_null_and_empty(lib):
+    assert _sum(lib, y=None) == dq.DQ_ENULL and _sum(lib, out=None) == dq.DQ_ENULL
+    assert _sum(lib, tokens=0, y=None, out=None) == dq.DQ_OK
+
+
+@pytest.mark.parametrize("bad", [
+    dict(kind=2), dict(rows=-1), dict(cols=-1), dict(xs=-1), dict(rows=1 << 46), dict(cols=1 << 40), dict(x=FAKE + 1),
+    dict(codes=FAKE + 319), dict(codes=3 * FAKE - 159), dict(exponents=FAKE), *[dict(key=_key(**k)) for k in KEYS],
+    dict(key=_key(d_round=2 * FAKE + 156)), dict(key=_key(d_round=3 * FAKE))])
+def test_keep_refuses(lib, bad):
+    assert _keep(lib, **bad) == dq.DQ_EINVAL
+
+
+@pytest.mark.parametrize("bad", [
+    dict(kind=2), dict(rows=-1), dict(cols=-1), dict(ys=39), dict(y=3 * FAKE + 1), dict(y=FAKE + 158), dict(y=2 * FAKE),
+    dict(y=2 * FAKE - 316)])
+def test_restore_refuses(lib, bad):
+    assert _restore(lib, **bad) == dq.DQ_EINVAL
+
+
+def test_keep_and_restore_null_and_empty(lib):
+    for name in ("x", "codes", "exponents"):
+        assert _keep(lib, **{name: None}) == dq.DQ_ENULL
+    for name in ("y", "codes", "exponents"):
+        assert _restore(lib, **{name: None}) == dq.DQ_ENULL
+    assert lib.dq_keep8(FAKE, 0, 4, 40, 40, 2 * FAKE, 3 * FAKE, None, None) == dq.DQ_ENULL
+    for empty in (dict(rows=0), dict(cols=0)):
+        assert _keep(lib, x=None, **empty) == dq.DQ_OK and _restore(lib, y=None, **empty) == dq.DQ_OK
+
+
+@pytest.mark.parametrize("bad", [
+    dict(act=2), dict(act=-1), dict(kind=2), dict(width=0), dict(us=-1), dict(as_=15), dict(u=4 * FAKE + 1),
+    dict(gates=5 * FAKE + 2), dict(a=6 * FAKE + 1), *[dict(key=_key(**k)) for k in KEYS], dict(a=4 * FAKE + 1022),
+    dict(a=5 * FAKE + 62), dict(a=7 * FAKE), dict(codes=8 * FAKE - 511), dict(exponents=4 * FAKE), dict(a=2 * FAKE),
+    dict(key=_key(d_round=7 * FAKE + 508))])
+def test_act_refuses(lib, bad):
+    assert _act(lib, **bad) == dq.DQ_EINVAL
+
+
+def test_act_null_and_empty(lib):
+    for bad in (dict(u=None), dict(gates=None), dict(a=None), dict(codes=None), dict(exponents=None), dict(key=None)):
+        assert _act(lib, **bad) == dq.DQ_ENULL, bad
+    assert _act(lib, tokens=0, u=None, a=None) == dq.DQ_OK
+
+
+@pytest.mark.parametrize("bad", [
+    dict(act=2), dict(kind=2), dict(width=0), dict(us=-1), dict(das=-1), dict(dus=31), dict(as_=15), dict(u=4 * FAKE + 1),
+    dict(da=5 * FAKE + 1), dict(gates=6 * FAKE + 2), dict(du=7 * FAKE + 1), dict(again=8 * FAKE + 1),
+    dict(dgates=9 * FAKE + 2), dict(codes=10 * FAKE, exponents=11 * FAKE), dict(du=4 * FAKE), dict(du=5 * FAKE + 510),
+    dict(again=5 * FAKE), dict(again=7 * FAKE), dict(dgates=6 * FAKE), dict(dgates=8 * FAKE + 508),
+    dict(u=None, codes=10 * FAKE, exponents=11 * FAKE, du=10 * FAKE), dict(dgates=3 * FAKE)])
+def test_act_backward_refuses(lib, bad):
+    assert _back(lib, **bad) == dq.DQ_EINVAL
+
+
+def test_act_backward_null_and_empty(lib):
+    for bad in (dict(u=None), dict(da=None), dict(gates=None), dict(du=None), dict(codes=FAKE), dict(u=None, exponents=FAKE)):
+        assert _back(lib, **bad) == dq.DQ_ENULL, bad
+    assert _back(lib, tokens=0, u=None, da=None, du=None) == dq.DQ_OK
+
+
+# ---- refusals of the binding -----------------------------------------------------
+
+def test_binding_refuses_host_tensors_and_types():
+    x = torch.zeros(4, 8)
+    i = torch.zeros(4, 2, dtype=torch.int32)
+    for call in (lambda: dq.keep8(x), lambda: dq.expert_rows(i, 4), lambda: dq.expert_rows(x, 4),
+                 lambda: dq.ExpertRows(i[0], i[0], i), lambda: dq.Kept8(x.to(torch.int8), x, torch.float32),
+                 lambda: train.experts(x, i, x, x, x), lambda: train.experts(x, i, x, x, x, keep=True, site=(1 << 31) - 1)):
+        with pytest.raises((ValueError, TypeError)):
+            call()
+    for call in (lambda: dq.expert_matmul(x, x, None), lambda: dq.expert_matmul_grad(x, x, i),
+                 lambda: dq.expert_sum(x, None), lambda: dq.expert_act(x, x, None),
+                 lambda: dq.expert_act_backward(x, x, x, None), lambda: dq.restore8(x), lambda: dq.keep8(x.half()),
+                 lambda: dq.keep8(None)):
+        with pytest.raises(TypeError):
+            call()
+
+
+def test_matrix_rows_of_views():
+    x = torch.zeros(6, 4, 32)
+    assert dq._matrix_rows(x, "x") == (24, 32, 32)
+    assert dq._matrix_rows(x[:, :, 3:9], "x") == (24, 6, 32)
+    assert dq._matrix_rows(x[0, 0], "x") == (1, 32, 32)
+    assert dq._matrix_rows(x[:0], "x") == (0, 32, 32) and dq._matrix_rows(x[:, :, :0].contiguous(), "x")[0] == 0
+    for bad in (x.transpose(1, 2), x[:, :, ::2], torch.zeros(())):
+        with pytest.raises(ValueError):
+            dq._matrix_rows(bad, "x")

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import experts_ref as ref
-from compressed_hop_gradient_amd import dq
+from compressed_hop_gradient_amd import dq, train
 
 pytestmark = pytest.mark.gpu
 
@@ -336,3 +336,412 @@ def test_act_far_from_zero(dtype):
         u[0, 0] = bad
         assert not torch.isfinite(dq.expert_act(u, gates, rows)[0, 0])
         assert torch.isfinite(dq.expert_act(u, gates, rows)[0, 1:]).all()
+
+
+# ---- larger shapes, against fp64 products on the GPU -------------------------------
+
+def gpu_matmul(x, w, rows, gather):
+    """(y, sum of |x| |w|) in fp64, expert by expert."""
+    x = x[rows.source.long() // rows.top_k] if gather else x
+    at = rows.offsets.tolist()
+    y, mag = (torch.zeros(at[-1], w.shape[2], dtype=torch.float64, device="cuda") for _ in range(2))
+    for e in range(rows.experts):
+        r = slice(at[e], at[e + 1])
+        y[r] = x[r].double() @ w[e].double()
+        mag[r] = x[r].double().abs() @ w[e].double().abs()
+    return y, mag
+
+
+def gpu_grad(x, dy, rows, gather):
+    token = rows.source.long() // rows.top_k
+    x, dy = x[token] if gather == "x" else x, dy[token] if gather == "dout" else dy
+    at = rows.offsets.tolist()
+    dw, mag = (torch.zeros(rows.experts, x.shape[1], dy.shape[1], dtype=torch.float64, device="cuda") for _ in range(2))
+    for e in range(rows.experts):
+        r = slice(at[e], at[e + 1])
+        dw[e] = x[r].double().t() @ dy[r].double()
+        mag[e] = x[r].double().t().abs() @ dy[r].double().abs()
+    return dw, mag, max(b - a for a, b in zip(at, at[1:]))
+
+
+def near(got, want, bound, dtype):
+    err = (got.double() - want).abs()
+    tol = bound * (1 + 2 * half_step(dtype)) + half_step(dtype) * want.abs() + 1e-37
+    assert (err <= tol).all(), f"{(err > tol).sum()} of {err.numel()} off, worst {(err / tol).max():.3g} of its bound"
+
+
+# every tile: from few rows an expert to many, narrow and wide, whole steps and not
+LARGE = [(3, 2, 4, 1024, 520), (200, 2, 8, 1032, 264), (400, 2, 8, 512, 1040), (2048, 2, 8, 264, 520), (4100, 2, 4, 320, 776),
+         (1500, 1, 2, 96, 72), (9000, 2, 3, 40, 24), (700, 4, 5, 333, 1029)]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("T,k,E,K,N", LARGE)
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("turned", [False, True])
+def test_matmul_large(T, k, E, K, N, gather, turned, dtype):
+    rows = dq.expert_rows(choices(T, k, E, seed=N, none=0.1).cuda(), E)
+    n = rows.offsets[-1].item()
+    x = randn((T if gather else T * k, K), dtype, 1)
+    w = randn((E, N, K) if turned else (E, K, N), dtype, 2)
+    w = w.transpose(1, 2) if turned else w
+    out = torch.full((T * k, N), SENTINEL, dtype=dtype, device="cuda")
+    dq.expert_matmul(x, w, rows, gather=gather, out=out)
+    y, mag = gpu_matmul(x, w, rows, gather)
+    near(out[:n], y, product_bound(K, mag), dtype)
+    assert (out[n:] == SENTINEL).all()
+    again = torch.full_like(out, SENTINEL)
+    dq.expert_matmul(x, w, rows, gather=gather, out=again)
+    assert torch.equal(out, again)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("T,k,E,K,N", LARGE)
+@pytest.mark.parametrize("gather", [None, "x", "dout"])
+@pytest.mark.parametrize("kept", [False, True])
+def test_matmul_grad_large(T, k, E, K, N, gather, kept, dtype):
+    rows = dq.expert_rows(choices(T, k, E, seed=N, none=0.1).cuda(), E)
+    x, dy = randn((T if gather == "x" else T * k, K), dtype, 1), randn((T if gather == "dout" else T * k, N), dtype, 2)
+    given = x
+    if kept:
+        given = dq.keep8(x)
+        x = dq.restore8(given)
+    dw, mag, most = gpu_grad(x, dy, rows, gather)
+    for out in {dtype, torch.float32}:
+        got = dq.expert_matmul_grad(given, dy, rows, gather=gather, dtype=out)
+        near(got, dw, product_bound(most, mag), out)
+        assert torch.equal(got, dq.expert_matmul_grad(given, dy, rows, gather=gather, dtype=out))
+
+
+def test_rows_far_apart():
+    """Offsets of 2^31 bytes and more, which the kernels' 32-bit loads take, and beyond
+    2^32, which they do not; outputs and experts as far apart."""
+    E, K, N = 2, 72, 40
+    ids = torch.tensor([[0, 1], [1, 0], [1, -1]], dtype=torch.int32, device="cuda")
+    for apart in (1 << 30, 3 << 30):
+        T = 2 if apart == 1 << 30 else 3
+        rows = dq.expert_rows(ids[:T].contiguous(), E)
+        n = rows.offsets[-1].item()
+        mem = torch.empty((T - 1) * apart + 4096, dtype=torch.bfloat16, device="cuda")
+        x = mem.as_strided((T, K), (apart, 1))
+        x.copy_(randn((T, K), torch.bfloat16, 1))
+        w = randn((E, K, N), torch.bfloat16, 2)
+        y, mag = gpu_matmul(x, w, rows, True)
+        near(dq.expert_matmul(x, w, rows, gather=True)[:n], y, product_bound(K, mag), torch.bfloat16)
+        dy = randn((2 * T, N), torch.bfloat16, 3)
+        dw, mag, most = gpu_grad(x, dy, rows, "x")
+        near(dq.expert_matmul_grad(x, dy, rows, gather="x"), dw, product_bound(most, mag), torch.bfloat16)
+        # the same memory as an output, and as weights
+        far = mem.as_strided((T, N), (apart, 1), 256)
+        z, mag = gpu_back(dy, rows)
+        dq.expert_sum(dy, rows, out=far)
+        near(far, z, 4 * U * mag, torch.bfloat16)
+        wf = mem.as_strided((E, K, N), (apart, N, 1), 1024)
+        wf.copy_(w)
+        xs = x.contiguous()
+        assert torch.equal(dq.expert_matmul(xs, wf, rows, gather=True)[:n], dq.expert_matmul(xs, w, rows, gather=True)[:n])
+        kept = dq.keep8(x)
+        assert torch.equal(kept.codes, dq.keep8(xs).codes)
+        del mem, x, far, wf
+
+
+def gpu_back(y, rows):
+    at = rows.row.long()
+    v = torch.where((at >= 0)[:, :, None], y.double()[at.clamp(min=0)], 0.0)
+    return v.sum(1), v.abs().sum(1)
+
+
+def test_keep_beyond_32_bits():
+    """2^32 + 4096 elements of rows 1000 wide (dithers at any offset) and 1024 wide."""
+    for cols in (1000, 1024):
+        n = ((1 << 32) + 4096) // cols
+        x = torch.empty((n, cols), dtype=torch.bfloat16, device="cuda").fill_(0.3)
+        x[-1] = randn((cols,), torch.bfloat16, 1)
+        kept = dq.keep8(x, **KEY)
+        first = (n - 1) * cols
+        b0 = first // 8
+        key = dict(KEY)
+        from oracle import pyoracle as po
+        d = []
+        for b in range(b0, b0 + cols // 8 + 1):
+            w = po.philox4x32([b & 0xFFFFFFFF, (b >> 32) | 0x8000 | key["worker"] << 16, key["rnd"], (1 << 31) | key["site"]],
+                              [key["seed"] & 0xFFFFFFFF, key["seed"] >> 32])
+            d += [h for v in w for h in (int(v) & 0xFFFF, int(v) >> 16)]
+        codes, exps, _ = ref.keep(f64(x[-1:]), np.array(d[first - 8 * b0:][:cols], np.int64))
+        assert np.array_equal(kept.codes[-1:].cpu().numpy(), codes)
+        assert np.array_equal(kept.exponents[-1:].cpu().numpy(), exps)
+        assert torch.equal(dq.restore8(dq.Kept8(kept.codes[-1:].clone(), kept.exponents[-1:].clone(), kept.dtype))[0],
+                           dq.restore8(kept)[-1])
+        del x, kept
+
+
+def test_entries_out_of_range_are_no_rows():
+    """Lists that no call of expert_rows makes: slots out of range read as zeros, rows
+    out of range add nothing, offsets are held to the rows there are."""
+    dtype = torch.bfloat16
+    ids = torch.tensor([[0], [1], [1], [0]], dtype=torch.int32, device="cuda")
+    good = dq.expert_rows(ids, 2)
+    x, w, dy = randn((4, 64), dtype, 1), randn((2, 64, 64), dtype, 2), randn((4, 64), dtype, 3)
+    source = good.source.clone()
+    source[1], source[2] = 1 << 30, -5
+    bad = dq.ExpertRows(good.offsets, source, good.row)
+    want = dq.expert_matmul(x, w, good, gather=True)
+    got = dq.expert_matmul(x, w, bad, gather=True)
+    assert torch.equal(got[[0, 3]], want[[0, 3]]) and (got[1:3] == 0).all()
+    dy[1:3] = 0
+    assert torch.equal(dq.expert_matmul_grad(x, dy, bad, gather="x"), dq.expert_matmul_grad(x, dy, good, gather="x"))
+    row = good.row.clone()
+    row[0], row[1] = 4, -(1 << 30)
+    assert (dq.expert_sum(dy, dq.ExpertRows(good.offsets, good.source, row))[:2] == 0).all()
+    gates = torch.ones(4, 1, device="cuda")
+    a = dq.expert_act(x, gates, bad)
+    assert (a[1:3] == 0).all() and torch.equal(a[[0, 3]], dq.expert_act(x, gates, good)[[0, 3]])
+    high = dq.ExpertRows(torch.tensor([-3, 2, 1 << 30], dtype=torch.int32, device="cuda"), good.source, good.row)
+    assert torch.equal(dq.expert_matmul(x, w, high, gather=True), want)
+    none = dq.ExpertRows(torch.tensor([3, 2, 1], dtype=torch.int32, device="cuda"), good.source, good.row)
+    out = torch.full((4, 64), SENTINEL, dtype=dtype, device="cuda")
+    assert (dq.expert_matmul(x, w, none, gather=True, out=out) == SENTINEL).all()
+    assert (dq.expert_matmul_grad(x, dy, none, gather="x") == 0).all()
+
+
+def test_infinities_stay_in_their_rows():
+    dtype = torch.bfloat16
+    ids = choices(64, 2, 4, none=0).cuda()
+    rows = dq.expert_rows(ids, 4)
+    x, w = randn((64, 72), dtype, 1), randn((4, 72, 40), dtype, 2)
+    clean = dq.expert_matmul(x, w, rows, gather=True)
+    x[5, 3], x[9, 0] = float("inf"), float("nan")
+    got = dq.expert_matmul(x, w, rows, gather=True)
+    hit = torch.isin(rows.source // 2, torch.tensor([5, 9], device="cuda"))
+    assert torch.equal(got[~hit], clean[~hit]) and not torch.isfinite(got[hit]).any()
+    w[2] = float("nan")
+    got = dq.expert_matmul(x, w, rows, gather=True)
+    at = rows.offsets.tolist()
+    other = torch.ones(128, dtype=torch.bool, device="cuda")
+    other[at[2]:at[3]] = False
+    assert torch.equal(got[other & ~hit], clean[other & ~hit])
+
+
+def test_expanded_operands():
+    ids = choices(40, 2, 4, none=0).cuda()
+    rows = dq.expert_rows(ids, 4)
+    row, w = randn((1, 64), torch.float32, 1), randn((1, 64, 24), torch.float32, 2)
+    a = dq.expert_matmul(row.expand(40, 64), w.expand(4, 64, 24), rows, gather=True)
+    assert torch.equal(a, dq.expert_matmul(row.repeat(40, 1), w.repeat(4, 1, 1), rows, gather=True))
+    dy = randn((80, 24), torch.float32, 3)
+    assert torch.equal(dq.expert_matmul_grad(row.expand(40, 64), dy, rows, gather="x"),
+                       dq.expert_matmul_grad(row.repeat(40, 1), dy, rows, gather="x"))
+
+
+# ---- through autograd, streams, graphs ----------------------------------------------
+
+def layer(seed, T, k, E, H, F, kind, dtype, none=0.2):
+    ids = choices(T, k, E, seed=seed, none=none).cuda()
+    x, dy = randn((T, H), dtype, seed), randn((T, H), dtype, seed + 1)
+    gates = torch.rand(T, k, generator=torch.Generator().manual_seed(seed)).cuda()
+    w_in = randn((E, H, F * (2 if kind == "swiglu" else 1)), dtype, seed + 2, H ** -0.5)
+    w_out = randn((E, F, H), dtype, seed + 3, F ** -0.5)
+    return ids, x, dy, gates, w_in, w_out
+
+
+def by_calls(ids, x, dy, gates, w_in, w_out, kind, keep, key):
+    """The same layer by the calls it is made of."""
+    rows = dq.expert_rows(ids, w_in.shape[0])
+    u = dq.expert_matmul(x, w_in, rows, gather=True)
+    a = dq.expert_act(u, gates, rows, kind)
+    y = dq.expert_sum(dq.expert_matmul(a, w_out, rows), rows)
+    kx, ku = x, u
+    if keep:
+        kx, ku = dq.keep8(x, **key), dq.keep8(u, **{**key, "site": key["site"] + 1})
+    da = dq.expert_matmul(dy, w_out.transpose(1, 2), rows, gather=True)
+    du, dgates, again = dq.expert_act_backward(ku, da, gates, rows, kind)
+    return [y, dq.expert_sum(dq.expert_matmul(du, w_in.transpose(1, 2), rows), rows), dgates,
+            dq.expert_matmul_grad(kx, du, rows, gather="x"), dq.expert_matmul_grad(again, dy, rows, gather="dout")]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("kind", ["swiglu", "relu"])
+@pytest.mark.parametrize("keep", [False, True])
+@pytest.mark.parametrize("T,H,F", [(1, 64, 32), (50, 72, 40), (33, 65, 31), (300, 256, 128)])
+def test_experts_autograd(T, H, F, keep, kind, dtype):
+    ids, x, dy, gates, w_in, w_out = layer(T, T, 2, 4, H, F, kind, dtype, none=0.2 if T > 1 else 0)
+    leaves = [t.clone().requires_grad_() for t in (x, gates, w_in, w_out)]
+    y = train.experts(leaves[0], ids, *leaves[1:], act=kind, keep=keep, **KEY)
+    got = [y.detach(), *torch.autograd.grad(y, leaves, dy)]
+    for g, w in zip(got, by_calls(ids, x, dy, gates, w_in, w_out, kind, keep, KEY)):
+        assert g.dtype == w.dtype and torch.equal(g, w)
+    # only what is asked for
+    y = train.experts(x, ids, gates, leaves[2], w_out, act=kind, keep=keep, **KEY)
+    assert torch.equal(torch.autograd.grad(y, leaves[2], dy)[0], got[3])
+
+
+@pytest.mark.parametrize("kind", ["swiglu", "relu"])
+def test_experts_autograd_against_fp64(kind):
+    """fp32 against autograd in fp64 of the plain loop.  Every step of the chain is off by
+    less than (H + 2 F + 40) 2 U of its magnitude, and passes on at most 4 times what
+    comes in (the slope of silu is below 1.1, gates below 1); magnitudes are the same
+    loop's on absolute values, without the activation."""
+    T, k, E, H, F = 60, 2, 4, 64, 48
+    ids, x, dy, gates, w_in, w_out = layer(5, T, k, E, H, F, kind, torch.float32)
+    leaves = [t.clone().requires_grad_() for t in (x, gates, w_in, w_out)]
+    y = train.experts(leaves[0], ids, *leaves[1:], act=kind)
+    got = [y.detach(), *torch.autograd.grad(y, leaves, dy)]
+
+    def loop(x, gates, w_in, w_out, f):
+        y = torch.zeros(T, H, dtype=torch.float64)
+        for t in range(T):
+            for j in range(k):
+                e = int(ids[t, j])
+                if e >= 0:
+                    y[t] = y[t] + gates[t, j] * (f(x[t] @ w_in[e]) @ w_out[e])
+        return y
+
+    def swiglu(u):
+        return torch.nn.functional.silu(u[:F]) * u[F:]
+
+    args = [t.detach().cpu().double().requires_grad_() for t in leaves]
+    want = loop(*args, swiglu if kind == "swiglu" else torch.relu)
+    want = [want.detach(), *torch.autograd.grad(want, args, dy.cpu().double())]
+    mags = [t.detach().cpu().double().abs().requires_grad_() for t in leaves]
+    mag = loop(*mags, (lambda u: u[:F] * u[F:]) if kind == "swiglu" else (lambda u: u))
+    mag = [mag.detach(), *torch.autograd.grad(mag, mags, dy.cpu().double().abs())]
+    for g, w, m in zip(got, want, mag):
+        err = (g.cpu().double() - w).abs()
+        bound = 4 * 4 * (H + 2 * F + 40) * 2 * U * m
+        assert (err <= bound).all(), (err / bound).max()
+
+
+def test_kept_weight_gradient_is_right_in_the_mean():
+    """x kept with dither: dw = sum of kept(x)^T du over draws comes near x^T du."""
+    T, H, N = 64, 64, 8
+    rows = dq.expert_rows(torch.zeros((T, 1), dtype=torch.int32, device="cuda"), 1)
+    x, du = randn((T, H), torch.float32, 1), randn((T, N), torch.float32, 2)
+    n = 400
+    mean = sum(dq.expert_matmul_grad(dq.keep8(x, rnd=i), du, rows).double() for i in range(n)) / n
+    want = x.double().t() @ du.double()
+    step = torch.exp2(dq.keep8(x).exponents.double() - 127).repeat_interleave(32, 1)
+    # an element's draw has a variance of at most step^2 / 4; sums of 64 of them
+    sd = (0.25 * (step ** 2).t() @ du.double() ** 2).sqrt()[None] / n ** 0.5
+    assert ((mean - want).abs() <= 6 * sd + 1e-4 * sd * n ** 0.5 + 2 ** -15 * sd * n ** 0.5).all()
+
+
+def test_no_tokens():
+    ids = torch.zeros((0, 2), dtype=torch.int32, device="cuda")
+    for dtype in DTYPES:
+        args = [torch.zeros(s, dtype=d, device="cuda", requires_grad=True) for s, d in
+                (((0, 16), dtype), ((0, 2), torch.float32), ((3, 16, 8), dtype), ((3, 4, 16), dtype))]
+        for keep in (False, True):
+            y = train.experts(args[0], ids, *args[1:], keep=keep)
+            assert y.shape == (0, 16)
+            grads = torch.autograd.grad(y.sum(), args)
+            assert all(g.shape == a.shape and (g == 0).all() for g, a in zip(grads, args))
+
+
+def test_on_another_stream():
+    ids, x, dy, gates, w_in, w_out = layer(3, 200, 2, 4, 64, 48, "swiglu", torch.bfloat16)
+    want = by_calls(ids, x, dy, gates, w_in, w_out, "swiglu", True, KEY)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        got = by_calls(ids, x, dy, gates, w_in, w_out, "swiglu", True, KEY)
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    rows = dq.expert_rows(ids, 4, stream=side)
+    u = dq.expert_matmul(x, w_in, rows, gather=True, stream=side)
+    a, kept = dq.expert_act(u, gates, rows, keep=True, stream=side, **KEY)
+    y = dq.expert_sum(dq.expert_matmul(a, w_out, rows, stream=side), rows, stream=side)
+    r = dq.restore8(dq.keep8(x, stream=side), stream=side)
+    dw = dq.expert_matmul_grad(x, a, rows, gather="x", stream=side)
+    side.synchronize()
+    assert torch.equal(y, want[0]) and torch.equal(r, dq.restore8(dq.keep8(x)))
+    assert torch.equal(dw, dq.expert_matmul_grad(x, a, rows, gather="x"))
+
+
+def test_layer_in_graph_replays():
+    """Two captured layers over the same inputs, replayed in turn with other tokens,
+    choices and rounds, and eager work between: every replay gives the eager bits."""
+    T, k, E, H, F = 120, 2, 4, 64, 48
+    ids, x, dy, gates, w_in, w_out = layer(7, T, k, E, H, F, "swiglu", torch.bfloat16)
+    rnd = torch.zeros(1, dtype=torch.int32, device="cuda")
+    key = dict(KEY, rnd=rnd)
+
+    def step():
+        return by_calls(ids, x, dy, gates, w_in, w_out, "swiglu", True, key)
+
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        step()
+    side.synchronize()
+    graphs, outs = [], []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(step())
+        graphs.append(g)
+    for i in range(6):
+        fresh = layer(100 + i, T, k, E, H, F, "swiglu", torch.bfloat16, none=0.2 if i % 2 else 0.9)
+        for to, new in zip((ids, x, dy, gates), fresh):
+            to.copy_(new)
+        rnd.fill_(i)
+        n = int((ids >= 0).sum())
+        want = [t.clone() for t in step()]
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        for out in outs:
+            assert all(torch.equal(a, b) for a, b in zip(out, want)), (i, n)
+
+
+def test_route_experts_dropout_together():
+    """A step of a mixture-of-experts block as a program runs it: route, experts with
+    kept activations, dropout onto the residual, backward through all of them."""
+    T, k, E, H, F = 200, 2, 8, 64, 48
+    dtype = torch.bfloat16
+    x = randn((T, H), dtype, 1)
+    leaves = [randn(s, dtype, i, H ** -0.5).requires_grad_() for i, s in
+              enumerate(((H, E), (E, H, 2 * F), (E, F, H)))]
+    mask = torch.rand(T, generator=torch.Generator().manual_seed(0)) > 0.1
+    xs = x.clone().requires_grad_()
+    r = train.route((xs @ leaves[0]).float(), k, masks=mask.cuda())
+    y = train.experts(xs, r.ids, r.gates, *leaves[1:], keep=True, rnd=3)
+    z = train.dropout(y, 0.1, residual=xs, rnd=3)
+    grads = torch.autograd.grad((z.float() ** 2).mean() + 0.01 * r.loss.sum(), [xs, *leaves])
+    assert all(torch.isfinite(g).all() and g.abs().sum() > 0 for g in grads)
+    # tokens left out: the experts add nothing, and their gradient is the residual's alone
+    assert (y[~mask.cuda()] == 0).all() and torch.equal(z[~mask.cuda()], x[~mask.cuda()])
+    dz = (2 * z.detach().float() / z.numel()).to(dtype)
+    assert torch.equal(grads[0][~mask.cuda()], dz[~mask.cuda()])
+
+
+def test_refusals():
+    ids = torch.zeros((4, 2), dtype=torch.int32, device="cuda")
+    rows = dq.expert_rows(ids, 3)
+    x, w = torch.zeros(8, 16, device="cuda"), torch.zeros(3, 16, 24, device="cuda")
+    gates = torch.ones(4, 2, device="cuda")
+    for call in (lambda: dq.expert_matmul(x[:4], w, rows), lambda: dq.expert_matmul(x, w, rows, gather=True),
+                 lambda: dq.expert_matmul(x, w[:2], rows), lambda: dq.expert_matmul(x, w.bfloat16(), rows),
+                 lambda: dq.expert_matmul(x, w[:, :, ::2], rows), lambda: dq.expert_matmul(x.t(), w, rows),
+                 lambda: dq.expert_matmul(x, w, rows, out=x), lambda: dq.expert_matmul(x, w, rows, out=torch.zeros(8, 24)),
+                 lambda: dq.expert_matmul_grad(x, x, rows, gather="y"), lambda: dq.expert_matmul_grad(x, x[:4], rows),
+                 lambda: dq.expert_matmul_grad(dq.keep8(x[:4]), x, rows),
+                 lambda: dq.expert_matmul_grad(dq.keep8(x.bfloat16()), x, rows),
+                 lambda: dq.expert_matmul_grad(x, x, rows, out=torch.zeros(3, 16, 15, device="cuda")),
+                 lambda: dq.expert_sum(x[:4], rows), lambda: dq.expert_sum(x, rows, residual=x),
+                 lambda: dq.expert_act(x, gates[:3], rows), lambda: dq.expert_act(x, gates, rows, "tanh"),
+                 lambda: dq.expert_act(x[:, :15], gates, rows), lambda: dq.expert_act_backward(x, x, gates, rows),
+                 lambda: dq.expert_act_backward(x, x[:, :8], gates, rows, du=x[:, :8]),
+                 lambda: dq.expert_rows(ids, 0), lambda: dq.expert_rows(ids, 1025), lambda: dq.expert_rows(ids[0], 3),
+                 lambda: dq.keep8(x, seed=-1), lambda: dq.keep8(x, worker=1 << 16), lambda: dq.keep8(x.t()),
+                 lambda: dq.restore8(dq.keep8(x), out=x[:4]),
+                 lambda: dq.Kept8(torch.zeros(4, 40, dtype=torch.int8, device="cuda"),
+                                  torch.zeros(4, 1, dtype=torch.uint8, device="cuda"), torch.float32)):
+        with pytest.raises(ValueError):
+            call()
+    for call in (lambda: dq.expert_matmul_grad(x, x, rows, dtype=torch.bfloat16), lambda: dq.expert_rows(ids.long(), 3),
+                 lambda: dq.expert_act(x, gates.double(), rows), lambda: dq.keep8(x.half()),
+                 lambda: dq.Kept8(torch.zeros(4, 40, dtype=torch.int8, device="cuda"),
+                                  torch.zeros(4, 2, dtype=torch.uint8, device="cuda"), torch.float16)):
+        with pytest.raises(TypeError):
+            call()
+    with pytest.raises(dq.DQError):
+        dq.expert_sum(x, rows, out=x[:4])            # over its operand
