@@ -16,6 +16,7 @@ template <class C, int LA, int LB, bool TURNED>
 __device__ __forceinline__ void product_tile(const ExpertProductArgs &a, const RowTile &t, int n0, int from, int inner,
                                              char *lds, Acc<C> &acc) {
     typedef typename C::T T;
+    const bool mine = acc.m0() < t.rows && n0 + acc.n0() < a.N;
     Along<C, C::BM, LA> x;
     x.start(static_cast<const T *>(a.x) + (a.gather ? 0 : t.first * a.xs) + from, inner, [&](int i) {
         i = min(i, t.rows - 1);
@@ -25,11 +26,11 @@ __device__ __forceinline__ void product_tile(const ExpertProductArgs &a, const R
     if constexpr (TURNED) {
         Along<C, C::BN, LB> b;
         b.start(w + n0 * a.ws + from, inner, [&](int i) { return min(i, a.N - 1 - n0) * a.ws; });
-        multiply<C>(lds, x, b, inner, acc);
+        multiply<C>(lds, x, b, inner, mine, acc);
     } else {
         Across<C, C::BN, LB, false> b(RowsDown<false>(a.ws, from));
         b.start(w, n0, a.N, inner);
-        multiply<C>(lds, x, b, inner, acc);
+        multiply<C>(lds, x, b, inner, mine, acc);
     }
 }
 
@@ -42,7 +43,8 @@ __global__ __launch_bounds__(C::kThreads) void k_product(ExpertProductArgs a, in
     const int n0 = t.n * C::BN;
     Acc<C> acc;
     product_tile<C, LA, LB, TURNED>(a, t, n0, 0, a.K, lds, acc);
-    acc.store([&](int m) { return m < t.rows ? static_cast<T *>(a.y) + (t.first + m) * a.ys : nullptr; }, n0, a.N);
+    acc.template store<T>(lds, [&](int m) { return m < t.rows ? static_cast<T *>(a.y) + (t.first + m) * a.ys : nullptr; },
+                          n0, a.N);
 }
 
 // The same for few rows, which the weights' bytes bound: a tile is one wave's, four of
@@ -68,7 +70,10 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_product_few(ExpertProductArg
 #pragma unroll
     for (int w = 0; w < kFewWaves; w++)
         sum += *reinterpret_cast<const f32x4 *>(lds + w * C::kLds + 16 * threadIdx.x);
-    store_columns(static_cast<T *>(a.y) + (t.first + m) * a.ys, n0 + n, a.N, sum);
+    T out[4];
+#pragma unroll
+    for (int q = 0; q < 4; q++) put_one(out + q, sum[q]);
+    store_columns<4>(static_cast<T *>(a.y) + (t.first + m) * a.ys, n0 + n, a.N, out);
 }
 
 constexpr int kWeightsRun = 8;
@@ -103,10 +108,10 @@ __global__ __launch_bounds__(C::kThreads) void k_weights(ExpertWeightsArgs a, in
     else
         x.start(static_cast<const T *>(a.x), m0, a.K, rows);
     dy.start(static_cast<const T *>(a.dy), n0, a.N, rows);
-    multiply<C>(lds, x, dy, rows, acc);
+    multiply<C>(lds, x, dy, rows, m0 + acc.m0() < a.K && n0 + acc.n0() < a.N, acc);
     Out *dw = static_cast<Out *>(a.parts > 1 ? (void *)a.partial : a.dw) +
               ((int64_t)part * a.l.E + e) * a.K * a.N;
-    acc.store([&](int m) { return m0 + m < a.K ? dw + (int64_t)(m0 + m) * a.N : nullptr; }, n0, a.N);
+    acc.template store<Out>(lds, [&](int m) { return m0 + m < a.K ? dw + (int64_t)(m0 + m) * a.N : nullptr; }, n0, a.N);
 }
 
 // The parts' sums, in their order.
@@ -115,7 +120,7 @@ __global__ __launch_bounds__(256) void k_weights_join(const float *partial, int 
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
         float s = partial[i];
         for (int p = 1; p < parts; p++) s += partial[p * n + i];
-        store_one(dw + i, s);
+        put_one(dw + i, s);
     }
 }
 
