@@ -307,7 +307,7 @@ hipError_t launch_expert_product(const ExpertProductArgs &a, int f32, hipStream_
 
 // Enough parts that tiles of 128 x 128 give every CU a block, of 128 rows of an average
 // expert at least.
-int expert_weights_parts(int64_t slots, int E, int64_t K, int64_t N, int) {
+int expert_weights_parts(int64_t slots, int E, int64_t K, int64_t N) {
     const int64_t tiles = (K + 127) / 128 * ((N + 127) / 128) * E, most = slots / E / 128;
     const int64_t parts = tiles >= 256 ? 1 : (255 + tiles) / tiles;
     return (int)std::max((int64_t)1, std::min(parts, most));

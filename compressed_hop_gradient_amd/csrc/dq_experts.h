@@ -58,6 +58,7 @@ struct RestoreArgs {
     const uint8_t *exponents;
     void *y;
     int64_t rows, cols, ys;
+    const int32_t *d_rows;              // as above
 };
 hipError_t launch_restore8(const RestoreArgs &a, int f32, hipStream_t s);
 
@@ -112,7 +113,7 @@ struct ExpertWeightsArgs {
     int32_t parts;
 };
 // parts into which the rows are split, whose sums meet in a second launch
-int expert_weights_parts(int64_t slots, int E, int64_t K, int64_t N, int f32);
+int expert_weights_parts(int64_t slots, int E, int64_t K, int64_t N);
 hipError_t launch_expert_weights(const ExpertWeightsArgs &a, int f32, hipStream_t s);
 
 }  // namespace dq

@@ -49,6 +49,22 @@ KeepKey key_of(const dq_keep_key *k) {
                    k->flags & DQ_KEEP_DITHER};
 }
 
+// The workspace of a weights' gradient: parts' sums, then x restored from its codes.
+size_t weights_partial_bytes(int64_t slots, int32_t E, int64_t inner, int64_t outer) {
+    const int parts = expert_weights_parts(slots, E, inner, outer);
+    return parts > 1 ? (4 * (size_t)parts * E * inner * outer + kAlign - 1) / kAlign * kAlign : 0;
+}
+// 0 where the codes are decoded as they are read.  Where the product is long, x restored
+// once and read 16 bytes at a time is faster: 60 experts of 55 tokens' choices, 1000 x 1416
+// bf16 into fp32 234 us from the codes, 157 + 6 restored; 64 x 1024, 2048 x 2816 1455 and 873 +
+// 10; 64 x 8, 1024 x 1024 50 and 38 + 6.  Short ones save the launch: 8 x 16, 512 x 512 10 and 10
+// + 6.
+size_t weights_restored_bytes(int64_t rows_x, int64_t slots, int32_t E, int64_t inner, int64_t outer, int f32) {
+    const double weights = (double)E * inner * outer, work = (double)slots * inner * outer;
+    if (inner % 8 != 0 || (weights < (double)(1 << 25) && work < 4.0 * (1 << 30))) return 0;
+    return (size_t)rows_x * inner * (f32 ? 4 : 2);
+}
+
 }  // namespace
 
 extern "C" {
@@ -66,7 +82,7 @@ dq_status dq_expert_rows(const int32_t *ids, int64_t tokens, int32_t k, int32_t 
     if (!offsets || (slots > 0 && (!ids || !source || !row))) return DQ_ENULL;
     if (!aligned(ids, 4) || !aligned(offsets, 4) || !aligned(source, 4) || !aligned(row, 4)) return DQ_EINVAL;
     const size_t need = dq_expert_rows_bytes(tokens, k, E);
-    if (!work || !aligned(work, kAlign) || work_bytes < need) return DQ_EWORKSPACE;
+    if ((!work && need > kAlign) || !aligned(work, kAlign) || work_bytes < need) return DQ_EWORKSPACE;
     Spans spans;
     spans.add(bytes(ids, 4 * (size_t)slots, false));
     spans.add(bytes(offsets, 4 * ((size_t)E + 1), true));
@@ -138,7 +154,7 @@ dq_status dq_restore8(const int8_t *codes, const uint8_t *exponents, int32_t kin
     spans.add(bytes(exponents, (size_t)(rows * ((cols + 31) / 32)), false));
     spans.add(span(y, rows, ys, cols, es, true));
     if (spans.clash()) return DQ_EINVAL;
-    const RestoreArgs a{codes, exponents, y, rows, cols, ys};
+    const RestoreArgs a{codes, exponents, y, rows, cols, ys, nullptr};
     return hip_status(launch_restore8(a, kind == DQ_F32, static_cast<hipStream_t>(stream)));
 }
 
@@ -262,10 +278,15 @@ dq_status dq_expert_matmul(const dq_expert_lists *l, const void *x, int64_t xs, 
     return hip_status(launch_expert_product(a, kind == DQ_F32, static_cast<hipStream_t>(stream)));
 }
 
-size_t dq_expert_matmul_grad_bytes(int64_t tokens, int32_t k, int32_t E, int32_t kind, int64_t inner, int64_t outer) {
-    if (bad_counts(tokens, k, E) || !is_kind(kind) || bad_width(inner) || bad_width(outer)) return 0;
-    const int parts = expert_weights_parts(tokens * k, E, inner, outer, kind == DQ_F32);
-    return kAlign + (parts > 1 ? 4 * (size_t)parts * E * inner * outer : 0);
+size_t dq_expert_matmul_grad_bytes(int64_t tokens, int32_t k, int32_t E, int32_t kind, int32_t gather, int64_t inner,
+                                   int64_t outer, int32_t kept) {
+    if (bad_counts(tokens, k, E) || !is_kind(kind) || bad_width(inner) || bad_width(outer) || gather < 0 ||
+        gather > DQ_GATHER_DOUT)
+        return 0;
+    return kAlign + weights_partial_bytes(tokens * k, E, inner, outer) +
+           (kept ? weights_restored_bytes(gather == DQ_GATHER_X ? tokens : tokens * k, tokens * k, E, inner, outer,
+                                          kind == DQ_F32)
+                 : 0);
 }
 
 dq_status dq_expert_matmul_grad(const dq_expert_lists *l, const void *x, int64_t xs, const int8_t *codes,
@@ -283,7 +304,8 @@ dq_status dq_expert_matmul_grad(const dq_expert_lists *l, const void *x, int64_t
     if (!dw || (slots > 0 && ((!x && !codes) || !dy))) return DQ_ENULL;
     const int64_t es = (int64_t)elem_bytes(kind), os = (int64_t)elem_bytes(out_kind);
     if (!aligned(x, es) || !aligned(dy, es) || !aligned(dw, os)) return DQ_EINVAL;
-    const size_t need = dq_expert_matmul_grad_bytes(l->tokens, l->top_k, l->n_experts, kind, inner, outer);
+    const size_t need =
+        dq_expert_matmul_grad_bytes(l->tokens, l->top_k, l->n_experts, kind, gather, inner, outer, codes != nullptr);
     if (!work || !aligned(work, kAlign) || work_bytes < need) return DQ_EWORKSPACE;
     const int64_t rows_x = gather == DQ_GATHER_X ? l->tokens : slots;
     Spans spans;
@@ -312,7 +334,17 @@ dq_status dq_expert_matmul_grad(const dq_expert_lists *l, const void *x, int64_t
     a.K = (int32_t)inner;
     a.N = (int32_t)outer;
     a.partial = static_cast<float *>(work);
-    a.parts = expert_weights_parts(slots, l->n_experts, inner, outer, kind == DQ_F32);
+    a.parts = expert_weights_parts(slots, l->n_experts, inner, outer);
+    if (codes && slots > 0 && weights_restored_bytes(rows_x, slots, l->n_experts, inner, outer, kind == DQ_F32)) {
+        // of the rows, those of experts alone
+        const RestoreArgs r{codes, exponents, static_cast<char *>(work) + weights_partial_bytes(slots, l->n_experts, inner, outer),
+                            rows_x, inner, inner, gather == DQ_GATHER_X ? nullptr : l->d_offsets + l->n_experts};
+        const hipError_t e = launch_restore8(r, kind == DQ_F32, static_cast<hipStream_t>(stream));
+        if (e != hipSuccess) return hip_status(e);
+        a.x = r.y;
+        a.xs = inner;
+        a.codes = nullptr;
+    }
     return hip_status(launch_expert_weights(a, kind == DQ_F32, static_cast<hipStream_t>(stream)));
 }
 

@@ -39,9 +39,10 @@ __global__ __launch_bounds__(256) void k_keep8(KeepArgs a, int32_t blocks, int64
 
 template <bool F32>
 __global__ __launch_bounds__(256) void k_restore8(RestoreArgs a, int32_t blocks, int64_t total) {
-    const int64_t per_row = (a.cols + 7) / 8;
+    const int64_t per_row = (a.cols + 7) / 8, rows = a.d_rows ? min(a.rows, (int64_t)max(0, *a.d_rows)) : a.rows;
     for (int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x; id < total; id += (int64_t)gridDim.x * 256) {
         const int64_t row = id / per_row, col = (id - row * per_row) * 8;
+        if (row >= rows) return;
         const float scale = kept_scale(a.exponents[row * blocks + col / 32]);
         const auto eight = [&](auto full) {
             constexpr bool kFull = decltype(full)::value;

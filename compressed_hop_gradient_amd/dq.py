@@ -137,7 +137,8 @@ _SIGS = {
                                  C.c_void_p, C.c_size_t, C.c_void_p]),
     "dq_expert_matmul": (C.c_int, [C.c_void_p, C.c_void_p, C.c_int64, C.c_int32, C.c_void_p, C.c_int64, C.c_int64,
                                    C.c_void_p, C.c_int64, C.c_int32, C.c_int64, C.c_int64, C.c_void_p]),
-    "dq_expert_matmul_grad_bytes": (C.c_size_t, [C.c_int64, C.c_int32, C.c_int32, C.c_int32, C.c_int64, C.c_int64]),
+    "dq_expert_matmul_grad_bytes": (C.c_size_t, [C.c_int64, C.c_int32, C.c_int32, C.c_int32, C.c_int32, C.c_int64,
+                                                 C.c_int64, C.c_int32]),
     "dq_expert_matmul_grad": (C.c_int, [C.c_void_p, C.c_void_p, C.c_int64, C.c_void_p, C.c_void_p, C.c_void_p,
                                         C.c_int64, C.c_int32, C.c_void_p, C.c_int32, C.c_int32, C.c_int64,
                                         C.c_int64, C.c_void_p, C.c_size_t, C.c_void_p]),
@@ -637,6 +638,15 @@ class Kept8:
     ``exponents`` (one for every 32 elements of its last dimension, which it
     replaces), and the ``dtype`` it had."""
 
+    @classmethod
+    def _made(cls, shape, x):
+        """Buffers for what is to be kept of ``x``."""
+        kept = cls.__new__(cls)
+        kept.codes = x.new_empty(shape, dtype=torch.int8)
+        kept.exponents = x.new_empty((*shape[:-1], (shape[-1] + 31) // 32), dtype=torch.uint8)
+        kept.dtype = x.dtype
+        return kept
+
     def __init__(self, codes, exponents, dtype):
         if not isinstance(codes, torch.Tensor) or codes.dim() == 0 or codes.device.type != "cuda":
             raise ValueError("codes: expected a tensor of at least one dimension on a GPU")
@@ -680,11 +690,11 @@ def keep8(x, dither=True, seed=1, rnd=0, worker=0, site=0):
     :func:`dropout`."""
     dev = _gpu(x, "x").device
     rows, cols, stride = _matrix_rows(x, "x")
-    codes = torch.empty(x.shape, dtype=torch.int8, device=dev)
-    exponents = torch.empty(x.shape[:-1] + ((cols + 31) // 32,), dtype=torch.uint8, device=dev)
-    _call(dev, "dq_keep8", x.data_ptr(), _kind(x), rows, cols, stride, codes.data_ptr(), exponents.data_ptr(),
-          _keep_key(dither, seed, rnd, worker, site, dev))
-    return Kept8(codes, exponents, x.dtype)
+    key = _keep_key(dither, seed, rnd, worker, site, dev)
+    kept = Kept8._made(x.shape, x)
+    _call(dev, "dq_keep8", x.data_ptr(), _kind(x), rows, cols, stride, kept.codes.data_ptr(),
+          kept.exponents.data_ptr(), key)
+    return kept
 
 
 @_on_stream
@@ -694,7 +704,7 @@ def restore8(kept, out=None):
     if not isinstance(kept, Kept8):
         raise TypeError(f"kept: expected a Kept8, got {type(kept).__name__}")
     if out is None:
-        out = torch.empty(kept.shape, dtype=kept.dtype, device=kept.device)
+        out = kept.codes.new_empty(kept.shape, dtype=kept.dtype)
     elif _gpu(out, "out").shape != kept.shape or out.dtype != kept.dtype or out.device != kept.device:
         raise ValueError(f"out: {tuple(out.shape)} {out.dtype} on {out.device}, "
                          f"kept is {tuple(kept.shape)} {kept.dtype} on {kept.device}")
@@ -719,11 +729,14 @@ class ExpertRows:
         _tensor(offsets, "offsets", dev, dtype=torch.int32)
         if offsets.dim() != 1 or offsets.numel() < 2:
             raise ValueError(f"offsets: shape {tuple(offsets.shape)}, expected [experts + 1]")
+        self._set(offsets, source, row, dev, *row.shape, offsets.numel() - 1)
+
+    def _set(self, offsets, source, row, dev, tokens, top_k, experts):
         self.offsets, self.source, self.row, self.device = offsets, source, row, dev
-        self.tokens, self.top_k = row.shape
-        self.slots, self.experts = row.numel(), offsets.numel() - 1
-        self._io = C.byref(dq_expert_lists(offsets.data_ptr(), source.data_ptr(), row.data_ptr(), self.tokens,
-                                           self.top_k, self.experts))
+        self.tokens, self.top_k, self.slots, self.experts = tokens, top_k, tokens * top_k, experts
+        self._io = C.byref(dq_expert_lists(offsets.data_ptr(), source.data_ptr(), row.data_ptr(), tokens, top_k,
+                                           experts))
+        return self
 
 
 @functools.lru_cache(maxsize=256)
@@ -745,13 +758,11 @@ def expert_rows(ids, experts):
     need = _rows_bytes(tokens, top_k, experts)
     if not need:
         raise ValueError(f"{tokens} tokens of {top_k} choices among {experts} experts")
-    offsets = torch.empty(experts + 1, dtype=torch.int32, device=dev)
-    source = torch.empty(tokens * top_k, dtype=torch.int32, device=dev)
-    row = torch.empty((tokens, top_k), dtype=torch.int32, device=dev)
-    work = torch.empty(need, dtype=torch.uint8, device=dev)
+    offsets, source, row = ids.new_empty(experts + 1), ids.new_empty(tokens * top_k), ids.new_empty((tokens, top_k))
+    work = None if need <= 256 else ids.new_empty(need // 4)
     _call(dev, "dq_expert_rows", ids.data_ptr(), tokens, top_k, experts, offsets.data_ptr(), source.data_ptr(),
-          row.data_ptr(), work.data_ptr(), need)
-    return ExpertRows(offsets, source, row)
+          row.data_ptr(), _opt(work), need)
+    return ExpertRows.__new__(ExpertRows)._set(offsets, source, row, dev, tokens, top_k, experts)
 
 
 def _expert_rows(rows):
@@ -762,6 +773,10 @@ def _expert_rows(rows):
 
 def _row_matrix(t, what, n, dev, cols=None, dtype=None):
     """An operand [n, cols] whose rows are contiguous; its row stride."""
+    if isinstance(t, torch.Tensor) and t.dim() == 2 and t.size(0) == n and t.device == dev and t.is_contiguous() and \
+            (cols is None or t.size(1) == cols) and (dtype is None or t.dtype == dtype) and \
+            (t.dtype == torch.bfloat16 or t.dtype == torch.float32):
+        return t.size(1)                        # what almost all are
     _gpu(t, what)
     if t.dim() != 2 or t.size(0) != n or cols is not None and t.size(1) != cols or t.device != dev or \
             dtype is not None and t.dtype != dtype:
@@ -775,7 +790,7 @@ def _row_matrix(t, what, n, dev, cols=None, dtype=None):
 def _row_result(t, what, n, cols, x):
     """A caller's buffer [n, cols] for a result like ``x``, or a new one."""
     if t is None:
-        return torch.empty((n, cols), dtype=x.dtype, device=x.device), cols
+        return x.new_empty((n, cols)), cols
     return t, _row_matrix(t, what, n, x.device, cols, x.dtype)
 
 
@@ -812,8 +827,8 @@ def expert_matmul(x, w, rows, gather=False, out=None):
 
 
 @functools.lru_cache(maxsize=256)
-def _grad_bytes(tokens, top_k, experts, kind, inner, outer):
-    return lib().dq_expert_matmul_grad_bytes(tokens, top_k, experts, kind, inner, outer)
+def _grad_bytes(tokens, top_k, experts, kind, gather, inner, outer, kept):
+    return lib().dq_expert_matmul_grad_bytes(tokens, top_k, experts, kind, gather, inner, outer, kept)
 
 
 @_on_stream
@@ -823,7 +838,8 @@ def expert_matmul_grad(x, dout, rows, gather=None, dtype=None, out=None):
     (that of ``dout``, or fp32); zeros for an expert without rows.
 
     ``gather`` names which of ``"x"`` and ``"dout"`` holds tokens instead of rows, if one
-    does.  ``x`` may be a :class:`Kept8`, which is decoded as it is read."""
+    does.  ``x`` may be a :class:`Kept8`: it is decoded as it is read, or for long products
+    once into scratch memory."""
     dev = _expert_rows(rows).device
     if gather not in (None, "x", "dout"):
         raise ValueError(f"gather {gather!r}: expected None, 'x' or 'dout'")
@@ -843,11 +859,11 @@ def expert_matmul_grad(x, dout, rows, gather=None, dtype=None, out=None):
         raise TypeError(f"dtype {dtype}: expected {dout.dtype} or fp32")
     out = _result(out, (rows.experts, inner, outer), "out", dtype, dev)
     kind = _kind(dout)
-    need = _grad_bytes(rows.tokens, rows.top_k, rows.experts, kind, inner, outer)
-    work = torch.empty(need, dtype=torch.uint8, device=dev)
-    _call(dev, "dq_expert_matmul_grad", rows._io, at, xs, codes, exponents, dout.data_ptr(), ds,
-          GATHER_X if gather == "x" else GATHER_DOUT if gather else GATHER_NONE, out.data_ptr(), kind, _kind(out),
-          inner, outer, work.data_ptr(), need)
+    side = GATHER_X if gather == "x" else GATHER_DOUT if gather else GATHER_NONE
+    need = _grad_bytes(rows.tokens, rows.top_k, rows.experts, kind, side, inner, outer, codes is not None)
+    work = dout.new_empty(need, dtype=torch.uint8)
+    _call(dev, "dq_expert_matmul_grad", rows._io, at, xs, codes, exponents, dout.data_ptr(), ds, side,
+          out.data_ptr(), kind, _kind(out), inner, outer, work.data_ptr(), need)
     return out
 
 
@@ -900,8 +916,7 @@ def expert_act(u, gates, rows, act="swiglu", keep=False, dither=True, seed=1, rn
     kept = codes = exponents = key = None
     if keep:
         key = _keep_key(dither, seed, rnd, worker, site, dev)
-        kept = Kept8(torch.empty((rows.slots, columns), dtype=torch.int8, device=dev),
-                     torch.empty((rows.slots, (columns + 31) // 32), dtype=torch.uint8, device=dev), u.dtype)
+        kept = Kept8._made((rows.slots, columns), u)
         codes, exponents = kept.codes.data_ptr(), kept.exponents.data_ptr()
     _call(dev, "dq_expert_act", rows._io, number, u.data_ptr(), us, at, a.data_ptr(), as_, _kind(u), width, codes,
           exponents, key)
@@ -930,7 +945,7 @@ def expert_act_backward(u, da, gates, rows, act="swiglu", du=None, dgates=None, 
         raise ValueError(f"da: {da.size(1)} columns, expected {width}")
     g = _gates(gates, rows)
     du, dus = _row_result(du, "du", rows.slots, columns, da)
-    dgates = _result(dgates, gates.shape, "dgates", torch.float32, dev)
+    dgates = gates.new_empty(gates.shape) if dgates is None else _result(dgates, gates.shape, "dgates", torch.float32, dev)
     as_ = 0
     if again or a is not None:
         a, as_ = _row_result(a, "a", rows.slots, width, da)

@@ -535,7 +535,8 @@ typedef struct dq_expert_lists {
 
 /* The lists of d_ids[tokens][top_k] (of dq_route, or any; a token may name an
  * expert twice).  d_work: 256-byte aligned, dq_expert_rows_bytes (0 on bad
- * arguments); two calls in flight need one each. */
+ * arguments; 256 for short lists, where it may be NULL); two calls in flight need
+ * one each. */
 size_t dq_expert_rows_bytes(int64_t tokens, int32_t top_k, int32_t n_experts);
 dq_status dq_expert_rows(const int32_t *d_ids, int64_t tokens, int32_t top_k, int32_t n_experts,
                          int32_t *d_offsets, int32_t *d_source, int32_t *d_row, void *d_work,
@@ -556,12 +557,13 @@ dq_status dq_expert_matmul(const dq_expert_lists *lists, const void *d_x, int64_
 /* dw[e] = sum over e's rows of x[r]^T dy[r], [n_experts][inner][outer] of out_kind
  * (DQ_F32 or `kind`), zeros for an expert without rows.  One of x and dy may hold
  * tokens, gathered as above; x may be given as the codes of dq_keep8 (d_codes and
- * d_exponents, rows without gaps; d_x NULL), which are decoded as they are read.
- * Sums in fp32; the same call gives the same bits.  d_work: 256-byte aligned,
- * dq_expert_matmul_grad_bytes (0 on bad arguments). */
+ * d_exponents, rows without gaps; d_x NULL), which are decoded as they are read or,
+ * for long products, once into d_work.  Sums in fp32; the same call gives the same
+ * bits.  d_work: 256-byte aligned, dq_expert_matmul_grad_bytes (0 on bad arguments;
+ * kept: whether x comes as codes); two calls in flight need one each. */
 typedef enum dq_expert_gather { DQ_GATHER_NONE = 0, DQ_GATHER_X = 1, DQ_GATHER_DOUT = 2 } dq_expert_gather;
 size_t dq_expert_matmul_grad_bytes(int64_t tokens, int32_t top_k, int32_t n_experts, int32_t kind,
-                                   int64_t inner, int64_t outer);
+                                   int32_t gather, int64_t inner, int64_t outer, int32_t kept);
 dq_status dq_expert_matmul_grad(const dq_expert_lists *lists, const void *d_x, int64_t x_stride,
                                 const int8_t *d_codes, const uint8_t *d_exponents, const void *d_dy,
                                 int64_t dy_stride, int32_t gather, void *d_dw, int32_t kind,

@@ -174,7 +174,7 @@ def test_rows_refuses(lib):
         assert _rows(lib, **bad) == dq.DQ_EINVAL, bad
     for bad in (dict(ids=None), dict(offsets=None), dict(source=None), dict(row=None)):
         assert _rows(lib, **bad) == dq.DQ_ENULL, bad
-    for bad in (dict(work=None), dict(work=5 * FAKE + 128), dict(size=255), dict(tokens=100000, size=1024)):
+    for bad in (dict(tokens=100000, work=None), dict(work=5 * FAKE + 128), dict(size=255), dict(tokens=100000, size=1024)):
         assert _rows(lib, **bad) == dq.DQ_EWORKSPACE, bad
     assert lib.dq_expert_rows_bytes(8, 2, 4) == 256 and lib.dq_expert_rows_bytes(1 << 30, 2, 4) == 0
     assert lib.dq_expert_rows_bytes(8, 0, 4) == 0 and lib.dq_expert_rows_bytes(8, 2, 1025) == 0
@@ -213,10 +213,14 @@ def test_matmul_grad_null_and_workspace(lib):
     for bad in (dict(work=None), dict(work=7 * FAKE + 128), dict(size=255), dict(tokens=100000, size=4096)):
         assert _grad(lib, **bad) == dq.DQ_EWORKSPACE, bad
     size = lib.dq_expert_matmul_grad_bytes
-    assert size(8, 2, 4, dq.BF16, 32, 16) == 256 and size(100000, 2, 4, dq.BF16, 32, 16) > 256
-    for bad in ((-1, 2, 4, 0, 32, 16), (8, 17, 4, 0, 32, 16), (8, 2, 0, 0, 32, 16), (8, 2, 4, 2, 32, 16), (8, 2, 4, 0, 0, 16),
-                (8, 2, 4, 0, 32, 1 << 25)):
-        assert size(*bad) == 0
+    assert size(8, 2, 4, dq.BF16, 0, 32, 16, 0) == 256 and size(100000, 2, 4, dq.BF16, 0, 32, 16, 0) > 256
+    # long products from codes hold x, of the tokens or of all rows
+    for gather, rows in ((0, 2000), (1, 1000), (2, 2000)):
+        assert size(1000, 2, 16, dq.BF16, gather, 2048, 1024, 1) == 256 + rows * 2048 * 2
+    assert size(8, 2, 4, dq.BF16, 1, 32, 16, 1) == 256
+    for bad in ((-1, 2, 4, 0, 0, 32, 16), (8, 17, 4, 0, 0, 32, 16), (8, 2, 0, 0, 0, 32, 16), (8, 2, 4, 2, 0, 32, 16),
+                (8, 2, 4, 0, 3, 32, 16), (8, 2, 4, 0, -1, 32, 16), (8, 2, 4, 0, 0, 0, 16), (8, 2, 4, 0, 0, 32, 1 << 25)):
+        assert size(*bad, 0) == 0
 
 
 @pytest.mark.parametrize("bad", [

@@ -372,7 +372,7 @@ def near(got, want, bound, dtype):
 
 # every tile: from few rows an expert to many, narrow and wide, whole steps and not
 LARGE = [(3, 2, 4, 1024, 520), (200, 2, 8, 1032, 264), (400, 2, 8, 512, 1040), (2048, 2, 8, 264, 520), (4100, 2, 4, 320, 776),
-         (1500, 1, 2, 96, 72), (9000, 2, 3, 40, 24), (700, 4, 5, 333, 1029)]
+         (1500, 1, 2, 96, 72), (9000, 2, 3, 40, 24), (700, 4, 5, 333, 1029), (60, 2, 33, 1024, 1000)]
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
