@@ -18,14 +18,14 @@ __device__ __forceinline__ void product_tile(const ExpertProductArgs &a, const R
     typedef typename C::T T;
     const bool mine = acc.m0() < t.rows && n0 + acc.n0() < a.N;
     Along<C, C::BM, LA> x;
-    x.start(static_cast<const T *>(a.x) + (a.gather ? 0 : t.first * a.xs) + from, inner, [&](int i) {
+    x.start(static_cast<const T *>(a.x) + (a.gather ? 0 : t.first * a.xs) + from, a.K, inner, [&](int i) {
         i = min(i, t.rows - 1);
         return a.gather ? row_at(a.l, t.first + i, 1, a.xs) : i * a.xs;
     });
     const T *w = static_cast<const T *>(a.w) + t.e * a.we;
     if constexpr (TURNED) {
         Along<C, C::BN, LB> b;
-        b.start(w + n0 * a.ws + from, inner, [&](int i) { return min(i, a.N - 1 - n0) * a.ws; });
+        b.start(w + n0 * a.ws + from, a.K, inner, [&](int i) { return min(i, a.N - 1 - n0) * a.ws; });
         multiply<C>(lds, x, b, inner, mine, acc);
     } else {
         Across<C, C::BN, LB, false> b(RowsDown<false>(a.ws, from));

@@ -44,7 +44,7 @@ typedef Tiling<uint16_t, 128, 128, 2, 2, 128, 2> TileAny;
 typedef Tiling<float, 128, 128, 2, 2, 64, 4> TileMidF32;
 typedef Tiling<float, 64, 64, 2, 2, 64, 4> TileSmallF32;
 typedef Tiling<float, 16, 64, 1, 1, 64, 4> TileFewF32;
-typedef Tiling<float, 64, 64, 2, 1, 128, 2> TileAnyF32;
+typedef Tiling<float, 64, 64, 2, 2, 128, 2> TileAnyF32;
 typedef Tiling<uint16_t, 16, 64, 1, 1, 128, 2> TileFewAny;
 typedef Tiling<float, 16, 64, 1, 1, 128, 2> TileFewAnyF32;
 typedef Tiling<uint16_t, 64, 64, 2, 2, 64, 4> TileNarrow;
@@ -184,22 +184,37 @@ __device__ __forceinline__ bool find_tile(const ExpertLists &l, int bm, int nt, 
 }
 
 // 16 bytes of elements from p (at any alignment: the hardware splits such loads), of
-// which `have` are there, perhaps none.
-template <typename T>
-__device__ __forceinline__ u32x4 load_some(const T *p, int have) {
+// which `have` are before the row's end, perhaps none, and none if not `there`; the others
+// are 0.  kWhole: all are before it.  kEdge: one load without a branch, of the row's last
+// 16 bytes where that is less, moved down (a load under a condition is waited for where
+// the branches join).  kTiny: rows shorter than 16 bytes.
+constexpr int kWhole = 0, kEdge = 1, kTiny = 2;
+template <int HOW, typename T>
+__device__ __forceinline__ u32x4 load_some(const T *p, int have, bool there) {
     constexpr int kMost = 16 / (int)sizeof(T), kWord = 4 / (int)sizeof(T);
     u32x4 v = {0, 0, 0, 0};
-    if (have >= kMost) {
-        __builtin_memcpy(&v, p, 16);
-        return v;
-    }
+    if constexpr (HOW == kTiny) {
 #pragma unroll
-    for (int j = 0; j < kMost; j++) {
-        if (j >= have) continue;
-        if constexpr (sizeof(T) == 4)
-            v[j] = __builtin_bit_cast(uint32_t, p[j]);
-        else
-            v[j / kWord] |= (uint32_t)(typename std::make_unsigned<T>::type)p[j] << 32 / kWord * (j % kWord);
+        for (int j = 0; j < kMost; j++) {
+            if (!there || j >= have) continue;
+            if constexpr (sizeof(T) == 4)
+                v[j] = __builtin_bit_cast(uint32_t, p[j]);
+            else
+                v[j / kWord] |= (uint32_t)(typename std::make_unsigned<T>::type)p[j] << 32 / kWord * (j % kWord);
+        }
+    } else if constexpr (HOW == kWhole) {
+        u32x4 w;
+        __builtin_memcpy(&w, p, 16);
+        v = there ? w : v;
+    } else {
+        uint64_t q[2];
+        __builtin_memcpy(q, p + (have < kMost ? have - kMost : 0), 16);
+        const uint32_t bytes = have < kMost ? (uint32_t)(kMost - have) * sizeof(T) : 0, bits = bytes % 8 * 8;
+        const uint64_t lo = bytes & 8 ? q[1] : q[0], hi = bytes & 8 ? 0 : q[1];
+        const bool some = there && have > 0;
+        q[0] = some ? lo >> bits | (hi << 1) << (63 - bits) : 0;
+        q[1] = some ? hi >> bits : 0;
+        v = u32x4{(uint32_t)q[0], (uint32_t)(q[0] >> 32), (uint32_t)q[1], (uint32_t)(q[1] >> 32)};
     }
     return v;
 }
@@ -242,6 +257,8 @@ struct Along {
     Stream from;                       // kAsync
     uint32_t off[kAsyncLoad ? kPer : 1];
     const T *p[kAsyncLoad ? 1 : kPer];  // else
+    uint32_t none;                     // a bit for every chunk of a row that starts nowhere
+    bool tiny;
     struct Regs {
         u32x4 v[kAsyncLoad ? 1 : kPer];
     };
@@ -250,32 +267,45 @@ struct Along {
     static __device__ __forceinline__ int swap(int chunk, int row) {
         return kRowChunks == 8 ? chunk ^ (row & 7) : chunk ^ (row >> 1 & 3);
     }
-    // row(i): where the tile's row i starts, from base (below 0: nowhere)
+    // row(i): where the tile's row i starts, from base (below 0: nowhere); of rows of
+    // `whole` elements the next `inner`
     template <class Row>
-    __device__ __forceinline__ void start(const T *base, int inner, Row row) {
+    __device__ __forceinline__ void start(const T *base, int whole, int inner, Row row) {
         K = inner;
+        tiny = whole < C::kChunk;
+        none = 0;
         const int r0 = C::tid() / kRowChunks;
         kc = swap(C::tid() % kRowChunks, r0) * C::kChunk;
         if constexpr (kAsyncLoad) from.at(base);
 #pragma unroll
         for (int i = 0; i < kPer; i++) {
             const int64_t at = row(r0 + i * (C::kThreads / kRowChunks));
-            if constexpr (kAsyncLoad)
+            if constexpr (kAsyncLoad) {
                 off[i] = at < 0 ? kNowhere : (uint32_t)((at + kc) * sizeof(T));
-            else
-                p[i] = at < 0 ? nullptr : base + at + kc;
+            } else {
+                p[i] = base + (at < 0 ? 0 : at) + kc;
+                none |= (uint32_t)(at < 0) << i;
+            }
         }
+    }
+    template <int HOW>
+    __device__ __forceinline__ void to_regs(int k0, Regs &r) {
+#pragma unroll
+        for (int i = 0; i < kPer; i++) r.v[i] = load_some<HOW>(p[i] + k0, K - k0 - kc, !(none >> i & 1));
     }
     __device__ __forceinline__ void ahead(int, Entries &) const {}
     __device__ __forceinline__ void issue(char *buf, int k0, const Entries &, Regs &r) {
-        const int have = K - k0 - kc;
+        if constexpr (kAsyncLoad) {
 #pragma unroll
-        for (int i = 0; i < kPer; i++) {
-            if constexpr (kAsyncLoad)
-                from.to_lds((int64_t)k0 * sizeof(T), have > 0 ? off[i] : kNowhere,
+            for (int i = 0; i < kPer; i++)
+                from.to_lds((int64_t)k0 * sizeof(T), K - k0 > kc ? off[i] : kNowhere,
                             buf + (64 * C::wave() + i * C::kThreads) * 16);
-            else
-                r.v[i] = load_some(p[i] + k0, p[i] ? have : 0);
+        } else if (K - k0 >= C::BK) {
+            to_regs<kWhole>(k0, r);
+        } else if (!tiny) {
+            to_regs<kEdge>(k0, r);
+        } else {
+            to_regs<kTiny>(k0, r);
         }
     }
     __device__ __forceinline__ void commit(char *buf, const Regs &r) {
@@ -301,9 +331,10 @@ struct Across {
     static constexpr int kRow = COLS * (int)sizeof(T), kBytes = C::BK * kRow, kUnits = COLS / 16;
     static constexpr bool kFromKept = L == kKept;
     static constexpr int kPieces = kFromKept ? C::BK * kUnits : kBytes / 16;
-    static constexpr int kPer = kPieces / C::kThreads, kPerRow = kPieces / C::BK, BK = C::BK;
+    static constexpr bool kSome = kPieces < C::kThreads;     // the last waves have none
+    static constexpr int kPer = kSome ? 1 : kPieces / C::kThreads, kPerRow = kPieces / C::BK, BK = C::BK;
     static constexpr bool kAsyncLoad = L == kAsync;
-    static_assert(kPieces % C::kThreads == 0 && kUnits % 4 == 0, "whole pieces");
+    static_assert((kPieces % C::kThreads == 0 || (kSome && !kAsyncLoad && kPieces % 64 == 0)) && kUnits % 4 == 0, "whole pieces");
     Stream from;                       // kAsync
     const T *base;                     // kAny
     const int8_t *codes;               // kKept
@@ -359,7 +390,7 @@ struct Across {
                     e.at[i][j] = rows.shared_entry(k0 + row + j + i * (C::kThreads / kPerRow));
         } else if constexpr (GATHER || !kAsyncLoad) {
 #pragma unroll
-            for (int i = 0; i < kPer; i++) e.at[i][0] = rows.entry(k0 + piece_row(i));
+            for (int i = 0; i < kPer; i++) e.at[i][0] = rows.entry(min(k0 + piece_row(i), K - 1));
         }
     }
     static __device__ __forceinline__ uint32_t entry_of(const Entries &e, int i) {
@@ -370,11 +401,30 @@ struct Across {
             v ^= (e.at[i][j - 1] ^ e.at[i][j]) & -(uint32_t)((threadIdx.x & 63) / kPerRow >= j);
         return v;
     }
-    __device__ __forceinline__ void issue(char *buf, int k0, const Entries &e, Regs &r) {
+    template <int HOW>
+    __device__ __forceinline__ void to_regs(int k0, const Entries &e, Regs &r) {
 #pragma unroll
         for (int i = 0; i < kPer; i++) {
+            if (kSome && C::tid() >= kPieces) continue;
             const int col = piece_col(i);
-            if constexpr (L == kAsync) {
+            int64_t off = rows.offset(e.at[i][0]);
+            const bool there = off >= 0 && k0 + piece_row(i) < K;
+            off = off < 0 ? 0 : off;
+            if constexpr (kFromKept) {
+                // zeros of a row past the end are not to meet another block's infinity
+                const uint8_t ex = exponents[off * ((N + 31) / 32) + min(col, N - 1) / 32];
+                r.ex[i] = there ? ex : 127;
+                r.v[i] = load_some<HOW>(codes + off * N + col, N - col, there);
+            } else {
+                r.v[i] = load_some<HOW>(base + off + col, N - col, there);
+            }
+        }
+    }
+    __device__ __forceinline__ void issue(char *buf, int k0, const Entries &e, Regs &r) {
+        if constexpr (kAsyncLoad) {
+#pragma unroll
+            for (int i = 0; i < kPer; i++) {
+                const int col = piece_col(i);
                 // rows that are not gathered: the base moves, the offsets stay
                 const int64_t moved = GATHER ? 0 : (int64_t)(rows.first + k0) * rows.stride * (int64_t)sizeof(T);
                 const uint32_t off = GATHER ? rows.near_offset(entry_of(e, GATHER ? i : 0), sizeof(T))
@@ -382,21 +432,13 @@ struct Across {
                 const bool there = off < kNowhere && col < N && k0 + piece_row(i) < K;
                 from.to_lds(moved, there ? off + (uint32_t)(col * sizeof(T)) : kNowhere,
                             buf + (64 * C::wave() + i * C::kThreads) * 16);
-                continue;
             }
-            const int64_t off = rows.offset(e.at[i][0]);
-            const bool there = off >= 0 && col < N && k0 + piece_row(i) < K;
-            if constexpr (L == kAny) {
-                r.v[i] = load_some(base + off + col, there ? N - col : 0);
-            } else if constexpr (kFromKept) {
-                r.v[i] = u32x4{0, 0, 0, 0};
-                r.ex[i] = 127;
-                if (there) {
-                    r.ex[i] = exponents[off * ((N + 31) / 32) + col / 32];
-                    const int8_t *c = codes + off * N + col;
-                    r.v[i] = load_some(c, N - col);
-                }
-            }
+        } else if (N - col0 >= COLS) {
+            to_regs<kWhole>(k0, e, r);
+        } else if (N >= (kFromKept ? 16 : C::kChunk)) {
+            to_regs<kEdge>(k0, e, r);
+        } else {
+            to_regs<kTiny>(k0, e, r);
         }
     }
     __device__ __forceinline__ void commit(char *buf, const Regs &r) {
@@ -407,6 +449,7 @@ struct Across {
         } else if constexpr (kFromKept) {
 #pragma unroll
             for (int i = 0; i < kPer; i++) {
+                if (kSome && C::tid() >= kPieces) continue;
                 const int k = piece_row(i), unit = (C::tid() + i * C::kThreads) % kPerRow;
                 u32x4 *to = reinterpret_cast<u32x4 *>(buf + k * kRow + (unit ^ swap(k)) * 16 * sizeof(T));
                 const float scale = __uint_as_float((uint32_t)r.ex[i] << 23);
@@ -581,8 +624,8 @@ __device__ __forceinline__ void all_waves() {
         asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(LEFT) : "memory");
 }
 
-// Step k0 into LDS: by loads that land there, or from registers, whose next step is then
-// loaded.  Past the end zeros are stored.
+// Step k0 into LDS: by loads that land there, or from registers, which then take the step
+// two after it.  Past the end zeros are stored.
 template <class Op>
 __device__ __forceinline__ void fill(Op &op, char *buf, int k0, typename Op::Entries &e, typename Op::Regs &r) {
     if constexpr (Op::kAsyncLoad) {
@@ -590,70 +633,71 @@ __device__ __forceinline__ void fill(Op &op, char *buf, int k0, typename Op::Ent
         op.ahead(k0 + Op::BK, e);
     } else {
         op.commit(buf, r);
-        op.issue(nullptr, k0 + Op::BK, e, r);
-        op.ahead(k0 + 2 * Op::BK, e);
+        op.issue(nullptr, k0 + 2 * Op::BK, e, r);
+        op.ahead(k0 + 3 * Op::BK, e);
     }
 }
 
-// acc += A B over `inner`, an operand at least through registers.  Two steps in LDS; the
-// barrier stands in the middle of a step's products, when the step after it is in LDS and
-// the second half's operands are in registers: LDS reads run beside the other half's
-// products, loads beside a whole step's.
+// acc += A B over `inner`, an operand at least through registers, where two steps are on
+// their way; two more are in LDS.  The barrier stands in the middle of a step's products,
+// when the step after it is in LDS and the second half's operands are in registers: LDS
+// reads run beside the other half's products, loads beside two steps'.
 template <class C, class A, class B>
 __device__ __forceinline__ void multiply_halves(char *lds, A &a, B &b, int inner, Acc<C> &acc) {
     constexpr int kStep = C::kBytesA + C::kBytesB;
+    // loads into registers are waited for where they are used
+    constexpr int kLeft = A::kAsyncLoad || B::kAsyncLoad ? 0 : 63;
     if (inner <= 0) return;
     const int steps = (inner + C::BK - 1) / C::BK;
-    typename A::Entries ea;
-    typename B::Entries eb;
-    typename A::Regs ra;
-    typename B::Regs rb;
-    {
-        typename A::Entries ea1;
-        typename B::Entries eb1;
-        typename A::Regs ra1;
-        typename B::Regs rb1;
-        a.ahead(0, ea);
-        b.ahead(0, eb);
-        a.ahead(C::BK, ea1);
-        b.ahead(C::BK, eb1);
-        a.issue(lds, 0, ea, ra);
-        b.issue(lds + C::kBytesA, 0, eb, rb);
-        a.issue(lds + kStep, C::BK, ea1, ra1);
-        b.issue(lds + kStep + C::kBytesA, C::BK, eb1, rb1);
-        a.ahead(2 * C::BK, ea);
-        b.ahead(2 * C::BK, eb);
-        a.commit(lds, ra);
-        b.commit(lds + C::kBytesA, rb);
-        a.commit(lds + kStep, ra1);
-        b.commit(lds + kStep + C::kBytesA, rb1);
+    typename A::Entries ea[2];
+    typename B::Entries eb[2];
+    typename A::Regs ra[2];
+    typename B::Regs rb[2];
+    const auto entries = [&](int i, int t) {
+        a.ahead(t * C::BK, ea[i]);
+        b.ahead(t * C::BK, eb[i]);
+    };
+    entries(0, 0);
+    entries(1, 1);
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+        a.issue(lds + i * kStep, i * C::BK, ea[i], ra[i]);
+        b.issue(lds + i * kStep + C::kBytesA, i * C::BK, eb[i], rb[i]);
     }
-    if constexpr (!A::kAsyncLoad) {
-        a.issue(nullptr, 2 * C::BK, ea, ra);
-        a.ahead(3 * C::BK, ea);
+    entries(0, 2);
+    entries(1, 3);
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+        a.commit(lds + i * kStep, ra[i]);
+        b.commit(lds + i * kStep + C::kBytesA, rb[i]);
+        if constexpr (!A::kAsyncLoad) a.issue(nullptr, (2 + i) * C::BK, ea[i], ra[i]);
+        if constexpr (!B::kAsyncLoad) b.issue(nullptr, (2 + i) * C::BK, eb[i], rb[i]);
     }
-    if constexpr (!B::kAsyncLoad) {
-        b.issue(nullptr, 2 * C::BK, eb, rb);
-        b.ahead(3 * C::BK, eb);
-    }
-    all_waves<C, 0>();
+    // from here: entries of the staged operands' next step, of the others' step t + 2
+    if constexpr (!A::kAsyncLoad) a.ahead(4 * C::BK, ea[0]);
+    if constexpr (!B::kAsyncLoad) b.ahead(4 * C::BK, eb[0]);
+    all_waves<C, kLeft>();
     typename Acc<C>::Half first, second;
     first.template read<A, B>(lds, 0);
-    for (int t = 0; t < steps; t++) {
+    const auto step = [&](int t, typename A::Regs &va, typename B::Regs &vb) {
         char *now = lds + (t & 1) * kStep, *next = lds + (~t & 1) * kStep;
         second.template read<A, B>(now, 1);
         acc.add(first);
         __builtin_amdgcn_sched_barrier(0);
-        all_waves<C, 0>();
+        all_waves<C, kLeft>();
         __builtin_amdgcn_sched_barrier(0);
         if (t + 1 < steps) {
             first.template read<A, B>(next, 0);
             const int k = (t + 2) * C::BK;
-            fill(a, now, k, ea, ra);
-            fill(b, now + C::kBytesA, k, eb, rb);
+            fill(a, now, k, ea[0], va);
+            fill(b, now + C::kBytesA, k, eb[0], vb);
         }
         acc.add(second);
         __builtin_amdgcn_sched_barrier(0);
+    };
+    for (int t = 0; t < steps; t += 2) {
+        step(t, ra[0], rb[0]);
+        if (t + 1 < steps) step(t + 1, ra[1], rb[1]);
     }
 }
 
