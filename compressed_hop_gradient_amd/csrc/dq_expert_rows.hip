@@ -131,35 +131,37 @@ __global__ __launch_bounds__(kRowsThreads) void k_rows_place(ExpertRowsArgs a) {
 // token's rows in flight.
 template <bool F32, bool RES, bool EVEN>
 __global__ __launch_bounds__(256) void k_expert_sum(ExpertSumArgs a, int lanes) {
-    const int64_t token = (int64_t)blockIdx.x * (256 / lanes) + threadIdx.x / lanes;
-    if (token >= a.l.tokens) return;
-    const int32_t *rows = a.l.row + token * a.l.k;
-    by_eights<EVEN>((threadIdx.x % lanes) * 8, lanes * 8, a.width, [&](auto full, int c) {
-        constexpr bool kFull = decltype(full)::value;
-        const int have = a.width - c;
-        float s[8];
-        if constexpr (RES) {
-            load_eight<F32, kFull>(a.residual, token * a.rs + c, have, s);
-        } else {
+    const int each = 256 / lanes;
+    for (int64_t token = (int64_t)blockIdx.x * each + threadIdx.x / lanes; token < a.l.tokens;
+         token += (int64_t)gridDim.x * each) {
+        const int32_t *rows = a.l.row + token * a.l.k;
+        by_eights<EVEN>((threadIdx.x % lanes) * 8, lanes * 8, a.width, [&](auto full, int c) {
+            constexpr bool kFull = decltype(full)::value;
+            const int have = a.width - c;
+            float s[8];
+            if constexpr (RES) {
+                load_eight<F32, kFull>(a.residual, token * a.rs + c, have, s);
+            } else {
 #pragma unroll
-            for (int q = 0; q < 8; q++) s[q] = 0.0f;
-        }
-        for (int j0 = 0; j0 < a.l.k; j0 += 4) {
-            float v[4][8];
-            bool there[4];
-#pragma unroll
-            for (int j = 0; j < 4; j++) {
-                const uint32_t r = j0 + j < a.l.k ? (uint32_t)rows[j0 + j] : 0xFFFFFFFFu;
-                there[j] = r < (uint32_t)a.l.slots;
-                load_eight<F32, kFull>(a.y, (there[j] ? (int64_t)r : 0) * a.ys + c, have, v[j]);
+                for (int q = 0; q < 8; q++) s[q] = 0.0f;
             }
+            for (int j0 = 0; j0 < a.l.k; j0 += 4) {
+                float v[4][8];
+                bool there[4];
 #pragma unroll
-            for (int j = 0; j < 4; j++)
+                for (int j = 0; j < 4; j++) {
+                    const uint32_t r = j0 + j < a.l.k ? (uint32_t)rows[j0 + j] : 0xFFFFFFFFu;
+                    there[j] = r < (uint32_t)a.l.slots;
+                    load_eight<F32, kFull>(a.y, (there[j] ? (int64_t)r : 0) * a.ys + c, have, v[j]);
+                }
 #pragma unroll
-                for (int q = 0; q < 8; q++) s[q] += there[j] ? v[j][q] : 0.0f;
-        }
-        store_eight<F32, kFull>(a.out, token * a.os + c, have, s);
-    });
+                for (int j = 0; j < 4; j++)
+#pragma unroll
+                    for (int q = 0; q < 8; q++) s[q] += there[j] ? v[j][q] : 0.0f;
+            }
+            store_eight<F32, kFull>(a.out, token * a.os + c, have, s);
+        });
+    }
 }
 
 // ---- activation ---------------------------------------------------------------
@@ -186,31 +188,32 @@ template <bool F32, bool GATED, bool EVEN, bool KEEP>
 __global__ __launch_bounds__(256) void k_act(ExpertActArgs a, int lanes) {
     const int rows = clampi(a.l.offsets[a.l.E], 0, a.l.slots), U = GATED ? 2 * a.width : a.width;
     const uint32_t round = KEEP ? a.key.round + (a.key.d_round ? *a.key.d_round : 0) : 0;
-    const int64_t row = (int64_t)blockIdx.x * (256 / lanes) + threadIdx.x / lanes;
-    if (row >= rows) return;
-    const uint32_t slot = (uint32_t)a.l.source[row];
-    const float gate = slot < (uint32_t)a.l.slots ? a.gates[slot] : 0.0f;
-    by_eights<EVEN>((threadIdx.x % lanes) * 8, lanes * 8, a.width, [&](auto full, int c) {
-        constexpr bool kFull = decltype(full)::value;
-        const int have = a.width - c;
-        float g[8], v[8], o[8];
-        load_eight<F32, kFull>(a.u, row * a.us + c, have, g);
-        if (GATED) load_eight<F32, kFull>(a.u, row * a.us + a.width + c, have, v);
+    const int each = 256 / lanes;
+    for (int64_t row = (int64_t)blockIdx.x * each + threadIdx.x / lanes; row < rows; row += (int64_t)gridDim.x * each) {
+        const uint32_t slot = (uint32_t)a.l.source[row];
+        const float gate = slot < (uint32_t)a.l.slots ? a.gates[slot] : 0.0f;
+        by_eights<EVEN>((threadIdx.x % lanes) * 8, lanes * 8, a.width, [&](auto full, int c) {
+            constexpr bool kFull = decltype(full)::value;
+            const int have = a.width - c;
+            float g[8], v[8], o[8];
+            load_eight<F32, kFull>(a.u, row * a.us + c, have, g);
+            if (GATED) load_eight<F32, kFull>(a.u, row * a.us + a.width + c, have, v);
 #pragma unroll
-        for (int q = 0; q < 8; q++) o[q] = gate * (GATED ? g[q] * sigmoid(g[q]) * v[q] : relu(g[q]));
-        store_eight<F32, kFull>(a.a, row * a.as + c, have, o);
-        if constexpr (KEEP && kFull) {
-            const int64_t blocks = U / 32;
+            for (int q = 0; q < 8; q++) o[q] = gate * (GATED ? g[q] * sigmoid(g[q]) * v[q] : relu(g[q]));
+            store_eight<F32, kFull>(a.a, row * a.as + c, have, o);
+            if constexpr (KEEP && kFull) {
+                const int64_t blocks = U / 32;
 #pragma unroll
-            for (int half = 0; half < (GATED ? 2 : 1); half++) {
-                const int col = half * a.width + c;
-                uint32_t w[4], exponent;
-                keep_dithers<true>(row * U + col, a.key, round, w);
-                store_codes<true>(a.codes + row * U + col, 8, keep_eight(half ? v : g, w, exponent));
-                if ((threadIdx.x & 3) == 0) a.exponents[row * blocks + col / 32] = (uint8_t)exponent;
+                for (int half = 0; half < (GATED ? 2 : 1); half++) {
+                    const int col = half * a.width + c;
+                    uint32_t w[4], exponent;
+                    keep_dithers<true>(row * U + col, a.key, round, w);
+                    store_codes<true>(a.codes + row * U + col, 8, keep_eight(half ? v : g, w, exponent));
+                    if ((threadIdx.x & 3) == 0) a.exponents[row * blocks + col / 32] = (uint8_t)exponent;
+                }
             }
-        }
-    });
+        });
+    }
 }
 
 // From the kept codes or from u itself: du, the activation again, and the gates'
@@ -218,60 +221,62 @@ __global__ __launch_bounds__(256) void k_act(ExpertActArgs a, int lanes) {
 template <bool F32, bool GATED, bool EVEN, bool KEPT>
 __global__ __launch_bounds__(256) void k_act_backward(ExpertActArgs a, int lanes) {
     const int rows = clampi(a.l.offsets[a.l.E], 0, a.l.slots), U = GATED ? 2 * a.width : a.width;
-    const int64_t row = (int64_t)blockIdx.x * (256 / lanes) + threadIdx.x / lanes;
-    if (row >= a.l.slots) return;
-    const uint32_t slot = (uint32_t)a.l.source[row];
-    const bool known = slot < (uint32_t)a.l.slots;
-    const int lane = threadIdx.x % lanes;
-    if (row >= rows) {
-        if (a.dgates && known && lane == 0) a.dgates[slot] = 0.0f;
-        return;
-    }
-    const float gate = known ? a.gates[slot] : 0.0f;
-    const int64_t blocks = (U + 31) / 32;
-    float sum = 0.0f;
-    by_eights<EVEN>(lane * 8, lanes * 8, a.width, [&](auto full, int c) {
-        constexpr bool kFull = decltype(full)::value;
-        const int have = a.width - c;
-        const auto columns = [&](int col, float *v) {
-            if constexpr (!KEPT) {
-                load_eight<F32, kFull>(a.u, row * a.us + col, have, v);
-            } else {
-                // of one block, or (the value half of an odd width) of two
-                const uint8_t *e = a.exponents + row * blocks;
-                const float s0 = kept_scale(e[col / 32]);
-                const float s1 = EVEN ? s0 : kept_scale(e[(col + (have < 8 ? have : 8) - 1) / 32]);
-                const uint2 w = load_codes<kFull>(a.codes + row * U + col, have);
-#pragma unroll
-                for (int q = 0; q < 8; q++)
-                    v[q] = kept_value(q < 4 ? w.x : w.y, q & 3, EVEN || col % 32 + q < 32 ? s0 : s1);
-            }
-        };
-        float g[8], v[8], d[8], dg[8], dv[8], o[8];
-        columns(c, g);
-        if (GATED) columns(a.width + c, v);
-        load_eight<F32, kFull>(a.da, row * a.das + c, have, d);
-#pragma unroll
-        for (int q = 0; q < 8; q++) {
-            float h;
-            if (GATED) {
-                const float s = sigmoid(g[q]), silu = g[q] * s, t = gate * d[q];
-                h = silu * v[q];
-                dv[q] = t * silu;
-                dg[q] = t * v[q] * s * (1.0f + g[q] * (1.0f - s));
-            } else {
-                h = relu(g[q]);
-                dg[q] = relu_back(g[q], gate * d[q]);
-            }
-            o[q] = gate * h;
-            sum += kFull || q < have ? d[q] * h : 0.0f;
+    const int each = 256 / lanes;
+    for (int64_t row = (int64_t)blockIdx.x * each + threadIdx.x / lanes; row < a.l.slots;
+         row += (int64_t)gridDim.x * each) {
+        const uint32_t slot = (uint32_t)a.l.source[row];
+        const bool known = slot < (uint32_t)a.l.slots;
+        const int lane = threadIdx.x % lanes;
+        if (row >= rows) {
+            if (a.dgates && known && lane == 0) a.dgates[slot] = 0.0f;
+            continue;
         }
-        store_eight<F32, kFull>(a.du, row * a.dus + c, have, dg);
-        if (GATED) store_eight<F32, kFull>(a.du, row * a.dus + a.width + c, have, dv);
-        if (a.a) store_eight<F32, kFull>(a.a, row * a.as + c, have, o);
-    });
-    for (int d = lanes / 2; d > 0; d /= 2) sum += __shfl_xor(sum, d, 64);
-    if (a.dgates && known && lane == 0) a.dgates[slot] = sum;
+        const float gate = known ? a.gates[slot] : 0.0f;
+        const int64_t blocks = (U + 31) / 32;
+        float sum = 0.0f;
+        by_eights<EVEN>(lane * 8, lanes * 8, a.width, [&](auto full, int c) {
+            constexpr bool kFull = decltype(full)::value;
+            const int have = a.width - c;
+            const auto columns = [&](int col, float *v) {
+                if constexpr (!KEPT) {
+                    load_eight<F32, kFull>(a.u, row * a.us + col, have, v);
+                } else {
+                    // of one block, or (the value half of an odd width) of two
+                    const uint8_t *e = a.exponents + row * blocks;
+                    const float s0 = kept_scale(e[col / 32]);
+                    const float s1 = EVEN ? s0 : kept_scale(e[(col + (have < 8 ? have : 8) - 1) / 32]);
+                    const uint2 w = load_codes<kFull>(a.codes + row * U + col, have);
+#pragma unroll
+                    for (int q = 0; q < 8; q++)
+                        v[q] = kept_value(q < 4 ? w.x : w.y, q & 3, EVEN || col % 32 + q < 32 ? s0 : s1);
+                }
+            };
+            float g[8], v[8], d[8], dg[8], dv[8], o[8];
+            columns(c, g);
+            if (GATED) columns(a.width + c, v);
+            load_eight<F32, kFull>(a.da, row * a.das + c, have, d);
+#pragma unroll
+            for (int q = 0; q < 8; q++) {
+                float h;
+                if (GATED) {
+                    const float s = sigmoid(g[q]), silu = g[q] * s, t = gate * d[q];
+                    h = silu * v[q];
+                    dv[q] = t * silu;
+                    dg[q] = t * v[q] * s * (1.0f + g[q] * (1.0f - s));
+                } else {
+                    h = relu(g[q]);
+                    dg[q] = relu_back(g[q], gate * d[q]);
+                }
+                o[q] = gate * h;
+                sum += kFull || q < have ? d[q] * h : 0.0f;
+            }
+            store_eight<F32, kFull>(a.du, row * a.dus + c, have, dg);
+            if (GATED) store_eight<F32, kFull>(a.du, row * a.dus + a.width + c, have, dv);
+            if (a.a) store_eight<F32, kFull>(a.a, row * a.as + c, have, o);
+        });
+        for (int d = lanes / 2; d > 0; d /= 2) sum += __shfl_xor(sum, d, 64);
+        if (a.dgates && known && lane == 0) a.dgates[slot] = sum;
+    }
 }
 
 // Threads to a row of so many columns.
@@ -281,7 +286,11 @@ int lanes_for(int width, int least) {
     return lanes;
 }
 
-dim3 row_grid(int64_t rows, int lanes) { return dim3((unsigned)((rows + 256 / lanes - 1) / (256 / lanes))); }
+// Blocks that go over so many rows once, up to 2^22 (a launch has below 2^32 threads).
+dim3 row_grid(int64_t rows, int lanes) {
+    const int64_t want = (rows + 256 / lanes - 1) / (256 / lanes);
+    return dim3((unsigned)(want < (1 << 22) ? want : (1 << 22)));
+}
 
 template <bool F32, bool GATED>
 hipError_t act_as(const ExpertActArgs &a, hipStream_t s) {

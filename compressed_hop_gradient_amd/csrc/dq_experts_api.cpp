@@ -10,7 +10,7 @@ using namespace dq;
 
 namespace {
 
-constexpr int64_t kMostSlots = ((int64_t)1 << 31) - 1;
+constexpr int64_t kMostSlots = (int64_t)1 << 30;
 constexpr int64_t kMostWidth = (int64_t)1 << 24;
 constexpr int64_t kMostStride = (int64_t)1 << 40;
 

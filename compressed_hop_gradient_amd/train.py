@@ -171,7 +171,7 @@ def experts(x, ids, gates, w_in, w_out, act="swiglu", keep=False, dither=True, s
     With ``keep`` the backward pass works from ``x`` and ``x @ w_in`` in 8 bits (a half or
     a quarter of the memory), kept as ``dq.keep8`` does with these numbers: ``x`` at
     ``site``, the rows at ``site + 1`` (below 2^31), so the next call in a model takes ``site + 2``.
-    ``rnd`` is the round index of the step, an int.  Given the gradient by ``x @ w_in``, that by
+    ``rnd`` is the step, as in :func:`dropout`.  Given the gradient by ``x @ w_in``, that by
     ``w_in`` is then right in the mean; the activation's gradient and ``w_out``'s are taken
     at the kept values, off by their rounding (a 64th to a 127th of a block's largest)."""
     if keep and not 0 <= site < (1 << 31) - 1:

@@ -515,7 +515,7 @@ dq_status dq_route_backward(const dq_route_grad *h_workers, int32_t n_workers, i
  * products over them, the activation between two products, and activations kept
  * in 8 bits for the backward pass.  Stateless, and with the errors and overlap
  * rules of the training step above; nothing is launched where a check fails.
- * Sizes: n_experts in 1..1024, top_k in 1..16, tokens * top_k below 2^31, widths
+ * Sizes: n_experts in 1..1024, top_k in 1..16, tokens * top_k up to 2^30, widths
  * in 1..2^24.
  *
  * Slot t * top_k + j is token t's choice j.  The slots sorted by their expert,
