@@ -54,7 +54,7 @@ __global__ __launch_bounds__(C::kThreads) void k_product(ExpertProductArgs a, in
     Acc<C> acc;
     product_tile<C, LA, LB, TURNED>(a, t, n0, 0, a.K, lds, acc);
     const auto row = [&](int m) { return m < t.rows ? static_cast<T *>(a.y) + (t.first + m) * a.ys : nullptr; };
-    acc.template store<T>(lds, row, n0, a.N);
+    acc.template store<T>(lds, row, n0, a.N, past_caches<C>(static_cast<const T *>(a.y), a.ys));
 }
 
 // The same for few rows, which the weights' bytes bound: a tile is one wave's, four of
@@ -129,7 +129,8 @@ __global__ __launch_bounds__(C::kThreads) void k_weights(ExpertWeightsArgs a, in
     multiply<C>(lds, x, dy, rows, m0 + acc.m0() < a.K && n0 + acc.n0() < a.N, acc);
     Out *dw = static_cast<Out *>(a.parts > 1 ? (void *)a.partial : a.dw) +
               ((int64_t)part * a.l.E + e) * a.K * a.N;
-    acc.template store<Out>(lds, [&](int m) { return m0 + m < a.K ? dw + (int64_t)(m0 + m) * a.N : nullptr; }, n0, a.N);
+    acc.template store<Out>(lds, [&](int m) { return m0 + m < a.K ? dw + (int64_t)(m0 + m) * a.N : nullptr; }, n0, a.N,
+                            a.parts == 1 && past_caches<C>(dw, a.N));   // k_weights_join reads parts at once
 }
 
 // The parts' sums, in their order.
