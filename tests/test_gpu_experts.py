@@ -338,6 +338,33 @@ def test_act_far_from_zero(dtype):
         assert torch.isfinite(dq.expert_act(u, gates, rows)[0, 1:]).all()
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_act_at_the_lowest_end(dtype):
+    """Gates' arguments down to the type's lowest value, where silu is 0: as a mask
+    leaves them."""
+    lowest = torch.finfo(dtype).min
+    g = torch.tensor([lowest, lowest / 2, -1e38, -1e36, -1e32, -88.0, -87.5, -86.0], dtype=torch.float64).to(dtype)
+    n = len(g)
+    u = torch.cat((g, torch.full((n,), 3.0, dtype=dtype))).cuda()[None]
+    da = torch.full((1, n), 2.0, dtype=dtype, device="cuda")
+    rows = dq.expert_rows(torch.zeros((1, 1), dtype=torch.int32, device="cuda"), 1)
+    gates = torch.full((1, 1), 0.5, device="cuda")
+    g64 = f64(g)
+    with np.errstate(over="ignore"):
+        s = 1 / (1 + np.exp(-g64))
+    a = dq.expert_act(u, gates, rows)
+    du, dgates, again = dq.expert_act_backward(u, da, gates, rows)
+    # below -87 the sigmoid is 0 instead of e^g: off by at most 88 e^-87 < 2^-118 of the factors
+    want = 0.5 * g64 * s * 3
+    close(a, want[None], ((ref.SIGMOID + 4) * U * np.abs(want) + 1.5 * 2.0 ** -118)[None], dtype)
+    assert torch.equal(again, a)
+    slope = 3 * s * (1 + g64 * (1 - s))                  # gate da = 1
+    back = np.concatenate((slope, g64 * s))
+    bound = np.concatenate((3 * s * (2 * ref.SIGMOID + 8) * U * (1 + np.abs(g64)), (ref.SIGMOID + 4) * U * np.abs(g64 * s)))
+    close(du, back[None], (bound + 3 * 2.0 ** -118)[None], dtype)
+    close(dgates, np.array([[(2 * g64 * s * 3).sum()]]), n * 2.0 ** -115, torch.float32)
+
+
 # ---- larger shapes, against fp64 products on the GPU -------------------------------
 
 def gpu_matmul(x, w, rows, gather):
