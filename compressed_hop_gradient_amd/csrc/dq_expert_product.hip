@@ -149,18 +149,19 @@ int64_t most_row_tiles(const ExpertLists &l) {
     return most < l.slots ? most : l.slots;
 }
 
-dim3 whole_rounds(int64_t tiles, int run = 1) {
-    return dim3((unsigned)((tiles + 8 * run - 1) / (8 * run) * (8 * run)));
-}
+int64_t whole_rounds(int64_t tiles, int run = 1) { return (tiles + 8 * run - 1) / (8 * run) * (8 * run); }
+// A launch has below 2^32 threads.
+bool too_many(int64_t blocks, int threads) { return blocks > ((int64_t)1 << 32) / threads - 1; }
 
 template <class C, class K>
 hipError_t product_launch(K kernel, int threads, int lds, const ExpertProductArgs &a, hipStream_t s) {
     const int nt = (a.N + C::BN - 1) / C::BN;
     const int64_t tiles = most_row_tiles<C>(a.l) * nt;
-    if (tiles > (1 << 30)) return hipErrorInvalidValue;
+    const int64_t blocks = whole_rounds(tiles);
+    if (too_many(blocks, threads)) return hipErrorInvalidConfiguration;
     const hipError_t e = room_for(kernel, lds);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(kernel, whole_rounds(tiles), dim3(threads), lds, s, a, nt);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(threads), lds, s, a, nt);
     return hipGetLastError();
 }
 template <class C, int LA, int LB>
@@ -191,11 +192,12 @@ template <class C, int LA, int LB, int GATHER, typename Out>
 hipError_t weights_gathered(const ExpertWeightsArgs &a, hipStream_t s) {
     const int mt = (a.K + C::BM - 1) / C::BM, nt = (a.N + C::BN - 1) / C::BN;
     const int64_t tiles = (int64_t)mt * nt * a.l.E * a.parts;
-    if (tiles > (1 << 30)) return hipErrorInvalidValue;
+    const int64_t blocks = whole_rounds(tiles, kWeightsRun);
+    if (too_many(blocks, C::kThreads)) return hipErrorInvalidConfiguration;
     const auto kernel = k_weights<C, LA, LB, GATHER, Out>;
     const hipError_t e = room_for(kernel, C::kLds);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(kernel, whole_rounds(tiles, kWeightsRun), dim3(C::kThreads), C::kLds, s, a, mt, nt, tiles);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(C::kThreads), C::kLds, s, a, mt, nt, tiles);
     return hipGetLastError();
 }
 

@@ -49,6 +49,9 @@ KeepKey key_of(const dq_keep_key *k) {
                    k->flags & DQ_KEEP_DITHER};
 }
 
+// of a product, which may want more tiles than a launch has
+dq_status product_status(hipError_t e) { return e == hipErrorInvalidConfiguration ? DQ_EINVAL : hip_status(e); }
+
 // The workspace of a weights' gradient: parts' sums, then x restored from its codes.
 size_t weights_partial_bytes(int64_t slots, int32_t E, int64_t inner, int64_t outer) {
     const int parts = expert_weights_parts(slots, E, inner, outer);
@@ -275,7 +278,7 @@ dq_status dq_expert_matmul(const dq_expert_lists *l, const void *x, int64_t xs, 
     spans.add(span(y, slots, ys, outer, es, true));
     if (spans.clash()) return DQ_EINVAL;
     const ExpertProductArgs a{lists_of(l), x, xs, gather, w, we, ws, turned, y, ys, (int32_t)inner, (int32_t)outer};
-    return hip_status(launch_expert_product(a, kind == DQ_F32, static_cast<hipStream_t>(stream)));
+    return product_status(launch_expert_product(a, kind == DQ_F32, static_cast<hipStream_t>(stream)));
 }
 
 size_t dq_expert_matmul_grad_bytes(int64_t tokens, int32_t k, int32_t E, int32_t kind, int32_t gather, int64_t inner,
@@ -346,7 +349,7 @@ dq_status dq_expert_matmul_grad(const dq_expert_lists *l, const void *x, int64_t
         a.xs = inner;
         a.codes = nullptr;
     }
-    return hip_status(launch_expert_weights(a, kind == DQ_F32, static_cast<hipStream_t>(stream)));
+    return product_status(launch_expert_weights(a, kind == DQ_F32, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

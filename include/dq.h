@@ -516,7 +516,8 @@ dq_status dq_route_backward(const dq_route_grad *h_workers, int32_t n_workers, i
  * in 8 bits for the backward pass.  Stateless, and with the errors and overlap
  * rules of the training step above; nothing is launched where a check fails.
  * Sizes: n_experts in 1..1024, top_k in 1..16, tokens * top_k up to 2^30, widths
- * in 1..2^24.
+ * in 1..2^24; products whose results take 2^24 tiles or more (2^23 of 256 x 256) are
+ * refused, DQ_EINVAL.
  *
  * Slot t * top_k + j is token t's choice j.  The slots sorted by their expert,
  * stably, are the ROWS; those without one (an id outside 0..n_experts-1) come last

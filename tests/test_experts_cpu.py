@@ -196,6 +196,14 @@ def test_matmul_null_and_empty(lib):
     assert _matmul(lib, tokens=0, source=None, row=None, x=None, y=None) == dq.DQ_OK
 
 
+def test_products_refuse_more_tiles_than_a_launch_has(lib):
+    """The checks pass, the tiles do not fit; before anything is launched."""
+    far = dict(tokens=1 << 30, k=1, E=1, xs=0, inner=1)
+    assert _matmul(lib, **far, kind=dq.F32, outer=1, ws=1, we=1, y=1 << 50, ys=1) == dq.DQ_EINVAL
+    assert _matmul(lib, **far, outer=129, ws=129, we=129, y=1 << 50, ys=129) == dq.DQ_EINVAL
+    assert _grad(lib, E=1024, inner=1 << 24, xs=1 << 24, outer=1, dys=1, x=1 << 44, dw=1 << 50) == dq.DQ_EINVAL
+
+
 @pytest.mark.parametrize("bad", [
     dict(kind=2), dict(out=2), dict(kind=dq.F32, out=dq.BF16), dict(gather=-1), dict(gather=3), dict(inner=0), dict(outer=0),
     dict(xs=-1), dict(dys=1 << 41), dict(x=4 * FAKE + 1), dict(dy=5 * FAKE + 1), dict(dw=6 * FAKE + 1),
