@@ -36,14 +36,15 @@ __device__ __forceinline__ void product_tile(const ExpertProductArgs &a, const R
 }
 
 // Many rows: matrix instructions bound it.  65536 rows of 64 experts, 2048 x 2816 bf16
-// (756 GFLOP): 735 us with equal experts, 770 with a router's, 980 TFLOP/s, where one library
+// (756 GFLOP): 735 us with equal experts, 776 with a router's, 970 TFLOP/s, where one library
 // product of all rows by one weight takes 625 to 640 (1210 TFLOP/s).  A step of 256 x 256 x
-// 32 takes 0.92 us, 0.75 on zeros: most of it is the clock under the products' power.  What
-// is left per tile, 9 us, is its first loads (no other block on the CU runs meanwhile) and
-// its store.  Tried and slower: steps of 64 with two in LDS (979 us), one block of 256 x 128
-// with two to a CU (1031), 4 waves of 128 x 128 (905, spills), 32 x 32 products (820), a
-// higher wave priority for the products (850), blocks that go on to a next tile whose first
-// loads run beside the store (818).
+// 32 takes 0.92 us, 0.75 on zeros: the products' power brings the clock down to 1.75 GHz.
+// The matrix units are busy 54% of the cycles; LDS moves 96 KB out and 32 in for a step, as
+// many cycles as its products.  What is left per tile, 9 us, is its first loads (no other block on
+// the CU runs meanwhile) and its store.  Tried and slower: steps of 64 with two in LDS (979
+// us), one block of 256 x 128 with two to a CU (1031), 4 waves of 128 x 128 (905, spills), 32 x
+// 32 products (820), a higher wave priority for the products (850), blocks that go on to a
+// next tile whose first loads run beside the store (818).
 template <class C, int LA, int LB, bool TURNED>
 __global__ __launch_bounds__(C::kThreads) void k_product(ExpertProductArgs a, int nt) {
     typedef typename C::T T;
@@ -59,7 +60,7 @@ __global__ __launch_bounds__(C::kThreads) void k_product(ExpertProductArgs a, in
 
 // The same for few rows, which the weights' bytes bound: a tile is one wave's, four of
 // them take a quarter of the inner index each, wait for their own loads alone, and add up
-// in the waves' order.  One token of 8 experts, 2048 x 2816 bf16 (92 MB): 19 us, 4.8 TB/s; 8
+// in the waves' order.  One token of 8 experts, 2048 x 2816 bf16 (92 MB): 20 us, 4.6 TB/s; 8
 // tokens (about 460 MB of weights met) 84 us, 5.5 TB/s.
 constexpr int kFewWaves = 4;
 template <class C, int L, bool TURNED>
@@ -95,8 +96,8 @@ constexpr int kWeightsRun = 8;
 // dw[e] = the sum of x[r]^T dy[r] over e's rows (or over a part of them, into fp32): both
 // operands lie across the inner index and are turned by the LDS read.  64 experts of 1024
 // rows, 2048 x 2816 bf16 (756 GFLOP, 738 MB out): 790 us, with a router's experts, gathered,
-// 870 (870 TFLOP/s); 16 steps a tile, so that a tile's start and end weigh more than above.
-// With 64 rows an expert 218 us, 3.4 TB/s out.
+// 877 (860 TFLOP/s); 32 steps a tile, so that a tile's start and end weigh more than above.
+// With 32 rows an expert 192 us, 3.9 TB/s out.
 template <class C, int LA, int LB, int GATHER, typename Out>
 __global__ __launch_bounds__(C::kThreads) void k_weights(ExpertWeightsArgs a, int mt, int nt, int64_t total) {
     typedef typename C::T T;
