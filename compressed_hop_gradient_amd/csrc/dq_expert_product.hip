@@ -42,9 +42,11 @@ __device__ __forceinline__ void product_tile(const ExpertProductArgs &a, const R
 // The matrix units are busy 54% of the cycles; LDS moves 96 KB out and 32 in for a step, as
 // many cycles as its products.  What is left per tile, 9 us, is its first loads (no other block on
 // the CU runs meanwhile) and its store.  Tried and slower: steps of 64 with two in LDS (979
-// us), one block of 256 x 128 with two to a CU (1031), 4 waves of 128 x 128 (905, spills), 32 x
-// 32 products (820), a higher wave priority for the products (850), blocks that go on to a
-// next tile whose first loads run beside the store (818).
+// us), one block of 256 x 128 with two to a CU (1031), 4 waves of 128 x 128, which read a third
+// less from LDS (905; without spills, a row's operand replaced behind its last use, 947, and
+// TURNED 790 instead of 737: one wave on a SIMD waits for nobody's products), 32 x 32 products
+// (820), a higher wave priority for the products (850), blocks that go on to a next tile whose
+// first loads run beside the store (818).
 template <class C, int LA, int LB, bool TURNED>
 __global__ __launch_bounds__(C::kThreads) void k_product(ExpertProductArgs a, int nt) {
     typedef typename C::T T;
