@@ -173,8 +173,10 @@ __global__ __launch_bounds__(256) void k_expert_sum(ExpertSumArgs a, int lanes) 
 // 1 / (1 + exp(-x)), off by a few units of the last place: the exponent's product is
 // carried with its error (2^p (1 + r ln 2)).  0 below -87, where the sum's reciprocal is
 // no normal number: x of fp32's lowest end times the least normal one would be -4, and is 0.
+// Above 126 the exponential is 0 and the result 1; held there, since of x beyond 2.36e38 the
+// product is infinite and its error NaN.
 __device__ __forceinline__ float sigmoid(float x) {
-    const float t = __builtin_fminf(-x, 87.0f);
+    const float t = __builtin_fmaxf(__builtin_fminf(-x, 87.0f), -126.0f);
     const float p = t * 1.44269502f;
     const float r = __builtin_fmaf(t, 1.92596303e-08f, __builtin_fmaf(t, 1.44269502f, -p));
     const float e = __builtin_amdgcn_exp2f(p);

@@ -365,6 +365,75 @@ def test_act_at_the_lowest_end(dtype):
     close(dgates, np.array([[(2 * g64 * s * 3).sum()]]), n * 2.0 ** -115, torch.float32)
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("width", [1, 8, 32])
+def test_act_at_the_upper_end(width, dtype):
+    """Gates' arguments up to the type's largest value, where the sigmoid is 1: a, both
+    gradients, the gates' gradient and the activation again, from u and from codes."""
+    most = torch.finfo(dtype).max
+    g = torch.tensor([20.0, 88.0, 1e30, 1e38, 2.3e38, 2.36e38, 2.4e38, most / 2, most], dtype=torch.float64).to(dtype)
+    n = len(g)
+    u = torch.ones(n, 2 * width, dtype=dtype)
+    u[:, 0], u[:, width:] = g, 0.75
+    u, da = u.cuda(), torch.full((n, width), 0.5, dtype=dtype, device="cuda")
+    rows = dq.expert_rows(torch.zeros((n, 1), dtype=torch.int32, device="cuda"), 1)
+    gates = torch.full((n, 1), 0.5, device="cuda")
+    a, kept = dq.expert_act(u, gates, rows, keep=True, dither=False)
+    whole = kept.exponents[:, 0] != 255
+    assert not whole[-1] and whole[:-1].all()            # beyond 127 2^121 alone a block is not kept
+    for source, values, there in ((u, f64(u), torch.ones_like(whole)), (kept, f64(dq.restore8(kept)), whole)):
+        du, dgates, again = dq.expert_act_backward(source, da, gates, rows)
+        there = there.cpu().numpy()
+        (wdu, wgate, wa), (e_du, e_gate, e_a) = ref.act_backward(values[there], f64(da)[there], np.full(there.sum(), 0.5), "swiglu")
+        # from 20 on the sum 1 + e^-g is 1 in fp32 (e^-20 < 2^-28), and so are the sigmoid and the slope, but for
+        # g e^-g < 2^-24: what is left of dg's roundings are its products'
+        e_du[:, 0] = (ref.SIGMOID + 5) * U * np.abs(wdu[:, 0])
+        if source is u:
+            close(a, wa, e_a, dtype)
+            assert torch.equal(again, a)
+        close(again[whole if source is kept else slice(None)], wa, e_a, dtype)
+        close(du[whole if source is kept else slice(None)], wdu, e_du, dtype)
+        close(dgates[whole if source is kept else slice(None)], wgate[:, None], e_gate[:, None], torch.float32)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_act_of_infinities(dtype):
+    """silu of +infinity is +infinity, of -infinity and NaN NaN, as g / (1 + exp(-g)) gives
+    them; the neighbours keep their values."""
+    inf = float("inf")
+    u = torch.tensor([[inf, inf, -inf, float("nan"), 1.0, -1.0, 2.0, 0.0] + [0.5, -0.5] + [0.5] * 6], dtype=dtype).cuda()
+    rows = dq.expert_rows(torch.zeros((1, 1), dtype=torch.int32, device="cuda"), 1)
+    a = dq.expert_act(u, torch.ones(1, 1, device="cuda"), rows)[0]
+    assert a[0] == inf and a[1] == -inf and torch.isnan(a[2:4]).all()
+    u[0, :4] = 0
+    assert torch.equal(a[4:], dq.expert_act(u, torch.ones(1, 1, device="cuda"), rows)[0, 4:])
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_act_gradients_far_from_zero(dtype):
+    """The far arguments of test_act_far_from_zero by value: below -87 the sigmoid is 0, from
+    20 on it is 1."""
+    g = torch.tensor([-1e30, -500.0, -100.0, -87.5, 30.0, 89.0, 500.0, 1e30], dtype=torch.float64).to(dtype)
+    n = len(g)
+    u = torch.cat((g, torch.ones(n, dtype=dtype))).cuda()[None]
+    da = torch.full((1, n), 0.5, dtype=dtype, device="cuda")
+    rows = dq.expert_rows(torch.zeros((1, 1), dtype=torch.int32, device="cuda"), 1)
+    gates = torch.ones(1, 1, device="cuda")
+    g64 = f64(g)
+    with np.errstate(over="ignore"):
+        s = 1 / (1 + np.exp(-g64))
+    silu = g64 * s
+    # below -87 off by at most 88 e^-87 < 2^-118 of the factors
+    far = 2.0 ** -118
+    close(dq.expert_act(u, gates, rows), silu[None], ((ref.SIGMOID + 4) * U * np.abs(silu) + far)[None], dtype)
+    du, dgates, _ = dq.expert_act_backward(u, da, gates, rows)
+    slope = np.where(g64 > 0, 1.0, s * (1 + g64 * (1 - s)))          # 30 e^-30 < 2^-38
+    want = 0.5 * np.concatenate((slope, silu))
+    close(du, want[None], ((ref.SIGMOID + 5) * U * np.abs(want) + far)[None], dtype)
+    total = (0.5 * silu).sum()
+    close(dgates, np.array([[total]]), (n + ref.SIGMOID + 5) * U * 0.5 * np.abs(silu).sum() + n * far, torch.float32)
+
+
 # ---- larger shapes, against fp64 products on the GPU -------------------------------
 
 def gpu_matmul(x, w, rows, gather):
