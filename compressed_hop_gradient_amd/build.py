@@ -21,7 +21,8 @@ FLAGS = [
     "-Wall", "-Wno-unused-command-line-argument",
 ]
 SOURCES = ["dq_kernels.hip", "dq_api.cpp", "dq_dropout.hip", "dq_route.hip", "dq_route_backward.hip",
-           "dq_train_api.cpp", "dq_expert_rows.hip", "dq_expert_product.hip", "dq_keep8.hip", "dq_experts_api.cpp"]
+           "dq_train_api.cpp", "dq_expert_rows.hip", "dq_expert_product.hip", "dq_keep8.hip", "dq_experts_api.cpp",
+           "dq_expert_pick.cpp"]
 
 
 def build(verbose=False):

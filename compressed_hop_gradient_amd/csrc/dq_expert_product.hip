@@ -1,7 +1,5 @@
 // dq_expert_product.hip -- products grouped by expert for gfx950: rows by the
 // experts' weights, and the weights' gradient.
-#include <algorithm>
-
 #include "dq.h"
 #include "dq_expert_tile.h"
 
@@ -64,7 +62,6 @@ __global__ __launch_bounds__(C::kThreads) void k_product(ExpertProductArgs a, in
 // them take a quarter of the inner index each, wait for their own loads alone, and add up
 // in the waves' order.  One token of 8 experts, 2048 x 2816 bf16 (92 MB): 20 us, 4.6 TB/s; 8
 // tokens (about 460 MB of weights met) 84 us, 5.5 TB/s.
-constexpr int kFewWaves = 4;
 template <class C, int L, bool TURNED>
 __global__ __launch_bounds__(64 * kFewWaves) void k_product_few(ExpertProductArgs a, int nt) {
     typedef typename C::T T;
@@ -90,10 +87,6 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_product_few(ExpertProductArg
     for (int q = 0; q < 4; q++) put_one(out + q, sum[q]);
     store_columns<4>(static_cast<T *>(a.y) + (t.first + m) * a.ys, n0 + n, a.N, out);
 }
-
-// Tiles of an XCD's run: 2000 us where 32 took 2260 and an eighth of all at once 2830 (a
-// router's uneven experts, before the loads went ahead).
-constexpr int kWeightsRun = 8;
 
 // dw[e] = the sum of x[r]^T dy[r] over e's rows (or over a part of them, into fp32): both
 // operands lie across the inner index and are turned by the LDS read.  64 experts of 1024
@@ -146,202 +139,96 @@ __global__ __launch_bounds__(256) void k_weights_join(const float *partial, int 
     }
 }
 
-template <class C>
-int64_t most_row_tiles(const ExpertLists &l) {
-    const int64_t most = ((int64_t)l.slots + (int64_t)l.E * (C::BM - 1)) / C::BM;
-    return most < l.slots ? most : l.slots;
+template <class C, bool FEW = false>
+constexpr bool shaped(ExpertTile t) {
+    constexpr int kThreads = FEW ? 64 * kFewWaves : C::kThreads;
+    const TileShape s = expert_tile_shape(t, C::kF32);
+    return s.bm == C::BM && s.bn == C::BN && s.threads == kThreads;
 }
-
-int64_t whole_rounds(int64_t tiles, int run = 1) { return (tiles + 8 * run - 1) / (8 * run) * (8 * run); }
-// A launch has below 2^32 threads.
-bool too_many(int64_t blocks, int threads) { return blocks > ((int64_t)1 << 32) / threads - 1; }
+static_assert(shaped<TileBig>(ExpertTile::Big) && shaped<TileMid>(ExpertTile::Mid) &&
+                  shaped<TileSmall>(ExpertTile::Small) && shaped<TileNarrow>(ExpertTile::Narrow) &&
+                  shaped<TileAny>(ExpertTile::Any) && shaped<TileFew, true>(ExpertTile::Few) &&
+                  shaped<TileFewAny, true>(ExpertTile::FewAny),
+              "the blocks were counted for these");
+static_assert(shaped<TileMidF32>(ExpertTile::Mid) && shaped<TileSmallF32>(ExpertTile::Small) &&
+                  shaped<TileAnyF32>(ExpertTile::Any) && shaped<TileFewF32, true>(ExpertTile::Few) &&
+                  shaped<TileFewAnyF32, true>(ExpertTile::FewAny),
+              "and for these");
 
 template <class C, class K>
-hipError_t product_launch(K kernel, int threads, int lds, const ExpertProductArgs &a, hipStream_t s) {
-    const int nt = (a.N + C::BN - 1) / C::BN;
-    const int64_t tiles = most_row_tiles<C>(a.l) * nt;
-    const int64_t blocks = whole_rounds(tiles);
-    if (too_many(blocks, threads)) return hipErrorInvalidConfiguration;
+hipError_t product_launch(K kernel, int threads, int lds, const ExpertProductArgs &a, const ExpertPick &p, hipStream_t s) {
     const hipError_t e = room_for(kernel, lds);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(threads), lds, s, a, nt);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)p.blocks), dim3(threads), lds, s, a, (a.N + C::BN - 1) / C::BN);
     return hipGetLastError();
 }
 template <class C, int LA, int LB>
-hipError_t product_as(const ExpertProductArgs &a, hipStream_t s) {
-    if (a.turned) return product_launch<C>(k_product<C, LA, LB, true>, C::kThreads, C::kLds, a, s);
-    return product_launch<C>(k_product<C, LA, LB, false>, C::kThreads, C::kLds, a, s);
+hipError_t product_as(const ExpertProductArgs &a, const ExpertPick &p, hipStream_t s) {
+    if (a.turned) return product_launch<C>(k_product<C, LA, LB, true>, C::kThreads, C::kLds, a, p, s);
+    return product_launch<C>(k_product<C, LA, LB, false>, C::kThreads, C::kLds, a, p, s);
 }
 template <class C, int L>
-hipError_t product_few(const ExpertProductArgs &a, hipStream_t s) {
-    if (a.turned) return product_launch<C>(k_product_few<C, L, true>, 64 * kFewWaves, kFewWaves * C::kLds, a, s);
-    return product_launch<C>(k_product_few<C, L, false>, 64 * kFewWaves, kFewWaves * C::kLds, a, s);
-}
-
-// Whether offsets into so many rows fit the 32 bits of the loads into LDS.
-bool near(int64_t rows, int64_t stride, int64_t cols, int64_t es) {
-    return ((rows - 1) * stride + cols) * es < (int64_t)kNowhere;
-}
-
-template <typename T>
-bool product_async(const ExpertProductArgs &a) {
-    constexpr int64_t es = sizeof(T), chunk = 16 / es;
-    return on16(a.x, a.xs * es) && a.K % chunk == 0 && on16(a.w, a.ws * es) && (a.l.E == 1 || a.we * es % 16 == 0) &&
-           (a.turned ? a.K : a.N) % chunk == 0 && near(a.gather ? a.l.tokens : 256, a.xs, a.K, es) &&
-           near(a.turned ? 256 : 64, a.ws, a.turned ? a.K : a.N, es);
+hipError_t product_few(const ExpertProductArgs &a, const ExpertPick &p, hipStream_t s) {
+    if (a.turned) return product_launch<C>(k_product_few<C, L, true>, 64 * kFewWaves, kFewWaves * C::kLds, a, p, s);
+    return product_launch<C>(k_product_few<C, L, false>, 64 * kFewWaves, kFewWaves * C::kLds, a, p, s);
 }
 
 template <class C, int LA, int LB, int GATHER, typename Out>
-hipError_t weights_gathered(const ExpertWeightsArgs &a, hipStream_t s) {
+hipError_t weights_gathered(const ExpertWeightsArgs &a, const ExpertPick &p, hipStream_t s) {
     const int mt = (a.K + C::BM - 1) / C::BM, nt = (a.N + C::BN - 1) / C::BN;
-    const int64_t tiles = (int64_t)mt * nt * a.l.E * a.parts;
-    const int64_t blocks = whole_rounds(tiles, kWeightsRun);
-    if (too_many(blocks, C::kThreads)) return hipErrorInvalidConfiguration;
     const auto kernel = k_weights<C, LA, LB, GATHER, Out>;
     const hipError_t e = room_for(kernel, C::kLds);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(C::kThreads), C::kLds, s, a, mt, nt, tiles);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)p.blocks), dim3(C::kThreads), C::kLds, s, a, mt, nt, p.tiles);
     return hipGetLastError();
 }
 
 template <class C, int LA, int LB, typename Out>
-hipError_t weights_as(const ExpertWeightsArgs &a, hipStream_t s) {
-    if (a.gather == DQ_GATHER_X) return weights_gathered<C, LA, LB, DQ_GATHER_X, Out>(a, s);
-    if (a.gather == DQ_GATHER_DOUT) return weights_gathered<C, LA, LB, DQ_GATHER_DOUT, Out>(a, s);
-    return weights_gathered<C, LA, LB, DQ_GATHER_NONE, Out>(a, s);
+hipError_t weights_as(const ExpertWeightsArgs &a, const ExpertPick &p, hipStream_t s) {
+    if (a.gather == DQ_GATHER_X) return weights_gathered<C, LA, LB, DQ_GATHER_X, Out>(a, p, s);
+    if (a.gather == DQ_GATHER_DOUT) return weights_gathered<C, LA, LB, DQ_GATHER_DOUT, Out>(a, p, s);
+    return weights_gathered<C, LA, LB, DQ_GATHER_NONE, Out>(a, p, s);
 }
-
-template <typename T>
-struct WeightsLoads {
-    static constexpr int64_t es = sizeof(T), chunk = 16 / es;
-    bool x, dy;
-    explicit WeightsLoads(const ExpertWeightsArgs &a) {
-        dy = on16(a.dy, a.dys * es) && a.N % chunk == 0 &&
-             near(a.gather == DQ_GATHER_DOUT ? a.l.tokens : 64, a.dys, a.N, es);
-        x = a.x && on16(a.x, a.xs * es) && a.K % chunk == 0 &&
-            near(a.gather == DQ_GATHER_X ? a.l.tokens : 64, a.xs, a.K, es);
-    }
-};
-
-// Which tile: the one whose blocks are done first, by how many of them a CU gets.
-// Measured: a block's start and end take about 4 us, a step s1 where it has the CU to
-// itself and sN where the CU is full of them; a wave of the few-row form takes a quarter
-// of the steps.  bf16, 64 experts, 2048 x 2816, us of few / small / mid / big: 0.125 rows
-// an expert 20 / 24 / 29 / 52, 16: 163 / 142 / 146 / 191, 64: 328 / 185 / 190 / 200, 512:
-// 1909 / 673 / 559 / 457; 8 experts of 1024 x 1024 and 64 rows 14 / 15 / 18 / 29, 512 rows
-// 60 / 24 / 25 / 36.  fp32, 8 experts of 1024 x 1024, few / small / mid: 2 rows 13 / 29 /
-// 76, 64: 28 / 30 / 78, 1024: 238 / 170 / 209.
-struct TileCost {
-    int bm, bn, step, full;              // step: inner elements; full: blocks a CU holds
-    float s1, sn;                        // us
-};
-constexpr TileCost kCostBf16[] = {
-    {64, 128, 32, 3, 0.30f, 0.68f}, {128, 128, 32, 2, 0.39f, 0.70f}, {256, 256, 32, 1, 0.80f, 0.80f},
-    {16, 64, 32 * kFewWaves, 2, 0.40f, 0.67f}};
-constexpr TileCost kCostF32[] = {
-    {64, 64, 16, 5, 0.39f, 1.45f}, {128, 128, 16, 2, 1.12f, 2.10f}, {16, 64, 16 * kFewWaves, 2, 0.40f, 0.90f}};
-
-template <int N>
-int pick_tile(const TileCost (&costs)[N], const ExpertProductArgs &a, double es) {
-    const double slots = a.l.slots, E = a.l.E, met = slots < E ? slots : E;
-    const double memory = met * a.K * a.N * es / 5.5e6;
-    int best = 0;
-    double least = 0;
-    for (int i = 0; i < N; i++) {
-        const TileCost &c = costs[i];
-        const double mt = std::max(met, std::min(slots, slots / c.bm + E / 2));
-        const int64_t per_cu = ((int64_t)mt * ((a.N + c.bn - 1) / c.bn) + 255) / 256, rest = per_cu % c.full;
-        const double rounds = (double)(per_cu / c.full) * c.sn +
-                              (rest ? c.s1 + (c.sn - c.s1) * (rest - 1) / std::max(1, c.full - 1) : 0.0);
-        const double us = std::max(memory, 4 + rounds * ((a.K + c.step - 1) / c.step));
-        if (i == 0 || us < 0.97 * least) {
-            best = i;
-            least = us;
-        }
-    }
-    return best;
-}
-
-// As above, for tiles of dw whose inner index is an expert's rows.  bf16, us of big / mid /
-// narrow: 60 experts, 218 rows, 1000 x 1416 into fp32 155 / 194 / 264; 8 experts, 1024 rows,
-// 1024 x 1024 58 / 50 / 79; 4096 rows, 256 x 512 64 / 52 / 55; 128 rows, 512 x 512 15 / 13 / 12.
-// fp32, mid / small: 16 experts, 512 rows, 1024 x 1024 226 / 193; 8 of 2048 rows, 1024 x 2048 694 /
-// 653; 64 of 8 rows, 1024 x 1024 76 / 83.
-template <int N>
-int pick_weights_tile(const TileCost (&costs)[N], const ExpertWeightsArgs &a) {
-    int best = 0;
-    double least = 0;
-    for (int i = 0; i < N; i++) {
-        const TileCost &c = costs[i];
-        const int64_t blocks = (int64_t)((a.K + c.bm - 1) / c.bm) * ((a.N + c.bn - 1) / c.bn) * a.l.E * a.parts;
-        const int64_t per_cu = (blocks + 255) / 256, rest = per_cu % c.full;
-        const double steps = (double)a.l.slots / a.l.E / a.parts / c.step + 8;       // 8: a tile's start and end
-        const double us = steps * ((double)(per_cu / c.full) * c.sn +
-                                   (rest ? c.s1 + (c.sn - c.s1) * (rest - 1) / std::max(1, c.full - 1) : 0.0));
-        if (i == 0 || us < 0.97 * least) {
-            best = i;
-            least = us;
-        }
-    }
-    return best;
-}
-constexpr TileCost kWeightsBf16[] = {
-    {256, 256, 32, 1, 0.80f, 0.80f}, {128, 128, 32, 2, 0.39f, 0.70f}, {64, 64, 32, 4, 0.25f, 0.55f}};
-constexpr TileCost kWeightsF32[] = {{128, 128, 16, 2, 1.12f, 2.10f}, {64, 64, 16, 5, 0.39f, 1.45f}};
 
 template <typename Out>
-hipError_t weights_bf16(const ExpertWeightsArgs &a, hipStream_t s) {
-    const WeightsLoads<uint16_t> on(a);
-    if (a.codes && on.dy) return weights_as<TileAny, kKept, kAsync, Out>(a, s);
-    if (a.codes) return weights_as<TileAny, kKept, kAny, Out>(a, s);
-    if (!on.x || !on.dy) return weights_as<TileAny, kAny, kAny, Out>(a, s);
-    const int pick = pick_weights_tile(kWeightsBf16, a);
-    if (pick == 0) return weights_as<TileBig, kAsync, kAsync, Out>(a, s);
-    if (pick == 1) return weights_as<TileMid, kAsync, kAsync, Out>(a, s);
-    return weights_as<TileNarrow, kAsync, kAsync, Out>(a, s);
+hipError_t weights_bf16(const ExpertWeightsArgs &a, const ExpertPick &p, hipStream_t s) {
+    if (a.codes && p.dy_async) return weights_as<TileAny, kKept, kAsync, Out>(a, p, s);
+    if (a.codes) return weights_as<TileAny, kKept, kAny, Out>(a, p, s);
+    if (p.tile == ExpertTile::Any) return weights_as<TileAny, kAny, kAny, Out>(a, p, s);
+    if (p.tile == ExpertTile::Big) return weights_as<TileBig, kAsync, kAsync, Out>(a, p, s);
+    if (p.tile == ExpertTile::Mid) return weights_as<TileMid, kAsync, kAsync, Out>(a, p, s);
+    return weights_as<TileNarrow, kAsync, kAsync, Out>(a, p, s);
 }
-hipError_t weights_f32(const ExpertWeightsArgs &a, hipStream_t s) {
-    const WeightsLoads<float> on(a);
-    if (a.codes && on.dy) return weights_as<TileAnyF32, kKept, kAsync, float>(a, s);
-    if (a.codes) return weights_as<TileAnyF32, kKept, kAny, float>(a, s);
-    if (!on.x || !on.dy) return weights_as<TileAnyF32, kAny, kAny, float>(a, s);
-    const int pick = pick_weights_tile(kWeightsF32, a);
-    if (pick == 0) return weights_as<TileMidF32, kAsync, kAsync, float>(a, s);
-    return weights_as<TileSmallF32, kAsync, kAsync, float>(a, s);
+hipError_t weights_f32(const ExpertWeightsArgs &a, const ExpertPick &p, hipStream_t s) {
+    if (a.codes && p.dy_async) return weights_as<TileAnyF32, kKept, kAsync, float>(a, p, s);
+    if (a.codes) return weights_as<TileAnyF32, kKept, kAny, float>(a, p, s);
+    if (p.tile == ExpertTile::Any) return weights_as<TileAnyF32, kAny, kAny, float>(a, p, s);
+    if (p.tile == ExpertTile::Mid) return weights_as<TileMidF32, kAsync, kAsync, float>(a, p, s);
+    return weights_as<TileSmallF32, kAsync, kAsync, float>(a, p, s);
 }
 
 }  // namespace
 
-hipError_t launch_expert_product(const ExpertProductArgs &a, int f32, hipStream_t s) {
+hipError_t launch_expert_product(const ExpertProductArgs &a, const ExpertPick &p, int f32, hipStream_t s) {
     if (a.l.slots == 0) return hipSuccess;
     if (f32) {
-        const int pick = pick_tile(kCostF32, a, 4);
-        if (!product_async<float>(a))
-            return pick == 2 ? product_few<TileFewAnyF32, kAny>(a, s) : product_as<TileAnyF32, kAny, kAny>(a, s);
-        if (pick == 0) return product_as<TileSmallF32, kAsync, kAsync>(a, s);
-        if (pick == 1) return product_as<TileMidF32, kAsync, kAsync>(a, s);
-        return product_few<TileFewF32, kAsync>(a, s);
+        if (p.tile == ExpertTile::FewAny) return product_few<TileFewAnyF32, kAny>(a, p, s);
+        if (p.tile == ExpertTile::Any) return product_as<TileAnyF32, kAny, kAny>(a, p, s);
+        if (p.tile == ExpertTile::Small) return product_as<TileSmallF32, kAsync, kAsync>(a, p, s);
+        if (p.tile == ExpertTile::Mid) return product_as<TileMidF32, kAsync, kAsync>(a, p, s);
+        return product_few<TileFewF32, kAsync>(a, p, s);
     }
-    const int pick = pick_tile(kCostBf16, a, 2);
-    if (!product_async<uint16_t>(a))
-        return pick == 3 ? product_few<TileFewAny, kAny>(a, s) : product_as<TileAny, kAny, kAny>(a, s);
-    if (pick == 0) return product_as<TileSmall, kAsync, kAsync>(a, s);
-    if (pick == 1) return product_as<TileMid, kAsync, kAsync>(a, s);
-    if (pick == 2) return product_as<TileBig, kAsync, kAsync>(a, s);
-    return product_few<TileFew, kAsync>(a, s);
+    if (p.tile == ExpertTile::FewAny) return product_few<TileFewAny, kAny>(a, p, s);
+    if (p.tile == ExpertTile::Any) return product_as<TileAny, kAny, kAny>(a, p, s);
+    if (p.tile == ExpertTile::Small) return product_as<TileSmall, kAsync, kAsync>(a, p, s);
+    if (p.tile == ExpertTile::Mid) return product_as<TileMid, kAsync, kAsync>(a, p, s);
+    if (p.tile == ExpertTile::Big) return product_as<TileBig, kAsync, kAsync>(a, p, s);
+    return product_few<TileFew, kAsync>(a, p, s);
 }
 
-// Enough parts that tiles of 128 x 128 give every CU a block, of 128 rows of an average
-// expert at least: 3 experts of 3300 rows, 8 x 24 13 us, in one part 106.
-int expert_weights_parts(int64_t slots, int E, int64_t K, int64_t N) {
-    const int64_t tiles = (K + 127) / 128 * ((N + 127) / 128) * E, most = slots / E / 128;
-    const int64_t parts = tiles >= 256 ? 1 : (255 + tiles) / tiles;
-    return (int)std::max((int64_t)1, std::min(parts, most));
-}
-
-hipError_t launch_expert_weights(const ExpertWeightsArgs &a, int f32, hipStream_t s) {
-    const hipError_t e = f32 ? weights_f32(a, s)
-                             : a.out_f32 || a.parts > 1 ? weights_bf16<float>(a, s) : weights_bf16<uint16_t>(a, s);
+hipError_t launch_expert_weights(const ExpertWeightsArgs &a, const ExpertPick &p, int f32, hipStream_t s) {
+    const hipError_t e = f32 ? weights_f32(a, p, s)
+                             : a.out_f32 || a.parts > 1 ? weights_bf16<float>(a, p, s) : weights_bf16<uint16_t>(a, p, s);
     if (e != hipSuccess || a.parts == 1) return e;
     const int64_t n = (int64_t)a.l.E * a.K * a.N, blocks = (n + 255) / 256;
     const dim3 grid((unsigned)(blocks < 65536 ? blocks : 65536));

@@ -226,7 +226,6 @@ __device__ __forceinline__ u32x4 load_some(const T *p, int have, bool there) {
 // of it, holds every transposing LDS read back until all such loads have landed; it has
 // no result in registers, and all_waves() waits for it.  M0, where in LDS it goes, is
 // used by nothing else here, and needs a cycle to arrive.
-constexpr uint32_t kNowhere = 0xFFFFFFF0u;
 struct Stream {
     uint32_t lo, hi;
     __device__ __forceinline__ void at(const void *p) {
@@ -813,10 +812,6 @@ template <class K>
 hipError_t room_for(K kernel, int lds) {
     if (lds <= 65536) return hipSuccess;
     return hipFuncSetAttribute(reinterpret_cast<const void *>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
-}
-
-bool on16(const void *p, int64_t stride_bytes) {
-    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride_bytes % 16 == 0;
 }
 
 }  // namespace

@@ -1,6 +1,7 @@
 // dq_experts.h -- declarations shared by the experts' entry points
-// (dq_experts_api.cpp) and their kernels (dq_expert_rows.hip,
-// dq_expert_product*.hip, dq_keep8.hip).  Not part of the public ABI.
+// (dq_experts_api.cpp), their kernels (dq_expert_rows.hip, dq_expert_product.hip,
+// dq_keep8.hip) and the choice among the products' (dq_expert_pick.cpp).  Not part of
+// the public ABI.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -10,6 +11,8 @@ namespace dq {
 
 constexpr int kExpertsMost = 1024;
 constexpr int kExpertsMostTopK = 16;
+// the offset of a load into LDS that reads zeros, and all beyond it
+constexpr uint32_t kNowhere = 0xFFFFFFF0u;
 
 // Rows of every expert.  A kernel takes nothing in the lists on trust: offsets are
 // held to 0 .. slots and in order, a slot outside of them has no token.
@@ -95,7 +98,6 @@ struct ExpertProductArgs {
     int64_t ys;
     int32_t K, N;
 };
-hipError_t launch_expert_product(const ExpertProductArgs &a, int f32, hipStream_t s);
 
 struct ExpertWeightsArgs {
     ExpertLists l;
@@ -114,6 +116,38 @@ struct ExpertWeightsArgs {
 };
 // parts into which the rows are split, whose sums meet in a second launch
 int expert_weights_parts(int64_t slots, int E, int64_t K, int64_t N);
-hipError_t launch_expert_weights(const ExpertWeightsArgs &a, int f32, hipStream_t s);
+
+// Tiles of a product, rows by columns.  Any: operands through registers or from codes; Few: one
+// wave's, whose block's waves share the inner index.
+enum class ExpertTile { Big, Mid, Small, Narrow, Few, Any, FewAny };
+struct TileShape {
+    int bm, bn, threads;
+};
+constexpr int kFewWaves = 4;
+constexpr TileShape expert_tile_shape(ExpertTile t, bool f32) {
+    switch (t) {
+    case ExpertTile::Big: return TileShape{256, 256, 512};
+    case ExpertTile::Mid: return TileShape{128, 128, 256};
+    case ExpertTile::Small: return TileShape{64, f32 ? 64 : 128, 256};
+    case ExpertTile::Any: return f32 ? TileShape{64, 64, 256} : TileShape{128, 128, 256};
+    case ExpertTile::Narrow: return TileShape{64, 64, 256};
+    default: return TileShape{16, 64, 64 * kFewWaves};
+    }
+}
+// Tiles of an XCD's run: 2000 us where 32 took 2260 and an eighth of all at once 2830 (a
+// router's uneven experts, before the loads went ahead).
+constexpr int kWeightsRun = 8;
+
+// The kernel of a call.
+struct ExpertPick {
+    ExpertTile tile;
+    bool x_async, dy_async;             // loads straight into LDS (of a product: of both operands)
+    int64_t tiles, blocks;
+    bool fits;                          // a launch has so many blocks
+};
+ExpertPick pick_expert_product(const ExpertProductArgs &a, bool f32);
+ExpertPick pick_expert_weights(const ExpertWeightsArgs &a, bool f32);
+hipError_t launch_expert_product(const ExpertProductArgs &a, const ExpertPick &p, int f32, hipStream_t s);
+hipError_t launch_expert_weights(const ExpertWeightsArgs &a, const ExpertPick &p, int f32, hipStream_t s);
 
 }  // namespace dq

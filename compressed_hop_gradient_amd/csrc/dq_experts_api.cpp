@@ -49,9 +49,6 @@ KeepKey key_of(const dq_keep_key *k) {
                    k->flags & DQ_KEEP_DITHER};
 }
 
-// of a product, which may want more tiles than a launch has
-dq_status product_status(hipError_t e) { return e == hipErrorInvalidConfiguration ? DQ_EINVAL : hip_status(e); }
-
 // The workspace of a weights' gradient: parts' sums, then x restored from its codes.
 size_t weights_partial_bytes(int64_t slots, int32_t E, int64_t inner, int64_t outer) {
     const int parts = expert_weights_parts(slots, E, inner, outer);
@@ -278,7 +275,9 @@ dq_status dq_expert_matmul(const dq_expert_lists *l, const void *x, int64_t xs, 
     spans.add(span(y, slots, ys, outer, es, true));
     if (spans.clash()) return DQ_EINVAL;
     const ExpertProductArgs a{lists_of(l), x, xs, gather, w, we, ws, turned, y, ys, (int32_t)inner, (int32_t)outer};
-    return product_status(launch_expert_product(a, kind == DQ_F32, static_cast<hipStream_t>(stream)));
+    const ExpertPick p = pick_expert_product(a, kind == DQ_F32);
+    if (!p.fits) return DQ_EINVAL;
+    return hip_status(launch_expert_product(a, p, kind == DQ_F32, static_cast<hipStream_t>(stream)));
 }
 
 size_t dq_expert_matmul_grad_bytes(int64_t tokens, int32_t k, int32_t E, int32_t kind, int32_t gather, int64_t inner,
@@ -338,18 +337,23 @@ dq_status dq_expert_matmul_grad(const dq_expert_lists *l, const void *x, int64_t
     a.N = (int32_t)outer;
     a.partial = static_cast<float *>(work);
     a.parts = expert_weights_parts(slots, l->n_experts, inner, outer);
+    RestoreArgs r{};
     if (codes && slots > 0 && weights_restored_bytes(rows_x, slots, l->n_experts, inner, outer, kind == DQ_F32)) {
         // of the rows, those of experts alone
         char *const at = static_cast<char *>(work) + weights_partial_bytes(slots, l->n_experts, inner, outer);
-        const RestoreArgs r{codes, exponents, at, rows_x, inner, inner,
-                            gather == DQ_GATHER_X ? nullptr : l->d_offsets + l->n_experts};
-        const hipError_t e = launch_restore8(r, kind == DQ_F32, static_cast<hipStream_t>(stream));
-        if (e != hipSuccess) return hip_status(e);
-        a.x = r.y;
+        r = RestoreArgs{codes, exponents, at, rows_x, inner, inner,
+                        gather == DQ_GATHER_X ? nullptr : l->d_offsets + l->n_experts};
+        a.x = at;
         a.xs = inner;
         a.codes = nullptr;
     }
-    return product_status(launch_expert_weights(a, kind == DQ_F32, static_cast<hipStream_t>(stream)));
+    const ExpertPick p = pick_expert_weights(a, kind == DQ_F32);
+    if (!p.fits) return DQ_EINVAL;
+    if (r.y) {
+        const hipError_t e = launch_restore8(r, kind == DQ_F32, static_cast<hipStream_t>(stream));
+        if (e != hipSuccess) return hip_status(e);
+    }
+    return hip_status(launch_expert_weights(a, p, kind == DQ_F32, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -204,6 +204,13 @@ def test_products_refuse_more_tiles_than_a_launch_has(lib):
     assert _grad(lib, E=1024, inner=1 << 24, xs=1 << 24, outer=1, dys=1, x=1 << 44, dw=1 << 50) == dq.DQ_EINVAL
 
 
+def test_too_many_tiles_are_refused_before_the_codes_are_restored(lib):
+    """A product long enough that its codes are restored first: nothing is launched (without a GPU
+    a launch fails with another error)."""
+    assert _grad(lib, E=1024, inner=1 << 24, outer=1, dys=1, x=None, codes=1 << 44, exponents=1 << 46, dw=1 << 50,
+                 work=1 << 54, size=1 << 50) == dq.DQ_EINVAL
+
+
 @pytest.mark.parametrize("bad", [
     dict(kind=2), dict(out=2), dict(kind=dq.F32, out=dq.BF16), dict(gather=-1), dict(gather=3), dict(inner=0), dict(outer=0),
     dict(xs=-1), dict(dys=1 << 41), dict(x=4 * FAKE + 1), dict(dy=5 * FAKE + 1), dict(dw=6 * FAKE + 1),
