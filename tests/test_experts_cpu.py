@@ -2,14 +2,17 @@
 compare with (gradients against differences, dithers against the kernels'
 documented counter), and the argument checks of the C ABI and the binding."""
 import ctypes as C
+import os
+import subprocess
 
 import numpy as np
 import pytest
 import torch
 
 import experts_ref as ref
+import test_gpu_experts as gpu
 import train_ref
-from compressed_hop_gradient_amd import dq, train
+from compressed_hop_gradient_amd import build, dq, train
 
 FAKE = 1 << 20      # never dereferenced: every call below fails its checks first, or has nothing to do
 
@@ -305,6 +308,74 @@ def test_act_backward_null_and_empty(lib):
     for bad in (dict(u=None), dict(da=None), dict(gates=None), dict(du=None), dict(codes=FAKE), dict(u=None, exponents=FAKE)):
         assert _back(lib, **bad) == dq.DQ_ENULL, bad
     assert _back(lib, tokens=0, u=None, da=None, du=None) == dq.DQ_OK
+
+
+# ---- which kernel ------------------------------------------------------------------
+
+@pytest.fixture(scope="module")
+def tiles(tmp_path_factory):
+    """Lines of tests/native/expert_tiles.cpp to its answers."""
+    here = os.path.dirname(os.path.abspath(__file__))
+    exe = str(tmp_path_factory.mktemp("tiles") / "expert_tiles")
+    subprocess.run([build.HIPCC, "-O1", "-I", os.path.join(build.ROOT, "include"), "-I", build.CSRC,
+                    os.path.join(here, "native", "expert_tiles.cpp"), os.path.join(build.CSRC, "dq_expert_pick.cpp"),
+                    "-o", exe], check=True, capture_output=True)
+
+    def ask(lines):
+        text = "\n".join(" ".join(str(int(v) if not isinstance(v, str) else v) for v in l) for l in lines) + "\n"
+        out = subprocess.run([exe], input=text, capture_output=True, text=True, check=True).stdout.split("\n")[:-1]
+        assert len(out) == len(lines)
+        return [(o.split()[0], *(int(v) for v in o.split()[1:])) for o in out]
+    return ask
+
+
+# bytes of a row of a step, and steps in LDS
+RING = {"Any": (128, 2), "FewAny": (128, 2)}
+
+
+def test_every_product_kernel_is_tested_in_many_steps(tiles):
+    """By the rule that picks them, the shapes of the GPU tests reach every tile in both
+    types, gathered or not, turned or not, in steps that go round its stages twice."""
+    lines = [("p", f32, *shape, gather, turned, off) for shapes, offs in ((gpu.DEEP, (0, 1)), (gpu.LARGE, (0,)))
+             for shape in shapes for f32 in (0, 1) for gather in (0, 1) for turned in (0, 1) for off in offs]
+    met = set()
+    for line, (tile, *_) in zip(lines, tiles(lines)):
+        f32, K = line[1], line[5]
+        row, stages = RING.get(tile, (64, 4))
+        step = row // (4 if f32 else 2) * (4 if tile.startswith("Few") else 1)       # Few: a quarter for each wave
+        if K > 2 * stages * step:
+            met.add((tile, f32, *line[7:9]))
+    want = {(tile, f32, gather, turned) for f32 in (0, 1) for gather in (0, 1) for turned in (0, 1)
+            for tile in ("Big", "Mid", "Small", "Few", "Any", "FewAny") if not (f32 and tile == "Big")}
+    assert met == want, want ^ met
+
+
+def test_every_gradient_kernel_is_tested_in_many_steps(lib, tiles):
+    lines = [("w", f32, *shape, gather, kept, off) for shapes, offs in ((gpu.DEEP, (0, 1)), (gpu.LARGE, (0,)))
+             for shape in shapes for f32 in (0, 1) for gather in (0, 1, 2) for kept in (0, 1) for off in offs]
+    asked = []
+    for op, f32, T, k, E, K, N, gather, kept, off in lines:
+        if kept:
+            # codes of long products are restored first, and read as rows on 16 bytes
+            size = [lib.dq_expert_matmul_grad_bytes(T, k, E, dq.F32 if f32 else dq.BF16, gather, K, N, c) for c in (0, 1)]
+            if size[0] != size[1]:
+                kept = 0
+        asked.append((op, f32, T, k, E, K, N, gather, kept, off))
+    met, split = set(), set()
+    for line, (tile, x_lds, dy_lds, parts, _) in zip(asked, tiles(asked)):
+        _, f32, T, k, E, K, N, gather, kept, off = line
+        row, stages = RING.get(tile, (64, 4))
+        loads = "kept" if kept else "lds" if tile != "Any" else "any"
+        # of an average expert, a tenth of whose rows are left out
+        if 0.85 * T * k / E / parts > 2 * stages * row // (4 if f32 else 2):
+            met.add((tile, f32, gather, loads, dy_lds if kept else 1))
+        split.add((tile, f32, parts > 1))
+    want = {(tile, f32, gather, "lds", 1) for f32 in (0, 1) for gather in (0, 1, 2)
+            for tile in (("Mid", "Small") if f32 else ("Big", "Mid", "Narrow"))}
+    want |= {("Any", f32, gather, "any", 1) for f32 in (0, 1) for gather in (0, 1, 2)}
+    want |= {("Any", f32, gather, "kept", dy) for f32 in (0, 1) for gather in (0, 1, 2) for dy in (0, 1)}
+    assert met == want, want ^ met
+    assert {("Any", 0, True), ("Any", 1, True), ("Narrow", 0, True), ("Mid", 0, True), ("Small", 1, True)} <= split
 
 
 # ---- refusals of the binding -----------------------------------------------------

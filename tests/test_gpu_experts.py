@@ -509,6 +509,64 @@ def test_matmul_grad_large(T, k, E, K, N, gather, kept, dtype):
         assert torch.equal(got, dq.expert_matmul_grad(given, dy, rows, gather=gather, dtype=out))
 
 
+# every tile of the products and of their gradients in many inner steps, so that its stages in
+# LDS are gone round more than once; test_experts_cpu.py holds the lists of shapes to that
+DEEP = [(4096, 2, 4, 264, 2056), (8192, 2, 4, 264, 2056), (2048, 2, 2, 1032, 4104), (1500, 2, 4, 2056, 2056),
+        (1500, 2, 4, 1032, 1032), (65536, 2, 4, 64, 56), (16, 2, 4, 4104, 264)]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("T,k,E,K,N", DEEP)
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("turned", [False, True])
+def test_matmul_deep(T, k, E, K, N, gather, turned, dtype):
+    rows = dq.expert_rows(choices(T, k, E, seed=K, none=0.1).cuda(), E)
+    n = rows.offsets[-1].item()
+    x = randn((T if gather else T * k, K), dtype, 1)
+    if not gather:
+        x[n:] = float("nan")                         # nobody's rows
+    w = randn((E, N, K) if turned else (E, K, N), dtype, 2)
+    w = w.transpose(1, 2) if turned else w
+    y, mag = gpu_matmul(x, w, rows, gather)
+    bound = product_bound(K, mag)
+    out = torch.full((T * k, N), SENTINEL, dtype=dtype, device="cuda")
+    for _ in range(2):
+        dq.expert_matmul(x, w, rows, gather=gather, out=out)
+        near(out[:n], y, bound, dtype)
+        assert (out[n:] == SENTINEL).all()
+    again = wide(torch.full((T * k, N), SENTINEL, dtype=dtype, device="cuda"))
+    dq.expert_matmul(wide(x), w, rows, gather=gather, out=again)
+    near(again[:n], y, bound, dtype)
+    assert (again[n:] == SENTINEL).all()
+    base = again._base
+    assert torch.isnan(base[:, 0]).all() and torch.isnan(base[:, -2:]).all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("T,k,E,K,N", DEEP)
+@pytest.mark.parametrize("gather", [None, "x", "dout"])
+@pytest.mark.parametrize("kept", [False, True])
+def test_matmul_grad_deep(T, k, E, K, N, gather, kept, dtype):
+    rows = dq.expert_rows(choices(T, k, E, seed=K, none=0.1).cuda(), E)
+    n = rows.offsets[-1].item()
+    x, dy = randn((T if gather == "x" else T * k, K), dtype, 1), randn((T if gather == "dout" else T * k, N), dtype, 2)
+    if gather != "x":
+        x[n:] = float("nan")
+    if gather != "dout":
+        dy[n:] = float("nan")
+    given = x
+    if kept:
+        given = dq.keep8(x)
+        x = dq.restore8(given)
+    dw, mag, most = gpu_grad(x, dy, rows, gather)
+    bound = product_bound(most, mag)
+    for out in {dtype, torch.float32}:
+        got = dq.expert_matmul_grad(given, dy, rows, gather=gather, dtype=out)
+        near(got, dw, bound, out)
+        assert torch.equal(got, dq.expert_matmul_grad(given, dy, rows, gather=gather, dtype=out))
+    near(dq.expert_matmul_grad(given if kept else wide(x), wide(dy), rows, gather=gather), dw, bound, dtype)
+
+
 def test_rows_far_apart():
     """Offsets of 2^31 bytes and more, which the kernels' 32-bit loads take, and beyond
     2^32, which they do not; outputs and experts as far apart."""
