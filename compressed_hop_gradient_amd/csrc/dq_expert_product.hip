@@ -50,7 +50,7 @@ __global__ __launch_bounds__(C::kThreads) void k_product(ExpertProductArgs a, in
     typedef typename C::T T;
     extern __shared__ __align__(1024) char lds[];
     RowTile t;
-    if (!find_tile<C::kThreads>(a.l, C::BM, nt, t, reinterpret_cast<int *>(lds))) return;
+    if (!find_tile<C::kThreads>(a.l, C::BM, nt, t, lds)) return;
     const int n0 = t.n * C::BN;
     Acc<C> acc;
     product_tile<C, LA, LB, TURNED>(a, t, n0, 0, a.K, lds, acc);
@@ -67,7 +67,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_product_few(ExpertProductArg
     typedef typename C::T T;
     extern __shared__ __align__(1024) char lds[];
     RowTile t;
-    if (!find_tile<64 * kFewWaves>(a.l, C::BM, nt, t, reinterpret_cast<int *>(lds))) return;
+    if (!find_tile<64 * kFewWaves>(a.l, C::BM, nt, t, lds)) return;
     const int n0 = t.n * C::BN, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int per = ((a.K + kFewWaves - 1) / kFewWaves + C::BK - 1) / C::BK * C::BK, from = min(wave * per, a.K);
     char *own = lds + wave * C::kLds;
@@ -156,7 +156,8 @@ static_assert(shaped<TileMidF32>(ExpertTile::Mid) && shaped<TileSmallF32>(Expert
               "and for these");
 
 template <class C, class K>
-hipError_t product_launch(K kernel, int threads, int lds, const ExpertProductArgs &a, const ExpertPick &p, hipStream_t s) {
+hipError_t product_launch(K kernel, int threads, int lds, const ExpertProductArgs &a, const ExpertPick &p,
+                          hipStream_t s) {
     const hipError_t e = room_for(kernel, lds);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(kernel, dim3((unsigned)p.blocks), dim3(threads), lds, s, a, (a.N + C::BN - 1) / C::BN);
@@ -227,8 +228,9 @@ hipError_t launch_expert_product(const ExpertProductArgs &a, const ExpertPick &p
 }
 
 hipError_t launch_expert_weights(const ExpertWeightsArgs &a, const ExpertPick &p, int f32, hipStream_t s) {
-    const hipError_t e = f32 ? weights_f32(a, p, s)
-                             : a.out_f32 || a.parts > 1 ? weights_bf16<float>(a, p, s) : weights_bf16<uint16_t>(a, p, s);
+    const hipError_t e = f32                          ? weights_f32(a, p, s)
+                         : a.out_f32 || a.parts > 1 ? weights_bf16<float>(a, p, s)
+                                                    : weights_bf16<uint16_t>(a, p, s);
     if (e != hipSuccess || a.parts == 1) return e;
     const int64_t n = (int64_t)a.l.E * a.K * a.N, blocks = (n + 255) / 256;
     const dim3 grid((unsigned)(blocks < 65536 ? blocks : 65536));

@@ -128,12 +128,16 @@ struct RowTile {
 };
 
 // The block's tile among the experts' ragged rows: expert by expert, column of
-// tiles by column.  All threads call it; false: nothing left for this block.
+// tiles by column.  All threads call it; false: nothing left for this block.  Counted in
+// 64 bits: offsets out of order may name every row for each other expert.
 template <int THREADS>
-__device__ __forceinline__ bool find_tile(const ExpertLists &l, int bm, int nt, RowTile &t, int *sh) {
+__device__ __forceinline__ bool find_tile(const ExpertLists &l, int bm, int nt, RowTile &t, void *lds) {
     constexpr int kWaves = THREADS / 64, kPer = (kExpertsMost + THREADS - 1) / THREADS;
+    int64_t *const sums = static_cast<int64_t *>(lds);
+    int *const sh = reinterpret_cast<int *>(sums + kWaves);
     const int tid = threadIdx.x, per = (l.E + THREADS - 1) / THREADS;
-    int first[kPer], rows[kPer], sum = 0;
+    int first[kPer], rows[kPer];
+    int64_t sum = 0;
 #pragma unroll
     for (int i = 0; i < kPer; i++) {
         const int e = tid * per + i;
@@ -144,42 +148,42 @@ __device__ __forceinline__ bool find_tile(const ExpertLists &l, int bm, int nt, 
             if (rows[i] > 0) sum += (rows[i] + bm - 1) / bm;
         }
     }
-    int upto = sum;
+    int64_t upto = sum;
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) {
-        const int o = __shfl_up(upto, d, 64);
+        const int64_t o = __shfl_up(upto, d, 64);
         if ((tid & 63) >= d) upto += o;
     }
-    if ((tid & 63) == 63) sh[tid >> 6] = upto;
+    if ((tid & 63) == 63) sums[tid >> 6] = upto;
     __syncthreads();
-    int total = 0;
+    int64_t total = 0;
 #pragma unroll
     for (int w = 0; w < kWaves; w++) {
-        if (w < tid >> 6) upto += sh[w];
-        total += sh[w];
+        if (w < tid >> 6) upto += sums[w];
+        total += sums[w];
     }
-    const int64_t tiles = (int64_t)total * nt, id = own_tile(blockIdx.x, tiles);
+    const int64_t tiles = total * nt, id = own_tile(blockIdx.x, tiles);
     if (id >= tiles) return false;
-    int64_t at = (int64_t)(upto - sum) * nt;
+    int64_t at = (upto - sum) * nt;
 #pragma unroll
     for (int i = 0; i < kPer; i++) {
         if (rows[i] <= 0) continue;
         const int mt = (rows[i] + bm - 1) / bm;
         const int64_t in = id - at;
         if (in >= 0 && in < (int64_t)mt * nt) {
-            const int n = (int)(in / mt), m = (int)in - n * mt;
-            sh[kWaves] = tid * per + i;
-            sh[kWaves + 1] = first[i] + m * bm;
-            sh[kWaves + 2] = rows[i] - m * bm;
-            sh[kWaves + 3] = n;
+            const int n = (int)(in / mt), m = (int)(in - (int64_t)n * mt);
+            sh[0] = tid * per + i;
+            sh[1] = first[i] + m * bm;
+            sh[2] = rows[i] - m * bm;
+            sh[3] = n;
         }
         at += (int64_t)mt * nt;
     }
     __syncthreads();
-    t.e = __builtin_amdgcn_readfirstlane(sh[kWaves]);
-    t.first = __builtin_amdgcn_readfirstlane(sh[kWaves + 1]);
-    t.rows = __builtin_amdgcn_readfirstlane(sh[kWaves + 2]);
-    t.n = __builtin_amdgcn_readfirstlane(sh[kWaves + 3]);
+    t.e = __builtin_amdgcn_readfirstlane(sh[0]);
+    t.first = __builtin_amdgcn_readfirstlane(sh[1]);
+    t.rows = __builtin_amdgcn_readfirstlane(sh[2]);
+    t.n = __builtin_amdgcn_readfirstlane(sh[3]);
     __syncthreads();
     return true;
 }

@@ -658,6 +658,25 @@ def test_entries_out_of_range_are_no_rows():
     assert (dq.expert_matmul_grad(x, dy, none, gather="x") == 0).all()
 
 
+def test_offsets_that_name_every_row_for_every_other_expert():
+    """512 experts that claim all of 2^29 + 1 rows: 2^32 + 512 tiles of 64 rows.  What the blocks
+    there are compute is right, and nothing beyond the rows is written."""
+    slots, E = (1 << 29) + 1, 1024
+    offsets = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    offsets[1::2] = slots
+    source = torch.arange(slots, dtype=torch.int32, device="cuda")
+    rows = dq.ExpertRows(offsets, source, torch.empty((slots, 1), dtype=torch.int32, device="cuda"))
+    mem = torch.full((slots + 4096,), SENTINEL, device="cuda")
+    x, w = torch.full((1, 1), 3.0, device="cuda"), torch.full((1, 1, 1), 2.0, device="cuda")
+    for gather in (False, True):
+        dq.expert_matmul(x.expand(slots, 1), w.expand(E, 1, 1), rows, gather=gather, out=mem[:slots].view(slots, 1))
+        done = mem == 6.0
+        assert (done | (mem == SENTINEL)).all() and not done[slots:].any()
+        # a block for every tile of the rows at least, 64 or so of them at the same rows
+        assert done.sum() > 1 << 25
+        mem.fill_(SENTINEL)
+
+
 def test_infinities_stay_in_their_rows():
     dtype = torch.bfloat16
     ids = choices(64, 2, 4, none=0).cuda()
