@@ -37,6 +37,14 @@ Span span(const void *p, int64_t rows, int64_t stride, int64_t cols, int64_t es,
     return Span{lo, hi > UINT64_MAX ? UINT64_MAX : (uint64_t)hi, windows ? (uint64_t)stride * es : 0,
                 (uint64_t)cols * es, out};
 }
+// An input of `many` such matrices, `apart` elements apart: from the first element to the last.
+Span span_all(const void *p, int64_t many, int64_t apart, int64_t rows, int64_t stride, int64_t cols, int64_t es) {
+    const uint64_t lo = reinterpret_cast<uintptr_t>(p);
+    typedef unsigned __int128 wide;
+    const wide hi = lo + ((wide)(many - 1) * (uint64_t)apart + (wide)(rows - 1) * (uint64_t)stride + (uint64_t)cols) *
+                             (uint64_t)es;
+    return Span{lo, hi > UINT64_MAX ? UINT64_MAX : (uint64_t)hi, 0, 0, false};
+}
 Span bytes(const void *p, size_t n, bool out) { return span(p, 1, 0, (int64_t)n, 1, out); }
 
 // Whether two of them meet.  Windows of equal stride may interleave (two halves of

@@ -12,7 +12,7 @@ namespace {
 
 // Whether offsets into so many rows fit the 32 bits of the loads into LDS.
 bool near(int64_t rows, int64_t stride, int64_t cols, int64_t es) {
-    return ((rows - 1) * stride + cols) * es < (int64_t)kNowhere;
+    return ((__int128)(rows - 1) * stride + cols) * es < (__int128)kNowhere;
 }
 
 bool on16(const void *p, int64_t stride_bytes) {

@@ -270,8 +270,7 @@ dq_status dq_expert_matmul(const dq_expert_lists *l, const void *x, int64_t xs, 
     Spans spans;
     add_lists(spans, l);
     spans.add(span(x, gather ? l->tokens : slots, xs, inner, es, false));
-    // from the first expert's first element to the last one's last
-    spans.add(span(w, 1, 0, (int64_t)(l->n_experts - 1) * we + (rows_w - 1) * ws + cols_w, es, false));
+    spans.add(span_all(w, l->n_experts, we, rows_w, ws, cols_w, es));
     spans.add(span(y, slots, ys, outer, es, true));
     if (spans.clash()) return DQ_EINVAL;
     const ExpertProductArgs a{lists_of(l), x, xs, gather, w, we, ws, turned, y, ys, (int32_t)inner, (int32_t)outer};

@@ -207,6 +207,19 @@ def test_products_refuse_more_tiles_than_a_launch_has(lib):
     assert _grad(lib, E=1024, inner=1 << 24, xs=1 << 24, outer=1, dys=1, x=1 << 44, dw=1 << 50) == dq.DQ_EINVAL
 
 
+def test_extents_beyond_64_bits_are_seen(lib, tiles):
+    """Weights whose last element lies 2^64 elements from the first, at the largest widths and
+    strides there are: any result above them meets them.  Rows that far apart are not near
+    enough for 32-bit offsets."""
+    far = dict(E=1024, inner=1 << 24, we=1 << 40, ws=1 << 40, xs=0)
+    assert _matmul(lib, **far, y=1 << 60) == dq.DQ_EINVAL
+    assert _matmul(lib, **far, flags=dq.EXPERT_TURNED, outer=1 << 24, ys=1 << 24, y=1 << 60) == dq.DQ_EINVAL
+    shape = (1, 2, 64, 64, 1, 0, 0)
+    near, beyond, wrapped = tiles([("p", 0, 1 << 24, *shape, 64), ("p", 0, 1 << 24, *shape, 1 << 10),
+                                   ("p", 0, (1 << 24) + 1, *shape, 1 << 40)])
+    assert near[1] and not beyond[1] and not wrapped[1]
+
+
 def test_too_many_tiles_are_refused_before_the_codes_are_restored(lib):
     """A product long enough that its codes are restored first: nothing is launched (without a GPU
     a launch fails with another error)."""
