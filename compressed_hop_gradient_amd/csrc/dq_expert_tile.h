@@ -228,8 +228,8 @@ __device__ __forceinline__ u32x4 load_some(const T *p, int have, bool there) {
 // offsets straight into LDS, 1 KB for a wave.  At kNowhere and beyond, the range
 // check of the buffer gives zeros.  The load is written out because the compiler, told
 // of it, holds every transposing LDS read back until all such loads have landed; it has
-// no result in registers, and all_waves() waits for it.  M0, where in LDS it goes, is
-// used by nothing else here, and needs a cycle to arrive.
+// no result in registers, and all_waves() waits for it.  M0, where in LDS it goes, is an
+// operand, which the compiler sets; the load follows a cycle later, as it has to.
 struct Stream {
     uint32_t lo, hi;
     __device__ __forceinline__ void at(const void *p) {
@@ -241,8 +241,7 @@ struct Stream {
         const uint64_t q = ((uint64_t)hi << 32 | lo) + (uint64_t)ahead;
         const u32x4 buffer = {(uint32_t)q, (uint32_t)(q >> 32) & 0xFFFFu, kNowhere, 0x00020000u};
         const uint32_t m0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)DQ_LDS(const_cast<char *>(wave_base)));
-        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(m0), "v"(offset),
-                     "s"(buffer)
+        asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"{m0}"(m0), "v"(offset), "s"(buffer)
                      : "memory");
     }
 };

@@ -3,6 +3,7 @@ compare with (gradients against differences, dithers against the kernels'
 documented counter), and the argument checks of the C ABI and the binding."""
 import ctypes as C
 import os
+import re
 import subprocess
 
 import numpy as np
@@ -389,6 +390,26 @@ def test_every_gradient_kernel_is_tested_in_many_steps(lib, tiles):
     want |= {("Any", f32, gather, "kept", dy) for f32 in (0, 1) for gather in (0, 1, 2) for dy in (0, 1)}
     assert met == want, want ^ met
     assert {("Any", 0, True), ("Any", 1, True), ("Narrow", 0, True), ("Mid", 0, True), ("Small", 1, True)} <= split
+
+
+# ---- assembly -----------------------------------------------------------------------
+
+def test_assembly_tells_the_compiler_of_m0():
+    """Loads into LDS go where M0 says: it is an operand of the statement, never written
+    behind the compiler's back."""
+    loads = 0
+    for name in sorted(os.listdir(build.CSRC)):
+        with open(os.path.join(build.CSRC, name)) as f:
+            statements = re.findall(r"asm volatile\((.*?)\);", f.read(), re.S)
+        for s in statements:
+            text = "".join(re.findall(r'"((?:[^"\\]|\\.)*)"', s.split(":")[0]))
+            for line in text.split("\\n"):
+                words = line.replace("\\t", " ").split()
+                assert "m0" not in [w.strip(",") for w in words[1:2]], (name, line)
+                if words and words[-1] == "lds":
+                    loads += 1
+                    assert '"{m0}"' in s, (name, line)
+    assert loads
 
 
 # ---- refusals of the binding -----------------------------------------------------
