@@ -43,10 +43,17 @@ bool fits(int64_t blocks, int threads) { return blocks <= ((int64_t)1 << 32) / t
 // Measured: a block's start and end take about 4 us, a step s1 where it has the CU to
 // itself and sN where the CU is full of them; a wave of the few-row form takes a quarter
 // of the steps.  bf16, 64 experts, 2048 x 2816, us of few / small / mid / big: 0.125 rows
-// an expert 20 / 24 / 29 / 52, 16: 163 / 142 / 146 / 191, 64: 328 / 185 / 190 / 200, 512:
-// 1909 / 673 / 559 / 457; 8 experts of 1024 x 1024 and 64 rows 14 / 15 / 18 / 29, 512 rows
-// 60 / 24 / 25 / 36.  fp32, 8 experts of 1024 x 1024, few / small / mid: 2 rows 13 / 29 /
-// 76, 64: 28 / 30 / 78, 1024: 238 / 170 / 209.
+// an expert 20 / 25 / 32 / 38, 16: 163 / 141 / 146 / 142, 64: 328 / 182 / 188 / 168 (the costs
+// say small), 512: 1924 / 672 / 570 / 428; 8 experts of 1024 x 1024 and 64 rows 15 / 16 / 20 /
+// 23, 512 rows 65 / 25 / 27 / 31.  fp32, 8 experts of 1024 x 1024, few / small / mid: 2 rows 12 /
+// 25 / 77, 64: 28 / 28 / 78, 1024: 243 / 158 / 208, 8192: 1784 / 1130 / 1127.
+//
+// Operands off 16 bytes go by the same costs, few or not, and what is not is one tile, Any.  Its
+// steps through registers cost more than these, so that few would do for longer than it is
+// taken: bf16, 64 experts, 2049 x 2817, us of few / any: 0.125 rows 30 / 61, 1: 138 / 184 and 2:
+// 169 / 256 (any is taken), 8: 214 / 276 (any), 16: 290 / 274, 64: 696 / 349, 512: 4276 / 990; 8
+// experts of 1025 x 1025, 2 rows 16 / 32, 64: 30 / 33 (any), 512: 135 / 44.  fp32, the same 8:
+// 21 / 45, 45 / 52, 1024 rows 424 / 228; 16 of 257 x 515, 8 rows 11 / 16, 125: 32 / 21.
 struct TileCost {
     ExpertTile tile;
     int step, full;                      // step: inner elements; full: blocks a CU holds
@@ -82,11 +89,12 @@ ExpertTile pick_tile(const TileCost (&costs)[N], const ExpertProductArgs &a, boo
     return costs[best].tile;
 }
 
-// As above, for tiles of dw whose inner index is an expert's rows.  bf16, us of big / mid /
-// narrow: 60 experts, 218 rows, 1000 x 1416 into fp32 155 / 194 / 264; 8 experts, 1024 rows,
-// 1024 x 1024 58 / 50 / 79; 4096 rows, 256 x 512 64 / 52 / 55; 128 rows, 512 x 512 15 / 13 / 12.
-// fp32, mid / small: 16 experts, 512 rows, 1024 x 1024 226 / 193; 8 of 2048 rows, 1024 x 2048 694 /
-// 653; 64 of 8 rows, 1024 x 1024 76 / 83.
+// As above, for tiles of dw whose inner index is an expert's rows; operands off 16 bytes, or
+// in codes, have the tile Any alone.  bf16, us of big / mid / narrow: 60 experts, 218 rows, 1000 x
+// 1416 into fp32 117 / 145 / 215; 8 experts, 1024 rows, 1024 x 1024 55 / 49 / 77; 4096 rows, 256 x
+// 512 64 / 52 / 55; 128 rows, 512 x 512 15 / 11 / 10; 64 of 32 rows, 2048 x 2816 187 / 253 / 466.
+// fp32, mid / small: 16 experts, 512 rows, 1024 x 1024 199 / 175 and 8 of 2048 rows, 1024 x 2048
+// 666 / 616 (the costs say mid for both); 64 of 8 rows, 1024 x 1024 66 / 81.
 template <int N>
 ExpertTile pick_weights_tile(const TileCost (&costs)[N], const ExpertWeightsArgs &a, bool f32) {
     int best = 0;

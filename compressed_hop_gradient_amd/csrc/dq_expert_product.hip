@@ -34,8 +34,10 @@ __device__ __forceinline__ void product_tile(const ExpertProductArgs &a, const R
 }
 
 // Many rows: matrix instructions bound it.  65536 rows of 64 experts, 2048 x 2816 bf16
-// (756 GFLOP): 735 us with equal experts, 776 with a router's, 970 TFLOP/s, where one library
-// product of all rows by one weight takes 625 to 640 (1210 TFLOP/s).  A step of 256 x 256 x
+// (756 GFLOP): 700 to 740 us with equal experts, 768 to 784 with a router's, 970 TFLOP/s, where
+// one library product of all rows by one weight takes 625 to 640 (1200 TFLOP/s).  By way of
+// registers (TileAny), 2049 x 2817: 1855 us; fp32, 65536 rows of 8 experts, 1024 x 1024 (137
+// GFLOP): 1128 us, 122 TFLOP/s.  A step of 256 x 256 x
 // 32 takes 0.92 us, 0.75 on zeros: the products' power brings the clock down to 1.75 GHz.
 // The matrix units are busy 54% of the cycles; LDS moves 96 KB out and 32 in for a step, as
 // many cycles as its products.  What is left per tile, 9 us, is its first loads (no other block on
@@ -60,8 +62,7 @@ __global__ __launch_bounds__(C::kThreads) void k_product(ExpertProductArgs a, in
 
 // The same for few rows, which the weights' bytes bound: a tile is one wave's, four of
 // them take a quarter of the inner index each, wait for their own loads alone, and add up
-// in the waves' order.  One token of 8 experts, 2048 x 2816 bf16 (92 MB): 20 us, 4.6 TB/s; 8
-// tokens (about 460 MB of weights met) 84 us, 5.5 TB/s.
+// in the waves' order.  One token of 8 experts, 2048 x 2816 bf16 (92 MB): 20 us, 4.6 TB/s.
 template <class C, int L, bool TURNED>
 __global__ __launch_bounds__(64 * kFewWaves) void k_product_few(ExpertProductArgs a, int nt) {
     typedef typename C::T T;
@@ -90,9 +91,12 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_product_few(ExpertProductArg
 
 // dw[e] = the sum of x[r]^T dy[r] over e's rows (or over a part of them, into fp32): both
 // operands lie across the inner index and are turned by the LDS read.  64 experts of 1024
-// rows, 2048 x 2816 bf16 (756 GFLOP, 738 MB out): 790 us, with a router's experts, gathered,
-// 877 (860 TFLOP/s); 32 steps a tile, so that a tile's start and end weigh more than above.
-// With 32 rows an expert 192 us, 3.9 TB/s out.
+// rows, 2048 x 2816 bf16 (756 GFLOP, 738 MB out): 835 to 850 us, with a router's experts,
+// gathered, 857 to 880 (870 TFLOP/s); 32 steps a tile, so that a tile's start and end weigh more
+// than above, and 2.7 GB are read where the operands are 0.64: a run is a column of all row
+// tiles, the next column another XCD's, so that every XCD reads all of an expert's x.  With 32 rows
+// an expert 187 us, 4.0 TB/s out.  By way of registers, 2049 x 2817: 2150 us; fp32, 16 experts of
+// 512 rows, 1024 x 1024 (17 GFLOP): 200 us, 274 at 1025 x 1025.
 template <class C, int LA, int LB, int GATHER, typename Out>
 __global__ __launch_bounds__(C::kThreads) void k_weights(ExpertWeightsArgs a, int mt, int nt, int64_t total) {
     typedef typename C::T T;

@@ -55,10 +55,10 @@ size_t weights_partial_bytes(int64_t slots, int32_t E, int64_t inner, int64_t ou
     return parts > 1 ? (4 * (size_t)parts * E * inner * outer + kAlign - 1) / kAlign * kAlign : 0;
 }
 // 0 where the codes are decoded as they are read.  Where the product is long, x restored
-// once and read 16 bytes at a time is faster: 60 experts of 55 tokens' choices, 1000 x 1416
-// bf16 into fp32 234 us from the codes, 157 + 6 restored; 64 x 1024, 2048 x 2816 1455 and 873 +
-// 10; 64 x 8, 1024 x 1024 50 and 38 + 6.  Short ones save the launch: 8 x 16, 512 x 512 10 and 10
-// + 6.
+// once and read 16 bytes at a time is faster.  bf16, us from the codes / restored, with that
+// launch: 60 experts, 273 rows, 1000 x 1416 into fp32 178 / 130; 64 of 1024 rows, 2048 x 2816 1474 /
+// 863; 64 of 8 rows, 1024 x 1024 58 / 40, of 64 rows 68 / 46.  Short ones save the launch: 8 of
+// 16 rows, 512 x 512 10 / 13.
 size_t weights_restored_bytes(int64_t rows_x, int64_t slots, int32_t E, int64_t inner, int64_t outer, int f32) {
     const double weights = (double)E * inner * outer, work = (double)slots * inner * outer;
     if (inner % 8 != 0 || (weights < (double)(1 << 25) && work < 4.0 * (1 << 30))) return 0;

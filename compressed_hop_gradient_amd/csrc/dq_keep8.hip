@@ -8,8 +8,8 @@ namespace {
 // A thread takes eight elements of a row, four neighbouring threads a block of 32 (a
 // row's last block may be short: its missing elements are zeros).  EIGHTS: rows of
 // whole eights, whose dithers come from one generator call.  8192 x 4096 bf16 (102 MB): 27 us,
-// 3.7 TB/s; the generator's products and the codes' arithmetic come to as much time as the
-// bytes.  Restored: 18 us, 5.6 TB/s.
+// 3.7 TB/s; the generator's products, the codes' arithmetic and the 64-bit division that finds
+// a thread's row come to as much time as the bytes.  Restored: 18 us, 5.6 TB/s.
 template <bool F32, bool EIGHTS>
 __global__ __launch_bounds__(256) void k_keep8(KeepArgs a, int32_t blocks, int64_t total) {
     const uint32_t round = a.key.round + (a.key.d_round ? *a.key.d_round : 0);

@@ -906,7 +906,7 @@ def expert_act(u, gates, rows, act="swiglu", keep=False, dither=True, seed=1, rn
 
     ``u`` is [tokens * top_k, columns].  With ``keep`` returns (a, kept): the rows of
     ``u`` are also kept in 8 bits, as :func:`keep8` would keep them with the same
-    numbers, in one pass."""
+    numbers, in the same pass where the width is a multiple of 32."""
     dev = _expert_rows(rows).device
     us = _row_matrix(u, "u", rows.slots, dev)
     columns = u.size(1)

@@ -611,7 +611,8 @@ dq_status dq_restore8(const int8_t *d_codes, const uint8_t *d_exponents, int32_t
  *   DQ_ACT_RELU    u of width columns:            a = gate max(u, 0)
  * in fp32, rounded once; 1 / (1 + exp(-g)) is 0 below g = -87.  With d_codes and
  * d_exponents the rows of u are kept as dq_keep8 keeps a matrix of tokens * top_k
- * rows (key: its numbers), in the same pass. */
+ * rows (key: its numbers), in the same pass where width is a multiple of 32, else by
+ * a second launch, which reads u again. */
 typedef enum dq_act { DQ_ACT_SWIGLU = 0, DQ_ACT_RELU = 1 } dq_act;
 dq_status dq_expert_act(const dq_expert_lists *lists, int32_t act, const void *d_u, int64_t u_stride,
                         const float *d_gates, void *d_a, int64_t a_stride, int32_t kind, int64_t width,
