@@ -4,6 +4,7 @@ documented counter), and the argument checks of the C ABI and the binding."""
 import ctypes as C
 import os
 import re
+import struct
 import subprocess
 
 import numpy as np
@@ -410,6 +411,65 @@ def test_assembly_tells_the_compiler_of_m0():
                     loads += 1
                     assert '"{m0}"' in s, (name, line)
     assert loads
+
+
+def _listings(tmp):
+    """The library's gfx950 code, as the assembler's listing: [(address, instruction) ...] by
+    address."""
+    objdump = "/opt/rocm/llvm/bin/llvm-objdump"
+    if not os.path.exists(objdump):
+        pytest.skip("no llvm-objdump")
+    with open(dq.LIB_PATH, "rb") as f:
+        image = f.read()
+    for m in re.finditer(b"__CLANG_OFFLOAD_BUNDLE__", image):
+        at, entry = m.start(), m.start() + 32
+        for _ in range(min(struct.unpack_from("<Q", image, at + 24)[0], 8)):
+            off, size, n = struct.unpack_from("<QQQ", image, entry)
+            name, entry = image[entry + 24:entry + 24 + n], entry + 24 + n
+            if name.endswith(b"gfx950") and size:
+                path = tmp / "code"
+                path.write_bytes(image[at + off:at + off + size])
+                text = subprocess.run([objdump, "-d", str(path)], capture_output=True, text=True, check=True).stdout
+                found = re.findall(r"^\t(\S.*?)\s*// ([0-9A-F]+):", text, re.M)
+                yield [(int(a, 16), i) for i, a in found]
+
+
+def _scalars(operand):
+    m = re.match(r"s\[(\d+):(\d+)\]$", operand)
+    return {f"s{i}" for i in range(int(m[1]), int(m[2]) + 1)} if m else {operand}
+
+
+def test_loads_into_lds_wait_for_their_scalars(tmp_path):
+    """Nothing behind the compiler's back counts the waits in front of an instruction written
+    out: five for a scalar that a vector instruction wrote (descriptor, M0), one for M0 from
+    the scalar unit.  On every way to every such load of the built code."""
+    loads = 0
+    for code in _listings(tmp_path):
+        jumps = {}
+        for n, (a, i) in enumerate(code):
+            if i.startswith(("s_branch", "s_cbranch")):
+                to = int(i.split()[1])
+                jumps.setdefault(a + 4 + 4 * (to - (to >> 15 << 16)), []).append(n)
+        for at, (_, load) in enumerate(code):
+            if not load.endswith(" lds"):
+                continue
+            loads += 1
+            need = _scalars(load.split(None, 1)[1].split(", ")[1]) | {"m0"}
+            ways, seen = [(at, 0)], set()
+            while ways:
+                n, waited = ways.pop()
+                if (n, waited) in seen or waited >= 5:
+                    continue
+                seen.add((n, waited))
+                # before instruction n: the one above it, and those that jump to it
+                for b in ([n - 1] if n and not code[n - 1][1].startswith(("s_branch", "s_endpgm")) else []) + \
+                        jumps.get(code[n][0], []):
+                    words = code[b][1].replace(",", " ").split()
+                    wrote = need & _scalars(words[1]) if len(words) > 1 else set()
+                    assert not (wrote and words[0].startswith("v_")), (code[b], load, waited)
+                    assert not ("m0" in wrote and words[0].startswith("s_") and waited < 1), (code[b], load)
+                    ways.append((b, waited + (1 + int(words[1], 0) if words[0] == "s_nop" else 1)))
+    assert loads > 500
 
 
 # ---- refusals of the binding -----------------------------------------------------
